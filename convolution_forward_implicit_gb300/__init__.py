@@ -6,3 +6,4 @@ the package never needs a GPU, but the first call fails loudly if the library
 has not been built.
 """
 from .binding import *  # noqa: F401,F403
+from .seq import *  # noqa: F401,F403

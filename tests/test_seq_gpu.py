@@ -1,0 +1,441 @@
+"""The sequence-mixing operators on the GPU against the 64-bit oracle, element by element, within
+bounds counted from their operations (tests/seq_oracle.py): sizes, strides, sequence lengths and
+states where they can go wrong, both types, every direction."""
+import numpy as np
+import pytest
+
+from convolution_forward_implicit_gb300 import seq as Q
+from convolution_forward_implicit_gb300.binding import CONV_BF16, CONV_F32
+from tests import seq_oracle as O
+
+pytestmark = pytest.mark.gpu
+SENTINEL = -12288.0
+
+
+class Box:
+    """Device tensors of one case: rounded inputs with their exact values, outputs between guards."""
+
+    def __init__(self, seed, bf16):
+        import torch
+        self.rng = np.random.default_rng(seed)
+        self.bf16 = bf16
+        self.t = torch.bfloat16 if bf16 else torch.float32
+        self.guards = []
+
+    def put(self, a, dtype=None, pad=0, shift=0):
+        """The values as a device tensor (rows with `pad` further columns, starting `shift` elements
+        behind an aligned address) and their exact 64-bit values."""
+        import torch
+        dtype = dtype or self.t
+        v = torch.from_numpy(np.asarray(a, dtype=np.float32)).to(dtype)
+        exact = v.double().numpy()
+        if pad or shift:
+            cols = v.shape[-1] + pad
+            flat = torch.full((v.shape[0] * cols + shift + 8,), SENTINEL, dtype=dtype, device="cuda")
+            d = flat[shift:shift + v.shape[0] * cols].view(v.shape[0], cols)[:, :v.shape[-1]]
+            d.copy_(v)
+            return d, exact
+        return v.cuda(), exact
+
+    def normal(self, *shape, std=1.0, **kw):
+        return self.put(self.rng.standard_normal(shape) * std, **kw)
+
+    def out(self, *shape, dtype=None, pad=0):
+        import torch
+        dtype = dtype or self.t
+        cols = shape[-1] + pad
+        n = int(np.prod(shape[:-1], dtype=np.int64)) * cols
+        buf = torch.full((n + 128,), SENTINEL, dtype=dtype, device="cuda")
+        full = buf[64:64 + n].view(*shape[:-1], cols)
+        self.guards.append((buf, n, full, shape[-1]))
+        return full[..., :shape[-1]]
+
+    def check_guards(self):
+        for buf, n, full, width in self.guards:
+            assert bool((buf[:64].float() == SENTINEL).all()) and bool((buf[64 + n:].float() == SENTINEL).all())
+            assert bool((full[..., width:].float() == SENTINEL).all())
+
+
+def host(t):
+    return t.detach().double().cpu().numpy()
+
+
+def starts_of(lens):
+    import torch
+    return torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device="cuda")
+
+
+def slots_of(S, rng, count, drop=()):
+    """A slot of its own for every sequence; those in `drop` get none."""
+    import torch
+    s = rng.permutation(count)[:S]
+    s[list(drop)] = -1
+    return s, torch.tensor(s, dtype=torch.int32, device="cuda")
+
+
+UNIFORM = [[1], [7] * 3, [33], [300], [1] * 5, [16] * 2]
+RAGGED = [[0, 1, 0, 0, 5, 2, 0], [3, 40, 1, 17], [0], [0, 0], [1, 1, 1, 1, 1, 1, 1, 1, 1], [129, 2, 64], [1, 0, 700, 3]]
+
+
+# ------------------------------------------------------------------------------ convolution
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("lens,ragged", [(v, False) for v in UNIFORM] + [(v, True) for v in RAGGED])
+@pytest.mark.parametrize("D,W,pad", [(16, 4, 0), (13, 3, 0), (264, 4, 8), (8, 1, 3), (24, 8, 0), (1, 2, 0)])
+def test_conv(bf16, lens, ragged, D, W, pad):
+    import torch
+    S, T = len(lens), sum(lens)
+    b = Box(17 * D + 3 * W + T, bf16)
+    x, xe = b.normal(T, D, pad=pad)
+    w, we = b.normal(D, W, std=W ** -0.5)
+    bias, be = b.normal(D, std=0.3)
+    dy, dye = b.normal(T, D, pad=pad)
+    code = CONV_BF16 if bf16 else CONV_F32
+    starts = starts_of(lens) if ragged else None
+    # states: slots in any order, one sequence without a state
+    state = state_out = sl = None
+    se = np.zeros((S, W - 1, D))
+    if W > 1:
+        at, sl = slots_of(S, b.rng, S + 2, drop=[S // 2] if S > 2 else [])
+        state, full = b.normal(S + 2, W - 1, D)
+        se = np.where((at >= 0)[:, None, None], full[at], 0)
+        state_out = b.out(S + 2, W - 1, D)
+    y = b.out(T, D, pad=pad)
+    p = Q.SeqConvPlan(S, T, D, W, code, ragged=ragged)
+    p.forward(x, w, bias, y, starts=starts, state_in=state, state_out=state_out, slots=sl)
+    ref, left, mag = O.conv(xe, we, be, lens, se)
+    O.check("y", host(y), ref, mag, W + 100, bf16)
+    if W > 1:
+        got = host(state_out)
+        for s in range(S):
+            if at[s] >= 0:
+                assert np.array_equal(got[at[s]], left[s])
+        named = set(at[at >= 0])
+        for r in range(S + 2):
+            if r not in named:
+                assert (got[r] == SENTINEL).all()
+        # the same buffer for both states
+        both = state.clone()
+        p.forward(x, w, bias, y, starts=starts, state_in=both, state_out=both, slots=sl)
+        O.check("y", host(y), ref, mag, W + 100, bf16)
+        for s in range(S):
+            if at[s] >= 0:
+                assert np.array_equal(host(both)[at[s]], left[s])
+    # gradients; no activation in half of the cases
+    act = (D + W + S) % 2 == 0
+    dx, dw, db = b.out(T, D, pad=pad), b.out(D, W, dtype=torch.float32), b.out(D, dtype=torch.float32)
+    q = Q.SeqConvPlan(S, T, D, W, code, direction="bwd", ragged=ragged, silu=act)
+    q.backward(x, w, bias, dy, dx, dw, db, starts=starts, state_in=state, slots=sl)
+    ref, mag = O.conv_grad(xe, we, be, lens, se, dye, act=act)
+    for name, v in (("dx", dx), ("dw", dw), ("dbias", db)):
+        O.check(name, host(v), ref[name], mag[name], W + 100 + (0 if name == "dx" else T), bf16 and name == "dx")
+    b.check_guards()
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("S,D,W", [(1, 1, 2), (3, 40, 4), (5, 37, 3), (70, 8, 4), (2, 1032, 8), (4, 16, 1)])
+def test_conv_step_continues_a_prompt(bf16, S, D, W):
+    """Steps after a prompt give what the whole sequence gives."""
+    L, more = 6, 3
+    b = Box(S * D + W, bf16)
+    code = CONV_BF16 if bf16 else CONV_F32
+    x, xe = b.normal(S * (L + more), D)
+    w, we = b.normal(D, W, std=W ** -0.5)
+    bias, be = b.normal(D, std=0.3)
+    ref, left, mag = O.conv(xe, we, be, [L + more] * S, np.zeros((S, W - 1, D)))
+    x3, ref, mag = x.view(S, L + more, D), ref.reshape(S, -1, D), mag.reshape(S, -1, D)
+    state = b.out(S, W - 1, D) if W > 1 else None
+    y = b.out(S * L, D)
+    Q.SeqConvPlan(S, S * L, D, W, code).forward(x3[:, :L].contiguous(), w, bias, y, state_out=state)
+    O.check("prompt", host(y).reshape(S, L, D), ref[:, :L], mag[:, :L], W + 100, bf16)
+    step = Q.SeqConvPlan(S, S, D, W, code, direction="step")
+    for i in range(more):
+        y1 = b.out(S, D)
+        step.step(x3[:, L + i], w, bias, state, state, y1)      # rows L + more tokens apart
+        O.check("step", host(y1), ref[:, L + i], mag[:, L + i], W + 100, bf16)
+    if W > 1:
+        assert np.array_equal(host(state), left)
+    b.check_guards()
+
+
+def test_conv_handles_unaligned_rows_and_extreme_inputs():
+    b = Box(5, True)
+    x, xe = b.normal(20, 64, shift=3, pad=5)
+    w, we = b.normal(64, 4)
+    big = xe.copy()
+    big[3], big[7] = 3e4, -3e4
+    x.copy_(b.put(big)[0])
+    big = host(x)
+    bias, be = b.normal(64)
+    y = b.out(20, 64, pad=1)
+    Q.SeqConvPlan(2, 20, 64, 4, CONV_BF16).forward(x, w, bias, y)
+    ref, _, mag = O.conv(big, we, be, [10, 10], np.zeros((2, 3, 64)))
+    O.check("y", host(y), ref, mag, 104, True)
+    b.check_guards()
+
+
+# ------------------------------------------------------------------------------------- scan
+def scan_case(seed, bf16, lens, D, N, G, pad=0, z=True, skip=True, bias=True, act=True, states=True):
+    import torch
+    S, T = len(lens), sum(lens)
+    b = Box(seed, bf16)
+    f32 = torch.float32
+    c = dict(S=S, T=T, D=D, N=N, G=G, act=act, box=b)
+    dev, ex = {}, {}
+
+    def put(name, pair):
+        dev[name], ex[name] = pair
+
+    put("x", b.normal(T, D, pad=pad))
+    put("dt", b.put(b.rng.standard_normal((T, D)) * 0.7 + (-1 if act else 0), pad=pad))
+    if not act:
+        put("dt", b.put(b.rng.uniform(0.01, 0.7, (T, D)), pad=pad))
+    put("A", b.put(-b.rng.uniform(0.2, 4, (D, N)), dtype=f32))
+    put("B", b.normal(T, G * N, pad=pad))
+    put("C", b.normal(T, G * N, pad=pad))
+    if skip:
+        put("D", b.normal(D, dtype=f32))
+    if z:
+        put("z", b.normal(T, D, std=2.0, pad=pad))
+    if bias:
+        put("dt_bias", b.normal(D, std=0.2, dtype=f32) if act else b.put(b.rng.uniform(0, 0.1, D), dtype=f32))
+    c.update(dev=dev, ex=ex)
+    c["at"], c["slots"], c["h"], he = None, None, None, np.zeros((S, D, N))
+    if states:
+        c["at"], c["slots"] = slots_of(S, b.rng, S + 1, drop=[S // 2] if S > 2 else [])
+        c["h"], full = b.normal(S + 1, D, N, dtype=f32)
+        he = np.where((c["at"] >= 0)[:, None, None], full[c["at"]], 0)
+    c["he"] = he
+    return c
+
+
+def check_states(c, got, ref, mag, k, name):
+    for s in range(c["S"]):
+        if c["at"][s] >= 0:
+            O.check(name, got[c["at"][s]], ref[s], mag[s], k, False)
+    named = set(c["at"][c["at"] >= 0])
+    for r in range(len(got)):
+        if r not in named:
+            assert (got[r] == SENTINEL).all()
+
+
+SCANS = [  # D, N, G, pad, z, skip, bias, act
+    (16, 16, 1, 0, 1, 1, 1, 1), (40, 16, 2, 8, 1, 1, 1, 1), (7, 1, 1, 0, 0, 0, 0, 1), (130, 5, 2, 3, 1, 0, 1, 0),
+    (33, 24, 3, 0, 0, 1, 1, 1), (12, 64, 1, 0, 1, 1, 0, 1), (6, 128, 2, 1, 1, 1, 1, 1), (260, 8, 1, 0, 1, 1, 1, 1),
+    (1, 16, 1, 0, 1, 1, 1, 0), (520, 4, 1, 8, 1, 1, 1, 1),
+]
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("lens,ragged", [(v, False) for v in UNIFORM] + [(v, True) for v in RAGGED])
+@pytest.mark.parametrize("spec", SCANS)
+def test_scan(bf16, lens, ragged, spec):
+    import torch
+    D, N, G, pad, z, skip, bias, act = spec
+    S, T = len(lens), sum(lens)
+    states = (D + T) % 3 != 0
+    c = scan_case(31 * D + N + 7 * T, bf16, lens, D, N, G, pad, z, skip, bias, bool(act), states)
+    b, dev, f32 = c["box"], c["dev"], torch.float32
+    code = CONV_BF16 if bf16 else CONV_F32
+    starts = starts_of(lens) if ragged else None
+    dy, dye = b.normal(T, D, pad=pad)
+    dh = dhe = None
+    if states:
+        dh, full = b.normal(S + 1, D, N, dtype=f32)
+        dhe = np.where((c["at"] >= 0)[:, None, None], full[c["at"]], 0)
+    ref, mag = O.scan(**c["ex"], G=G, lens=lens, h0=c["he"], act=bool(act), dy=dye, dh_out=dhe)
+    k = 4 * max(lens, default=0) + N + 100
+    arr = [dev.get(n) for n in ("x", "dt", "A", "B", "C")]
+    opt = {n: dev.get(n) for n in ("D", "z", "dt_bias")}
+
+    p = Q.SeqScanPlan(S, T, D, N, code, G=G, ragged=ragged, softplus=bool(act))
+    q = Q.SeqScanPlan(S, T, D, N, code, direction="bwd", G=G, ragged=ragged, softplus=bool(act))
+    assert p.saved_bytes == q.saved_bytes
+    y, saved = b.out(T, D, pad=pad), q.allocate_saved()
+    h_out = b.out(S + 1, D, N, dtype=f32) if states else None
+    p.forward(*arr, y, **opt, starts=starts, h_in=c["h"], h_out=h_out, slots=c["slots"], saved=saved)
+    O.check("y", host(y), ref["y"], mag["y"], k, bf16)
+    if states:
+        check_states(c, host(h_out), ref["h"], mag["h"], k, "h")
+
+    dx, ddt, dz = (b.out(T, D, pad=pad) for _ in range(3))
+    dB, dC = (b.out(T, G * N, pad=pad) for _ in range(2))
+    dA, dD, ddb = b.out(D, N, dtype=f32), b.out(D, dtype=f32), b.out(D, dtype=f32)
+    dh_in = b.out(S + 1, D, N, dtype=f32) if states else None
+    q.backward(*arr, dy, saved, dx, ddt, dA, dB, dC, **opt, starts=starts, h_in=c["h"], dh_out=dh, dh_in=dh_in,
+               slots=c["slots"], dz=dz if z else None, dD=dD if skip else None, ddt_bias=ddb if bias else None)
+    got = dict(dx=(dx, 0), ddt=(ddt, 0), dB=(dB, D), dC=(dC, D), dA=(dA, T))
+    got.update({n: (v, T) for n, v, on in (("dD", dD, skip), ("ddt_bias", ddb, bias)) if on})
+    if z:
+        got["dz"] = (dz, 0)
+    for name, (v, more) in got.items():
+        O.check(name, host(v), ref[name], mag[name], 2 * k + more, bf16 and v.dtype == torch.bfloat16)
+    if states:
+        check_states(c, host(dh_in), ref["dh_in"], mag["dh_in"], 2 * k, "dh_in")
+        # the states may be left where they came from
+        both = c["h"].clone()
+        p.forward(*arr, y, **opt, starts=starts, h_in=both, h_out=both, slots=c["slots"])
+        O.check("y", host(y), ref["y"], mag["y"], k, bf16)
+        for s in range(S):
+            if c["at"][s] >= 0:
+                O.check("h in place", host(both)[c["at"][s]], ref["h"][s], mag["h"][s], k, False)
+    b.check_guards()
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("S,D,N,G", [(1, 16, 16, 1), (3, 70, 16, 2), (5, 9, 7, 1), (66, 8, 64, 1), (2, 140, 128, 1),
+                                     (4, 33, 1, 3), (2, 24, 3, 1)])
+def test_scan_step_continues_a_prompt(bf16, S, D, N, G):
+    import torch
+    L, more = 5, 3
+    lens = [L + more] * S
+    c = scan_case(S * D + N, bf16, lens, D, N, G, states=False)
+    code = CONV_BF16 if bf16 else CONV_F32
+    dev, b = c["dev"], c["box"]
+    ref, mag = O.scan(**c["ex"], G=G, lens=lens, h0=np.zeros((S, D, N)))
+    k = 4 * (L + more) + N + 100
+    rows = {n: dev[n].view(S, L + more, -1) for n in ("x", "dt", "B", "C", "z")}
+    head = {n: v[:, :L].contiguous() for n, v in rows.items()}
+    h, y = b.out(S, D, N, dtype=torch.float32), b.out(S * L, D)
+    Q.SeqScanPlan(S, S * L, D, N, code, G=G).forward(head["x"], head["dt"], dev["A"], head["B"], head["C"], y, D=dev["D"],
+                                                     z=head["z"], dt_bias=dev["dt_bias"], h_out=h)
+    yr, ym = ref["y"].reshape(S, -1, D), mag["y"].reshape(S, -1, D)
+    O.check("prompt", host(y).reshape(S, L, D), yr[:, :L], ym[:, :L], k, bf16)
+    step = Q.SeqScanPlan(S, S, D, N, code, direction="step", G=G)
+    for i in range(more):
+        t = {n: v[:, L + i] for n, v in rows.items()}           # rows L + more tokens apart
+        y1 = b.out(S, D)
+        step.step(t["x"], t["dt"], dev["A"], t["B"], t["C"], h, h, y1, D=dev["D"], z=t["z"], dt_bias=dev["dt_bias"])
+        O.check("step", host(y1), yr[:, L + i], ym[:, L + i], k, bf16)
+    O.check("h", host(h), ref["h"], mag["h"], k, False)
+    b.check_guards()
+
+
+def test_scan_step_with_slots():
+    """Rows without a slot start from zero and leave nothing behind."""
+    import torch
+    S, D, N = 6, 20, 16
+    c = scan_case(9, False, [1] * S, D, N, 1)
+    dev = c["dev"]
+    ref, mag = O.scan(**c["ex"], G=1, lens=[1] * S, h0=c["he"])
+    h, y = c["box"].out(S + 1, D, N, dtype=torch.float32), c["box"].out(S, D)
+    Q.SeqScanPlan(S, S, D, N, CONV_F32, direction="step").step(
+        dev["x"], dev["dt"], dev["A"], dev["B"], dev["C"], c["h"], h, y, D=dev["D"], z=dev["z"], dt_bias=dev["dt_bias"],
+        slots=c["slots"])
+    O.check("y", host(y), ref["y"], mag["y"], 120, False)
+    check_states(c, host(h), ref["h"], mag["h"], 120, "h")
+
+
+def test_scan_is_the_same_twice_and_on_another_stream():
+    import torch
+    lens = [700, 0, 1, 300]
+    c = scan_case(11, True, lens, 136, 16, 1, states=False)
+    dev = c["dev"]
+    T = sum(lens)
+    starts = starts_of(lens)
+    p = Q.SeqScanPlan(4, T, 136, 16, CONV_BF16, ragged=True)
+    ys = []
+    for stream in (None, torch.cuda.Stream()):
+        y = torch.empty(T, 136, dtype=torch.bfloat16, device="cuda")
+        torch.cuda.synchronize()
+        p.forward(dev["x"], dev["dt"], dev["A"], dev["B"], dev["C"], y, starts=starts,
+                  stream=None if stream is None else stream.cuda_stream)
+        torch.cuda.synchronize()
+        ys.append(y)
+    assert torch.equal(*ys)
+
+
+def test_scan_forward_in_a_graph():
+    import torch
+    c = scan_case(12, False, [40, 40], 24, 16, 1, states=False)
+    dev = c["dev"]
+    p = Q.SeqScanPlan(2, 80, 24, 16, CONV_F32).allocate()
+    y, want = torch.empty(80, 24, device="cuda"), torch.empty(80, 24, device="cuda")
+    args = [dev[n] for n in ("x", "dt", "A", "B", "C")]
+    p.forward(*args, want)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        p.forward(*args, y)
+    y.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, want)
+
+
+# ------------------------------------------------------------------------------------- norm
+@pytest.mark.parametrize("types", ["f32", "bf16", "bf16/f32"])
+@pytest.mark.parametrize("layer", [False, True])
+@pytest.mark.parametrize("rows,D,pad", [(1, 1, 0), (3, 8, 0), (5, 13, 2), (70, 384, 8), (2, 1288, 0), (9, 4096, 0),
+                                        (3, 9001, 0), (2, 16384, 0), (611, 40, 0)])
+@pytest.mark.parametrize("post,pre,gate,res,scale", [(0, 1, "none", 1, 0), (1, 1, "before", 1, 1), (1, 0, "after", 0, 0),
+                                                     (1, 0, "none", 1, 1), (0, 1, "after", 0, 1), (1, 1, "after", 1, 1)])
+def test_norm(types, layer, rows, D, pad, post, pre, gate, res, scale):
+    import torch
+    bf16 = types != "f32"
+    rt = torch.bfloat16 if types == "bf16" else torch.float32
+    b = Box(rows + D + 3 * post + pre, bf16)
+    f32 = torch.float32
+    code, rcode = CONV_BF16 if bf16 else CONV_F32, CONV_BF16 if types == "bf16" else CONV_F32
+    eps = 1e-3
+    dev, ex = {}, {}
+
+    def put(name, on, pair):
+        if on:
+            dev[name], ex[name] = pair
+
+    put("x", True, b.normal(rows, D, pad=pad))
+    put("gate", gate != "none", b.normal(rows, D, std=2.0, pad=pad))
+    put("w_post", post, b.put(b.rng.uniform(0.5, 1.5, D)))
+    put("b_post", post and layer, b.normal(D, std=0.2))
+    put("scale", scale, b.put(b.rng.uniform(0.1, 1, D)))
+    put("res", res, b.put(b.rng.standard_normal((rows, D)) + 0.5, dtype=rt, pad=pad))
+    put("w_pre", pre, b.put(b.rng.uniform(0.5, 1.5, D)))
+    put("b_pre", pre and layer, b.normal(D, std=0.2))
+    has_y = pre or not res
+    dy, dye = b.normal(rows, D, pad=pad) if has_y else (None, None)
+    dro, droe = b.normal(rows, D, dtype=rt, pad=pad) if res else (None, None)
+    ref, mag = O.norm(**ex, layer=layer, eps=eps, post=post, pre=pre, after=gate == "after", dy=dye, dres_out=droe)
+    kw = dict(res_dtype=rcode, kind="layer" if layer else "rms", post=bool(post), pre=bool(pre), gate=gate,
+              residual=bool(res), eps=eps)
+    y = b.out(rows, D, pad=pad) if has_y else None
+    ro = b.out(rows, D, dtype=rt, pad=pad) if res else None
+    others = {n: v for n, v in dev.items() if n != "x"}
+    Q.SeqNormPlan(rows, D, code, **kw).forward(dev["x"], y=y, res_out=ro, **others)
+    k = D ** 0.5 + 120        # a row's sums run over at most D / 32 + 10 values one after another
+    k = max(k, D / 32 + 120)
+    if has_y:
+        O.check("y", host(y), ref["y"], mag["y"], k, bf16)
+    if res:
+        O.check("res_out", host(ro), ref["res_out"], mag["res_out"], k, rt == torch.bfloat16)
+    grads = dict(dx=b.out(rows, D, pad=pad))
+    if gate != "none":
+        grads["dgate"] = b.out(rows, D, pad=pad)
+    if res:
+        grads["dres"] = b.out(rows, D, dtype=rt, pad=pad)
+    for n in ("w_post", "b_post", "scale", "w_pre", "b_pre"):
+        if n in dev:
+            grads["d" + n] = b.out(D, dtype=f32)
+    Q.SeqNormPlan(rows, D, code, direction="bwd", **kw).backward(dev["x"], dy=dy, dres_out=dro, **grads, **others)
+    for n, v in grads.items():
+        whole = v.dim() == 1
+        O.check(n, host(v), ref[n], mag[n], 2 * k + (rows if whole else 0), v.dtype == torch.bfloat16)
+    b.check_guards()
+
+
+def test_norm_in_place_and_zero_rows():
+    """The residual may be updated in place; a row of zeros normalises to the bias."""
+    import torch
+    b = Box(3, True)
+    x, xe = b.normal(5, 64)
+    r0, re_ = b.normal(5, 64, dtype=torch.float32)
+    x[2], r0[2] = 0, 0
+    xe[2], re_[2] = 0, 0
+    w, we = b.normal(64)
+    bias, be = b.normal(64)
+    r = r0.clone()
+    y = b.out(5, 64)
+    Q.SeqNormPlan(5, 64, CONV_BF16, kind="layer").forward(x, y=y, res=r, res_out=r, w_pre=w, b_pre=bias)
+    ref, mag = O.norm(xe, True, 1e-5, False, True, res=re_, w_pre=we, b_pre=be)
+    O.check("y", host(y), ref["y"], mag["y"], 130, True)
+    O.check("res", host(r), ref["res_out"], mag["res_out"], 130, False)
+    assert np.array_equal(host(y)[2], be)

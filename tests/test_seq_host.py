@@ -1,0 +1,231 @@
+"""Host-side checks of the sequence-mixing operators that need no GPU: exported symbols, argument
+structs, plan and call refusals, and the 64-bit oracle's gradients against differences.  No call
+here launches a kernel."""
+import ctypes
+import os
+import re
+
+import numpy as np
+import pytest
+
+from convolution_forward_implicit_gb300 import binding as B
+from convolution_forward_implicit_gb300 import seq as Q
+from tests import seq_oracle as O
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+HEADER = re.sub(r"/\*.*?\*/", "", open(os.path.join(ROOT, "include", "seq.h")).read(), flags=re.S)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from convolution_forward_implicit_gb300.build import build_library
+    build_library()
+    return Q._library()
+
+
+def test_library_exports_every_declared_symbol(lib):
+    names = set(re.findall(r"^\s*(?:const\s+)?[a-z_][a-z_0-9]*\**\s+\**(seq_[a-z_0-9]+)\s*\(", HEADER, re.M))
+    assert len(names) == 16
+    for n in names:
+        assert hasattr(lib, n), n
+    assert names == set(Q.SEQ_EXPORTED)
+
+
+@pytest.mark.parametrize("name,fields", [("conv", Q.CONV_FIELDS), ("scan", Q.SCAN_FIELDS), ("norm", Q.NORM_FIELDS)])
+def test_argument_structs_match_the_header(name, fields):
+    body = re.search(r"typedef struct \{([^}]*)\} seq_%s_args;" % name, HEADER, re.S).group(1)
+    assert tuple(re.findall(r"(\w+);", body)) == fields
+
+
+def _conv(S=2, T=8, D=16, W=4, dtype=B.CONV_BF16, direction=Q.SEQ_FWD, flags=Q.SEQ_CONV_SILU):
+    return Q.seq_conv_plan_create(S, T, D, W, dtype, direction, flags)
+
+
+def _scan(S=2, T=8, D=16, N=16, G=1, dtype=B.CONV_BF16, direction=Q.SEQ_FWD, flags=Q.SEQ_SCAN_SOFTPLUS):
+    return Q.seq_scan_plan_create(S, T, D, N, G, dtype, direction, flags)
+
+
+def _norm(rows=8, D=16, dtype=B.CONV_BF16, res=B.CONV_F32, direction=Q.SEQ_FWD,
+          flags=Q.SEQ_NORM_PRE | Q.SEQ_NORM_RESIDUAL, eps=1e-5):
+    return Q.seq_norm_plan_create(rows, D, dtype, res, direction, flags, eps)
+
+
+@pytest.mark.parametrize("make,kw,status", [
+    (_conv, dict(S=0), 1), (_conv, dict(T=-1), 1), (_conv, dict(D=0), 1), (_conv, dict(W=0), 1), (_conv, dict(W=9), 2),
+    (_conv, dict(T=9), 1), (_conv, dict(dtype=5), 1), (_conv, dict(direction=3), 1), (_conv, dict(flags=4), 1),
+    (_conv, dict(S=1, T=(1 << 30) + 1), 2), (_conv, dict(D=(1 << 22) + 1), 2),
+    (_conv, dict(direction=Q.SEQ_STEP), 1), (_conv, dict(T=2, direction=Q.SEQ_STEP, flags=Q.SEQ_RAGGED), 1),
+    (_scan, dict(N=0), 1), (_scan, dict(N=129), 2), (_scan, dict(G=3), 1), (_scan, dict(G=0), 1), (_scan, dict(T=7), 1),
+    (_scan, dict(flags=2), 1), (_scan, dict(direction=Q.SEQ_STEP), 1), (_scan, dict(dtype=-1), 1),
+    (_norm, dict(rows=0), 1), (_norm, dict(D=0), 1), (_norm, dict(D=16385), 2), (_norm, dict(flags=0), 1),
+    (_norm, dict(flags=Q.SEQ_NORM_POST | Q.SEQ_NORM_GATE_BEFORE | Q.SEQ_NORM_GATE_AFTER), 1), (_norm, dict(eps=-1.0), 1),
+    (_norm, dict(eps=float("nan")), 1), (_norm, dict(direction=Q.SEQ_STEP), 1), (_norm, dict(flags=Q.SEQ_NORM_PRE | 1), 1),
+    (_norm, dict(dtype=B.CONV_F32, res=B.CONV_BF16), 2),
+])
+def test_plans_refuse_what_they_do_not_take(lib, make, kw, status):
+    with pytest.raises(B.ConvError) as e:
+        make(**kw)
+    assert e.value.status == status
+
+
+def _status(lib, name, plan, fields, **values):
+    v = [int(values.pop(f, 0)) for f in fields]
+    assert not values
+    arr = (ctypes.c_int64 * len(v))(*v)
+    return getattr(lib, name)(plan, ctypes.cast(arr, ctypes.c_char_p), None)
+
+
+P = 1 << 20          # an address that is never read: every call below is refused before a launch
+
+
+def test_conv_calls_check_their_arguments(lib):
+    good = dict(x=P, x_ld=16, w=P, y=P, y_ld=16)
+    st = lambda plan, name="seq_conv_fwd", **kw: _status(lib, name, plan, Q.CONV_FIELDS, **kw)      # noqa: E731
+    fwd, bwd, rag = _conv(), _conv(direction=Q.SEQ_BWD), _conv(flags=Q.SEQ_RAGGED)
+    assert st(None, **good) == 1 and st(bwd, **good) == 1 and st(fwd, "seq_conv_step", **good) == 1
+    for k in ("x", "w", "y"):
+        assert st(fwd, **{**good, k: 0}) == 1, k
+        assert st(fwd, **{**good, k: P + 1}) == 3, k
+    assert st(fwd, **{**good, "x_ld": 15}) == 1 and st(fwd, **{**good, "y_ld": 0}) == 1
+    assert st(fwd, **good, starts=P) == 1 and st(rag, **good) == 1
+    assert st(fwd, **good, state_in=P, slot_count=1) == 1          # fewer rows than sequences
+    assert st(fwd, **good, state_in=P, slots=P, slot_count=-1) == 1
+    b = dict(x=P, x_ld=16, w=P, dy=P, dy_ld=16, dx=P, dx_ld=16, dw=P)
+    assert st(bwd, "seq_conv_bwd", **b) == 4                        # no workspace
+    assert st(bwd, "seq_conv_bwd", **{**b, "dw": P + 2}) == 3
+    assert st(bwd, "seq_conv_bwd", **b, dbias=P) == 1               # a gradient without its parameter
+    one = _conv(W=1)
+    assert st(one, **good, state_in=P, state_out=P, slot_count=2) == 1   # one tap keeps no state
+    for p in (fwd, bwd, rag, one):
+        Q.seq_plan_destroy(p)
+
+
+def test_scan_calls_check_their_arguments(lib):
+    good = dict(x=P, x_ld=16, dt=P, dt_ld=16, A=P, B=P, B_ld=16, C=P, C_ld=16, y=P, y_ld=16)
+    st = lambda plan, name="seq_scan_fwd", **kw: _status(lib, name, plan, Q.SCAN_FIELDS, **kw)      # noqa: E731
+    fwd, bwd = _scan(), _scan(direction=Q.SEQ_BWD)
+    assert st(bwd, **good) == 1
+    for k in ("x", "dt", "A", "B", "C", "y"):
+        assert st(fwd, **{**good, k: 0}) == 1, k
+        assert st(fwd, **{**good, k: P + 1}) == 3, k
+    assert st(fwd, **{**good, "B_ld": 15}) == 1
+    assert st(fwd, **good, z=P, z_ld=8) == 1
+    assert st(fwd, **good, saved=P + 4) == 3
+    assert st(fwd, **good, h_out=P, slot_count=1) == 1
+    b = {**good, **dict(dy=P, dy_ld=16, dx=P, dx_ld=16, ddt=P, ddt_ld=16, dB=P, dB_ld=16, dC=P, dC_ld=16, dA=P, saved=P)}
+    assert st(bwd, "seq_scan_bwd", **b) == 4
+    for k in ("dy", "saved", "dx", "ddt", "dB", "dC", "dA"):
+        assert st(bwd, "seq_scan_bwd", **{**b, k: 0}) == 1, k
+    for k in ("dD", "ddt_bias"):
+        assert st(bwd, "seq_scan_bwd", **b, **{k: P}) == 1, k
+    assert st(bwd, "seq_scan_bwd", **b, D=P) == 1 and st(bwd, "seq_scan_bwd", **b, z=P, z_ld=16) == 1
+    for p in (fwd, bwd):
+        Q.seq_plan_destroy(p)
+
+
+def test_norm_calls_check_their_arguments(lib):
+    good = dict(x=P, x_ld=16, res=P, res_ld=16, res_out=P, res_out_ld=16, y=P, y_ld=16)
+    st = lambda plan, name="seq_norm_fwd", **kw: _status(lib, name, plan, Q.NORM_FIELDS, **kw)      # noqa: E731
+    fwd, bwd = _norm(), _norm(direction=Q.SEQ_BWD)
+    for k in ("x", "res", "res_out", "y"):
+        assert st(fwd, **{**good, k: 0}) == 1, k
+        assert st(fwd, **{**good, k: P + 1}) == 3, k
+    for k in ("gate", "w_post", "b_post"):                          # not part of this plan
+        assert st(fwd, **good, **{k: P}, **({"gate_ld": 16} if k == "gate" else {})) == 1, k
+    b = dict(x=P, x_ld=16, res=P, res_ld=16, dy=P, dy_ld=16, dx=P, dx_ld=16, dres=P, dres_ld=16)
+    assert st(bwd, "seq_norm_bwd", **b, w_pre=P, dw_pre=P) == 4
+    assert st(bwd, "seq_norm_bwd", **b, dw_pre=P) == 1
+    for k in ("x", "res", "dy", "dx", "dres"):
+        assert st(bwd, "seq_norm_bwd", **{**b, k: 0}) == 1, k
+    for p in (fwd, bwd):
+        Q.seq_plan_destroy(p)
+
+
+def test_workspaces(lib):
+    p = _conv(direction=Q.SEQ_BWD)
+    need = Q.seq_workspace_bytes(p)
+    assert need > 0 and lib.seq_plan_set_workspace(p, P, need - 1) == 4
+    assert lib.seq_plan_set_workspace(p, P + 8, need) == 3 and lib.seq_plan_set_workspace(p, P, need) == 0
+    Q.seq_plan_destroy(p)
+    assert lib.seq_workspace_bytes(None) == 0 and lib.seq_scan_saved_bytes(None) == 0
+    assert lib.seq_plan_set_workspace(None, P, 1) == 1 and lib.seq_plan_destroy(None) == 0
+    f, b = _scan(T=50, D=12, N=6), _scan(T=50, D=12, N=6, direction=Q.SEQ_BWD)
+    assert Q.seq_scan_saved_bytes(f) == Q.seq_scan_saved_bytes(b) > 0
+    Q.seq_plan_destroy(f)
+    Q.seq_plan_destroy(b)
+
+
+def test_python_plans_refuse_tensors_that_do_not_fit(lib):
+    import torch
+    p = Q.SeqConvPlan(2, 8, 16, 4, B.CONV_F32)
+    x, w = torch.zeros(8, 16), torch.zeros(16, 4)
+    for bad in (x, torch.zeros(8, 16, dtype=torch.bfloat16), torch.zeros(7, 16)):       # not on the GPU, type, rows
+        with pytest.raises(B.ConvError) as e:
+            p.forward(bad, w, None, x)
+        assert e.value.status == B.CONV_ERR_INVALID_ARG
+    with pytest.raises(B.ConvError):
+        p.backward(x, w, None, x, x, w, None)
+    with pytest.raises(ValueError):
+        Q.SeqConvPlan(2, 8, 16, 4, B.CONV_F32, direction="sideways")
+    p.close()
+
+
+# ------------------------------------------------------- the oracle's gradients against differences
+def _directional(f, args, grads, name, rng, eps=1e-5):
+    d = rng.standard_normal(args[name].shape)
+    hi, lo = dict(args), dict(args)
+    hi[name], lo[name] = args[name] + eps * d, args[name] - eps * d
+    num = (f(**hi) - f(**lo)) / (2 * eps)
+    ana = float((grads["d" + name] * d).sum())
+    assert abs(num - ana) <= 1e-6 * max(1.0, abs(ana)), (name, num, ana)
+
+
+def test_conv_gradients_against_differences():
+    rng = np.random.default_rng(1)
+    lens, D, W = [5, 0, 1, 7], 6, 4
+    a = dict(x=rng.standard_normal((13, D)), w=rng.standard_normal((D, W)), bias=rng.standard_normal(D))
+    state, dy = rng.standard_normal((4, W - 1, D)), rng.standard_normal((13, D))
+    f = lambda x, w, bias: float((O.conv(x, w, bias, lens, state)[0] * dy).sum())       # noqa: E731
+    g, _ = O.conv_grad(**a, lens=lens, state=state, dy=dy)
+    for k in a:
+        _directional(f, a, g, k, rng)
+
+
+@pytest.mark.parametrize("act", [True, False])
+def test_scan_gradients_against_differences(act):
+    rng = np.random.default_rng(2)
+    lens, W, N, G, T = [5, 0, 1, 7], 6, 3, 2, 13
+    a = dict(x=rng.standard_normal((T, W)), dt=rng.standard_normal((T, W)) * 0.3 + (0 if act else 0.5),
+             A=-rng.uniform(0.5, 2, (W, N)), B=rng.standard_normal((T, G * N)), C=rng.standard_normal((T, G * N)),
+             D=rng.standard_normal(W), z=rng.standard_normal((T, W)), dt_bias=rng.standard_normal(W) * 0.2)
+    h0, dy, dh = rng.standard_normal((4, W, N)), rng.standard_normal((T, W)), rng.standard_normal((4, W, N))
+
+    def f(h_in=h0, **kw):
+        o, _ = O.scan(**kw, G=G, lens=lens, h0=h_in, act=act)
+        return float((o["y"] * dy).sum() + (o["h"] * dh).sum())
+
+    g, _ = O.scan(**a, G=G, lens=lens, h0=h0, act=act, dy=dy, dh_out=dh)
+    full = dict(a, h_in=h0)
+    for k in full:
+        _directional(f, full, g, k, rng)
+
+
+@pytest.mark.parametrize("layer", [False, True])
+@pytest.mark.parametrize("post,pre,gate,after,res", [(1, 1, 1, 0, 1), (1, 1, 1, 1, 1), (0, 1, 0, 0, 1), (1, 0, 1, 1, 0),
+                                                     (1, 0, 0, 0, 1), (0, 1, 1, 0, 0)])
+def test_norm_gradients_against_differences(layer, post, pre, gate, after, res):
+    rng = np.random.default_rng(3)
+    R, D = 3, 7
+    n = lambda *s: rng.standard_normal(s)       # noqa: E731
+    a = dict(x=n(R, D), gate=n(R, D) if gate else None, w_post=n(D) if post else None, b_post=n(D) if post else None,
+             scale=n(D), res=n(R, D) if res else None, w_pre=n(D) if pre else None, b_pre=n(D) if pre else None)
+    dy, dres = n(R, D), n(R, D) if res else None
+
+    def f(**kw):
+        o, _ = O.norm(**kw, layer=layer, eps=1e-3, post=post, pre=pre, after=bool(after))
+        return float((o["y"] * dy).sum() if "y" in o else 0) + float((o["res_out"] * dres).sum() if res else 0)
+
+    g, _ = O.norm(**a, layer=layer, eps=1e-3, post=post, pre=pre, after=bool(after), dy=dy, dres_out=dres)
+    for k in a:
+        if a[k] is not None:
+            _directional(f, a, g, k, rng)
