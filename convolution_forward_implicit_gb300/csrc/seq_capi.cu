@@ -78,7 +78,7 @@ seq_plan* new_plan(Op op, int64_t S, int64_t T, int64_t D, conv_dtype dtype, seq
 // every tensor seen has 16-byte aligned rows.
 struct Checker {
     conv_status st = CONV_OK;
-    bool wide = true;
+    bool wide = true, words = true;      // words: 4-byte aligned rows
     void fail(conv_status s) { if (st == CONV_OK) st = s; }
     void ptr(const void* v, size_t esize, bool needed, size_t align = 0) {
         if (!v) {
@@ -88,12 +88,14 @@ struct Checker {
         const uintptr_t a = reinterpret_cast<uintptr_t>(v);
         if (a % (align ? align : esize)) fail(CONV_ERR_ALIGNMENT);
         if (a % 16) wide = false;
+        if (a % 4) words = false;
     }
     void rows(const void* v, int64_t ld, int64_t width, size_t esize, bool needed = true) {
         ptr(v, esize, needed);
         if (!v) return;
         if (ld < width) fail(CONV_ERR_INVALID_ARG);
         if (((uint64_t)ld * esize) % 16) wide = false;
+        if (((uint64_t)ld * esize) % 4) words = false;
     }
 };
 
@@ -115,23 +117,30 @@ void check_states(const seq_plan* p, Checker& c, const int32_t* starts, const in
     if ((in || out) && (slot_count < 0 || (!slots && slot_count < p->S))) c.fail(CONV_ERR_INVALID_ARG);
 }
 
-// How many pieces the scan cuts the token axis into.  `blocks` thread blocks walk one piece of all
-// channels.  Without a cut the blocks run the whole length of a sequence; with one every token is
-// walked twice (once for the pieces' final states), so a cut has to give at least 3 pieces to pay.
-ScanPieces scan_pieces(const seq_plan* p, int blocks) {
-    ScanPieces pc = {1, SCAN_TILE, 0};
-    const int want_blocks = 4 * p->sms, shortest = 32;
+// How many pieces the scan cuts a sequence (a ragged axis) of `axis` tokens into.  `base` thread
+// blocks walk one piece of every sequence and all channels; `slots` of them keep the GPU busy.  Uncut,
+// a block walks all tokens in order; cut, `again` of the work is done twice, for the states between the
+// pieces, and joining the pieces costs about as much as `join` tokens a piece.  The estimate: waves of blocks, times the work of a block.
+ScanPieces scan_pieces(const seq_plan* p, int blocks, int slots, float again, float join) {
+    const int shortest = 32, most_pieces = 64;
     const long long axis = p->L > 0 ? p->L : p->T;
     const long long base = p->L > 0 ? (long long)p->S * blocks : blocks;
-    long long n = (want_blocks + base - 1) / base;
-    const long long most = (axis + shortest - 1) / shortest;
-    if (n > most) n = most;
-    if (n < 3) n = 1;
-    long long len = ((axis + n - 1) / n + SCAN_TILE - 1) / SCAN_TILE * SCAN_TILE;
-    if (len < SCAN_TILE) len = SCAN_TILE;
-    n = (axis + len - 1) / len;
-    if (n < 1) n = 1;
-    pc.len = (int)len;
+    long long best_len = 0;
+    float best = 0.f;
+    for (int n = 1; n <= most_pieces; ++n) {
+        long long len = ((axis + n - 1) / n + SCAN_TILE - 1) / SCAN_TILE * SCAN_TILE;
+        if (len < SCAN_TILE) len = SCAN_TILE;
+        if (n > 1 && len < shortest) break;
+        const long long count = (axis + len - 1) / len;
+        const long long waves = (base * (count < 1 ? 1 : count) + slots - 1) / slots;
+        const float cost = (float)waves * ((float)len * (count > 1 ? 1.f + again : 1.f) + join * (float)count);
+        if (!best_len || cost < best) {
+            best = cost;
+            best_len = len;
+        }
+    }
+    ScanPieces pc = {1, (int)best_len, 0};
+    const long long n = (axis + best_len - 1) / best_len < 1 ? 1 : (axis + best_len - 1) / best_len;
     if (p->L > 0) {
         pc.pps = (int)n;
         pc.count = (int)(n * p->S);
@@ -145,6 +154,9 @@ int scan_fwd_blocks(int D, int N, int G) {
     const int ln = N <= 16 ? 1 : N <= 32 ? 2 : N <= 64 ? 4 : 8, cb = 128 / ln, per = D / G;
     return G * ((per + cb - 1) / cb);
 }
+
+// Floats of a token's partial dB and dC in the backward workspace: states padded as the kernel's lanes hold them.
+size_t scan_bc_row(const seq_plan* p) { return 2 * (size_t)(p->N <= 8 ? 8 : p->N <= 16 ? 16 : p->N <= 32 ? 32 : p->N <= 64 ? 64 : 128); }
 
 size_t scan_state_row(const seq_plan* p) { return (size_t)((p->N + 3) / 4) * 4 * p->D; }   // floats
 
@@ -246,17 +258,18 @@ conv_status seq_scan_plan_create(seq_plan_t* out, int64_t S, int64_t T, int64_t 
     if (direction == SEQ_FWD) {
         const int blocks = scan_fwd_blocks(p->D, p->N, p->G);
         if (blocks > 65535) st = CONV_ERR_UNSUPPORTED;
-        p->pc = scan_pieces(p, blocks);
+        p->pc = scan_pieces(p, blocks, 6 * p->sms, 0.75f, 1.f);
         if (p->pc.pps != 1 && p->pc.count > 1)
             p->ws_bytes = 2 * align256(scan_state_row(p) * p->pc.count * sizeof(float)) +
                           align256((size_t)p->pc.count * D * sizeof(float));
     } else if (direction == SEQ_BWD) {
         p->blocks = seq_scan_bwd_channel_blocks(p->D, p->N, p->G);
         if (p->blocks > 65535) st = CONV_ERR_UNSUPPORTED;
-        if (p->L > 0) p->pc = ScanPieces{p->S, (p->L + SCAN_TILE - 1) / SCAN_TILE * SCAN_TILE, 1};
-        else p->pc = ScanPieces{1, (p->T + SCAN_TILE - 1) / SCAN_TILE * SCAN_TILE, 0};
-        p->ws_bytes = align256((size_t)p->blocks * p->T * 2 * N * sizeof(float)) +
+        p->pc = scan_pieces(p, p->blocks, 3 * p->sms, 0.25f, 1.f);
+        p->ws_bytes = align256((size_t)p->blocks * p->T * scan_bc_row(p) * sizeof(float)) +
                       align256((size_t)p->pc.count * (N + 2) * D * sizeof(float));
+        if (p->pc.pps != 1 && p->pc.count > 1)
+            p->ws_bytes += align256(scan_state_row(p) * p->pc.count * sizeof(float)) + align256((size_t)p->pc.count * D * sizeof(float));
     }
     if (st != CONV_OK) {
         delete p;
@@ -322,6 +335,7 @@ static conv_status scan_call(seq_plan_t p, const seq_scan_args* a, seq_direction
     q.x_ld = a->x_ld; q.dt_ld = a->dt_ld; q.B_ld = a->B_ld; q.C_ld = a->C_ld; q.z_ld = a->z_ld; q.y_ld = a->y_ld;
     q.dy_ld = a->dy_ld; q.dx_ld = a->dx_ld; q.ddt_ld = a->ddt_ld; q.dB_ld = a->dB_ld; q.dC_ld = a->dC_ld; q.dz_ld = a->dz_ld;
     q.cblocks = p->blocks;
+    q.wide = c.wide && (p->D / p->G * e) % 16 == 0 ? 16 : c.words && (p->D / p->G * e) % 4 == 0 ? 4 : 0;
     unsigned char* w = static_cast<unsigned char*>(p->ws);
     if (dir == SEQ_FWD && p->ws_bytes) {
         const size_t row = align256(scan_state_row(p) * p->pc.count * sizeof(float));
@@ -330,7 +344,11 @@ static conv_status scan_call(seq_plan_t p, const seq_scan_args* a, seq_direction
         q.piece_delta = reinterpret_cast<float*>(w + 2 * row);
     } else if (bwd) {
         q.part_bc = reinterpret_cast<float*>(w);
-        q.part_par = reinterpret_cast<float*>(w + align256((size_t)p->blocks * p->T * 2 * p->N * sizeof(float)));
+        w += align256((size_t)p->blocks * p->T * scan_bc_row(p) * sizeof(float));
+        q.part_par = reinterpret_cast<float*>(w);
+        w += align256((size_t)p->pc.count * (p->N + 2) * p->D * sizeof(float));
+        q.piece_state = reinterpret_cast<float*>(w);
+        q.piece_delta = reinterpret_cast<float*>(w + align256(scan_state_row(p) * p->pc.count * sizeof(float)));
     }
     const bool bf16 = p->dtype == CONV_BF16;
     cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -109,4 +109,99 @@ __device__ __forceinline__ float softplus(float v) {
     return fmaf(2.0f * r, s, fmaxf(v, 0.0f));
 }
 
+// Copies of 16 bytes from global to shared memory that run on while the thread goes on; `on` false:
+// zeros, and no access to the source.
+__device__ __forceinline__ void copy16_async(void* to, const void* from, bool on) {
+    const uint32_t d = (uint32_t)__cvta_generic_to_shared(to);
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(from), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy4_async(void* to, const void* from, bool on) {
+    const uint32_t d = (uint32_t)__cvta_generic_to_shared(to);
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(d), "l"(from), "r"(on ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits until at most N of this thread's latest groups are still on their way.
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// rows_to_shared for rows that are not whole 16-byte groups.  Out of line: it is rare, and its registers
+// would count in the kernels' loops.
+template <typename T, int ROWS, int W, int THREADS>
+__device__ __noinline__ void rows_to_shared_odd(T (*to)[W], const T* from, long long ld, int n, int width, int grain) {
+    if (grain == 4) {
+        constexpr int E = 4 / sizeof(T), CPR = W / E;
+#pragma unroll 4
+        for (int i = threadIdx.x; i < ROWS * CPR; i += THREADS) {
+            const int r = i / CPR, c = i % CPR * E;
+            const bool on = r < n && c < width;
+            copy4_async(&to[r][c], on ? from + r * ld + c : from, on);
+        }
+    } else {
+#pragma unroll 8
+        for (int i = threadIdx.x; i < ROWS * W; i += THREADS) {
+            const int r = i / W, c = i % W;
+            to[r][c] = r < n && c < width ? from[r * ld + c] : T(0.f);
+        }
+    }
+}
+// n rows of W elements (a multiple of 16 bytes), ROWS at most, to shared memory by the block's THREADS
+// threads, as part of the copy group at hand.  Columns at and behind `width` and rows at and behind n
+// become zero.  grain: 16 or 4 when rows are whole and aligned groups of as many bytes; else 0: plain
+// loads (2-byte elements at odd places), which are done on return.
+template <typename T, int ROWS, int W, int THREADS>
+__device__ __forceinline__ void rows_to_shared(T (*to)[W], const T* from, long long ld, int n, int width, int grain) {
+    if (grain == 16) {
+        constexpr int E = 16 / sizeof(T), CPR = W / E, ALL = ROWS * CPR;
+        static_assert(W % E == 0, "rows of whole 16-byte groups");
+#pragma unroll
+        for (int j = 0; j < (ALL + THREADS - 1) / THREADS; ++j) {
+            const int i = threadIdx.x + j * THREADS, r = i / CPR, c = i % CPR * E;
+            if (ALL % THREADS == 0 || i < ALL) {
+                const bool on = r < n && c < width;
+                copy16_async(&to[r][c], on ? from + r * ld + c : from, on);
+            }
+        }
+    } else {
+        rows_to_shared_odd<T, ROWS, W, THREADS>(to, from, ld, n, width, grain);
+    }
+}
+
+// softplus and, if wanted, its derivative sigmoid(v) of two values: see softplus.
+__device__ __forceinline__ float2 softplus2(float2 v, float2* slope) {
+    const float2 q = make_float2(ex2_approx(-LOG2E * fabsf(v.x)), ex2_approx(-LOG2E * fabsf(v.y)));
+    const float2 two = make_float2(2.f, 2.f);
+    const float2 d = __fadd2_rn(two, q);
+    const float2 r = __fmul2_rn(q, make_float2(rcp_approx(d.x), rcp_approx(d.y)));
+    const float2 r2 = __fmul2_rn(r, r);
+    auto step = [&](float2 s, float c) { return __ffma2_rn(r2, s, make_float2(c, c)); };
+    float2 s = step(make_float2(1.0f / 15.0f, 1.0f / 15.0f), 1.0f / 13.0f);
+    s = step(s, 1.0f / 11.0f);
+    s = step(s, 1.0f / 9.0f);
+    s = step(s, 1.0f / 7.0f);
+    s = step(s, 1.0f / 5.0f);
+    s = step(s, 1.0f / 3.0f);
+    s = step(s, 1.0f);
+    if (slope) {                     // 1 / (1 + e^-v) = (v < 0 ? q : 1) / (1 + q)
+        slope->x = (v.x < 0.f ? q.x : 1.f) * rcp_approx(1.f + q.x);
+        slope->y = (v.y < 0.f ? q.y : 1.f) * rcp_approx(1.f + q.y);
+    }
+    return __ffma2_rn(__fmul2_rn(two, r), s, make_float2(fmaxf(v.x, 0.f), fmaxf(v.y, 0.f)));
+}
+
+__device__ __forceinline__ float2 seq_ld2(const float* p) { return *reinterpret_cast<const float2*>(p); }
+__device__ __forceinline__ float2 seq_ld2(const __nv_bfloat16* p) {
+    float2 v;
+    bf2_unpack(*reinterpret_cast<const uint32_t*>(p), v.x, v.y);
+    return v;
+}
+// Two neighbouring values; `pair`: both are there and the address is aligned to both.
+__device__ __forceinline__ void seq_st2(float* p, float2 v, bool pair, bool one) {
+    if (pair) *reinterpret_cast<float2*>(p) = v;
+    else if (one) *p = v.x;
+}
+__device__ __forceinline__ void seq_st2(__nv_bfloat16* p, float2 v, bool pair, bool one) {
+    if (pair) *reinterpret_cast<uint32_t*>(p) = bf2_pack(v.x, v.y);
+    else if (one) *p = __float2bfloat16_rn(v.x);
+}
+
 }  // namespace convfwd

@@ -83,12 +83,14 @@ struct SeqScanParams {
     float *h_out, *saved, *dA, *dD, *ddt_bias, *dh_in;
     long long x_ld, dt_ld, B_ld, C_ld, z_ld, y_ld, dy_ld, dx_ld, ddt_ld, dB_ld, dC_ld, dz_ld;
     // workspace
-    float* piece_state;             // [pieces][D][N]: a piece's contribution to the state behind it (or before it, backward)
+    float* piece_state;             // [pieces][D][N]: what a piece adds to the state behind it (backward: to the gradient
+                                    // before it); then the state before it (the gradient behind it)
     float* piece_init;              // [pieces][D][N]: starting state of the last sequence that starts in a piece
     float* piece_delta;             // [pieces][D]: sum of delta over a piece
     float* part_bc;                 // backward: [channel blocks][T][2][N] partial dB, dC
     float* part_par;                // backward: [pieces][N + 2][D] partial dA, dD, ddt_bias
     int cblocks;                    // backward: channel blocks (over all groups)
+    int wide;                       // rows and groups consist of whole aligned pieces of so many bytes: 16, 4 or 0 (of single elements)
 };
 
 #ifdef __CUDACC__
@@ -114,6 +116,8 @@ __device__ __forceinline__ long long scan_tile_row(const SeqAxis& a, int t) {
 cudaError_t launch_seq_scan_fwd(const SeqScanParams& p, bool bf16, cudaStream_t stream);
 cudaError_t launch_seq_scan_bwd(const SeqScanParams& p, bool bf16, cudaStream_t stream);
 cudaError_t launch_seq_scan_step(const SeqScanParams& p, bool bf16, cudaStream_t stream);
+// From what every piece adds to what reaches every piece: piece_state in place, piece after piece.
+cudaError_t launch_seq_scan_join(const SeqScanParams& p, bool reverse, cudaStream_t stream);
 // States of empty sequences: from -> to (zero where from is NULL).
 cudaError_t launch_seq_scan_empty(const SeqScanParams& p, const float* from, float* to, cudaStream_t stream);
 int seq_scan_bwd_channel_blocks(int D, int N, int G);

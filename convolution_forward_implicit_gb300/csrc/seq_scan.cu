@@ -9,119 +9,271 @@
 namespace convfwd {
 namespace {
 
-constexpr int THREADS = 128;
+constexpr int THREADS = 64;         // of the scan; a thread has two channels
+constexpr int STEP_THREADS = 128;   // of the one-token step
 
-template <typename T, int NPT, int LN, bool SUMMARY>
-__global__ void __launch_bounds__(THREADS) seq_scan_kernel(const __grid_constant__ SeqScanParams p) {
-    constexpr int CB = THREADS / LN, NP = NPT * LN;
-    __shared__ __align__(16) float sB[SCAN_TILE][NP], sC[SUMMARY ? 1 : SCAN_TILE][NP];
-    __shared__ ScanBounds sb;
+// Rows of B or C of a tile, on their way through registers to shared memory as fp32.
+template <typename T, int NP>
+struct TileRows {
+    static constexpr int J = (SCAN_TILE * NP + THREADS - 1) / THREADS;
+    T v[J];
+    __device__ __forceinline__ void load(const void* base, long long ld, int col, int N, int tb, int n) {
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const int i = threadIdx.x + j * THREADS, t = min(i / NP, n - 1), k = min(i % NP, N - 1);
+            v[j] = static_cast<const T*>(base)[(long long)(tb + t) * ld + col + k];
+        }
+    }
+    __device__ __forceinline__ void store(float (*to)[NP], int N) const {
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const int i = threadIdx.x + j * THREADS;
+            if (J * THREADS == SCAN_TILE * NP || i < SCAN_TILE * NP) to[i / NP][i % NP] = i % NP < N ? seq_ld(&v[j]) : 0.f;
+        }
+    }
+};
+
+// A block walks a piece, a tile of SCAN_TILE tokens at a time.  x, dt and z of the next tiles are copied
+// to shared memory while this one is computed (STAGES tiles in flight or in use); B and C pass through
+// registers into two buffers of fp32.  One barrier a tile.  A thread has two neighbouring channels: what
+// a token costs besides its states (conversions, softplus, silu, addresses, the rows of B and C) is shared
+// by the two.  SUMMARY: only the state behind the piece and the sum of delta.
+template <typename T, int NPT, int LN, bool SUMMARY, bool GATED>
+__global__ void __launch_bounds__(THREADS, 6) seq_scan_kernel(const __grid_constant__ SeqScanParams p) {
+    constexpr int CB = 2 * THREADS / LN, NP = NPT * LN, STAGES = sizeof(T) == 2 ? 4 : 3;
+    __shared__ __align__(16) float sB[2][SCAN_TILE][NP], sC[2][SUMMARY ? 1 : SCAN_TILE][NP];
+    __shared__ __align__(16) T sx[STAGES][SCAN_TILE][CB], sdt[STAGES][SCAN_TILE][CB], sz[GATED ? STAGES : 1][GATED ? SCAN_TILE : 1][CB];
     const int piece = blockIdx.x;
     int t0, t1;
     scan_piece_range(p.ax, p.pc, piece, t0, t1);
     if (SUMMARY) {                  // the last piece of a sequence (of the axis) hands nothing on
         if (p.pc.pps > 0 ? piece % p.pc.pps == p.pc.pps - 1 : piece == p.pc.count - 1) return;
     }
+    if (t0 >= t1) return;
     const int per = p.D / p.G, bpg = (per + CB - 1) / CB;
     const int g = blockIdx.y / bpg;
-    const int cl = (blockIdx.y - g * bpg) * CB + threadIdx.x / LN;      // channel in its group
-    const bool on = cl < per;
-    const int d = g * per + (on ? cl : per - 1);
+    const int cb0 = (blockIdx.y - g * bpg) * CB;                        // the block's first channel in its group
+    const int width = min(CB, per - cb0), d0 = g * per + cb0;
+    const int c = threadIdx.x / LN * 2;                                 // the thread's first channel in the block
+    const bool on[2] = {c < width, c + 1 < width};
+    const int d[2] = {d0 + min(c, width - 1), d0 + min(c + 1, width - 1)};
     const int ln = threadIdx.x % LN, n0 = ln * NPT;
-    float A2[NPT], h[NPT];
-#pragma unroll
-    for (int k = 0; k < NPT; ++k) {
-        A2[k] = n0 + k < p.N ? p.A[(long long)d * p.N + n0 + k] * LOG2E : 0.f;
-        h[k] = 0.f;
-    }
-    const float Dd = p.Dskip ? p.Dskip[d] : 0.f, bias = p.dt_bias ? p.dt_bias[d] : 0.f;
-    float total = 0.f;
-    // the state before the piece: what the sequence's earlier pieces leave, one after another
-    if (!SUMMARY && t0 < t1) {
-        const int s = seq_first_at(p.ax, t0 + 1) - 1;
-        const int begin = s < 0 ? t0 : seq_start(p.ax, s, 0);
-        if (begin < t0) {
-            const int q0 = p.pc.pps > 0 ? piece - piece % p.pc.pps : begin / p.pc.len;
-            for (int q = q0; q < piece; ++q) {
-                const float sum = p.piece_delta[(long long)q * p.D + d];
-#pragma unroll
-                for (int k = 0; k < NPT; ++k) {
-                    const float e = n0 + k < ((p.N + 3) & ~3) ? p.piece_state[scan_state_at(p, q, (n0 + k) >> 2, d) + (k & 3)] : 0.f;
-                    h[k] = fmaf(ex2_approx(sum * A2[k]), h[k], e);
-                }
-            }
+    const int padded = (p.N + 3) & ~3;
+    T* yp = SUMMARY ? nullptr : static_cast<T*>(p.y) + (long long)t0 * p.y_ld + d[0];
+
+    auto fetch = [&](int tb, int stage) {
+        if (tb < t1) {
+            const int n = min(SCAN_TILE, t1 - tb);
+            auto rows = [&](T (*to)[CB], const void* from, long long ld) {
+                rows_to_shared<T, SCAN_TILE, CB, THREADS>(to, static_cast<const T*>(from) + (long long)tb * ld + d0, ld, n, width, p.wide);
+            };
+            rows(sx[stage], p.x, p.x_ld);
+            rows(sdt[stage], p.dt, p.dt_ld);
+            if (GATED) rows(sz[stage], p.z, p.z_ld);
         }
-    }
-    const T* x = static_cast<const T*>(p.x) + d;
-    const T* dt = static_cast<const T*>(p.dt) + d;
-    const T* z = static_cast<const T*>(p.z) + d;
-    T* y = static_cast<T*>(p.y) + d;
-    for (int tb = t0; tb < t1; tb += SCAN_TILE) {
+        copies_commit();
+    };
+    TileRows<T, NP> Br, Cr;
+    auto fetch_bc = [&](int tb) {
         const int n = min(SCAN_TILE, t1 - tb);
-        __syncthreads();
-        for (int i = threadIdx.x; i < n * NP; i += THREADS) {
-            const int t = i / NP, k = i - t * NP;
-            sB[t][k] = k < p.N ? seq_ld(static_cast<const T*>(p.B) + (long long)(tb + t) * p.B_ld + g * p.N + k) : 0.f;
-            if (!SUMMARY)
-                sC[t][k] = k < p.N ? seq_ld(static_cast<const T*>(p.C) + (long long)(tb + t) * p.C_ld + g * p.N + k) : 0.f;
+        Br.load(p.B, p.B_ld, g * p.N, p.N, tb, n);
+        if (!SUMMARY) Cr.load(p.C, p.C_ld, g * p.N, p.N, tb, n);
+    };
+#pragma unroll
+    for (int i = 0; i < STAGES - 1; ++i) fetch(t0 + i * SCAN_TILE, i);
+    fetch_bc(t0);
+
+    // packed values hold states 2 k and 2 k + 1 of the thread's, or its two channels
+    float2 A2[2][NPT / 2], h[2][NPT / 2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int k = 0; k < NPT / 2; ++k) {
+            const float* A = p.A + (long long)d[e] * p.N + n0 + 2 * k;
+            A2[e][k] = make_float2(n0 + 2 * k < p.N ? A[0] * LOG2E : 0.f, n0 + 2 * k + 1 < p.N ? A[1] * LOG2E : 0.f);
+            h[e][k] = make_float2(0.f, 0.f);
         }
-        if (threadIdx.x < 32) scan_bounds(p.ax, tb, n, &sb);
+    const float2 Dd = p.Dskip ? make_float2(p.Dskip[d[0]], p.Dskip[d[1]]) : make_float2(0.f, 0.f);
+    const float2 bias = p.dt_bias ? make_float2(p.dt_bias[d[0]], p.dt_bias[d[1]]) : make_float2(0.f, 0.f);
+    float2 total = make_float2(0.f, 0.f);
+    ScanPlace q = scan_place(p.ax, t0);
+    // states at the workspace's layout and at the caller's
+    auto get = [&](const float* from, long long row) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int k = 0; k < NPT / 2; k += 2) {
+                h[e][k] = h[e][k + 1] = make_float2(0.f, 0.f);
+                if (n0 + 2 * k < padded) ld2(from + scan_state_at(p, row, (n0 + 2 * k) >> 2, d[e]), h[e][k], h[e][k + 1]);
+            }
+    };
+    auto put = [&](float* to, long long row) {
+#pragma unroll
+        for (int k = 0; k < NPT / 2; k += 2)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                if (on[e] && n0 + 2 * k < padded) st2(to + scan_state_at(p, row, (n0 + 2 * k) >> 2, d[e]), h[e][k], h[e][k + 1]);
+    };
+    auto begin_sequence = [&](int t) {
+        const ScanPlace r = t >= q.begin && t < q.end ? q : scan_place(p.ax, t);
+        // a sequence that runs on behind the piece: its starting state was put aside by the pass
+        // before, since the block that ends it may already have written h_out
+        if (!SUMMARY && p.h_in && p.pc.pps != 1 && p.pc.count > 1 && r.end > t1) {
+            get(p.piece_init, piece);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float v[NPT];
+                scan_h_load<NPT>(p, p.h_in, seq_slot(p.sl, r.s), d[e], n0, v);
+#pragma unroll
+                for (int k = 0; k < NPT / 2; ++k) h[e][k] = make_float2(v[2 * k], v[2 * k + 1]);
+            }
+        }
+        if (SUMMARY && p.h_in) put(p.piece_init, piece);
+        total = make_float2(0.f, 0.f);
+    };
+    auto end_sequence = [&](int t) {
+        if (SUMMARY || !p.h_out) return;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            float v[NPT];
+#pragma unroll
+            for (int k = 0; k < NPT / 2; ++k) unpack(h[e][k], v[2 * k], v[2 * k + 1]);
+            if (on[e]) scan_h_store<NPT>(p, p.h_out, scan_slot(p.ax, p.sl, t, q), d[e], n0, v);
+        }
+    };
+    // one token from its row in the stage and its rows of B and C in shared memory
+    auto token = [&](const T* xs, const T* dts, const T* zs, const float* b, const float* cc) {
+        const float2 x = seq_ld2(xs + c), raw = sum2(seq_ld2(dts + c), bias);
+        float2 delta = softplus2(raw, nullptr);
+        if (!p.softplus) delta = raw;
+        const float2 u = mul2(delta, x);
+        const float2 dl[2] = {dup2(delta.x), dup2(delta.y)}, uu[2] = {dup2(u.x), dup2(u.y)};
+        float2 acc[2][2];
+#pragma unroll
+        for (int k = 0; k < NPT / 2; k += 2) {
+            float2 bk[2], ck[2];
+            ld2(b + n0 + 2 * k, bk[0], bk[1]);
+            if (!SUMMARY) ld2(cc + n0 + 2 * k, ck[0], ck[1]);
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    h[e][k + j] = fma2(exp2_2(mul2(dl[e], A2[e][k + j])), h[e][k + j], mul2(uu[e], bk[j]));
+                    if (!SUMMARY) acc[e][j] = k ? fma2(ck[j], h[e][k + j], acc[e][j]) : mul2(ck[j], h[e][k + j]);
+                }
+        }
+        total = sum2(total, delta);
+        if (!SUMMARY) {
+            const float2 s0 = sum2(acc[0][0], acc[0][1]), s1 = sum2(acc[1][0], acc[1][1]);
+            float2 y = make_float2(s0.x + s0.y, s1.x + s1.y);
+#pragma unroll
+            for (int o = LN / 2; o > 0; o >>= 1)
+                y = sum2(y, make_float2(__shfl_xor_sync(~0u, y.x, o), __shfl_xor_sync(~0u, y.y, o)));
+            y = fma2(Dd, x, y);
+            if (GATED) {
+                const float2 z = seq_ld2(zs + c);
+                y = mul2(y, make_float2(silu(z.x), silu(z.y)));
+            }
+            if (ln == 0) {
+                seq_st2(yp, y, on[1] && p.wide == 16, on[0]);
+                if (on[1] && p.wide != 16) seq_st(yp + 1, y.y);
+            }
+            yp += p.y_ld;
+        }
+    };
+    if (!SUMMARY && q.begin < t0) get(p.piece_state, piece);      // the state that the pieces before leave
+    int buf = 0, stage = 0;
+    for (int tb = t0; tb < t1; tb += SCAN_TILE, buf ^= 1) {
+        const int n = min(SCAN_TILE, t1 - tb);
+        Br.store(sB[buf], p.N);
+        if (!SUMMARY) Cr.store(sC[buf], p.N);
+        copies_wait<STAGES - 2>();
         __syncthreads();
-        const unsigned first = sb.first, last = sb.last;
-        for (int i = 0; i < n; ++i) {
-            const long long t = tb + i;
-            if (first >> i & 1) {
-                const int s = sb.seq[i];
-                // a sequence that runs on behind the piece: its starting state was put aside by the
-                // pass before, since the block that ends it may already have written h_out
-                if (!SUMMARY && p.h_in && p.pc.pps != 1 && p.pc.count > 1 && seq_start(p.ax, s + 1, 0) > t1) {
+        // into the stage that the tile before this one used: every thread is past it
+        fetch(tb + (STAGES - 1) * SCAN_TILE, stage == 0 ? STAGES - 1 : stage - 1);
+        if (tb + SCAN_TILE < t1) fetch_bc(tb + SCAN_TILE);
+        const ScanMarks m = scan_marks(p.ax, tb, n, q);
+        if (m.first & 1) begin_sequence(tb);
+        if (!SUMMARY && p.saved) put(p.saved, scan_tile_row(p.ax, tb));
+        const T(*xs)[CB] = sx[stage], (*dts)[CB] = sdt[stage], (*zs)[CB] = sz[GATED ? stage : 0];
+        if (n == SCAN_TILE && !(m.first >> 1)) {
 #pragma unroll
-                    for (int k = 0; k < NPT; ++k)
-                        h[k] = n0 + k < p.N ? p.piece_init[scan_state_at(p, piece, (n0 + k) >> 2, d) + (k & 3)] : 0.f;
-                } else {
-                    scan_h_load<NPT>(p, p.h_in, seq_slot(p.sl, s), d, n0, h);
-                }
-                if (SUMMARY && on && p.h_in) {
-#pragma unroll
-                    for (int k = 0; k < NPT; ++k)
-                        if (n0 + k < p.N) p.piece_init[scan_state_at(p, piece, (n0 + k) >> 2, d) + (k & 3)] = h[k];
-                }
-                total = 0.f;
+            for (int i = 0; i < SCAN_TILE; ++i) token(xs[i], dts[i], zs[GATED ? i : 0], sB[buf][i], sC[buf][SUMMARY ? 0 : i]);
+            if (m.last) end_sequence(tb + n - 1);
+        } else {                                        // a short tile, or one that sequences begin in
+#pragma unroll 1
+            for (int i = 0; i < n; ++i) {
+                if (i > 0 && (m.first >> i & 1)) begin_sequence(tb + i);
+                token(xs[i], dts[i], zs[GATED ? i : 0], sB[buf][i], sC[buf][SUMMARY ? 0 : i]);
+                if (m.last >> i & 1) end_sequence(tb + i);
             }
-            if (!SUMMARY && i == 0 && p.saved && on) {
-                const long long row = scan_tile_row(p.ax, tb);
-#pragma unroll
-                for (int k = 0; k < NPT; ++k)
-                    if (n0 + k < ((p.N + 3) & ~3)) p.saved[scan_state_at(p, row, (n0 + k) >> 2, d) + (k & 3)] = h[k];
-            }
-            const float xv = seq_ld(x + t * p.x_ld);
-            float delta = seq_ld(dt + t * p.dt_ld) + bias;
-            if (p.softplus) delta = softplus(delta);
-            const float u = delta * xv;
-            float acc = 0.f;
-#pragma unroll
-            for (int k = 0; k < NPT; ++k) {
-                h[k] = fmaf(ex2_approx(delta * A2[k]), h[k], u * sB[i][n0 + k]);
-                if (!SUMMARY) acc = fmaf(sC[i][n0 + k], h[k], acc);
-            }
-            total += delta;
-            if (!SUMMARY) {
-#pragma unroll
-                for (int o = LN / 2; o > 0; o >>= 1) acc += __shfl_xor_sync(~0u, acc, o);
-                if (ln == 0 && on) {
-                    float v = fmaf(Dd, xv, acc);
-                    if (p.z) v *= silu(seq_ld(z + t * p.z_ld));
-                    seq_st(y + t * p.y_ld, v);
-                }
-                if ((last >> i & 1) && on) scan_h_store<NPT>(p, p.h_out, seq_slot(p.sl, sb.seq[i]), d, n0, h);
-            }
+        }
+        stage = stage == STAGES - 1 ? 0 : stage + 1;
+    }
+    if (SUMMARY) {
+        put(p.piece_state, piece);
+        if (ln == 0) {
+            if (on[0]) p.piece_delta[(long long)piece * p.D + d[0]] = total.x;
+            if (on[1]) p.piece_delta[(long long)piece * p.D + d[1]] = total.y;
         }
     }
-    if (SUMMARY && on) {
+}
+
+// Joins the pieces of a sequence (of a ragged axis): with e_r what piece r adds to the state behind it and
+// sum_r its sum of delta, the state before piece r + 1 is c_{r+1} = e_r + exp(sum_r A) c_r, or e_r alone where
+// a sequence begins in piece r (backward: the same from the last piece down).  A thread has 4 states of a
+// channel and replaces e_r by c_r, a batch of pieces at a time so that their loads overlap.
+template <bool REVERSE>
+__global__ void __launch_bounds__(STEP_THREADS) seq_scan_join_kernel(const __grid_constant__ SeqScanParams p) {
+    const int pieces = p.pc.pps > 0 ? p.pc.pps : p.pc.count, first = blockIdx.y * pieces;
+    // which pieces cut the chain: lane l looks at pieces l and l + 32
+    unsigned long long cut = 0;
 #pragma unroll
-        for (int k = 0; k < NPT; ++k)
-            if (n0 + k < ((p.N + 3) & ~3)) p.piece_state[scan_state_at(p, piece, (n0 + k) >> 2, d) + (k & 3)] = h[k];
-        if (ln == 0) p.piece_delta[(long long)piece * p.D + d] = total;
+    for (int half = 0; half < 2; ++half) {
+        const int r = half * 32 + (threadIdx.x & 31);
+        bool stop = false;
+        if (r < pieces) {
+            int t0, t1;
+            scan_piece_range(p.ax, p.pc, first + r, t0, t1);
+            const int s = seq_first_at(p.ax, REVERSE ? t0 + 1 : t0);      // the first sequence that begins in the piece (behind its first token)
+            const int begin = seq_start(p.ax, s, t0);
+            stop = REVERSE ? begin <= t1 : begin < t1;
+        }
+        cut |= (unsigned long long)__ballot_sync(~0u, stop) << (32 * half);
+    }
+    const int quads = (p.N + 3) >> 2;
+    const long long i = blockIdx.x * (long long)STEP_THREADS + threadIdx.x;
+    if (i >= (long long)quads * p.D) return;
+    const int quad = (int)(i / p.D), d = (int)(i - (long long)quad * p.D);
+    float A2[4], c[4] = {};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) A2[k] = 4 * quad + k < p.N ? p.A[(long long)d * p.N + 4 * quad + k] * LOG2E : 0.f;
+    constexpr int BATCH = 8;
+    for (int r0 = 0; r0 < pieces; r0 += BATCH) {
+        float4 e[BATCH];
+        float sum[BATCH];
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j) {
+            const int r = r0 + j;
+            e[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+            sum[j] = 0.f;
+            if (r < pieces - 1) {                    // (the last piece hands nothing on)
+                const int at = REVERSE ? pieces - 1 - r : r;
+                e[j] = *reinterpret_cast<const float4*>(p.piece_state + scan_state_at(p, first + at, quad, d));
+                sum[j] = p.piece_delta[(long long)(first + at) * p.D + d];
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j) {
+            const int r = r0 + j, at = REVERSE ? pieces - 1 - r : r;
+            if (r >= pieces) break;
+            *reinterpret_cast<float4*>(p.piece_state + scan_state_at(p, first + at, quad, d)) = make_float4(c[0], c[1], c[2], c[3]);
+            const float v[4] = {e[j].x, e[j].y, e[j].z, e[j].w};
+            const bool stop = cut >> at & 1;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) c[k] = stop ? v[k] : fmaf(ex2_approx(sum[j] * A2[k]), c[k], v[k]);
+        }
     }
 }
 
@@ -139,8 +291,8 @@ __global__ void __launch_bounds__(128) seq_scan_empty_kernel(SeqAxis ax, SeqSlot
 // One token per sequence.  A lane holds 4 states of a channel (16 bytes of its state row), LN lanes
 // share the channel.
 template <typename T, int LN>
-__global__ void __launch_bounds__(THREADS) seq_scan_step_kernel(const __grid_constant__ SeqScanParams p) {
-    const int d0 = (blockIdx.x * THREADS + threadIdx.x) / LN;
+__global__ void __launch_bounds__(STEP_THREADS) seq_scan_step_kernel(const __grid_constant__ SeqScanParams p) {
+    const int d0 = (blockIdx.x * STEP_THREADS + threadIdx.x) / LN;
     const bool on = d0 < p.D;
     const int d = on ? d0 : p.D - 1;
     const int n0 = threadIdx.x % LN * 4, g = d / (p.D / p.G);
@@ -177,15 +329,17 @@ __global__ void __launch_bounds__(THREADS) seq_scan_step_kernel(const __grid_con
 
 template <typename T, int NPT, int LN>
 cudaError_t launch_fwd(const SeqScanParams& p, cudaStream_t stream) {
-    constexpr int CB = THREADS / LN;
+    constexpr int CB = 2 * THREADS / LN;
     const int per = p.D / p.G;
     const dim3 grid((unsigned)p.pc.count, (unsigned)(p.G * ((per + CB - 1) / CB)));
     cudaError_t e = cudaSuccess;
     if (p.ax.T > 0) {
         if (p.pc.pps != 1 && p.pc.count > 1)
-            e = launch_kernel(seq_scan_kernel<T, NPT, LN, true>, grid, dim3(THREADS), 0, stream, false, 1, p);
+            e = launch_kernel(seq_scan_kernel<T, NPT, LN, true, false>, grid, dim3(THREADS), 0, stream, false, 1, p);
+        if (e == cudaSuccess && p.pc.pps != 1 && p.pc.count > 1) e = launch_seq_scan_join(p, false, stream);
         if (e == cudaSuccess)
-            e = launch_kernel(seq_scan_kernel<T, NPT, LN, false>, grid, dim3(THREADS), 0, stream, false, 1, p);
+            e = p.z ? launch_kernel(seq_scan_kernel<T, NPT, LN, false, true>, grid, dim3(THREADS), 0, stream, false, 1, p)
+                    : launch_kernel(seq_scan_kernel<T, NPT, LN, false, false>, grid, dim3(THREADS), 0, stream, false, 1, p);
     }
     if (e == cudaSuccess && p.h_out && p.h_out != p.h_in && p.ax.L == 0) e = launch_seq_scan_empty(p, p.h_in, p.h_out, stream);
     return e;
@@ -203,8 +357,8 @@ cudaError_t launch_t(const SeqScanParams& p, cudaStream_t stream) {
 
 template <typename T, int LN>
 cudaError_t launch_step(const SeqScanParams& p, cudaStream_t stream) {
-    const dim3 grid((unsigned)(((long long)p.D * LN + THREADS - 1) / THREADS), (unsigned)(p.ax.S < 32768 ? p.ax.S : 32768));
-    return launch_kernel(seq_scan_step_kernel<T, LN>, grid, dim3(THREADS), 0, stream, false, 1, p);
+    const dim3 grid((unsigned)(((long long)p.D * LN + STEP_THREADS - 1) / STEP_THREADS), (unsigned)(p.ax.S < 32768 ? p.ax.S : 32768));
+    return launch_kernel(seq_scan_step_kernel<T, LN>, grid, dim3(STEP_THREADS), 0, stream, false, 1, p);
 }
 template <typename T>
 cudaError_t launch_step_t(const SeqScanParams& p, cudaStream_t stream) {
@@ -218,6 +372,12 @@ cudaError_t launch_step_t(const SeqScanParams& p, cudaStream_t stream) {
 
 }  // namespace
 
+cudaError_t launch_seq_scan_join(const SeqScanParams& p, bool reverse, cudaStream_t stream) {
+    const long long all = (long long)((p.N + 3) / 4) * p.D;
+    const dim3 grid((unsigned)((all + STEP_THREADS - 1) / STEP_THREADS), (unsigned)(p.pc.pps > 0 ? p.ax.S : 1));
+    return reverse ? launch_kernel(seq_scan_join_kernel<true>, grid, dim3(STEP_THREADS), 0, stream, false, 1, p)
+                   : launch_kernel(seq_scan_join_kernel<false>, grid, dim3(STEP_THREADS), 0, stream, false, 1, p);
+}
 cudaError_t launch_seq_scan_empty(const SeqScanParams& p, const float* from, float* to, cudaStream_t stream) {
     const long long DN = (long long)p.D * p.N, blocks = DN / 1024 + 1;
     return launch_kernel(seq_scan_empty_kernel, dim3((unsigned)(blocks < 64 ? blocks : 64), (unsigned)(p.ax.S < 32768 ? p.ax.S : 32768)),

@@ -12,28 +12,46 @@ __device__ __forceinline__ long long scan_state_at(const SeqScanParams& p, long 
     return ((row * ((p.N + 3) >> 2) + quad) * p.D + d) * 4;
 }
 
-// Where sequences begin and end among the tokens t0 .. t0 + n - 1 of a tile: bit i of `first`
-// (`last`) is set when token t0 + i is the first (last) of its sequence, seq[i].
-struct ScanBounds {
-    unsigned first, last;
-    int seq[SCAN_TILE];
+// The sequence at hand while a block walks the tokens of a piece, in either direction.  Every thread
+// holds the same values.
+struct ScanPlace {
+    int s, begin, end;
 };
-// Called by one whole warp.
-__device__ __forceinline__ void scan_bounds(const SeqAxis& ax, int t0, int n, ScanBounds* out) {
-    const int i = threadIdx.x & 31;
+__device__ __forceinline__ ScanPlace scan_place(const SeqAxis& ax, int t) {
+    ScanPlace q;
+    q.s = seq_first_at(ax, t + 1) - 1;       // the last sequence that starts at or before t
+    q.begin = q.s < 0 ? 0 : seq_start(ax, q.s, 0);
+    q.end = seq_start(ax, q.s + 1, t + 1);
+    return q;
+}
+// Where sequences begin and end among the tokens t0 .. t0 + n - 1 of a tile: bit i of `first`
+// (`last`) is set when token t0 + i is the first (last) of its sequence.  Most tiles lie within the
+// sequence at hand and need no look at the bounds.
+struct ScanMarks {
+    unsigned first, last;
+};
+__device__ __forceinline__ ScanMarks scan_marks(const SeqAxis& ax, int t0, int n, ScanPlace& q) {
+    ScanMarks m = {0u, 0u};
+    if (t0 < q.begin || t0 >= q.end) q = scan_place(ax, t0);
+    if (q.s >= 0 && q.begin == t0) m.first = 1u;
+    if (t0 + n <= q.end) {
+        if (q.s >= 0 && t0 + n == q.end) m.last = 1u << (n - 1);
+        return m;
+    }
+    const int lane = threadIdx.x & 31;
     bool f = false, l = false;
-    if (i < n) {
-        const int t = t0 + i;
-        const int s = seq_first_at(ax, t + 1) - 1;
-        f = s >= 0 && seq_start(ax, s, 0) == t;
-        l = s >= 0 && seq_start(ax, s + 1, t + 1) == t + 1;
-        out->seq[i] = s;
+    if (lane < n) {
+        const ScanPlace r = scan_place(ax, t0 + lane);
+        f = r.s >= 0 && r.begin == t0 + lane;
+        l = r.s >= 0 && r.end == t0 + lane + 1;
     }
-    const unsigned mf = __ballot_sync(~0u, f), ml = __ballot_sync(~0u, l);
-    if (i == 0) {
-        out->first = mf;
-        out->last = ml;
-    }
+    m.first = __ballot_sync(~0u, f);
+    m.last = __ballot_sync(~0u, l);
+    return m;
+}
+// The slot of the sequence that token t belongs to.
+__device__ __forceinline__ long long scan_slot(const SeqAxis& ax, const SeqSlots& sl, int t, const ScanPlace& q) {
+    return seq_slot(sl, t >= q.begin && t < q.end ? q.s : seq_first_at(ax, t + 1) - 1);
 }
 
 // The states (d, n0 .. n0 + NPT - 1) of a row of h_in / h_out: D x N fp32 values.
@@ -49,5 +67,25 @@ __device__ __forceinline__ void scan_h_store(const SeqScanParams& p, float* h, l
     for (int k = 0; k < NPT; ++k)
         if (n0 + k < p.N) h[(slot * p.D + d) * p.N + n0 + k] = v[k];
 }
+
+// Packed fp32 pairs.  The compiler's own f32x2 operations on float2 keep a loop's values in place;
+// the same instructions written as asm on 64-bit values cost a register move for each value carried
+// from one token to the next (measured: 66 moves a token in the backward kernel).
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 sum2(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 dup2(float a) { return make_float2(a, a); }
+__device__ __forceinline__ float2 exp2_2(float2 v) { return make_float2(ex2_approx(v.x), ex2_approx(v.y)); }
+__device__ __forceinline__ void unpack(float2 v, float& a, float& b) {
+    a = v.x;
+    b = v.y;
+}
+// Two pairs from 16 bytes.
+__device__ __forceinline__ void ld2(const float* p, float2& a, float2& b) {
+    const float4 v = *reinterpret_cast<const float4*>(p);
+    a = make_float2(v.x, v.y);
+    b = make_float2(v.z, v.w);
+}
+__device__ __forceinline__ void st2(float* p, float2 a, float2 b) { *reinterpret_cast<float4*>(p) = make_float4(a.x, a.y, b.x, b.y); }
 
 }  // namespace convfwd
