@@ -35,6 +35,7 @@ struct seq_plan {
     unsigned flags;
     int S, T, D, L;        // L: tokens per sequence, 0 when ragged (or T = 0)
     int W, N, G;
+    int run;               // conv: tokens a thread walks
     int sms;
     ScanPieces pc;
     int blocks;            // conv backward: token blocks; scan backward: channel blocks; norm backward: partial rows
@@ -191,12 +192,13 @@ conv_status seq_conv_plan_create(seq_plan_t* out, int64_t S, int64_t T, int64_t 
     seq_plan* p = new_plan(Op::Conv, S, T, D, dtype, direction, flags);
     if (!p) return CONV_ERR_INVALID_ARG;
     p->W = (int)W;
+    p->run = seq_conv_run(T, p->D, p->sms);
     if (direction == SEQ_BWD) {
-        p->blocks = seq_conv_bwd_token_blocks(T);
+        p->blocks = seq_conv_bwd_token_blocks(T, p->run);
         p->ws_bytes = align256((size_t)(p->blocks > 0 ? p->blocks : 1) * (W + 1) * D * sizeof(float));
     }
-    snprintf(p->desc, sizeof p->desc, "op=conv direction=%s dtype=%s sequences=%d tokens=%d ragged=%d width=%d taps=%d silu=%d blocks=%d",
-             dir_name(direction), type_name(dtype), p->S, p->T, p->ragged(), p->D, p->W, !!(flags & SEQ_CONV_SILU), p->blocks);
+    snprintf(p->desc, sizeof p->desc, "op=conv direction=%s dtype=%s sequences=%d tokens=%d ragged=%d width=%d taps=%d silu=%d run=%d blocks=%d",
+             dir_name(direction), type_name(dtype), p->S, p->T, p->ragged(), p->D, p->W, !!(flags & SEQ_CONV_SILU), p->run, p->blocks);
     *out = p;
     return CONV_OK;
 }
@@ -231,6 +233,7 @@ static conv_status conv_call(seq_plan_t p, const seq_conv_args* a, seq_direction
     q.dy = a->dy; q.dx = a->dx; q.dw = a->dw; q.dbias = a->dbias;
     q.x_ld = a->x_ld; q.y_ld = a->y_ld; q.dy_ld = a->dy_ld; q.dx_ld = a->dx_ld;
     q.ws = static_cast<float*>(p->ws);
+    q.run = p->run;
     q.tblocks = p->blocks;
     q.vec = c.wide && (p->D * e) % 16 == 0;
     const bool bf16 = p->dtype == CONV_BF16;
@@ -374,8 +377,8 @@ conv_status seq_norm_plan_create(seq_plan_t* out, int64_t rows, int64_t D, conv_
     p->res_dtype = res_dtype;
     p->eps = eps;
     if (direction == SEQ_BWD) {
-        p->blocks = seq_norm_bwd_blocks(p->T, p->D, p->sms);
-        p->ws_bytes = align256((size_t)p->blocks * 5 * D * sizeof(float));
+        p->blocks = seq_norm_bwd_blocks(p->T, p->D, flags, (int)p->esize(), (int)p->rsize(), p->sms);
+        p->ws_bytes = align256((size_t)p->blocks * 4 * D * sizeof(float));
     }
     snprintf(p->desc, sizeof p->desc, "op=norm direction=%s dtype=%s residual=%s rows=%d width=%d kind=%s post=%d pre=%d gate=%s partial_rows=%d",
              dir_name(direction), type_name(dtype), flags & SEQ_NORM_RESIDUAL ? type_name(res_dtype) : "none", p->T, p->D,
@@ -439,7 +442,6 @@ static conv_status norm_call(seq_plan_t p, const seq_norm_args* a, seq_direction
     q.x_ld = a->x_ld; q.gate_ld = a->gate_ld; q.res_ld = a->res_ld; q.y_ld = a->y_ld; q.res_out_ld = a->res_out_ld;
     q.dy_ld = a->dy_ld; q.dres_out_ld = a->dres_out_ld; q.dx_ld = a->dx_ld; q.dgate_ld = a->dgate_ld; q.dres_ld = a->dres_ld;
     q.ws = sums ? static_cast<float*>(p->ws) : nullptr;
-    q.blocks = p->blocks;
     q.vec = c.wide && p->D % 8 == 0;
     q.sms = p->sms;
     const bool bf16 = p->dtype == CONV_BF16, rbf16 = p->res_dtype == CONV_BF16;

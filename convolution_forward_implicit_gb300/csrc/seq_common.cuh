@@ -22,8 +22,8 @@ __device__ __forceinline__ uint32_t bf2_pack(float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// V consecutive elements <-> fp32 registers; V > 1 needs V * sizeof(T) a multiple of 16 and the
-// address 16-byte aligned.
+// V consecutive elements <-> fp32 registers; V > 1: whole
+// 16-byte groups (or 8 bytes: 4 bf16) at an address aligned to them.
 template <int V>
 __device__ __forceinline__ void seq_ldv(const float* p, float (&v)[V]) {
     if constexpr (V % 4 == 0) {
@@ -48,6 +48,10 @@ __device__ __forceinline__ void seq_ldv(const __nv_bfloat16* p, float (&v)[V]) {
             bf2_unpack(q.z, v[8 * i + 4], v[8 * i + 5]);
             bf2_unpack(q.w, v[8 * i + 6], v[8 * i + 7]);
         }
+    } else if constexpr (V == 4) {
+        const uint2 q = *reinterpret_cast<const uint2*>(p);
+        bf2_unpack(q.x, v[0], v[1]);
+        bf2_unpack(q.y, v[2], v[3]);
     } else {
 #pragma unroll
         for (int i = 0; i < V; ++i) v[i] = __bfloat162float(p[i]);
@@ -59,6 +63,8 @@ __device__ __forceinline__ void seq_stv(float* p, const float (&v)[V]) {
 #pragma unroll
         for (int i = 0; i < V / 4; ++i)
             reinterpret_cast<float4*>(p)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    } else if constexpr (V == 2) {
+        *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]);
     } else {
 #pragma unroll
         for (int i = 0; i < V; ++i) p[i] = v[i];
@@ -72,6 +78,8 @@ __device__ __forceinline__ void seq_stv(__nv_bfloat16* p, const float (&v)[V]) {
             reinterpret_cast<uint4*>(p)[i] =
                 make_uint4(bf2_pack(v[8 * i], v[8 * i + 1]), bf2_pack(v[8 * i + 2], v[8 * i + 3]),
                            bf2_pack(v[8 * i + 4], v[8 * i + 5]), bf2_pack(v[8 * i + 6], v[8 * i + 7]));
+    } else if constexpr (V == 4) {
+        *reinterpret_cast<uint2*>(p) = make_uint2(bf2_pack(v[0], v[1]), bf2_pack(v[2], v[3]));
     } else {
 #pragma unroll
         for (int i = 0; i < V; ++i) p[i] = __float2bfloat16_rn(v[i]);
@@ -164,6 +172,31 @@ __device__ __forceinline__ void rows_to_shared(T (*to)[W], const T* from, long l
     } else {
         rows_to_shared_odd<T, ROWS, W, THREADS>(to, from, ld, n, width, grain);
     }
+}
+
+// Sum of the values at `rows` rows `step` apart, of 32 neighbouring columns (`src`: the column of lane
+// threadIdx.x & 31) by a block of COLUMN_THREADS: warps take turns at the rows, then the first warp adds their
+// sums in order and holds the result.  Called by the whole block.
+constexpr int COLUMN_THREADS = 512;
+__device__ __forceinline__ float column_sum(const float* src, long long step, int rows, bool on) {
+    constexpr int WARPS = COLUMN_THREADS / 32;
+    __shared__ float part[WARPS][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float s[4] = {};
+    if (on) {
+        int r = warp;
+        for (; r + 3 * WARPS < rows; r += 4 * WARPS)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[i] += src[(r + i * WARPS) * step];
+        for (; r < rows; r += WARPS) s[0] += src[r * step];
+    }
+    part[warp][lane] = (s[0] + s[1]) + (s[2] + s[3]);
+    __syncthreads();
+    float v = 0.f;
+    if (warp == 0)
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) v += part[w][lane];
+    return v;
 }
 
 // softplus and, if wanted, its derivative sigmoid(v) of two values: see softplus.

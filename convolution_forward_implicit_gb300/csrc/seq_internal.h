@@ -56,13 +56,15 @@ struct SeqConvParams {
     float *dw, *dbias;
     float* ws;                      // backward: partial sums [token blocks][W + 1][D]
     long long x_ld, y_ld, dy_ld, dx_ld;
+    int run;                        // tokens a thread walks (whole sequences)
     int tblocks;                    // backward: token blocks
     int vec;                        // 1: 16-byte rows
 };
 cudaError_t launch_seq_conv_fwd(const SeqConvParams& p, bool bf16, cudaStream_t stream);
 cudaError_t launch_seq_conv_bwd(const SeqConvParams& p, bool bf16, cudaStream_t stream);
 cudaError_t launch_seq_conv_step(const SeqConvParams& p, bool bf16, cudaStream_t stream);
-int seq_conv_bwd_token_blocks(long long T);
+int seq_conv_run(long long T, int D, int sms);
+int seq_conv_bwd_token_blocks(long long T, int run);
 
 // ---- selective scan ----
 constexpr int SCAN_TILE = 8;        // tokens between two saved states
@@ -131,13 +133,12 @@ struct SeqNormParams {
     void *y, *res_out, *dx, *dgate, *dres;
     float *dw_post, *db_post, *dscale, *dw_pre, *db_pre;
     long long x_ld, gate_ld, res_ld, y_ld, res_out_ld, dy_ld, dres_out_ld, dx_ld, dgate_ld, dres_ld;
-    float* ws;                      // backward: [blocks][5][D] partial parameter gradients
-    int blocks;                     // backward: thread blocks
+    float* ws;                      // backward: [rows of partial sums][4][D]
     int vec;                        // 1: rows of whole 16-byte aligned groups of 8
     int sms;
 };
 cudaError_t launch_seq_norm_fwd(const SeqNormParams& p, bool bf16, bool res_bf16, cudaStream_t stream);
 cudaError_t launch_seq_norm_bwd(const SeqNormParams& p, bool bf16, bool res_bf16, cudaStream_t stream);
-int seq_norm_bwd_blocks(int rows, int D, int sms);
+int seq_norm_bwd_blocks(int rows, int D, unsigned flags, int esize, int rsize, int sms);
 
 }  // namespace convfwd

@@ -1,89 +1,70 @@
 // Norm, gate and residual around a block, forward: see seq.h for the formulas.  Bound by bytes: each
-// row is read once into registers, normalised there (up to twice) and written once.
+// row is read once into registers (all of its tensors before the first sum), normalised there, up to twice,
+// and written once.  A block has one row, or several narrow ones; many blocks on an SM hide the barriers of
+// each other's sums.
 #include "seq_norm.cuh"
 
 namespace convfwd {
 namespace {
 
-template <typename T, typename RT, bool WIDE, int UPT>
-__global__ void __launch_bounds__(1024) seq_norm_fwd_kernel(const __grid_constant__ SeqNormParams p) {
-    __shared__ float buf[2][32][2];
+template <typename T, typename RT, bool WIDE, int UPT, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) seq_norm_fwd_kernel(const __grid_constant__ SeqNormParams p) {
+    __shared__ __align__(16) NormSums buf;
     int turn = 0;
-    const int row = blockIdx.x * blockDim.y + threadIdx.y;
-    const bool on = row < p.rows;
-    const int D = on ? p.D : 0;            // a row behind the last one has no columns
-    const bool layer = p.flags & SEQ_NORM_LAYER;
-    float v[UPT][8], a[UPT][8], b[UPT][8];
-    row_load<T, WIDE, UPT>(p.x, (long long)row * p.x_ld, D, v);
-    if (p.flags & (SEQ_NORM_GATE_BEFORE | SEQ_NORM_GATE_AFTER)) {
-        row_load<T, WIDE, UPT>(p.gate, (long long)row * p.gate_ld, D, b);
-#pragma unroll
-        for (int u = 0; u < UPT; ++u)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) b[u][e] = silu(b[u][e]);
-    }
+    const long long row = (long long)blockIdx.x * blockDim.y + threadIdx.y;
+    const int D = row < p.rows ? p.D : 0;            // a row behind the last one has no columns
+    const bool layer = p.flags & SEQ_NORM_LAYER, gate = p.flags & (SEQ_NORM_GATE_BEFORE | SEQ_NORM_GATE_AFTER);
+    const bool residual = p.flags & SEQ_NORM_RESIDUAL;
+    // all of the row is on its way before the first sum
+    RowIn<T, WIDE, UPT> x_in, g_in;
+    RowIn<RT, WIDE, UPT> r_in;
+    x_in.load(p.x, row * p.x_ld, D);
+    if (gate) g_in.load(p.gate, row * p.gate_ld, D);
+    if (residual) r_in.load(p.res, row * p.res_ld, D);
+    row_sum_init(buf);
+    float2 v[UPT][4], a[UPT][4];
+    x_in.get(v);
     if (p.flags & SEQ_NORM_GATE_BEFORE) {
-#pragma unroll
-        for (int u = 0; u < UPT; ++u)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[u][e] *= b[u][e];
+        g_in.get(a);
+        EACH_PAIR v[u][e] = pmul(v[u][e], silu2(a[u][e]));
     }
     if (p.flags & SEQ_NORM_POST) {
         row_norm(v, p.D, layer, p.eps, buf, turn);
-        col_load<T, WIDE, UPT>(p.w_post, 1.f, D, a);
-#pragma unroll
-        for (int u = 0; u < UPT; ++u)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[u][e] *= a[u][e];
-        if (p.b_post) {
-            col_load<T, WIDE, UPT>(p.b_post, 0.f, D, a);
-#pragma unroll
-            for (int u = 0; u < UPT; ++u)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[u][e] += a[u][e];
-        }
+        col_mul<T, WIDE, UPT>(p.w_post, D, v);
+        col_add<T, WIDE, UPT>(p.b_post, D, v);
     }
     if (p.flags & SEQ_NORM_GATE_AFTER) {
-#pragma unroll
-        for (int u = 0; u < UPT; ++u)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[u][e] *= b[u][e];
+        g_in.get(a);
+        EACH_PAIR v[u][e] = pmul(v[u][e], silu2(a[u][e]));
     }
-    if (p.scale) {
-        col_load<T, WIDE, UPT>(p.scale, 1.f, D, a);
-#pragma unroll
-        for (int u = 0; u < UPT; ++u)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[u][e] *= a[u][e];
-    }
-    if (p.flags & SEQ_NORM_RESIDUAL) {
-        row_load<RT, WIDE, UPT>(p.res, (long long)row * p.res_ld, D, a);
-#pragma unroll
-        for (int u = 0; u < UPT; ++u)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[u][e] += a[u][e];
-        row_store<RT, WIDE, UPT>(p.res_out, (long long)row * p.res_out_ld, D, v);
+    col_mul<T, WIDE, UPT>(p.scale, D, v);
+    if (residual) {
+        r_in.get(a);
+        EACH_PAIR v[u][e] = padd(v[u][e], a[u][e]);
+        row_store<RT, WIDE, UPT>(p.res_out, row * p.res_out_ld, D, v);
     }
     if (p.flags & SEQ_NORM_PRE) {
         row_norm(v, p.D, layer, p.eps, buf, turn);
-        col_load<T, WIDE, UPT>(p.w_pre, 1.f, D, a);
-        col_load<T, WIDE, UPT>(p.b_pre, 0.f, D, b);
-#pragma unroll
-        for (int u = 0; u < UPT; ++u)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[u][e] = fmaf(v[u][e], a[u][e], b[u][e]);
+        col_mul<T, WIDE, UPT>(p.w_pre, D, v);
+        col_add<T, WIDE, UPT>(p.b_pre, D, v);
     }
-    if ((p.flags & SEQ_NORM_PRE) || !(p.flags & SEQ_NORM_RESIDUAL))
-        row_store<T, WIDE, UPT>(p.y, (long long)row * p.y_ld, D, v);
+    if ((p.flags & SEQ_NORM_PRE) || !residual) row_store<T, WIDE, UPT>(p.y, row * p.y_ld, D, v);
+}
+
+template <typename T, typename RT, bool WIDE, int UPT, int THREADS>
+cudaError_t launch_u(const SeqNormParams& p, cudaStream_t stream) {
+    const dim3 block = norm_block(p.D, UPT);
+    return launch_kernel(seq_norm_fwd_kernel<T, RT, WIDE, UPT, THREADS>, dim3((unsigned)((p.rows + block.y - 1) / block.y)), block, 0, stream,
+                         false, 1, p);
 }
 
 template <typename T, typename RT, bool WIDE>
 cudaError_t launch(const SeqNormParams& p, cudaStream_t stream) {
-    const int upt = p.D > 8192 ? 2 : 1;
-    const dim3 block = norm_block(p.D, upt, 128);
-    const dim3 grid((unsigned)((p.rows + block.y - 1) / block.y));
-    return upt == 2 ? launch_kernel(seq_norm_fwd_kernel<T, RT, WIDE, 2>, grid, block, 0, stream, false, 1, p)
-                    : launch_kernel(seq_norm_fwd_kernel<T, RT, WIDE, 1>, grid, block, 0, stream, false, 1, p);
+    // 8 values a thread keep more rows in flight; 16 halve what the sums cost each
+    if (p.D <= 2048) return launch_u<T, RT, WIDE, 1, 256>(p, stream);
+    if (p.D <= 4096) return p.rows < 4 * p.sms ? launch_u<T, RT, WIDE, 1, 512>(p, stream) : launch_u<T, RT, WIDE, 2, 256>(p, stream);
+    if (p.D <= 8192) return launch_u<T, RT, WIDE, 2, 512>(p, stream);
+    return launch_u<T, RT, WIDE, 2, 1024>(p, stream);
 }
 
 }  // namespace

@@ -1,6 +1,9 @@
 // Norm, gate and residual around a block, gradients.  With hat = norm(v), r = 1 / sqrt(...) and d the
 // gradient at w hat + b:  dw = sum_rows d hat, db = sum_rows d, and at v, with e = d w,
 //   dv = r (e - hat mean(e hat))           (RMS; layer: also less mean(e)).
+// The sums S1 = sum_rows d' hat and S0 = sum_rows d' over the rows of POST, with d' the gradient at r (times
+// silu(gate) where it comes after), serve three parameters: r = res + scale (w_post hat + b_post) gives
+//   dw_post = scale S1,   db_post = scale S0,   dscale = w_post S1 + b_post S0.
 // Bound by bytes.  A block keeps its share of the rows' parameter sums in registers (its threads stay
 // on their columns), writes them once, and a second kernel adds the blocks up in their order.
 #include "seq_norm.cuh"
@@ -8,178 +11,280 @@
 namespace convfwd {
 namespace {
 
-constexpr int SUMS = 5;      // w_post, b_post, scale, w_pre, b_pre
+constexpr int SUMS = 4;      // S1, S0, and those of w_pre and b_pre
 
 // e (the gradient behind w) -> the gradient at v, in place
 template <int UPT>
-__device__ __forceinline__ void norm_back(float (&d)[UPT][8], const float (&hat)[UPT][8], float r, int D, bool layer,
-                                          float (*buf)[32][2], int& turn) {
-    float s[2] = {};
-#pragma unroll
-    for (int u = 0; u < UPT; ++u)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            s[0] = fmaf(d[u][e], hat[u][e], s[0]);
-            s[1] += d[u][e];
+__device__ __forceinline__ void norm_back(float2 (&d)[UPT][4], const float2 (&hat)[UPT][4], float r, int D, bool layer,
+                                          NormSums& buf, int& turn) {
+    float c, m = 0.f;
+    const float inv = 1.0f / (float)D;
+    if (layer) {
+        float s[2] = {lane_dot(d, hat), lane_total(d)};
+        row_sum(s, buf, turn);
+        c = s[0] * inv;
+        m = s[1] * inv;
+    } else {
+        float s[1] = {lane_dot(d, hat)};
+        row_sum(s, buf, turn);
+        c = s[0] * inv;
+    }
+    // r (d - hat c - m)
+    EACH_PAIR d[u][e] = pmul(pdup(r), pfma(hat[u][e], pdup(-c), padd(d[u][e], pdup(-m))));
+    if (layer) {
+        EACH_PAIR {
+            const int at = (threadIdx.x + u * blockDim.x) * 8 + 2 * e;
+            if (at >= D) d[u][e].x = 0.f;
+            if (at + 1 >= D) d[u][e].y = 0.f;
         }
-    row_sum(s, buf, turn);
-    const float c = s[0] / (float)D, m = layer ? s[1] / (float)D : 0.f;
-#pragma unroll
-    for (int u = 0; u < UPT; ++u)
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if ((threadIdx.x + u * blockDim.x) * 8 + e < D) d[u][e] = r * (d[u][e] - fmaf(hat[u][e], c, m));
+    }
 }
 
-#define EACH_UE _Pragma("unroll") for (int u = 0; u < UPT; ++u) _Pragma("unroll") for (int e = 0; e < 8; ++e)
-
-template <typename T, typename RT, bool WIDE, int UPT, bool BIAS>
-__global__ void __launch_bounds__(1024) seq_norm_bwd_kernel(const __grid_constant__ SeqNormParams p) {
-    __shared__ float buf[2][32][2];
+// A block walks its rows.  RING: the next row is on its way to shared memory while this one is computed,
+// and what a row needs twice (x, gate) is taken from there twice.
+template <typename T, typename RT, bool WIDE, bool RING, int UPT, bool BIAS, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS <= 512 ? 512 / THREADS : 1) seq_norm_bwd_kernel(const __grid_constant__ SeqNormParams p) {
+    extern __shared__ __align__(16) unsigned char ring[];
+    __shared__ __align__(16) NormSums buf;
     int turn = 0;
     const bool layer = p.flags & SEQ_NORM_LAYER;
     const bool post = p.flags & SEQ_NORM_POST, pre = p.flags & SEQ_NORM_PRE, residual = p.flags & SEQ_NORM_RESIDUAL;
     const bool gate = p.flags & (SEQ_NORM_GATE_BEFORE | SEQ_NORM_GATE_AFTER), after = p.flags & SEQ_NORM_GATE_AFTER;
-    float s_wpost[UPT][8] = {}, s_bpost[UPT][8] = {}, s_scale[UPT][8] = {}, s_wpre[UPT][8] = {}, s_bpre[UPT][8] = {};
-    for (long long base = (long long)blockIdx.x * blockDim.y; base < p.rows; base += (long long)gridDim.x * blockDim.y) {
-        const long long row = base + threadIdx.y;
+    const bool has_dy = pre || !residual, has_dro = residual && p.dres_out, use_res = residual && pre;
+    constexpr int tb = row_bytes<T, UPT, THREADS>(), rb = row_bytes<RT, UPT, THREADS>();
+    // places in a stage: x, gate, dy, res, dres_out
+    const int at_g = tb, at_dy = at_g + (gate ? tb : 0), at_res = at_dy + (has_dy ? tb : 0), at_dro = at_res + (use_res ? rb : 0);
+    const int stage_bytes = at_dro + (has_dro ? rb : 0);
+    uint32_t mine = (uint32_t)__cvta_generic_to_shared(ring) + (threadIdx.y * blockDim.x + threadIdx.x) * 16;
+    asm volatile("" : "+r"(mine));             // (not to be worked out again at every use)
+    const long long step = (long long)gridDim.x * blockDim.y;
+    auto fetch = [&](long long row, int stage) {
+        if (!RING) return;
+        if (row < p.rows) {
+            const uint32_t at = mine + stage * stage_bytes;
+            row_copy<T, UPT, THREADS>(at, p.x, row * p.x_ld, p.D);
+            if (gate) row_copy<T, UPT, THREADS>(at + at_g, p.gate, row * p.gate_ld, p.D);
+            if (has_dy) row_copy<T, UPT, THREADS>(at + at_dy, p.dy, row * p.dy_ld, p.D);
+            if (use_res) row_copy<RT, UPT, THREADS>(at + at_res, p.res, row * p.res_ld, p.D);
+            if (has_dro) row_copy<RT, UPT, THREADS>(at + at_dro, p.dres_out, row * p.dres_out_ld, p.D);
+        }
+        copies_commit();
+    };
+    float2 s_1[UPT][4], s_0[UPT][4], s_wpre[UPT][4], s_bpre[UPT][4];
+    EACH_PAIR s_1[u][e] = s_0[u][e] = s_wpre[u][e] = s_bpre[u][e] = make_float2(0.f, 0.f);
+    long long row = (long long)blockIdx.x * blockDim.y + threadIdx.y;
+#pragma unroll
+    for (int i = 0; i < NORM_RING - 1; ++i) fetch(row + i * step, i);
+    int stage = 0;
+    Column<T, WIDE, UPT, THREADS <= 512> w_post, b_post, scale, w_pre;
+    w_post.open(p.w_post, p.D);
+    b_post.open(BIAS ? p.b_post : nullptr, p.D);
+    scale.open(p.scale, p.D);
+    w_pre.open(p.w_pre, p.D);
+    row_sum_init(buf);
+    for (long long base = (long long)blockIdx.x * blockDim.y; base < p.rows; base += step, row += step, stage = stage == NORM_RING - 1 ? 0 : stage + 1) {
+        fetch(row + (NORM_RING - 1) * step, stage == 0 ? NORM_RING - 1 : stage - 1);
         const int D = row < p.rows ? p.D : 0;
-        float x[UPT][8], g[UPT][8], hat[UPT][8], hat2[UPT][8], d[UPT][8], t[UPT][8];
-        float r_post = 0.f, r_pre = 0.f;
-        // the forward pass again: hat (POST), u in t, r in hat2 -> hat2 (PRE)
-        row_load<T, WIDE, UPT>(p.x, row * p.x_ld, D, x);
-        if (gate) row_load<T, WIDE, UPT>(p.gate, row * p.gate_ld, D, g);
-        EACH_UE hat[u][e] = gate && !after ? x[u][e] * silu(g[u][e]) : x[u][e];
-        if (post) r_post = row_norm(hat, p.D, layer, p.eps, buf, turn);
-        EACH_UE hat2[u][e] = hat[u][e];
-        if (post) {
-            col_load<T, WIDE, UPT>(p.w_post, 1.f, D, t);
-            EACH_UE hat2[u][e] *= t[u][e];
-            if (BIAS && p.b_post) {
-                col_load<T, WIDE, UPT>(p.b_post, 0.f, D, t);
-                EACH_UE hat2[u][e] += t[u][e];
+        const uint32_t at = mine + stage * stage_bytes;
+        if (RING) copies_wait<NORM_RING - 1>();
+        auto take = [&](auto type, const void* from, long long ld, int place, float2 (&v)[UPT][4]) {
+            using E = decltype(type);
+            if (RING) {
+                row_take<E, UPT, THREADS>(at + place, v);
+                if (blockDim.y > 1 && D == 0) EACH_PAIR v[u][e] = make_float2(0.f, 0.f);
+            } else {
+                row_load<E, WIDE, UPT>(from, row * ld, D, v);
             }
+        };
+        // behind POST: u from its hat, times silu(gate) if it comes after
+        auto behind_post = [&](float2 (&v)[UPT][4], bool gated) {
+            if (post) {
+                w_post.mul(D, v);
+                if (BIAS) b_post.add(D, v);
+            }
+            if (after && gated) {
+                float2 g[UPT][4];
+                take(T(), p.gate, p.gate_ld, at_g, g);
+                EACH_PAIR v[u][e] = pmul(v[u][e], silu2(g[u][e]));
+            }
+        };
+        float2 hat[UPT][4], d[UPT][4];
+        float r_post = 0.f;
+        take(T(), p.x, p.x_ld, 0, hat);
+        if (gate && !after) {
+            float2 g[UPT][4];
+            take(T(), p.gate, p.gate_ld, at_g, g);
+            EACH_PAIR hat[u][e] = pmul(hat[u][e], silu2(g[u][e]));
         }
-        if (after) EACH_UE hat2[u][e] *= silu(g[u][e]);
-        EACH_UE t[u][e] = hat2[u][e];
-        if (p.scale) {
-            col_load<T, WIDE, UPT>(p.scale, 1.f, D, d);
-            EACH_UE hat2[u][e] *= d[u][e];
-        }
-        if (residual && pre) {
-            row_load<RT, WIDE, UPT>(p.res, row * p.res_ld, D, d);
-            EACH_UE hat2[u][e] += d[u][e];
-        }
+        if (post) r_post = row_norm(hat, p.D, layer, p.eps, buf, turn);
         // d: the gradient at r
+        if (has_dy) take(T(), p.dy, p.dy_ld, at_dy, d);
+        else EACH_PAIR d[u][e] = make_float2(0.f, 0.f);
         if (pre) {
-            r_pre = row_norm(hat2, p.D, layer, p.eps, buf, turn);
-            row_load<T, WIDE, UPT>(p.dy, row * p.dy_ld, D, d);
-            EACH_UE s_wpre[u][e] = fmaf(d[u][e], hat2[u][e], s_wpre[u][e]);
-            if (BIAS) EACH_UE s_bpre[u][e] += d[u][e];
-            float w[UPT][8];
-            col_load<T, WIDE, UPT>(p.w_pre, 1.f, D, w);
-            EACH_UE d[u][e] *= w[u][e];
+            float2 hat2[UPT][4];
+            EACH_PAIR hat2[u][e] = hat[u][e];
+            behind_post(hat2, true);
+            scale.mul(D, hat2);
+            if (use_res) {
+                float2 r[UPT][4];
+                take(RT(), p.res, p.res_ld, at_res, r);
+                EACH_PAIR hat2[u][e] = padd(hat2[u][e], r[u][e]);
+            }
+            const float r_pre = row_norm(hat2, p.D, layer, p.eps, buf, turn);
+            EACH_PAIR s_wpre[u][e] = pfma(d[u][e], hat2[u][e], s_wpre[u][e]);
+            if (BIAS) EACH_PAIR s_bpre[u][e] = padd(d[u][e], s_bpre[u][e]);
+            w_pre.mul(D, d);
             norm_back(d, hat2, r_pre, p.D, layer, buf, turn);
-        } else if (!residual) {
-            row_load<T, WIDE, UPT>(p.dy, row * p.dy_ld, D, d);
-        } else {
-            EACH_UE d[u][e] = 0.f;
         }
         if (residual) {
-            if (p.dres_out) {
-                row_load<RT, WIDE, UPT>(p.dres_out, row * p.dres_out_ld, D, hat2);
-                EACH_UE d[u][e] += hat2[u][e];
+            if (has_dro) {
+                float2 r[UPT][4];
+                take(RT(), p.dres_out, p.dres_out_ld, at_dro, r);
+                EACH_PAIR d[u][e] = padd(d[u][e], r[u][e]);
             }
             row_store<RT, WIDE, UPT>(p.dres, row * p.dres_ld, D, d);
         }
         // back through scale, gate, POST, gate
-        if (p.scale) {
-            EACH_UE s_scale[u][e] = fmaf(d[u][e], t[u][e], s_scale[u][e]);
-            col_load<T, WIDE, UPT>(p.scale, 1.f, D, hat2);
-            EACH_UE d[u][e] *= hat2[u][e];
-        }
-        if (post) col_load<T, WIDE, UPT>(p.w_post, 1.f, D, hat2);     // w_post
-        if (after) {
-            if (BIAS && p.b_post) col_load<T, WIDE, UPT>(p.b_post, 0.f, D, t);
-            EACH_UE {
-                const float s = sigmoid(g[u][e]);
-                const float n = post ? fmaf(hat[u][e], hat2[u][e], BIAS && p.b_post ? t[u][e] : 0.f) : x[u][e];
-                const float dg = d[u][e] * n * silu_grad(g[u][e], s);
-                d[u][e] *= g[u][e] * s;
-                g[u][e] = dg;
+        // through u * silu(g): dg = d u silu'(g), d *= silu(g)
+        auto back_gate = [&](float2 (&n)[UPT][4]) {
+            float2 g[UPT][4];
+            take(T(), p.gate, p.gate_ld, at_g, g);
+            EACH_PAIR {
+                const float2 s = make_float2(sigmoid(g[u][e].x), sigmoid(g[u][e].y)), v = g[u][e], dv = pmul(d[u][e], s);
+                // silu' = s (1 + v (1 - s))
+                n[u][e] = pmul(pmul(dv, n[u][e]), pfma(v, padd(pdup(1.f), make_float2(-s.x, -s.y)), pdup(1.f)));
+                d[u][e] = pmul(dv, v);
             }
-            row_store<T, WIDE, UPT>(p.dgate, row * p.dgate_ld, D, g);
+            row_store<T, WIDE, UPT>(p.dgate, row * p.dgate_ld, D, n);
+        };
+        if (after) {
+            float2 n[UPT][4];
+            EACH_PAIR n[u][e] = hat[u][e];
+            behind_post(n, false);
+            scale.mul(D, n);                   // (d has not been through scale yet)
+            back_gate(n);
         }
+        EACH_PAIR s_1[u][e] = pfma(d[u][e], hat[u][e], s_1[u][e]);
+        if (BIAS) EACH_PAIR s_0[u][e] = padd(d[u][e], s_0[u][e]);
+        scale.mul(D, d);
         if (post) {
-            EACH_UE s_wpost[u][e] = fmaf(d[u][e], hat[u][e], s_wpost[u][e]);
-            if (BIAS) EACH_UE s_bpost[u][e] += d[u][e];
-            EACH_UE d[u][e] *= hat2[u][e];
+            w_post.mul(D, d);
             norm_back(d, hat, r_post, p.D, layer, buf, turn);
         }
         if (gate && !after) {
-            EACH_UE {
-                const float s = sigmoid(g[u][e]);
-                const float dg = d[u][e] * x[u][e] * silu_grad(g[u][e], s);
-                d[u][e] *= g[u][e] * s;
-                g[u][e] = dg;
-            }
-            row_store<T, WIDE, UPT>(p.dgate, row * p.dgate_ld, D, g);
+            float2 n[UPT][4];
+            take(T(), p.x, p.x_ld, 0, n);
+            back_gate(n);
         }
         row_store<T, WIDE, UPT>(p.dx, row * p.dx_ld, D, d);
     }
     if (!p.ws) return;
     const long long part = ((long long)blockIdx.x * blockDim.y + threadIdx.y) * SUMS * p.D;
-    if (p.dw_post) row_store<float, WIDE, UPT>(p.ws, part, p.D, s_wpost);
-    if (BIAS && p.db_post) row_store<float, WIDE, UPT>(p.ws, part + p.D, p.D, s_bpost);
-    if (p.dscale) row_store<float, WIDE, UPT>(p.ws, part + 2 * p.D, p.D, s_scale);
-    if (p.dw_pre) row_store<float, WIDE, UPT>(p.ws, part + 3 * p.D, p.D, s_wpre);
-    if (BIAS && p.db_pre) row_store<float, WIDE, UPT>(p.ws, part + 4 * p.D, p.D, s_bpre);
+    row_store<float, WIDE, UPT>(p.ws, part, p.D, s_1);
+    if (BIAS) row_store<float, WIDE, UPT>(p.ws, part + p.D, p.D, s_0);
+    if (p.dw_pre) row_store<float, WIDE, UPT>(p.ws, part + 2 * p.D, p.D, s_wpre);
+    if (BIAS && p.db_pre) row_store<float, WIDE, UPT>(p.ws, part + 3 * p.D, p.D, s_bpre);
 }
 
-__global__ void __launch_bounds__(128) seq_norm_param_kernel(const __grid_constant__ SeqNormParams p, int parts) {
-    const int c = blockIdx.x * 128 + threadIdx.x, k = blockIdx.y;
-    float* out = k == 0 ? p.dw_post : k == 1 ? p.db_post : k == 2 ? p.dscale : k == 3 ? p.dw_pre : p.db_pre;
-    if (!out || c >= p.D) return;
-    float s[4] = {};
-    const float* src = p.ws + (long long)k * p.D + c;
-    const long long step = (long long)SUMS * p.D;
-    int b = 0;
-    for (; b + 4 <= parts; b += 4)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s[i] += src[(b + i) * step];
-    for (; b < parts; ++b) s[0] += src[b * step];
-    out[c] = (s[0] + s[1]) + (s[2] + s[3]);
+// The parameters' gradients: the blocks' rows of partial sums, added up in a fixed order.
+template <typename T>
+__global__ void __launch_bounds__(COLUMN_THREADS) seq_norm_param_kernel(const __grid_constant__ SeqNormParams p, int parts, bool bias) {
+    const int c = blockIdx.x * 32 + (threadIdx.x & 31);
+    const bool on = c < p.D, first = threadIdx.x < 32 && on;
+    auto total = [&](int k) { return column_sum(p.ws + (long long)k * p.D + c, (long long)SUMS * p.D, parts, on); };
+    auto param = [&](const void* v, float none) { return v && on ? seq_ld(static_cast<const T*>(v) + c) : none; };
+    if (blockIdx.y == 0) {
+        const float s1 = total(0);
+        float s0 = 0.f;
+        if (bias) {
+            __syncthreads();
+            s0 = total(1);
+        }
+        if (first && p.dw_post) p.dw_post[c] = param(p.scale, 1.f) * s1;
+        if (first && p.db_post) p.db_post[c] = param(p.scale, 1.f) * s0;
+        if (first && p.dscale) p.dscale[c] = fmaf(param(p.w_post, 1.f), s1, param(p.b_post, 0.f) * s0);
+    } else {
+        if (p.dw_pre) {
+            const float v = total(2);
+            if (first) p.dw_pre[c] = v;
+        }
+        if (p.db_pre) {
+            __syncthreads();
+            const float v = total(3);
+            if (first) p.db_pre[c] = v;
+        }
+    }
 }
 
-dim3 bwd_block(int D) { return norm_block(D, D > 8192 ? 2 : 1, 256); }
+// How rows are spread: upt groups of 8 columns to a thread, `threads` (128, 256, 512 or 1024) at most in a
+// block, rows through shared memory or not.
+struct Shape {
+    int upt, threads;
+    bool ring;
+    dim3 block;
+    int smem, blocks;
+};
+// `wide`: rows of aligned groups.  8 columns a thread up to 4096 (8192 x 4096 bf16 with everything on: 204 us with
+// one block of 512 threads an SM; 212 with two of 256 and 16 columns each, which spills; 237 with two of 512
+// and 64 registers).
+Shape shape_of(int rows, int D, unsigned flags, bool wide, int esize, int rsize, int sms) {
+    const bool gate = flags & (SEQ_NORM_GATE_BEFORE | SEQ_NORM_GATE_AFTER), residual = flags & SEQ_NORM_RESIDUAL;
+    const bool pre = flags & SEQ_NORM_PRE;
+    const int row = esize * (1 + gate + (pre || !residual)) + rsize * ((residual && pre) + residual);
+    Shape s;
+    s.upt = D > 4096 ? 2 : 1;
+    s.block = norm_block(D, s.upt);
+    const int threads = (int)(s.block.x * s.block.y);
+    s.threads = threads <= 128 ? 128 : threads <= 256 ? 256 : 512;
+    s.smem = NORM_RING * s.threads * s.upt * 8 * row;
+    s.ring = wide && D <= 8192 && s.smem <= NORM_RING_MAX;
+    if (!s.ring) {
+        s.smem = 0;
+        s.threads = s.upt == 1 ? 512 : 1024;
+    }
+    int fit = 65536 / ((s.threads == 1024 ? 64 : 128) * threads);
+    if (s.smem > 0 && 228 * 1024 / (s.smem + 1536) < fit) fit = 228 * 1024 / (s.smem + 1536);
+    const int most = (rows + (int)s.block.y - 1) / (int)s.block.y, want = (fit < 1 ? 1 : fit) * sms;
+    s.blocks = most < want ? most : want;
+    return s;
+}
 
-template <typename T, typename RT, bool WIDE, int UPT>
-cudaError_t launch_u(const SeqNormParams& p, cudaStream_t stream) {
-    const dim3 block = bwd_block(p.D), grid((unsigned)(p.blocks / block.y));
-    const bool bias = p.b_post || p.b_pre || p.db_post || p.db_pre;
-    cudaError_t e = bias ? launch_kernel(seq_norm_bwd_kernel<T, RT, WIDE, UPT, true>, grid, block, 0, stream, false, 1, p)
-                         : launch_kernel(seq_norm_bwd_kernel<T, RT, WIDE, UPT, false>, grid, block, 0, stream, false, 1, p);
+template <typename T, typename RT, bool WIDE, bool RING, int UPT, int THREADS>
+cudaError_t launch_u(const SeqNormParams& p, const Shape& s, bool bias, cudaStream_t stream) {
+    const auto kernel = bias ? seq_norm_bwd_kernel<T, RT, WIDE, RING, UPT, true, THREADS> : seq_norm_bwd_kernel<T, RT, WIDE, RING, UPT, false, THREADS>;
+    cudaError_t e = RING ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, s.smem) : cudaSuccess;
+    if (e == cudaSuccess) e = launch_kernel(kernel, dim3((unsigned)s.blocks), s.block, (size_t)s.smem, stream, false, 1, p);
     if (e == cudaSuccess && p.ws)
-        e = launch_kernel(seq_norm_param_kernel, dim3((unsigned)((p.D + 127) / 128), SUMS), dim3(128), 0, stream, false, 1,
-                          p, p.blocks);
+        e = launch_kernel(seq_norm_param_kernel<T>, dim3((unsigned)((p.D + 31) / 32), 2), dim3(COLUMN_THREADS), 0, stream, false, 1, p,
+                          s.blocks * (int)s.block.y, bias);
     return e;
 }
 
 template <typename T, typename RT>
 cudaError_t launch(const SeqNormParams& p, cudaStream_t stream) {
-    if (p.D > 8192) return p.vec ? launch_u<T, RT, true, 2>(p, stream) : launch_u<T, RT, false, 2>(p, stream);
-    return p.vec ? launch_u<T, RT, true, 1>(p, stream) : launch_u<T, RT, false, 1>(p, stream);
+    const bool bias = p.b_post || p.b_pre;
+    const Shape s = shape_of(p.rows, p.D, p.flags, p.vec, (int)sizeof(T), (int)sizeof(RT), p.sms);
+    if (s.ring) {
+        if (s.upt == 2) return launch_u<T, RT, true, true, 2, 512>(p, s, bias, stream);
+        return s.threads == 128   ? launch_u<T, RT, true, true, 1, 128>(p, s, bias, stream)
+               : s.threads == 256 ? launch_u<T, RT, true, true, 1, 256>(p, s, bias, stream)
+                                  : launch_u<T, RT, true, true, 1, 512>(p, s, bias, stream);
+    }
+    if (s.threads == 1024) return p.vec ? launch_u<T, RT, true, false, 2, 1024>(p, s, bias, stream) : launch_u<T, RT, false, false, 2, 1024>(p, s, bias, stream);
+    return p.vec ? launch_u<T, RT, true, false, 1, 512>(p, s, bias, stream) : launch_u<T, RT, false, false, 1, 512>(p, s, bias, stream);
 }
 
 }  // namespace
 
-// Rows of partial sums: blocks times the rows a block holds at once.
-int seq_norm_bwd_blocks(int rows, int D, int sms) {
-    const dim3 block = bwd_block(D);
-    const int most = (rows + (int)block.y - 1) / (int)block.y;
-    const int per_sm = 1024 / (int)(block.x * block.y) < 1 ? 1 : 1024 / (int)(block.x * block.y);
-    const int want = sms * per_sm;
-    return (most < want ? most : want) * (int)block.y;
+// Rows of partial sums at most, with and without wide rows.
+int seq_norm_bwd_blocks(int rows, int D, unsigned flags, int esize, int rsize, int sms) {
+    int most = 1;
+    for (int wide = 0; wide < 2; ++wide) {
+        const Shape s = shape_of(rows, D, flags, wide, esize, rsize, sms);
+        const int parts = s.blocks * (int)s.block.y;
+        if (parts > most) most = parts;
+    }
+    return most;
 }
 
 cudaError_t launch_seq_norm_bwd(const SeqNormParams& p, bool bf16, bool res_bf16, cudaStream_t stream) {
