@@ -95,6 +95,7 @@ struct Checker {
         ptr(v, esize, needed);
         if (!v) return;
         if (ld < width) fail(CONV_ERR_INVALID_ARG);
+        if (ld > INT32_MAX) fail(CONV_ERR_UNSUPPORTED);      // the kernels multiply it in 32 bits by 32
         if (((uint64_t)ld * esize) % 16) wide = false;
         if (((uint64_t)ld * esize) % 4) words = false;
     }
@@ -115,6 +116,7 @@ void check_states(const seq_plan* p, Checker& c, const int32_t* starts, const in
     c.ptr(slots, 4, false);
     c.ptr(in, esize, false);
     c.ptr(out, esize, false);
+    if (slot_count > MAX_EXTENT) c.fail(CONV_ERR_UNSUPPORTED);
     if ((in || out) && (slot_count < 0 || (!slots && slot_count < p->S))) c.fail(CONV_ERR_INVALID_ARG);
 }
 
@@ -253,7 +255,7 @@ conv_status seq_scan_plan_create(seq_plan_t* out, int64_t S, int64_t T, int64_t 
     conv_status st = check_axis(S, T, D, direction, flags & SEQ_RAGGED);
     if (st != CONV_OK) return st;
     if (D % G != 0) return CONV_ERR_INVALID_ARG;
-    if (N > 128 || G > 32768) return CONV_ERR_UNSUPPORTED;
+    if (N > 128 || G > 32768 || D * N > INT32_MAX) return CONV_ERR_UNSUPPORTED;
     seq_plan* p = new_plan(Op::Scan, S, T, D, dtype, direction, flags);
     if (!p) return CONV_ERR_INVALID_ARG;
     p->N = (int)N; p->G = (int)G;
@@ -338,6 +340,9 @@ static conv_status scan_call(seq_plan_t p, const seq_scan_args* a, seq_direction
     q.x_ld = a->x_ld; q.dt_ld = a->dt_ld; q.B_ld = a->B_ld; q.C_ld = a->C_ld; q.z_ld = a->z_ld; q.y_ld = a->y_ld;
     q.dy_ld = a->dy_ld; q.dx_ld = a->dx_ld; q.ddt_ld = a->ddt_ld; q.dB_ld = a->dB_ld; q.dC_ld = a->dC_ld; q.dz_ld = a->dz_ld;
     q.cblocks = p->blocks;
+    auto aligned = [](const void* v, size_t n) { return reinterpret_cast<uintptr_t>(v) % n == 0; };
+    q.quads = p->N % 4 == 0 && aligned(a->A, 16) && aligned(a->h_in, 16) && aligned(a->h_out, 16) && aligned(a->B, 4 * e) &&
+              aligned(a->C, 4 * e) && a->B_ld % 4 == 0 && a->C_ld % 4 == 0;
     q.wide = c.wide && (p->D / p->G * e) % 16 == 0 ? 16 : c.words && (p->D / p->G * e) % 4 == 0 ? 4 : 0;
     unsigned char* w = static_cast<unsigned char*>(p->ws);
     if (dir == SEQ_FWD && p->ws_bytes) {

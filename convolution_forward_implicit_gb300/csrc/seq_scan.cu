@@ -288,41 +288,108 @@ __global__ void __launch_bounds__(128) seq_scan_empty_kernel(SeqAxis ax, SeqSlot
     }
 }
 
-// One token per sequence.  A lane holds 4 states of a channel (16 bytes of its state row), LN lanes
-// share the channel.
-template <typename T, int LN>
-__global__ void __launch_bounds__(STEP_THREADS) seq_scan_step_kernel(const __grid_constant__ SeqScanParams p) {
-    const int d0 = (blockIdx.x * STEP_THREADS + threadIdx.x) / LN;
+// One token per sequence: bound by the bytes of the states.  A lane holds 4 states of a channel (16 bytes of
+// its state row), LN lanes share the channel; a thread keeps its row of A and takes ROWS sequences at a
+// time, all of their loads on their way before the first is used.  VEC: states, A, B and C in whole aligned
+// groups of 4.
+template <typename T, int LN, int ROWS, bool VEC>
+__global__ void __launch_bounds__(STEP_THREADS, ROWS > 1 && VEC ? 7 : 1) seq_scan_step_kernel(const __grid_constant__ SeqScanParams p) {
+    const int d0 = (int)((blockIdx.x * (long long)STEP_THREADS + threadIdx.x) / LN);
     const bool on = d0 < p.D;
     const int d = on ? d0 : p.D - 1;
-    const int n0 = threadIdx.x % LN * 4, g = d / (p.D / p.G);
-    float A2[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) A2[k] = n0 + k < p.N ? p.A[(long long)d * p.N + n0 + k] * LOG2E : 0.f;
-    const float bias = p.dt_bias ? p.dt_bias[d] : 0.f, Dd = p.Dskip ? p.Dskip[d] : 0.f;
-    for (long long s = blockIdx.y; s < p.ax.S; s += gridDim.y) {
-        const long long slot = seq_slot(p.sl, (int)s);
-        float h[4];
-        scan_h_load<4>(p, p.h_in, slot, d, n0, h);
-        const float xv = seq_ld(static_cast<const T*>(p.x) + s * p.x_ld + d);
-        float delta = seq_ld(static_cast<const T*>(p.dt) + s * p.dt_ld + d) + bias;
-        if (p.softplus) delta = softplus(delta);
-        const float u = delta * xv;
-        float acc = 0.f;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float b = n0 + k < p.N ? seq_ld(static_cast<const T*>(p.B) + s * p.B_ld + g * p.N + n0 + k) : 0.f;
-            const float c = n0 + k < p.N ? seq_ld(static_cast<const T*>(p.C) + s * p.C_ld + g * p.N + n0 + k) : 0.f;
-            h[k] = fmaf(ex2_approx(delta * A2[k]), h[k], u * b);
-            acc = fmaf(c, h[k], acc);
+    const int n0 = threadIdx.x % LN * 4, bc = d / (p.D / p.G) * p.N + n0;
+    const bool any = n0 < p.N;                       // (lanes behind the states only take part in the sum)
+    const float2 zero = make_float2(0.f, 0.f);
+    auto four = [&](const float* from, float2 (&v)[2]) {
+        v[0] = v[1] = zero;
+        if (VEC) {
+            if (any) ld2(from, v[0], v[1]);
+        } else {
+            if (n0 < p.N) v[0].x = from[0];
+            if (n0 + 1 < p.N) v[0].y = from[1];
+            if (n0 + 2 < p.N) v[1].x = from[2];
+            if (n0 + 3 < p.N) v[1].y = from[3];
         }
-        if (on) scan_h_store<4>(p, p.h_out, slot, d, n0, h);
+    };
+    auto four_t = [&](const T* from, float2 (&v)[2]) {
+        v[0] = v[1] = zero;
+        if (VEC) {
+            if (any) {
+                v[0] = seq_ld2(from);
+                v[1] = seq_ld2(from + 2);
+            }
+        } else {
+            if (n0 < p.N) v[0].x = seq_ld(from);
+            if (n0 + 1 < p.N) v[0].y = seq_ld(from + 1);
+            if (n0 + 2 < p.N) v[1].x = seq_ld(from + 2);
+            if (n0 + 3 < p.N) v[1].y = seq_ld(from + 3);
+        }
+    };
+    float2 A2[2];
+    const int at = d * p.N + n0, DN = p.D * p.N;     // (D N < 2^31: see the plan)
+    four(p.A + at, A2);
+    A2[0] = mul2(A2[0], dup2(LOG2E));
+    A2[1] = mul2(A2[1], dup2(LOG2E));
+    const float bias = p.dt_bias ? p.dt_bias[d] : 0.f, Dd = p.Dskip ? p.Dskip[d] : 0.f;
+    // row s of a tensor (rows are less than 2^31 elements apart)
+    auto row = [](const void* base, int s, long long ld) { return static_cast<const T*>(base) + (long long)s * (int)ld; };
+    for (int s0 = blockIdx.y * ROWS; s0 < p.ax.S; s0 += gridDim.y * ROWS) {
+        float2 h[ROWS][2], B[ROWS][2], C[ROWS][2];
+        float x[ROWS], raw[ROWS], z[ROWS];
+        int slot[ROWS];
 #pragma unroll
-        for (int o = LN / 2; o > 0; o >>= 1) acc += __shfl_xor_sync(~0u, acc, o);
-        if (n0 == 0 && on) {
-            float v = fmaf(Dd, xv, acc);
-            if (p.z) v *= silu(seq_ld(static_cast<const T*>(p.z) + s * p.z_ld + d));
-            seq_st(static_cast<T*>(p.y) + s * p.y_ld + d, v);
+        for (int r = 0; r < ROWS; ++r) slot[r] = s0 + r < p.ax.S ? (int)seq_slot(p.sl, s0 + r) : -1;
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
+            const int s = min(s0 + r, p.ax.S - 1);
+            h[r][0] = h[r][1] = zero;
+            if (p.h_in && slot[r] >= 0) four(p.h_in + (long long)slot[r] * DN + at, h[r]);
+            x[r] = seq_ld(row(p.x, s, p.x_ld) + d);
+            raw[r] = seq_ld(row(p.dt, s, p.dt_ld) + d) + bias;
+            z[r] = p.z ? seq_ld(row(p.z, s, p.z_ld) + d) : 0.f;
+            four_t(row(p.B, s, p.B_ld) + bc, B[r]);
+            four_t(row(p.C, s, p.C_ld) + bc, C[r]);
+        }
+        float delta[ROWS];
+#pragma unroll
+        for (int r = 0; r < ROWS; r += 2) {
+            if (ROWS == 1) {
+                delta[0] = p.softplus ? softplus(raw[0]) : raw[0];
+            } else {
+                float2 v = make_float2(raw[r], raw[r + 1 < ROWS ? r + 1 : r]);
+                if (p.softplus) v = softplus2(v, nullptr);
+                delta[r] = v.x;
+                if (r + 1 < ROWS) delta[r + 1] = v.y;
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
+            const float2 dl = dup2(delta[r]), u = dup2(delta[r] * x[r]);
+            float2 acc = zero;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                h[r][k] = fma2(exp2_2(mul2(dl, A2[k])), h[r][k], mul2(u, B[r][k]));
+                acc = fma2(C[r][k], h[r][k], acc);
+            }
+            if (on && p.h_out && slot[r] >= 0) {
+                float* to = p.h_out + (long long)slot[r] * DN + at;
+                if (VEC) {
+                    if (any) st2(to, h[r][0], h[r][1]);
+                } else {
+                    if (n0 < p.N) to[0] = h[r][0].x;
+                    if (n0 + 1 < p.N) to[1] = h[r][0].y;
+                    if (n0 + 2 < p.N) to[2] = h[r][1].x;
+                    if (n0 + 3 < p.N) to[3] = h[r][1].y;
+                }
+            }
+            float a = acc.x + acc.y;
+#pragma unroll
+            for (int o = LN / 2; o > 0; o >>= 1) a += __shfl_xor_sync(~0u, a, o);
+            if (n0 == 0 && on && s0 + r < p.ax.S) {
+                float v = fmaf(Dd, x[r], a);
+                if (p.z) v *= silu(z[r]);
+                seq_st(const_cast<T*>(row(p.y, s0 + r, p.y_ld)) + d, v);
+            }
         }
     }
 }
@@ -357,8 +424,18 @@ cudaError_t launch_t(const SeqScanParams& p, cudaStream_t stream) {
 
 template <typename T, int LN>
 cudaError_t launch_step(const SeqScanParams& p, cudaStream_t stream) {
-    const dim3 grid((unsigned)(((long long)p.D * LN + STEP_THREADS - 1) / STEP_THREADS), (unsigned)(p.ax.S < 32768 ? p.ax.S : 32768));
-    return launch_kernel(seq_scan_step_kernel<T, LN>, grid, dim3(STEP_THREADS), 0, stream, false, 1, p);
+    const long long blocks = ((long long)p.D * LN + STEP_THREADS - 1) / STEP_THREADS;
+    // 4 sequences a thread once that still leaves the GPU several blocks an SM (256 x 4096 x 16: 54 us with one)
+    constexpr int ROWS = 4;
+    if (blocks * p.ax.S < 16 * 152 * ROWS) {
+        const dim3 grid((unsigned)blocks, (unsigned)(p.ax.S < 32768 ? p.ax.S : 32768));
+        return p.quads ? launch_kernel(seq_scan_step_kernel<T, LN, 1, true>, grid, dim3(STEP_THREADS), 0, stream, false, 1, p)
+                       : launch_kernel(seq_scan_step_kernel<T, LN, 1, false>, grid, dim3(STEP_THREADS), 0, stream, false, 1, p);
+    }
+    const int rows = (p.ax.S + ROWS - 1) / ROWS;
+    const dim3 grid((unsigned)blocks, (unsigned)(rows < 32768 ? rows : 32768));
+    return p.quads ? launch_kernel(seq_scan_step_kernel<T, LN, ROWS, true>, grid, dim3(STEP_THREADS), 0, stream, false, 1, p)
+                   : launch_kernel(seq_scan_step_kernel<T, LN, ROWS, false>, grid, dim3(STEP_THREADS), 0, stream, false, 1, p);
 }
 template <typename T>
 cudaError_t launch_step_t(const SeqScanParams& p, cudaStream_t stream) {

@@ -145,9 +145,11 @@ class _SeqPlan:
         self._ws_bytes = seq_workspace_bytes(handle)
         self._pack = struct.Struct(f"={len(self._fields)}q").pack
         self._place = {f: i for i, f in enumerate(self._fields)}
+        self._seen = {}          # argument -> the last layout found good for it
         name = self._names[direction]
         self._name, self._fn = name, getattr(_library(), name)
-        self._stream = torch.cuda.current_stream
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)      # (current_stream builds an object)
+        self._stream = raw or (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
     @staticmethod
     def _direction(direction, allowed):
@@ -162,7 +164,8 @@ class _SeqPlan:
         """Allocate the workspace, if the plan needs one."""
         import torch
         if self._ws_bytes:
-            dev = device or torch.device("cuda", torch.cuda.current_device())
+            dev = torch.device("cuda", torch.cuda.current_device() if device is None else device) if not isinstance(
+                device, torch.device) else device
             self.workspace = torch.empty(self._ws_bytes, dtype=torch.uint8, device=dev)
             seq_plan_set_workspace(self.handle, self.workspace.data_ptr(), self._ws_bytes)
         return self
@@ -176,9 +179,17 @@ class _SeqPlan:
         """A tensor of the token axis: (rows, width) or (S, rows / S, width)."""
         if t is None:
             return
+        sh, st = t.shape, t.stride()
+        seen = self._seen.get(name)
+        if seen is None or seen[0] != sh or seen[1] != st or seen[2] is not t.dtype or not t.is_cuda:
+            seen = self._seen[name] = self._rows_layout(name, t, sh, st, width, dtype)
+        i = seen[4]
+        v[i] = t.data_ptr()
+        v[i + 1] = seen[3]
+
+    def _rows_layout(self, name, t, sh, st, width, dtype):
         if t.dtype is not dtype or not t.is_cuda:
             _fail(self._name, f"{name} is not a {dtype} tensor on the GPU")
-        sh, st = t.shape, t.stride()
         n = len(sh)
         if n == 2:
             rows, ld = sh[0], st[0]
@@ -191,9 +202,7 @@ class _SeqPlan:
         if rows != self._tokens or sh[-1] != width or (st[-1] != 1 and width > 1 and rows):
             _fail(self._name, f"{name} has shape {tuple(sh)}, strides {tuple(st)}: {self._tokens} rows of {width} contiguous "
                               "values are wanted")
-        i = self._place[name]
-        v[i] = t.data_ptr()
-        v[i + 1] = ld if rows > 1 else width
+        return sh, st, dtype, ld if rows > 1 else width, self._place[name]
 
     def _flat(self, v, name, t, shape, dtype):
         """A contiguous tensor of a fixed shape."""
@@ -209,13 +218,13 @@ class _SeqPlan:
         for name, t in states.items():
             if t is None:
                 continue
-            if (t.dtype is not dtype or not t.is_cuda or t.dim() != 1 + len(row) or t.shape[1:] != row
-                    or not t.is_contiguous()):
+            sh = t.shape
+            if t.dtype is not dtype or not t.is_cuda or sh[1:] != row or not t.is_contiguous():
                 _fail(self._name, f"{name} is not a contiguous {dtype} tensor of shape (slots, {', '.join(map(str, row))}) "
                                   "on the GPU")
-            if count >= 0 and t.shape[0] != count:
+            if count >= 0 and sh[0] != count:
                 _fail(self._name, "the state buffers have different numbers of rows")
-            count = t.shape[0]
+            count = sh[0]
             v[self._place[name]] = t.data_ptr()
         v[self._place["slot_count"]] = max(count, 0)
         if slots is not None:
@@ -226,7 +235,7 @@ class _SeqPlan:
     def _call(self, v, device, stream):
         if self._ws_bytes and self.workspace is None:
             self.allocate(device)
-        s = stream if stream is not None else self._stream(device).cuda_stream
+        s = stream if stream is not None else self._stream(device)
         st = self._fn(self.handle, self._pack(*v), s)
         if st != CONV_OK:
             raise ConvError(st, self._name)
@@ -270,7 +279,7 @@ class SeqConvPlan(_SeqPlan):
         v = self._common(x, w, bias)
         self._rows(v, "y", y, self.D, self.torch_dtype)
         self._states(v, slots, starts, (self.W - 1, self.D), self.torch_dtype, state_in=state_in, state_out=state_out)
-        self._call(v, x.device, stream)
+        self._call(v, x.get_device(), stream)
         return y
 
     def backward(self, x, w, bias, dy, dx, dw, dbias, starts=None, state_in=None, slots=None, stream=None):
@@ -281,7 +290,7 @@ class SeqConvPlan(_SeqPlan):
         self._flat(v, "dw", dw, (self.D, self.W), self._f32)
         self._flat(v, "dbias", dbias, (self.D,), self._f32)
         self._states(v, slots, starts, (self.W - 1, self.D), self.torch_dtype, state_in=state_in)
-        self._call(v, x.device, stream)
+        self._call(v, x.get_device(), stream)
         return dx, dw, dbias
 
     def step(self, x, w, bias, state_in, state_out, y, slots=None, stream=None):
@@ -289,7 +298,7 @@ class SeqConvPlan(_SeqPlan):
         v = self._common(x, w, bias)
         self._rows(v, "y", y, self.D, self.torch_dtype)
         self._states(v, slots, None, (self.W - 1, self.D), self.torch_dtype, state_in=state_in, state_out=state_out)
-        self._call(v, x.device, stream)
+        self._call(v, x.get_device(), stream)
         return y
 
 
@@ -339,7 +348,7 @@ class SeqScanPlan(_SeqPlan):
         self._rows(v, "y", y, self.D, self.torch_dtype)
         self._saved(v, saved)
         self._states(v, slots, starts, (self.D, self.N), self._f32, h_in=h_in, h_out=h_out)
-        self._call(v, x.device, stream)
+        self._call(v, x.get_device(), stream)
         return y
 
     def backward(self, x, dt, A, B, C, dy, saved, dx, ddt, dA, dB, dC, D=None, z=None, dt_bias=None, dD=None, dz=None,
@@ -356,7 +365,7 @@ class SeqScanPlan(_SeqPlan):
         self._flat(v, "ddt_bias", ddt_bias, (self.D,), f32)
         self._saved(v, saved)
         self._states(v, slots, starts, (self.D, self.N), f32, h_in=h_in, dh_out=dh_out, dh_in=dh_in)
-        self._call(v, x.device, stream)
+        self._call(v, x.get_device(), stream)
         return dx
 
     def step(self, x, dt, A, B, C, h_in, h_out, y, D=None, z=None, dt_bias=None, slots=None, stream=None):
@@ -364,7 +373,7 @@ class SeqScanPlan(_SeqPlan):
         v = self._common(x, dt, A, B, C, D, z, dt_bias)
         self._rows(v, "y", y, self.D, self.torch_dtype)
         self._states(v, slots, None, (self.D, self.N), self._f32, h_in=h_in, h_out=h_out)
-        self._call(v, x.device, stream)
+        self._call(v, x.get_device(), stream)
         return y
 
 
@@ -405,7 +414,7 @@ class SeqNormPlan(_SeqPlan):
         v = self._common(x, gate, w_post, b_post, scale, res, w_pre, b_pre)
         self._rows(v, "y", y, self.D, self.torch_dtype)
         self._rows(v, "res_out", res_out, self.D, self.res_torch_dtype)
-        self._call(v, x.device, stream)
+        self._call(v, x.get_device(), stream)
         return y, res_out
 
     def backward(self, x, dx, dy=None, dres_out=None, gate=None, w_post=None, b_post=None, scale=None, res=None,
@@ -419,5 +428,5 @@ class SeqNormPlan(_SeqPlan):
         for name, t in (("dw_post", dw_post), ("db_post", db_post), ("dscale", dscale), ("dw_pre", dw_pre),
                         ("db_pre", db_pre)):
             self._flat(v, name, t, (self.D,), self._f32)
-        self._call(v, x.device, stream)
+        self._call(v, x.get_device(), stream)
         return dx

@@ -12,8 +12,8 @@
  * range: they give other results, never an access outside the T tokens.)
  *
  * Layout of a tensor of T tokens: element (t, c) at t * ld + c, c contiguous; `ld` (in
- * elements, at least the row's width) lets a call read a slice of a wider projection.
- * Offsets are 64-bit.  Pointers need the alignment of their element only; rows that are
+ * elements, at least the row's width, at most 2^31 - 1) lets a call read a slice of a wider
+ * projection.  Offsets are 64-bit.  Pointers need the alignment of their element only; rows that are
  * 16-byte aligned (pointer and ld) are read with wide loads.  Inputs and outputs do not
  * overlap, except that the state a call leaves may be the buffer it starts from.
  *
@@ -115,7 +115,7 @@ conv_status seq_conv_step(seq_plan_t plan, const seq_conv_args* args, void* stre
  * with g(d) = d / (D/G): the D channels share B and C in G groups (G divides D).  h starts
  * from the sequence's state (fp32), or zero.  1 <= N <= 128 states per channel.
  * CONV_ERR_INVALID_ARG for sizes out of range, CONV_ERR_UNSUPPORTED for N > 128, more
- * than 2^30 tokens or 2^22 channels.
+ * than 2^30 tokens or 2^22 channels, or D N beyond 2^31 - 1.
  */
 conv_status seq_scan_plan_create(seq_plan_t* out, int64_t S, int64_t T, int64_t D, int64_t N, int64_t G,
                                  conv_dtype dtype, seq_direction direction, unsigned flags);
