@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(THREADS, 6) seq_scan_kernel(const __grid_const
             for (int e = 0; e < 2; ++e)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    h[e][k + j] = fma2(exp2_2(mul2(dl[e], A2[e][k + j])), h[e][k + j], mul2(uu[e], bk[j]));
+                    h[e][k + j] = fma2(decay2(dl[e], A2[e][k + j]), h[e][k + j], mul2(uu[e], bk[j]));
                     if (!SUMMARY) acc[e][j] = k ? fma2(ck[j], h[e][k + j], acc[e][j]) : mul2(ck[j], h[e][k + j]);
                 }
         }
@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(STEP_THREADS, ROWS > 1 && VEC ? 7 : 1) seq_sca
             float2 acc = zero;
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                h[r][k] = fma2(exp2_2(mul2(dl, A2[k])), h[r][k], mul2(u, B[r][k]));
+                h[r][k] = fma2(decay2(dl, A2[k]), h[r][k], mul2(u, B[r][k]));
                 acc = fma2(C[r][k], h[r][k], acc);
             }
             if (on && p.h_out && slot[r] >= 0) {

@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(THREADS, 3) seq_scan_bwd_kernel(const __grid_c
                 const float2 delta = *reinterpret_cast<const float2*>(&sm.tok[t].delta[place_c[i]]);
                 const float2 u = *reinterpret_cast<const float2*>(&sm.tok[t].u[place_c[i]]);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) h[i][k] = fma2(exp2_2(mul2(delta, A2[i][k])), h[i][k], mul2(u, b[k]));
+                for (int k = 0; k < 4; ++k) h[i][k] = fma2(decay2(delta, A2[i][k]), h[i][k], mul2(u, b[k]));
             }
         }
         // Backward.  Shared memory holds the state before every other token; the one before an odd token is
@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(THREADS, 3) seq_scan_bwd_kernel(const __grid_c
                         const float2 delta = *reinterpret_cast<const float2*>(&sm.tok[t - 1].delta[place_c[i]]);
                         const float2 u = *reinterpret_cast<const float2*>(&sm.tok[t - 1].u[place_c[i]]);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) hp[i][k] = fma2(exp2_2(mul2(delta, A2[i][k])), hp[i][k], mul2(u, b[k]));
+                        for (int k = 0; k < 4; ++k) hp[i][k] = fma2(decay2(delta, A2[i][k]), hp[i][k], mul2(u, b[k]));
                     }
                 }
             }
@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(THREADS, 3) seq_scan_bwd_kernel(const __grid_c
                 const float2 dyc = *reinterpret_cast<const float2*>(&sm.tok[t].dyc[place_c[i]]);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const float2 a = exp2_2(mul2(delta, A2[i][k]));
+                    const float2 a = decay2(delta, A2[i][k]);
                     const float2 ah = mul2(a, hp[i][k]);
                     const float2 h = fma2(u, b[k], ah);
                     const float2 gr = fma2(c[k], dyc, gam[i][k]);
@@ -585,7 +585,7 @@ __global__ void __launch_bounds__(BACK_THREADS) seq_scan_back_kernel(const __gri
                 for (int e = 0; e < 2; ++e)
 #pragma unroll
                     for (int j = 0; j < 2; ++j)
-                        gam[e][k + j] = mul2(exp2_2(mul2(dl[e], A2[e][k + j])), fma2(ck[j], dc[e], gam[e][k + j]));
+                        gam[e][k + j] = mul2(decay2(dl[e], A2[e][k + j]), fma2(ck[j], dc[e], gam[e][k + j]));
             }
             total = sum2(total, delta);
         }

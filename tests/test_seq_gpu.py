@@ -439,3 +439,15 @@ def test_norm_in_place_and_zero_rows():
     O.check("y", host(y), ref["y"], mag["y"], 130, True)
     O.check("res", host(r), ref["res_out"], mag["res_out"], 130, False)
     assert np.array_equal(host(y)[2], be)
+
+
+# ---------------------------------------------------------------------------------- together
+def test_block_example_decodes_what_the_whole_sequence_gives():
+    """examples/ssm_block.py: a prompt and steps behind it against all tokens at once.  Between the calls
+    every activation is rounded to bf16 (2^-9 relative); the two ways differ by such roundings only, over the
+    handful of them that a token passes: far below 1e-2."""
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import ssm_block
+    assert ssm_block.main(["--batch", "3", "--length", "40", "--width", "64", "--steps", "5"]) < 1e-2
