@@ -341,8 +341,10 @@ static conv_status scan_call(seq_plan_t p, const seq_scan_args* a, seq_direction
     q.dy_ld = a->dy_ld; q.dx_ld = a->dx_ld; q.ddt_ld = a->ddt_ld; q.dB_ld = a->dB_ld; q.dC_ld = a->dC_ld; q.dz_ld = a->dz_ld;
     q.cblocks = p->blocks;
     auto aligned = [](const void* v, size_t n) { return reinterpret_cast<uintptr_t>(v) % n == 0; };
-    q.quads = p->N % 4 == 0 && aligned(a->A, 16) && aligned(a->h_in, 16) && aligned(a->h_out, 16) && aligned(a->B, 4 * e) &&
-              aligned(a->C, 4 * e) && a->B_ld % 4 == 0 && a->C_ld % 4 == 0;
+    q.quads = p->N % 4 == 0 && aligned(a->A, 16);
+    if (dir == SEQ_STEP)
+        q.quads = q.quads && aligned(a->h_in, 16) && aligned(a->h_out, 16) && aligned(a->B, 4 * e) && aligned(a->C, 4 * e) &&
+                  a->B_ld % 4 == 0 && a->C_ld % 4 == 0;
     q.wide = c.wide && (p->D / p->G * e) % 16 == 0 ? 16 : c.words && (p->D / p->G * e) % 4 == 0 ? 4 : 0;
     unsigned char* w = static_cast<unsigned char*>(p->ws);
     if (dir == SEQ_FWD && p->ws_bytes) {

@@ -177,7 +177,7 @@ __device__ __forceinline__ void rows_to_shared(T (*to)[W], const T* from, long l
 // Sum of the values at `rows` rows `step` apart, of 32 neighbouring columns (`src`: the column of lane
 // threadIdx.x & 31) by a block of COLUMN_THREADS: warps take turns at the rows, then the first warp adds their
 // sums in order and holds the result.  Called by the whole block.
-constexpr int COLUMN_THREADS = 512;
+constexpr int COLUMN_THREADS = 1024;
 __device__ __forceinline__ float column_sum(const float* src, long long step, int rows, bool on) {
     constexpr int WARPS = COLUMN_THREADS / 32;
     __shared__ float part[WARPS][32];

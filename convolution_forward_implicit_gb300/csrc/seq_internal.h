@@ -92,7 +92,7 @@ struct SeqScanParams {
     float* part_bc;                 // backward: [channel blocks][T][2][N] partial dB, dC
     float* part_par;                // backward: [pieces][N + 2][D] partial dA, dD, ddt_bias
     int cblocks;                    // backward: channel blocks (over all groups)
-    int quads;                      // step: 1 when states, A, B and C lie in whole aligned groups of 4
+    int quads;                      // 1 when A (step: states, B and C too) lies in whole aligned groups of 4
     int wide;                       // rows and groups consist of whole aligned pieces of so many bytes: 16, 4 or 0 (of single elements)
 };
 

@@ -193,26 +193,25 @@ __global__ void __launch_bounds__(COLUMN_THREADS) seq_norm_param_kernel(const __
     const bool on = c < p.D, first = threadIdx.x < 32 && on;
     auto total = [&](int k) { return column_sum(p.ws + (long long)k * p.D + c, (long long)SUMS * p.D, parts, on); };
     auto param = [&](const void* v, float none) { return v && on ? seq_ld(static_cast<const T*>(v) + c) : none; };
+    // y 0: S1 alone; 1 (with biases): S1 and S0; 2, 3: those of w_pre and b_pre
     if (blockIdx.y == 0) {
+        if (!p.dw_post && (bias || !p.dscale)) return;
         const float s1 = total(0);
-        float s0 = 0.f;
-        if (bias) {
-            __syncthreads();
-            s0 = total(1);
-        }
         if (first && p.dw_post) p.dw_post[c] = param(p.scale, 1.f) * s1;
+        if (first && !bias && p.dscale) p.dscale[c] = param(p.w_post, 1.f) * s1;
+    } else if (blockIdx.y == 1) {
+        if (!bias || (!p.db_post && !p.dscale)) return;
+        const float s0 = total(1);
         if (first && p.db_post) p.db_post[c] = param(p.scale, 1.f) * s0;
-        if (first && p.dscale) p.dscale[c] = fmaf(param(p.w_post, 1.f), s1, param(p.b_post, 0.f) * s0);
+        if (!p.dscale) return;
+        __syncthreads();
+        const float s1 = total(0);
+        if (first) p.dscale[c] = fmaf(param(p.w_post, 1.f), s1, param(p.b_post, 0.f) * s0);
     } else {
-        if (p.dw_pre) {
-            const float v = total(2);
-            if (first) p.dw_pre[c] = v;
-        }
-        if (p.db_pre) {
-            __syncthreads();
-            const float v = total(3);
-            if (first) p.db_pre[c] = v;
-        }
+        float* out = blockIdx.y == 2 ? p.dw_pre : p.db_pre;
+        if (!out) return;
+        const float v = total(blockIdx.y);
+        if (first) out[c] = v;
     }
 }
 
@@ -255,7 +254,7 @@ cudaError_t launch_u(const SeqNormParams& p, const Shape& s, bool bias, cudaStre
     cudaError_t e = RING ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, s.smem) : cudaSuccess;
     if (e == cudaSuccess) e = launch_kernel(kernel, dim3((unsigned)s.blocks), s.block, (size_t)s.smem, stream, false, 1, p);
     if (e == cudaSuccess && p.ws)
-        e = launch_kernel(seq_norm_param_kernel<T>, dim3((unsigned)((p.D + 31) / 32), 2), dim3(COLUMN_THREADS), 0, stream, false, 1, p,
+        e = launch_kernel(seq_norm_param_kernel<T>, dim3((unsigned)((p.D + 31) / 32), SUMS), dim3(COLUMN_THREADS), 0, stream, false, 1, p,
                           s.blocks * (int)s.block.y, bias);
     return e;
 }

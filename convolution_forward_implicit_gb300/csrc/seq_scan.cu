@@ -86,13 +86,11 @@ __global__ void __launch_bounds__(THREADS, 6) seq_scan_kernel(const __grid_const
     // packed values hold states 2 k and 2 k + 1 of the thread's, or its two channels
     float2 A2[2][NPT / 2], h[2][NPT / 2];
 #pragma unroll
-    for (int e = 0; e < 2; ++e)
+    for (int e = 0; e < 2; ++e) {
+        scan_decays<NPT>(p, d[e], n0, A2[e]);
 #pragma unroll
-        for (int k = 0; k < NPT / 2; ++k) {
-            const float* A = p.A + (long long)d[e] * p.N + n0 + 2 * k;
-            A2[e][k] = make_float2(n0 + 2 * k < p.N ? A[0] * LOG2E : 0.f, n0 + 2 * k + 1 < p.N ? A[1] * LOG2E : 0.f);
-            h[e][k] = make_float2(0.f, 0.f);
-        }
+        for (int k = 0; k < NPT / 2; ++k) h[e][k] = make_float2(0.f, 0.f);
+    }
     const float2 Dd = p.Dskip ? make_float2(p.Dskip[d[0]], p.Dskip[d[1]]) : make_float2(0.f, 0.f);
     const float2 bias = p.dt_bias ? make_float2(p.dt_bias[d[0]], p.dt_bias[d[1]]) : make_float2(0.f, 0.f);
     float2 total = make_float2(0.f, 0.f);
@@ -182,6 +180,10 @@ __global__ void __launch_bounds__(THREADS, 6) seq_scan_kernel(const __grid_const
             yp += p.y_ld;
         }
     };
+    // Launched behind the joining kernel, this one may have started before it ended: what is above here reads the
+    // call's inputs only, which were there before its first kernel began.
+    if (SUMMARY) griddep_launch();
+    else griddep_wait();
     if (!SUMMARY && q.begin < t0) get(p.piece_state, piece);      // the state that the pieces before leave
     int buf = 0, stage = 0;
     for (int tb = t0; tb < t1; tb += SCAN_TILE, buf ^= 1) {
@@ -222,59 +224,81 @@ __global__ void __launch_bounds__(THREADS, 6) seq_scan_kernel(const __grid_const
 
 // Joins the pieces of a sequence (of a ragged axis): with e_r what piece r adds to the state behind it and
 // sum_r its sum of delta, the state before piece r + 1 is c_{r+1} = e_r + exp(sum_r A) c_r, or e_r alone where
-// a sequence begins in piece r (backward: the same from the last piece down).  A thread has 4 states of a
-// channel and replaces e_r by c_r, a batch of pieces at a time so that their loads overlap.
-template <bool REVERSE>
-__global__ void __launch_bounds__(STEP_THREADS) seq_scan_join_kernel(const __grid_constant__ SeqScanParams p) {
+// a sequence begins in piece r (backward: the same from the last piece down).  A thread replaces e_r by c_r for
+// 4 states of a channel in a quarter of the pieces.  It first joins its own quarter from a zero state, keeping
+// the sum of delta over it; the four quarters' results pass through shared memory; then it walks the quarter
+// again from the state before it.  (One thread for all 52 pieces of a 2048 x 2048 x 16 prompt: 8.3 us, most of
+// it waiting for one batch of loads after another.)
+// Up to 16 pieces one part is enough.
+constexpr int JOIN_THREADS = 128, JOIN_MOST = 16;
+template <bool REVERSE, int JOIN_PARTS>
+__global__ void __launch_bounds__(JOIN_THREADS) seq_scan_join_kernel(const __grid_constant__ SeqScanParams p) {
+    constexpr int JOIN_LANES = JOIN_THREADS / JOIN_PARTS;
+    __shared__ float4 sh_e[JOIN_PARTS][JOIN_LANES];
+    __shared__ float sh_sum[JOIN_PARTS][JOIN_LANES];
+    __shared__ bool sh_cut[JOIN_PARTS];
     const int pieces = p.pc.pps > 0 ? p.pc.pps : p.pc.count, first = blockIdx.y * pieces;
-    // which pieces cut the chain: lane l looks at pieces l and l + 32
-    unsigned long long cut = 0;
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-        const int r = half * 32 + (threadIdx.x & 31);
-        bool stop = false;
-        if (r < pieces) {
-            int t0, t1;
-            scan_piece_range(p.ax, p.pc, first + r, t0, t1);
-            const int s = seq_first_at(p.ax, REVERSE ? t0 + 1 : t0);      // the first sequence that begins in the piece (behind its first token)
-            const int begin = seq_start(p.ax, s, t0);
-            stop = REVERSE ? begin <= t1 : begin < t1;
-        }
-        cut |= (unsigned long long)__ballot_sync(~0u, stop) << (32 * half);
+    const int lane = threadIdx.x % JOIN_LANES, part = threadIdx.x / JOIN_LANES;
+    const int len = (pieces + JOIN_PARTS - 1) / JOIN_PARTS, r0 = part * len, r1 = min(r0 + len, pieces);
+    // which of the quarter's pieces cut the chain, in the order of the walk: lane l looks at the l-th
+    bool stop = false;
+    const int look = r0 + (threadIdx.x & 31);
+    if (look < r1) {
+        int t0, t1;
+        scan_piece_range(p.ax, p.pc, first + (REVERSE ? pieces - 1 - look : look), t0, t1);
+        const int s = seq_first_at(p.ax, REVERSE ? t0 + 1 : t0);      // the first sequence that begins in the piece (behind its first token)
+        const int begin = seq_start(p.ax, s, t0);
+        stop = REVERSE ? begin <= t1 : begin < t1;
     }
+    const unsigned cut = __ballot_sync(~0u, stop);
     const int quads = (p.N + 3) >> 2;
-    const long long i = blockIdx.x * (long long)STEP_THREADS + threadIdx.x;
-    if (i >= (long long)quads * p.D) return;
-    const int quad = (int)(i / p.D), d = (int)(i - (long long)quad * p.D);
-    float A2[4], c[4] = {};
+    const long long i = blockIdx.x * (long long)JOIN_LANES + lane;
+    const bool on = i < (long long)quads * p.D;
+    const int quad = on ? (int)(i / p.D) : 0, d = on ? (int)(i - (long long)quad * p.D) : 0;
+    float A2[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) A2[k] = 4 * quad + k < p.N ? p.A[(long long)d * p.N + 4 * quad + k] * LOG2E : 0.f;
-    constexpr int BATCH = 8;
-    for (int r0 = 0; r0 < pieces; r0 += BATCH) {
-        float4 e[BATCH];
-        float sum[BATCH];
+    for (int k = 0; k < 4; ++k) A2[k] = on && 4 * quad + k < p.N ? p.A[(long long)d * p.N + 4 * quad + k] * LOG2E : 0.f;
+    griddep_wait();                  // from here on: what the pass before wrote
+    griddep_launch();
+    float4 e[JOIN_MOST];
+    float sum[JOIN_MOST];
 #pragma unroll
-        for (int j = 0; j < BATCH; ++j) {
-            const int r = r0 + j;
-            e[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-            sum[j] = 0.f;
-            if (r < pieces - 1) {                    // (the last piece hands nothing on)
-                const int at = REVERSE ? pieces - 1 - r : r;
-                e[j] = *reinterpret_cast<const float4*>(p.piece_state + scan_state_at(p, first + at, quad, d));
-                sum[j] = p.piece_delta[(long long)(first + at) * p.D + d];
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < BATCH; ++j) {
-            const int r = r0 + j, at = REVERSE ? pieces - 1 - r : r;
-            if (r >= pieces) break;
-            *reinterpret_cast<float4*>(p.piece_state + scan_state_at(p, first + at, quad, d)) = make_float4(c[0], c[1], c[2], c[3]);
-            const float v[4] = {e[j].x, e[j].y, e[j].z, e[j].w};
-            const bool stop = cut >> at & 1;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) c[k] = stop ? v[k] : fmaf(ex2_approx(sum[j] * A2[k]), c[k], v[k]);
+    for (int j = 0; j < JOIN_MOST; ++j) {
+        const int r = r0 + j, at = first + (REVERSE ? pieces - 1 - r : r);
+        e[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        sum[j] = 0.f;
+        if (on && r < r1 && r < pieces - 1) {                        // (the last piece hands nothing on)
+            e[j] = *reinterpret_cast<const float4*>(p.piece_state + scan_state_at(p, at, quad, d));
+            sum[j] = p.piece_delta[(long long)at * p.D + d];
         }
     }
+    float4 c = make_float4(0.f, 0.f, 0.f, 0.f);
+    float total = 0.f;
+    auto step = [&](float4 c, float4 e, float sum, bool stop) {
+        if (stop) return e;
+        return make_float4(fmaf(ex2_approx(sum * A2[0]), c.x, e.x), fmaf(ex2_approx(sum * A2[1]), c.y, e.y),
+                           fmaf(ex2_approx(sum * A2[2]), c.z, e.z), fmaf(ex2_approx(sum * A2[3]), c.w, e.w));
+    };
+#pragma unroll
+    for (int j = 0; j < JOIN_MOST; ++j)
+        if (r0 + j < r1) {
+            c = step(c, e[j], sum[j], cut >> j & 1);
+            total = cut >> j & 1 ? 0.f : total + sum[j];
+        }
+    sh_e[part][lane] = c;
+    sh_sum[part][lane] = total;
+    if (lane == 0) sh_cut[part] = cut != 0;
+    __syncthreads();
+    c = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int q = 0; q < part; ++q) c = step(c, sh_e[q][lane], sh_sum[q][lane], sh_cut[q]);
+    if (!on) return;
+#pragma unroll
+    for (int j = 0; j < JOIN_MOST; ++j)
+        if (r0 + j < r1) {
+            const int r = r0 + j, at = first + (REVERSE ? pieces - 1 - r : r);
+            *reinterpret_cast<float4*>(p.piece_state + scan_state_at(p, at, quad, d)) = c;
+            c = step(c, e[j], sum[j], cut >> j & 1);
+        }
 }
 
 // Empty sequences hand their state on.
@@ -401,12 +425,13 @@ cudaError_t launch_fwd(const SeqScanParams& p, cudaStream_t stream) {
     const dim3 grid((unsigned)p.pc.count, (unsigned)(p.G * ((per + CB - 1) / CB)));
     cudaError_t e = cudaSuccess;
     if (p.ax.T > 0) {
-        if (p.pc.pps != 1 && p.pc.count > 1)
+        const bool cut = p.pc.pps != 1 && p.pc.count > 1;
+        if (cut)
             e = launch_kernel(seq_scan_kernel<T, NPT, LN, true, false>, grid, dim3(THREADS), 0, stream, false, 1, p);
-        if (e == cudaSuccess && p.pc.pps != 1 && p.pc.count > 1) e = launch_seq_scan_join(p, false, stream);
+        if (e == cudaSuccess && cut) e = launch_seq_scan_join(p, false, stream);
         if (e == cudaSuccess)
-            e = p.z ? launch_kernel(seq_scan_kernel<T, NPT, LN, false, true>, grid, dim3(THREADS), 0, stream, false, 1, p)
-                    : launch_kernel(seq_scan_kernel<T, NPT, LN, false, false>, grid, dim3(THREADS), 0, stream, false, 1, p);
+            e = p.z ? launch_kernel(seq_scan_kernel<T, NPT, LN, false, true>, grid, dim3(THREADS), 0, stream, cut, 1, p)
+                    : launch_kernel(seq_scan_kernel<T, NPT, LN, false, false>, grid, dim3(THREADS), 0, stream, cut, 1, p);
     }
     if (e == cudaSuccess && p.h_out && p.h_out != p.h_in && p.ax.L == 0) e = launch_seq_scan_empty(p, p.h_in, p.h_out, stream);
     return e;
@@ -451,9 +476,11 @@ cudaError_t launch_step_t(const SeqScanParams& p, cudaStream_t stream) {
 
 cudaError_t launch_seq_scan_join(const SeqScanParams& p, bool reverse, cudaStream_t stream) {
     const long long all = (long long)((p.N + 3) / 4) * p.D;
-    const dim3 grid((unsigned)((all + STEP_THREADS - 1) / STEP_THREADS), (unsigned)(p.pc.pps > 0 ? p.ax.S : 1));
-    return reverse ? launch_kernel(seq_scan_join_kernel<true>, grid, dim3(STEP_THREADS), 0, stream, false, 1, p)
-                   : launch_kernel(seq_scan_join_kernel<false>, grid, dim3(STEP_THREADS), 0, stream, false, 1, p);
+    const int pieces = p.pc.pps > 0 ? p.pc.pps : p.pc.count, parts = pieces <= JOIN_MOST ? 1 : 4, lanes = JOIN_THREADS / parts;
+    const dim3 grid((unsigned)((all + lanes - 1) / lanes), (unsigned)(p.pc.pps > 0 ? p.ax.S : 1));
+    auto kernel = parts == 1 ? (reverse ? seq_scan_join_kernel<true, 1> : seq_scan_join_kernel<false, 1>)
+                             : (reverse ? seq_scan_join_kernel<true, 4> : seq_scan_join_kernel<false, 4>);
+    return launch_kernel(kernel, grid, dim3(JOIN_THREADS), 0, stream, true, 1, p);
 }
 cudaError_t launch_seq_scan_empty(const SeqScanParams& p, const float* from, float* to, cudaStream_t stream) {
     const long long DN = (long long)p.D * p.N, blocks = DN / 1024 + 1;

@@ -93,4 +93,25 @@ __device__ __forceinline__ void ld2(const float* p, float2& a, float2& b) {
 }
 __device__ __forceinline__ void st2(float* p, float2 a, float2 b) { *reinterpret_cast<float4*>(p) = make_float4(a.x, a.y, b.x, b.y); }
 
+// A2 = A log2(e) of states n0 .. n0 + NPT - 1 of channel d, as pairs; zero behind the last state.  Rows of
+// whole aligned quads are read 16 bytes at a time.
+template <int NPT>
+__device__ __forceinline__ void scan_decays(const SeqScanParams& p, int d, int n0, float2 (&A2)[NPT / 2]) {
+    const float* A = p.A + (long long)d * p.N + n0;
+#pragma unroll
+    for (int k = 0; k < NPT / 2; k += 2) {
+        float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (p.quads) {
+            if (n0 + 2 * k < p.N) q = *reinterpret_cast<const float4*>(A + 2 * k);
+        } else {
+            if (n0 + 2 * k < p.N) q.x = A[2 * k];
+            if (n0 + 2 * k + 1 < p.N) q.y = A[2 * k + 1];
+            if (n0 + 2 * k + 2 < p.N) q.z = A[2 * k + 2];
+            if (n0 + 2 * k + 3 < p.N) q.w = A[2 * k + 3];
+        }
+        A2[k] = mul2(make_float2(q.x, q.y), dup2(LOG2E));
+        A2[k + 1] = mul2(make_float2(q.z, q.w), dup2(LOG2E));
+    }
+}
+
 }  // namespace convfwd

@@ -162,18 +162,27 @@ __global__ void __launch_bounds__(THREADS, 3) seq_scan_bwd_kernel(const __grid_c
     // Every packed value holds channels cw[i] and cw[i] + 1.
     float2 A2[2][4], gam[2][4], dA[2][4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < 2; ++i) {
+        float2 v[2][2];                           // channel, pair of states in the lane's own order
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            float v[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int cl = cw[i] + e, nk = n0[k >> 1] + (k & 1);
-                v[e] = cl < width && nk < p.N ? p.A[(long long)(d0 + cl) * p.N + nk] * LOG2E : 0.f;
+        for (int e = 0; e < 2; ++e) {
+            scan_decays<4>(p, d0 + min(cw[i] + e, width - 1), nq, v[e]);
+            if (cw[i] + e >= width) v[e][0] = v[e][1] = make_float2(0.f, 0.f);
+            if (nh) {
+                const float2 t = v[e][0];
+                v[e][0] = v[e][1];
+                v[e][1] = t;
             }
-            A2[i][k] = make_float2(v[0], v[1]);
-            gam[i][k] = dA[i][k] = make_float2(0.f, 0.f);
         }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            A2[i][2 * k] = make_float2(v[0][k].x, v[1][k].x);
+            A2[i][2 * k + 1] = make_float2(v[0][k].y, v[1][k].y);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) gam[i][k] = dA[i][k] = make_float2(0.f, 0.f);
+    }
+    griddep_wait();          // (as the forward kernel: above here, the call's inputs only)
     // the gradient that the sequence's later pieces send back to the state behind this piece
     if (t0 < t1 && p.pc.pps != 1 && p.pc.count > 1) {
         const int s = seq_first_at(p.ax, t1) - 1;                // the sequence of the piece's last token
@@ -533,13 +542,11 @@ __global__ void __launch_bounds__(BACK_THREADS) seq_scan_back_kernel(const __gri
 
     float2 A2[2][NPT / 2], gam[2][NPT / 2];
 #pragma unroll
-    for (int e = 0; e < 2; ++e)
+    for (int e = 0; e < 2; ++e) {
+        scan_decays<NPT>(p, d[e], n0, A2[e]);
 #pragma unroll
-        for (int k = 0; k < NPT / 2; ++k) {
-            const float* A = p.A + (long long)d[e] * p.N + n0 + 2 * k;
-            A2[e][k] = make_float2(n0 + 2 * k < p.N ? A[0] * LOG2E : 0.f, n0 + 2 * k + 1 < p.N ? A[1] * LOG2E : 0.f);
-            gam[e][k] = make_float2(0.f, 0.f);
-        }
+        for (int k = 0; k < NPT / 2; ++k) gam[e][k] = make_float2(0.f, 0.f);
+    }
     const float2 bias = p.dt_bias ? make_float2(p.dt_bias[d[0]], p.dt_bias[d[1]]) : make_float2(0.f, 0.f);
     float2 total = make_float2(0.f, 0.f);
     // the only end of a sequence here is at t1, and the only beginning at t0
@@ -555,6 +562,7 @@ __global__ void __launch_bounds__(BACK_THREADS) seq_scan_back_kernel(const __gri
             }
         }
     }
+    griddep_launch();
     for (int tile = tiles - 1; tile >= 0; --tile) {
         const int tb = t0 + tile * SCAN_TILE, n = min(SCAN_TILE, t1 - tb), buf = tile & 1, stage = tile % STAGES;
 #pragma unroll
@@ -603,6 +611,7 @@ __global__ void __launch_bounds__(BACK_THREADS) seq_scan_back_kernel(const __gri
 // dB and dC: the partial rows of a group's channel blocks, added in block order.
 template <typename T, int NP>
 __global__ void __launch_bounds__(128) seq_scan_bc_kernel(const __grid_constant__ SeqScanParams p) {
+    griddep_wait();
     const int bpg = p.cblocks / p.G;
     const long long all = (long long)p.ax.T * p.G * 2 * NP;
     for (long long i = blockIdx.x * 128ll + threadIdx.x; i < all; i += gridDim.x * 128ll) {
@@ -627,6 +636,7 @@ __global__ void __launch_bounds__(128) seq_scan_bc_kernel(const __grid_constant_
 
 // dA, dD, ddt_bias: the pieces' partial sums, added in piece order.
 __global__ void __launch_bounds__(128) seq_scan_par_kernel(const __grid_constant__ SeqScanParams p) {
+    griddep_wait();
     const int d = blockIdx.x * 128 + threadIdx.x, k = blockIdx.y;
     if (d >= p.D) return;
     float s[4] = {};
@@ -650,7 +660,7 @@ cudaError_t launch_main(const SeqScanParams& p, cudaStream_t stream) {
                                                (int)sizeof(BwdSmem<T, LN>));
     if (e != cudaSuccess) return e;
     return launch_kernel(seq_scan_bwd_kernel<T, LN, GATED>, dim3((unsigned)p.pc.count, (unsigned)p.cblocks), dim3(THREADS),
-                         sizeof(BwdSmem<T, LN>), stream, false, 1, p);
+                         sizeof(BwdSmem<T, LN>), stream, p.pc.pps != 1 && p.pc.count > 1, 1, p);
 }
 
 // LN: lanes of the main kernel; NPT, LB: states and lanes of the pieces' kernel
@@ -669,12 +679,12 @@ cudaError_t launch_ln(const SeqScanParams& p, cudaStream_t stream) {
         if (e == cudaSuccess) e = p.z ? launch_main<T, LN, true>(p, stream) : launch_main<T, LN, false>(p, stream);
         const long long all = ((long long)p.ax.T * p.G * 8 * LN + 127) / 128;
         if (e == cudaSuccess)
-            e = launch_kernel(seq_scan_bc_kernel<T, 4 * LN>, dim3((unsigned)(all < 65536 ? all : 65536)), dim3(128), 0, stream, false, 1, p);
+            e = launch_kernel(seq_scan_bc_kernel<T, 4 * LN>, dim3((unsigned)(all < 65536 ? all : 65536)), dim3(128), 0, stream, true, 1, p);
     }
     if (e == cudaSuccess && p.dh_in && p.ax.L == 0) e = launch_seq_scan_empty(p, p.dh_out, p.dh_in, stream);
     if (e == cudaSuccess)
         e = launch_kernel(seq_scan_par_kernel, dim3((unsigned)((p.D + 127) / 128), (unsigned)(p.N + 2)), dim3(128), 0, stream,
-                          false, 1, p);
+                          p.ax.T > 0 && !p.dh_in, 1, p);
     return e;
 }
 
