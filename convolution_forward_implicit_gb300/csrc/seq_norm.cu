@@ -10,7 +10,7 @@ namespace {
 template <typename T, typename RT, bool WIDE, int UPT, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS) seq_norm_fwd_kernel(const __grid_constant__ SeqNormParams p) {
     __shared__ __align__(16) NormSums buf;
-    int turn = 0;
+    RowSums<THREADS> sums;
     const long long row = (long long)blockIdx.x * blockDim.y + threadIdx.y;
     const int D = row < p.rows ? p.D : 0;            // a row behind the last one has no columns
     const bool layer = p.flags & SEQ_NORM_LAYER, gate = p.flags & (SEQ_NORM_GATE_BEFORE | SEQ_NORM_GATE_AFTER);
@@ -21,7 +21,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) seq_norm_fwd_kernel(c
     x_in.load(p.x, row * p.x_ld, D);
     if (gate) g_in.load(p.gate, row * p.gate_ld, D);
     if (residual) r_in.load(p.res, row * p.res_ld, D);
-    row_sum_init(buf);
+    sums.template init<UPT>(buf, p.D);
     float2 v[UPT][4], a[UPT][4];
     x_in.get(v);
     if (p.flags & SEQ_NORM_GATE_BEFORE) {
@@ -29,7 +29,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) seq_norm_fwd_kernel(c
         EACH_PAIR v[u][e] = pmul(v[u][e], silu2(a[u][e]));
     }
     if (p.flags & SEQ_NORM_POST) {
-        row_norm(v, p.D, layer, p.eps, buf, turn);
+        row_norm<WIDE>(v, p.D, layer, p.eps, sums, D > 0);
         col_mul<T, WIDE, UPT>(p.w_post, D, v);
         col_add<T, WIDE, UPT>(p.b_post, D, v);
     }
@@ -44,7 +44,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) seq_norm_fwd_kernel(c
         row_store<RT, WIDE, UPT>(p.res_out, row * p.res_out_ld, D, v);
     }
     if (p.flags & SEQ_NORM_PRE) {
-        row_norm(v, p.D, layer, p.eps, buf, turn);
+        row_norm<WIDE>(v, p.D, layer, p.eps, sums, D > 0);
         col_mul<T, WIDE, UPT>(p.w_pre, D, v);
         col_add<T, WIDE, UPT>(p.b_pre, D, v);
     }

@@ -188,51 +188,87 @@ __device__ __forceinline__ void row_take(uint32_t at, float2 (&v)[UPT][4]) {
     }
 }
 
-// Sums K values over the threads of a row; every thread of the block calls it together.  `turn`
-// alternates between two halves of the shared buffer, so one barrier a call is enough.  The warps' sums lie
-// in groups of four, which each thread reads at once and adds up in order.
+// Sums over the threads of a row.  A warp sums by shuffles, so that all of its lanes hold the same value and
+// store it to the warp's slot (one store, no predicate); behind a barrier each thread reads the row's slots
+// four at a time and adds them up in order.  Two halves of the buffer take turns, so one barrier a sum is
+// enough.  Every thread of the block takes part.  THREADS: of the block at most.
 struct NormSums {
-    float v[2][2][32];       // turn, value, warp
+    float v[2][4][64];       // turn, value, slot: a row has THREADS / 32 of them, or more threads in one row
+    float n[64];             // columns of the slot's warp
 };
-template <int N>
-struct NormGroups {
-    static constexpr int n = N;
-};
-__device__ __forceinline__ void row_sum_init(NormSums& b) {
-    for (int i = threadIdx.y * blockDim.x + threadIdx.x; i < 128; i += blockDim.x * blockDim.y) (&b.v[0][0][0])[i] = 0.f;
-    __syncthreads();
-}
-template <int K>
-__device__ __forceinline__ void row_sum(float (&v)[K], NormSums& b, int& turn) {
+template <int THREADS>
+struct RowSums {
+    static constexpr int SLOTS = (THREADS / 32 + 3) / 4 * 4;
+    uint32_t put, half, get, counts;     // shared addresses: the warp's slot (and, for lanes 16 .. 31, the next value's)
+    int turn;
+    float n, inv_n;
+    template <int UPT>
+    __device__ __forceinline__ void init(NormSums& b, int D) {
+        const int tid = threadIdx.y * blockDim.x + threadIdx.x, all = blockDim.x * blockDim.y;
+        for (int i = tid; i < (int)(sizeof(NormSums) / 4); i += all) (&b.v[0][0][0])[i] = 0.f;
+        __syncthreads();
+        const int first = threadIdx.y * SLOTS, warp = threadIdx.x >> 5;
+        int columns = 0;
 #pragma unroll
-    for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v[k] += __shfl_xor_sync(~0u, v[k], o);
-    const int wpr = blockDim.x >> 5;
-    if (wpr == 1) return;
-    const int fours = (wpr + 3) >> 2, first = threadIdx.y * fours * 4;
-    if ((threadIdx.x & 31) == 0) {
-#pragma unroll
-        for (int k = 0; k < K; ++k) b.v[turn][k][first + (threadIdx.x >> 5)] = v[k];
+        for (int u = 0; u < UPT; ++u) columns += max(0, min(256, D - (int)(warp * 32 + u * blockDim.x) * 8));
+        n = (float)columns;
+        inv_n = 1.0f / (float)max(columns, 1);
+        b.n[first + warp] = n;           // (read behind a sum's barrier)
+        get = (uint32_t)__cvta_generic_to_shared(&b.v[0][0][first]);
+        counts = (uint32_t)__cvta_generic_to_shared(&b.n[first]);
+        put = get + warp * 4;
+        half = put + (threadIdx.x & 16) * 16;
+        asm volatile("" : "+r"(put), "+r"(half), "+r"(get));       // (not to be worked out again at every use)
+        turn = 4 * 64 * 4;
     }
-    __syncthreads();
-    auto add = [&](auto groups) {                  // (slots behind the row's warps hold zeros)
+    __device__ __forceinline__ void next() { put += turn, half += turn, get += turn, turn = -turn; }
+    static __device__ __forceinline__ void store(uint32_t at, float v) { asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory"); }
+    static __device__ __forceinline__ float4 four(uint32_t at) {
+        float4 q;
+        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(q.x), "=f"(q.y), "=f"(q.z), "=f"(q.w) : "r"(at) : "memory");
+        return q;
+    }
+    static __device__ __forceinline__ void barrier() {
+        if (blockDim.x == 32) __syncwarp();
+        else __syncthreads();
+    }
+    // of one value over the warp; of two, one in lanes 0 .. 15 and the other in 16 .. 31
+    static __device__ __forceinline__ float warp(float a) {
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            float4 q[decltype(groups)::n];
+        for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(~0u, a, o);
+        return a;
+    }
+    static __device__ __forceinline__ float warp(float a, float b) {
+        const bool up = threadIdx.x & 16;
+        float v = (up ? b : a) + __shfl_xor_sync(~0u, up ? a : b, 16);
 #pragma unroll
-            for (int w = 0; w < decltype(groups)::n; ++w) q[w] = *reinterpret_cast<const float4*>(&b.v[turn][k][first + 4 * w]);
-            v[k] = 0.f;
+        for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+        return v;
+    }
+    __device__ __forceinline__ float slots(int k) const {
+        float s = 0.f;
 #pragma unroll
-            for (int w = 0; w < decltype(groups)::n; ++w) v[k] += (q[w].x + q[w].y) + (q[w].z + q[w].w);
+        for (int w = 0; w < SLOTS; w += 4) {
+            const float4 q = four(get + (k * 64 + w) * 4);
+            s += (q.x + q.y) + (q.z + q.w);
         }
-    };
-    if (fours == 1) add(NormGroups<1>());
-    else if (fours == 2) add(NormGroups<2>());
-    else if (fours <= 4) add(NormGroups<4>());
-    else add(NormGroups<8>());
-    turn ^= 1;
-}
+        return s;
+    }
+    __device__ __forceinline__ float sum(float a) {
+        store(put, warp(a));
+        barrier();
+        a = slots(0);
+        next();
+        return a;
+    }
+    __device__ __forceinline__ void sum(float& a, float& b) {
+        store(half, warp(a, b));
+        barrier();
+        a = slots(0);
+        b = slots(1);
+        next();
+    }
+};
 template <int UPT>
 __device__ __forceinline__ float lane_total(const float2 (&v)[UPT][4]) {
     float2 s = make_float2(0.f, 0.f);
@@ -245,27 +281,79 @@ __device__ __forceinline__ float lane_dot(const float2 (&v)[UPT][4], const float
     EACH_PAIR s = pfma(v[u][e], w[u][e], s);
     return s.x + s.y;
 }
-
-// v -> (v - mean) / sqrt(var + eps) (layer) or v / sqrt(mean(v^2) + eps) in place; returns the
-// factor 1 / sqrt(...).  Columns at and behind D stay zero.  The variance is summed from the centred
-// values, which keeps it exact for rows far from zero.
-template <int UPT>
-__device__ __forceinline__ float row_norm(float2 (&v)[UPT][4], int D, bool layer, float eps, NormSums& buf, int& turn) {
-    const float inv = 1.0f / (float)D;
-    float s[1];
-    if (layer) {
-        s[0] = lane_total(v);
-        row_sum(s, buf, turn);
-        const float mean = s[0] * inv;
-        EACH_PAIR {
-            const int c = (threadIdx.x + u * blockDim.x) * 8 + 2 * e;
-            if (c < D) v[u][e].x -= mean;
-            if (c + 1 < D) v[u][e].y -= mean;
+// v -= m in the row's columns
+template <bool WIDE, int UPT>
+__device__ __forceinline__ void row_shift(float2 (&v)[UPT][4], int D, float m) {
+    EACH_PAIR {
+        const int c = (threadIdx.x + u * blockDim.x) * 8;
+        if constexpr (WIDE) {
+            v[u][e] = padd(v[u][e], pdup(c < D ? -m : 0.f));
+        } else {
+            if (c + 2 * e < D) v[u][e].x -= m;
+            if (c + 2 * e + 1 < D) v[u][e].y -= m;
         }
     }
-    s[0] = lane_dot(v, v);
-    row_sum(s, buf, turn);
-    const float r = 1.0f / sqrtf(fmaf(s[0], inv, eps));
+}
+
+// What a layer norm's row is made of, from its warps' parts: warp w has n_w columns of mean m_w, the sum Q_w of
+// (v - m_w)^2, and (BACK) the sums P_w of e (v - m_w) and E_w of e.  With d_w = m_w - m_0,
+//   mean = m_0 + sum n_w d_w / D,   sum (v - mean)^2 = sum (Q_w + n_w d_w^2) - (sum n_w d_w)^2 / D,
+//   sum e (v - mean) = sum (P_w + d_w E_w) - (mean - m_0) sum E_w.
+// Only differences of the warps' means are squared, so rows far from zero lose nothing.  (Values 0 .. 3: m, E, Q, P.)
+template <bool BACK, int THREADS>
+__device__ __forceinline__ void row_moments(const RowSums<THREADS>& s, float inv_D, float& mean, float& Q, float& P, float& E) {
+    float a = 0.f, b = 0.f, m0 = 0.f;
+    Q = P = E = 0.f;
+#pragma unroll
+    for (int w = 0; w < s.SLOTS; w += 4) {
+        const float4 m = s.four(s.get + w * 4), q = s.four(s.get + (128 + w) * 4), n = s.four(s.counts + w * 4);
+        if (w == 0) m0 = m.x;
+        const float mm[4] = {m.x, m.y, m.z, m.w}, nn[4] = {n.x, n.y, n.z, n.w};
+        float d[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            d[i] = mm[i] - m0;
+            const float t = nn[i] * d[i];
+            a += t;
+            b = fmaf(t, d[i], b);
+        }
+        Q += (q.x + q.y) + (q.z + q.w);
+        if (BACK) {
+            const float4 e = s.four(s.get + (64 + w) * 4), p = s.four(s.get + (192 + w) * 4);
+            E += (e.x + e.y) + (e.z + e.w);
+            P += (p.x + p.y) + (p.z + p.w);
+            P = fmaf(d[0], e.x, fmaf(d[1], e.y, fmaf(d[2], e.z, fmaf(d[3], e.w, P))));
+        }
+    }
+    const float shift = a * inv_D;
+    mean = m0 + shift;
+    Q += fmaf(-shift, a, b);
+    if (BACK) P = fmaf(-shift, E, P);
+}
+
+// 1 / sqrt(v); 0 in the place of a row behind the last one, which must add nothing to the parameters' sums even
+// where eps is 0.
+__device__ __forceinline__ float norm_factor(float v, bool there) { return there ? 1.0f / sqrtf(v) : 0.f; }
+// v -> (v - mean) / sqrt(var + eps) (layer) or v / sqrt(mean(v^2) + eps) in place; returns the
+// factor 1 / sqrt(...).  Columns at and behind D stay zero.  One barrier.
+template <bool WIDE, int UPT, int THREADS>
+__device__ __forceinline__ float row_norm(float2 (&v)[UPT][4], int D, bool layer, float eps, RowSums<THREADS>& s, bool there) {
+    const float inv = 1.0f / (float)D;
+    float q;
+    if (layer) {
+        const float m = s.warp(lane_total(v)) * s.inv_n;
+        row_shift<WIDE>(v, D, m);
+        s.store(s.put, m);
+        s.store(s.put + 2 * 64 * 4, s.warp(lane_dot(v, v)));
+        s.barrier();
+        float mean, unused;
+        row_moments<false>(s, inv, mean, q, unused, unused);
+        s.next();
+        row_shift<WIDE>(v, D, mean - m);
+    } else {
+        q = s.sum(lane_dot(v, v));
+    }
+    const float r = norm_factor(fmaf(q, inv, eps), there);
     EACH_PAIR v[u][e] = pmul(v[u][e], pdup(r));
     return r;
 }

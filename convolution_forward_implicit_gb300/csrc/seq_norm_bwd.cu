@@ -13,31 +13,11 @@ namespace {
 
 constexpr int SUMS = 4;      // S1, S0, and those of w_pre and b_pre
 
-// e (the gradient behind w) -> the gradient at v, in place
-template <int UPT>
-__device__ __forceinline__ void norm_back(float2 (&d)[UPT][4], const float2 (&hat)[UPT][4], float r, int D, bool layer,
-                                          NormSums& buf, int& turn) {
-    float c, m = 0.f;
-    const float inv = 1.0f / (float)D;
-    if (layer) {
-        float s[2] = {lane_dot(d, hat), lane_total(d)};
-        row_sum(s, buf, turn);
-        c = s[0] * inv;
-        m = s[1] * inv;
-    } else {
-        float s[1] = {lane_dot(d, hat)};
-        row_sum(s, buf, turn);
-        c = s[0] * inv;
-    }
-    // r (d - hat c - m)
-    EACH_PAIR d[u][e] = pmul(pdup(r), pfma(hat[u][e], pdup(-c), padd(d[u][e], pdup(-m))));
-    if (layer) {
-        EACH_PAIR {
-            const int at = (threadIdx.x + u * blockDim.x) * 8 + 2 * e;
-            if (at >= D) d[u][e].x = 0.f;
-            if (at + 1 >= D) d[u][e].y = 0.f;
-        }
-    }
+// d (the gradient behind w) -> the gradient at v, in place, with hat, its r, c = mean(d hat), m = mean(d)
+template <bool WIDE, int UPT>
+__device__ __forceinline__ void norm_back(float2 (&d)[UPT][4], const float2 (&hat)[UPT][4], float r, float c, float m, int D, bool layer) {
+    if (layer) row_shift<WIDE>(d, D, m);
+    EACH_PAIR d[u][e] = pmul(pdup(r), pfma(hat[u][e], pdup(-c), d[u][e]));
 }
 
 // A block walks its rows.  RING: the next row is on its way to shared memory while this one is computed,
@@ -46,7 +26,8 @@ template <typename T, typename RT, bool WIDE, bool RING, int UPT, bool BIAS, int
 __global__ void __launch_bounds__(THREADS, THREADS <= 512 ? 512 / THREADS : 1) seq_norm_bwd_kernel(const __grid_constant__ SeqNormParams p) {
     extern __shared__ __align__(16) unsigned char ring[];
     __shared__ __align__(16) NormSums buf;
-    int turn = 0;
+    constexpr bool ONE = THREADS > 128 && RING;      // one row at a time
+    const int ty = ONE ? 0 : threadIdx.y, rows_at_once = ONE ? 1 : blockDim.y;
     const bool layer = p.flags & SEQ_NORM_LAYER;
     const bool post = p.flags & SEQ_NORM_POST, pre = p.flags & SEQ_NORM_PRE, residual = p.flags & SEQ_NORM_RESIDUAL;
     const bool gate = p.flags & (SEQ_NORM_GATE_BEFORE | SEQ_NORM_GATE_AFTER), after = p.flags & SEQ_NORM_GATE_AFTER;
@@ -55,9 +36,10 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 512 ? 512 / THREADS : 1) s
     // places in a stage: x, gate, dy, res, dres_out
     const int at_g = tb, at_dy = at_g + (gate ? tb : 0), at_res = at_dy + (has_dy ? tb : 0), at_dro = at_res + (use_res ? rb : 0);
     const int stage_bytes = at_dro + (has_dro ? rb : 0);
-    uint32_t mine = (uint32_t)__cvta_generic_to_shared(ring) + (threadIdx.y * blockDim.x + threadIdx.x) * 16;
+    uint32_t mine = (uint32_t)__cvta_generic_to_shared(ring) + (ty * blockDim.x + threadIdx.x) * 16;
     asm volatile("" : "+r"(mine));             // (not to be worked out again at every use)
-    const long long step = (long long)gridDim.x * blockDim.y;
+    const float inv_D = 1.0f / (float)p.D;
+    const long long step = (long long)gridDim.x * rows_at_once;
     auto fetch = [&](long long row, int stage) {
         if (!RING) return;
         if (row < p.rows) {
@@ -72,7 +54,7 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 512 ? 512 / THREADS : 1) s
     };
     float2 s_1[UPT][4], s_0[UPT][4], s_wpre[UPT][4], s_bpre[UPT][4];
     EACH_PAIR s_1[u][e] = s_0[u][e] = s_wpre[u][e] = s_bpre[u][e] = make_float2(0.f, 0.f);
-    long long row = (long long)blockIdx.x * blockDim.y + threadIdx.y;
+    long long row = (long long)blockIdx.x * rows_at_once + ty;
 #pragma unroll
     for (int i = 0; i < NORM_RING - 1; ++i) fetch(row + i * step, i);
     int stage = 0;
@@ -81,17 +63,18 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 512 ? 512 / THREADS : 1) s
     b_post.open(BIAS ? p.b_post : nullptr, p.D);
     scale.open(p.scale, p.D);
     w_pre.open(p.w_pre, p.D);
-    row_sum_init(buf);
-    for (long long base = (long long)blockIdx.x * blockDim.y; base < p.rows; base += step, row += step, stage = stage == NORM_RING - 1 ? 0 : stage + 1) {
+    RowSums<THREADS> sums;
+    sums.template init<UPT>(buf, p.D);
+    for (long long base = (long long)blockIdx.x * rows_at_once; base < p.rows; base += step, row += step, stage = stage == NORM_RING - 1 ? 0 : stage + 1) {
         fetch(row + (NORM_RING - 1) * step, stage == 0 ? NORM_RING - 1 : stage - 1);
-        const int D = row < p.rows ? p.D : 0;
+        const int D = ONE || row < p.rows ? p.D : 0;
         const uint32_t at = mine + stage * stage_bytes;
         if (RING) copies_wait<NORM_RING - 1>();
         auto take = [&](auto type, const void* from, long long ld, int place, float2 (&v)[UPT][4]) {
             using E = decltype(type);
             if (RING) {
                 row_take<E, UPT, THREADS>(at + place, v);
-                if (blockDim.y > 1 && D == 0) EACH_PAIR v[u][e] = make_float2(0.f, 0.f);
+                if (!ONE && D == 0) EACH_PAIR v[u][e] = make_float2(0.f, 0.f);
             } else {
                 row_load<E, WIDE, UPT>(from, row * ld, D, v);
             }
@@ -116,7 +99,7 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 512 ? 512 / THREADS : 1) s
             take(T(), p.gate, p.gate_ld, at_g, g);
             EACH_PAIR hat[u][e] = pmul(hat[u][e], silu2(g[u][e]));
         }
-        if (post) r_post = row_norm(hat, p.D, layer, p.eps, buf, turn);
+        if (post) r_post = row_norm<WIDE>(hat, p.D, layer, p.eps, sums, D > 0);
         // d: the gradient at r
         if (has_dy) take(T(), p.dy, p.dy_ld, at_dy, d);
         else EACH_PAIR d[u][e] = make_float2(0.f, 0.f);
@@ -130,11 +113,36 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 512 ? 512 / THREADS : 1) s
                 take(RT(), p.res, p.res_ld, at_res, r);
                 EACH_PAIR hat2[u][e] = padd(hat2[u][e], r[u][e]);
             }
-            const float r_pre = row_norm(hat2, p.D, layer, p.eps, buf, turn);
+            // hat2 is still v.  Its norm and the sums behind the gradient through it need one barrier together:
+            // mean(e hat) = r mean(e (v - mean)), e = d w.
+            float q, c, m = 0.f;
+            {
+                float2 e_[UPT][4];
+                EACH_PAIR e_[u][e] = d[u][e];
+                w_pre.mul(D, e_);
+                if (layer) {
+                    const float first = sums.warp(lane_total(hat2), lane_total(e_));
+                    const float mine_m = __shfl_sync(~0u, first, 0) * sums.inv_n;
+                    row_shift<WIDE>(hat2, p.D, mine_m);
+                    sums.store(sums.half, threadIdx.x & 16 ? first : mine_m);
+                    sums.store(sums.half + 2 * 64 * 4, sums.warp(lane_dot(hat2, hat2), lane_dot(e_, hat2)));
+                    sums.barrier();
+                    float mean;
+                    row_moments<true>(sums, inv_D, mean, q, c, m);
+                    sums.next();
+                    row_shift<WIDE>(hat2, p.D, mean - mine_m);
+                } else {
+                    q = lane_dot(hat2, hat2);
+                    c = lane_dot(e_, hat2);
+                    sums.sum(q, c);
+                }
+            }
+            const float r_pre = norm_factor(fmaf(q, inv_D, p.eps), D > 0);
+            EACH_PAIR hat2[u][e] = pmul(hat2[u][e], pdup(r_pre));
             EACH_PAIR s_wpre[u][e] = pfma(d[u][e], hat2[u][e], s_wpre[u][e]);
             if (BIAS) EACH_PAIR s_bpre[u][e] = padd(d[u][e], s_bpre[u][e]);
             w_pre.mul(D, d);
-            norm_back(d, hat2, r_pre, p.D, layer, buf, turn);
+            norm_back<WIDE>(d, hat2, r_pre, c * r_pre * inv_D, m * inv_D, p.D, layer);
         }
         if (residual) {
             if (has_dro) {
@@ -169,7 +177,14 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 512 ? 512 / THREADS : 1) s
         scale.mul(D, d);
         if (post) {
             w_post.mul(D, d);
-            norm_back(d, hat, r_post, p.D, layer, buf, turn);
+            float c = lane_dot(d, hat), m = 0.f;
+            if (layer) {
+                m = lane_total(d);
+                sums.sum(c, m);
+            } else {
+                c = sums.sum(c);
+            }
+            norm_back<WIDE>(d, hat, r_post, c * inv_D, m * inv_D, p.D, layer);
         }
         if (gate && !after) {
             float2 n[UPT][4];
@@ -179,7 +194,7 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 512 ? 512 / THREADS : 1) s
         row_store<T, WIDE, UPT>(p.dx, row * p.dx_ld, D, d);
     }
     if (!p.ws) return;
-    const long long part = ((long long)blockIdx.x * blockDim.y + threadIdx.y) * SUMS * p.D;
+    const long long part = ((long long)blockIdx.x * rows_at_once + ty) * SUMS * p.D;
     row_store<float, WIDE, UPT>(p.ws, part, p.D, s_1);
     if (BIAS) row_store<float, WIDE, UPT>(p.ws, part + p.D, p.D, s_0);
     if (p.dw_pre) row_store<float, WIDE, UPT>(p.ws, part + 2 * p.D, p.D, s_wpre);
@@ -242,7 +257,7 @@ Shape shape_of(int rows, int D, unsigned flags, bool wide, int esize, int rsize,
         s.threads = s.upt == 1 ? 512 : 1024;
     }
     int fit = 65536 / ((s.threads == 1024 ? 64 : 128) * threads);
-    if (s.smem > 0 && 228 * 1024 / (s.smem + 1536) < fit) fit = 228 * 1024 / (s.smem + 1536);
+    if (s.smem > 0 && 228 * 1024 / (s.smem + 3584) < fit) fit = 228 * 1024 / (s.smem + 3584);
     const int most = (rows + (int)s.block.y - 1) / (int)s.block.y, want = (fit < 1 ? 1 : fit) * sms;
     s.blocks = most < want ? most : want;
     return s;

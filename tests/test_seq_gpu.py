@@ -441,6 +441,42 @@ def test_norm_in_place_and_zero_rows():
     assert np.array_equal(host(y)[2], be)
 
 
+@pytest.mark.parametrize("layer", [False, True])
+@pytest.mark.parametrize("rows,D", [(5, 64), (3, 200), (2, 512)])
+def test_norm_without_eps(rows, D, layer):
+    """eps 0: rows that share a thread block with places behind the last row, which must add nothing."""
+    import torch
+    b = Box(rows + D, False)
+    x, xe = b.normal(rows, D)
+    r, re_ = b.normal(rows, D)
+    w, we = b.put(b.rng.uniform(0.5, 1.5, D))
+    wp, wpe = b.put(b.rng.uniform(0.5, 1.5, D))
+    dy, dye = b.normal(rows, D)
+    ref, mag = O.norm(xe, layer, 0.0, True, True, res=re_, w_post=wpe, w_pre=we, dy=dye)
+    g = dict(dx=b.out(rows, D), dres=b.out(rows, D), dw_pre=b.out(D), dw_post=b.out(D))
+    plan = Q.SeqNormPlan(rows, D, CONV_F32, direction="bwd", kind="layer" if layer else "rms", post=True, pre=True, eps=0.0)
+    plan.backward(x, dy=dy, res=r, w_post=wp, w_pre=w, **g)
+    k = 2 * max(D ** 0.5 + 120, D / 32 + 120)
+    for n, v in g.items():
+        O.check(n, host(v), ref[n], mag[n], k + (rows if v.dim() == 1 else 0), False)
+
+
+def test_layer_norm_far_from_zero():
+    """Whole numbers around 4096, and rows whose parts lie around different ones: their sums are exact in 24
+    bits, so only the squares, the root and the last product round, about 40 times in a row in all."""
+    import torch
+    rng = np.random.default_rng(5)
+    v = rng.integers(-8, 9, (6, 1024)).astype(np.float64) + 4096
+    v[3:, 256:512] -= 64
+    v[3:, 700:] += 32
+    x = torch.from_numpy(v).float().cuda()
+    y = torch.empty_like(x)
+    Q.SeqNormPlan(6, 1024, CONV_F32, kind="layer", post=True, pre=False, residual=False, eps=0.0).forward(x, y=y)
+    m = v - v.mean(1, keepdims=True)
+    want = m / np.sqrt((m * m).mean(1, keepdims=True))
+    assert np.all(np.abs(host(y) - want) <= 64 * 2.0 ** -24 * np.maximum(np.abs(want), 1))
+
+
 # ---------------------------------------------------------------------------------- together
 def test_block_example_decodes_what_the_whole_sequence_gives():
     """examples/ssm_block.py: a prompt and steps behind it against all tokens at once.  Between the calls
