@@ -24,6 +24,7 @@ struct Raw8<__nv_bfloat16> {
     uint4 q;
     __device__ __forceinline__ void load(const __nv_bfloat16* p) { q = *reinterpret_cast<const uint4*>(p); }
     __device__ __forceinline__ void zero() { q = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void ones() { q = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u); }
     __device__ __forceinline__ void get(float2 (&v)[4]) const {
         bf2_unpack(q.x, v[0].x, v[0].y);
         bf2_unpack(q.y, v[1].x, v[1].y);
@@ -39,6 +40,7 @@ struct Raw8<float> {
         b = reinterpret_cast<const float4*>(p)[1];
     }
     __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ void ones() { a = b = make_float4(1.f, 1.f, 1.f, 1.f); }
     __device__ __forceinline__ void get(float2 (&v)[4]) const {
         v[0] = make_float2(a.x, a.y);
         v[1] = make_float2(a.z, a.w);
@@ -103,28 +105,44 @@ __device__ __forceinline__ void row_store(void* base, long long off, int D, cons
         }
     }
 }
-// A parameter of the columns, held in registers as loaded (KEEP) or loaded at each use.
-template <typename T, bool WIDE, int UPT, bool KEEP>
+// A parameter of the columns, held in registers as loaded (KEEP) or loaded at each use; ones or zeros where there
+// is none, so that its uses need no branch (a branch costs a register move for each value that it may change).
+template <typename T, bool WIDE, int UPT, bool KEEP, bool ONES>
 struct Column {
     RowIn<T, WIDE, UPT> in;
     const void* base;
+    __device__ __forceinline__ void load(RowIn<T, WIDE, UPT>& to, int D) const {
+        if (base) {
+            to.load(base, 0, D);
+        } else if constexpr (WIDE) {
+#pragma unroll
+            for (int u = 0; u < UPT; ++u) {
+                if (ONES) to.raw[u].ones();
+                else to.raw[u].zero();
+            }
+        } else {
+            EACH_PAIR to.val[u][e] = pdup(ONES ? 1.f : 0.f);
+        }
+    }
     __device__ __forceinline__ void open(const void* from, int D) {
         base = from;
-        if (KEEP && base) in.load(base, 0, D);
+        if (KEEP) load(in, D);
     }
     __device__ __forceinline__ void get(int D, float2 (&w)[UPT][4]) const {
-        if constexpr (KEEP) in.get(w);
-        else row_load<T, WIDE, UPT>(base, 0, D, w);
+        if constexpr (KEEP) {
+            in.get(w);
+        } else {
+            RowIn<T, WIDE, UPT> now;
+            load(now, D);
+            now.get(w);
+        }
     }
-    // v *= it, v += it: nothing where there is none
     __device__ __forceinline__ void mul(int D, float2 (&v)[UPT][4]) const {
-        if (!base) return;
         float2 w[UPT][4];
         get(D, w);
         EACH_PAIR v[u][e] = pmul(v[u][e], w[u][e]);
     }
     __device__ __forceinline__ void add(int D, float2 (&v)[UPT][4]) const {
-        if (!base) return;
         float2 w[UPT][4];
         get(D, w);
         EACH_PAIR v[u][e] = padd(v[u][e], w[u][e]);
@@ -190,7 +208,7 @@ __device__ __forceinline__ void row_take(uint32_t at, float2 (&v)[UPT][4]) {
 
 // Sums over the threads of a row.  A warp sums by shuffles, so that all of its lanes hold the same value and
 // store it to the warp's slot (one store, no predicate); behind a barrier each thread reads the row's slots
-// four at a time and adds them up in order.  Two halves of the buffer take turns, so one barrier a sum is
+// four at a time and adds them up, always in the same order.  Two halves of the buffer take turns, so one barrier a sum is
 // enough.  Every thread of the block takes part.  THREADS: of the block at most.
 struct NormSums {
     float v[2][4][64];       // turn, value, slot: a row has THREADS / 32 of them, or more threads in one row
@@ -246,13 +264,17 @@ struct RowSums {
         return v;
     }
     __device__ __forceinline__ float slots(int k) const {
-        float s = 0.f;
+        float2 s[SLOTS / 4];
 #pragma unroll
-        for (int w = 0; w < SLOTS; w += 4) {
-            const float4 q = four(get + (k * 64 + w) * 4);
-            s += (q.x + q.y) + (q.z + q.w);
+        for (int w = 0; w < SLOTS / 4; ++w) {
+            const float4 q = four(get + (k * 64 + 4 * w) * 4);
+            s[w] = padd(make_float2(q.x, q.y), make_float2(q.z, q.w));
         }
-        return s;
+#pragma unroll
+        for (int o = SLOTS / 8; o > 0; o /= 2)
+#pragma unroll
+            for (int w = 0; w < o; ++w) s[w] = padd(s[w], s[w + o]);
+        return s[0].x + s[0].y;
     }
     __device__ __forceinline__ float sum(float a) {
         store(put, warp(a));

@@ -58,7 +58,8 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 512 ? 512 / THREADS : 1) s
 #pragma unroll
     for (int i = 0; i < NORM_RING - 1; ++i) fetch(row + i * step, i);
     int stage = 0;
-    Column<T, WIDE, UPT, THREADS <= 512> w_post, b_post, scale, w_pre;
+    Column<T, WIDE, UPT, THREADS <= 512, true> w_post, scale, w_pre;
+    Column<T, WIDE, UPT, THREADS <= 512, false> b_post;
     w_post.open(p.w_post, p.D);
     b_post.open(BIAS ? p.b_post : nullptr, p.D);
     scale.open(p.scale, p.D);
