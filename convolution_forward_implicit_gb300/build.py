@@ -18,7 +18,7 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libconvfwd.so")
 SOURCES = ["capi.cu", "tc_conv.cu", "tc_pair.cu", "tc_slab.cu", "tc_slab_pair.cu", "simt.cu", "wgrad.cu",
-           "tc_wgrad.cu", "seq_capi.cu", "seq_conv.cu", "seq_scan.cu", "seq_scan_bwd.cu", "seq_norm.cu",
+           "tc_wgrad.cu", "seq_capi.cu", "seq_conv.cu", "seq_scan.cu", "seq_scan_step.cu", "seq_scan_bwd.cu", "seq_norm.cu",
            "seq_norm_bwd.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -123,42 +123,65 @@ __device__ __forceinline__ void copy16_async(void* to, const void* from, bool on
     const uint32_t d = (uint32_t)__cvta_generic_to_shared(to);
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(from), "r"(on ? 16 : 0) : "memory");
 }
-__device__ __forceinline__ void copy4_async(void* to, const void* from, bool on) {
-    const uint32_t d = (uint32_t)__cvta_generic_to_shared(to);
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(d), "l"(from), "r"(on ? 4 : 0) : "memory");
-}
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // Waits until at most N of this thread's latest groups are still on their way.
 template <int N>
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// rows_to_shared for rows that are not whole 16-byte groups.  Out of line: it is rare, and its registers
-// would count in the kernels' loops.
+// rows_to_shared for rows that are not whole 16-byte groups.  A thread stays in its columns and steps from row to
+// row, so that a copy costs little more than one addition.
 template <typename T, int ROWS, int W, int THREADS>
 __device__ __noinline__ void rows_to_shared_odd(T (*to)[W], const T* from, long long ld, int n, int width, int grain) {
     if (grain == 4) {
-        constexpr int E = 4 / sizeof(T), CPR = W / E;
-#pragma unroll 4
-        for (int i = threadIdx.x; i < ROWS * CPR; i += THREADS) {
-            const int r = i / CPR, c = i % CPR * E;
-            const bool on = r < n && c < width;
-            copy4_async(&to[r][c], on ? from + r * ld + c : from, on);
+        constexpr int E = 4 / sizeof(T), CPR = W / E, CPT = CPR > THREADS ? CPR / THREADS : 1;
+        constexpr int STEP = CPR > THREADS ? 1 : THREADS / CPR, J = (ROWS + STEP - 1) / STEP;
+        static_assert(CPR % THREADS == 0 || THREADS % CPR == 0, "whole columns to a thread");
+        const int r0 = CPR >= THREADS ? 0 : threadIdx.x / CPR;
+#pragma unroll
+        for (int u = 0; u < CPT; ++u) {
+            const int c = (threadIdx.x % CPR + u * THREADS) * E;
+            const bool on = c < width;
+            const T* at = on ? from + r0 * ld + c : from;
+            const long long next = on ? STEP * ld : 0;
+            uint32_t d = (uint32_t)__cvta_generic_to_shared(&to[r0][c]);
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                if (ROWS % STEP == 0 || r0 + j * STEP < ROWS) {
+                    const bool there = on && r0 + j * STEP < n;
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(d + j * STEP * W * (int)sizeof(T)), "l"(there ? at : from),
+                                 "r"(there ? 4 : 0) : "memory");
+                }
+                at += next;
+            }
         }
     } else {
-#pragma unroll 8
-        for (int i = threadIdx.x; i < ROWS * W; i += THREADS) {
-            const int r = i / W, c = i % W;
-            to[r][c] = r < n && c < width ? from[r * ld + c] : T(0.f);
+        constexpr int CPT = W > THREADS ? W / THREADS : 1, STEP = W > THREADS ? 1 : THREADS / W, J = (ROWS + STEP - 1) / STEP;
+        static_assert(W % THREADS == 0 || THREADS % W == 0, "whole columns to a thread");
+        const int r0 = W >= THREADS ? 0 : threadIdx.x / W;
+#pragma unroll
+        for (int u = 0; u < CPT; ++u) {
+            const int c = threadIdx.x % W + u * THREADS;
+            const bool on = c < width;
+            const T* at = on ? from + r0 * ld + c : from;
+            T v[J];
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                v[j] = on && r0 + j * STEP < n ? at[0] : T(0.f);
+                at += STEP * ld;
+            }
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+                if (ROWS % STEP == 0 || r0 + j * STEP < ROWS) to[r0 + j * STEP][c] = v[j];
         }
     }
 }
 // n rows of W elements (a multiple of 16 bytes), ROWS at most, to shared memory by the block's THREADS
 // threads, as part of the copy group at hand.  Columns at and behind `width` and rows at and behind n
-// become zero.  grain: 16 or 4 when rows are whole and aligned groups of as many bytes; else 0: plain
-// loads (2-byte elements at odd places), which are done on return.
-template <typename T, int ROWS, int W, int THREADS>
+// become zero.  WIDE: rows are whole and aligned groups of 16 bytes.  Otherwise grain: 4 when they are such groups
+// of 4 bytes; else 0: plain loads (2-byte elements at odd places), which are done on return.
+template <typename T, int ROWS, int W, int THREADS, bool WIDE>
 __device__ __forceinline__ void rows_to_shared(T (*to)[W], const T* from, long long ld, int n, int width, int grain) {
-    if (grain == 16) {
+    if constexpr (WIDE) {
         constexpr int E = 16 / sizeof(T), CPR = W / E, ALL = ROWS * CPR;
         static_assert(W % E == 0, "rows of whole 16-byte groups");
 #pragma unroll

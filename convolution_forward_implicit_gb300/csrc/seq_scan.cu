@@ -1,8 +1,7 @@
-// Selective state space scan, forward and one-token step: see seq.h for the formulas.
+// Selective state space scan, forward: see seq.h for the formulas.
 //
 // Per token, channel and state: one exponential (exp(delta A) as 2^(delta A log2 e)) and four
-// multiply-adds, so the forward pass is bound by the special-function and FMA pipes, and the step by
-// the bytes of the states.  A thread holds NPT states of one channel in registers and walks the
+// multiply-adds, so the pass is bound by the special-function and FMA pipes.  A thread holds NPT states of one channel in registers and walks the
 // tokens of a piece; LN neighbouring lanes share a channel when it has more states.
 #include "seq_scan.cuh"
 
@@ -10,7 +9,6 @@ namespace convfwd {
 namespace {
 
 constexpr int THREADS = 64;         // of the scan; a thread has two channels
-constexpr int STEP_THREADS = 128;   // of the one-token step
 
 // Rows of B or C of a tile, on their way through registers to shared memory as fp32.
 template <typename T, int NP>
@@ -38,7 +36,7 @@ struct TileRows {
 // registers into two buffers of fp32.  One barrier a tile.  A thread has two neighbouring channels: what
 // a token costs besides its states (conversions, softplus, silu, addresses, the rows of B and C) is shared
 // by the two.  SUMMARY: only the state behind the piece and the sum of delta.
-template <typename T, int NPT, int LN, bool SUMMARY, bool GATED>
+template <typename T, int NPT, int LN, bool SUMMARY, bool GATED, bool WIDE>
 __global__ void __launch_bounds__(THREADS, 6) seq_scan_kernel(const __grid_constant__ SeqScanParams p) {
     constexpr int CB = 2 * THREADS / LN, NP = NPT * LN, STAGES = sizeof(T) == 2 ? 4 : 3;
     __shared__ __align__(16) float sB[2][SCAN_TILE][NP], sC[2][SUMMARY ? 1 : SCAN_TILE][NP];
@@ -65,7 +63,7 @@ __global__ void __launch_bounds__(THREADS, 6) seq_scan_kernel(const __grid_const
         if (tb < t1) {
             const int n = min(SCAN_TILE, t1 - tb);
             auto rows = [&](T (*to)[CB], const void* from, long long ld) {
-                rows_to_shared<T, SCAN_TILE, CB, THREADS>(to, static_cast<const T*>(from) + (long long)tb * ld + d0, ld, n, width, p.wide);
+                rows_to_shared<T, SCAN_TILE, CB, THREADS, WIDE>(to, static_cast<const T*>(from) + (long long)tb * ld + d0, ld, n, width, p.wide);
             };
             rows(sx[stage], p.x, p.x_ld);
             rows(sdt[stage], p.dt, p.dt_ld);
@@ -174,8 +172,8 @@ __global__ void __launch_bounds__(THREADS, 6) seq_scan_kernel(const __grid_const
                 y = mul2(y, make_float2(silu(z.x), silu(z.y)));
             }
             if (ln == 0) {
-                seq_st2(yp, y, on[1] && p.wide == 16, on[0]);
-                if (on[1] && p.wide != 16) seq_st(yp + 1, y.y);
+                seq_st2(yp, y, on[1] && WIDE, on[0]);
+                if (on[1] && !WIDE) seq_st(yp + 1, y.y);
             }
             yp += p.y_ld;
         }
@@ -312,114 +310,8 @@ __global__ void __launch_bounds__(128) seq_scan_empty_kernel(SeqAxis ax, SeqSlot
     }
 }
 
-// One token per sequence: bound by the bytes of the states.  A lane holds 4 states of a channel (16 bytes of
-// its state row), LN lanes share the channel; a thread keeps its row of A and takes ROWS sequences at a
-// time, all of their loads on their way before the first is used.  VEC: states, A, B and C in whole aligned
-// groups of 4.
-template <typename T, int LN, int ROWS, bool VEC>
-__global__ void __launch_bounds__(STEP_THREADS, ROWS > 1 && VEC ? 7 : 1) seq_scan_step_kernel(const __grid_constant__ SeqScanParams p) {
-    const int d0 = (int)((blockIdx.x * (long long)STEP_THREADS + threadIdx.x) / LN);
-    const bool on = d0 < p.D;
-    const int d = on ? d0 : p.D - 1;
-    const int n0 = threadIdx.x % LN * 4, bc = d / (p.D / p.G) * p.N + n0;
-    const bool any = n0 < p.N;                       // (lanes behind the states only take part in the sum)
-    const float2 zero = make_float2(0.f, 0.f);
-    auto four = [&](const float* from, float2 (&v)[2]) {
-        v[0] = v[1] = zero;
-        if (VEC) {
-            if (any) ld2(from, v[0], v[1]);
-        } else {
-            if (n0 < p.N) v[0].x = from[0];
-            if (n0 + 1 < p.N) v[0].y = from[1];
-            if (n0 + 2 < p.N) v[1].x = from[2];
-            if (n0 + 3 < p.N) v[1].y = from[3];
-        }
-    };
-    auto four_t = [&](const T* from, float2 (&v)[2]) {
-        v[0] = v[1] = zero;
-        if (VEC) {
-            if (any) {
-                v[0] = seq_ld2(from);
-                v[1] = seq_ld2(from + 2);
-            }
-        } else {
-            if (n0 < p.N) v[0].x = seq_ld(from);
-            if (n0 + 1 < p.N) v[0].y = seq_ld(from + 1);
-            if (n0 + 2 < p.N) v[1].x = seq_ld(from + 2);
-            if (n0 + 3 < p.N) v[1].y = seq_ld(from + 3);
-        }
-    };
-    float2 A2[2];
-    const int at = d * p.N + n0, DN = p.D * p.N;     // (D N < 2^31: see the plan)
-    four(p.A + at, A2);
-    A2[0] = mul2(A2[0], dup2(LOG2E));
-    A2[1] = mul2(A2[1], dup2(LOG2E));
-    const float bias = p.dt_bias ? p.dt_bias[d] : 0.f, Dd = p.Dskip ? p.Dskip[d] : 0.f;
-    // row s of a tensor (rows are less than 2^31 elements apart)
-    auto row = [](const void* base, int s, long long ld) { return static_cast<const T*>(base) + (long long)s * (int)ld; };
-    for (int s0 = blockIdx.y * ROWS; s0 < p.ax.S; s0 += gridDim.y * ROWS) {
-        float2 h[ROWS][2], B[ROWS][2], C[ROWS][2];
-        float x[ROWS], raw[ROWS], z[ROWS];
-        int slot[ROWS];
-#pragma unroll
-        for (int r = 0; r < ROWS; ++r) slot[r] = s0 + r < p.ax.S ? (int)seq_slot(p.sl, s0 + r) : -1;
-#pragma unroll
-        for (int r = 0; r < ROWS; ++r) {
-            const int s = min(s0 + r, p.ax.S - 1);
-            h[r][0] = h[r][1] = zero;
-            if (p.h_in && slot[r] >= 0) four(p.h_in + (long long)slot[r] * DN + at, h[r]);
-            x[r] = seq_ld(row(p.x, s, p.x_ld) + d);
-            raw[r] = seq_ld(row(p.dt, s, p.dt_ld) + d) + bias;
-            z[r] = p.z ? seq_ld(row(p.z, s, p.z_ld) + d) : 0.f;
-            four_t(row(p.B, s, p.B_ld) + bc, B[r]);
-            four_t(row(p.C, s, p.C_ld) + bc, C[r]);
-        }
-        float delta[ROWS];
-#pragma unroll
-        for (int r = 0; r < ROWS; r += 2) {
-            if (ROWS == 1) {
-                delta[0] = p.softplus ? softplus(raw[0]) : raw[0];
-            } else {
-                float2 v = make_float2(raw[r], raw[r + 1 < ROWS ? r + 1 : r]);
-                if (p.softplus) v = softplus2(v, nullptr);
-                delta[r] = v.x;
-                if (r + 1 < ROWS) delta[r + 1] = v.y;
-            }
-        }
-#pragma unroll
-        for (int r = 0; r < ROWS; ++r) {
-            const float2 dl = dup2(delta[r]), u = dup2(delta[r] * x[r]);
-            float2 acc = zero;
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                h[r][k] = fma2(decay2(dl, A2[k]), h[r][k], mul2(u, B[r][k]));
-                acc = fma2(C[r][k], h[r][k], acc);
-            }
-            if (on && p.h_out && slot[r] >= 0) {
-                float* to = p.h_out + (long long)slot[r] * DN + at;
-                if (VEC) {
-                    if (any) st2(to, h[r][0], h[r][1]);
-                } else {
-                    if (n0 < p.N) to[0] = h[r][0].x;
-                    if (n0 + 1 < p.N) to[1] = h[r][0].y;
-                    if (n0 + 2 < p.N) to[2] = h[r][1].x;
-                    if (n0 + 3 < p.N) to[3] = h[r][1].y;
-                }
-            }
-            float a = acc.x + acc.y;
-#pragma unroll
-            for (int o = LN / 2; o > 0; o >>= 1) a += __shfl_xor_sync(~0u, a, o);
-            if (n0 == 0 && on && s0 + r < p.ax.S) {
-                float v = fmaf(Dd, x[r], a);
-                if (p.z) v *= silu(z[r]);
-                seq_st(const_cast<T*>(row(p.y, s0 + r, p.y_ld)) + d, v);
-            }
-        }
-    }
-}
-
-template <typename T, int NPT, int LN>
-cudaError_t launch_fwd(const SeqScanParams& p, cudaStream_t stream) {
+template <typename T, int NPT, int LN, bool WIDE>
+cudaError_t launch_fwd_of(const SeqScanParams& p, cudaStream_t stream) {
     constexpr int CB = 2 * THREADS / LN;
     const int per = p.D / p.G;
     const dim3 grid((unsigned)p.pc.count, (unsigned)(p.G * ((per + CB - 1) / CB)));
@@ -427,14 +319,21 @@ cudaError_t launch_fwd(const SeqScanParams& p, cudaStream_t stream) {
     if (p.ax.T > 0) {
         const bool cut = p.pc.pps != 1 && p.pc.count > 1;
         if (cut)
-            e = launch_kernel(seq_scan_kernel<T, NPT, LN, true, false>, grid, dim3(THREADS), 0, stream, false, 1, p);
+            e = launch_kernel(seq_scan_kernel<T, NPT, LN, true, false, WIDE>, grid, dim3(THREADS), 0, stream, false, 1, p);
         if (e == cudaSuccess && cut) e = launch_seq_scan_join(p, false, stream);
         if (e == cudaSuccess)
-            e = p.z ? launch_kernel(seq_scan_kernel<T, NPT, LN, false, true>, grid, dim3(THREADS), 0, stream, cut, 1, p)
-                    : launch_kernel(seq_scan_kernel<T, NPT, LN, false, false>, grid, dim3(THREADS), 0, stream, cut, 1, p);
+            e = p.z ? launch_kernel(seq_scan_kernel<T, NPT, LN, false, true, WIDE>, grid, dim3(THREADS), 0, stream, cut, 1, p)
+                    : launch_kernel(seq_scan_kernel<T, NPT, LN, false, false, WIDE>, grid, dim3(THREADS), 0, stream, cut, 1, p);
     }
     if (e == cudaSuccess && p.h_out && p.h_out != p.h_in && p.ax.L == 0) e = launch_seq_scan_empty(p, p.h_in, p.h_out, stream);
     return e;
+}
+
+// (Rows that are not whole 16-byte groups have kernels of their own: their copies beside the others in one kernel, even
+// out of line, cost the others registers.)
+template <typename T, int NPT, int LN>
+cudaError_t launch_fwd(const SeqScanParams& p, cudaStream_t stream) {
+    return p.wide == 16 ? launch_fwd_of<T, NPT, LN, true>(p, stream) : launch_fwd_of<T, NPT, LN, false>(p, stream);
 }
 
 template <typename T>
@@ -445,31 +344,6 @@ cudaError_t launch_t(const SeqScanParams& p, cudaStream_t stream) {
     if (p.N <= 32) return launch_fwd<T, 16, 2>(p, stream);
     if (p.N <= 64) return launch_fwd<T, 16, 4>(p, stream);
     return launch_fwd<T, 16, 8>(p, stream);
-}
-
-template <typename T, int LN>
-cudaError_t launch_step(const SeqScanParams& p, cudaStream_t stream) {
-    const long long blocks = ((long long)p.D * LN + STEP_THREADS - 1) / STEP_THREADS;
-    // 4 sequences a thread once that still leaves the GPU several blocks an SM (256 x 4096 x 16: 54 us with one)
-    constexpr int ROWS = 4;
-    if (blocks * p.ax.S < 16 * 152 * ROWS) {
-        const dim3 grid((unsigned)blocks, (unsigned)(p.ax.S < 32768 ? p.ax.S : 32768));
-        return p.quads ? launch_kernel(seq_scan_step_kernel<T, LN, 1, true>, grid, dim3(STEP_THREADS), 0, stream, false, 1, p)
-                       : launch_kernel(seq_scan_step_kernel<T, LN, 1, false>, grid, dim3(STEP_THREADS), 0, stream, false, 1, p);
-    }
-    const int rows = (p.ax.S + ROWS - 1) / ROWS;
-    const dim3 grid((unsigned)blocks, (unsigned)(rows < 32768 ? rows : 32768));
-    return p.quads ? launch_kernel(seq_scan_step_kernel<T, LN, ROWS, true>, grid, dim3(STEP_THREADS), 0, stream, false, 1, p)
-                   : launch_kernel(seq_scan_step_kernel<T, LN, ROWS, false>, grid, dim3(STEP_THREADS), 0, stream, false, 1, p);
-}
-template <typename T>
-cudaError_t launch_step_t(const SeqScanParams& p, cudaStream_t stream) {
-    if (p.N <= 4) return launch_step<T, 1>(p, stream);
-    if (p.N <= 8) return launch_step<T, 2>(p, stream);
-    if (p.N <= 16) return launch_step<T, 4>(p, stream);
-    if (p.N <= 32) return launch_step<T, 8>(p, stream);
-    if (p.N <= 64) return launch_step<T, 16>(p, stream);
-    return launch_step<T, 32>(p, stream);
 }
 
 }  // namespace
@@ -489,9 +363,6 @@ cudaError_t launch_seq_scan_empty(const SeqScanParams& p, const float* from, flo
 }
 cudaError_t launch_seq_scan_fwd(const SeqScanParams& p, bool bf16, cudaStream_t stream) {
     return bf16 ? launch_t<__nv_bfloat16>(p, stream) : launch_t<float>(p, stream);
-}
-cudaError_t launch_seq_scan_step(const SeqScanParams& p, bool bf16, cudaStream_t stream) {
-    return bf16 ? launch_step_t<__nv_bfloat16>(p, stream) : launch_step_t<float>(p, stream);
 }
 
 }  // namespace convfwd

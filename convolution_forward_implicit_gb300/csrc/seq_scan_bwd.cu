@@ -83,7 +83,7 @@ struct BwdSmem {
     T x[SCAN_TILE][S::CB], dt[SCAN_TILE][S::CB], dy[SCAN_TILE][S::CB], z[SCAN_TILE][S::CB];
 };
 
-template <typename T, int LN, bool GATED>
+template <typename T, int LN, bool GATED, bool WIDE>
 __global__ void __launch_bounds__(THREADS, 3) seq_scan_bwd_kernel(const __grid_constant__ SeqScanParams p) {
     using S = BwdShape<LN>;
     extern __shared__ __align__(16) unsigned char smem_raw[];
@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(THREADS, 3) seq_scan_bwd_kernel(const __grid_c
     auto fetch = [&](int tb) {
         const int n = min(SCAN_TILE, t1 - tb);
         auto rows = [&](T (*to)[S::CB], const void* from, long long ld) {
-            rows_to_shared<T, SCAN_TILE, S::CB, THREADS>(to, static_cast<const T*>(from) + (long long)tb * ld + d0, ld, n, width, p.wide);
+            rows_to_shared<T, SCAN_TILE, S::CB, THREADS, WIDE>(to, static_cast<const T*>(from) + (long long)tb * ld + d0, ld, n, width, p.wide);
         };
         rows(sm.x, p.x, p.x_ld);
         rows(sm.dt, p.dt, p.dt_ld);
@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(THREADS, 3) seq_scan_bwd_kernel(const __grid_c
             for (int j = 0; j < S::J; ++j) {
                 const int t = tok0 + j * S::STEP;
                 if (t < n) {
-                    const bool both = on1 && p.wide == 16, one = on0;
+                    const bool both = on1 && WIDE, one = on0;
                     const float2 gB = *reinterpret_cast<const float2*>(&sm.tok[t].gB[pc]);
                     const float2 dyc = *reinterpret_cast<const float2*>(&sm.tok[t].dyc[pc]);
                     const float2 delta = *reinterpret_cast<const float2*>(&sm.tok[t].delta[pc]);
@@ -432,7 +432,7 @@ __global__ void __launch_bounds__(THREADS, 3) seq_scan_bwd_kernel(const __grid_c
                         dz = mul2(wz[j], fma2(Dd, xv[j], *reinterpret_cast<const float2*>(&sm.tok[t].u[pc])));
                         seq_st2(qz, dz, both, one);
                     }
-                    if (on1 && p.wide != 16) {
+                    if (on1 && !WIDE) {
                         seq_st(qx + 1, dx.y);
                         seq_st(qt + 1, dd.y);
                         if (GATED) seq_st(qz + 1, dz.y);
@@ -492,7 +492,7 @@ __global__ void __launch_bounds__(THREADS, 3) seq_scan_bwd_kernel(const __grid_c
 // first sequence alone, if another begins in it), and the sum of delta over it.  Threads hold channels and
 // states as in the forward kernel: two channels, NPT states of each, LN lanes to a channel.
 constexpr int BACK_THREADS = 64;
-template <typename T, int NPT, int LN, bool GATED>
+template <typename T, int NPT, int LN, bool GATED, bool WIDE>
 __global__ void __launch_bounds__(BACK_THREADS) seq_scan_back_kernel(const __grid_constant__ SeqScanParams p) {
     constexpr int CB = 2 * BACK_THREADS / LN, NP = NPT * LN, STAGES = sizeof(T) == 2 ? 4 : 3;
     constexpr int JR = (SCAN_TILE * NP + BACK_THREADS - 1) / BACK_THREADS;
@@ -519,7 +519,7 @@ __global__ void __launch_bounds__(BACK_THREADS) seq_scan_back_kernel(const __gri
         if (tile >= 0) {
             const int tb = t0 + tile * SCAN_TILE, n = min(SCAN_TILE, t1 - tb), stage = tile % STAGES;
             auto rows = [&](T (*to)[CB], const void* from, long long ld) {
-                rows_to_shared<T, SCAN_TILE, CB, BACK_THREADS>(to, static_cast<const T*>(from) + (long long)tb * ld + d0, ld, n, width, p.wide);
+                rows_to_shared<T, SCAN_TILE, CB, BACK_THREADS, WIDE>(to, static_cast<const T*>(from) + (long long)tb * ld + d0, ld, n, width, p.wide);
             };
             rows(sdt[stage], p.dt, p.dt_ld);
             rows(sdy[stage], p.dy, p.dy_ld);
@@ -654,13 +654,10 @@ __global__ void __launch_bounds__(128) seq_scan_par_kernel(const __grid_constant
     else if (p.ddt_bias) p.ddt_bias[d] = v;
 }
 
-template <typename T, int LN, bool GATED>
-cudaError_t launch_main(const SeqScanParams& p, cudaStream_t stream) {
-    const cudaError_t e = cudaFuncSetAttribute(seq_scan_bwd_kernel<T, LN, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)sizeof(BwdSmem<T, LN>));
-    if (e != cudaSuccess) return e;
-    return launch_kernel(seq_scan_bwd_kernel<T, LN, GATED>, dim3((unsigned)p.pc.count, (unsigned)p.cblocks), dim3(THREADS),
-                         sizeof(BwdSmem<T, LN>), stream, p.pc.pps != 1 && p.pc.count > 1, 1, p);
+// The kernel for the call's rows: gated or not, in whole 16-byte groups or not.
+inline auto of_rows(const SeqScanParams& p, void (*gated_wide)(const SeqScanParams), void (*wide)(const SeqScanParams),
+             void (*gated)(const SeqScanParams), void (*other)(const SeqScanParams)) {
+    return p.wide == 16 ? (p.z ? gated_wide : wide) : (p.z ? gated : other);
 }
 
 // LN: lanes of the main kernel; NPT, LB: states and lanes of the pieces' kernel
@@ -672,11 +669,17 @@ cudaError_t launch_ln(const SeqScanParams& p, cudaStream_t stream) {
             constexpr int CB = 2 * BACK_THREADS / LB;
             const int per = p.D / p.G;
             const dim3 grid((unsigned)p.pc.count, (unsigned)(p.G * ((per + CB - 1) / CB)));
-            e = p.z ? launch_kernel(seq_scan_back_kernel<T, NPT, LB, true>, grid, dim3(BACK_THREADS), 0, stream, false, 1, p)
-                    : launch_kernel(seq_scan_back_kernel<T, NPT, LB, false>, grid, dim3(BACK_THREADS), 0, stream, false, 1, p);
+            e = launch_kernel(of_rows(p, seq_scan_back_kernel<T, NPT, LB, true, true>, seq_scan_back_kernel<T, NPT, LB, false, true>,
+                                         seq_scan_back_kernel<T, NPT, LB, true, false>, seq_scan_back_kernel<T, NPT, LB, false, false>),
+                              grid, dim3(BACK_THREADS), 0, stream, false, 1, p);
         }
         if (e == cudaSuccess && p.pc.pps != 1 && p.pc.count > 1) e = launch_seq_scan_join(p, true, stream);
-        if (e == cudaSuccess) e = p.z ? launch_main<T, LN, true>(p, stream) : launch_main<T, LN, false>(p, stream);
+        const auto main = of_rows(p, seq_scan_bwd_kernel<T, LN, true, true>, seq_scan_bwd_kernel<T, LN, false, true>,
+                                     seq_scan_bwd_kernel<T, LN, true, false>, seq_scan_bwd_kernel<T, LN, false, false>);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(main, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(BwdSmem<T, LN>));
+        if (e == cudaSuccess)
+            e = launch_kernel(main, dim3((unsigned)p.pc.count, (unsigned)p.cblocks), dim3(THREADS), sizeof(BwdSmem<T, LN>), stream,
+                              p.pc.pps != 1 && p.pc.count > 1, 1, p);
         const long long all = ((long long)p.ax.T * p.G * 8 * LN + 127) / 128;
         if (e == cudaSuccess)
             e = launch_kernel(seq_scan_bc_kernel<T, 4 * LN>, dim3((unsigned)(all < 65536 ? all : 65536)), dim3(128), 0, stream, true, 1, p);
