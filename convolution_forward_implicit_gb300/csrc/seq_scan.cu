@@ -223,22 +223,23 @@ __global__ void __launch_bounds__(THREADS, 6) seq_scan_kernel(const __grid_const
 // Joins the pieces of a sequence (of a ragged axis): with e_r what piece r adds to the state behind it and
 // sum_r its sum of delta, the state before piece r + 1 is c_{r+1} = e_r + exp(sum_r A) c_r, or e_r alone where
 // a sequence begins in piece r (backward: the same from the last piece down).  A thread replaces e_r by c_r for
-// 4 states of a channel in a quarter of the pieces.  It first joins its own quarter from a zero state, keeping
-// the sum of delta over it; the four quarters' results pass through shared memory; then it walks the quarter
-// again from the state before it.  (One thread for all 52 pieces of a 2048 x 2048 x 16 prompt: 8.3 us, most of
-// it waiting for one batch of loads after another.)
-// Up to 16 pieces one part is enough.
-constexpr int JOIN_THREADS = 128, JOIN_MOST = 16;
+// 4 states of a channel in one part of the pieces, 16 at most, whose loads are all on their way at once.  It first
+// joins its own part from a zero state, keeping the sum of delta over it; the parts' results pass through shared
+// memory; then it walks its part again from the state before it.  (2048 x 2048 x 16 in 52 pieces: one part, in
+// batches of loads, 8.3 us; 4 parts 4.)  Up to 16 pieces one part is enough, and faster: 4 us against 15 with 4 parts
+// for 4 x 2048 x 4096 x 16 in 7 pieces a sequence.
+constexpr int JOIN_MOST = 16;
+__host__ __device__ constexpr int join_threads(int parts) { return parts == 8 ? 256 : 128; }       // several parts: a warp has one of them
 template <bool REVERSE, int JOIN_PARTS>
-__global__ void __launch_bounds__(JOIN_THREADS) seq_scan_join_kernel(const __grid_constant__ SeqScanParams p) {
-    constexpr int JOIN_LANES = JOIN_THREADS / JOIN_PARTS;
+__global__ void __launch_bounds__(join_threads(JOIN_PARTS)) seq_scan_join_kernel(const __grid_constant__ SeqScanParams p) {
+    constexpr int JOIN_LANES = join_threads(JOIN_PARTS) / JOIN_PARTS;
     __shared__ float4 sh_e[JOIN_PARTS][JOIN_LANES];
     __shared__ float sh_sum[JOIN_PARTS][JOIN_LANES];
     __shared__ bool sh_cut[JOIN_PARTS];
     const int pieces = p.pc.pps > 0 ? p.pc.pps : p.pc.count, first = blockIdx.y * pieces;
     const int lane = threadIdx.x % JOIN_LANES, part = threadIdx.x / JOIN_LANES;
     const int len = (pieces + JOIN_PARTS - 1) / JOIN_PARTS, r0 = part * len, r1 = min(r0 + len, pieces);
-    // which of the quarter's pieces cut the chain, in the order of the walk: lane l looks at the l-th
+    // which of the part's pieces cut the chain, in the order of the walk: lane l looks at the l-th
     bool stop = false;
     const int look = r0 + (threadIdx.x & 31);
     if (look < r1) {
@@ -350,11 +351,14 @@ cudaError_t launch_t(const SeqScanParams& p, cudaStream_t stream) {
 
 cudaError_t launch_seq_scan_join(const SeqScanParams& p, bool reverse, cudaStream_t stream) {
     const long long all = (long long)((p.N + 3) / 4) * p.D;
-    const int pieces = p.pc.pps > 0 ? p.pc.pps : p.pc.count, parts = pieces <= JOIN_MOST ? 1 : 4, lanes = JOIN_THREADS / parts;
+    const int pieces = p.pc.pps > 0 ? p.pc.pps : p.pc.count;
+    const int parts = pieces <= JOIN_MOST ? 1 : pieces <= 4 * JOIN_MOST ? 4 : 8, lanes = join_threads(parts) / parts;
+    if (pieces > 8 * JOIN_MOST) return cudaErrorInvalidValue;
     const dim3 grid((unsigned)((all + lanes - 1) / lanes), (unsigned)(p.pc.pps > 0 ? p.ax.S : 1));
-    auto kernel = parts == 1 ? (reverse ? seq_scan_join_kernel<true, 1> : seq_scan_join_kernel<false, 1>)
-                             : (reverse ? seq_scan_join_kernel<true, 4> : seq_scan_join_kernel<false, 4>);
-    return launch_kernel(kernel, grid, dim3(JOIN_THREADS), 0, stream, true, 1, p);
+    auto kernel = parts == 1   ? (reverse ? seq_scan_join_kernel<true, 1> : seq_scan_join_kernel<false, 1>)
+                  : parts == 4 ? (reverse ? seq_scan_join_kernel<true, 4> : seq_scan_join_kernel<false, 4>)
+                               : (reverse ? seq_scan_join_kernel<true, 8> : seq_scan_join_kernel<false, 8>);
+    return launch_kernel(kernel, grid, dim3(join_threads(parts)), 0, stream, true, 1, p);
 }
 cudaError_t launch_seq_scan_empty(const SeqScanParams& p, const float* from, float* to, cudaStream_t stream) {
     const long long DN = (long long)p.D * p.N, blocks = DN / 1024 + 1;

@@ -325,6 +325,37 @@ def test_scan_step_with_slots():
     check_states(c, host(h), ref["h"], mag["h"], 120, "h")
 
 
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("lens,ragged", [([4100], False), ([2300, 2300], False), ([1, 900, 0, 2100, 33, 777, 8, 450], True),
+                                         ([41 + i % 7 for i in range(100)], True)])
+@pytest.mark.parametrize("spec", [(40, 16, 1, 0, 1, 1, 1, 1), (17, 5, 1, 1, 1, 1, 1, 1)])
+def test_scan_in_many_pieces(bf16, lens, ragged, spec):
+    """Few channels and a long axis: more pieces than one or four parts of the joining kernel take."""
+    D, N, G = spec[:3]
+    for direction in ("fwd", "bwd"):
+        text = Q.SeqScanPlan(len(lens), sum(lens), D, N, CONV_BF16 if bf16 else CONV_F32, direction=direction, ragged=ragged).describe()
+        assert 64 < int(text.split("pieces=")[1].split()[0])
+    test_scan(bf16, lens, ragged, spec)
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("S,D,N,G,pad", [(1300, 256, 16, 1, 0), (1301, 256, 16, 2, 8), (1301, 255, 16, 1, 0), (4901, 36, 24, 3, 0),
+                                         (4900, 64, 7, 1, 0), (611, 24, 128, 1, 8)])
+def test_scan_step_of_many_sequences(bf16, S, D, N, G, pad):
+    """Several sequences, and where rows allow it two channels, to a thread; the last thread's may be fewer."""
+    import torch
+    c = scan_case(S + N, bf16, [1] * S, D, N, G, pad=pad)
+    dev, b = c["dev"], c["box"]
+    ref, mag = O.scan(**c["ex"], G=G, lens=[1] * S, h0=c["he"])
+    h, y = b.out(S + 1, D, N, dtype=torch.float32), b.out(S, D, pad=pad)
+    Q.SeqScanPlan(S, S, D, N, CONV_BF16 if bf16 else CONV_F32, direction="step", G=G).step(
+        dev["x"], dev["dt"], dev["A"], dev["B"], dev["C"], c["h"], h, y, D=dev["D"], z=dev["z"], dt_bias=dev["dt_bias"],
+        slots=c["slots"])
+    O.check("y", host(y), ref["y"], mag["y"], N + 120, bf16)
+    check_states(c, host(h), ref["h"], mag["h"], 120, "h")
+    b.check_guards()
+
+
 def test_scan_is_the_same_twice_and_on_another_stream():
     import torch
     lens = [700, 0, 1, 300]
