@@ -195,7 +195,7 @@ conv_status seq_conv_plan_create(seq_plan_t* out, int64_t S, int64_t T, int64_t 
     seq_plan* p = new_plan(Op::Conv, S, T, D, dtype, direction, flags);
     if (!p) return CONV_ERR_INVALID_ARG;
     p->W = (int)W;
-    p->run = seq_conv_run(T, p->D, p->sms);
+    p->run = seq_conv_run(T, p->D, p->W, dtype == CONV_BF16, direction == SEQ_BWD, p->sms);
     if (direction == SEQ_BWD) {
         p->blocks = seq_conv_bwd_token_blocks(T, p->run);
         p->ws_bytes = align256((size_t)(p->blocks > 0 ? p->blocks : 1) * (W + 1) * D * sizeof(float));

@@ -69,13 +69,35 @@ __device__ __forceinline__ long long state_slot(const SeqConvParams& p, int s) {
 
 template <typename T, int V, int W>
 __device__ __forceinline__ void load_params(const SeqConvParams& p, int c, float2 (&w)[W][V == 1 ? 1 : V / 2], float2 (&b)[V == 1 ? 1 : V / 2]) {
-    constexpr int P = V == 1 ? 1 : V / 2;
+    constexpr int P = V == 1 ? 1 : V / 2, BYTES = V * W * (int)sizeof(T);
     auto at = [&](const void* from, long long i) { return seq_ld(static_cast<const T*>(from) + i); };
+    if (BYTES % 8 == 0 && reinterpret_cast<uintptr_t>(p.w) % 8 == 0) {          // the channels' taps lie together
+        uint2 q[BYTES / 8 + 1];
+#pragma unroll
+        for (int i = 0; i < BYTES / 8; ++i) q[i] = reinterpret_cast<const uint2*>(static_cast<const T*>(p.w) + (long long)c * W)[i];
+        auto tap = [&](int i) {
+            if constexpr (sizeof(T) == 2) {
+                const uint32_t two = i & 2 ? q[i / 4].y : q[i / 4].x;
+                return __uint_as_float(i & 1 ? two & 0xffff0000u : two << 16);
+            } else {
+                return __uint_as_float(i & 1 ? q[i / 2].y : q[i / 2].x);
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < P; ++i)
+#pragma unroll
+            for (int j = 0; j < W; ++j) w[j][i] = make_float2(tap(2 * i * W + j), V == 1 ? 0.f : tap((2 * i + (V > 1)) * W + j));
+    } else {
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const long long c0 = c + 2 * i, c1 = V == 1 ? c0 : c0 + 1;
+#pragma unroll
+            for (int j = 0; j < W; ++j) w[j][i] = make_float2(at(p.w, c0 * W + j), V == 1 ? 0.f : at(p.w, c1 * W + j));
+        }
+    }
 #pragma unroll
     for (int i = 0; i < P; ++i) {
         const long long c0 = c + 2 * i, c1 = V == 1 ? c0 : c0 + 1;
-#pragma unroll
-        for (int j = 0; j < W; ++j) w[j][i] = make_float2(at(p.w, c0 * W + j), V == 1 ? 0.f : at(p.w, c1 * W + j));
         b[i] = p.bias ? make_float2(at(p.bias, c0), V == 1 ? 0.f : at(p.bias, c1)) : make_float2(0.f, 0.f);
     }
 }
@@ -86,7 +108,25 @@ struct Place {
 };
 __device__ __forceinline__ Place place_of(const SeqAxis& ax, int t) {
     Place q;
-    q.s = seq_first_at(ax, t + 1) - 1;      // the last sequence that starts at or before t
+    // the last sequence that starts at or before t: a ragged axis is searched in eight parts a step, whose bounds
+    // are read together, so that a step costs one wait for memory
+    if (ax.L > 0) {
+        q.s = min(t / ax.L, ax.S - 1);
+    } else {
+        int lo = 0, hi = ax.S;
+        while (lo < hi) {
+            const int step = (hi - lo + 7) >> 3;
+            int less = 0;
+#pragma unroll
+            for (int k = 1; k <= 8; ++k) {
+                const int m = lo + k * step;
+                if (m <= hi && seq_start(ax, m - 1, 0) <= t) less = k;
+            }
+            lo += less * step;
+            hi = min(hi, lo + step - 1);
+        }
+        q.s = lo - 1;
+    }
     q.begin = q.s < 0 ? 0 : seq_start(ax, q.s, 0);
     q.end = seq_start(ax, q.s + 1, t + 1);
     return q;
@@ -106,6 +146,7 @@ __global__ void __launch_bounds__(128, 4) seq_conv_fwd_kernel(const __grid_const
     const int c = (blockIdx.y * 128 + threadIdx.x) * V;
     if (c >= p.D) return;
     const int t0 = blockIdx.x * p.run, t1 = min(t0 + p.run, p.ax.T);
+    griddep_launch();
     const T* x = static_cast<const T*>(p.x) + (long long)t0 * p.x_ld + c;
     T* y = static_cast<T*>(p.y) + (long long)t0 * p.y_ld + c;
     RowVec<T, V> next[GROUP];
@@ -158,22 +199,26 @@ __global__ void __launch_bounds__(128, 4) seq_conv_fwd_kernel(const __grid_const
 }
 
 // The states after the last tokens.  A launch of its own behind the forward kernel: with
-// state_out == state_in a thread there may still read the state that this one replaces.
+// state_out == state_in a thread there may still read the state that this one replaces.  It starts while that
+// one runs, and waits for its end only between its loads and its stores.
 template <typename T, int V, int W>
 __global__ void __launch_bounds__(128) seq_conv_state_kernel(const __grid_constant__ SeqConvParams p) {
     const int c = (blockIdx.x * 128 + threadIdx.x) * V;
-    if (c >= p.D) return;
+    bool waited = false;
     for (int s = blockIdx.y; s < p.ax.S; s += gridDim.y) {
         const long long to = seq_slot(p.sl, s);
-        if (to < 0) continue;
+        if (to < 0 || c >= p.D) continue;
         const int begin = seq_start(p.ax, s, 0), end = seq_start(p.ax, s + 1, begin);
         const T* x = static_cast<const T*>(p.x) + (long long)end * p.x_ld + c;
         float2 win[W][RowVec<T, V>::P];
 #pragma unroll
         for (int k = 1; k < W; ++k) load_before<T, V>(p, state_slot(p, s), x, end - begin, k, c, win[W - k]);
+        if (!waited) griddep_wait();
+        waited = true;
 #pragma unroll
         for (int k = 1; k < W; ++k) row_put<T, V>(static_cast<T*>(p.state_out) + (to * (W - 1) + W - 1 - k) * p.D + c, win[W - k]);
     }
+    if (!waited) griddep_wait();
 }
 
 // One token per sequence: row s of x follows the W - 1 rows of its state.
@@ -340,6 +385,7 @@ __global__ void __launch_bounds__(BWD_LANES * BWD_ROWS, W <= 4 ? 2 : 1) seq_conv
             }
         }
     }
+    griddep_launch();
 #pragma unroll
     for (int j = 0; j <= W; ++j) {
         __syncthreads();
@@ -363,6 +409,7 @@ __global__ void __launch_bounds__(BWD_LANES * BWD_ROWS, W <= 4 ? 2 : 1) seq_conv
 // dw and dbias: the blocks' rows of partial sums, added up in a fixed order.
 __global__ void __launch_bounds__(COLUMN_THREADS) seq_conv_param_kernel(const __grid_constant__ SeqConvParams p) {
     const int d = blockIdx.x * 32 + (threadIdx.x & 31), j = blockIdx.y;
+    griddep_wait();
     const float v = column_sum(p.ws + (long long)j * p.D + d, (long long)(p.W + 1) * p.D, p.tblocks, d < p.D);
     if (threadIdx.x >= 32 || d >= p.D) return;
     if (j < p.W) p.dw[(long long)d * p.W + j] = v;
@@ -385,7 +432,7 @@ cudaError_t launch_w(const SeqConvParams& p, Pass pass, cudaStream_t stream) {
                               dim3((unsigned)((p.ax.T + p.run - 1) / p.run), (unsigned)((p.D + 128 * V4 - 1) / (128 * V4))), dim3(128), 0,
                               stream, false, 1, p);
         if (e == cudaSuccess && p.state_out && W > 1)
-            e = launch_kernel(seq_conv_state_kernel<T, V, W>, dim3(cb, sb), dim3(128), 0, stream, false, 1, p);
+            e = launch_kernel(seq_conv_state_kernel<T, V, W>, dim3(cb, sb), dim3(128), 0, stream, p.ax.T > 0, 1, p);
         return e;
     }
     if (p.ax.T > 0)
@@ -394,7 +441,7 @@ cudaError_t launch_w(const SeqConvParams& p, Pass pass, cudaStream_t stream) {
                           dim3(BWD_LANES * BWD_ROWS), 0, stream, false, 1, p);
     if (e == cudaSuccess)
         e = launch_kernel(seq_conv_param_kernel, dim3((unsigned)((p.D + 31) / 32), (unsigned)(W + 1)), dim3(COLUMN_THREADS), 0,
-                          stream, false, 1, p);
+                          stream, p.ax.T > 0, 1, p);
     return e;
 }
 
@@ -422,12 +469,24 @@ cudaError_t launch(const SeqConvParams& p, bool bf16, Pass pass, cudaStream_t st
 
 }  // namespace
 
-// A thread's first rows cost it several waits for memory (its sequence, its window, its weights), so runs are
-// as long as the GPU stays full: about two rounds of resident threads (512 an SM), 8 to 256 tokens each.
-int seq_conv_run(long long T, int D, int sms) {
-    const long long want = (T * ((D + 3) / 4) + 1024ll * sms - 1) / (1024ll * sms);
-    const long long run = (want + 7) / 8 * 8;
-    return (int)(run < 8 ? 8 : run > 256 ? 256 : run);
+// Tokens a thread walks, 8 to 256: whole rounds of resident blocks (4, 5 or 8 an SM forward, 2 or 1 backward), where
+// a round costs its run and, for the several waits for memory before a thread's first token (its sequence, its
+// window, its weights), about `start` tokens more.  (Two rounds of 512 threads an SM instead, whatever is left
+// over: 6011 x 2560 ragged bf16 25.9 us, here 20.6; 8 x 2048 x 4096 bf16 forward and backward 154, here 144; 8 x 1500 x
+// 1280 fp32 89, here 76.)
+int seq_conv_run(long long T, int D, int W, bool bf16, bool bwd, int sms) {
+    const bool vec = D * (bf16 ? 2 : 4) % 16 == 0;
+    const int columns = bwd ? BWD_LANES * (!vec ? 1 : bf16 ? 4 : 2) : 128 * (vec ? 4 : 1), rows = bwd ? BWD_ROWS : 1;
+    const long long cb = (D + columns - 1) / columns, slots = (bwd ? (W <= 4 ? 2ll : 1ll) : !vec ? 8ll : bf16 ? 5ll : 4ll) * sms;
+    const int start = bwd ? 16 : 12;
+    long long best = 0;
+    int run = 8;
+    for (int r = 8; r <= 256; r += 8) {
+        const long long blocks = (T + (long long)r * rows - 1) / ((long long)r * rows) * cb;
+        const long long cost = (blocks + slots - 1) / slots * (r + start);
+        if (r == 8 || cost < best) best = cost, run = r;
+    }
+    return run;
 }
 int seq_conv_bwd_token_blocks(long long T, int run) { return (int)((T + (long long)run * BWD_ROWS - 1) / ((long long)run * BWD_ROWS)); }
 cudaError_t launch_seq_conv_fwd(const SeqConvParams& p, bool bf16, cudaStream_t stream) { return launch(p, bf16, Pass::Fwd, stream); }

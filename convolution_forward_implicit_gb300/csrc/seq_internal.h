@@ -63,7 +63,7 @@ struct SeqConvParams {
 cudaError_t launch_seq_conv_fwd(const SeqConvParams& p, bool bf16, cudaStream_t stream);
 cudaError_t launch_seq_conv_bwd(const SeqConvParams& p, bool bf16, cudaStream_t stream);
 cudaError_t launch_seq_conv_step(const SeqConvParams& p, bool bf16, cudaStream_t stream);
-int seq_conv_run(long long T, int D, int sms);
+int seq_conv_run(long long T, int D, int W, bool bf16, bool bwd, int sms);
 int seq_conv_bwd_token_blocks(long long T, int run);
 
 // ---- selective scan ----

@@ -194,6 +194,7 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 512 ? 512 / THREADS : 1) s
         }
         row_store<T, WIDE, UPT>(p.dx, row * p.dx_ld, D, d);
     }
+    griddep_launch();
     if (!p.ws) return;
     const long long part = ((long long)blockIdx.x * rows_at_once + ty) * SUMS * p.D;
     row_store<float, WIDE, UPT>(p.ws, part, p.D, s_1);
@@ -205,6 +206,7 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 512 ? 512 / THREADS : 1) s
 // The parameters' gradients: the blocks' rows of partial sums, added up in a fixed order.
 template <typename T>
 __global__ void __launch_bounds__(COLUMN_THREADS) seq_norm_param_kernel(const __grid_constant__ SeqNormParams p, int parts, bool bias) {
+    griddep_wait();
     const int c = blockIdx.x * 32 + (threadIdx.x & 31);
     const bool on = c < p.D, first = threadIdx.x < 32 && on;
     auto total = [&](int k) { return column_sum(p.ws + (long long)k * p.D + c, (long long)SUMS * p.D, parts, on); };
@@ -270,7 +272,7 @@ cudaError_t launch_u(const SeqNormParams& p, const Shape& s, bool bias, cudaStre
     cudaError_t e = RING ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, s.smem) : cudaSuccess;
     if (e == cudaSuccess) e = launch_kernel(kernel, dim3((unsigned)s.blocks), s.block, (size_t)s.smem, stream, false, 1, p);
     if (e == cudaSuccess && p.ws)
-        e = launch_kernel(seq_norm_param_kernel<T>, dim3((unsigned)((p.D + 31) / 32), SUMS), dim3(COLUMN_THREADS), 0, stream, false, 1, p,
+        e = launch_kernel(seq_norm_param_kernel<T>, dim3((unsigned)((p.D + 31) / 32), SUMS), dim3(COLUMN_THREADS), 0, stream, true, 1, p,
                           s.blocks * (int)s.block.y, bias);
     return e;
 }
