@@ -7,6 +7,10 @@
 // plus W - 1 rows at the start of a run.  The inputs lie in a ring of W slots; tokens are unrolled in groups of
 // a multiple of W, so that every token's slots are known to the compiler and nothing moves.  The next group's
 // rows are on their way while this one is computed.
+//
+// 8 x 2048 x 4096 bf16, 4 taps, silu: forward 46 us (268 MB: 5.8 TB/s, 87% of a plain copy's rate), backward 90 us
+// (403 MB: 4.5 TB/s; a sigmoid and 12 multiply-adds a value, 0.55 instructions a clock and scheduler at the 15 warps
+// an SM that the registers of its windows and sums allow).
 #include <type_traits>
 
 #include "seq_common.cuh"

@@ -6,6 +6,10 @@
 //   dw_post = scale S1,   db_post = scale S0,   dscale = w_post S1 + b_post S0.
 // Bound by bytes.  A block keeps its share of the rows' parameter sums in registers (its threads stay
 // on their columns), writes them once, and a second kernel adds the blocks up in their order.
+//
+// 8192 x 4096 bf16 with an fp32 residual and everything on: 180 us for 738 MB (4.1 TB/s, 61% of a plain copy's
+// rate); 6007 x 1280 fp32 layer norm: 48 us for 185 MB (58%).  With the sums' registers, 15 or 16 warps an SM: each
+// row is a chain of loads, special functions, sums and barriers that few other rows overlap.
 #include "seq_norm.cuh"
 
 namespace convfwd {
@@ -241,9 +245,9 @@ struct Shape {
     dim3 block;
     int smem, blocks;
 };
-// `wide`: rows of aligned groups.  8 columns a thread up to 4096 (8192 x 4096 bf16 with everything on: 204 us with
-// one block of 512 threads an SM; 212 with two of 256 and 16 columns each, which spills; 237 with two of 512
-// and 64 registers).
+// `wide`: rows of aligned groups.  8 columns a thread up to 4096 (8192 x 4096 bf16 with everything on, measured before
+// the sums shared their barriers: 204 us with one block of 512 threads an SM; 212 with two of 256 and 16 columns
+// each, which spills; 237 with two of 512 and 64 registers).
 Shape shape_of(int rows, int D, unsigned flags, bool wide, int esize, int rsize, int sms) {
     const bool gate = flags & (SEQ_NORM_GATE_BEFORE | SEQ_NORM_GATE_AFTER), residual = flags & SEQ_NORM_RESIDUAL;
     const bool pre = flags & SEQ_NORM_PRE;

@@ -3,6 +3,10 @@
 // Per token, channel and state: one exponential (exp(delta A) as 2^(delta A log2 e)) and four
 // multiply-adds, so the pass is bound by the special-function and FMA pipes.  A thread holds NPT states of one channel in registers and walks the
 // tokens of a piece; LN neighbouring lanes share a channel when it has more states.
+//
+// 4 x 2048 x 4096 x 16 bf16 in 7 pieces a sequence: 157 us, and 106 for the pieces' contributions before it (the
+// exponentials alone are 58 us of each; uncut, the 4 x 4096 channels fill a third of the GPU's warps: 710 us at an
+// earlier state, cut 410).  0.58 instructions a clock and scheduler: what is left is dependent latency.
 #include "seq_scan.cuh"
 
 namespace convfwd {
