@@ -411,7 +411,7 @@ __global__ void __launch_bounds__(BWD_LANES * BWD_ROWS, W <= 4 ? 2 : 1) seq_conv
 }
 
 // dw and dbias: the blocks' rows of partial sums, added up in a fixed order.
-__global__ void __launch_bounds__(COLUMN_THREADS) seq_conv_param_kernel(const __grid_constant__ SeqConvParams p) {
+__global__ void __launch_bounds__(COLUMN_THREADS, 2) seq_conv_param_kernel(const __grid_constant__ SeqConvParams p) {
     const int d = blockIdx.x * 32 + (threadIdx.x & 31), j = blockIdx.y;
     griddep_wait();
     const float v = column_sum(p.ws + (long long)j * p.D + d, (long long)(p.W + 1) * p.D, p.tblocks, d < p.D);

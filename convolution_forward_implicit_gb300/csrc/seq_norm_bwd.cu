@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 512 ? 512 / THREADS : 1) s
 
 // The parameters' gradients: the blocks' rows of partial sums, added up in a fixed order.
 template <typename T>
-__global__ void __launch_bounds__(COLUMN_THREADS) seq_norm_param_kernel(const __grid_constant__ SeqNormParams p, int parts, bool bias) {
+__global__ void __launch_bounds__(COLUMN_THREADS, 2) seq_norm_param_kernel(const __grid_constant__ SeqNormParams p, int parts, bool bias) {
     griddep_wait();
     const int c = blockIdx.x * 32 + (threadIdx.x & 31);
     const bool on = c < p.D, first = threadIdx.x < 32 && on;
