@@ -140,7 +140,8 @@ class _SeqPlan:
         self.handle = handle
         self.dtype, self.direction = int(dtype), direction
         self.torch_dtype = _torch_dtype(dtype)
-        self.workspace = None
+        self.workspace = None                    # of the latest call
+        self._workspaces, self._ws_stream = {}, None      # stream -> its workspace; the stream of self.workspace
         self._f32, self._i32 = torch.float32, torch.int32
         self._ws_bytes = seq_workspace_bytes(handle)
         self._pack = struct.Struct(f"={len(self._fields)}q").pack
@@ -161,14 +162,31 @@ class _SeqPlan:
         return seq_plan_describe(self.handle)
 
     def allocate(self, device=None):
-        """Allocate the workspace, if the plan needs one."""
+        """Allocate the workspace of the current stream, if the plan needs one (a call does so for its own stream)."""
         import torch
         if self._ws_bytes:
-            dev = torch.device("cuda", torch.cuda.current_device() if device is None else device) if not isinstance(
-                device, torch.device) else device
-            self.workspace = torch.empty(self._ws_bytes, dtype=torch.uint8, device=dev)
-            seq_plan_set_workspace(self.handle, self.workspace.data_ptr(), self._ws_bytes)
+            index = device.index if isinstance(device, torch.device) else device
+            index = torch.cuda.current_device() if index is None else index
+            self._use_workspace(self._stream(index), index)
         return self
+
+    def _use_workspace(self, s, index):
+        """Take the workspace of stream s, allocated on that stream: PyTorch hands a freed block on in the order of
+        the stream it was allocated on, so on another stream's block the kernels on s could meet the work of its last owner, or,
+        once the plan is gone, of its next.  A plan keeps the workspaces of all its streams.  (A call that is being
+        captured takes one that is there, since a graph runs on any stream: the plan must outlive the graph.)"""
+        import torch
+        ws = self._workspaces.get(s)
+        if ws is None:
+            on = torch.cuda.default_stream(index) if s == 0 else torch.cuda.ExternalStream(s, device=index)
+            with torch.cuda.stream(on):
+                if self._workspaces and torch.cuda.is_current_stream_capturing():
+                    ws, s = next(iter(self._workspaces.values())), None
+                else:
+                    ws = torch.empty(self._ws_bytes, dtype=torch.uint8, device=torch.device("cuda", index))
+                    self._workspaces[s] = ws
+        self.workspace, self._ws_stream = ws, s
+        seq_plan_set_workspace(self.handle, ws.data_ptr(), self._ws_bytes)
 
     # -- argument checks -------------------------------------------------------------------
     def _need(self, direction):
@@ -233,9 +251,9 @@ class _SeqPlan:
             self._flat(v, "starts", starts, (self.S + 1,), self._i32)
 
     def _call(self, v, device, stream):
-        if self._ws_bytes and self.workspace is None:
-            self.allocate(device)
         s = stream if stream is not None else self._stream(device)
+        if self._ws_bytes and s != self._ws_stream:
+            self._use_workspace(s, device)
         st = self._fn(self.handle, self._pack(*v), s)
         if st != CONV_OK:
             raise ConvError(st, self._name)

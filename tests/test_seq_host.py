@@ -229,3 +229,49 @@ def test_norm_gradients_against_differences(layer, post, pre, gate, after, res):
     for k in a:
         if a[k] is not None:
             _directional(f, a, g, k, rng)
+
+
+# ------------------------------------------------------------------ the Python plans without a GPU
+def test_a_workspace_is_allocated_on_the_stream_that_uses_it(lib, monkeypatch):
+    """The allocator orders a block's owners by the stream it was allocated on.  Streams and memory are stood in
+    for by numbers and host memory, the call by a function that notes the plan's workspace."""
+    import contextlib
+    import torch
+    current, made, used = [7], [], []
+
+    @contextlib.contextmanager
+    def on(s):
+        before, current[0] = current[0], s
+        yield
+        current[0] = before
+
+    empty = torch.empty
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda s, device=None: s)
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: 0)
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: current[0] >= 100)
+    p = Q.SeqConvPlan(2, 8, 16, 4, B.CONV_F32, direction="bwd")
+    v = [0] * len(Q.CONV_FIELDS)
+    p._stream = lambda index: current[0]
+    p._fn = lambda handle, args, s: used.append((s, p.workspace.data_ptr())) or 0
+    monkeypatch.setattr(torch, "empty", lambda n, dtype=None, device=None: made.append(current[0]) or empty(n, dtype=dtype))
+    p._call(v, 0, 9)                 # a first call on another stream than the current one
+    assert made == [9]
+    p._call(v, 0, None)
+    p._call(v, 0, 0)
+    assert made == [9, 7, 0]
+    for s in (9, None, 0, 9):        # every stream keeps its own
+        p._call(v, 0, s)
+    assert made == [9, 7, 0] and current == [7]
+    at = dict(used)
+    assert len(set(at.values())) == 3 and all(at[s] == w for s, w in used)
+    p._call(v, 0, 100)               # captured: one that is there, and nothing allocated
+    assert made == [9, 7, 0] and used[-1][1] in at.values()
+    p._call(v, 0, None)
+    assert used[-1] == (7, at[7])
+    p.close()
+    q = Q.SeqConvPlan(2, 8, 16, 4, B.CONV_F32, direction="bwd")
+    q._stream = p._stream
+    q.allocate(torch.device("cuda", 0)).allocate(0)
+    assert made == [9, 7, 0, 7]
+    q.close()
