@@ -381,7 +381,8 @@ __device__ __forceinline__ float row_norm(float2 (&v)[UPT][4], int D, bool layer
 }
 
 constexpr int NORM_RING = 2;                  // stages: a row in use and one on its way
-constexpr int NORM_RING_MAX = 226 * 1024;     // bytes of a block's stages; wider rows are loaded directly
+constexpr int NORM_RING_MAX = 224 * 1024;     // bytes of a block's stages; wider rows are loaded directly
+static_assert(NORM_RING_MAX + sizeof(NormSums) <= 227 * 1024, "a block's shared memory");
 
 // Threads per row and rows per block: upt groups of 8 columns to a thread.
 inline dim3 norm_block(int D, int upt) {

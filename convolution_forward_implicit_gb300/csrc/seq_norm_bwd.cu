@@ -273,7 +273,9 @@ Shape shape_of(int rows, int D, unsigned flags, bool wide, int esize, int rsize,
 template <typename T, typename RT, bool WIDE, bool RING, int UPT, int THREADS>
 cudaError_t launch_u(const SeqNormParams& p, const Shape& s, bool bias, cudaStream_t stream) {
     const auto kernel = bias ? seq_norm_bwd_kernel<T, RT, WIDE, RING, UPT, true, THREADS> : seq_norm_bwd_kernel<T, RT, WIDE, RING, UPT, false, THREADS>;
-    cudaError_t e = RING ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, s.smem) : cudaSuccess;
+    // always the same limit, not this call's bytes: host threads may call at the same time, and what one sets must
+    // do for the other's launch
+    cudaError_t e = RING ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, NORM_RING_MAX) : cudaSuccess;
     if (e == cudaSuccess) e = launch_kernel(kernel, dim3((unsigned)s.blocks), s.block, (size_t)s.smem, stream, false, 1, p);
     if (e == cudaSuccess && p.ws)
         e = launch_kernel(seq_norm_param_kernel<T>, dim3((unsigned)((p.D + 31) / 32), SUMS), dim3(COLUMN_THREADS), 0, stream, true, 1, p,

@@ -3,7 +3,7 @@ threads, graphs."""
 import pytest
 
 from convolution_forward_implicit_gb300 import seq as Q
-from convolution_forward_implicit_gb300.binding import CONV_F32
+from convolution_forward_implicit_gb300.binding import CONV_BF16, CONV_F32
 
 pytestmark = pytest.mark.gpu
 
@@ -86,3 +86,60 @@ def test_one_plan_on_two_streams():
                 p.forward(*a, y)
     torch.cuda.synchronize()
     assert all(torch.equal(y, want) for y in ys)
+
+
+# ---------------------------------------------------------------------------- host threads
+def test_norm_gradients_from_two_host_threads():
+    """Plans of other flags share a kernel and want other amounts of shared memory of it; calls with workspaces
+    of their own may come from any threads."""
+    import sys
+    import threading
+    import torch
+    rows, D = 3, 4096
+    g = torch.Generator(device="cuda").manual_seed(3)
+    n = lambda *s, dtype=torch.bfloat16: torch.randn(*s, generator=g, device="cuda").to(dtype)      # noqa: E731
+    x, gate, dy = n(rows, D), n(rows, D), n(rows, D)
+    res, dro = n(rows, D, dtype=torch.float32), n(rows, D, dtype=torch.float32)
+    e = torch.empty_like
+
+    def large():
+        p = Q.SeqNormPlan(rows, D, CONV_BF16, "bwd", post=True, pre=True, gate=Q.SEQ_GATE_BEFORE)
+        dx, dg, dr = e(x), e(gate), e(res)
+        return lambda: p.backward(x, dx, dy=dy, gate=gate, res=res, dres_out=dro, dgate=dg, dres=dr), (dx, dg, dr)
+
+    def small():
+        p = Q.SeqNormPlan(rows, D, CONV_BF16, "bwd", post=True, pre=False, residual=False, gate=Q.SEQ_GATE_BEFORE)
+        dx, dg = e(x), e(gate)
+        return lambda: p.backward(x, dx, dy=dy, gate=gate, dgate=dg), (dx, dg)
+
+    made = [large(), small()]
+    want = []
+    for call, out in made:
+        call()
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in out])
+    errors = []
+
+    def work(call):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(30000):
+                    call()
+                torch.cuda.current_stream().synchronize()
+        except Exception as exc:      # noqa: BLE001
+            errors.append(exc)
+
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=(call,)) for call, _ in made]
+    interval = sys.getswitchinterval()
+    sys.setswitchinterval(1e-6)          # (so that a thread is ready to go on when the other one enters the library)
+    try:
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+    finally:
+        sys.setswitchinterval(interval)
+    assert not errors, errors
+    for (_, out), w in zip(made, want):
+        assert all(torch.equal(a, b) for a, b in zip(out, w))
