@@ -194,7 +194,7 @@ class _SeqPlan:
             _fail(self._name, f"the plan's direction is {self.direction!r}")
 
     def _rows(self, v, name, t, width, dtype):
-        """A tensor of the token axis: (rows, width) or (S, rows / S, width)."""
+        """A tensor of the token axis: (rows, width), (1, rows, width) or (S, rows / S, width)."""
         if t is None:
             return
         sh, st = t.shape, t.stride()
@@ -217,6 +217,9 @@ class _SeqPlan:
                 ld = st[0]
         else:
             _fail(self._name, f"{name} is not rows of one token axis: shape {tuple(sh)}, strides {tuple(st)}")
+        if n == 3 and self._sequences and sh[0] > 1 and sh[1] > 1 and sh[0] != self._sequences:
+            _fail(self._name, f"{name} has shape {tuple(sh)}: ({self._sequences}, {self._tokens // self._sequences}, {width}) or "
+                              f"({self._tokens}, {width}) is wanted, sequences first")
         if rows != self._tokens or sh[-1] != width or (st[-1] != 1 and width > 1 and rows):
             _fail(self._name, f"{name} has shape {tuple(sh)}, strides {tuple(st)}: {self._tokens} rows of {width} contiguous "
                               "values are wanted")
@@ -280,7 +283,7 @@ class SeqConvPlan(_SeqPlan):
     def __init__(self, S, T, D, W, dtype, direction="fwd", ragged=False, silu=True):
         code = self._direction(direction, self._names)
         self.S, self.T, self.D, self.W = int(S), int(T), int(D), int(W)
-        self._tokens = self.T
+        self._tokens, self._sequences = self.T, self.S
         self._open(seq_conv_plan_create(S, T, D, W, dtype, code, SEQ_RAGGED * bool(ragged) + SEQ_CONV_SILU * bool(silu)),
                    dtype, direction)
 
@@ -331,7 +334,7 @@ class SeqScanPlan(_SeqPlan):
     def __init__(self, S, T, D, N, dtype, direction="fwd", G=1, ragged=False, softplus=True):
         code = self._direction(direction, self._names)
         self.S, self.T, self.D, self.N, self.G = int(S), int(T), int(D), int(N), int(G)
-        self._tokens = self.T
+        self._tokens, self._sequences = self.T, self.S
         self._open(seq_scan_plan_create(S, T, D, N, G, dtype, code,
                                         SEQ_RAGGED * bool(ragged) + SEQ_SCAN_SOFTPLUS * bool(softplus)), dtype, direction)
         self.saved_bytes = seq_scan_saved_bytes(self.handle)
@@ -413,6 +416,7 @@ class SeqNormPlan(_SeqPlan):
                  SEQ_NORM_RESIDUAL * bool(residual))
         self.rows, self.D, self.eps = int(rows), int(D), float(eps)
         self._tokens = self.rows
+        self._sequences = None               # (rows have no order)
         self.res_torch_dtype = _torch_dtype(res_dtype)
         self._open(seq_norm_plan_create(rows, D, dtype, res_dtype, code, flags, eps), dtype, direction)
 

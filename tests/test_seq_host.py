@@ -275,3 +275,42 @@ def test_a_workspace_is_allocated_on_the_stream_that_uses_it(lib, monkeypatch):
     q.allocate(torch.device("cuda", 0)).allocate(0)
     assert made == [9, 7, 0, 7]
     q.close()
+
+
+class OnGpu:
+    """What the plans' layout checks look at in a tensor, of a tensor that is not there."""
+    is_cuda = True
+
+    def __init__(self, host):
+        self.dtype, self.shape, self.stride = host.dtype, host.shape, host.stride
+
+    def data_ptr(self):
+        return P
+
+    def get_device(self):
+        return 0
+
+
+def _layout(plan, host, width):
+    v = [0] * len(plan._fields)
+    plan._rows(v, "x", OnGpu(host), width, plan.torch_dtype)
+    assert v[plan._place["x"]] == P
+    return v[plan._place["x_ld"]]
+
+
+@pytest.mark.parametrize("make", [lambda **k: Q.SeqConvPlan(4, 24, 16, 4, B.CONV_F32, **k), lambda **k: Q.SeqScanPlan(4, 24, 16, 8, B.CONV_F32, **k)])
+def test_python_plans_take_sequences_first(lib, make):
+    """(L, S, D) has as many rows as (S, L, D), in another order."""
+    import torch
+    for p in (make(), make(ragged=True)):
+        for good, ld in ((torch.zeros(24, 16), 16), (torch.zeros(24, 20)[:, 4:], 20), (torch.zeros(4, 6, 16), 16), (torch.zeros(1, 24, 16), 16),
+                         (torch.zeros(4, 6, 40)[..., :16], 40), (torch.zeros(24, 1, 16), 16)):
+            assert _layout(p, good, 16) == ld
+        for bad in (torch.zeros(6, 4, 16), torch.zeros(2, 12, 16), torch.zeros(6, 4, 16).transpose(0, 1)):
+            with pytest.raises(B.ConvError) as e:
+                _layout(p, bad, 16)
+            assert e.value.status == B.CONV_ERR_INVALID_ARG
+        p.close()
+    n = Q.SeqNormPlan(24, 16, B.CONV_F32)             # its rows have no order
+    assert _layout(n, torch.zeros(6, 4, 16), 16) == 16 and _layout(n, torch.zeros(4, 6, 16), 16) == 16
+    n.close()
