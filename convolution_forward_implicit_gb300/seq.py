@@ -211,7 +211,7 @@ class _SeqPlan:
         n = len(sh)
         if n == 2:
             rows, ld = sh[0], st[0]
-        elif n == 3 and (sh[0] <= 1 or sh[1] == 0 or st[0] == sh[1] * st[1]):
+        elif n == 3 and (sh[0] <= 1 or sh[1] <= 1 or st[0] == sh[1] * st[1]):
             rows, ld = sh[0] * sh[1], st[1]
             if sh[1] == 1:
                 ld = st[0]

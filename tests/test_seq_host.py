@@ -314,3 +314,16 @@ def test_python_plans_take_sequences_first(lib, make):
     n = Q.SeqNormPlan(24, 16, B.CONV_F32)             # its rows have no order
     assert _layout(n, torch.zeros(6, 4, 16), 16) == 16 and _layout(n, torch.zeros(4, 6, 16), 16) == 16
     n.close()
+
+
+def test_python_plans_take_one_token_of_longer_sequences(lib):
+    """x[:, -1:, :] of (S, L, D): rows that lie L tokens apart."""
+    import torch
+    x = torch.zeros(4, 6, 20)
+    for p in (Q.SeqConvPlan(4, 4, 16, 4, B.CONV_F32, direction="step"), Q.SeqScanPlan(4, 4, 16, 8, B.CONV_F32, direction="step"),
+              Q.SeqNormPlan(4, 16, B.CONV_F32)):
+        assert _layout(p, x[:, 5, :16], 16) == 120 and _layout(p, x[:, 5:, :16], 16) == 120
+        p.close()
+    p = Q.SeqConvPlan(1, 1, 16, 4, B.CONV_F32, direction="step")
+    assert _layout(p, x[:1, 5:, :16], 16) == 16          # one row: its distance to the next does not matter
+    p.close()
