@@ -146,11 +146,14 @@ class _SeqPlan:
         self._ws_bytes = seq_workspace_bytes(handle)
         self._pack = struct.Struct(f"={len(self._fields)}q").pack
         self._place = {f: i for i, f in enumerate(self._fields)}
+        self._blank = [0] * (len(self._fields) + 1)
         self._seen = {}          # argument -> the last layout found good for it
+        self._state_shape = None                 # the same of the states
         name = self._names[direction]
         self._name, self._fn = name, getattr(_library(), name)
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)      # (current_stream builds an object)
         self._stream = raw or (lambda index: torch.cuda.current_stream(index).cuda_stream)
+        self._current = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
     @staticmethod
     def _direction(direction, allowed):
@@ -189,9 +192,15 @@ class _SeqPlan:
         seq_plan_set_workspace(self.handle, ws.data_ptr(), self._ws_bytes)
 
     # -- argument checks -------------------------------------------------------------------
-    def _need(self, direction):
+    # `v` collects the values of the argument struct; behind them stands the device, x's, that all tensors are on.
+    def _values(self, x, direction):
         if self.direction != direction:
             _fail(self._name, f"the plan's direction is {self.direction!r}")
+        v = self._blank.copy()
+        v[-1] = device = x.get_device()
+        if device < 0 or device != self._current():
+            _fail(self._name, f"x is on {x.device}, not on the current GPU")
+        return v
 
     def _rows(self, v, name, t, width, dtype):
         """A tensor of the token axis: (rows, width), (1, rows, width) or (S, rows / S, width)."""
@@ -199,15 +208,15 @@ class _SeqPlan:
             return
         sh, st = t.shape, t.stride()
         seen = self._seen.get(name)
-        if seen is None or seen[0] != sh or seen[1] != st or seen[2] is not t.dtype or not t.is_cuda:
-            seen = self._seen[name] = self._rows_layout(name, t, sh, st, width, dtype)
+        if seen is None or seen[0] != sh or seen[1] != st or seen[2] is not t.dtype or t.get_device() != v[-1]:
+            seen = self._seen[name] = self._rows_layout(name, t, sh, st, width, dtype, v[-1])
         i = seen[4]
         v[i] = t.data_ptr()
         v[i + 1] = seen[3]
 
-    def _rows_layout(self, name, t, sh, st, width, dtype):
-        if t.dtype is not dtype or not t.is_cuda:
-            _fail(self._name, f"{name} is not a {dtype} tensor on the GPU")
+    def _rows_layout(self, name, t, sh, st, width, dtype, device):
+        if t.dtype is not dtype or t.get_device() != device:
+            _fail(self._name, f"{name} is not a {dtype} tensor on x's GPU")
         n = len(sh)
         if n == 2:
             rows, ld = sh[0], st[0]
@@ -229,8 +238,8 @@ class _SeqPlan:
         """A contiguous tensor of a fixed shape."""
         if t is None:
             return
-        if t.dtype is not dtype or not t.is_cuda or t.shape != shape or not t.is_contiguous():
-            _fail(self._name, f"{name} is not a contiguous {dtype} tensor of shape {tuple(shape)} on the GPU")
+        if t.dtype is not dtype or t.get_device() != v[-1] or t.shape != shape or not t.is_contiguous():
+            _fail(self._name, f"{name} is not a contiguous {dtype} tensor of shape {tuple(shape)} on x's GPU")
         v[self._place[name]] = t.data_ptr()
 
     def _states(self, v, slots, starts, row, dtype, **states):
@@ -240,14 +249,16 @@ class _SeqPlan:
             if t is None:
                 continue
             sh = t.shape
-            if t.dtype is not dtype or not t.is_cuda or sh[1:] != row or not t.is_contiguous():
+            if (t.dtype is not dtype or t.get_device() != v[-1] or (sh != self._state_shape and sh[1:] != row)
+                    or not t.is_contiguous()):
                 _fail(self._name, f"{name} is not a contiguous {dtype} tensor of shape (slots, {', '.join(map(str, row))}) "
-                                  "on the GPU")
+                                  "on x's GPU")
             if count >= 0 and sh[0] != count:
                 _fail(self._name, "the state buffers have different numbers of rows")
             count = sh[0]
+            self._state_shape = sh
             v[self._place[name]] = t.data_ptr()
-        v[self._place["slot_count"]] = max(count, 0)
+        v[self._place["slot_count"]] = count if count > 0 else 0
         if slots is not None:
             self._flat(v, "slots", slots, (self.S,), self._i32)
         if starts is not None:
@@ -284,42 +295,40 @@ class SeqConvPlan(_SeqPlan):
         code = self._direction(direction, self._names)
         self.S, self.T, self.D, self.W = int(S), int(T), int(D), int(W)
         self._tokens, self._sequences = self.T, self.S
+        self._width, self._taps, self._row = (self.D,), (self.D, self.W), (self.W - 1, self.D)
         self._open(seq_conv_plan_create(S, T, D, W, dtype, code, SEQ_RAGGED * bool(ragged) + SEQ_CONV_SILU * bool(silu)),
                    dtype, direction)
 
-    def _common(self, x, w, bias):
-        v = [0] * len(self._fields)
+    def _common(self, direction, x, w, bias):
+        v = self._values(x, direction)
         dt = self.torch_dtype
         self._rows(v, "x", x, self.D, dt)
-        self._flat(v, "w", w, (self.D, self.W), dt)
-        self._flat(v, "bias", bias, (self.D,), dt)
+        self._flat(v, "w", w, self._taps, dt)
+        self._flat(v, "bias", bias, self._width, dt)
         return v
 
     def forward(self, x, w, bias, y, starts=None, state_in=None, state_out=None, slots=None, stream=None):
-        self._need("fwd")
-        v = self._common(x, w, bias)
+        v = self._common("fwd", x, w, bias)
         self._rows(v, "y", y, self.D, self.torch_dtype)
-        self._states(v, slots, starts, (self.W - 1, self.D), self.torch_dtype, state_in=state_in, state_out=state_out)
-        self._call(v, x.get_device(), stream)
+        self._states(v, slots, starts, self._row, self.torch_dtype, state_in=state_in, state_out=state_out)
+        self._call(v, v.pop(), stream)
         return y
 
     def backward(self, x, w, bias, dy, dx, dw, dbias, starts=None, state_in=None, slots=None, stream=None):
-        self._need("bwd")
-        v = self._common(x, w, bias)
+        v = self._common("bwd", x, w, bias)
         self._rows(v, "dy", dy, self.D, self.torch_dtype)
         self._rows(v, "dx", dx, self.D, self.torch_dtype)
         self._flat(v, "dw", dw, (self.D, self.W), self._f32)
         self._flat(v, "dbias", dbias, (self.D,), self._f32)
-        self._states(v, slots, starts, (self.W - 1, self.D), self.torch_dtype, state_in=state_in)
-        self._call(v, x.get_device(), stream)
+        self._states(v, slots, starts, self._row, self.torch_dtype, state_in=state_in)
+        self._call(v, v.pop(), stream)
         return dx, dw, dbias
 
     def step(self, x, w, bias, state_in, state_out, y, slots=None, stream=None):
-        self._need("step")
-        v = self._common(x, w, bias)
+        v = self._common("step", x, w, bias)
         self._rows(v, "y", y, self.D, self.torch_dtype)
-        self._states(v, slots, None, (self.W - 1, self.D), self.torch_dtype, state_in=state_in, state_out=state_out)
-        self._call(v, x.get_device(), stream)
+        self._states(v, slots, None, self._row, self.torch_dtype, state_in=state_in, state_out=state_out)
+        self._call(v, v.pop(), stream)
         return y
 
 
@@ -335,6 +344,7 @@ class SeqScanPlan(_SeqPlan):
         code = self._direction(direction, self._names)
         self.S, self.T, self.D, self.N, self.G = int(S), int(T), int(D), int(N), int(G)
         self._tokens, self._sequences = self.T, self.S
+        self._width, self._row = (self.D,), (self.D, self.N)
         self._open(seq_scan_plan_create(S, T, D, N, G, dtype, code,
                                         SEQ_RAGGED * bool(ragged) + SEQ_SCAN_SOFTPLUS * bool(softplus)), dtype, direction)
         self.saved_bytes = seq_scan_saved_bytes(self.handle)
@@ -345,17 +355,17 @@ class SeqScanPlan(_SeqPlan):
         return torch.empty(self.saved_bytes // 4, dtype=torch.float32,
                            device=device or torch.device("cuda", torch.cuda.current_device()))
 
-    def _common(self, x, dt, A, B, C, D, z, dt_bias):
-        v = [0] * len(self._fields)
+    def _common(self, direction, x, dt, A, B, C, D, z, dt_bias):
+        v = self._values(x, direction)
         td, f32 = self.torch_dtype, self._f32
         self._rows(v, "x", x, self.D, td)
         self._rows(v, "dt", dt, self.D, td)
         self._rows(v, "B", B, self.G * self.N, td)
         self._rows(v, "C", C, self.G * self.N, td)
         self._rows(v, "z", z, self.D, td)
-        self._flat(v, "A", A, (self.D, self.N), f32)
-        self._flat(v, "D", D, (self.D,), f32)
-        self._flat(v, "dt_bias", dt_bias, (self.D,), f32)
+        self._flat(v, "A", A, self._row, f32)
+        self._flat(v, "D", D, self._width, f32)
+        self._flat(v, "dt_bias", dt_bias, self._width, f32)
         return v
 
     def _saved(self, v, saved):
@@ -364,18 +374,16 @@ class SeqScanPlan(_SeqPlan):
 
     def forward(self, x, dt, A, B, C, y, D=None, z=None, dt_bias=None, starts=None, h_in=None, h_out=None, slots=None,
                 saved=None, stream=None):
-        self._need("fwd")
-        v = self._common(x, dt, A, B, C, D, z, dt_bias)
+        v = self._common("fwd", x, dt, A, B, C, D, z, dt_bias)
         self._rows(v, "y", y, self.D, self.torch_dtype)
         self._saved(v, saved)
-        self._states(v, slots, starts, (self.D, self.N), self._f32, h_in=h_in, h_out=h_out)
-        self._call(v, x.get_device(), stream)
+        self._states(v, slots, starts, self._row, self._f32, h_in=h_in, h_out=h_out)
+        self._call(v, v.pop(), stream)
         return y
 
     def backward(self, x, dt, A, B, C, dy, saved, dx, ddt, dA, dB, dC, D=None, z=None, dt_bias=None, dD=None, dz=None,
                  ddt_bias=None, starts=None, h_in=None, dh_out=None, dh_in=None, slots=None, stream=None):
-        self._need("bwd")
-        v = self._common(x, dt, A, B, C, D, z, dt_bias)
+        v = self._common("bwd", x, dt, A, B, C, D, z, dt_bias)
         td, f32 = self.torch_dtype, self._f32
         for name, t in (("dy", dy), ("dx", dx), ("ddt", ddt), ("dz", dz)):
             self._rows(v, name, t, self.D, td)
@@ -385,16 +393,15 @@ class SeqScanPlan(_SeqPlan):
         self._flat(v, "dD", dD, (self.D,), f32)
         self._flat(v, "ddt_bias", ddt_bias, (self.D,), f32)
         self._saved(v, saved)
-        self._states(v, slots, starts, (self.D, self.N), f32, h_in=h_in, dh_out=dh_out, dh_in=dh_in)
-        self._call(v, x.get_device(), stream)
+        self._states(v, slots, starts, self._row, f32, h_in=h_in, dh_out=dh_out, dh_in=dh_in)
+        self._call(v, v.pop(), stream)
         return dx
 
     def step(self, x, dt, A, B, C, h_in, h_out, y, D=None, z=None, dt_bias=None, slots=None, stream=None):
-        self._need("step")
-        v = self._common(x, dt, A, B, C, D, z, dt_bias)
+        v = self._common("step", x, dt, A, B, C, D, z, dt_bias)
         self._rows(v, "y", y, self.D, self.torch_dtype)
-        self._states(v, slots, None, (self.D, self.N), self._f32, h_in=h_in, h_out=h_out)
-        self._call(v, x.get_device(), stream)
+        self._states(v, slots, None, self._row, self._f32, h_in=h_in, h_out=h_out)
+        self._call(v, v.pop(), stream)
         return y
 
 
@@ -415,40 +422,39 @@ class SeqNormPlan(_SeqPlan):
                  SEQ_NORM_GATE_BEFORE * (gate == SEQ_GATE_BEFORE) + SEQ_NORM_GATE_AFTER * (gate == SEQ_GATE_AFTER) +
                  SEQ_NORM_RESIDUAL * bool(residual))
         self.rows, self.D, self.eps = int(rows), int(D), float(eps)
-        self._tokens = self.rows
+        self._tokens, self._width = self.rows, (self.D,)
         self._sequences = None               # (rows have no order)
         self.res_torch_dtype = _torch_dtype(res_dtype)
         self._open(seq_norm_plan_create(rows, D, dtype, res_dtype, code, flags, eps), dtype, direction)
 
-    def _common(self, x, gate, w_post, b_post, scale, res, w_pre, b_pre):
-        v = [0] * len(self._fields)
+    def _common(self, direction, x, gate, w_post, b_post, scale, res, w_pre, b_pre):
+        v = self._values(x, direction)
         td = self.torch_dtype
         self._rows(v, "x", x, self.D, td)
         self._rows(v, "gate", gate, self.D, td)
         self._rows(v, "res", res, self.D, self.res_torch_dtype)
         for name, t in (("w_post", w_post), ("b_post", b_post), ("scale", scale), ("w_pre", w_pre), ("b_pre", b_pre)):
-            self._flat(v, name, t, (self.D,), td)
+            if t is not None:
+                self._flat(v, name, t, self._width, td)
         return v
 
     def forward(self, x, y=None, gate=None, w_post=None, b_post=None, scale=None, res=None, res_out=None, w_pre=None,
                 b_pre=None, stream=None):
-        self._need("fwd")
-        v = self._common(x, gate, w_post, b_post, scale, res, w_pre, b_pre)
+        v = self._common("fwd", x, gate, w_post, b_post, scale, res, w_pre, b_pre)
         self._rows(v, "y", y, self.D, self.torch_dtype)
         self._rows(v, "res_out", res_out, self.D, self.res_torch_dtype)
-        self._call(v, x.get_device(), stream)
+        self._call(v, v.pop(), stream)
         return y, res_out
 
     def backward(self, x, dx, dy=None, dres_out=None, gate=None, w_post=None, b_post=None, scale=None, res=None,
                  w_pre=None, b_pre=None, dgate=None, dres=None, dw_post=None, db_post=None, dscale=None, dw_pre=None,
                  db_pre=None, stream=None):
-        self._need("bwd")
-        v = self._common(x, gate, w_post, b_post, scale, res, w_pre, b_pre)
+        v = self._common("bwd", x, gate, w_post, b_post, scale, res, w_pre, b_pre)
         td, rd = self.torch_dtype, self.res_torch_dtype
         for name, t, dt in (("dy", dy, td), ("dres_out", dres_out, rd), ("dx", dx, td), ("dgate", dgate, td), ("dres", dres, rd)):
             self._rows(v, name, t, self.D, dt)
         for name, t in (("dw_post", dw_post), ("db_post", db_post), ("dscale", dscale), ("dw_pre", dw_pre),
                         ("db_pre", db_pre)):
             self._flat(v, name, t, (self.D,), self._f32)
-        self._call(v, x.get_device(), stream)
+        self._call(v, v.pop(), stream)
         return dx

@@ -327,3 +327,45 @@ def test_python_plans_take_one_token_of_longer_sequences(lib):
     p = Q.SeqConvPlan(1, 1, 16, 4, B.CONV_F32, direction="step")
     assert _layout(p, x[:1, 5:, :16], 16) == 16          # one row: its distance to the next does not matter
     p.close()
+
+
+class On(OnGpu):
+    """The same on a certain GPU, with the strides of `host` and any device."""
+
+    def __init__(self, host, device=0):
+        super().__init__(host)
+        self.at, self.is_contiguous, self.device = device, host.is_contiguous, f"cuda:{device}"
+
+    def get_device(self):
+        return self.at
+
+
+@pytest.mark.parametrize("current", [0, 1])
+def test_python_plans_want_every_tensor_on_the_launching_gpu(lib, current):
+    import torch
+    z = torch.zeros
+    calls = []
+
+    def ready(p):
+        p._current, p._stream, p._fn = (lambda: current), (lambda index: 0), (lambda *a: calls.append(a) or 0)
+        return p
+
+    conv = ready(Q.SeqConvPlan(2, 8, 16, 4, B.CONV_F32))
+    scan = ready(Q.SeqScanPlan(2, 8, 16, 8, B.CONV_F32, ragged=True))
+    norm = ready(Q.SeqNormPlan(8, 16, B.CONV_F32))
+    a = dict(x=z(8, 16), w=z(16, 4), bias=z(16), y=z(8, 16), state_in=z(2, 3, 16), slots=z(2, dtype=torch.int32))
+    b = dict(x=z(8, 16), dt=z(8, 16), A=z(16, 8), B=z(8, 8), C=z(8, 8), y=z(8, 16), D=z(16), h_in=z(2, 16, 8), starts=z(3, dtype=torch.int32))
+    c = dict(x=z(8, 16), y=z(8, 16), res=z(8, 16), res_out=z(8, 16), w_pre=z(16))
+    for plan, args in ((conv, a), (scan, b), (norm, c)):
+        on = {k: On(t, current) for k, t in args.items()}
+        n = len(calls)
+        plan.forward(**on)
+        assert len(calls) == n + 1
+        for k, t in args.items():                 # one of them elsewhere, after the same call was good
+            with pytest.raises(B.ConvError) as e:
+                plan.forward(**{**on, k: On(t, 1 - current)})
+            assert e.value.status == B.CONV_ERR_INVALID_ARG
+        with pytest.raises(B.ConvError):          # all of them on a GPU that is not the current one
+            plan.forward(**{k: On(t, 1 - current) for k, t in args.items()})
+        assert len(calls) == n + 1
+        plan.close()
