@@ -259,12 +259,16 @@ __global__ void __launch_bounds__(128) seq_conv_step_kernel(const __grid_constan
 // A thread walks its run and W - 1 tokens behind it (they see its last inputs), keeps the last
 // W values of dpre in slots as its inputs, and emits dx with a delay of W - 1 tokens.  The parameter sums of
 // the block's runs meet in shared memory in a fixed order and leave as one partial row per block.
-template <typename T, int V, int W>
+// LAYERS: rows of more channel blocks than a launch's second dimension takes lie on the third as well.  Kernels of
+// their own: the third index in the others costs 4 taps of bf16 8 bytes of spilled registers and 144 -> 172 us
+// a training pass of 8 x 2048 x 4096.
+template <typename T, int V, int W, bool LAYERS = false>
 __global__ void __launch_bounds__(BWD_LANES * BWD_ROWS, W <= 4 ? 2 : 1) seq_conv_bwd_kernel(const __grid_constant__ SeqConvParams p) {
     constexpr int P = RowVec<T, V>::P, GROUP = group_of(W, 4);
     __shared__ float sums[BWD_ROWS][BWD_LANES * V + 1];
     const int lane = threadIdx.x % BWD_LANES, row = threadIdx.x / BWD_LANES;
-    const int c = (blockIdx.y * BWD_LANES + lane) * V;
+    const int cblock = LAYERS ? blockIdx.z * gridDim.y + blockIdx.y : blockIdx.y;
+    const int c = (cblock * BWD_LANES + lane) * V;
     const int t0 = (int)min(((long long)blockIdx.x * BWD_ROWS + row) * p.run, (long long)p.ax.T);
     const int t1 = min(t0 + p.run, p.ax.T);
     float2 acc[W + 1][P];
@@ -400,7 +404,7 @@ __global__ void __launch_bounds__(BWD_LANES * BWD_ROWS, W <= 4 ? 2 : 1) seq_conv
         }
         __syncthreads();
         for (int i = threadIdx.x; i < BWD_LANES * V; i += BWD_LANES * BWD_ROWS) {
-            const int d = blockIdx.y * BWD_LANES * V + i;
+            const int d = cblock * BWD_LANES * V + i;
             if (d >= p.D) break;
             float s = 0.f;
 #pragma unroll
@@ -439,10 +443,14 @@ cudaError_t launch_w(const SeqConvParams& p, Pass pass, cudaStream_t stream) {
             e = launch_kernel(seq_conv_state_kernel<T, V, W>, dim3(cb, sb), dim3(128), 0, stream, p.ax.T > 0, 1, p);
         return e;
     }
-    if (p.ax.T > 0)
-        e = launch_kernel(seq_conv_bwd_kernel<T, VB, W>,
-                          dim3((unsigned)p.tblocks, (unsigned)((p.D + BWD_LANES * VB - 1) / (BWD_LANES * VB))),
-                          dim3(BWD_LANES * BWD_ROWS), 0, stream, false, 1, p);
+    if (p.ax.T > 0) {
+        const unsigned most = 65535, blocks = (unsigned)((p.D + BWD_LANES * VB - 1) / (BWD_LANES * VB));
+        const unsigned single = (unsigned)((p.D + BWD_LANES - 1) / BWD_LANES), layers = (single + most - 1) / most;
+        e = blocks <= most ? launch_kernel(seq_conv_bwd_kernel<T, VB, W>, dim3((unsigned)p.tblocks, blocks), dim3(BWD_LANES * BWD_ROWS), 0,
+                                           stream, false, 1, p)
+                           : launch_kernel(seq_conv_bwd_kernel<T, 1, W, true>, dim3((unsigned)p.tblocks, (single + layers - 1) / layers, layers),
+                                           dim3(BWD_LANES * BWD_ROWS), 0, stream, false, 1, p);
+    }
     if (e == cudaSuccess)
         e = launch_kernel(seq_conv_param_kernel, dim3((unsigned)((p.D + 31) / 32), (unsigned)(W + 1)), dim3(COLUMN_THREADS), 0,
                           stream, p.ax.T > 0, 1, p);

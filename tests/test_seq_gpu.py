@@ -518,3 +518,22 @@ def test_block_example_decodes_what_the_whole_sequence_gives():
     sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
     import ssm_block
     assert ssm_block.main(["--batch", "3", "--length", "40", "--width", "64", "--steps", "5"]) < 1e-2
+
+
+@pytest.mark.parametrize("bf16,D", [(False, (1 << 22) - 3), (False, 1 << 22), (True, (1 << 22) - 3), (True, 2097121)])
+def test_conv_gradients_of_the_widest_rows(bf16, D):
+    """More blocks of channels than a launch's second dimension takes."""
+    import torch
+    lens, W = [2, 1], 2
+    b = Box(D, bf16)
+    x, xe = b.normal(3, D)
+    w, we = b.normal(D, W)
+    bias, be = b.normal(D, std=0.3)
+    dy, dye = b.normal(3, D)
+    dx, dw, db = b.out(3, D), b.out(D, W, dtype=torch.float32), b.out(D, dtype=torch.float32)
+    Q.SeqConvPlan(2, 3, D, W, CONV_BF16 if bf16 else CONV_F32, direction="bwd", ragged=True).backward(
+        x, w, bias, dy, dx, dw, db, starts=starts_of(lens))
+    ref, mag = O.conv_grad(xe, we, be, lens, np.zeros((2, W - 1, D)), dye)
+    for name, v in (("dx", dx), ("dw", dw), ("dbias", db)):
+        O.check(name, host(v), ref[name], mag[name], W + 103, bf16 and name == "dx")
+    b.check_guards()
