@@ -76,26 +76,30 @@ seq_plan* new_plan(Op op, int64_t S, int64_t T, int64_t D, conv_dtype dtype, seq
 }
 
 // A tensor argument: present, aligned to its element, rows wide enough.  `wide` stays true while
-// every tensor seen has 16-byte aligned rows.
+// every tensor that the kernels read or write in groups of elements lies in 16-byte aligned rows; what they read
+// one element at a time (`Elements`: bounds, slots, parameter gradients, the scan's B and C, ...) has no part in it.
 struct Checker {
+    enum Access { Groups, Elements };
     conv_status st = CONV_OK;
     bool wide = true, words = true;      // words: 4-byte aligned rows
     void fail(conv_status s) { if (st == CONV_OK) st = s; }
-    void ptr(const void* v, size_t esize, bool needed, size_t align = 0) {
+    void ptr(const void* v, size_t esize, bool needed, Access access = Elements, size_t align = 0) {
         if (!v) {
             if (needed) fail(CONV_ERR_INVALID_ARG);
             return;
         }
         const uintptr_t a = reinterpret_cast<uintptr_t>(v);
         if (a % (align ? align : esize)) fail(CONV_ERR_ALIGNMENT);
+        if (access == Elements) return;
         if (a % 16) wide = false;
         if (a % 4) words = false;
     }
-    void rows(const void* v, int64_t ld, int64_t width, size_t esize, bool needed = true) {
-        ptr(v, esize, needed);
+    void rows(const void* v, int64_t ld, int64_t width, size_t esize, bool needed = true, Access access = Groups) {
+        ptr(v, esize, needed, access);
         if (!v) return;
         if (ld < width) fail(CONV_ERR_INVALID_ARG);
         if (ld > INT32_MAX) fail(CONV_ERR_UNSUPPORTED);      // the kernels multiply it in 32 bits by 32
+        if (access == Elements) return;
         if (((uint64_t)ld * esize) % 16) wide = false;
         if (((uint64_t)ld * esize) % 4) words = false;
     }
@@ -110,12 +114,12 @@ conv_status check_call(seq_plan_t p, const void* args, Op op, seq_direction dir)
 
 // starts goes with the plan's kind of axis; the state buffers with their slots.
 void check_states(const seq_plan* p, Checker& c, const int32_t* starts, const int32_t* slots, int64_t slot_count,
-                  const void* in, const void* out, size_t esize) {
+                  const void* in, const void* out, size_t esize, Checker::Access access) {
     if (p->ragged() ? !starts : starts != nullptr) c.fail(CONV_ERR_INVALID_ARG);
     c.ptr(starts, 4, false);
     c.ptr(slots, 4, false);
-    c.ptr(in, esize, false);
-    c.ptr(out, esize, false);
+    c.ptr(in, esize, false, access);
+    c.ptr(out, esize, false, access);
     if (slot_count > MAX_EXTENT) c.fail(CONV_ERR_UNSUPPORTED);
     if ((in || out) && (slot_count < 0 || (!slots && slot_count < p->S))) c.fail(CONV_ERR_INVALID_ARG);
 }
@@ -215,7 +219,7 @@ static conv_status conv_call(seq_plan_t p, const seq_conv_args* a, seq_direction
     c.rows(a->x, a->x_ld, p->D, e, any);
     c.ptr(a->w, e, true);
     c.ptr(a->bias, e, false);
-    check_states(p, c, a->starts, a->slots, a->slot_count, a->state_in, bwd ? nullptr : a->state_out, e);
+    check_states(p, c, a->starts, a->slots, a->slot_count, a->state_in, bwd ? nullptr : a->state_out, e, Checker::Groups);
     if (p->W == 1 && !bwd && a->state_out) c.fail(CONV_ERR_INVALID_ARG);
     if (!bwd) {
         c.rows(a->y, a->y_ld, p->D, e, any);
@@ -304,22 +308,22 @@ static conv_status scan_call(seq_plan_t p, const seq_scan_args* a, seq_direction
     const int64_t GN = (int64_t)p->G * p->N;
     c.rows(a->x, a->x_ld, p->D, e, any);
     c.rows(a->dt, a->dt_ld, p->D, e, any);
-    c.rows(a->B, a->B_ld, GN, e, any);
-    c.rows(a->C, a->C_ld, GN, e, any);
+    c.rows(a->B, a->B_ld, GN, e, any, Checker::Elements);
+    c.rows(a->C, a->C_ld, GN, e, any, Checker::Elements);
     c.rows(a->z, a->z_ld, p->D, e, false);
     c.ptr(a->A, 4, true);
     c.ptr(a->D, 4, false);
     c.ptr(a->dt_bias, 4, false);
-    check_states(p, c, a->starts, a->slots, a->slot_count, bwd && !a->h_in ? a->dh_in : a->h_in, bwd ? a->dh_out : a->h_out, 4);
-    if (dir != SEQ_STEP) c.ptr(a->saved, 4, bwd && any, 16);
+    check_states(p, c, a->starts, a->slots, a->slot_count, bwd && !a->h_in ? a->dh_in : a->h_in, bwd ? a->dh_out : a->h_out, 4, Checker::Elements);
+    if (dir != SEQ_STEP) c.ptr(a->saved, 4, bwd && any, Checker::Elements, 16);
     if (!bwd) {
         c.rows(a->y, a->y_ld, p->D, e, any);
     } else {
         c.rows(a->dy, a->dy_ld, p->D, e, any);
         c.rows(a->dx, a->dx_ld, p->D, e, any);
         c.rows(a->ddt, a->ddt_ld, p->D, e, any);
-        c.rows(a->dB, a->dB_ld, GN, e, any);
-        c.rows(a->dC, a->dC_ld, GN, e, any);
+        c.rows(a->dB, a->dB_ld, GN, e, any, Checker::Elements);
+        c.rows(a->dC, a->dC_ld, GN, e, any, Checker::Elements);
         c.rows(a->dz, a->dz_ld, p->D, e, a->z && any);
         c.ptr(a->dA, 4, true);
         c.ptr(a->dD, 4, a->D != nullptr);
@@ -408,7 +412,7 @@ static conv_status norm_call(seq_plan_t p, const seq_norm_args* a, seq_direction
     c.rows(a->x, a->x_ld, p->D, e);
     c.rows(a->gate, a->gate_ld, p->D, e, gate);
     c.rows(a->res, a->res_ld, p->D, r, residual);
-    for (const void* v : {a->w_post, a->b_post, a->scale, a->w_pre, a->b_pre}) c.ptr(v, e, false);
+    for (const void* v : {a->w_post, a->b_post, a->scale, a->w_pre, a->b_pre}) c.ptr(v, e, false, Checker::Groups);
     unwanted(a->gate, gate);
     unwanted(a->res, residual);
     unwanted(a->w_post, f & SEQ_NORM_POST);

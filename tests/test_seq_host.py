@@ -369,3 +369,34 @@ def test_python_plans_want_every_tensor_on_the_launching_gpu(lib, current):
             plan.forward(**{k: On(t, 1 - current) for k, t in args.items()})
         assert len(calls) == n + 1
         plan.close()
+
+
+def test_arguments_read_by_elements_do_not_choose_the_kernel(tmp_path):
+    """Rows in aligned groups have kernels of their own.  Only what those read or write in groups decides; bounds,
+    slots, single parameters, the scan's B and C and parameter gradients may lie at any element."""
+    import shutil
+    import subprocess
+    nvcc = shutil.which("nvcc") or "/usr/local/cuda/bin/nvcc"
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include")
+    gxx = shutil.which("g++")
+    if gxx is None or not os.path.exists(os.path.join(cuda, "cuda.h")):
+        pytest.skip("needs g++ and the CUDA headers")
+    exe = tmp_path / "seq_dispatch_check"
+    subprocess.check_call([gxx, "-O1", "-std=c++17", "-I", os.path.join(ROOT, "convolution_forward_implicit_gb300", "csrc"), "-I",
+                           os.path.join(ROOT, "include"), "-I", cuda, os.path.join(ROOT, "tests", "native", "seq_dispatch_check.cpp"), "-o", str(exe)])
+    out = subprocess.run([str(exe)], capture_output=True, text=True, timeout=60)
+    assert out.returncode == 0, out.stdout + out.stderr
+    got = {name: rest.split() for name, rest in (line.split(":") for line in out.stdout.splitlines())}
+    both = lambda *names: [v for n in names for v in (n, n + "_ld")]      # noqa: E731
+    params = ["w_post", "b_post", "scale", "w_pre", "b_pre"]
+    assert got.pop("conv_fwd 1") == both("x") + ["state_in", "state_out"] + both("y")
+    assert got.pop("conv_bwd 1") == both("x") + ["state_in"] + both("dy", "dx")
+    assert got.pop("conv_step 1") == both("x") + ["state_in", "state_out"] + both("y")
+    assert got.pop("scan_fwd 16") == both("x", "dt", "z", "y") and got.pop("scan_fwd quads 1") == ["A"]
+    assert got.pop("scan_bwd 16") == both("x", "dt", "z", "dy", "dx", "ddt", "dz") and got.pop("scan_bwd quads 1") == ["A"]
+    assert got.pop("scan_step 16") == both("x", "dt", "z", "y")
+    assert got.pop("scan_step quads 1") == ["A"] + both("B", "C") + ["h_in", "h_out"]
+    # (an fp32 residual's rows one element further are aligned to 4 bytes only)
+    assert sorted(got.pop("norm_fwd 1")) == sorted(both("x", "gate", "res", "y", "res_out") + params)
+    assert sorted(got.pop("norm_bwd 1")) == sorted(both("x", "gate", "res", "dy", "dres_out", "dx", "dgate", "dres") + params)
+    assert not got, got

@@ -143,3 +143,95 @@ def test_norm_gradients_from_two_host_threads():
     assert not errors, errors
     for (_, out), w in zip(made, want):
         assert all(torch.equal(a, b) for a, b in zip(out, w))
+
+
+# ---------------------------------------------------------------------- arguments at any place
+def shifted(t, by=1):
+    """The same values, `by` elements behind an aligned address."""
+    import torch
+    flat = torch.empty(t.numel() + by, dtype=t.dtype, device=t.device)[by:].view(t.shape)
+    flat.copy_(t)
+    return flat
+
+
+def strided(t, ld, by):
+    import torch
+    rows = torch.empty(t.shape[0], ld, dtype=t.dtype, device=t.device)[:, by:by + t.shape[1]]
+    rows.copy_(t)
+    return rows
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+def test_arguments_read_by_elements_lie_anywhere(bf16):
+    """Bounds, slots, parameters read one by one, the scan's B and C, and parameter gradients beside aligned rows: the
+    same bits wherever they lie."""
+    import torch
+    code, T, D, N, W, lens = (CONV_BF16 if bf16 else CONV_F32), 300, 256, 16, 4, [100, 0, 200]
+    g = torch.Generator(device="cuda").manual_seed(1)
+    td, f32 = torch.bfloat16 if bf16 else torch.float32, torch.float32
+    n = lambda *s, dtype=td: torch.randn(*s, generator=g, device="cuda").to(dtype)      # noqa: E731
+    o = lambda *s, dtype=td: torch.zeros(*s, dtype=dtype, device="cuda")      # noqa: E731
+    starts = torch.tensor([0, 100, 100, 300], dtype=torch.int32, device="cuda")
+    slots = torch.tensor([1, 2, 0], dtype=torch.int32, device="cuda")
+
+    def same(call, plain, moved):
+        want = [t.clone() for t in call(plain)]
+        got = call({**plain, **moved})
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+    # convolution
+    p, q = (Q.SeqConvPlan(3, T, D, W, code, d, ragged=True) for d in ("fwd", "bwd"))
+    a = dict(x=n(T, D), w=n(D, W), bias=n(D), starts=starts, slots=slots, state_in=n(3, W - 1, D))
+    more = dict(dy=n(T, D), dw=o(D, W, dtype=f32), dbias=o(D, dtype=f32))
+    moved = {k: shifted(a[k]) for k in ("w", "bias", "starts", "slots")}
+
+    def conv(t):
+        y, s = o(T, D), o(3, W - 1, D)
+        p.forward(t["x"], t["w"], t["bias"], y, starts=t["starts"], slots=t["slots"], state_in=t["state_in"], state_out=s)
+        return y, s
+
+    def conv_back(t):
+        dx = o(T, D)
+        q.backward(t["x"], t["w"], t["bias"], t["dy"], dx, t["dw"], t["dbias"], starts=t["starts"], slots=t["slots"], state_in=t["state_in"])
+        return dx, t["dw"], t["dbias"]
+
+    same(conv, a, moved)
+    same(conv_back, {**a, **more}, {**moved, "dw": shifted(more["dw"]), "dbias": shifted(more["dbias"])})
+
+    # scan
+    p, q = (Q.SeqScanPlan(3, T, D, N, code, d, ragged=True) for d in ("fwd", "bwd"))
+    a = dict(x=n(T, D), dt=n(T, D) - 1, A=-n(D, N, dtype=f32).abs(), B=n(T, N), C=n(T, N), D=n(D, dtype=f32), z=n(T, D), dt_bias=n(D, dtype=f32),
+             starts=starts, slots=slots, h_in=n(3, D, N, dtype=f32))
+    moved = {k: shifted(a[k]) for k in ("D", "dt_bias", "starts", "slots", "h_in")}
+    moved.update(B=strided(a["B"], 79 + 2 * N, 79), C=strided(a["C"], 79 + 2 * N, 79 + N))      # a projection of odd width
+    saved = q.allocate_saved()
+
+    def scan(t):
+        y, h = o(T, D), o(3, D, N, dtype=f32)
+        p.forward(t["x"], t["dt"], t["A"], t["B"], t["C"], y, D=t["D"], z=t["z"], dt_bias=t["dt_bias"], starts=t["starts"], slots=t["slots"],
+                  h_in=t["h_in"], h_out=h, saved=saved)
+        return y, h
+
+    def scan_back(t):
+        out = dict(dx=o(T, D), ddt=o(T, D), dz=o(T, D), **{k: t.get(k, v) for k, v in
+                   dict(dA=o(D, N, dtype=f32), dB=o(T, N), dC=o(T, N), dD=o(D, dtype=f32), ddt_bias=o(D, dtype=f32)).items()})
+        q.backward(t["x"], t["dt"], t["A"], t["B"], t["C"], t["dy"], saved, D=t["D"], z=t["z"], dt_bias=t["dt_bias"], starts=t["starts"],
+                   slots=t["slots"], h_in=t["h_in"], **out)
+        return tuple(out.values())
+
+    same(scan, a, moved)
+    b = {**a, "dy": n(T, D)}
+    moved.update(dA=shifted(o(D, N, dtype=f32)), dD=shifted(o(D, dtype=f32)), ddt_bias=shifted(o(D, dtype=f32)), dB=strided(o(T, N), N + 3, 3),
+                 dC=strided(o(T, N), N + 3, 1))
+    same(scan_back, b, moved)
+
+    # norm
+    q = Q.SeqNormPlan(T, D, code, "bwd", post=True)
+    a = dict(x=n(T, D), dy=n(T, D), res=n(T, D, dtype=f32), w_post=n(D), w_pre=n(D), dw_post=o(D, dtype=f32), dw_pre=o(D, dtype=f32))
+
+    def norm_back(t):
+        dx, dr = o(T, D), o(T, D, dtype=f32)
+        q.backward(t["x"], dx, dy=t["dy"], res=t["res"], w_post=t["w_post"], w_pre=t["w_pre"], dres=dr, dw_post=t["dw_post"], dw_pre=t["dw_pre"])
+        return dx, dr, t["dw_post"], t["dw_pre"]
+
+    same(norm_back, a, {k: shifted(a[k]) for k in ("dw_post", "dw_pre")})
