@@ -294,7 +294,7 @@ struct PlanChoice {
     int slab_pair = -1;    // 0 / 1: slab tile pairs off / on
     int epi_warps = 0;     // 8 or 16 epilogue warps in the per-tap kernel
     int cluster_red = -1;  // 0: split-K partials through the reduction kernel, not a cluster
-    int mc = -1;           // 0 / 1: CTA pairs sharing weight tiles by multicast off / on
+    int mc = -1;           // 0 / 1: two CTAs at a time on a weight tile off / on
     int pair = -1;         // 0 / 1: M = 256 tiles over CTA pairs (.cta_group::2 MMAs) off / on
     int ystore = -1;       // 0: per-lane stores of y even where a tensor-map (TMA) store could serve
     int slab_bw = 0;       // > 0: slab tiles this many output columns wide
@@ -324,7 +324,7 @@ struct conv_plan {
     int overlap;            // launch as programmatic dependents (conv_plan_set_overlap)
     int epi_warps;          // per-tap kernel epilogue warps (8 or 16)
     int cluster_red;        // split-K partials summed inside a cluster (no workspace, no reduce kernel)
-    int mc;                 // CTA pairs share each weight tile by multicast (units are pairs of M tiles)
+    int mc;                 // two CTAs at a time on a weight tile (units are pairs of M tiles)
     int pair;               // M = 256 tiles over CTA pairs with .cta_group::2 MMAs (units are pairs of M tiles)
     int ystore;             // the epilogue stores y with TMA boxes (tiles of one output row)
     size_t slab_smem;
@@ -761,11 +761,9 @@ static bool plan_tc(conv_plan* p, bool tf32, bool allow_slab) {
         g.K % 4 == 0 && p->ch.cluster_red != 0)
         p->cluster_red = 1;
     p->workspace_bytes = (p->splits > 1 && !p->cluster_red) ? (size_t)p->splits * g.M * g.G * g.K * sizeof(float) : 0;
-    // Weight multicast (bf16 per-tap TMA plans, N tiles of 128 or 256, no split): CTA pairs
-    // compute M tiles 2j and 2j+1 of the same (group, N tile) together and read each weight
-    // tile from L2 once per pair.  Only on request (the measured selector or CONV_FORCE_MC):
-    // measured on the 128 -> 1280 -> 1280 conv1d layers at batch 32 the pairs' lockstep costs
-    // more than the halved weight reads save (L1 105 -> 114 us, L2 309 -> 320 us).
+    // Two CTAs at a time on a weight tile (bf16 per-tap TMA plans, N tiles of 128 or 256, no
+    // split): neighbouring CTAs compute M tiles 2j and 2j+1 of the same (group, N tile), each
+    // with its own copy of the weights.  Only on request (CONV_FORCE_MC or a loaded table).
     // CTA pairs with M = 256 MMAs (tc_pair.cu): bf16 per-tap TMA plans with N tiles of 128 or
     // 256, no split and long reductions (8 epilogue warps), when the pairs' units fill every
     // pair of SMs at least once.  Each SM then stores and reads half of every weight tile
@@ -872,17 +870,11 @@ static bool plan_tc(conv_plan* p, bool tf32, bool allow_slab) {
     p->mc = 0;
     if (!tf32 && p->tma && !p->slab && p->splits == 1 && !p->cluster_red && bn >= 128 && p->num_mt >= 2 &&
         !p->pair && p->ch.mc == 1) {
-        int clusters = p->sm_count / 2;
-        int dev = 0;
-        if (cudaGetDevice(&dev) == cudaSuccess) {
-            const int n = tc_mc_max_clusters(bn, p->epi_warps);
-            if (n > 0) clusters = std::min(clusters, n);
-        }
-        cudaGetLastError();
-        if (clusters >= 1) {
+        const int pairs = p->sm_count / 2;
+        if (pairs >= 1) {
             p->mc = 1;
             p->total_units = (int)(cdiv(p->num_mt, 2) * g.G * p->num_nt);
-            p->grid = 2 * std::min(p->total_units, clusters);
+            p->grid = 2 * std::min(p->total_units, pairs);
         }
     }
     // Epilogue stores through a tensor map of y (bf16 per-tap plans, no split, tiles of one output
@@ -1034,8 +1026,8 @@ static void tune_table_lookup(const conv_plan* p, PlanChoice& c) {
 }
 
 // The candidates the selector times: the rules' own plan, each N tile x split factor x
-// gather mode, CTA pairs and weight multicast for wide tiles, slab units of one or two
-// accumulators on one CTA or a pair for narrow ones, and the FFMA kernel; candidates that land
+// gather mode, CTA pairs for wide tiles, slab units of one or two accumulators on one CTA or a
+// pair for narrow ones, and the FFMA kernel; candidates that land
 // on the same plan are timed once.
 static std::vector<conv_plan> tune_candidates(const conv_plan* p) {
     std::vector<PlanChoice> cs;
@@ -1047,12 +1039,11 @@ static std::vector<conv_plan> tune_candidates(const conv_plan* p) {
                 c.bn = bn; c.splits = sp; c.gather = ga;
                 cs.push_back(c);
             }
-    for (int bn : {128, 256}) {    // wide unsplit tiles: one CTA, CTA pairs, or weight multicast
+    for (int bn : {128, 256}) {    // wide unsplit tiles: one CTA or CTA pairs
         PlanChoice c;
         c.bn = bn; c.splits = 1;
         c.pair = 0; cs.push_back(c);
         c.pair = 1; cs.push_back(c);
-        c.pair = 0; c.mc = 1; cs.push_back(c);
     }
     for (int bn : {32, 64})        // slab units of one or two accumulators, on one CTA or a pair
         for (int tp : {0, 1})

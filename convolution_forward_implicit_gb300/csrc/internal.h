@@ -159,8 +159,8 @@ struct TcParams {
     int epi_warps;          // per-tap kernel: 8 or 16 epilogue warps
     int cluster_red;        // 1: the splits of a tile run as one cluster and sum their partial
                             // accumulators through distributed shared memory (no workspace)
-    int mc;                 // 1 (per-tap bf16 TMA kernel, no split): CTA pairs share each weight tile
-                            // by multicast; units are pairs of M tiles (see conv_fwd_tc_kernel)
+    int mc;                 // 1 (per-tap bf16 TMA kernel, no split): two CTAs work on each weight tile at
+                            // the same time; units are pairs of M tiles (see conv_fwd_tc_kernel)
     int ystore;             // 1: the epilogue stores y through a tensor map (TMA), one 64-channel x
                             // 32-pixel box per warp and chunk (tiles of one output row, BW % 32 == 0)
     Lattice lat;            // where the output pixels land in y (one phase of a strided backward data)
@@ -184,9 +184,6 @@ __host__ __device__ constexpr int tc_store_cols(int bn, int ew, bool pair) {
 cudaError_t launch_tc(const TcParams& p, const CUtensorMap* act_map, const CUtensorMap* y_map, int stages, int grid,
                       cudaStream_t stream);
 int tc_stages_for(int BN, int tf32, int epi_warps);
-// Clusters of two CTAs of the weight-multicast kernel for (BN, epi_warps) that can be resident at
-// once on the current device (0 if it cannot be queried).
-int tc_mc_max_clusters(int BN, int epi_warps);
 // CTA-pair kernel (tc_pair.cu): M = 256 tiles over two CTAs with .cta_group::2 MMAs; bf16 per-tap
 // TMA plans without a split.  w_map: the packed weights as 2-D rows of 128 bytes, boxes of BN/2 rows.
 cudaError_t launch_pair(const TcParams& p, const CUtensorMap* act_map, const CUtensorMap* w_map,

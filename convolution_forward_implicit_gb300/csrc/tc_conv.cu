@@ -90,18 +90,16 @@ struct Smem {
     static constexpr size_t TOTAL = 1024 + RING + STG + BIAS_BYTES + BARS;
 };
 
-// MC: the CTAs run as clusters of two that compute the tiles 2j and 2j+1 along M of the same
-// (group, N tile) in lockstep; each loads one half of every weight tile and multicasts it to
-// both, so the pair reads each weight tile from L2 once instead of twice.  A stage is then
-// refilled only after the MMAs of both CTAs have released it (each CTA's commits arrive on
-// the empty barriers of both).
+// MC: the CTAs 2j and 2j+1 of the grid compute the tiles 2i and 2i+1 along M of the same (group,
+// N tile) at the same time, so that the second read of each weight tile finds it in L2.  Each
+// loads its tiles itself and waits for nothing of the other.
 template <int BN, int STAGES, int KIND, int EW, bool MC>
 __global__ void __launch_bounds__(Traits<KIND, EW>::THREADS, 1)
     conv_fwd_tc_kernel(const __grid_constant__ TcParams p, const __grid_constant__ CUtensorMap act_map,
                        const __grid_constant__ CUtensorMap y_map) {
     using C = Cfg<BN, KIND>;
     using T = Traits<KIND, EW>;
-    static_assert(!MC || KIND == KIND_BF16_TMA, "weight multicast is built for the bf16 TMA kernel");
+    static_assert(!MC || KIND == KIND_BF16_TMA, "pairs of tiles are built for the bf16 TMA kernel");
     constexpr int RED_PITCH = BN + 4;   // floats per row of the cluster-reduction buffer
     static_assert((size_t)BM * RED_PITCH * 4 <= (size_t)STAGES * (T::A_STAGE + C::B_STAGE),
                   "the cluster-reduction buffer reuses the stage area");
@@ -131,7 +129,7 @@ __global__ void __launch_bounds__(Traits<KIND, EW>::THREADS, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(full_bar(s), T::FULL_COUNT);
-            mbar_init(empty_bar(s), MC ? 2 : 1);
+            mbar_init(empty_bar(s), 1);
             mbar_init(cvt_bar(s), T::CVT_WARPS > 0 ? T::CVT_WARPS : 1);
         }
         for (int a = 0; a < 2; ++a) {
@@ -153,17 +151,15 @@ __global__ void __launch_bounds__(Traits<KIND, EW>::THREADS, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
-    // the peer CTA's copies and commits reach this CTA's barriers only after both are set up
-    if (MC) cluster_sync_all();
     // set up: the next kernel on the stream may start (its own set-up and weight loads)
     if (p.pdl) griddep_launch();
 
     const Geom& g = p.g;
     const int GC = g.G * g.C;
     const int GK = g.G * g.K;
-    // units of this CTA: u0, u0 + ustep, ...; with MC a unit is a pair of M tiles (the CTA of
-    // cluster rank r takes tile 2 mt + r of it)
-    const uint32_t crank = MC ? cluster_ctarank() : 0u;
+    // units of this CTA: u0, u0 + ustep, ...; with MC a unit is a pair of M tiles (CTA 2j + r
+    // takes tile 2 mt + r of it)
+    const uint32_t crank = MC ? blockIdx.x & 1u : 0u;
     const int u0 = MC ? (int)(blockIdx.x >> 1) : (int)blockIdx.x;
     const int ustep = MC ? (int)(gridDim.x >> 1) : (int)gridDim.x;
     auto unit_tile = [&](int u, int& mt, int& gi, int& nt, int& split) {
@@ -248,25 +244,9 @@ __global__ void __launch_bounds__(Traits<KIND, EW>::THREADS, 1)
                                 tma_load_5d(sA + s * T::A_STAGE, &act_map, c0, gi, wi, hi, to.n, full_bar(s));
                         } else {
                             const size_t off = ((size_t)(gi * p.num_nt + nt) * p.nkb + kb) * C::B_STAGE;
-                            if (MC) {
-                                // this CTA's half of the weight tile (BN/2 rows), to both CTAs
-                                constexpr uint32_t HALF = C::B_STAGE / 2;
-                                bulk_g2s_multicast(sB + s * C::B_STAGE + crank * HALF, wp + off + crank * HALF, HALF,
-                                                   full_bar(s), (uint16_t)0x3);
-                            } else {
-                                bulk_g2s(sB + s * C::B_STAGE, wp + off, C::B_STAGE, full_bar(s));
-                            }
+                            bulk_g2s(sB + s * C::B_STAGE, wp + off, C::B_STAGE, full_bar(s));
                         }
                     }
-                }
-                if (MC && lane == 0) {
-                    // before the CTA may exit, every commit the peer's MMA role sends to this CTA's
-                    // empty barriers must have arrived: wait (bounded) for the phases that would
-                    // precede this warp's next STAGES refills
-                    for (uint32_t k = it; k < it + (uint32_t)STAGES; ++k)
-                        if ((int)((k % STAGES) % T::PROD_WARPS) == pw &&
-                            !wait_bar(empty_bar(k % STAGES), ((k / STAGES) & 1u) ^ 1u, abort_flag, p.err, false))
-                            break;
                 }
                 if (aborted && lane == 0) {
                     // before the CTA exits, the copies this warp issued into stages the MMA role never
@@ -400,8 +380,7 @@ __global__ void __launch_bounds__(Traits<KIND, EW>::THREADS, 1)
                     } else {
                         mma_bf16_k4(d_tmem, ad, bd, IDESC, kb > kb0 ? 1u : 0u);   // 4 x K=16 = one 128-byte row
                     }
-                    if (MC) mma_commit_multicast(empty_bar(s), (uint16_t)0x3);   // both CTAs' copy of the stage
-                    else mma_commit(empty_bar(s));
+                    mma_commit(empty_bar(s));
                 }
                 if (!aborted) mma_commit(tfull_bar(acc));
             }
@@ -622,8 +601,6 @@ __global__ void __launch_bounds__(Traits<KIND, EW>::THREADS, 1)
 
     tc_fence_before();
     __syncthreads();
-    // no CTA of a pair leaves while the other may still copy into or arrive on its shared memory
-    if (MC) cluster_sync_all();
     if (warp == T::MMA_WARP) {
         tc_fence_after();
         tmem_dealloc(tmem_base, C::TMEM_COLS);
@@ -654,7 +631,7 @@ cudaError_t launch_one(const TcParams& p, const CUtensorMap& map, const CUtensor
         if (dev >= 0 && dev < 64) attr_set[dev] = true;
     }
     return launch_kernel(kern, dim3(grid), dim3(Traits<KIND, EW>::THREADS), smem, stream, p.pdl != 0,
-                         MC ? 2 : p.cluster_red ? p.splits : 1, p, map, ymap);
+                         p.cluster_red ? p.splits : 1, p, map, ymap);
 }
 
 }  // namespace
@@ -663,7 +640,7 @@ cudaError_t launch_one(const TcParams& p, const CUtensorMap& map, const CUtensor
 #define TC_BF16_CONFIGS(X) X(256, 4) X(128, 6) X(64, 8) X(32, 8) X(16, 8)
 #define TC_BF16_EPI16_CONFIGS(X) X(256, 3) X(128, 5)
 #define TC_TF32_CONFIGS(X) X(256, 2) X(128, 3) X(64, 4) X(32, 4) X(16, 5)
-// weight multicast (bf16, 8 or 16 epilogue warps at the stage counts above)
+// pairs of CTAs on one weight tile (bf16, 8 or 16 epilogue warps at the stage counts above)
 #define TC_BF16_MC_CONFIGS(X) X(256, 4, 8) X(128, 6, 8) X(256, 3, 16) X(128, 5, 16)
 
 int tc_stages_for(int BN, int tf32, int epi_warps) {
@@ -671,40 +648,6 @@ int tc_stages_for(int BN, int tf32, int epi_warps) {
     if (tf32) { TC_TF32_CONFIGS(X) }
     else if (epi_warps == 16) { TC_BF16_EPI16_CONFIGS(X) }
     else { TC_BF16_CONFIGS(X) }
-#undef X
-    return 0;
-}
-
-int tc_mc_max_clusters(int BN, int epi_warps) {
-    const int st = tc_stages_for(BN, 0, epi_warps);
-    auto query = [&](auto kern, size_t smem, int threads) -> int {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
-            cudaGetLastError();
-            return 0;
-        }
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(2);
-        cfg.blockDim = dim3(threads);
-        cfg.dynamicSmemBytes = smem;
-        cudaLaunchAttribute attr;
-        attr.id = cudaLaunchAttributeClusterDimension;
-        attr.val.clusterDim.x = 2;
-        attr.val.clusterDim.y = 1;
-        attr.val.clusterDim.z = 1;
-        cfg.attrs = &attr;
-        cfg.numAttrs = 1;
-        int n = 0;
-        if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
-            cudaGetLastError();
-            return 0;
-        }
-        return n;
-    };
-#define X(bn, stg, ew)                                                                                  \
-    if (BN == bn && st == stg && epi_warps == ew)                                                       \
-        return query(conv_fwd_tc_kernel<bn, stg, KIND_BF16_TMA, ew, true>, smem_bytes_for<bn, stg, KIND_BF16_TMA, ew>(), \
-                     Traits<KIND_BF16_TMA, ew>::THREADS);
-    TC_BF16_MC_CONFIGS(X)
 #undef X
     return 0;
 }

@@ -168,3 +168,17 @@ def test_tensor_core_plan_units_match_their_tiles(lib, monkeypatch):
             assert grid <= units, where
         checked += 1
     assert checked > 600
+
+
+def test_no_bulk_load_goes_to_several_ctas():
+    """The library also runs as a replica on each of several GPUs, where bulk loads with a cluster multicast have no
+    place; the tensor cores' commits, which only arrive on barriers, may name several CTAs."""
+    import glob
+    import os
+    import re
+    root = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "convolution_forward_implicit_gb300", "csrc")
+    files = [f for f in glob.glob(os.path.join(root, "*")) if os.path.isfile(f)]
+    assert files
+    for f in files:
+        text = re.sub(r'"\s*"', "", open(f).read())        # one string of each instruction's lines
+        assert not re.search(r"cp\.async\.bulk[^\"]*multicast", text), f
