@@ -16,7 +16,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) seq_norm_fwd_kernel(c
     const int D = row < p.rows ? p.D : 0;            // a row behind the last one has no columns
     const bool layer = p.flags & SEQ_NORM_LAYER, gate = p.flags & (SEQ_NORM_GATE_BEFORE | SEQ_NORM_GATE_AFTER);
     const bool residual = p.flags & SEQ_NORM_RESIDUAL;
-    // all of the row is on its way before the first sum
+    // all of the row is on its way before the first sum (a thread stores the residual's columns that it has loaded
+    // itself, so that res_out may be res)
     RowIn<T, WIDE, UPT> x_in, g_in;
     RowIn<RT, WIDE, UPT> r_in;
     x_in.load(p.x, row * p.x_ld, D);

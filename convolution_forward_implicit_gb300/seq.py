@@ -408,7 +408,8 @@ class SeqScanPlan(_SeqPlan):
 class SeqNormPlan(_SeqPlan):
     """Norm, gate and residual around a block on rows of D values (seq_norm_*): see include/seq.h
     for the formulas.  kind is SEQ_NORM_RMS or SEQ_NORM_LAYER, gate SEQ_GATE_NONE, SEQ_GATE_BEFORE or
-    SEQ_GATE_AFTER (the POST norm).  The residual stream has the type res_dtype."""
+    SEQ_GATE_AFTER (the POST norm).  The residual stream has the type res_dtype; `forward` may update it in place
+    (res_out=res)."""
 
     _fields = NORM_FIELDS
     _names = {"fwd": "seq_norm_fwd", "bwd": "seq_norm_bwd"}

@@ -8,7 +8,8 @@ training step's gradients.
     y                = scan(x, dt, A, B, C, D) * silu(z)          seq_scan
     block            = out-projection(y)                          1x1 convolution
 
-Dense projections are 1x1 convolutions (conv1d with one tap), so every step runs in the library.
+Dense projections are 1x1 convolutions (conv1d with one tap), so all arithmetic runs in the library.  They
+take whole rows: the columns of dt_low, a slice of x's projection, are copied before theirs.
 
     python examples/ssm_block.py [--batch 4] [--length 512] [--width 384] [--steps 16]
 """

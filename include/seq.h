@@ -15,7 +15,8 @@
  * elements, at least the row's width, at most 2^31 - 1) lets a call read a slice of a wider
  * projection.  Offsets are 64-bit.  Pointers need the alignment of their element only; rows that are
  * 16-byte aligned (pointer and ld) are read with wide loads.  Inputs and outputs do not
- * overlap, except that the state a call leaves may be the buffer it starts from.
+ * overlap, except that the state a call leaves may be the buffer it starts from, and that
+ * seq_norm_fwd may update the residual stream in place (res_out = res, with the same ld).
  *
  * States.  Sequence s starts from row slots[s] of the state buffers, or row s when slots is
  * NULL; a slot outside 0 .. slot_count-1 names no state: that sequence starts from zero and

@@ -537,3 +537,29 @@ def test_conv_gradients_of_the_widest_rows(bf16, D):
     for name, v in (("dx", dx), ("dw", dw), ("dbias", db)):
         O.check(name, host(v), ref[name], mag[name], W + 103, bf16 and name == "dx")
     b.check_guards()
+
+
+@pytest.mark.parametrize("types", ["f32", "bf16", "bf16/f32"])
+@pytest.mark.parametrize("rows,D,pad", [(1, 1, 0), (7, 13, 2), (9, 40, 0), (70, 384, 8), (700, 1288, 0), (9, 4096, 0), (700, 4096, 0), (3, 9001, 0),
+                                        (2, 16384, 8)])
+def test_norm_updates_the_residual_in_place(types, rows, D, pad):
+    """res_out = res: the same bits as with a buffer of its own, behind the same rows, whatever else the call does."""
+    import torch
+    bf16, rt = types != "f32", torch.bfloat16 if types == "bf16" else torch.float32
+    b = Box(rows + D, bf16)
+    code, rcode = CONV_BF16 if bf16 else CONV_F32, CONV_BF16 if types == "bf16" else CONV_F32
+    x, gate = b.normal(rows, D, pad=pad)[0], b.normal(rows, D, pad=pad)[0]
+    w = {k: b.normal(D)[0] for k in ("w_post", "b_post", "scale", "w_pre", "b_pre")}
+    res = b.out(rows, D, dtype=rt, pad=pad)
+    first = b.put(b.rng.standard_normal((rows, D)), dtype=rt)[0]
+    for kind in ("rms", "layer"):
+        for post, pre in ((True, True), (False, True), (True, False)):
+            p = Q.SeqNormPlan(rows, D, code, res_dtype=rcode, kind=kind, post=post, pre=pre, gate="before")
+            args = {k: v for k, v in w.items() if not (k.endswith("post") and not post) and not (k.endswith("pre") and not pre)}
+            res.copy_(first)
+            y, ro = (b.out(rows, D, pad=pad) if pre else None), b.out(rows, D, dtype=rt, pad=pad)
+            p.forward(x, y=y, gate=gate, res=res, res_out=ro, **args)
+            y2 = b.out(rows, D, pad=pad) if pre else None
+            p.forward(x, y=y2, gate=gate, res=res, res_out=res, **args)
+            assert torch.equal(res, ro) and (not pre or torch.equal(y, y2))
+    b.check_guards()
