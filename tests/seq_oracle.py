@@ -230,3 +230,74 @@ def check(name, got, ref, mag, k, bf16):
         i = np.unravel_index(np.argmax(np.where(bad, np.abs(got - ref) / tol, 0)), ref.shape)
         raise AssertionError(f"{name}: {int(bad.sum())}/{ref.size} outside the bound; worst at {i}: got {got[i]!r}, "
                              f"64 bits {ref[i]!r}, tolerance {tol[i]!r}")
+
+
+# ------------------------------------------------------------------- cases of long memory
+def slow_case(rng, lens, D, N):
+    """Inputs of a scan whose states remember thousands of tokens: steps of 1e-3 to 1e-2 and A of -1 to -0.05.  x is zero
+    but at a sequence's beginning and a few tokens, dy but at its end and a few: what reaches the others comes a
+    long way.  For softplus without a bias."""
+    T, S = sum(lens), len(lens)
+    x, dy = rng.standard_normal((T, D)), rng.standard_normal((T, D))
+    keep = np.zeros(T, bool), np.zeros(T, bool)
+    for a, b in bounds(lens):
+        keep[0][a:min(a + 40, b)] = True
+        keep[1][max(b - 40, a):b] = True
+        keep[0][a + 499:b:997] = True
+        keep[1][a + 250:b:997] = True
+    x[~keep[0]] = 0
+    dy[~keep[1]] = 0
+    step = np.exp(rng.uniform(np.log(1e-3), np.log(1e-2), (T, D)))
+    return dict(x=x, dt=np.log(np.expm1(step)), A=-rng.uniform(0.05, 1, (D, N)), B=rng.standard_normal((T, N)), C=rng.standard_normal((T, N)),
+                D=rng.standard_normal(D)), dict(h=rng.standard_normal((S, D, N)), dy=dy, dh=rng.standard_normal((S, D, N)))
+
+
+def scan_in_pieces(x, dt, A, B, C, D, lens, h0, piece, parts, fault=None):
+    """y and the states left (one group, softplus, no gate) as the library forms them: every piece of `piece` tokens
+    from a zero state, the pieces' results joined in `parts` parts, every piece again from the state before it.
+    `fault` plants a mistake in the joining."""
+    T, W = x.shape
+    delta = softplus(dt)
+    a, add = np.exp(delta[:, :, None] * A), (delta * x)[:, :, None] * B[:, None]
+    begin = {i: s for s, (i, j) in enumerate(bounds(lens)) if j > i}
+    end = {j - 1: s for s, (i, j) in enumerate(bounds(lens)) if j > i}
+    count = (T + piece - 1) // piece
+    e, total, cut = [], [], []
+    for r in range(count):
+        h, t_sum, stop = np.zeros((W, A.shape[1])), np.zeros(W), False
+        for t in range(r * piece, min(T, (r + 1) * piece)):
+            if t in begin:
+                h, t_sum, stop = h0[begin[t]], np.zeros(W), True
+            h, t_sum = a[t] * h + add[t], t_sum + delta[t]
+        e.append(h), total.append(t_sum), cut.append(stop)
+
+    def step(c, e, total, stop):
+        return e if stop and fault != "ends of sequences" else e + np.exp(total[:, None] * A) * c
+
+    length = -(-count // parts)
+    before, result = [], []
+    for q in range(parts):
+        rs = range(q * length, min(count, (q + 1) * length))
+        c, t_sum, stop = np.zeros_like(e[0]), np.zeros(W), False
+        for r in rs:
+            c, t_sum, stop = step(c, e[r], total[r], cut[r]), np.zeros(W) if cut[r] else t_sum + total[r], stop or cut[r]
+        result.append((c, t_sum, stop))
+        c = np.zeros_like(e[0])
+        for k in range(q):
+            if fault == "parts before" or (fault == "older parts" and k < q - 1):
+                continue
+            c = step(c, result[k][0], result[k][1] * (fault != "decay over a part"), result[k][2])
+        for r in rs:
+            before.append(c)
+            c = step(c, e[r], total[r], cut[r])
+    y, left = np.zeros_like(x), h0.copy()
+    for r in range(count):
+        h = before[r]
+        for t in range(r * piece, min(T, (r + 1) * piece)):
+            if t in begin:
+                h = h0[begin[t]]
+            h = a[t] * h + add[t]
+            y[t] = (h * C[t]).sum(-1) + D * x[t]
+            if t in end:
+                left[end[t]] = h
+    return y, left

@@ -563,3 +563,205 @@ def test_norm_updates_the_residual_in_place(types, rows, D, pad):
             p.forward(x, y=y2, gate=gate, res=res, res_out=res, **args)
             assert torch.equal(res, ro) and (not pre or torch.equal(y, y2))
     b.check_guards()
+
+
+LONG = [([600], False), ([1300], False), ([300, 1200], True), ([4100], False), ([2300, 2300], False), ([1, 900, 0, 2100, 33, 777, 8, 450], True)]
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("lens,ragged", LONG)
+@pytest.mark.parametrize("D,N,pad", [(40, 16, 0), (17, 5, 1)])
+def test_scan_of_long_memory(bf16, lens, ragged, D, N, pad):
+    """States that keep half of what they held through every part of the pieces' joining, and inputs that are zero in
+    most tokens: outputs, states and gradients come a long way (wrong joins leave these bounds, see the host tests)."""
+    import torch
+    S, T, f32 = len(lens), sum(lens), torch.float32
+    b = Box(T + D, bf16)
+    a, more = O.slow_case(b.rng, lens, D, N)
+    dev, ex = {}, {}
+    for name, v in a.items():
+        one = name in ("A", "D")
+        dev[name], ex[name] = b.put(v, dtype=f32 if one else None, pad=0 if one else pad)
+    h, he = b.put(more["h"], dtype=f32)
+    dh, dhe = b.put(more["dh"], dtype=f32)
+    dy, dye = b.put(more["dy"], pad=pad)
+    ref, mag = O.scan(**ex, G=1, lens=lens, h0=he, dy=dye, dh_out=dhe)
+    k = 4 * max(lens) + N + 100
+    code, starts = CONV_BF16 if bf16 else CONV_F32, starts_of(lens) if ragged else None
+    arr = [dev[n] for n in ("x", "dt", "A", "B", "C")]
+    p, q = (Q.SeqScanPlan(S, T, D, N, code, direction=d, ragged=ragged) for d in ("fwd", "bwd"))
+    for plan in (p, q):
+        pieces = int(plan.describe().split("pieces=")[1].split()[0])
+        assert 16 < pieces / (1 if ragged else S) <= 128
+    y, saved, left = b.out(T, D, pad=pad), q.allocate_saved(), b.out(S, D, N, dtype=f32)
+    p.forward(*arr, y, D=dev["D"], starts=starts, h_in=h, h_out=left, saved=saved)
+    O.check("y", host(y), ref["y"], mag["y"], k, bf16)
+    O.check("h", host(left), ref["h"], mag["h"], k, False)
+    out = dict(dx=(T, D), ddt=(T, D), dA=(D, N), dB=(T, N), dC=(T, N), dD=(D,), dh_in=(S, D, N))
+    g = {n: b.out(*s, dtype=f32 if n in ("dA", "dD", "dh_in") else None, pad=pad if n in ("dx", "ddt", "dB", "dC") else 0) for n, s in out.items()}
+    q.backward(*arr, dy, saved, D=dev["D"], starts=starts, h_in=h, dh_out=dh, **g)
+    for n, v in g.items():
+        O.check(n, host(v), ref[n], mag[n], 2 * k + (T if n in ("dA", "dD") else D if n in ("dB", "dC") else 0), v.dtype == torch.bfloat16)
+    b.check_guards()
+
+
+# --------------------------------------------------------------------------------- rounding
+def test_bf16_outputs_are_rounded_to_nearest_even():
+    """Sums of two bf16 numbers on one grid of 2^-7 and products of two are exact in fp32: what is written is them
+    rounded once, many of the sums halfway between two bf16 numbers."""
+    import torch
+    rng = np.random.default_rng(6)
+    T, D = 96, 72
+    grid = lambda *s: torch.from_numpy(rng.integers(-255, 256, s).astype(np.float32) * 2.0 ** -7)      # noqa: E731
+    bf = lambda t: t.to(torch.bfloat16)      # noqa: E731   (nearest, ties to even)
+    gpu = lambda t: bf(t).cuda()      # noqa: E731
+    out = lambda *s, dtype=torch.bfloat16: torch.empty(*s, dtype=dtype, device="cuda")      # noqa: E731
+    x, r, dy = grid(T, D), grid(T, D), grid(T, D)
+    late = lambda v: torch.cat([v[1:], torch.zeros(1, D)])      # noqa: E731
+    early = lambda v: torch.cat([torch.zeros(1, D), v[:-1]])      # noqa: E731
+    ties = (bf(x + early(x)).float() != x + early(x)).float().mean()
+    assert ties > 0.1
+    # convolution with taps of one, without activation: forward, gradient, steps
+    w = torch.ones(D, 2)
+    y, dx = out(T, D), out(T, D)
+    Q.SeqConvPlan(1, T, D, 2, CONV_BF16, silu=False).forward(gpu(x), gpu(w), None, y)
+    assert torch.equal(y.cpu(), bf(x + early(x)))
+    q = Q.SeqConvPlan(1, T, D, 2, CONV_BF16, direction="bwd", silu=False)
+    q.backward(gpu(x), gpu(w), None, gpu(dy), dx, out(D, 2, dtype=torch.float32), None)
+    assert torch.equal(dx.cpu(), bf(dy + late(dy)))
+    state = gpu(r).view(T, 1, D)
+    Q.SeqConvPlan(T, T, D, 2, CONV_BF16, direction="step", silu=False).step(gpu(x), gpu(w), None, state, state, y)
+    assert torch.equal(y.cpu(), bf(x + r)) and torch.equal(state.cpu().view(T, D), bf(x))
+    # the residual
+    ro = out(T, D)
+    Q.SeqNormPlan(T, D, CONV_BF16, res_dtype=CONV_BF16).forward(gpu(x), y=y, res=gpu(r), res_out=ro)
+    assert torch.equal(ro.cpu(), bf(x + r))
+    # scan with steps of zero and no states: the skip connection alone, y = D x and dx = D dy
+    Dv = torch.from_numpy(rng.integers(129, 256, D).astype(np.float32) * 2.0 ** -7)
+    zero = torch.zeros(T, D, dtype=torch.bfloat16, device="cuda")
+    A, B = -torch.ones(D, 16, device="cuda"), gpu(grid(T, 16))
+    for S in (1, 12):
+        p, q = (Q.SeqScanPlan(S, T, D, 16, CONV_BF16, direction=d, softplus=False) for d in ("fwd", "bwd"))
+        saved = q.allocate_saved()
+        p.forward(gpu(x), zero, A, B, B, y, D=Dv.cuda(), saved=saved)
+        assert torch.equal(y.cpu(), bf(Dv * x))
+        q.backward(gpu(x), zero, A, B, B, gpu(dy), saved, dx, out(T, D), out(D, 16, dtype=torch.float32), out(T, 16), out(T, 16), D=Dv.cuda(),
+                   dD=out(D, dtype=torch.float32))
+        assert torch.equal(dx.cpu(), bf(Dv * dy))
+    h = torch.zeros(T, D, 16, device="cuda")
+    Q.SeqScanPlan(T, T, D, 16, CONV_BF16, direction="step", softplus=False).step(gpu(x), zero, A, B, B, h, h, y, D=Dv.cuda())
+    assert torch.equal(y.cpu(), bf(Dv * x))
+
+
+# ----------------------------------------------------------------------- one column, bad values
+@pytest.mark.parametrize("types", ["f32", "bf16", "bf16/f32"])
+@pytest.mark.parametrize("rows", [1, 5, 611])
+def test_layer_norm_of_one_column(types, rows):
+    """A column less its mean is zero: what is behind the norm is its bias, and nothing of a gradient passes it."""
+    import torch
+    bf16, rt = types != "f32", torch.bfloat16 if types == "bf16" else torch.float32
+    b = Box(rows, bf16)
+    f32 = torch.float32
+    code, rcode = CONV_BF16 if bf16 else CONV_F32, CONV_BF16 if types == "bf16" else CONV_F32
+    x = b.normal(rows, 1)[0]
+    (scale, se), (w, _), (wp, _), (bias, be), (bp, bpe) = (b.normal(1) for _ in range(5))
+    (res, re_), (dro, droe), (dy, dye) = b.normal(rows, 1, dtype=rt), b.normal(rows, 1, dtype=rt), b.normal(rows, 1)
+    kw = dict(res_dtype=rcode, kind="layer", post=True, pre=True, eps=1e-3)
+    args = dict(w_post=wp, b_post=bp, scale=scale, res=res, w_pre=w, b_pre=bias)
+    y, ro = b.out(rows, 1), b.out(rows, 1, dtype=rt)
+    Q.SeqNormPlan(rows, 1, code, **kw).forward(x, y=y, res_out=ro, **args)
+    assert np.array_equal(host(y), np.broadcast_to(be, (rows, 1)))
+    O.check("res_out", host(ro), re_ + se * bpe, np.abs(re_) + np.abs(se * bpe), 4, rt == torch.bfloat16)
+    g = {n: b.out(1, dtype=f32) for n in ("dw_post", "db_post", "dscale", "dw_pre", "db_pre")}
+    dx, dr = b.out(rows, 1), b.out(rows, 1, dtype=rt)
+    Q.SeqNormPlan(rows, 1, code, direction="bwd", **kw).backward(x, dx, dy=dy, dres_out=dro, dres=dr, **args, **g)
+    assert not host(dx).any() and not host(g["dw_post"]).any() and not host(g["dw_pre"]).any()
+    assert np.array_equal(host(dr), droe)
+    for n, terms in (("db_post", droe * se), ("dscale", droe * bpe), ("db_pre", dye)):
+        O.check(n, host(g[n]), terms.sum(0), np.abs(terms).sum(0), rows + 4, False)
+    b.check_guards()
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("lens,ragged", [([9, 3, 40, 0, 1, 700, 60], True), ([70] * 7, False), ([1] * 9, False), ([5] * 40, True)])
+@pytest.mark.parametrize("D,pad", [(40, 0), (17, 1)])
+def test_bad_values_stay_in_their_sequence(bf16, lens, ragged, D, pad):
+    """Infinities and NaN in some sequences, in every input and state: the others' results have the bits that they have
+    without them, and in the convolution and the scan so have the tokens before the first bad one."""
+    import torch
+    S, T, N, W = len(lens), sum(lens), 16, 4
+    c = scan_case(T + D, bf16, lens, D, N, 1, pad=pad)
+    b, dev, f32 = c["box"], c["dev"], torch.float32
+    code, starts = CONV_BF16 if bf16 else CONV_F32, starts_of(lens) if ragged else None
+    dev["dy"], dev["w"], dev["cbias"] = b.normal(T, D, pad=pad)[0], b.normal(D, W)[0], b.normal(D)[0]
+    dev["h"], dev["dh"] = b.normal(S, D, N, dtype=f32)[0], b.normal(S, D, N, dtype=f32)[0]
+    dev["cs"] = b.normal(S, W - 1, D)[0]
+    bounds = O.bounds(lens)
+    bad = [s for s in range(1, S, 2) if lens[s]]
+    at = {s: bounds[s][0] + lens[s] // 2 for s in bad}           # the first bad token
+    ok = np.ones(T, bool)
+    before = np.ones(T, bool)
+    for s in bad:
+        ok[bounds[s][0]:bounds[s][1]] = False
+        before[at[s]:bounds[s][1]] = False
+    good_s = [s for s in range(S) if s not in bad]
+    spoiled = {k: v.clone() for k, v in dev.items()}
+    for i, s in enumerate(bad):
+        for j, n in enumerate(("x", "dt", "B", "C", "z", "dy")):
+            v = spoiled[n][at[s]:bounds[s][1]]
+            v[:, (i + j) % 3::3] = (float("nan"), float("inf"), -float("inf"))[(i + j) % 3]
+    states_spoiled = {k: spoiled[k].clone() for k in ("h", "dh", "cs")}
+    for s in bad:
+        for v in states_spoiled.values():
+            v[s, ..., ::2] = float("nan")
+    conv, conv_b = (Q.SeqConvPlan(S, T, D, W, code, direction=d, ragged=ragged) for d in ("fwd", "bwd"))
+    scan, scan_b = (Q.SeqScanPlan(S, T, D, N, code, direction=d, ragged=ragged) for d in ("fwd", "bwd"))
+    o = lambda *s, dtype=None: torch.zeros(*s, dtype=dtype or c["box"].t, device="cuda")      # noqa: E731
+
+    def run(t):
+        r = {n: o(T, D) for n in ("y", "dx", "sy", "sdx", "ddt", "dz")}
+        r.update(dB=o(T, N), dC=o(T, N), cs=o(S, W - 1, D), h=o(S, D, N, dtype=f32), dh=o(S, D, N, dtype=f32))
+        conv.forward(t["x"], t["w"], t["cbias"], r["y"], starts=starts, state_in=t["cs"], state_out=r["cs"])
+        conv_b.backward(t["x"], t["w"], t["cbias"], t["dy"], r["dx"], o(D, W, dtype=f32), o(D, dtype=f32), starts=starts, state_in=t["cs"])
+        arr, kw, saved = [t[n] for n in ("x", "dt", "A", "B", "C")], dict(D=t["D"], z=t["z"], dt_bias=t["dt_bias"], starts=starts), scan_b.allocate_saved()
+        scan.forward(*arr, r["sy"], h_in=t["h"], h_out=r["h"], saved=saved, **kw)
+        scan_b.backward(*arr, t["dy"], saved, r["sdx"], r["ddt"], o(D, N, dtype=f32), r["dB"], r["dC"], dz=r["dz"], dD=o(D, dtype=f32),
+                        ddt_bias=o(D, dtype=f32), h_in=t["h"], dh_out=t["dh"], dh_in=r["dh"], **kw)
+        return r
+
+    clean, tokens, all_ = run(dev), run(spoiled), run({**spoiled, **states_spoiled})
+    for n, v in clean.items():
+        assert bool(torch.isfinite(v).all()), n
+        rows = good_s if n in ("cs", "h", "dh") else torch.from_numpy(ok).cuda()
+        assert torch.equal(tokens[n][rows], v[rows]) and torch.equal(all_[n][rows], v[rows]), n
+        if n in ("y", "sy"):                      # what comes later does not reach back
+            rows = torch.from_numpy(before).cuda()
+            assert torch.equal(tokens[n][rows], v[rows]), n
+    if T > 20:
+        assert not bool(torch.isfinite(tokens["sy"]).all()) and not bool(torch.isfinite(tokens["y"]).all())
+
+
+def test_bad_rows_of_a_norm_stay_bad_alone():
+    import torch
+    b = Box(8, True)
+    for rows, D in ((9, 40), (7, 384), (9, 4096), (5, 9001)):
+        x, g, dy = (b.normal(rows, D)[0] for _ in range(3))
+        r, dr = (b.normal(rows, D, dtype=torch.float32)[0] for _ in range(2))
+        w = b.normal(D)[0]
+        ok = [i for i in range(rows) if i not in (1, 4)]
+        for kind in ("rms", "layer"):
+            f, q = (Q.SeqNormPlan(rows, D, CONV_BF16, d, kind=kind, post=True, gate="before") for d in ("fwd", "bwd"))
+
+            def run():
+                y, ro, dx, dg, dres = (torch.empty_like(t) for t in (x, r, x, g, r))
+                f.forward(x, y=y, gate=g, w_post=w, res=r, res_out=ro, w_pre=w)
+                q.backward(x, dx, dy=dy, gate=g, w_post=w, res=r, dres_out=dr, w_pre=w, dgate=dg, dres=dres)
+                return y, ro, dx, dg, dres
+
+            want = [t.clone() for t in run()]
+            keep = [t.clone() for t in (x, g, r)]
+            x[1, 3], g[4, ::2], r[4, 5] = float("nan"), float("inf"), -float("inf")
+            for t, v in zip(run(), want):
+                assert torch.equal(t[ok], v[ok])
+            for t, v in zip((x, g, r), keep):
+                t.copy_(v)

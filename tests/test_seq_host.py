@@ -400,3 +400,30 @@ def test_arguments_read_by_elements_do_not_choose_the_kernel(tmp_path):
     assert sorted(got.pop("norm_fwd 1")) == sorted(both("x", "gate", "res", "y", "res_out") + params)
     assert sorted(got.pop("norm_bwd 1")) == sorted(both("x", "gate", "res", "dy", "dres_out", "dx", "dgate", "dres") + params)
     assert not got, got
+
+
+# ------------------------------------------------------ what the cases of long memory can tell
+SLOW = [([1300], False), ([300, 1200], True), ([4100], False), ([1, 900, 0, 2100, 33, 777, 8, 450], True)]
+
+
+@pytest.mark.parametrize("lens,ragged", SLOW)
+def test_cases_of_long_memory_tell_wrong_joins(lens, ragged):
+    """Joining the pieces of the token axis, with a mistake planted in it, leaves the bound that the kernels are held to
+    in these cases."""
+    rng = np.random.default_rng(len(lens))
+    D, N = 12, 4
+    a, more = O.slow_case(rng, lens, D, N)
+    want, mag = O.scan(**a, G=1, lens=lens, h0=more["h"])
+    k = 4 * max(lens) + N + 100
+    piece, parts = (32, 4) if sum(lens) < 2048 else (40, 8)
+    assert (parts == 4) == (sum(lens) <= 64 * piece)
+    y, h = O.scan_in_pieces(**a, lens=lens, h0=more["h"], piece=piece, parts=parts)
+    O.check("y", y, want["y"], mag["y"], k, True)
+    O.check("h", h, want["h"], mag["h"], k, False)
+    faults = ["parts before", "decay over a part"] + ["older parts"] * (len(lens) == 1) + ["ends of sequences"] * ragged
+    for fault in faults:
+        y, h = O.scan_in_pieces(**a, lens=lens, h0=more["h"], piece=piece, parts=parts, fault=fault)
+        with pytest.raises(AssertionError):
+            O.check("y", y, want["y"], mag["y"], k, True)
+        with pytest.raises(AssertionError):
+            O.check("h", h, want["h"], mag["h"], k, False)
