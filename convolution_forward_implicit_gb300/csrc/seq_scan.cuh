@@ -76,11 +76,12 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a
 __device__ __forceinline__ float2 sum2(float2 a, float2 b) { return __fadd2_rn(a, b); }
 __device__ __forceinline__ float2 dup2(float a) { return make_float2(a, a); }
 __device__ __forceinline__ float2 exp2_2(float2 v) { return make_float2(ex2_approx(v.x), ex2_approx(v.y)); }
-// exp(delta A) of two states or channels, with A2 = A log2(e).  The special-function unit's 2^v lies 1.6e-8
-// low on average for v near 0 (measured over 4 M values in [-0.01, 0]; 5e-8 below -1), and a slow state
-// multiplies hundreds of such factors: an offset of 2.3e-8 = 1.6e-8 / ln 2 in the argument, where it costs
-// nothing, takes the bias away.  (2^2.3e-8 is 1 in fp32: delta = 0 still changes nothing.)
-__device__ __forceinline__ float2 decay2(float2 delta, float2 A2) { return exp2_2(fma2(delta, A2, dup2(2.3e-8f))); }
+// exp(delta A) of two states or channels, with A2 = A log2(e).  The special-function unit's 2^v lies low on
+// average (measured over 1 M values an octave: 5e-9 to 1e-8 for |v| of 2^-9 to 2^-21, 2.7e-8 at 2^-7 and 2^-6, 5e-8 from
+// 1 on), and a state multiplies about 1 / |v| such factors.  An offset of 1.5e-8 in the argument, where it costs nothing, leaves
+// +5e-9 to 0 of it up to 2^-9, whose many factors add up most (2e-5 of a state after 4096 tokens; with 2.3e-8 +1e-8 a
+// factor and 4e-5, with 1e-8 +2e-9), and -1.6e-8 at 2^-7 (2.3e-8: -1e-8, 1e-8: -1.9e-8).  (2^1.5e-8 is 1 in fp32: delta = 0 still changes nothing.)
+__device__ __forceinline__ float2 decay2(float2 delta, float2 A2) { return exp2_2(fma2(delta, A2, dup2(1.5e-8f))); }
 __device__ __forceinline__ void unpack(float2 v, float& a, float& b) {
     a = v.x;
     b = v.y;

@@ -765,3 +765,38 @@ def test_bad_rows_of_a_norm_stay_bad_alone():
                 assert torch.equal(t[ok], v[ok])
             for t, v in zip((x, g, r), keep):
                 t.copy_(v)
+def test_decay_factors_have_no_bias():
+    """Thousands of factors close to one, of sequences that are not cut.  A systematic 1.6e-8 below the true factor (what
+    the special-function unit's 2^v has there) would leave every state 4096 times that, 6.6e-5, too small on average; the
+    roundings of a state's own path, random, average out over 65536 states: half of 6.6e-5 separates the two."""
+    import torch
+    S, L, D, N = 512, 4096, 8, 16
+    rng = np.random.default_rng(4)
+    step = np.exp(rng.uniform(np.log(1e-3), np.log(1e-2), (S * L, D))).astype(np.float32)
+    A = -rng.uniform(0.02, 0.1, (D, N)).astype(np.float32)
+    h = rng.uniform(1, 2, (S, D, N)).astype(np.float32)
+    put = lambda v: torch.from_numpy(v).cuda()      # noqa: E731
+    p = Q.SeqScanPlan(S, S * L, D, N, CONV_F32, softplus=False)
+    assert f"pieces={S} " in p.describe()
+    z, bc = torch.zeros(S * L, D, device="cuda"), torch.zeros(S * L, N, device="cuda")
+    y, left = torch.empty_like(z), torch.empty(S, D, N, device="cuda")
+    p.forward(z, put(step), put(A), bc, bc, y, h_in=put(h), h_out=left)
+    want = h.astype(np.float64) * np.exp(step.astype(np.float64).reshape(S, L, D).sum(1)[:, :, None] * A.astype(np.float64))
+    off = host(left) / want - 1
+    assert abs(off.mean()) < 0.5 * 1.6e-8 * L, off.mean()
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+def test_steps_of_zero_keep_the_states(bf16):
+    """delta = 0: a factor of exactly one and nothing added, over whole sequences and in steps."""
+    import torch
+    b = Box(1, bf16)
+    S, L, D, N = 3, 50, 24, 16
+    code, T = CONV_BF16 if bf16 else CONV_F32, 150
+    x, B, C = b.normal(T, D)[0], b.normal(T, N)[0], b.normal(T, N)[0]
+    A, h = b.put(-b.rng.uniform(0.01, 20, (D, N)), dtype=torch.float32)[0], b.normal(S, D, N, dtype=torch.float32)[0]
+    dt, y, left = torch.zeros_like(x), torch.empty_like(x), torch.empty_like(h)
+    Q.SeqScanPlan(S, T, D, N, code, softplus=False).forward(x, dt, A, B, C, y, h_in=h, h_out=left)
+    assert torch.equal(left, h)
+    Q.SeqScanPlan(S, S, D, N, code, direction="step", softplus=False).step(x[:S], dt[:S], A, B[:S], C[:S], h, left.zero_(), y[:S])
+    assert torch.equal(left, h)
