@@ -235,3 +235,67 @@ def test_arguments_read_by_elements_lie_anywhere(bf16):
         return dx, dr, t["dw_post"], t["dw_pre"]
 
     same(norm_back, a, {k: shifted(a[k]) for k in ("dw_post", "dw_pre")})
+
+
+# ----------------------------------------------------------------------------------- graphs
+def test_a_training_step_in_a_graph():
+    """Forward and backward calls of all three operators captured once and replayed on other inputs."""
+    import torch
+    S, L, D, N, W = 2, 600, 72, 16, 4
+    T, bf, f32 = S * L, torch.bfloat16, torch.float32
+    g = torch.Generator(device="cuda").manual_seed(5)
+    n = lambda *s, dtype=bf: torch.randn(*s, generator=g, device="cuda").to(dtype)      # noqa: E731
+    e = lambda *s, dtype=bf: torch.empty(*s, dtype=dtype, device="cuda")      # noqa: E731
+    t = dict(x=n(T, D), dt=n(T, D) - 1, B=n(T, N), C=n(T, N), z=n(T, D), dy=n(T, D), res=n(T, D, dtype=f32))
+    w, bias, nw, A, Dv = n(D, W), n(D), n(D), -n(D, N, dtype=f32).abs() - 0.1, n(D, dtype=f32)
+    o = dict(cx=e(T, D), y=e(T, D), normed=e(T, D), r=e(T, D, dtype=f32), dx=e(T, D), ddt=e(T, D), dz=e(T, D), dB=e(T, N), dC=e(T, N), dA=e(D, N, dtype=f32),
+             dD=e(D, dtype=f32), dcx=e(T, D), dw=e(D, W, dtype=f32), dbias=e(D, dtype=f32), dr=e(T, D, dtype=f32), dnw=e(D, dtype=f32), dn=e(T, D))
+    conv, conv_b = (Q.SeqConvPlan(S, T, D, W, CONV_BF16, d).allocate() for d in ("fwd", "bwd"))
+    scan, scan_b = (Q.SeqScanPlan(S, T, D, N, CONV_BF16, d).allocate() for d in ("fwd", "bwd"))
+    norm, norm_b = (Q.SeqNormPlan(T, D, CONV_BF16, d).allocate() for d in ("fwd", "bwd"))
+    saved = scan_b.allocate_saved()
+
+    def step():
+        conv.forward(t["x"], w, bias, o["cx"])
+        a = (o["cx"], t["dt"], A, t["B"], t["C"])
+        scan.forward(*a, o["y"], D=Dv, z=t["z"], saved=saved)
+        norm.forward(o["y"], y=o["normed"], res=t["res"], res_out=o["r"], w_pre=nw)
+        norm_b.backward(o["y"], o["dn"], dy=t["dy"], res=t["res"], w_pre=nw, dres=o["dr"], dw_pre=o["dnw"])
+        scan_b.backward(*a, o["dn"], saved, o["dx"], o["ddt"], o["dA"], o["dB"], o["dC"], D=Dv, z=t["z"], dz=o["dz"], dD=o["dD"])
+        conv_b.backward(t["x"], w, bias, o["dx"], o["dcx"], o["dw"], o["dbias"])
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(3):
+        for v in t.values():
+            v.copy_(torch.randn(v.shape, generator=g, device="cuda"))
+        step()
+        torch.cuda.synchronize()
+        want = {k: v.clone() for k, v in o.items()}
+        for v in o.values():
+            v.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(v, want[k]) for k, v in o.items())
+
+
+def test_a_call_captured_before_any_other():
+    """Without a workspace at hand the captured call allocates one of the graph's own memory."""
+    import torch
+    a, want = scan_reference()
+    p = Q.SeqScanPlan(1, T_, D_, N_, CONV_F32)
+    y = torch.empty(T_, D_, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        p.forward(*a, y)
+    for _ in range(2):
+        y.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want)
+    p.forward(*a, y.zero_())                 # and an ordinary call behind it
+    torch.cuda.synchronize()
+    assert torch.equal(y, want)
