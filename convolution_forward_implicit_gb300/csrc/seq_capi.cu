@@ -345,6 +345,7 @@ static conv_status scan_call(seq_plan_t p, const seq_scan_args* a, seq_direction
     q.x_ld = a->x_ld; q.dt_ld = a->dt_ld; q.B_ld = a->B_ld; q.C_ld = a->C_ld; q.z_ld = a->z_ld; q.y_ld = a->y_ld;
     q.dy_ld = a->dy_ld; q.dx_ld = a->dx_ld; q.ddt_ld = a->ddt_ld; q.dB_ld = a->dB_ld; q.dC_ld = a->dC_ld; q.dz_ld = a->dz_ld;
     q.cblocks = p->blocks;
+    q.sms = p->sms;
     auto aligned = [](const void* v, size_t n) { return reinterpret_cast<uintptr_t>(v) % n == 0; };
     q.quads = p->N % 4 == 0 && aligned(a->A, 16);
     if (dir == SEQ_STEP)

@@ -94,6 +94,7 @@ struct SeqScanParams {
     int cblocks;                    // backward: channel blocks (over all groups)
     int quads;                      // 1 when A (step: states, B and C too) lies in whole aligned groups of 4
     int wide;                       // rows and groups consist of whole aligned pieces of so many bytes: 16, 4 or 0 (of single elements)
+    int sms;
 };
 
 #ifdef __CUDACC__

@@ -154,7 +154,7 @@ cudaError_t launch_step(const SeqScanParams& p, cudaStream_t stream) {
     // Several sequences a thread once that still leaves the GPU several blocks an SM.  256 x 4096 x 16 bf16: one
     // sequence and channel 54 us; 4 sequences 32.5; 2 sequences of 2 channels, which share the rows' addresses,
     // 29.4; 4 of 2 (half the warps) 37.
-    if (blocks * p.ax.S < 16 * 152 * 4) return launch_step_of<T, LN, 1, 1>(p, stream);
+    if (blocks * p.ax.S < 16ll * p.sms * 4) return launch_step_of<T, LN, 1, 1>(p, stream);
     const bool pairs = p.quads && p.wide >= 2 * (int)sizeof(T);        // whole aligned pairs of channels
     return pairs ? launch_step_of<T, LN, 2, 2>(p, stream) : launch_step_of<T, LN, 4, 1>(p, stream);
 }
