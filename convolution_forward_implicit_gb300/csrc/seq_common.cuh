@@ -200,8 +200,9 @@ __device__ __forceinline__ void rows_to_shared(T (*to)[W], const T* from, long l
 // Sum of the values at `rows` rows `step` apart, of 32 neighbouring columns (`src`: the column of lane
 // threadIdx.x & 31) by a block of COLUMN_THREADS: warps take turns at the rows, then the first warp adds their
 // sums in order and holds the result.  Called by the whole block.
-// Eight loads a thread are on their way at once; with 16 and their registers one block an SM, and few of them next to
-// the kernel before (6007 x 1280 norm 80.8 us a training pass against 82.3, but the convolution's 147 against 144).
+// Eight loads a thread are on their way at once, in kernels of 32 registers (two blocks an SM) that spill a little (the norm's
+// 136 bytes, the convolution's 24).  With 16 and their registers, one block an SM and few of them next to the kernel
+// before: the norm's 6007 x 1280 training pass 80.8 us against 82.3, the convolution's 8 x 2048 x 4096 147 against 144.
 constexpr int COLUMN_THREADS = 1024;
 __device__ __forceinline__ float column_sum(const float* src, long long step, int rows, bool on) {
     constexpr int WARPS = COLUMN_THREADS / 32;

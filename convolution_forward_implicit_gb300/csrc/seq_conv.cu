@@ -481,7 +481,8 @@ cudaError_t launch(const SeqConvParams& p, bool bf16, Pass pass, cudaStream_t st
 
 }  // namespace
 
-// Tokens a thread walks, 8 to 256: whole rounds of resident blocks (4, 5 or 8 an SM forward, 2 or 1 backward), where
+// Tokens a thread walks, 8 to 256: whole rounds of resident blocks (4, 5 or 8 an SM forward, 2 or 1 backward, as the
+// kernels of 4 taps fit; fewer taps leave room for more: bf16 forward 6 at 2 taps and 7 at 3), where
 // a round costs its run and, for the several waits for memory before a thread's first token (its sequence, its
 // window, its weights), about `start` tokens more.  (Two rounds of 512 threads an SM instead, whatever is left
 // over: 6011 x 2560 ragged bf16 25.9 us, here 20.6; 8 x 2048 x 4096 bf16 forward and backward 154, here 144; 8 x 1500 x

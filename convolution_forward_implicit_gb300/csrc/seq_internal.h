@@ -84,12 +84,12 @@ struct SeqScanParams {
     void *y, *dx, *ddt, *dB, *dC, *dz;
     float *h_out, *saved, *dA, *dD, *ddt_bias, *dh_in;
     long long x_ld, dt_ld, B_ld, C_ld, z_ld, y_ld, dy_ld, dx_ld, ddt_ld, dB_ld, dC_ld, dz_ld;
-    // workspace
-    float* piece_state;             // [pieces][D][N]: what a piece adds to the state behind it (backward: to the gradient
+    // workspace; states lie as [row][quad of states][channel][4] (scan_state_at), as the saved ones do
+    float* piece_state;             // a row a piece: what it adds to the state behind it (backward: to the gradient
                                     // before it); then the state before it (the gradient behind it)
-    float* piece_init;              // [pieces][D][N]: starting state of the last sequence that starts in a piece
+    float* piece_init;              // a row a piece: starting state of the last sequence that starts in it
     float* piece_delta;             // [pieces][D]: sum of delta over a piece
-    float* part_bc;                 // backward: [channel blocks][T][2][N] partial dB, dC
+    float* part_bc;                 // backward: [channel blocks][T][2][P] partial dB, dC; P: N padded to 8, 16, 32, 64 or 128
     float* part_par;                // backward: [pieces][N + 2][D] partial dA, dD, ddt_bias
     int cblocks;                    // backward: channel blocks (over all groups)
     int quads;                      // 1 when A (step: states, B and C too) lies in whole aligned groups of 4
