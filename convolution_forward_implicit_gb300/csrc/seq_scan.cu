@@ -258,9 +258,9 @@ __global__ void __launch_bounds__(join_threads(JOIN_PARTS)) seq_scan_join_kernel
     const long long i = blockIdx.x * (long long)JOIN_LANES + lane;
     const bool on = i < (long long)quads * p.D;
     const int quad = on ? (int)(i / p.D) : 0, d = on ? (int)(i - (long long)quad * p.D) : 0;
-    float A2[4];
+    float A2[4];                     // A log2(e) / 2
 #pragma unroll
-    for (int k = 0; k < 4; ++k) A2[k] = on && 4 * quad + k < p.N ? p.A[(long long)d * p.N + 4 * quad + k] * LOG2E : 0.f;
+    for (int k = 0; k < 4; ++k) A2[k] = on && 4 * quad + k < p.N ? p.A[(long long)d * p.N + 4 * quad + k] * (0.5f * LOG2E) : 0.f;
     griddep_wait();                  // from here on: what the pass before wrote
     griddep_launch();
     float4 e[JOIN_MOST];
@@ -277,10 +277,15 @@ __global__ void __launch_bounds__(join_threads(JOIN_PARTS)) seq_scan_join_kernel
     }
     float4 c = make_float4(0.f, 0.f, 0.f, 0.f);
     float total = 0.f;
+    // exp(sum A) c + e, the factor in two halves: one beyond fp32's range (states that grow: A > 0) is then not infinity
+    // where there is nothing to grow, or little.
+    auto carry = [](float half_v, float c, float e) {
+        const float half = fminf(ex2_approx(half_v), 3.4e38f);
+        return fmaf(half * c, half, e);
+    };
     auto step = [&](float4 c, float4 e, float sum, bool stop) {
         if (stop) return e;
-        return make_float4(fmaf(ex2_approx(sum * A2[0]), c.x, e.x), fmaf(ex2_approx(sum * A2[1]), c.y, e.y),
-                           fmaf(ex2_approx(sum * A2[2]), c.z, e.z), fmaf(ex2_approx(sum * A2[3]), c.w, e.w));
+        return make_float4(carry(sum * A2[0], c.x, e.x), carry(sum * A2[1], c.y, e.y), carry(sum * A2[2], c.z, e.z), carry(sum * A2[3], c.w, e.w));
     };
 #pragma unroll
     for (int j = 0; j < JOIN_MOST; ++j)

@@ -800,3 +800,30 @@ def test_steps_of_zero_keep_the_states(bf16):
     assert torch.equal(left, h)
     Q.SeqScanPlan(S, S, D, N, code, direction="step", softplus=False).step(x[:S], dt[:S], A, B[:S], C[:S], h, left.zero_(), y[:S])
     assert torch.equal(left, h)
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("T", [300, 1300, 4100])
+def test_growing_states_of_nothing_are_nothing(bf16, T):
+    """A > 0: states grow by a third a token, by more than fp32 holds over a few pieces, but there is nothing to grow before
+    the first input, nor a gradient behind the last one: zero, not infinity times zero."""
+    import torch
+    D, N, f32 = 24, 16, torch.float32
+    b = Box(T, bf16)
+    x, dy = b.rng.standard_normal((T, D)), b.rng.standard_normal((T, D))
+    x[:-30], dy[30:] = 0, 0
+    (x, xe), (dy, dye), (B, Be), (C, Ce) = b.put(x), b.put(dy), b.normal(T, N), b.normal(T, N)
+    (dt, dte), (A, Ae) = b.put(np.ones((T, D))), b.put(b.rng.uniform(0.2, 0.4, (D, N)), dtype=f32)
+    code = CONV_BF16 if bf16 else CONV_F32
+    p, q = (Q.SeqScanPlan(1, T, D, N, code, direction=d, softplus=False) for d in ("fwd", "bwd"))
+    assert int(p.describe().split("pieces=")[1].split()[0]) > 1
+    y, saved, left = b.out(T, D), q.allocate_saved(), b.out(1, D, N, dtype=f32)
+    p.forward(x, dt, A, B, C, y, h_out=left, saved=saved)
+    g = {n: b.out(*s, dtype=f32 if n in ("dA", "dh_in") else None)
+         for n, s in dict(dx=(T, D), ddt=(T, D), dA=(D, N), dB=(T, N), dC=(T, N), dh_in=(1, D, N)).items()}
+    q.backward(x, dt, A, B, C, dy, saved, **g)
+    ref, mag = O.scan(xe, dte, Ae, Be, Ce, 1, [T], np.zeros((1, D, N)), act=False, dy=dye)
+    k = 4 * T + N + 100
+    for n, v in dict(g, y=y, h=left).items():
+        O.check(n, host(v), ref[n], mag[n], 2 * k + D + T, bf16 and v.dtype == torch.bfloat16)
+    b.check_guards()
