@@ -827,3 +827,34 @@ def test_growing_states_of_nothing_are_nothing(bf16, T):
     for n, v in dict(g, y=y, h=left).items():
         O.check(n, host(v), ref[n], mag[n], 2 * k + D + T, bf16 and v.dtype == torch.bfloat16)
     b.check_guards()
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("starts", [[5, 3, 700, -4, 90, 12], [0, 1 << 30, -(1 << 30), 40, 40, 10], [400] * 6, [-1] * 6, [300, 250, 200, 150, 100, 50]])
+@pytest.mark.parametrize("D,pad", [(40, 0), (17, 1)])
+def test_bounds_outside_their_contract_write_nothing_elsewhere(bf16, starts, D, pad):
+    """Other numbers, but the calls end and the outputs' surroundings are untouched.  (That no access leaves the
+    tensors is shown on the host, from the lookups' own code.)"""
+    import torch
+    S, T, N, W, f32 = 5, 400, 16, 4, torch.float32
+    b = Box(len(starts), bf16)
+    code = CONV_BF16 if bf16 else CONV_F32
+    n = lambda *s, **kw: b.normal(*s, **kw)[0]      # noqa: E731
+    st = torch.tensor(starts, dtype=torch.int32, device="cuda")
+    slots = torch.tensor([2, -7, 1 << 30, 0, 1], dtype=torch.int32, device="cuda")
+    x, dt, z, dy, B, C = n(T, D, pad=pad), n(T, D, pad=pad), n(T, D, pad=pad), n(T, D, pad=pad), n(T, N, pad=pad), n(T, N, pad=pad)
+    w, bias, A, cs, h = n(D, W), n(D), -n(D, N, dtype=f32).abs(), n(3, W - 1, D), n(3, D, N, dtype=f32)
+    o = lambda *s, dtype=None, p=pad: b.out(*s, dtype=dtype, pad=p)      # noqa: E731
+    for direction in ("fwd", "bwd"):
+        p = Q.SeqConvPlan(S, T, D, W, code, direction=direction, ragged=True)
+        q = Q.SeqScanPlan(S, T, D, N, code, direction=direction, ragged=True)
+        if direction == "fwd":
+            p.forward(x, w, bias, o(T, D), starts=st, slots=slots, state_in=cs, state_out=o(3, W - 1, D, p=0))
+            saved = q.allocate_saved().zero_()
+            q.forward(x, dt, A, B, C, o(T, D), z=z, starts=st, slots=slots, h_in=h, h_out=o(3, D, N, dtype=f32, p=0), saved=saved)
+        else:
+            p.backward(x, w, bias, dy, o(T, D), o(D, W, dtype=f32, p=0), o(D, dtype=f32, p=0), starts=st, slots=slots, state_in=cs)
+            q.backward(x, dt, A, B, C, dy, saved, o(T, D), o(T, D), o(D, N, dtype=f32, p=0), o(T, N), o(T, N), z=z, dz=o(T, D), starts=st, slots=slots,
+                       h_in=h, dh_out=h, dh_in=o(3, D, N, dtype=f32, p=0))
+        torch.cuda.synchronize()
+    b.check_guards()

@@ -427,3 +427,31 @@ def test_cases_of_long_memory_tell_wrong_joins(lens, ragged):
             O.check("y", y, want["y"], mag["y"], k, True)
         with pytest.raises(AssertionError):
             O.check("h", h, want["h"], mag["h"], k, False)
+
+
+def test_bounds_outside_their_contract_stay_inside_the_tensors(tmp_path):
+    """include/seq.h: sequence bounds and slots outside their contract lead to no access outside the tensors.  The
+    kernels' own lookups, compiled for the host, on such values."""
+    import shutil
+    import subprocess
+    gxx = shutil.which("g++")
+    if gxx is None:
+        pytest.skip("needs g++")
+    src = os.path.join(ROOT, "convolution_forward_implicit_gb300", "csrc")
+
+    def cut(name, what):
+        text = open(os.path.join(src, name)).read()
+        i = text.index(what)
+        j = text.index("\n};" if what.startswith("struct") else "\n}", i)
+        return text[i:j] + ("\n};\n" if what.startswith("struct") else "\n}\n")
+
+    d = "__device__ __forceinline__ "
+    parts = [("seq_internal.h", d + "int seq_start("), ("seq_internal.h", d + "int seq_first_at("), ("seq_internal.h", d + "long long seq_slot("),
+             ("seq_conv.cu", "struct Place {"), ("seq_conv.cu", d + "Place place_of("), ("seq_conv.cu", d + "void next_place("),
+             ("seq_scan.cuh", "struct ScanPlace {"), ("seq_scan.cuh", d + "ScanPlace scan_place(")]
+    (tmp_path / "seq_bounds.inc").write_text("".join(cut(*p) for p in parts))
+    exe = tmp_path / "seq_bounds_check"
+    subprocess.check_call([gxx, "-O1", "-std=c++17", "-fsanitize=undefined", "-fno-sanitize-recover=all", "-I", str(tmp_path),
+                           os.path.join(ROOT, "tests", "native", "seq_bounds_check.cpp"), "-o", str(exe)])
+    out = subprocess.run([str(exe)], capture_output=True, text=True, timeout=120)
+    assert out.returncode == 0 and " 0 wrong" in out.stdout, out.stdout + out.stderr
