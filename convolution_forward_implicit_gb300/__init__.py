@@ -7,3 +7,5 @@ has not been built.
 """
 from .binding import *  # noqa: F401,F403
 from .seq import *  # noqa: F401,F403
+from .delta import *  # noqa: F401,F403
+from .gnorm import *  # noqa: F401,F403

@@ -46,6 +46,46 @@ __device__ __forceinline__ long long seq_slot(const SeqSlots& s, int seq) {
 }
 #endif
 
+// A piece of the token axis that does not cross sequences: `len` tokens at most.  Sequence s has the slots from
+// cut_base(s) on, ceil(length / len) of them.  Equal lengths: s ceil(L / len).  Unequal ones: floor(start / len) + s,
+// which needs no sums over the sequences before it and leaves room, since ceil((b - a) / len) <= floor(b / len) -
+// floor(a / len) + 1; slots between are empty.  T / len + S slots are enough, for bounds outside their contract too
+// (they are clamped, so that a <= b <= T).
+struct CutPiece {
+    int s, index, t0, n;            // sequence, piece of it, first token, tokens (0: none)
+};
+__host__ __device__ inline long long cut_slots(long long S, long long T, long long L, int len) {
+    return L > 0 ? S * ((L + len - 1) / len) : T / len + S;
+}
+#ifdef __CUDACC__
+__device__ __forceinline__ int cut_base(const SeqAxis& a, int s, int len) {
+    return a.L > 0 ? s * ((a.L + len - 1) / len) : seq_start(a, s, 0) / len + s;
+}
+__device__ __forceinline__ CutPiece cut_piece(const SeqAxis& a, int slot, int len) {
+    CutPiece c;
+    if (a.L > 0) {
+        const int per = (a.L + len - 1) / len;
+        c.s = slot / per;
+        c.index = slot - c.s * per;
+        c.t0 = c.s * a.L + c.index * len;
+        c.n = min(len, a.L - c.index * len);
+        return c;
+    }
+    int lo = 0, hi = a.S - 1;       // the last sequence whose first slot is at or before this one
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (cut_base(a, mid, len) <= slot) lo = mid; else hi = mid - 1;
+    }
+    const int t0 = seq_start(a, lo, 0), t1 = seq_start(a, lo + 1, t0);
+    c.s = lo;
+    c.index = max(slot - cut_base(a, lo, len), 0);
+    const long long at = t0 + (long long)c.index * len;
+    c.t0 = (int)min(at, (long long)t1);
+    c.n = min(len, t1 - c.t0);
+    return c;
+}
+#endif
+
 // ---- short causal convolution ----
 struct SeqConvParams {
     SeqAxis ax;
@@ -142,5 +182,55 @@ struct SeqNormParams {
 cudaError_t launch_seq_norm_fwd(const SeqNormParams& p, bool bf16, bool res_bf16, cudaStream_t stream);
 cudaError_t launch_seq_norm_bwd(const SeqNormParams& p, bool bf16, bool res_bf16, cudaStream_t stream);
 int seq_norm_bwd_blocks(int rows, int D, unsigned flags, int esize, int rsize, int sms);
+
+// ---- group norm with an activation ----
+// The token axis is cut into slabs of `slab` tokens that do not cross sequences (AxisCut).
+struct SeqGnormParams {
+    SeqAxis ax;
+    int D, G, act;
+    float eps;
+    int slab, slots;
+    const void *x, *w, *b, *dy;
+    void *y, *dx;
+    float *stats, *dw, *db;
+    long long x_ld, y_ld, dy_ld, dx_ld;
+    float* part;                    // [slots][D][2]: a slab's mean and sum of squared differences; backward: sums
+    float* coef;                    // [S][G][2]: mean and rstd; backward: the group's two means
+    int vec;                        // 1: rows of whole 16-byte aligned groups of 8
+    int sms;
+};
+cudaError_t launch_seq_gnorm_fwd(const SeqGnormParams& p, bool bf16, cudaStream_t stream);
+cudaError_t launch_seq_gnorm_bwd(const SeqGnormParams& p, bool bf16, cudaStream_t stream);
+int seq_gnorm_slab(long long S, long long T, int D, int sms);
+
+// ---- gated delta rule ----
+constexpr int DELTA_CHUNK = 64;     // tokens worked on at once; saved states lie at every chunk's first token
+constexpr int DELTA_ROWS = 264;     // floats of a chunk's row factors (see seq_delta.cuh)
+struct SeqDeltaParams {
+    SeqAxis ax;
+    SeqSlots sl;
+    int Hk, Hv, Dk, Dv, norm;
+    float scale;
+    const void *q, *k, *v, *dy;
+    const float *g, *beta, *h_in, *dh_out;
+    void *y, *dq, *dk, *dv;
+    float *h_out, *saved, *dg, *dbeta, *dh_in;
+    long long q_ld, k_ld, v_ld, g_ld, beta_ld, y_ld, dy_ld, dq_ld, dk_ld, dv_ld, dg_ld, dbeta_ld;
+    int slots;                      // chunks of the token axis at most
+    // workspace, by chunk and value head
+    float* tri;                     // [slots][Hv][2][64][64]: T and A
+    float* rows;                    // [slots][Hv][DELTA_ROWS]
+    float* dstate;                  // backward: [slots][Hv][Dk][Dvp] gradient at the state a chunk leaves
+    float* dr;                      // backward: [slots][Hv][64][Dvp]
+    int Dvp;                        // Dv rounded up to 4
+    long long saved_u;              // where the saved u begin, in floats: [slots][Hv][64][Dvp] behind [slots][Hv][Dk][Dvp]
+    int wide;                       // q and k in whole aligned 16-byte groups
+    int pairs, key_pairs;           // v, y, dy, dv; dq, dk in aligned pairs of elements
+    int quads;                      // step: states in whole aligned groups of 4
+    int sms;
+};
+cudaError_t launch_seq_delta_fwd(const SeqDeltaParams& p, bool bf16, cudaStream_t stream);
+cudaError_t launch_seq_delta_bwd(const SeqDeltaParams& p, bool bf16, cudaStream_t stream);
+cudaError_t launch_seq_delta_step(const SeqDeltaParams& p, bool bf16, cudaStream_t stream);
 
 }  // namespace convfwd

@@ -59,15 +59,19 @@ NORM_FIELDS = ("x", "x_ld", "gate", "gate_ld", "w_post", "b_post", "scale", "res
                "dgate_ld", "dres", "dres_ld", "dw_post", "db_post", "dscale", "dw_pre", "db_pre")
 
 
+def _bind(sigs):
+    lib = load_library()
+    for name, (res, args) in sigs.items():
+        fn = getattr(lib, name)
+        fn.restype = res
+        fn.argtypes = args
+    return lib
+
+
 def _library():
     global _bound
     if _bound is None:
-        lib = load_library()
-        for name, (res, args) in _SIGS.items():
-            fn = getattr(lib, name)
-            fn.restype = res
-            fn.argtypes = args
-        _bound = lib
+        _bound = _bind(_SIGS)
     return _bound
 
 
