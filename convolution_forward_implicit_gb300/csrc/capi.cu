@@ -275,6 +275,20 @@ __global__ void splitk_reduce_kernel(const float* __restrict__ ws, int splits, l
 
 }  // namespace
 
+unsigned* convfwd::device_error_word() { return error_word_ptr(); }
+
+conv_status convfwd::check_error_word(cudaStream_t stream) {
+    if (cudaStreamSynchronize(stream) != cudaSuccess) return CONV_ERR_CUDA;
+    unsigned v = 0;
+    if (cudaMemcpyFromSymbol(&v, g_error_word, sizeof(v)) != cudaSuccess) return CONV_ERR_CUDA;
+    if (v) {
+        const unsigned zero = 0;
+        if (cudaMemcpyToSymbol(g_error_word, &zero, sizeof(zero)) != cudaSuccess) return CONV_ERR_CUDA;
+        return CONV_ERR_TIMEOUT;
+    }
+    return CONV_OK;
+}
+
 // ----------------------------------------------------------------------------- plan
 enum Variant { VAR_TC = 0, VAR_SIMT = 1, VAR_DG_SIMT = 2, VAR_WG_SIMT = 3, VAR_WG_TC = 4, VAR_DG_PHASED = 5 };
 constexpr int MAX_PHASES = 16;
@@ -1815,16 +1829,7 @@ conv_status conv_bwd_weight(conv_plan_t plan, const void* x, const void* dy, voi
 }
 
 conv_status conv_plan_check(conv_plan_t plan, void* stream) {
-    if (!plan) return CONV_ERR_INVALID_ARG;
-    if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return CONV_ERR_CUDA;
-    unsigned v = 0;
-    if (cudaMemcpyFromSymbol(&v, g_error_word, sizeof(v)) != cudaSuccess) return CONV_ERR_CUDA;
-    if (v) {
-        const unsigned zero = 0;
-        if (cudaMemcpyToSymbol(g_error_word, &zero, sizeof(zero)) != cudaSuccess) return CONV_ERR_CUDA;
-        return CONV_ERR_TIMEOUT;
-    }
-    return CONV_OK;
+    return plan ? check_error_word(static_cast<cudaStream_t>(stream)) : CONV_ERR_INVALID_ARG;
 }
 
 conv_status conv_plan_destroy(conv_plan_t plan) {

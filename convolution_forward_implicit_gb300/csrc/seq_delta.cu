@@ -75,7 +75,7 @@ template <typename T, int KP>
 struct ChunkSmem {
     static constexpr int LD = KP + 8;
     T q[DC * LD], k[DC * LD];
-    float L[DC * LSQ], inv[DC * LSQ], tmp[DC * LSQ];
+    float L[DC * LSQ], inv[DC * LSQ], tmp[DC * LSQ], a[DC * LSQ];
     float2 b[DC];
     float rq[DC], rk[DC], beta[DC];
 };
@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(DT) delta_chunk_kernel(const __grid_constant__
     warp_mma<8>(acc, Along<T>{warp < 4 ? s.k : s.q, LD}, Along<T>{s.k, LD}, m0, 0, 0, KP);
     for (int h = kh * rep; h < (kh + 1) * rep; ++h) {
         __syncthreads();             // (the lengths are there; the last head's matrices are read)
-        float* tri = p.tri + ((long long)blockIdx.x * p.Hv + h) * (2 * DC * DC);
+        float* tri = p.tri + ((long long)blockIdx.x * p.Hv + h) * (p.planes ? DELTA_PLANES / 4 : 2 * DC * DC);
         if (warp == 0) {
             float2 b[2];
             chunk_decay(p.g + cut.t0 * p.g_ld + h, p.g_ld, cut.n, b);
@@ -141,12 +141,50 @@ __global__ void __launch_bounds__(DT) delta_chunk_kernel(const __grid_constant__
                     const int j = 8 * n + t2 + e;
                     v[e] = j < i || (j == i && warp >= 4) ? acc[n][2 * half + e] * f * s.rk[j] * decay_between(bi, s.b[j]) : 0.f;
                 }
-                float* to = warp < 4 ? s.L + i * LSQ : tri + DC * DC + i * DC;
+                float* to = warp < 4 ? s.L + i * LSQ : p.planes ? s.a + i * LSQ : tri + DC * DC + i * DC;
                 *reinterpret_cast<float2*>(to + 8 * n + t2) = make_float2(v[0], v[1]);
             }
         }
         __syncthreads();
         invert(s.L, s.inv, s.tmp);
+        if (p.planes) {
+            const float* below = s.a;
+            if (p.planes == 1) {     // A T: y is then of R, like U
+                const int n0 = (warp >> 2) * 32;
+                float at[4][4];
+                zero(at);
+                warp_mma<4>(at, Along<float>{s.a, LSQ}, Across<float>{s.inv, LSQ}, m0, n0, 0, m0 + 16);
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    float* to = s.tmp + (m0 + g) * LSQ + n0 + 8 * n + t2;
+                    *reinterpret_cast<float2*>(to) = make_float2(at[n][0], at[n][1]);
+                    *reinterpret_cast<float2*>(to + 8 * LSQ) = make_float2(at[n][2], at[n][3]);
+                }
+                below = s.tmp;
+                __syncthreads();
+            }
+            for (int i = threadIdx.x; i < 2 * DC * 8; i += DT) {
+                const int r = i >> 3, c = i & 7;
+                const float* from = (r < DC ? s.inv + r * LSQ : below + (r - DC) * LSQ) + c * 8;
+                float x[8];
+                *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(from);
+                *reinterpret_cast<float4*>(x + 4) = *reinterpret_cast<const float4*>(from + 4);
+#pragma unroll
+                for (int k = 0; k < 3; ++k) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        w[e] = bf2_pack(x[2 * e], x[2 * e + 1]);
+                        float a, b;
+                        bf2_unpack(w[e], a, b);
+                        x[2 * e] -= a;
+                        x[2 * e + 1] -= b;
+                    }
+                    reinterpret_cast<uint4*>(tri)[(k * 2 * DC + r) * 8 + (c ^ (r & 7))] = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+            continue;
+        }
         for (int i = threadIdx.x; i < DC * DC / 4; i += DT) {
             const int r = i / (DC / 4), c = i % (DC / 4) * 4;
             *reinterpret_cast<float4*>(tri + r * DC + c) = *reinterpret_cast<const float4*>(s.inv + r * LSQ + c);
@@ -361,9 +399,12 @@ cudaError_t launch_seq_delta_chunks(const SeqDeltaParams& p, bool bf16, cudaStre
     return p.Dk <= 64 ? launch_chunks<float, 64>(p, stream) : launch_chunks<float, 128>(p, stream);
 }
 
-cudaError_t launch_seq_delta_fwd(const SeqDeltaParams& p, bool bf16, cudaStream_t stream) {
+cudaError_t launch_seq_delta_fwd(const SeqDeltaParams& args, bool bf16, cudaStream_t stream) {
+    SeqDeltaParams p = args;
+    p.planes = bf16 && p.wide && p.Dv > 16 ? 1 : 0;
     const cudaError_t e = launch_seq_delta_chunks(p, bf16, stream);
     if (e != cudaSuccess) return e;
+    if (p.planes) return launch_seq_delta_walk_tc(p, stream);
     return bf16 ? launch<__nv_bfloat16>(p, stream) : launch<float>(p, stream);
 }
 

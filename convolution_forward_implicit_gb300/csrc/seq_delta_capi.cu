@@ -10,7 +10,10 @@ using namespace convfwd;
 namespace {
 
 int padded(const seq_plan* p) { return (p->W + 3) / 4 * 4; }        // a state's row, in floats
-size_t tri_bytes(const seq_plan* p) { return align256((size_t)p->slots * p->Hv * 2 * DELTA_CHUNK * DELTA_CHUNK * sizeof(float)); }
+size_t tri_bytes(const seq_plan* p) {
+    const size_t each = p->dtype == CONV_BF16 ? DELTA_PLANES : 2 * DELTA_CHUNK * DELTA_CHUNK * sizeof(float);
+    return align256((size_t)p->slots * p->Hv * each);
+}
 size_t row_bytes(const seq_plan* p) { return align256((size_t)p->slots * p->Hv * DELTA_ROWS * sizeof(float)); }
 size_t state_bytes(const seq_plan* p) { return align256((size_t)p->slots * p->Hv * p->N * padded(p) * sizeof(float)); }
 size_t token_bytes(const seq_plan* p) { return align256((size_t)p->slots * p->Hv * DELTA_CHUNK * padded(p) * sizeof(float)); }
@@ -114,6 +117,9 @@ static conv_status delta_call(seq_plan_t p, const seq_delta_args* a, seq_directi
 }
 conv_status seq_delta_fwd(seq_plan_t plan, const seq_delta_args* args, void* stream) { return delta_call(plan, args, SEQ_FWD, stream); }
 conv_status seq_delta_bwd(seq_plan_t plan, const seq_delta_args* args, void* stream) { return delta_call(plan, args, SEQ_BWD, stream); }
+conv_status seq_delta_check(seq_plan_t plan, void* stream) {
+    return plan && plan->op == Op::Delta ? check_error_word(static_cast<cudaStream_t>(stream)) : CONV_ERR_INVALID_ARG;
+}
 conv_status seq_delta_step(seq_plan_t plan, const seq_delta_args* args, void* stream) { return delta_call(plan, args, SEQ_STEP, stream); }
 
 }  // extern "C"

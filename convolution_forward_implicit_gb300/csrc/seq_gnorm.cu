@@ -1,5 +1,5 @@
 // Group norm with an activation, channels last: see gnorm.h for the formulas.  Bound by bytes.  Statistics
-// cross the whole sequence, so a call reads its rows twice: a pass for the sums of every slab of tokens and channel, a
+// cross the whole sequence, so a call reads its rows twice: a pass for the sums of every slab of tokens, a
 // small one that joins them to the groups' statistics (a warp or a block a sequence and group), and one that
 // applies them, last slabs first, so that it finds in L2 what the first pass read last.
 //
@@ -7,6 +7,9 @@
 // sums over differences from the first value it meets in a channel; that value is one of the data, so the
 // variance it takes part in is at least (its distance from the mean)^2 / n, and the rounding of the sums stays below
 // about n 2^-24 of the result for n tokens a thread, wherever the mean lies.
+//
+// One kernel that keeps a sequence's rows in the shared memory of a cluster and reads global memory once was measured
+// too, and is not kept: its CTAs load, compute and store in step (16 x 56 x 56 x 512 bf16: 63 us).
 #include "gnorm.h"
 #include "seq_common.cuh"
 #include "seq_internal.h"
@@ -14,28 +17,117 @@
 namespace convfwd {
 namespace {
 
-constexpr int GN_BLOCK = 256;        // threads a block at most (those of whole rows of threads)
+constexpr int GT = 256;              // threads a block at most
 
-// How the channels lie on a block's threads: tx threads of V channels in a row, ty rows; cblocks blocks for all channels.
+// How the channels lie on a block's threads: tx threads of V channels in a row, ty rows; cblocks blocks for all
+// channels.  grouped: no group lies in two blocks, so that a block's sums can be those of groups.
 struct GnShape {
-    int tx, ty, cblocks;
+    int tx, ty, cblocks, grouped;
 };
-GnShape gn_shape(int D, int V) {
+GnShape gn_shape(int D, int cpg, int V) {
+    int a = cpg, b = V;
+    while (b) {
+        const int r = a % b;
+        a = b;
+        b = r;
+    }
+    const long long unit = cpg / a;                   // threads whose channels are whole groups: lcm(cpg, V) / V
     const int n = (D + V - 1) / V;
     GnShape s;
-    s.cblocks = (n + GN_BLOCK - 1) / GN_BLOCK;
-    s.tx = (n + s.cblocks - 1) / s.cblocks;
-    s.ty = GN_BLOCK / s.tx;
-    if (s.ty < 2 && s.cblocks == 1) s.ty = 2;         // (up to 512 threads)
+    if (n <= GT) {
+        s.tx = n;
+        s.cblocks = s.grouped = 1;
+    } else if (unit <= GT) {
+        const int most = (int)(GT / unit * unit);
+        const int blocks = (n + most - 1) / most;
+        s.tx = (int)(((n + blocks - 1) / blocks + unit - 1) / unit * unit);
+        s.cblocks = (n + s.tx - 1) / s.tx;
+        s.grouped = 1;
+    } else {
+        s.cblocks = (n + GT - 1) / GT;
+        s.tx = (n + s.cblocks - 1) / s.cblocks;
+        s.grouped = 0;
+    }
+    s.ty = GT / s.tx;
     return s;
 }
 
-// act(z), and its slope if wanted
-template <int ACT>
-__device__ __forceinline__ float act_of(float z) {
-    return ACT == SEQ_ACT_SILU ? silu(z) : ACT == SEQ_ACT_GELU ? gelu(z) : z;
+__device__ __forceinline__ void wait_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 neg2(float2 a) { return make_float2(-a.x, -a.y); }
+__device__ __forceinline__ float2 dup(float a) { return make_float2(a, a); }
+
+// V channels of a thread, as loaded; as pairs (one channel: the second of its pair is nothing).
+template <typename T, int V>
+struct Raw {
+    static constexpr int P = V > 1 ? V / 2 : 1, W = V * sizeof(T) >= 4 ? V * sizeof(T) / 4 : 1;
+    uint32_t w[W];
+    __device__ __forceinline__ void load(const T* p) {
+        if constexpr (W == 4) {
+            const uint4 q = *reinterpret_cast<const uint4*>(p);
+            w[0] = q.x; w[1] = q.y; w[2] = q.z; w[3] = q.w;
+        } else if constexpr (W == 2) {
+            const uint2 q = *reinterpret_cast<const uint2*>(p);
+            w[0] = q.x; w[1] = q.y;
+        } else if constexpr (V * sizeof(T) == 4) {
+            w[0] = *reinterpret_cast<const uint32_t*>(p);
+        } else {
+            w[0] = (uint32_t)*reinterpret_cast<const uint16_t*>(p);
+        }
+    }
+    __device__ __forceinline__ void get(float2 (&v)[P]) const {
+        if constexpr (sizeof(T) == 2) {
+#pragma unroll
+            for (int i = 0; i < P; ++i) bf2_unpack(w[i], v[i].x, v[i].y);
+        } else if constexpr (V == 1) {
+            v[0] = make_float2(__uint_as_float(w[0]), 0.f);
+        } else {
+#pragma unroll
+            for (int i = 0; i < P; ++i) v[i] = make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+        }
+    }
+};
+template <typename T, int V>
+__device__ __forceinline__ void put(T* p, const float2 (&v)[Raw<T, V>::P]) {
+    if constexpr (V == 1) {
+        seq_st(p, v[0].x);
+    } else if constexpr (V == 2) {
+        seq_st2(p, v[0], true, true);
+    } else {
+        float f[V];
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+            f[2 * i] = v[i].x;
+            f[2 * i + 1] = v[i].y;
+        }
+        seq_stv<V>(p, f);
+    }
 }
-// d gelu = Phi(z) + z phi(z).  Phi from A&S 7.1.28 as in gelu (y^-16 = erfc |z| / sqrt 2).
+template <typename T, int V>
+__device__ __forceinline__ void channel_param(const void* from, int c, float none, float2 (&v)[Raw<T, V>::P]) {
+#pragma unroll
+    for (int i = 0; i < Raw<T, V>::P; ++i) v[i] = dup(none);
+    if (from) {
+        Raw<T, V> r;
+        r.load(static_cast<const T*>(from) + c);
+        r.get(v);
+    }
+}
+
+// act(z) of a pair, and its slope
+template <int ACT>
+__device__ __forceinline__ float2 act_of(float2 z) {
+    if (ACT == SEQ_ACT_SILU) {
+        const float2 e = mul2(z, dup(-LOG2E)), d = add2(make_float2(ex2_approx(e.x), ex2_approx(e.y)), dup(1.f));
+        return mul2(z, make_float2(rcp_approx(d.x), rcp_approx(d.y)));
+    }
+    if (ACT == SEQ_ACT_GELU) return make_float2(gelu(z.x), gelu(z.y));
+    return z;
+}
+// d gelu = Phi(z) + z phi(z).  Phi from A&S 7.1.28 as in gelu (y^-16 = erfc(|z| / sqrt 2)).
 __device__ __forceinline__ float gelu_slope(float z) {
     const float u = fabsf(z) * 0.70710678118654752f;
     float y = fmaf(u, 0.0000430638f, 0.0002765672f);
@@ -50,20 +142,21 @@ __device__ __forceinline__ float gelu_slope(float z) {
     return fmaf(z, phi, z < 0.f ? tail : 1.f - tail);
 }
 template <int ACT>
-__device__ __forceinline__ float slope_of(float z) {
-    if (ACT == SEQ_ACT_SILU) return silu_grad(z, sigmoid(z));
-    if (ACT == SEQ_ACT_GELU) return gelu_slope(z);
-    return 1.f;
+__device__ __forceinline__ float2 slope_of(float2 z) {
+    if (ACT == SEQ_ACT_SILU) {           // s (1 + z (1 - s))
+        const float2 e = mul2(z, dup(-LOG2E)), d = add2(make_float2(ex2_approx(e.x), ex2_approx(e.y)), dup(1.f));
+        const float2 s = make_float2(rcp_approx(d.x), rcp_approx(d.y));
+        return mul2(s, fma2(z, add2(dup(1.f), neg2(s)), dup(1.f)));
+    }
+    if (ACT == SEQ_ACT_GELU) return make_float2(gelu_slope(z.x), gelu_slope(z.y));
+    return dup(1.f);
 }
-
-__device__ __forceinline__ void wait_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // A thread's place: its channels c .. c + V - 1 and row of threads.
 struct GnPlace {
-    int c, tx, ty, rows;
+    int c, tx, ty;
     bool on;
-    __device__ __forceinline__ GnPlace(int V, int D, int txn, int rows_) : rows(rows_) {
+    __device__ __forceinline__ GnPlace(int V, int D, int txn) {
         ty = threadIdx.x / txn;
         tx = threadIdx.x - ty * txn;
         c = (blockIdx.y * txn + tx) * V;
@@ -71,102 +164,118 @@ struct GnPlace {
     }
 };
 
-// Channel parameters of a group norm call for V channels.
+// mean, rstd w and b of V channels of a sequence: z = (x - mean) (rstd w) + b; `stats`: of the sequence's groups
 template <typename T, int V>
-__device__ __forceinline__ void channel_param(const void* from, int c, float none, float (&v)[V]) {
-    if (from) {
-        seq_ldv<V>(static_cast<const T*>(from) + c, v);
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = none;
+struct Affine {
+    static constexpr int P = Raw<T, V>::P;
+    float2 mean[P], a[P], b[P];
+    __device__ __forceinline__ void params(const SeqGnormParams& p, int c) {
+        channel_param<T, V>(p.w, c, 1.f, a);
+        channel_param<T, V>(p.b, c, 0.f, b);
     }
-}
-
-// Rows a thread has on their way at once.
-template <bool BWD>
-constexpr int GN_AHEAD = BWD ? 2 : 4;
-
-// The sums of a slab: forward a channel's mean and sum of squared differences over the slab's tokens, backward the
-// sums of dz and dz xhat.  Empty slabs write zeros.
-template <typename T, int V, bool BWD, int ACT>
-__global__ void __launch_bounds__(2 * GN_BLOCK) gn_sums_kernel(const __grid_constant__ SeqGnormParams p, int txn, int tyn) {
-    constexpr int AHEAD = GN_AHEAD<BWD>;
-    __shared__ float2 part[2 * GN_BLOCK][V + (V > 1)];
-    const CutPiece cut = cut_piece(p.ax, blockIdx.x, p.slab);
-    const GnPlace at(V, p.D, txn, tyn);
-    const T* x = static_cast<const T*>(p.x) + (long long)cut.t0 * p.x_ld + at.c;
-    const T* dy = BWD ? static_cast<const T*>(p.dy) + (long long)cut.t0 * p.dy_ld + at.c : nullptr;
-    float a[V], b[V], shift[V];
-    float mean[V], rstd[V], w[V], bias[V];
+    // rstd: kept where it is wanted by itself
+    __device__ __forceinline__ void stats(const float2* stats, int c, int cpg, float2* rstd = nullptr) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) a[i] = b[i] = shift[i] = 0.f;
-    if (BWD && at.on && cut.n > 0) {
-        channel_param<T, V>(p.w, at.c, 1.f, w);
-        channel_param<T, V>(p.b, at.c, 0.f, bias);
-        const int cpg = p.D / p.G;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const float2 st = reinterpret_cast<const float2*>(p.coef)[(long long)cut.s * p.G + (at.c + i) / cpg];
-            mean[i] = st.x;
-            rstd[i] = st.y;
+        for (int i = 0; i < P; ++i) {
+            const float2 s0 = stats[(c + 2 * i) / cpg], s1 = V > 1 ? stats[(c + 2 * i + 1) / cpg] : s0;
+            mean[i] = make_float2(s0.x, V > 1 ? s1.x : 0.f);
+            const float2 r = make_float2(s0.y, s1.y);
+            a[i] = mul2(a[i], r);
+            if (rstd) rstd[i] = r;
         }
     }
-    int n = 0;
-    if (at.on && cut.n > 0) {
-        if (!BWD && at.ty < cut.n) seq_ldv<V>(x + at.ty * p.x_ld, shift);
-        for (int t = at.ty; t < cut.n; t += AHEAD * tyn) {
-            float v[AHEAD][V], d[BWD ? AHEAD : 1][V];
+};
+
+// Rows a thread has on their way at once.
+constexpr int AHEAD = 4, AHEAD_BWD = 2;
+
+// The sums of a slab: forward a group's (or channel's) mean and sum of squared differences, backward every
+// channel's sums of dz and dz xhat and the groups' of those times w.  Empty slabs write zeros for the channels.
+template <typename T, int V, bool BWD, int ACT>
+__global__ void __launch_bounds__(GT, BWD ? 3 : 4) gn_sums_kernel(const __grid_constant__ SeqGnormParams p, int txn, int tyn, int grouped) {
+    constexpr int P = Raw<T, V>::P, N = BWD ? AHEAD_BWD : AHEAD;
+    extern __shared__ float2 part[];                  // [tyn][txn V]
+    const CutPiece cut = cut_piece(p.ax, blockIdx.x, p.slab);
+    const GnPlace at(V, p.D, txn);
+    const int cpg = p.D / p.G;
+    float2 a[P], b[P], shift[P];
 #pragma unroll
-            for (int u = 0; u < AHEAD; ++u)
+    for (int i = 0; i < P; ++i) a[i] = b[i] = shift[i] = dup(0.f);
+    launch_next();
+    if (at.on && at.ty < cut.n) {
+        const T* x = static_cast<const T*>(p.x) + (long long)cut.t0 * p.x_ld + at.c;
+        const T* dy = BWD ? static_cast<const T*>(p.dy) + (long long)cut.t0 * p.dy_ld + at.c : nullptr;
+        Affine<T, V> f;
+        float2 rstd[BWD ? P : 1];
+        if (BWD) {
+            f.params(p, at.c);
+            f.stats(reinterpret_cast<const float2*>(p.stats) + (long long)cut.s * p.G, at.c, cpg, rstd);
+        } else {
+            Raw<T, V> r;
+            r.load(x + at.ty * p.x_ld);
+            r.get(shift);
+        }
+        int n = 0;
+        for (int t = at.ty; t < cut.n; t += N * tyn) {
+            Raw<T, V> xr[N], dr[BWD ? N : 1];
+#pragma unroll
+            for (int u = 0; u < N; ++u)
                 if (t + u * tyn < cut.n) {
-                    seq_ldv<V>(x + (t + u * tyn) * p.x_ld, v[u]);
-                    if (BWD) seq_ldv<V>(dy + (t + u * tyn) * p.dy_ld, d[BWD ? u : 0]);
+                    xr[u].load(x + (t + u * tyn) * p.x_ld);
+                    if (BWD) dr[BWD ? u : 0].load(dy + (t + u * tyn) * p.dy_ld);
                 }
 #pragma unroll
-            for (int u = 0; u < AHEAD; ++u)
+            for (int u = 0; u < N; ++u)
                 if (t + u * tyn < cut.n) {
                     ++n;
+                    float2 v[P], d[P];
+                    xr[u].get(v);
+                    if (BWD) dr[BWD ? u : 0].get(d);
 #pragma unroll
-                    for (int i = 0; i < V; ++i) {
+                    for (int i = 0; i < P; ++i) {
                         if (BWD) {
-                            const float xh = (v[u][i] - mean[i]) * rstd[i];
-                            const float dz = d[BWD ? u : 0][i] * slope_of<ACT>(fmaf(xh, w[i], bias[i]));
-                            a[i] += dz;
-                            b[i] = fmaf(dz, xh, b[i]);
+                            const float2 e = add2(v[i], neg2(f.mean[i])), dz = mul2(d[i], slope_of<ACT>(fma2(e, f.a[i], f.b[i])));
+                            a[i] = add2(a[i], dz);
+                            b[i] = fma2(dz, e, b[i]);
                         } else {
-                            const float e = v[u][i] - shift[i];
-                            a[i] += e;
-                            b[i] = fmaf(e, e, b[i]);
+                            const float2 e = add2(v[i], neg2(shift[i]));
+                            a[i] = add2(a[i], e);
+                            b[i] = fma2(e, e, b[i]);
                         }
                     }
                 }
         }
-        if (!BWD && n > 0) {
+        if (BWD) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) {           // mean and squared differences from it
-                const float m = a[i] / (float)n;
-                b[i] = fmaxf(fmaf(-a[i], m, b[i]), 0.f) + (b[i] - b[i]);      // (a NaN or infinity stays one)
-                a[i] = shift[i] + m;
+            for (int i = 0; i < P; ++i) b[i] = mul2(b[i], rstd[BWD ? i : 0]);
+        } else {                                      // mean and squared differences from it
+            const float r = 1.f / (float)n;
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                const float2 m = mul2(a[i], dup(r)), q = fma2(neg2(a[i]), m, b[i]);
+                b[i] = make_float2(q.x < 0.f ? 0.f : q.x, q.y < 0.f ? 0.f : q.y);
+                a[i] = add2(shift[i], m);
             }
         }
     }
-    launch_next();
-    if (at.ty < tyn) {
+    const int width = txn * V, c0 = blockIdx.y * width, wide = min(width, p.D - c0);
 #pragma unroll
-        for (int i = 0; i < V; ++i) part[threadIdx.x][i] = make_float2(a[i], b[i]);
+    for (int i = 0; i < P; ++i) {
+        float2* to = part + at.ty * width + at.tx * V + 2 * i;
+        if (at.ty < tyn) {
+            to[0] = make_float2(a[i].x, b[i].x);
+            if (V > 1) to[1] = make_float2(a[i].y, b[i].y);
+        }
     }
     __syncthreads();
     // the rows of threads in order; forward: row r has the tokens r, r + tyn, ... of the slab
-    for (int j = threadIdx.x; j < txn * V; j += blockDim.x) {
-        const int tx = j / V, i = j - tx * V, c = blockIdx.y * txn * V + j;
-        if (c >= p.D) continue;
-        float2 s = part[tx][i];
+    for (int j = threadIdx.x; j < wide; j += blockDim.x) {
+        float2 s = part[j];
         float sn = (float)((cut.n + tyn - 1) / tyn);
         for (int r = 1; r < tyn && (BWD || r < cut.n); ++r) {
-            const float2 o = part[r * txn + tx][i];
+            const float2 o = part[r * width + j];
             if (BWD) {
-                s.x += o.x;
-                s.y += o.y;
+                s = add2(s, o);
             } else {
                 const float on = (float)((cut.n - r + tyn - 1) / tyn), all = sn + on, d = o.x - s.x;
                 s.x = fmaf(d, on / all, s.x);
@@ -174,99 +283,138 @@ __global__ void __launch_bounds__(2 * GN_BLOCK) gn_sums_kernel(const __grid_cons
                 sn = all;
             }
         }
-        reinterpret_cast<float2*>(p.part)[(long long)blockIdx.x * p.D + c] = cut.n > 0 ? s : make_float2(0.f, 0.f);
+        if (BWD || !grouped) reinterpret_cast<float2*>(p.part)[(long long)blockIdx.x * p.D + c0 + j] = cut.n > 0 ? s : dup(0.f);
+        if (BWD && grouped && p.w) {
+            const float w = seq_ld(static_cast<const T*>(p.w) + c0 + j);
+            s = make_float2(s.x * w, s.y * w);
+        }
+        part[j] = s;
+    }
+    if (!grouped) return;
+    __syncthreads();
+    // channels of equal counts to groups: a warp a group, or a thread
+    float2* to = reinterpret_cast<float2*>(p.gpart) + (long long)blockIdx.x * p.G + c0 / cpg;
+    const int groups = wide / cpg;
+    if (cpg <= 4) {
+        for (int gi = threadIdx.x; gi < groups; gi += blockDim.x) {
+            float2 s = part[gi * cpg];
+            for (int c = 1; c < cpg; ++c) {
+                const float2 o = part[gi * cpg + c];
+                if (BWD) {
+                    s = add2(s, o);
+                } else {
+                    const float d = o.x - s.x, share = 1.f / (float)(c + 1);
+                    s.x = fmaf(d, share, s.x);
+                    s.y += o.y + d * d * ((float)cut.n * (float)c * share);
+                }
+            }
+            to[gi] = s;
+        }
+        return;
+    }
+    const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;      // (a last part of a warp takes none)
+    if (threadIdx.x >> 5 >= warps) return;
+    for (int gi = threadIdx.x >> 5; gi < groups; gi += warps) {
+        float2 s = dup(0.f);
+        const float about = BWD ? 0.f : part[gi * cpg].x;
+        for (int c = lane; c < cpg; c += 32) {
+            const float2 o = part[gi * cpg + c];
+            s = add2(s, make_float2(o.x - about, o.y));
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) s = add2(s, make_float2(__shfl_xor_sync(0xffffffffu, s.x, d), __shfl_xor_sync(0xffffffffu, s.y, d)));
+        if (!BWD) {
+            const float off = s.x / (float)cpg;
+            float q = 0.f;
+            for (int c = lane; c < cpg; c += 32) {
+                const float d = (part[gi * cpg + c].x - about) - off;
+                q = fmaf(d, d, q);
+            }
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) q += __shfl_xor_sync(0xffffffffu, q, d);
+            s = make_float2(about + off, fmaf((float)cut.n, q, s.y));
+        }
+        if (lane == 0) to[gi] = s;
     }
 }
 
-// Sum over the threads of a group: the lanes of a warp, or all of a block of GN_BLOCK.
+// Sum over the threads of a group: the lanes of a warp, or all of a block of GT.
 template <bool BLOCK>
-__device__ __forceinline__ float group_sum(float v, float* buf) {
+__device__ __forceinline__ float2 group_sum(float2 v, float2* buf) {
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+    for (int d = 16; d > 0; d >>= 1) v = add2(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, d), __shfl_xor_sync(0xffffffffu, v.y, d)));
     if (!BLOCK) return v;
     __syncthreads();
     if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
     __syncthreads();
-    float s = 0.f;
+    float2 s = buf[0];
 #pragma unroll
-    for (int i = 0; i < GN_BLOCK / 32; ++i) s += buf[i];
+    for (int i = 1; i < GT / 32; ++i) s = add2(s, buf[i]);
     return s;
 }
 
-// Statistics of a sequence and group from its slabs' and channels': a warp (BLOCK: a block) each.
-template <bool BLOCK>
-__global__ void __launch_bounds__(GN_BLOCK) gn_stats_kernel(const __grid_constant__ SeqGnormParams p) {
-    __shared__ float buf[GN_BLOCK / 32];
+// A sequence's group from its slabs' entries, a warp (BLOCK: a block) each: forward mean and rstd, backward the means of
+// dz w and dz w xhat.  An entry of `part` is a group's (sub = 1), or a channel's (sub = channels of a group).
+template <typename T, bool BWD, bool BLOCK>
+__global__ void __launch_bounds__(GT) gn_join_kernel(const __grid_constant__ SeqGnormParams p, int grouped) {
+    __shared__ float2 buf[GT / 32];
     launch_next();
-    wait_before();
-    const long long at = BLOCK ? blockIdx.x : (long long)blockIdx.x * (GN_BLOCK / 32) + (threadIdx.x >> 5);
+    const long long at = BLOCK ? blockIdx.x : (long long)blockIdx.x * (GT / 32) + (threadIdx.x >> 5);
     if (at >= (long long)p.ax.S * p.G) return;          // (whole warps)
-    const int s = (int)(at / p.G), gi = (int)(at - (long long)s * p.G), cpg = p.D / p.G;
+    const int s = (int)(at / p.G), gi = (int)(at - (long long)s * p.G), cpg = p.D / p.G, sub = grouped ? 1 : cpg;
     const int t0 = p.ax.L > 0 ? s * p.ax.L : seq_start(p.ax, s, 0), t1 = p.ax.L > 0 ? t0 + p.ax.L : seq_start(p.ax, s + 1, t0);
     const int len = t1 - t0, slabs = (len + p.slab - 1) / p.slab;
-    const float2* from = reinterpret_cast<const float2*>(p.part) + (long long)cut_base(p.ax, s, p.slab) * p.D + gi * cpg;
-    const int step = BLOCK ? GN_BLOCK : 32, first = BLOCK ? threadIdx.x : threadIdx.x & 31;
-    const long long all = (long long)slabs * cpg;
-    const float tokens = (float)p.slab, rest = (float)(len - (slabs - 1) * p.slab);
-    float sum = 0.f, m2 = 0.f;
-    // about the first slab's and channel's mean, so that small differences of large means survive
-    const float about = len > 0 ? from[0].x : 0.f;
-    for (long long i = first; i < all; i += step) {
-        const int k = (int)(i / cpg);
-        sum = fmaf((from[(long long)k * p.D + (i - (long long)k * cpg)].x - about), k == slabs - 1 ? rest : tokens, sum);
-    }
+    const long long row = grouped ? p.G : p.D;
+    const float2* from = reinterpret_cast<const float2*>(grouped ? p.gpart : p.part) + (long long)cut_base(p.ax, s, p.slab) * row + gi * sub;
+    // a thread takes every kstep-th slab's entries c0, c0 + cstep, ...
+    const int step = BLOCK ? GT : 32, first = BLOCK ? threadIdx.x : threadIdx.x & 31;
+    const int per = sub < step ? sub : step, k0 = first / per, c0 = first - k0 * per, kstep = step / per;
+    const bool on = k0 < kstep;
+    const float each = (float)(cpg / sub), tokens = (float)p.slab * each, rest = (float)(len - (slabs - 1) * p.slab) * each;
     const float count = (float)len * (float)cpg;
-    sum = group_sum<BLOCK>(sum, buf);
-    const float shift = len > 0 ? sum / count : 0.f, mean = about + shift;
-    for (long long i = first; i < all; i += step) {
-        const int k = (int)(i / cpg);
-        const float2 v = from[(long long)k * p.D + (i - (long long)k * cpg)];
-        const float d = (v.x - about) - shift;
-        m2 += fmaf(d * d, k == slabs - 1 ? rest : tokens, v.y);
+    wait_before();
+    float2 st = dup(0.f);
+    if (BWD) {
+        const T* w = grouped ? nullptr : static_cast<const T*>(p.w);
+        for (int k = k0; on && k < slabs; k += kstep)
+            for (int c = c0; c < sub; c += per) {
+                const float2 v = from[k * row + c];
+                const float wc = w ? seq_ld(w + gi * cpg + c) : 1.f;
+                st = fma2(dup(wc), v, st);
+            }
+        st = group_sum<BLOCK>(st, buf);
+        if (len > 0) st = make_float2(st.x / count, st.y / count);
+        if (first == 0) reinterpret_cast<float2*>(p.coef)[at] = st;
+        return;
     }
-    m2 = group_sum<BLOCK>(m2, buf);
+    // about the first entry's mean, so that small differences of large means survive
+    const float about = len > 0 ? from[0].x : 0.f;
+    float sum = 0.f;
+    for (int k = k0; on && k < slabs; k += kstep)
+        for (int c = c0; c < sub; c += per) sum = fmaf(from[k * row + c].x - about, k == slabs - 1 ? rest : tokens, sum);
+    sum = group_sum<BLOCK>(make_float2(sum, 0.f), buf).x;
+    const float shift = len > 0 ? sum / count : 0.f;
+    float m2 = 0.f;
+    for (int k = k0; on && k < slabs; k += kstep)
+        for (int c = c0; c < sub; c += per) {
+            const float2 v = from[k * row + c];
+            const float d = (v.x - about) - shift;
+            m2 += fmaf(d * d, k == slabs - 1 ? rest : tokens, v.y);
+        }
+    m2 = group_sum<BLOCK>(make_float2(m2, 0.f), buf).x;
     if (first == 0) {
-        const float2 st = len > 0 ? make_float2(mean, 1.f / sqrtf(m2 / count + p.eps)) : make_float2(0.f, 0.f);
+        if (len > 0) st = make_float2(about + shift, 1.f / sqrtf(m2 / count + p.eps));
         reinterpret_cast<float2*>(p.coef)[at] = st;
         if (p.stats) reinterpret_cast<float2*>(p.stats)[at] = st;
     }
 }
 
-// Backward: the group's means of dz w and dz w xhat.
-template <typename T, bool BLOCK>
-__global__ void __launch_bounds__(GN_BLOCK) gn_means_kernel(const __grid_constant__ SeqGnormParams p) {
-    __shared__ float buf[GN_BLOCK / 32];
-    launch_next();
-    wait_before();
-    const long long at = BLOCK ? blockIdx.x : (long long)blockIdx.x * (GN_BLOCK / 32) + (threadIdx.x >> 5);
-    if (at >= (long long)p.ax.S * p.G) return;
-    const int s = (int)(at / p.G), gi = (int)(at - (long long)s * p.G), cpg = p.D / p.G;
-    const int t0 = p.ax.L > 0 ? s * p.ax.L : seq_start(p.ax, s, 0), t1 = p.ax.L > 0 ? t0 + p.ax.L : seq_start(p.ax, s + 1, t0);
-    const int len = t1 - t0, slabs = (len + p.slab - 1) / p.slab;
-    const float2* from = reinterpret_cast<const float2*>(p.part) + (long long)cut_base(p.ax, s, p.slab) * p.D + gi * cpg;
-    const int step = BLOCK ? GN_BLOCK : 32, first = BLOCK ? threadIdx.x : threadIdx.x & 31;
-    const T* w = static_cast<const T*>(p.w);
-    float m1 = 0.f, m2 = 0.f;
-    for (long long i = first; i < (long long)slabs * cpg; i += step) {
-        const int k = (int)(i / cpg), c = (int)(i - (long long)k * cpg);
-        const float2 v = from[(long long)k * p.D + c];
-        const float wc = w ? seq_ld(w + gi * cpg + c) : 1.f;
-        m1 = fmaf(wc, v.x, m1);
-        m2 = fmaf(wc, v.y, m2);
-    }
-    m1 = group_sum<BLOCK>(m1, buf);
-    m2 = group_sum<BLOCK>(m2, buf);
-    if (first == 0) {
-        const float count = (float)len * (float)cpg;
-        reinterpret_cast<float2*>(p.coef)[at] = len > 0 ? make_float2(m1 / count, m2 / count) : make_float2(0.f, 0.f);
-    }
-}
-
 // dw and db: the slabs' sums of all sequences in order.
 __global__ void __launch_bounds__(COLUMN_THREADS, 2) gn_param_kernel(const __grid_constant__ SeqGnormParams p) {
-    wait_before();
     const long long col = (long long)blockIdx.x * 32 + (threadIdx.x & 31);      // db and dw of a channel side by side
     const bool on = col < 2LL * p.D;
+    launch_next();
+    wait_before();
     const float v = column_sum(p.part + col, 2LL * p.D, p.slots, on);
     if (threadIdx.x < 32 && on) {
         float* to = col & 1 ? p.dw : p.db;
@@ -274,115 +422,162 @@ __global__ void __launch_bounds__(COLUMN_THREADS, 2) gn_param_kernel(const __gri
     }
 }
 
-// y, or dx, of a slab.
-template <typename T, int V, bool BWD, int ACT>
-__global__ void __launch_bounds__(2 * GN_BLOCK) gn_apply_kernel(const __grid_constant__ SeqGnormParams p, int txn, int tyn) {
-    constexpr int AHEAD = GN_AHEAD<BWD>;
-    const CutPiece cut = cut_piece(p.ax, gridDim.x - 1 - blockIdx.x, p.slab);
-    const GnPlace at(V, p.D, txn, tyn);
-    float w[V], bias[V], mean[V], rstd[V];
-    const bool on = at.on && at.ty < tyn && cut.n > 0;
-    if (on) {
-        channel_param<T, V>(p.w, at.c, 1.f, w);
-        channel_param<T, V>(p.b, at.c, 0.f, bias);
-    }
-    wait_before();
-    if (!on) return;
-    const int cpg = p.D / p.G;
-    const float2* stats = reinterpret_cast<const float2*>(BWD ? p.stats : p.coef) + (long long)cut.s * p.G;
-    float m1[BWD ? V : 1], m2[BWD ? V : 1];
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int gi = (at.c + i) / cpg;
-        if (BWD) {
-            const float2 m = reinterpret_cast<const float2*>(p.coef)[(long long)cut.s * p.G + gi];
-            m1[BWD ? i : 0] = m.x;
-            m2[BWD ? i : 0] = m.y;
+// The groups' joined entries of a sequence (see gn_join_kernel), by every block for its own channels: `groups` of them from
+// g0 on, to `to` (shared memory; `buf`: 2 float2 a thread).  Sums of the differences d from the first slab's mean and of
+// their squares: M2 = sum (M2k + nk d^2) - (sum nk d)^2 / n; the first slab is one of the data, so that this loses about
+// as little as a thread's own sums do.
+template <bool BWD>
+__device__ __forceinline__ void join_groups(const SeqGnormParams& p, const CutPiece& cut, int g0, int groups, float2* to, float2* buf) {
+    const int parts = blockDim.x / groups, gi = threadIdx.x % groups, k0 = threadIdx.x / groups, cpg = p.D / p.G;
+    const int t0 = cut.t0 - cut.index * p.slab, t1 = p.ax.L > 0 ? t0 + p.ax.L : seq_start(p.ax, cut.s + 1, t0);
+    const int len = t1 - t0, slabs = (len + p.slab - 1) / p.slab;
+    const float2* from = reinterpret_cast<const float2*>(p.gpart) + (long long)cut_base(p.ax, cut.s, p.slab) * p.G + g0 + gi;
+    const float tokens = (float)p.slab * (float)cpg, rest = (float)(len - (slabs - 1) * p.slab) * (float)cpg, count = (float)len * (float)cpg;
+    float2 st = dup(0.f);
+    float about = 0.f;
+    if (k0 < parts) {
+        if (!BWD) about = from[0].x;
+#pragma unroll 4
+        for (int k = k0; k < slabs; k += parts) {
+            const float2 v = from[(long long)k * p.G];
+            if (BWD) {
+                st = add2(st, v);
+            } else {
+                const float d = v.x - about, n = k == slabs - 1 ? rest : tokens;
+                st.x = fmaf(n, d, st.x);
+                st.y += fmaf(n * d, d, v.y);
+            }
         }
-        const float2 st = stats[gi];
-        mean[i] = st.x;
-        rstd[i] = st.y;
+        buf[threadIdx.x] = st;
+    }
+    __syncthreads();
+    if (threadIdx.x < groups) {
+        st = buf[threadIdx.x];
+        for (int k = 1; k < parts; ++k) st = add2(st, buf[k * groups + threadIdx.x]);
+        if (BWD) {
+            st = make_float2(st.x / count, st.y / count);
+        } else {
+            const float shift = st.x / count, var = fmaf(-shift, shift, st.y / count);
+            st = make_float2(about + shift, 1.f / sqrtf((var < 0.f ? 0.f : var) + p.eps));
+            if (p.stats && cut.index == 0) reinterpret_cast<float2*>(p.stats)[(long long)cut.s * p.G + g0 + threadIdx.x] = st;
+        }
+        to[threadIdx.x] = st;
+    }
+    __syncthreads();
+}
+
+// y, or dx, of a slab.  SELF: the block joins its groups' entries itself.
+template <typename T, int V, bool BWD, int ACT, bool SELF>
+__global__ void __launch_bounds__(GT, BWD ? 3 : 4) gn_apply_kernel(const __grid_constant__ SeqGnormParams p, int txn, int tyn) {
+    constexpr int P = Raw<T, V>::P, N = BWD ? AHEAD_BWD : AHEAD;
+    __shared__ float2 joined[SELF ? GT : 1], buf[SELF ? GT : 1];
+    const CutPiece cut = cut_piece(p.ax, gridDim.x - 1 - blockIdx.x, p.slab);
+    const GnPlace at(V, p.D, txn);
+    const bool on = at.on && at.ty < tyn && at.ty < cut.n;
+    const int cpg = p.D / p.G;
+    Affine<T, V> f;
+    if (on) f.params(p, at.c);
+    wait_before();
+    if (SELF) {
+        if (cut.n <= 0) return;
+        const int g0 = blockIdx.y * txn * V / cpg;
+        join_groups<BWD>(p, cut, g0, min(txn * V, p.D - blockIdx.y * txn * V) / cpg, joined, buf);
+    }
+    if (!on) return;
+    float2 c1[BWD ? P : 1], c2[BWD ? P : 1], rstd[BWD ? P : 1];
+    const long long first = (long long)cut.s * p.G;
+    const float2* join = SELF ? joined - blockIdx.y * txn * V / cpg : reinterpret_cast<const float2*>(p.coef) + first;
+    f.stats(BWD ? reinterpret_cast<const float2*>(p.stats) + first : join, at.c, cpg, BWD ? rstd : nullptr);
+    if (BWD) {                                        // dx = rstd w dz - rstd m1 - (x - mean) rstd^2 m2
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const float2 m0 = join[(at.c + 2 * i) / cpg], m1 = V > 1 ? join[(at.c + 2 * i + 1) / cpg] : m0;
+            const float2 r = rstd[BWD ? i : 0];
+            c1[BWD ? i : 0] = mul2(make_float2(-m0.x, -m1.x), r);
+            c2[BWD ? i : 0] = mul2(make_float2(-m0.y, -m1.y), mul2(r, r));
+        }
     }
     const T* x = static_cast<const T*>(p.x) + (long long)cut.t0 * p.x_ld + at.c;
     const T* dy = BWD ? static_cast<const T*>(p.dy) + (long long)cut.t0 * p.dy_ld + at.c : nullptr;
     T* to = static_cast<T*>(BWD ? p.dx : p.y) + (long long)cut.t0 * (BWD ? p.dx_ld : p.y_ld) + at.c;
     const long long to_ld = BWD ? p.dx_ld : p.y_ld;
-    for (int t = at.ty; t < cut.n; t += AHEAD * tyn) {
-        float v[AHEAD][V], d[BWD ? AHEAD : 1][V];
+    for (int t = at.ty; t < cut.n; t += N * tyn) {
+        Raw<T, V> xr[N], dr[BWD ? N : 1];
 #pragma unroll
-        for (int u = 0; u < AHEAD; ++u)
+        for (int u = 0; u < N; ++u)
             if (t + u * tyn < cut.n) {
-                seq_ldv<V>(x + (t + u * tyn) * p.x_ld, v[u]);
-                if (BWD) seq_ldv<V>(dy + (t + u * tyn) * p.dy_ld, d[BWD ? u : 0]);
+                xr[u].load(x + (t + u * tyn) * p.x_ld);
+                if (BWD) dr[BWD ? u : 0].load(dy + (t + u * tyn) * p.dy_ld);
             }
 #pragma unroll
-        for (int u = 0; u < AHEAD; ++u)
+        for (int u = 0; u < N; ++u)
             if (t + u * tyn < cut.n) {
-                float out[V];
+                float2 v[P], d[P];
+                xr[u].get(v);
+                if (BWD) dr[BWD ? u : 0].get(d);
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const float xh = (v[u][i] - mean[i]) * rstd[i];
-                    const float z = fmaf(xh, w[i], bias[i]);
+                for (int i = 0; i < P; ++i) {
+                    const float2 e = add2(v[i], neg2(f.mean[i])), z = fma2(e, f.a[i], f.b[i]);
                     if (BWD) {
-                        const float dn = d[BWD ? u : 0][i] * slope_of<ACT>(z) * w[i];
-                        out[i] = rstd[i] * ((dn - m1[BWD ? i : 0]) - xh * m2[BWD ? i : 0]);
+                        const float2 r = fma2(e, c2[BWD ? i : 0], c1[BWD ? i : 0]);
+                        v[i] = fma2(f.a[i], mul2(d[i], slope_of<ACT>(z)), r);
                     } else {
-                        out[i] = act_of<ACT>(z);
+                        v[i] = act_of<ACT>(z);
                     }
                 }
-                seq_stv<V>(to + (t + u * tyn) * to_ld, out);
+                put<T, V>(to + (t + u * tyn) * to_ld, v);
             }
     }
 }
 
 template <typename T, int V, bool BWD, int ACT>
 cudaError_t launch_act(const SeqGnormParams& p, cudaStream_t stream) {
-    const GnShape s = gn_shape(p.D, V);
+    const GnShape s = gn_shape(p.D, p.D / p.G, V);
     const dim3 grid((unsigned)p.slots, (unsigned)s.cblocks), block((unsigned)(s.tx * s.ty));
-    SeqGnormParams sums = p;
-    if (BWD) sums.coef = p.stats;                      // (the sums need the forward call's statistics there)
-    cudaError_t e = launch_kernel(gn_sums_kernel<T, V, BWD, ACT>, grid, block, 0, stream, false, 1, sums, s.tx, s.ty);
+    cudaError_t e = launch_kernel(gn_sums_kernel<T, V, BWD, ACT>, grid, block, (size_t)s.tx * s.ty * V * sizeof(float2), stream, false, 1, p, s.tx, s.ty, s.grouped);
     if (e != cudaSuccess) return e;
-    const long long groups = (long long)p.ax.S * p.G;
-    // entries of a sequence's group: with few of them a warp each, else a block
-    const long long entries = (long long)(p.ax.T / p.ax.S / p.slab + 1) * (p.D / p.G);
-    const bool big = entries > 512;
-    const dim3 sgrid((unsigned)(big ? groups : (groups + GN_BLOCK / 32 - 1) / (GN_BLOCK / 32)));
-    if (BWD)
-        e = launch_kernel(big ? gn_means_kernel<T, true> : gn_means_kernel<T, false>, sgrid, dim3(GN_BLOCK), 0, stream, true, 1, p);
-    else
-        e = launch_kernel(big ? gn_stats_kernel<true> : gn_stats_kernel<false>, sgrid, dim3(GN_BLOCK), 0, stream, true, 1, p);
-    if (e == cudaSuccess) e = launch_kernel(gn_apply_kernel<T, V, BWD, ACT>, grid, block, 0, stream, true, 1, p, s.tx, s.ty);
+    const long long groups = (long long)p.ax.S * p.G, slabs = p.ax.T / p.ax.S / p.slab + 1;
+    const int own = s.tx * V / (p.D / p.G);           // groups of a block
+    // few entries: every block joins its groups' itself, one launch less.  (Unequal lengths with
+    // statistics wanted go the other way: empty sequences have statistics too.)
+    const bool self = s.grouped && own <= s.tx * s.ty && own * slabs <= 16 * GT && (BWD || !p.stats || p.ax.L > 0);
+    if (!self) {
+        // a warp for a few entries, a block for many
+        const bool big = slabs * (s.grouped ? 1 : p.D / p.G) > 256;
+        const dim3 jgrid((unsigned)(big ? groups : (groups + GT / 32 - 1) / (GT / 32)));
+        e = launch_kernel(big ? gn_join_kernel<T, BWD, true> : gn_join_kernel<T, BWD, false>, jgrid, dim3(GT), 0, stream, true, 1, p, s.grouped);
+    }
     if (BWD && e == cudaSuccess && (p.dw || p.db))
-        e = launch_kernel(gn_param_kernel, dim3((unsigned)((2LL * p.D + 31) / 32)), dim3(COLUMN_THREADS), 0, stream, false, 1, p);
+        e = launch_kernel(gn_param_kernel, dim3((unsigned)((2LL * p.D + 31) / 32)), dim3(COLUMN_THREADS), 0, stream, true, 1, p);
+    if (e == cudaSuccess)
+        e = launch_kernel(self ? gn_apply_kernel<T, V, BWD, ACT, true> : gn_apply_kernel<T, V, BWD, ACT, false>, grid, block, 0, stream, true, 1, p, s.tx, s.ty);
     return e;
 }
-
+template <typename T, int V, bool BWD>
+cudaError_t launch_v(const SeqGnormParams& p, cudaStream_t stream) {
+    if (p.act == SEQ_ACT_SILU) return launch_act<T, V, BWD, SEQ_ACT_SILU>(p, stream);
+    if (p.act == SEQ_ACT_GELU) return launch_act<T, V, BWD, SEQ_ACT_GELU>(p, stream);
+    return launch_act<T, V, BWD, SEQ_ACT_NONE>(p, stream);
+}
 template <typename T, bool BWD>
 cudaError_t launch(const SeqGnormParams& p, cudaStream_t stream) {
     if (p.slots == 0) return cudaSuccess;
-    if (p.vec) {
-        if (p.act == SEQ_ACT_SILU) return launch_act<T, 8, BWD, SEQ_ACT_SILU>(p, stream);
-        if (p.act == SEQ_ACT_GELU) return launch_act<T, 8, BWD, SEQ_ACT_GELU>(p, stream);
-        return launch_act<T, 8, BWD, 0>(p, stream);
-    }
-    if (p.act == SEQ_ACT_SILU) return launch_act<T, 1, BWD, SEQ_ACT_SILU>(p, stream);
-    if (p.act == SEQ_ACT_GELU) return launch_act<T, 1, BWD, SEQ_ACT_GELU>(p, stream);
-    return launch_act<T, 1, BWD, 0>(p, stream);
+    if (p.grain == 16) return launch_v<T, 16 / sizeof(T), BWD>(p, stream);
+    return p.grain ? launch_v<T, 2, BWD>(p, stream) : launch_v<T, 1, BWD>(p, stream);
 }
 
 }  // namespace
 
-// Tokens of a slab: about four blocks of 256 threads an SM, 8 tokens at least and 256 at most.
-int seq_gnorm_slab(long long S, long long T, int D, int sms) {
-    const GnShape s = gn_shape(D, 8);
-    const long long L = S > 0 && T > S ? T / S : 1, want = 4LL * sms;
+// Tokens of a slab: one round of four blocks an SM, 4 tokens a thread at least and 64 at most.
+int seq_gnorm_slab(long long S, long long T, int D, int G, int esize, int sms) {
+    const GnShape s = gn_shape(D, D / G, 16 / esize);
+    const long long L = S > 0 && T > S ? T / S : 1, want = 4LL * sms * (s.tx * s.ty <= 128 ? 2 : 1);
     long long slabs = want / ((S < 1 ? 1 : S) * s.cblocks);          // of a sequence
     if (slabs < 1) slabs = 1;
     long long len = (L + slabs - 1) / slabs;
-    const long long least = 8 * (s.ty < 1 ? 1 : s.ty) > 64 ? 64 : 8;
-    if (len < least) len = least;
-    return (int)(len > 256 ? 256 : len);
+    if (len < 4 * s.ty) len = 4 * s.ty;
+    if (len > 64 * s.ty) len = 64 * s.ty;
+    return (int)len;
 }
 
 cudaError_t launch_seq_gnorm_fwd(const SeqGnormParams& p, bool bf16, cudaStream_t stream) {

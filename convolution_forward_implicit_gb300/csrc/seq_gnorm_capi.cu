@@ -5,6 +5,13 @@
 
 using namespace convfwd;
 
+namespace {
+
+size_t part_bytes(const seq_plan* p) { return align256((size_t)p->slots * p->D * 2 * sizeof(float)); }
+size_t gpart_bytes(const seq_plan* p) { return align256((size_t)p->slots * p->G * 2 * sizeof(float)); }
+
+}  // namespace
+
 extern "C" {
 
 conv_status seq_gnorm_plan_create(seq_plan_t* out, int64_t S, int64_t T, int64_t D, int64_t G, conv_dtype dtype,
@@ -21,14 +28,14 @@ conv_status seq_gnorm_plan_create(seq_plan_t* out, int64_t S, int64_t T, int64_t
     p->G = (int)G;
     p->act = (int)act;
     p->eps = eps;
-    p->run = seq_gnorm_slab(S, T, p->D, p->sms);
+    p->run = seq_gnorm_slab(S, T, p->D, p->G, (int)p->esize(), p->sms);
     const int64_t slots = cut_slots(S, T, p->L, p->run);
     if (slots > INT32_MAX) {
         delete p;
         return CONV_ERR_UNSUPPORTED;
     }
     p->slots = (int)slots;
-    p->ws_bytes = align256((size_t)slots * D * 2 * sizeof(float)) + align256((size_t)S * G * 2 * sizeof(float));
+    p->ws_bytes = part_bytes(p) + gpart_bytes(p) + align256((size_t)S * G * 2 * sizeof(float));
     snprintf(p->desc, sizeof p->desc,
              "op=gnorm direction=%s dtype=%s sequences=%d tokens=%d ragged=%d width=%d groups=%d act=%s slabs=%d slab_tokens=%d",
              dir_name(direction), type_name(dtype), p->S, p->T, p->ragged(), p->D, p->G,
@@ -60,6 +67,13 @@ static conv_status gnorm_call(seq_plan_t p, const seq_gnorm_args* a, seq_directi
     }
     if (c.st != CONV_OK) return c.st;
     if (!p->ws) return CONV_ERR_WORKSPACE;
+    bool paired = true;                  // rows of aligned pairs of elements: 4 bytes of bf16, 8 of fp32
+    auto pairs = [&](const void* v, int64_t ld) { paired = paired && reinterpret_cast<uintptr_t>(v) % (2 * e) == 0 && ld % 2 == 0; };
+    pairs(a->x, a->x_ld);
+    pairs(a->w, 0);
+    pairs(a->b, 0);
+    pairs(bwd ? a->dy : a->y, bwd ? a->dy_ld : a->y_ld);
+    if (bwd) pairs(a->dx, a->dx_ld);
     SeqGnormParams q = {};
     q.ax = p->axis(a->starts);
     q.D = p->D; q.G = p->G; q.act = p->act; q.eps = p->eps;
@@ -68,8 +82,9 @@ static conv_status gnorm_call(seq_plan_t p, const seq_gnorm_args* a, seq_directi
     q.stats = a->stats; q.dw = a->dw; q.db = a->db;
     q.x_ld = a->x_ld; q.y_ld = a->y_ld; q.dy_ld = a->dy_ld; q.dx_ld = a->dx_ld;
     q.part = static_cast<float*>(p->ws);
-    q.coef = reinterpret_cast<float*>(static_cast<unsigned char*>(p->ws) + align256((size_t)p->slots * p->D * 2 * sizeof(float)));
-    q.vec = c.wide && p->D % 8 == 0;
+    q.gpart = q.part + part_bytes(p) / sizeof(float);
+    q.coef = q.gpart + gpart_bytes(p) / sizeof(float);
+    q.grain = c.wide && (p->D * e) % 16 == 0 ? 16 : p->D % 2 == 0 && paired ? 2 : 0;
     q.sms = p->sms;
     const bool bf16 = p->dtype == CONV_BF16;
     cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -195,16 +195,18 @@ struct SeqGnormParams {
     float *stats, *dw, *db;
     long long x_ld, y_ld, dy_ld, dx_ld;
     float* part;                    // [slots][D][2]: a slab's mean and sum of squared differences; backward: sums
+    float* gpart;                   // [slots][G][2]: the same of groups
     float* coef;                    // [S][G][2]: mean and rstd; backward: the group's two means
-    int vec;                        // 1: rows of whole 16-byte aligned groups of 8
+    int grain;                      // rows in whole aligned groups of 16 bytes: 16, of pairs of elements: 2, else 0
     int sms;
 };
 cudaError_t launch_seq_gnorm_fwd(const SeqGnormParams& p, bool bf16, cudaStream_t stream);
 cudaError_t launch_seq_gnorm_bwd(const SeqGnormParams& p, bool bf16, cudaStream_t stream);
-int seq_gnorm_slab(long long S, long long T, int D, int sms);
+int seq_gnorm_slab(long long S, long long T, int D, int G, int esize, int sms);
 
 // ---- gated delta rule ----
 constexpr int DELTA_CHUNK = 64;     // tokens worked on at once; saved states lie at every chunk's first token
+constexpr int DELTA_PLANES = 3 * 128 * 128;      // bytes of a chunk's matrices in parts
 constexpr int DELTA_ROWS = 264;     // floats of a chunk's row factors (see seq_delta.cuh)
 struct SeqDeltaParams {
     SeqAxis ax;
@@ -218,7 +220,9 @@ struct SeqDeltaParams {
     long long q_ld, k_ld, v_ld, g_ld, beta_ld, y_ld, dy_ld, dq_ld, dk_ld, dv_ld, dg_ld, dbeta_ld;
     int slots;                      // chunks of the token axis at most
     // workspace, by chunk and value head
-    float* tri;                     // [slots][Hv][2][64][64]: T and A
+    float* tri;                     // [slots][Hv]: T and A, [2][64][64] fp32; or (planes) [3][128][64] bf16: the three
+                                    // parts of [T; A T] (1) or [T; A] (2), rows of 128 bytes in the 128-byte swizzle
+    int planes;
     float* rows;                    // [slots][Hv][DELTA_ROWS]
     float* dstate;                  // backward: [slots][Hv][Dk][Dvp] gradient at the state a chunk leaves
     float* dr;                      // backward: [slots][Hv][64][Dvp]
@@ -231,6 +235,7 @@ struct SeqDeltaParams {
 };
 cudaError_t launch_seq_delta_fwd(const SeqDeltaParams& p, bool bf16, cudaStream_t stream);
 cudaError_t launch_seq_delta_bwd(const SeqDeltaParams& p, bool bf16, cudaStream_t stream);
+cudaError_t launch_seq_delta_walk_tc(const SeqDeltaParams& p, cudaStream_t stream);
 cudaError_t launch_seq_delta_step(const SeqDeltaParams& p, bool bf16, cudaStream_t stream);
 
 }  // namespace convfwd

@@ -11,9 +11,11 @@ from __future__ import annotations
 import ctypes
 
 from . import seq as _seq
+from .binding import CONV_OK, ConvError
 from .seq import SEQ_RAGGED, _SeqPlan
 
-__all__ = ["SEQ_DELTA_QK_NORM", "DELTA_EXPORTED", "seq_delta_plan_create", "seq_delta_saved_bytes", "SeqDeltaPlan"]
+__all__ = ["SEQ_DELTA_QK_NORM", "DELTA_EXPORTED", "seq_delta_plan_create", "seq_delta_saved_bytes", "seq_delta_check",
+           "SeqDeltaPlan"]
 
 SEQ_DELTA_QK_NORM = 512
 
@@ -21,6 +23,7 @@ _I64, _I, _U = ctypes.c_int64, ctypes.c_int, ctypes.c_uint
 _SIGS = {
     "seq_delta_plan_create": (ctypes.c_int, [_seq._PLAN, _I64, _I64, _I64, _I64, _I64, _I64, _I, _I, _U, ctypes.c_float]),
     "seq_delta_saved_bytes": (ctypes.c_size_t, [ctypes.c_void_p]),
+    "seq_delta_check": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p]),
     "seq_delta_fwd": _seq._CALL, "seq_delta_bwd": _seq._CALL, "seq_delta_step": _seq._CALL,
 }
 DELTA_EXPORTED = tuple(_SIGS)
@@ -50,6 +53,12 @@ def seq_delta_saved_bytes(plan: int) -> int:
     return int(_library().seq_delta_saved_bytes(plan))
 
 
+def seq_delta_check(plan: int, stream: int):
+    st = _library().seq_delta_check(plan, stream)
+    if st != CONV_OK:
+        raise ConvError(st, "seq_delta_check")
+
+
 class SeqDeltaPlan(_SeqPlan):
     """Gated delta rule over S sequences on T tokens (seq_delta_*): Hk key heads of Dk values hold q and k, Hv value
     heads of Dv values v and y; g and beta are (T, Hv) float32, states (slots, Hv, Dk, Dv) float32.  `qk_norm` divides q
@@ -75,6 +84,11 @@ class SeqDeltaPlan(_SeqPlan):
         import torch
         return torch.empty(self.saved_bytes // 4, dtype=torch.float32,
                            device=device or torch.device("cuda", torch.cuda.current_device()))
+
+    def check(self, stream=None):
+        """Wait for the stream; raise if a kernel's wait for the tensor cores ran out (see seq_delta_check)."""
+        import torch
+        seq_delta_check(self.handle, torch.cuda.current_stream().cuda_stream if stream is None else stream)
 
     def _common(self, direction, q, k, v, g, beta):
         vals = self._values(q, direction)

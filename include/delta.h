@@ -66,6 +66,10 @@ typedef struct {
 
 conv_status seq_delta_fwd(seq_plan_t plan, const seq_delta_args* args, void* stream);
 conv_status seq_delta_bwd(seq_plan_t plan, const seq_delta_args* args, void* stream);
+/* The bf16 kernels wait for the tensor cores and for copies, for one second at most.  Waits for the stream (not while it
+ * is captured) and returns CONV_ERR_TIMEOUT if a wait ran out since the last check (of any plan, conv_plan_check's among
+ * them): the results of the calls between are not to be used. */
+conv_status seq_delta_check(seq_plan_t plan, void* stream);
 /* One token per sequence: q and k are S x Hk*Dk, v and y S x Hv*Dv, g and beta S x Hv. */
 conv_status seq_delta_step(seq_plan_t plan, const seq_delta_args* args, void* stream);
 
