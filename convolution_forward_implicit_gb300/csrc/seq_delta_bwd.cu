@@ -447,7 +447,8 @@ template <typename T>
 cudaError_t launch(const SeqDeltaParams& p, cudaStream_t stream) {
     const bool narrow = p.Dv <= 16 || p.ax.S * (long long)p.Hv * ((p.Dv + 31) / 32) < p.sms;
     cudaError_t e;
-    if (p.Dk <= 64) e = narrow ? launch_back<T, 64, 16>(p, stream) : launch_back<T, 64, 32>(p, stream);
+    if (p.planes) e = launch_seq_delta_back_tc(p, stream);
+    else if (p.Dk <= 64) e = narrow ? launch_back<T, 64, 16>(p, stream) : launch_back<T, 64, 32>(p, stream);
     else e = narrow ? launch_back<T, 128, 16>(p, stream) : launch_back<T, 128, 32>(p, stream);
     if (e != cudaSuccess || p.slots == 0) return e;
     return p.Dk <= 64 ? launch_grad<T, 64>(p, stream) : launch_grad<T, 128>(p, stream);
@@ -455,7 +456,9 @@ cudaError_t launch(const SeqDeltaParams& p, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_seq_delta_bwd(const SeqDeltaParams& p, bool bf16, cudaStream_t stream) {
+cudaError_t launch_seq_delta_bwd(const SeqDeltaParams& args, bool bf16, cudaStream_t stream) {
+    SeqDeltaParams p = args;
+    p.planes = bf16 && p.wide && p.Dv > 16 ? 2 : 0;
     const cudaError_t e = launch_seq_delta_chunks(p, bf16, stream);
     if (e != cudaSuccess) return e;
     return bf16 ? launch<__nv_bfloat16>(p, stream) : launch<float>(p, stream);

@@ -236,6 +236,7 @@ struct SeqDeltaParams {
 cudaError_t launch_seq_delta_fwd(const SeqDeltaParams& p, bool bf16, cudaStream_t stream);
 cudaError_t launch_seq_delta_bwd(const SeqDeltaParams& p, bool bf16, cudaStream_t stream);
 cudaError_t launch_seq_delta_walk_tc(const SeqDeltaParams& p, cudaStream_t stream);
+cudaError_t launch_seq_delta_back_tc(const SeqDeltaParams& p, cudaStream_t stream);
 cudaError_t launch_seq_delta_step(const SeqDeltaParams& p, bool bf16, cudaStream_t stream);
 
 }  // namespace convfwd
