@@ -401,7 +401,7 @@ cudaError_t launch_seq_delta_chunks(const SeqDeltaParams& p, bool bf16, cudaStre
 
 cudaError_t launch_seq_delta_fwd(const SeqDeltaParams& args, bool bf16, cudaStream_t stream) {
     SeqDeltaParams p = args;
-    p.planes = bf16 && p.wide && p.Dv > 16 ? 1 : 0;
+    p.planes = bf16 && p.wide && p.compact && p.Dv > 16 ? 1 : 0;
     const cudaError_t e = launch_seq_delta_chunks(p, bf16, stream);
     if (e != cudaSuccess) return e;
     if (p.planes) return launch_seq_delta_walk_tc(p, stream);

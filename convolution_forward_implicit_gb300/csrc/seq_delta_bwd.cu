@@ -458,7 +458,7 @@ cudaError_t launch(const SeqDeltaParams& p, cudaStream_t stream) {
 
 cudaError_t launch_seq_delta_bwd(const SeqDeltaParams& args, bool bf16, cudaStream_t stream) {
     SeqDeltaParams p = args;
-    p.planes = bf16 && p.wide && p.Dv > 16 ? 2 : 0;
+    p.planes = bf16 && p.wide && p.compact && p.Dv > 16 ? 2 : 0;
     const cudaError_t e = launch_seq_delta_chunks(p, bf16, stream);
     if (e != cudaSuccess) return e;
     return bf16 ? launch<__nv_bfloat16>(p, stream) : launch<float>(p, stream);

@@ -103,6 +103,8 @@ static conv_status delta_call(seq_plan_t p, const seq_delta_args* a, seq_directi
         q.dr = reinterpret_cast<float*>(w + tri_bytes(p) + row_bytes(p) + state_bytes(p));
     }
     q.wide = keys.wide && (p->N * e) % 16 == 0;
+    q.compact = 1;
+    for (int64_t ld : {a->q_ld, a->k_ld, a->v_ld, a->y_ld, a->dy_ld, a->dv_ld}) q.compact = q.compact && ld < (INT64_C(1) << 24);
     // pairs of elements: 4 bytes of bf16, 8 of fp32
     auto paired = [&](const void* v, int64_t ld) { return !v || (reinterpret_cast<uintptr_t>(v) % (2 * e) == 0 && ld % 2 == 0); };
     q.pairs = p->W % 2 == 0 && paired(a->v, a->v_ld) && paired(a->y, a->y_ld) && paired(a->dy, a->dy_ld) && paired(a->dv, a->dv_ld);

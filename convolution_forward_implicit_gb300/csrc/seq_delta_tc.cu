@@ -15,7 +15,10 @@
 namespace convfwd {
 namespace {
 
-constexpr int WT = 512;                       // threads: four warps a quarter of the lanes, a quarter of the columns each
+constexpr int WT = 512;                       // threads that hold lanes: two warps a quarter of the lanes, half of the columns each
+constexpr int TPT = 64 * 128 / WT;            // tokens of a chunk a thread holds of its lane
+constexpr int LOADERS = 3;                    // warps behind the first, issuing, one that fetch
+constexpr int WALK_THREADS = WT + 32 * (1 + LOADERS);
 constexpr uint32_t ATOM = 128 * 128;          // 128 rows of 64 bf16
 constexpr uint32_t PLANES = 3 * ATOM;         // [T; A T] (backward: [T; A]) in three parts
 
@@ -27,13 +30,27 @@ __device__ __forceinline__ uint64_t mn_desc(uint32_t saddr, uint32_t stride) {  
     d |= (uint64_t)2 << 61;
     return d;
 }
-// D += A B with A in TMEM (a lane's 16 bf16 of a step in 8 columns)
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+// D += A B for 64 of k, A in TMEM (a lane's 16 bf16 of a step in 8 columns), issued by the calling thread: four steps in one
+// block, B's address BSTEP bytes further each (4 steps one by one took about 100 cycles each to issue).
+template <int BSTEP>
+__device__ __forceinline__ void mma_ts_k4(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+        "{\n\t.reg .pred p, t;\n\t.reg .b64 b1, b2, b3;\n\t.reg .b32 a1, a2, a3;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+        "add.s64 b1, %2, %5;\n\tadd.s64 b2, %2, %6;\n\tadd.s64 b3, %2, %7;\n\t"
+        "add.s32 a1, %1, 8;\n\tadd.s32 a2, %1, 16;\n\tadd.s32 a3, %1, 24;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "n"(BSTEP >> 4), "n"(2 * BSTEP >> 4), "n"(3 * BSTEP >> 4)
         : "memory");
+}
+// N steps of 16 along k: A's columns follow one another; B's lie side by side (64 of them, 128 bytes, an atom) or, ACROSS, in rows.
+template <int N, bool ACROSS_ROWS>
+__device__ __forceinline__ void steps(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+#pragma unroll
+    for (int k = 0; k < N; k += 4) mma_ts_k4<ACROSS_ROWS ? 2048 : 32>(d, a + k * 8, b + (ACROSS_ROWS ? k * (2048 >> 4) : k / 4 * (ATOM >> 4)), idesc, accumulate || k > 0);
 }
 __device__ __forceinline__ void tmem_st8(uint32_t at, const uint32_t (&v)[8]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]),
@@ -80,253 +97,382 @@ struct WalkTc {
     static constexpr uint32_t H = 0, P = 3 * KP / 2, ACC = P + 96;       // TMEM columns
 };
 
-// What a walk's CTA needs to wait: barriers of the products and of the two stages' copies, all bounded.
-struct Waits {
-    uint32_t mma, full;               // shared addresses (full: two)
-    uint32_t mma_phase;
+// A wait of a warp for a barrier's phase, for about a second at most.  The limit goes by the SM's clock: reading the global
+// timer between two looks costs more than a hand-off takes (8192 x 32 heads: walk 449 us with it, see the figures above).
+constexpr long long WAIT_CYCLES = 2000000000ll;
+// Every lane looks, and the arrivals below are predicated: a branch that only one lane takes costs a few hundred cycles
+// at each hand-off until its warp is together again (2048 x 16 heads: 233 us with them, 184 with the waits alone changed).
+__device__ __forceinline__ bool wait_turn(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned* err) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long since = clock64();
+    bool ok = true;
+    while (ok && !mbar_try_wait(bar, parity)) {
+        if (*abort_flag) {
+            ok = false;
+        } else if (clock64() - since > WAIT_CYCLES) {
+            *abort_flag = 1;
+            atomicOr(err, ERR_WAIT_TIMEOUT);
+            ok = false;
+        }
+    }
+    return __all_sync(0xffffffffu, ok) != 0;
+}
+__device__ __forceinline__ void arrive_once(uint32_t bar) {       // one arrival of a converged warp
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];\n\t}" ::"r"(bar)
+        : "memory");
+}
+
+// The barriers of a walk's CTA, every wait bounded.  The threads that hold lanes (16 warps) tell the issuing warp when its
+// operands are ready, and learn from `mma` when its products are done; `full`: a stage's operands have arrived, `empty`:
+// it may be written again.
+struct Turns {
+    uint32_t mma, ready, full, empty;         // shared addresses (full, empty: two)
+    uint32_t phase;                   // of mma (the issuing warp: of ready)
     volatile int* abort_flag;
     unsigned* err;
-    __device__ __forceinline__ bool products() {
-        const bool ok = wait_bar(mma, mma_phase, abort_flag, err);
-        mma_phase ^= 1;
+    __device__ __forceinline__ bool next(uint32_t bar) {
+        const bool ok = wait_turn(bar, phase, abort_flag, err);
+        phase ^= 1;
+        tc_fence_after();
         return ok;
     }
-    // After a wait ran out: the last fetched chunk's copies and products that were issued, before shared memory and TMEM go
-    // (bounded as well).
-    __device__ __forceinline__ void drain(int fetched) {
-        const unsigned long long since = globaltimer();
-        for (int c = fetched > 1 ? fetched - 2 : 0; c < fetched; ++c)
-            while (!mbar_try_wait(full + 8 * (c & 1), (c >> 1) & 1) && globaltimer() - since < WAIT_LIMIT_NS) {
+    // what this warp wrote to TMEM (and shared memory) is there
+    __device__ __forceinline__ void tell() {
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        arrive_once(ready);
+    }
+    __device__ __forceinline__ void release(int n) const {       // this warp has read the stage for the last time
+        __syncwarp();
+        arrive_once(empty + 8 * (n & 1));
+    }
+    __device__ __forceinline__ bool free(int n) { return n < 2 || wait_turn(empty + 8 * (n & 1), ((n >> 1) & 1) ^ 1, abort_flag, err); }
+    __device__ __forceinline__ bool arrived(int n) { return wait_turn(full + 8 * (n & 1), (n >> 1) & 1, abort_flag, err); }
+    // After a wait ran out: copies to shared memory and products that were issued, before it and TMEM go (bounded as well).
+    __device__ __forceinline__ void drain(int stages) {
+        const long long since = clock64();
+        for (int n = 0; n < 2 && n < stages; ++n)         // either phase: the last one that began has ended
+            while (!(mbar_try_wait(full + 8 * n, 0) && !mbar_try_wait(full + 8 * n, 1)) && !(mbar_try_wait(full + 8 * n, 1) && !mbar_try_wait(full + 8 * n, 0)) &&
+                   clock64() - since < WAIT_CYCLES) {
             }
-        while (!mbar_try_wait(mma, mma_phase) && !mbar_try_wait(mma, mma_phase ^ 1) && globaltimer() - since < WAIT_LIMIT_NS) {
-        }
     }
 };
 
 // K and Q rows of a chunk to [K; Q] atoms in the 128-byte swizzle; rows at and behind n and columns behind the width are zero.
 template <int KP>
-__device__ __forceinline__ void load_kq(uint32_t to, const __nv_bfloat16* k, const __nv_bfloat16* q, long long k_ld, long long q_ld, int n, int width) {
-    constexpr int CPR = KP / 8;
-#pragma unroll
-    for (int j = 0; j < 128 * CPR / WT; ++j) {
-        const int i = threadIdx.x + j * WT, row = i / CPR, c = i % CPR, r = row & 63;
-        const bool on = r < n && c * 8 < width;
+__device__ __forceinline__ void load_kq(uint32_t to, const __nv_bfloat16* k, const __nv_bfloat16* q, long long k_ld, long long q_ld, int n, int width, int thread) {
+    constexpr int CPR = KP / 8;                  // 16-byte pieces of a row
+    for (int i = thread; i < 128 * CPR; i += 32 * LOADERS) {
+        const int row = i / CPR, c = i % CPR, r = row & 63;
+        const bool there = r < n && c * 8 < width;
         const __nv_bfloat16* from = row < 64 ? k : q;
-        cp_async_16(to + (uint32_t)(c / 8) * ATOM + row * 128 + ((c % 8) ^ (row & 7)) * 16,
-                    on ? from + r * (row < 64 ? k_ld : q_ld) + c * 8 : from, on ? 16 : 0);
+        const uint32_t step = (uint32_t)(row < 64 ? k_ld : q_ld);
+        cp_async_16(to + (uint32_t)(c / 8) * ATOM + row * 128 + ((c % 8) ^ (row & 7)) * 16, there ? from + r * step + c * 8 : from, there ? 16 : 0);
+    }
+}
+
+// The start of a walk's CTA: its place, barriers, TMEM.
+template <int KP>
+struct Walk {
+    uint32_t base, tmem, lanes;
+    uint8_t* smem;
+    int warp, lane, cq, tok, h, seq, kh, dv, t0, t1, chunks, slot0;
+    bool on;
+    long long row, state;
+    Turns turn;
+    __device__ __forceinline__ Walk(const SeqDeltaParams& p, int dvbs, unsigned* err, uint8_t* raw) {
+        using W = WalkTc<KP>;
+        base = (smem_u32(raw) + 1023u) & ~1023u;
+        smem = raw + (base - smem_u32(raw));
+        const uint32_t bars = base + 2 * W::STAGE;
+        uint32_t* slot = reinterpret_cast<uint32_t*>(smem + 2 * W::STAGE + 64);
+        turn = {bars, bars + 24, bars + 8, bars + 32, 0, reinterpret_cast<volatile int*>(smem + 2 * W::STAGE + 72), err};
+        warp = threadIdx.x >> 5;
+        lane = threadIdx.x & 31;
+        cq = (warp >> 2) - 1;                     // (the first four warps hold no lanes)
+        tok = cq * TPT;                           // the thread's tokens of a chunk: tok .. tok + TPT - 1
+        const int dvb = blockIdx.x % dvbs, sh = blockIdx.x / dvbs;
+        h = sh % p.Hv;
+        seq = sh / p.Hv;
+        kh = h / (p.Hv / p.Hk);
+        dv = dvb * 128 + (warp & 3) * 32 + lane;
+        on = dv < p.Dv && warp > LOADERS;
+        t0 = p.ax.L > 0 ? seq * p.ax.L : seq_start(p.ax, seq, 0);
+        t1 = p.ax.L > 0 ? t0 + p.ax.L : seq_start(p.ax, seq + 1, t0);
+        chunks = (t1 - t0 + DC - 1) / DC;
+        slot0 = cut_base(p.ax, seq, DC);
+        row = seq_slot(p.sl, seq);
+        state = (row * p.Hv + h) * (long long)p.Dk * p.Dv + dv;
+        if (threadIdx.x == 0) {
+            mbar_init(turn.mma, 1);
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(turn.full + 8 * i, 1 + LOADERS);
+                mbar_init(turn.empty + 8 * i, WT / 32);
+            }
+            mbar_init(turn.ready, WT / 32);
+            *turn.abort_flag = 0;
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        }
+        if (warp == 0) {
+            tmem_alloc(smem_u32(slot), 512);
+            tmem_relinquish();
+        }
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        tmem = *slot;
+        lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    }
+    __device__ __forceinline__ long long at(const SeqDeltaParams& p, int c) const { return (long long)(slot0 + c) * p.Hv + h; }
+    __device__ __forceinline__ uint32_t stage(int n) const { return base + (n & 1) * WalkTc<KP>::STAGE; }
+    __device__ __forceinline__ const float* rows(int n) const {
+        return reinterpret_cast<const float*>(smem + (n & 1) * WalkTc<KP>::STAGE + WalkTc<KP>::KQ + PLANES);
+    }
+    // The loaders' part: the operands of every chunk in order (backward: from the last), copies of whole matrices, and K and Q
+    // in copies of 16 bytes.
+    __device__ __forceinline__ void load(const SeqDeltaParams& p, bool backward) {
+        const int thread = threadIdx.x - 32;
+        for (int i = 0; i < chunks; ++i) {
+            const int c = backward ? chunks - 1 - i : i, t = t0 + c * DC;
+            const uint32_t to = stage(i), bar = turn.full + 8 * (i & 1);
+            if (!turn.free(i)) break;
+            if (thread == 0) {
+                mbar_arrive_expect_tx(bar, PLANES + DELTA_ROWS * 4);
+                bulk_g2s(to + WalkTc<KP>::KQ, reinterpret_cast<const uint8_t*>(p.tri) + at(p, c) * PLANES, PLANES, bar);
+                bulk_g2s(to + WalkTc<KP>::KQ + PLANES, p.rows + at(p, c) * DELTA_ROWS, DELTA_ROWS * 4, bar);
+            }
+            load_kq<KP>(to, static_cast<const __nv_bfloat16*>(p.k) + t * p.k_ld + kh * p.Dk, static_cast<const __nv_bfloat16*>(p.q) + t * p.q_ld + kh * p.Dk,
+                        p.k_ld, p.q_ld, min(DC, t1 - t), p.Dk, thread);
+            cp_async_commit();
+            cp_async_wait<0>();
+            fence_proxy_async();
+            __syncwarp();
+            arrive_once(bar);
+        }
+        // after a wait ran out: what was copied to shared memory is waited for (bounded as well)
+        if (thread == 0 && *turn.abort_flag) turn.drain(chunks);
+    }
+    // The thread's values of a chunk's rows of v or dY, as pairs of tokens.
+    __device__ __forceinline__ void values(const void* from, long long ld, const SeqDeltaParams& p, int c, uint32_t (&v)[TPT / 2]) const {
+        const int t = t0 + c * DC + tok, n = on ? min(DC, t1 - t0 - c * DC) - tok : 0;
+        const uint16_t* at = static_cast<const uint16_t*>(from) + t * ld + h * p.Dv + dv;
+        const uint32_t step = (uint32_t)ld;       // (64 rows lie within 2^31 bytes: see the caller)
+        if (n >= TPT) {
+#pragma unroll
+            for (int i = 0; i < TPT / 2; ++i) v[i] = (uint32_t)at[2 * i * step] | (uint32_t)at[(2 * i + 1) * step] << 16;
+        } else {
+#pragma unroll
+            for (int i = 0; i < TPT / 2; ++i) {
+                const uint32_t a = 2 * i < n ? at[2 * i * step] : 0, b = 2 * i + 1 < n ? at[(2 * i + 1) * step] : 0;
+                v[i] = a | b << 16;
+            }
+        }
+    }
+    // 16 of the thread's values to rows first .. of a tensor whose chunk has n tokens.
+    __device__ __forceinline__ void store(void* to, long long ld, const SeqDeltaParams& p, int t, int n, int first, const float (&x)[16]) const {
+        __nv_bfloat16* at = static_cast<__nv_bfloat16*>(to) + (long long)(t + first) * ld + h * p.Dv + dv;
+        const uint32_t step = (uint32_t)ld;
+        if (n - first >= 16) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) at[i * step] = __float2bfloat16_rn(x[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (first + i < n) at[i * step] = __float2bfloat16_rn(x[i]);
+        }
+    }
+    // The thread's part of a state to rows of Dvp floats.
+    __device__ __forceinline__ void keep(float* to, const SeqDeltaParams& p, const float (&st)[KP * 128 / WT]) const {
+        if (dv >= p.Dvp) return;
+        float* at = to + cq * (KP * 128 / WT) * p.Dvp + dv;
+        if (p.Dk == KP) {
+#pragma unroll
+            for (int i = 0; i < KP * 128 / WT; ++i) at[i * p.Dvp] = st[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < KP * 128 / WT; ++i)
+                if (cq * (KP * 128 / WT) + i < p.Dk) at[i * p.Dvp] = st[i];
+        }
+    }
+    __device__ __forceinline__ void close() {
+        tc_fence_before();
+        __syncthreads();
+        if (warp == 0) {
+            tc_fence_after();
+            tmem_dealloc(tmem, 512);
+        }
+    }
+};
+
+// The thread's rows of the state in three parts to `to`, planes KP/2 columns apart.
+template <int KP>
+__device__ __forceinline__ void put_state(uint32_t to, const float (&st)[KP * 128 / WT]) {
+#pragma unroll
+    for (int i = 0; i < KP * 128 / WT; i += 16) {
+        float x[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[e] = st[i + e];
+        put_parts(to + i / 2, KP / 2, x);
+    }
+}
+// st <- decay st + the products' sums
+template <int KP>
+__device__ __forceinline__ void next_state(uint32_t from, float decay, float (&st)[KP * 128 / WT]) {
+#pragma unroll
+    for (int i = 0; i < KP * 128 / WT; i += 16) {
+        uint32_t a[16];
+        tmem_ld16(from + i, a);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) st[i + e] = fmaf(decay, st[i + e], __uint_as_float(a[e]));
     }
 }
 
 template <int KP>
-__global__ void __launch_bounds__(WT, 1) delta_walk_tc_kernel(const __grid_constant__ SeqDeltaParams p, int dvbs, unsigned* err) {
+__global__ void __launch_bounds__(WALK_THREADS, 1) delta_walk_tc_kernel(const __grid_constant__ SeqDeltaParams p, int dvbs, unsigned* err) {
     extern __shared__ uint8_t smem_raw[];
     using W = WalkTc<KP>;
     using T = __nv_bfloat16;
-    constexpr int HK = KP / 4;                  // the thread's rows of the state: cq HK ..; its tokens: 16 cq ..
-    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    uint8_t* smem = smem_raw + (base - smem_u32(smem_raw));
-    const uint32_t bars = base + 2 * W::STAGE;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + 2 * W::STAGE + 64);
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + 2 * W::STAGE + 72);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wq = warp & 3, cq = warp >> 2;
-    const int dvb = blockIdx.x % dvbs, sh = blockIdx.x / dvbs, h = sh % p.Hv, seq = sh / p.Hv, kh = h / (p.Hv / p.Hk);
-    const int dv = dvb * 128 + wq * 32 + lane;
-    const bool on = dv < p.Dv;
-    const int t0 = p.ax.L > 0 ? seq * p.ax.L : seq_start(p.ax, seq, 0), t1 = p.ax.L > 0 ? t0 + p.ax.L : seq_start(p.ax, seq + 1, t0);
-    const int chunks = (t1 - t0 + DC - 1) / DC, slot0 = cut_base(p.ax, seq, DC);
-    if (threadIdx.x == 0) {
-        mbar_init(bars, 1);
-        mbar_init(bars + 8, 1);
-        mbar_init(bars + 16, 1);
-        *abort_flag = 0;
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    }
-    if (warp == 0) {
-        tmem_alloc(smem_u32(tmem_slot), 512);
-        tmem_relinquish();
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = *tmem_slot, lanes = tmem + ((uint32_t)(wq * 32) << 16);
-    Waits wait = {bars, bars + 8, 0, abort_flag, err};
-
-    const long long row = seq_slot(p.sl, seq), state = (row * p.Hv + h) * (long long)p.Dk * p.Dv + dv;
-    float st[HK];                               // of column dv
-#pragma unroll
-    for (int i = 0; i < HK; ++i) {
-        const int r = cq * HK + i;
-        st[i] = p.h_in && row >= 0 && on && r < p.Dk ? p.h_in[state + (long long)r * p.Dv] : 0.f;
-    }
-    auto put_state = [&]() {
-#pragma unroll
-        for (int i = 0; i < HK; i += 16) {
-            float x[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) x[e] = st[i + e];
-            put_parts(lanes + W::H + cq * (HK / 2) + i / 2, KP / 2, x);
-        }
-    };
-    int fetched = 0;
-    auto fetch = [&](int c) {                   // a chunk's operands to its stage
-        fetched = c + 1;
-        const uint32_t to = base + (c & 1) * W::STAGE, bar = wait.full + 8 * (c & 1);
-        const int t = t0 + c * DC;
-        const long long at = (long long)(slot0 + c) * p.Hv + h;
-        if (threadIdx.x == 0) {
-            mbar_arrive_expect_tx(bar, PLANES + DELTA_ROWS * 4);
-            bulk_g2s(to + W::KQ, reinterpret_cast<const uint8_t*>(p.tri) + at * PLANES, PLANES, bar);
-            bulk_g2s(to + W::KQ + PLANES, p.rows + at * DELTA_ROWS, DELTA_ROWS * 4, bar);
-        }
-        load_kq<KP>(to, static_cast<const T*>(p.k) + t * p.k_ld + kh * p.Dk, static_cast<const T*>(p.q) + t * p.q_ld + kh * p.Dk, p.k_ld, p.q_ld,
-                    min(DC, t1 - t), p.Dk);
-        cp_async_commit();
-    };
-    dep_wait();
-    if (chunks > 0) {
-        put_state();
-        fetch(0);
-        tmem_st_wait();
-    }
-    bool ok = true;
-    constexpr uint32_t ID_64 = idesc_f32acc(128, 64, 1u), ID_128 = idesc_f32acc(128, 128, 1u), ID3 = idesc_f32acc(128, KP, 1u) | (1u << 16);
-    for (int c = 0; c < chunks; ++c) {
-        const uint32_t kq = base + (c & 1) * W::STAGE, tp = kq + W::KQ;
-        const float* rows = reinterpret_cast<const float*>(smem + (c & 1) * W::STAGE + W::KQ + PLANES);
-        const int t = t0 + c * DC, n = min(DC, t1 - t);
-        const long long at = (long long)(slot0 + c) * p.Hv + h;
-        // this chunk's K and Q are there, the state's parts are in TMEM
-        cp_async_wait<0>();
-        fence_proxy_async();
-        ok = wait_bar(wait.full + 8 * (c & 1), (c >> 1) & 1, abort_flag, err) && ok;
-        tc_fence_before();
-        if (__syncthreads_or(!ok)) break;
-        if (threadIdx.x == 0) {      // y needs two parts of h only: the last one goes with K alone
-            tc_fence_after();
-#pragma unroll
-            for (int q = 0; q < 3; ++q) {
-                const int pl = q == 0 ? 1 : q == 1 ? 0 : 2;
-#pragma unroll
-                for (int k = 0; k < KP / 16; ++k)
-                    mma_ts(tmem + W::ACC, tmem + W::H + pl * (KP / 2) + k * 8, sw128_desc(kq + (k / 4) * ATOM) + (uint64_t)((k % 4) * 2),
-                           pl == 2 ? ID_64 : ID_128, q > 0 || k > 0);
+    constexpr int HK = KP * 128 / WT;                  // the thread's rows of the state: cq HK ..
+    constexpr uint32_t ID_64 = idesc_f32acc(128, 64, 1u), ID_128 = idesc_f32acc(128, 128, 1u), ID_KP = idesc_f32acc(128, KP, 1u) | (1u << 16);
+    Walk<KP> w(p, dvbs, err, smem_raw);
+    if (w.warp > 0 && w.warp <= LOADERS) {
+        dep_wait();
+        w.load(p, false);
+    } else if (w.warp == 0) {                   // the issuing warp (the first: the oldest is served first)
+        bool ok = true;
+        for (int c = 0; c < w.chunks && ok; ++c) {
+            const uint32_t kq = w.stage(c), tp = kq + W::KQ, acc = w.tmem + W::ACC;
+            ok = w.turn.arrived(c) && w.turn.next(w.turn.ready);
+            if (!ok) break;
+            if (w.lane == 0) {
+                // y needs two parts of h only: the last one goes with K alone
+#pragma unroll 1
+                for (int q = 0; q < 3; ++q) {
+                    const int pl = q == 0 ? 1 : q == 1 ? 0 : 2;
+                    steps<KP / 16, false>(acc, w.tmem + W::H + pl * (KP / 2), sw128_desc(kq), pl == 2 ? ID_64 : ID_128, q > 0);
+                }
+                mma_commit(w.turn.mma);
             }
-            mma_commit(wait.mma);
+            __syncwarp();
+            if (!(ok = w.turn.next(w.turn.ready))) break;
+            if (w.lane == 0) {
+                // U needs six products of parts, y the three large ones: (1, 0), (0, 1), (0, 0), then (2, 0), (0, 2), (1, 1)
+#pragma unroll 1
+                for (int q = 0; q < 6; ++q)
+                    steps<4, false>(acc, w.tmem + W::P + (0x481 >> 2 * q & 3) * 32, sw128_desc(tp + (0x604 >> 2 * q & 3) * ATOM), q < 3 ? ID_128 : ID_64, q > 0);
+                mma_commit(w.turn.mma);
+            }
+            __syncwarp();
+            if (!(ok = w.turn.next(w.turn.ready))) break;
+            if (w.lane == 0) {
+#pragma unroll 1
+                for (int pl = 2; pl >= 0; --pl) steps<4, true>(acc, w.tmem + W::P + pl * 32, mn_desc(kq, ATOM), ID_KP, pl < 2);
+                mma_commit(w.turn.mma);
+            }
+            __syncwarp();
         }
-        if (c + 1 < chunks) fetch(c + 1);
-        const int tok = cq * 16;                 // the thread's tokens of the chunk
-        T v[16];
-        {
-            const T* from = static_cast<const T*>(p.v) + (long long)(t + tok) * p.v_ld + h * p.Dv + dv;
+    } else {
+        float st[HK];                           // of column dv
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = on && tok + i < n ? from[i * p.v_ld] : T(0.f);
+        for (int i = 0; i < HK; ++i) {
+            const int r = w.cq * HK + i;
+            st[i] = p.h_in && w.row >= 0 && w.on && r < p.Dk ? p.h_in[w.state + (long long)r * p.Dv] : 0.f;
         }
-        if (p.saved && dv < p.Dvp) {
-            float* to = p.saved + at * p.Dk * p.Dvp + dv;
+        uint32_t v[TPT / 2];
+        dep_wait();
+        if (w.chunks > 0) {
+            w.values(p.v, p.v_ld, p, 0, v);
+            put_state<KP>(w.lanes + W::H + w.cq * (HK / 2), st);
+        }
+        const int tok = w.tok;
+        for (int c = 0; c < w.chunks; ++c) {
+            const int t = w.t0 + c * DC, n = min(DC, w.t1 - t);
+            w.turn.tell();                        // h0's parts are in TMEM
+            const float* rows = w.rows(c);
+            if (p.saved) w.keep(p.saved + w.at(p, c) * p.Dk * p.Dvp, p, st);
+            if (!w.turn.next(w.turn.mma) || !w.turn.arrived(c)) break;
+            float y[TPT];
+#pragma unroll
+            for (int j = 0; j < TPT; j += 16) {
+                uint32_t a[16];
+                tmem_ld16(w.lanes + W::ACC + tok + j, a);
+                float r[16], f[16];
+                read16(rows + RF_BETA + tok + j, r);
+                read16(rows + RF_IN + tok + j, f);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    float v0, v1;
+                    bf2_unpack(v[j / 2 + i], v0, v1);
+                    r[2 * i] = r[2 * i] * v0 - f[2 * i] * __uint_as_float(a[2 * i]);
+                    r[2 * i + 1] = r[2 * i + 1] * v1 - f[2 * i + 1] * __uint_as_float(a[2 * i + 1]);
+                }
+                put_parts(w.lanes + W::P + (tok + j) / 2, 32, r);
+            }
+#pragma unroll
+            for (int j = 0; j < TPT; j += 16) {       // (before the products with R overwrite it)
+                uint32_t a[16];
+                tmem_ld16(w.lanes + W::ACC + 64 + tok + j, a);
+                float f[16];
+                read16(rows + RF_OUT + tok + j, f);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) y[j + i] = f[i] * __uint_as_float(a[i]);
+            }
+            w.turn.tell();
+            if (c + 1 < w.chunks) w.values(p.v, p.v_ld, p, c + 1, v);
+            if (!w.turn.next(w.turn.mma)) break;
+#pragma unroll
+            for (int j = 0; j < TPT; j += 16) {
+                uint32_t a[16];
+                tmem_ld16(w.lanes + W::ACC + tok + j, a);
+                float f[16];
+                read16(rows + RF_END + tok + j, f);
+                tmem_ld_wait();
+                if (p.saved && w.dv < p.Dvp) {
+                    float* to = p.saved + p.saved_u + (w.at(p, c) * DC + tok + j) * p.Dvp + w.dv;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) to[i * p.Dvp] = __uint_as_float(a[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i) f[i] *= __uint_as_float(a[i]);
+                put_parts(w.lanes + W::P + (tok + j) / 2, 32, f);
+            }
+#pragma unroll
+            for (int j = 0; j < TPT; j += 16) {
+                uint32_t a[16];
+                tmem_ld16(w.lanes + W::ACC + 64 + tok + j, a);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) y[j + i] += __uint_as_float(a[i]);
+            }
+            const float decay = rows[RF_DECAY];
+            w.turn.tell();
+            if (w.on) {
+#pragma unroll
+                for (int j = 0; j < TPT; j += 16) {
+                    float x[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) x[i] = y[j + i];
+                    w.store(p.y, p.y_ld, p, t, n, tok + j, x);
+                }
+            }
+            if (!w.turn.next(w.turn.mma)) break;
+            w.turn.release(c);
+            next_state<KP>(w.lanes + W::ACC + w.cq * HK, decay, st);
+            if (c + 1 < w.chunks) put_state<KP>(w.lanes + W::H + w.cq * (HK / 2), st);
+        }
+        if (p.h_out && w.row >= 0 && w.on) {
 #pragma unroll
             for (int i = 0; i < HK; ++i)
-                if (cq * HK + i < p.Dk) to[(cq * HK + i) * p.Dvp] = st[i];
-        }
-        ok = wait.products() && ok;
-        tc_fence_after();
-        float y[16];
-        {
-            uint32_t a[16], q[16];
-            tmem_ld16(lanes + W::ACC + tok, a);
-            tmem_ld16(lanes + W::ACC + 64 + tok, q);
-            float beta[16], in[16];
-            read16(rows + RF_BETA + tok, beta);
-            read16(rows + RF_IN + tok, in);
-            tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 16; ++i) beta[i] = beta[i] * __bfloat162float(v[i]) - in[i] * __uint_as_float(a[i]);
-            put_parts(lanes + W::P + cq * 8, 32, beta);
-            read16(rows + RF_OUT + tok, in);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) y[i] = in[i] * __uint_as_float(q[i]);
-        }
-        tmem_st_wait();
-        tc_fence_before();
-        if (__syncthreads_or(!ok)) break;
-        if (threadIdx.x == 0) {
-            tc_fence_after();
-            // U needs six products of parts, y the three large ones
-            constexpr int PA[6] = {1, 0, 0, 2, 0, 1}, PB[6] = {0, 1, 0, 0, 2, 1};
-#pragma unroll
-            for (int q = 0; q < 6; ++q)
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    mma_ts(tmem + W::ACC, tmem + W::P + PA[q] * 32 + k * 8, sw128_desc(tp + PB[q] * ATOM) + (uint64_t)(k * 2), q < 3 ? ID_128 : ID_64,
-                           q > 0 || k > 0);
-            mma_commit(wait.mma);
-        }
-        ok = wait.products() && ok;
-        tc_fence_after();
-        {
-            uint32_t a[16], q[16];
-            tmem_ld16(lanes + W::ACC + tok, a);
-            tmem_ld16(lanes + W::ACC + 64 + tok, q);
-            float end[16];
-            read16(rows + RF_END + tok, end);
-            tmem_ld_wait();
-            if (p.saved && dv < p.Dvp) {
-                float* to = p.saved + p.saved_u + (at * DC + tok) * p.Dvp + dv;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) to[i * p.Dvp] = __uint_as_float(a[i]);
-            }
-#pragma unroll
-            for (int i = 0; i < 16; ++i) end[i] *= __uint_as_float(a[i]);
-            put_parts(lanes + W::P + cq * 8, 32, end);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) y[i] += __uint_as_float(q[i]);
-        }
-        tmem_st_wait();
-        tc_fence_before();
-        if (__syncthreads_or(!ok)) break;
-        if (threadIdx.x == 0) {
-            tc_fence_after();
-#pragma unroll
-            for (int pl = 2; pl >= 0; --pl)
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    mma_ts(tmem + W::ACC, tmem + W::P + pl * 32 + k * 8, mn_desc(kq + k * 2048, ATOM), ID3, pl < 2 || k > 0);
-            mma_commit(wait.mma);
-        }
-        if (on) {
-            T* to = static_cast<T*>(p.y) + (long long)(t + tok) * p.y_ld + h * p.Dv + dv;
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                if (tok + i < n) to[i * p.y_ld] = __float2bfloat16_rn(y[i]);
-        }
-        const float decay = rows[RF_DECAY];
-        ok = wait.products() && ok;
-        tc_fence_after();
-#pragma unroll
-        for (int i = 0; i < HK; i += 16) {
-            uint32_t a[16];
-            tmem_ld16(lanes + W::ACC + cq * HK + i, a);
-            tmem_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 16; ++e) st[i + e] = fmaf(decay, st[i + e], __uint_as_float(a[e]));
-        }
-        if (c + 1 < chunks) {
-            put_state();
-            tmem_st_wait();
+                if (w.cq * HK + i < p.Dk) p.h_out[w.state + (long long)(w.cq * HK + i) * p.Dv] = st[i];
         }
     }
-    if (p.h_out && row >= 0 && on) {
-#pragma unroll
-        for (int i = 0; i < HK; ++i)
-            if (cq * HK + i < p.Dk) p.h_out[state + (long long)(cq * HK + i) * p.Dv] = st[i];
-    }
-    cp_async_wait<0>();
-    if (threadIdx.x == 0 && *abort_flag) wait.drain(fetched);
-    tc_fence_before();
-    __syncthreads();
-    if (warp == 0) {
-        tc_fence_after();
-        tmem_dealloc(tmem, 512);
-    }
+    w.close();
 }
 
 template <int KP>
@@ -334,7 +480,7 @@ cudaError_t launch_walk_tc(const SeqDeltaParams& p, unsigned* err, cudaStream_t 
     cudaError_t e = cudaFuncSetAttribute(delta_walk_tc_kernel<KP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)WalkTc<KP>::BYTES);
     if (e != cudaSuccess) return e;
     const int dvbs = (p.Dv + 127) / 128;
-    return launch_kernel(delta_walk_tc_kernel<KP>, dim3((unsigned)(p.ax.S * (long long)p.Hv * dvbs)), dim3(WT), WalkTc<KP>::BYTES, stream, p.slots > 0, 1, p,
+    return launch_kernel(delta_walk_tc_kernel<KP>, dim3((unsigned)(p.ax.S * (long long)p.Hv * dvbs)), dim3(WALK_THREADS), WalkTc<KP>::BYTES, stream, p.slots > 0, 1, p,
                          dvbs, err);
 }
 
@@ -349,225 +495,156 @@ struct BackTc {
 };
 
 template <int KP>
-__global__ void __launch_bounds__(WT, 1) delta_back_tc_kernel(const __grid_constant__ SeqDeltaParams p, int dvbs, unsigned* err) {
+__global__ void __launch_bounds__(WALK_THREADS, 1) delta_back_tc_kernel(const __grid_constant__ SeqDeltaParams p, int dvbs, unsigned* err) {
     extern __shared__ uint8_t smem_raw[];
     using W = WalkTc<KP>;
     using B = BackTc<KP>;
     using T = __nv_bfloat16;
-    constexpr int HK = KP / 4;
-    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    uint8_t* smem = smem_raw + (base - smem_u32(smem_raw));
-    const uint32_t bars = base + 2 * W::STAGE;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + 2 * W::STAGE + 64);
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + 2 * W::STAGE + 72);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wq = warp & 3, cq = warp >> 2;
-    const int dvb = blockIdx.x % dvbs, sh = blockIdx.x / dvbs, h = sh % p.Hv, seq = sh / p.Hv, kh = h / (p.Hv / p.Hk);
-    const int dv = dvb * 128 + wq * 32 + lane;
-    const bool on = dv < p.Dv;
-    const int t0 = p.ax.L > 0 ? seq * p.ax.L : seq_start(p.ax, seq, 0), t1 = p.ax.L > 0 ? t0 + p.ax.L : seq_start(p.ax, seq + 1, t0);
-    const int chunks = (t1 - t0 + DC - 1) / DC, slot0 = cut_base(p.ax, seq, DC);
-    if (threadIdx.x == 0) {
-        mbar_init(bars, 1);
-        mbar_init(bars + 8, 1);
-        mbar_init(bars + 16, 1);
-        *abort_flag = 0;
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    }
-    if (warp == 0) {
-        tmem_alloc(smem_u32(tmem_slot), 512);
-        tmem_relinquish();
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = *tmem_slot, lanes = tmem + ((uint32_t)(wq * 32) << 16);
-    Waits wait = {bars, bars + 8, 0, abort_flag, err};
-
-    const long long row = seq_slot(p.sl, seq), state = (row * p.Hv + h) * (long long)p.Dk * p.Dv + dv;
-    float st[HK];                               // of column dv: the gradient at the state the chunk leaves
-#pragma unroll
-    for (int i = 0; i < HK; ++i) {
-        const int r = cq * HK + i;
-        st[i] = p.dh_out && row >= 0 && on && r < p.Dk ? p.dh_out[state + (long long)r * p.Dv] : 0.f;
-    }
-    int fetched = 0;
-    const int tok = cq * 16;                    // the thread's tokens of a chunk
-    uint32_t dy[8];                             // and dY of those of the next one: pairs of tokens
-    auto fetch = [&](int s) {                   // the operands of the s-th chunk from the end
-        fetched = s + 1;
-        const uint32_t to = base + (s & 1) * W::STAGE, bar = wait.full + 8 * (s & 1);
-        const int c = chunks - 1 - s, t = t0 + c * DC, n = min(DC, t1 - t);
-        const long long at = (long long)(slot0 + c) * p.Hv + h;
-        if (threadIdx.x == 0) {
-            mbar_arrive_expect_tx(bar, PLANES + DELTA_ROWS * 4);
-            bulk_g2s(to + W::KQ, reinterpret_cast<const uint8_t*>(p.tri) + at * PLANES, PLANES, bar);
-            bulk_g2s(to + W::KQ + PLANES, p.rows + at * DELTA_ROWS, DELTA_ROWS * 4, bar);
-        }
-        load_kq<KP>(to, static_cast<const T*>(p.k) + t * p.k_ld + kh * p.Dk, static_cast<const T*>(p.q) + t * p.q_ld + kh * p.Dk, p.k_ld, p.q_ld, n, p.Dk);
-        cp_async_commit();
-        const uint16_t* from = static_cast<const uint16_t*>(p.dy) + (long long)(t + tok) * p.dy_ld + h * p.Dv + dv;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t a = on && tok + 2 * i < n ? from[2 * i * p.dy_ld] : 0, b = on && tok + 2 * i + 1 < n ? from[(2 * i + 1) * p.dy_ld] : 0;
-            dy[i] = a | b << 16;
-        }
-    };
-    auto put_state = [&]() {
-#pragma unroll
-        for (int i = 0; i < HK; i += 16) {
-            float x[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) x[e] = st[i + e];
-            put_parts(lanes + B::H + cq * (HK / 2) + i / 2, KP / 2, x);
-        }
-        tmem_st8(lanes + B::P + cq * 8, dy);    // dY is exact in one part
-    };
+    constexpr int HK = KP * 128 / WT;
+    constexpr uint32_t ACROSS = 1u << 16, ID_64 = idesc_f32acc(128, 64, 1u), ID_KP = idesc_f32acc(128, KP, 1u) | ACROSS;
+    Walk<KP> w(p, dvbs, err, smem_raw);
     dep_launch();
-    dep_wait();
-    if (chunks > 0) {
-        fetch(0);
-        put_state();
-        tmem_st_wait();
-    }
-    bool ok = true;
-    constexpr uint32_t ID_64 = idesc_f32acc(128, 64, 1u), ACROSS = 1u << 16, ID_KP = idesc_f32acc(128, KP, 1u) | ACROSS;
-    for (int s = 0; s < chunks; ++s) {
-        const uint32_t kq = base + (s & 1) * W::STAGE, tp = kq + W::KQ;
-        const float* rows = reinterpret_cast<const float*>(smem + (s & 1) * W::STAGE + W::KQ + PLANES);
-        const int c = chunks - 1 - s, t = t0 + c * DC, n = min(DC, t1 - t);
-        const long long at = (long long)(slot0 + c) * p.Hv + h;
-        cp_async_wait<0>();
-        fence_proxy_async();
-        ok = wait_bar(wait.full + 8 * (s & 1), (s >> 1) & 1, abort_flag, err) && ok;
-        tc_fence_before();
-        if (__syncthreads_or(!ok)) break;
-        if (threadIdx.x == 0) {
-            tc_fence_after();
-#pragma unroll
-            for (int pl = 2; pl >= 0; --pl)
-#pragma unroll
-                for (int k = 0; k < KP / 16; ++k)
-                    mma_ts(tmem + B::ACC, tmem + B::H + pl * (KP / 2) + k * 8, sw128_desc(kq + (k / 4) * ATOM) + (uint64_t)((k % 4) * 2), ID_64, pl < 2 || k > 0);
-#pragma unroll
-            for (int pl = 2; pl >= 0; --pl)
-#pragma unroll
-                for (int k = 0; k < 4; ++k)      // A's rows are behind T's 64 (8 KB)
-                    mma_ts(tmem + B::ACC + 64, tmem + B::P + k * 8, mn_desc(tp + pl * ATOM + 8192 + k * 2048, ATOM), ID_64 | ACROSS, pl < 2 || k > 0);
-            mma_commit(wait.mma);
-        }
-        // Y1 while the products run
-        {
-            float f[16];
-            read16(rows + RF_OUT + tok, f);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                float a, b;
-                bf2_unpack(dy[i], a, b);
-                f[2 * i] *= a;
-                f[2 * i + 1] *= b;
+    if (w.warp > 0 && w.warp <= LOADERS) {
+        dep_wait();
+        w.load(p, true);
+    } else if (w.warp == 0) {                   // the issuing warp (the first: the oldest is served first)
+        bool ok = true;
+        for (int s = 0; s < w.chunks && ok; ++s) {
+            const uint32_t kq = w.stage(s), tp = kq + W::KQ, acc = w.tmem + B::ACC;
+            ok = w.turn.arrived(s) && w.turn.next(w.turn.ready);
+            if (!ok) break;
+            if (w.lane == 0) {
+#pragma unroll 1
+                for (int pl = 2; pl >= 0; --pl) steps<KP / 16, false>(acc, w.tmem + B::H + pl * (KP / 2), sw128_desc(kq), ID_64, pl < 2);
+#pragma unroll 1
+                for (int pl = 2; pl >= 0; --pl)       // A's rows are behind T's 64 (8 KB)
+                    steps<4, true>(acc + 64, w.tmem + B::P, mn_desc(tp + pl * ATOM + 8192, ATOM), ID_64 | ACROSS, pl < 2);
+                mma_commit(w.turn.mma);
             }
-            put_parts(lanes + B::Y + cq * 8, 32, f);
+            __syncwarp();
+            if (!(ok = w.turn.next(w.turn.ready))) break;
+            if (w.lane == 0) {
+                // the six products of parts, small ones first: (2, 0), (0, 2), (1, 1), (1, 0), (0, 1), (0, 0)
+#pragma unroll 1
+                for (int q = 0; q < 6; ++q)
+                    steps<4, true>(acc, w.tmem + B::P + (0x052 >> 2 * q & 3) * 32, mn_desc(tp + (0x118 >> 2 * q & 3) * ATOM, ATOM), ID_64 | ACROSS, q > 0);
+                mma_commit(w.turn.mma);
+            }
+            __syncwarp();
+            if (!(ok = w.turn.next(w.turn.ready))) break;
+            if (w.lane == 0) {
+#pragma unroll 1
+                for (int pl = 2; pl >= 0; --pl) {     // K's rows are the first 64 of an atom, Q's the others
+                    steps<4, true>(acc, w.tmem + B::P + pl * 32, mn_desc(kq, ATOM), ID_KP, pl < 2);
+                    steps<4, true>(acc, w.tmem + B::Y + pl * 32, mn_desc(kq + 8192, ATOM), ID_KP, true);
+                }
+                mma_commit(w.turn.mma);
+            }
+            __syncwarp();
         }
-        if (s + 1 < chunks) fetch(s + 1);
-        if (dv < p.Dvp) {
-            float* to = p.dstate + at * p.Dk * p.Dvp + dv;
+    } else {
+        float st[HK];                           // of column dv: the gradient at the state the chunk leaves
+#pragma unroll
+        for (int i = 0; i < HK; ++i) {
+            const int r = w.cq * HK + i;
+            st[i] = p.dh_out && w.row >= 0 && w.on && r < p.Dk ? p.dh_out[w.state + (long long)r * p.Dv] : 0.f;
+        }
+        uint32_t dy[TPT / 2];
+        auto put_dy = [&]() {                   // dY is exact in one part
+#pragma unroll
+            for (int j = 0; j < TPT; j += 16) {
+                uint32_t x[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = dy[j / 2 + i];
+                tmem_st8(w.lanes + B::P + (w.tok + j) / 2, x);
+            }
+        };
+        dep_wait();
+        if (w.chunks > 0) {
+            w.values(p.dy, p.dy_ld, p, w.chunks - 1, dy);
+            put_state<KP>(w.lanes + B::H + w.cq * (HK / 2), st);
+            put_dy();
+        }
+        const int tok = w.tok;
+        for (int s = 0; s < w.chunks; ++s) {
+            const int c = w.chunks - 1 - s, t = w.t0 + c * DC, n = min(DC, w.t1 - t);
+            w.turn.tell();
+            const float* rows = w.rows(s);
+            w.keep(p.dstate + w.at(p, c) * p.Dk * p.Dvp, p, st);
+            if (!w.turn.next(w.turn.mma) || !w.turn.arrived(s)) break;
+#pragma unroll
+            for (int j = 0; j < TPT; j += 16) {
+                uint32_t a[16], b[16];
+                tmem_ld16(w.lanes + B::ACC + tok + j, a);
+                tmem_ld16(w.lanes + B::ACC + 64 + tok + j, b);
+                float f[16];
+                read16(rows + RF_END + tok + j, f);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) f[i] = fmaf(f[i], __uint_as_float(a[i]), __uint_as_float(b[i]));
+                put_parts(w.lanes + B::P + (tok + j) / 2, 32, f);
+            }
+            w.turn.tell();
+#pragma unroll
+            for (int j = 0; j < TPT; j += 16) {     // Y1, and the next chunk's dY, while the products run
+                float f[16];
+                read16(rows + RF_OUT + tok + j, f);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    float a, b;
+                    bf2_unpack(dy[j / 2 + i], a, b);
+                    f[2 * i] *= a;
+                    f[2 * i + 1] *= b;
+                }
+                put_parts(w.lanes + B::Y + (tok + j) / 2, 32, f);
+            }
+            if (s + 1 < w.chunks) w.values(p.dy, p.dy_ld, p, c - 1, dy);
+            if (!w.turn.next(w.turn.mma)) break;
+            const float decay = rows[RF_DECAY];
+            float dr[TPT];
+#pragma unroll
+            for (int j = 0; j < TPT; j += 16) {
+                uint32_t a[16];
+                tmem_ld16(w.lanes + B::ACC + tok + j, a);
+                float f[16];
+                read16(rows + RF_IN + tok + j, f);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    dr[j + i] = __uint_as_float(a[i]);
+                    f[i] *= -dr[j + i];
+                }
+                put_parts(w.lanes + B::P + (tok + j) / 2, 32, f);
+            }
+            w.turn.tell();
+#pragma unroll
+            for (int j = 0; j < TPT; j += 16) {
+                if (w.dv < p.Dvp) {
+                    float* to = p.dr + (w.at(p, c) * DC + tok + j) * p.Dvp + w.dv;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) to[i * p.Dvp] = dr[j + i];
+                }
+                float beta[16];
+                read16(rows + RF_BETA + tok + j, beta);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) beta[i] *= dr[j + i];
+                if (w.on) w.store(p.dv, p.dv_ld, p, t, n, tok + j, beta);
+            }
+            if (!w.turn.next(w.turn.mma)) break;
+            w.turn.release(s);
+            next_state<KP>(w.lanes + B::ACC + w.cq * HK, decay, st);
+            if (s + 1 < w.chunks) {
+                put_state<KP>(w.lanes + B::H + w.cq * (HK / 2), st);
+                put_dy();
+            }
+        }
+        if (p.dh_in && w.row >= 0 && w.on) {
 #pragma unroll
             for (int i = 0; i < HK; ++i)
-                if (cq * HK + i < p.Dk) to[(cq * HK + i) * p.Dvp] = st[i];
-        }
-        ok = wait.products() && ok;
-        tc_fence_after();
-        {
-            uint32_t a[16], b[16];
-            tmem_ld16(lanes + B::ACC + tok, a);
-            tmem_ld16(lanes + B::ACC + 64 + tok, b);
-            float f[16];
-            read16(rows + RF_END + tok, f);
-            tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 16; ++i) f[i] = fmaf(f[i], __uint_as_float(a[i]), __uint_as_float(b[i]));
-            put_parts(lanes + B::P + cq * 8, 32, f);
-        }
-        tmem_st_wait();
-        tc_fence_before();
-        if (__syncthreads_or(!ok)) break;
-        if (threadIdx.x == 0) {
-            tc_fence_after();
-            constexpr int PA[6] = {2, 0, 1, 1, 0, 0}, PB[6] = {0, 2, 1, 0, 1, 0};
-#pragma unroll
-            for (int q = 0; q < 6; ++q)
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    mma_ts(tmem + B::ACC, tmem + B::P + PA[q] * 32 + k * 8, mn_desc(tp + PB[q] * ATOM + k * 2048, ATOM), ID_64 | ACROSS, q > 0 || k > 0);
-            mma_commit(wait.mma);
-        }
-        ok = wait.products() && ok;
-        tc_fence_after();
-        {
-            uint32_t a[16];
-            tmem_ld16(lanes + B::ACC + tok, a);
-            float f[16], beta[16];
-            read16(rows + RF_IN + tok, f);
-            read16(rows + RF_BETA + tok, beta);
-            tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 16; ++i) f[i] *= -__uint_as_float(a[i]);
-            put_parts(lanes + B::P + cq * 8, 32, f);
-            if (dv < p.Dvp) {
-                float* to = p.dr + (at * DC + tok) * p.Dvp + dv;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) to[i * p.Dvp] = __uint_as_float(a[i]);
-            }
-            if (on) {
-                T* to = static_cast<T*>(p.dv) + (long long)(t + tok) * p.dv_ld + h * p.Dv + dv;
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (tok + i < n) to[i * p.dv_ld] = __float2bfloat16_rn(beta[i] * __uint_as_float(a[i]));
-            }
-        }
-        tmem_st_wait();
-        tc_fence_before();
-        if (__syncthreads_or(!ok)) break;
-        if (threadIdx.x == 0) {
-            tc_fence_after();
-#pragma unroll
-            for (int pl = 2; pl >= 0; --pl)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {    // K's rows are the first 64 of an atom, Q's the others
-                    mma_ts(tmem + B::ACC, tmem + B::P + pl * 32 + k * 8, mn_desc(kq + k * 2048, ATOM), ID_KP, pl < 2 || k > 0);
-                    mma_ts(tmem + B::ACC, tmem + B::Y + pl * 32 + k * 8, mn_desc(kq + 8192 + k * 2048, ATOM), ID_KP, true);
-                }
-            mma_commit(wait.mma);
-        }
-        const float decay = rows[RF_DECAY];
-        ok = wait.products() && ok;
-        tc_fence_after();
-#pragma unroll
-        for (int i = 0; i < HK; i += 16) {
-            uint32_t a[16];
-            tmem_ld16(lanes + B::ACC + cq * HK + i, a);
-            tmem_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 16; ++e) st[i + e] = fmaf(decay, st[i + e], __uint_as_float(a[e]));
-        }
-        if (s + 1 < chunks) {
-            put_state();
-            tmem_st_wait();
+                if (w.cq * HK + i < p.Dk) p.dh_in[w.state + (long long)(w.cq * HK + i) * p.Dv] = st[i];
         }
     }
-    if (p.dh_in && row >= 0 && on) {
-#pragma unroll
-        for (int i = 0; i < HK; ++i)
-            if (cq * HK + i < p.Dk) p.dh_in[state + (long long)(cq * HK + i) * p.Dv] = st[i];
-    }
-    cp_async_wait<0>();
-    if (threadIdx.x == 0 && *abort_flag) wait.drain(fetched);
-    tc_fence_before();
-    __syncthreads();
-    if (warp == 0) {
-        tc_fence_after();
-        tmem_dealloc(tmem, 512);
-    }
+    w.close();
 }
 
 template <int KP>
@@ -575,7 +652,7 @@ cudaError_t launch_back_tc(const SeqDeltaParams& p, unsigned* err, cudaStream_t 
     cudaError_t e = cudaFuncSetAttribute(delta_back_tc_kernel<KP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)WalkTc<KP>::BYTES);
     if (e != cudaSuccess) return e;
     const int dvbs = (p.Dv + 127) / 128;
-    return launch_kernel(delta_back_tc_kernel<KP>, dim3((unsigned)(p.ax.S * (long long)p.Hv * dvbs)), dim3(WT), WalkTc<KP>::BYTES, stream, p.slots > 0, 1, p,
+    return launch_kernel(delta_back_tc_kernel<KP>, dim3((unsigned)(p.ax.S * (long long)p.Hv * dvbs)), dim3(WALK_THREADS), WalkTc<KP>::BYTES, stream, p.slots > 0, 1, p,
                          dvbs, err);
 }
 

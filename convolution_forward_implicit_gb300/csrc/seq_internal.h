@@ -223,6 +223,7 @@ struct SeqDeltaParams {
     float* tri;                     // [slots][Hv]: T and A, [2][64][64] fp32; or (planes) [3][128][64] bf16: the three
                                     // parts of [T; A T] (1) or [T; A] (2), rows of 128 bytes in the 128-byte swizzle
     int planes;
+    int compact;                    // 64 rows of q, k, v, y, dy, dv lie within 2^31 bytes each
     float* rows;                    // [slots][Hv][DELTA_ROWS]
     float* dstate;                  // backward: [slots][Hv][Dk][Dvp] gradient at the state a chunk leaves
     float* dr;                      // backward: [slots][Hv][64][Dvp]
