@@ -19,7 +19,7 @@ BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libconvfwd.so")
 SOURCES = ["capi.cu", "tc_conv.cu", "tc_pair.cu", "tc_slab.cu", "tc_slab_pair.cu", "simt.cu", "wgrad.cu",
            "tc_wgrad.cu", "seq_capi.cu", "seq_conv.cu", "seq_scan.cu", "seq_scan_step.cu", "seq_scan_bwd.cu", "seq_norm.cu",
-           "seq_norm_bwd.cu", "seq_delta_capi.cu", "seq_delta.cu", "seq_delta_step.cu", "seq_delta_bwd.cu", "seq_delta_tc.cu", "seq_gnorm_capi.cu",
+           "seq_norm_bwd.cu", "seq_delta_capi.cu", "seq_delta.cu", "seq_delta_step.cu", "seq_delta_bwd.cu", "seq_delta_tc.cu", "seq_delta_grad_tc.cu", "seq_gnorm_capi.cu",
            "seq_gnorm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

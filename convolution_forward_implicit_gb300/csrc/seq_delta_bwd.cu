@@ -184,6 +184,7 @@ struct GradSmem {
     float dots[4][2][DC];            // q.dQ, k.X, k.Z, k.(exp(b_C - b) U dh^T): by the two warps of a row
     float dotq[DC], dotk[DC];        // sums over the value heads
     float hh[DT / 32];
+    int zero[DT / 32];
 };
 
 // Rows of W floats, `width` of them there (a multiple of 4), to rows of LB; `rows` of R rows.  Part of the copy group at hand.
@@ -231,6 +232,7 @@ __global__ void __launch_bounds__(DT, 1) delta_grad_kernel(const __grid_constant
         zero(da);
         zero(dl);
         float vdr = 0.f, hh = 0.f;
+        bool from_zero = true;       // the state before the chunk is zero
         for (int c0 = 0; c0 < p.Dv; c0 += GB) {
             __syncthreads();         // what was read of the block before (or of the last head's matrices)
             load_floats<KP>(s.h0, p.saved + at * p.Dk * p.Dvp, p.Dvp, p.Dk, c0, p.Dvp);
@@ -256,6 +258,7 @@ __global__ void __launch_bounds__(DT, 1) delta_grad_kernel(const __grid_constant
             for (int j = 0; j < KP * GB / DT; ++j) {
                 const int i = threadIdx.x + j * DT, o = i / GB * LB + i % GB;
                 hh = fmaf(s.h0[o], s.dh[o], hh);
+                from_zero = from_zero && s.h0[o] == 0.f;
             }
             warp_mma<NT>(dq, Along<T>{s.dy, LB}, Along<float>{s.h0, LB}, m0, n0, 0, GB);
             warp_mma<NT>(x, Along<float>{s.dr, LB}, Along<float>{s.h0, LB}, m0, n0, 0, GB);
@@ -270,7 +273,11 @@ __global__ void __launch_bounds__(DT, 1) delta_grad_kernel(const __grid_constant
         if ((threadIdx.x & 3) == 0) s.vdr[threadIdx.x >> 2] = vdr;
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) hh += __shfl_xor_sync(0xffffffffu, hh, d);
-        if (lane == 0) s.hh[warp] = hh;
+        from_zero = __all_sync(0xffffffffu, from_zero);
+        if (lane == 0) {
+            s.hh[warp] = hh;
+            s.zero[warp] = from_zero;
+        }
         float2 end = make_float2(0.f, 0.f);
         if (warp == 0) {
             float2 b[2];
@@ -373,12 +380,22 @@ __global__ void __launch_bounds__(DT, 1) delta_grad_kernel(const __grid_constant
                 if (lane + d < 32) sum += o;
             }
             const double next = __shfl_down_sync(0xffffffffu, sum, 1);
-            const float dg[2] = {(float)sum, (float)(db[1] + (lane < 31 ? next : 0.0))};
+            double dg[2] = {sum, db[1] + (lane < 31 ? next : 0.0)};
+            int zero = 1;
+#pragma unroll
+            for (int w = 0; w < DT / 32; ++w) zero = zero && s.zero[w];
+            // All of db together is <h0, gradient at h0>: nothing where h0 is.  The first half of the tokens then has dg from
+            // the sums before it, the very first none.
+            const double whole = __shfl_sync(0xffffffffu, sum, 0);
+            if (zero && lane < 16) {
+                dg[0] -= whole;
+                dg[1] -= whole;
+            }
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int r = 2 * lane + i;
                 if (r < cut.n)       // (nothing passes a factor of zero)
-                    p.dg[(cut.t0 + r) * p.dg_ld + h] = expf(p.g[(cut.t0 + r) * p.g_ld + h]) == 0.f ? 0.f : dg[i];
+                    p.dg[(cut.t0 + r) * p.dg_ld + h] = expf(p.g[(cut.t0 + r) * p.g_ld + h]) == 0.f ? 0.f : (float)dg[i];
             }
         }
         const float beta0 = s.beta[m0 + g], beta1 = s.beta[m0 + g + 8];
@@ -451,6 +468,7 @@ cudaError_t launch(const SeqDeltaParams& p, cudaStream_t stream) {
     else if (p.Dk <= 64) e = narrow ? launch_back<T, 64, 16>(p, stream) : launch_back<T, 64, 32>(p, stream);
     else e = narrow ? launch_back<T, 128, 16>(p, stream) : launch_back<T, 128, 32>(p, stream);
     if (e != cudaSuccess || p.slots == 0) return e;
+    if (p.planes) return launch_seq_delta_grad_tc(p, stream);
     return p.Dk <= 64 ? launch_grad<T, 64>(p, stream) : launch_grad<T, 128>(p, stream);
 }
 

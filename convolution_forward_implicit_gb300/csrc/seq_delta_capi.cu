@@ -109,6 +109,9 @@ static conv_status delta_call(seq_plan_t p, const seq_delta_args* a, seq_directi
     auto paired = [&](const void* v, int64_t ld) { return !v || (reinterpret_cast<uintptr_t>(v) % (2 * e) == 0 && ld % 2 == 0); };
     q.pairs = p->W % 2 == 0 && paired(a->v, a->v_ld) && paired(a->y, a->y_ld) && paired(a->dy, a->dy_ld) && paired(a->dv, a->dv_ld);
     q.key_pairs = p->N % 2 == 0 && paired(a->dq, a->dq_ld) && paired(a->dk, a->dk_ld);
+    auto grouped = [&](const void* v, int64_t ld) { return !v || (reinterpret_cast<uintptr_t>(v) % 16 == 0 && (uint64_t)ld * e % 16 == 0); };
+    q.val_wide = (p->W * e) % 16 == 0 && grouped(a->v, a->v_ld) && grouped(a->dy, a->dy_ld);
+    q.key_wide = (p->N * e) % 16 == 0 && grouped(a->dq, a->dq_ld) && grouped(a->dk, a->dk_ld);
     auto aligned = [](const void* v) { return reinterpret_cast<uintptr_t>(v) % 16 == 0; };
     q.quads = p->W % 4 == 0 && aligned(a->h_in) && aligned(a->h_out);
     q.sms = p->sms;

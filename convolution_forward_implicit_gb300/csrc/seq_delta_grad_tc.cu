@@ -1,0 +1,496 @@
+// Gated delta rule in bf16 backward, every chunk by itself, on tcgen05 tensor cores: see seq_delta_bwd.cu for the
+// formulas.  A CTA takes a chunk and a key head, its value heads in turn, and 64 columns of their states at a time.  Rows of
+// the chunk are TMEM lanes, those of dY (and dQ) the first 64, those of dR, U (and X, Z) the others:
+//   D1 = [dY; dR] h0^T     D2 = [dY; dR] U^T     D3 = [.; U] dh^T            over all columns, then with
+//   P = E . dY U^T, S = -E . dR U^T (from D2):
+//   D4 = [P |k|^-1; S |k|^-1] K                  D5 = [.; (P |q|^-1)^T Q + (S beta |k|^-1)^T K]
+// and dQ = scale exp(b) D1 + scale D4, X = D4 - exp(b) D1, Z = exp(b_C - b) D3 + D5 in the rows of a lane.  Operands that
+// are not exact in bf16 are three bf16 parts each (24 bits), written by the threads; products of two such take the six
+// large ones of the parts' nine.
+//
+// What bounds it: the products (about 10000 cycles of 64 for a chunk and value head at 128 x 128) and splitting the states into
+// parts, which runs beside them but for dY, dR and U.
+#include "seq_delta.cuh"
+#include "seq_delta_tc.cuh"
+
+namespace convfwd {
+namespace {
+
+constexpr int GT_WARPS = 8, GT_THREADS = 32 * (GT_WARPS + 1);        // the last warp issues
+constexpr int GW = 32 * GT_WARPS;
+
+template <int KP>
+struct GradTc {
+    static constexpr uint32_t KQ = KP / 64 * ATOM;                    // [K; Q], 64 columns an atom
+    static constexpr uint32_t A = KQ, U = A + 3 * ATOM, H = U + 3 * 8192, DH = H + 3 * ATOM;
+    static constexpr uint32_t M0 = H, M1 = DH, M3 = DH + 3 * 8192;    // the chunk's matrices, where the states were
+    static constexpr uint32_t REST = DH + 3 * ATOM;
+    static constexpr uint32_t BYTES = REST + 6144 + 1024;
+    static constexpr uint32_t D1 = 0, D3 = 128, D4 = 256, D5 = 384, D2 = 384;      // TMEM columns
+};
+struct GradRest {
+    float2 b[DC];
+    float rq[DC], rk[DC], beta[DC], vdr[DC], dotq[DC], dotk[DC];
+    float dots[4][2][DC];
+    float hh[GT_WARPS];
+    int zero[GT_WARPS];
+    alignas(8) uint64_t bars[4];
+    uint32_t slot;
+    int abort;
+};
+
+// 8 values to three parts of 16 bytes at `to`, `plane` bytes apart.
+__device__ __forceinline__ void split8(uint8_t* to, uint32_t plane, const float (&x)[8]) {
+    float r[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = x[i];
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            w[i] = bf2_pack(r[2 * i], r[2 * i + 1]);
+            if (k < 2) {
+                float a, b;
+                bf2_unpack(w[i], a, b);
+                r[2 * i] -= a;
+                r[2 * i + 1] -= b;
+            }
+        }
+        *reinterpret_cast<uint4*>(to + k * plane) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+__device__ __forceinline__ void floats8(const float* from, bool first, bool second, float (&x)[8]) {
+    const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float4 a = first ? *reinterpret_cast<const float4*>(from) : z, b = second ? *reinterpret_cast<const float4*>(from + 4) : z;
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+}
+// 8 bf16 of a row from column c of `width` on; wide: whole aligned groups
+__device__ __forceinline__ uint4 row8(const __nv_bfloat16* from, int c, int width, bool there, bool wide) {
+    uint32_t w[4] = {0, 0, 0, 0};
+    if (there) {
+        if (wide) {
+            if (c < width) return *reinterpret_cast<const uint4*>(from);
+        } else {
+            const uint16_t* h = reinterpret_cast<const uint16_t*>(from);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (c + i < width) w[i / 2] |= (uint32_t)h[i] << (i % 2 * 16);
+        }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void meet() { asm volatile("bar.sync 1, %0;" ::"n"(GW) : "memory"); }      // the eight warps
+
+// A from shared memory too
+__device__ __forceinline__ void mma_ss_k4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate, uint32_t astep, uint32_t bstep) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) mma_bf16(d, a + k * (astep >> 4), b + k * (bstep >> 4), idesc, accumulate || k > 0 ? 1u : 0u);
+}
+// the products of parts that carry 24 bits: (2, 0), (0, 2), (1, 1), (1, 0), (0, 1), (0, 0)
+__device__ __forceinline__ int part_a(int q) { return 0x052 >> 2 * q & 3; }
+__device__ __forceinline__ int part_b(int q) { return 0x118 >> 2 * q & 3; }
+
+template <int KP, bool SHARED>
+__global__ void __launch_bounds__(GT_THREADS, 1) delta_grad_tc_kernel(const __grid_constant__ SeqDeltaParams p, unsigned* err) {
+    extern __shared__ uint8_t smem_raw[];
+    using G = GradTc<KP>;
+    using T = __nv_bfloat16;
+    constexpr int HC = KP / 2;                   // columns of a row that a thread holds of a result
+    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    uint8_t* sm = smem_raw + (base - smem_u32(smem_raw));
+    GradRest& s = *reinterpret_cast<GradRest*>(sm + G::REST);
+    const CutPiece cut = cut_piece(p.ax, blockIdx.x, DC);
+    if (cut.n <= 0) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wq = warp & 3, hf = warp >> 2;
+    const int kh = blockIdx.y, rep = SHARED ? p.Hv / p.Hk : 1, blocks = (p.Dv + 63) / 64;
+    const uint32_t ready = smem_u32(&s.bars[0]), bar_h = smem_u32(&s.bars[1]), bar_e = smem_u32(&s.bars[2]);
+    volatile int* abort_flag = &s.abort;
+    if (threadIdx.x == 0) {
+        mbar_init(ready, GT_WARPS);
+        mbar_init(bar_h, 1);
+        mbar_init(bar_e, 1);
+        s.abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 0) {
+        tmem_alloc(smem_u32(&s.slot), 512);
+        tmem_relinquish();
+    }
+    if (warp < GT_WARPS) {
+        load_kq<KP, GW>(base, static_cast<const T*>(p.k) + cut.t0 * p.k_ld + kh * p.Dk, static_cast<const T*>(p.q) + cut.t0 * p.q_ld + kh * p.Dk, p.k_ld,
+                        p.q_ld, cut.n, p.Dk, threadIdx.x);
+        cp_async_commit();
+        for (int i = threadIdx.x; i < 2 * 8192 / 16; i += GW)      // dY is one part: its others are zero
+            *reinterpret_cast<uint4*>(sm + G::A + (1 + i / 512) * ATOM + i % 512 * 16) = make_uint4(0, 0, 0, 0);
+        if (threadIdx.x < DC) s.dotq[threadIdx.x] = s.dotk[threadIdx.x] = 0.f;
+        cp_async_wait<0>();
+        fence_proxy_async();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s.slot, lanes = tmem + ((uint32_t)(wq * 32) << 16);
+    constexpr uint32_t B_ACROSS = 1u << 16, A_ACROSS = 1u << 15, ID_KP = idesc_f32acc(128, KP, 1u), ID_64 = idesc_f32acc(128, 64, 1u);
+    // After a wait has run out every later one ends at once (see wait_turn); the warps go on together to the end.
+    if (warp == GT_WARPS) {                      // ---- the issuing warp
+        uint32_t turn = 0;
+        auto next = [&]() {
+            const bool ok = wait_turn(ready, turn, abort_flag, err);
+            turn ^= 1;
+            tc_fence_after();
+            return ok && lane == 0;
+        };
+        for (int h = 0; h < rep; ++h) {
+            for (int v = 0; v < blocks; ++v) {
+                if (next()) {
+#pragma unroll 1
+                    for (int q = 0; q < 6; ++q)
+                        mma_ss_k4(tmem + G::D2, sw128_desc(base + G::A + part_a(q) * ATOM), sw128_desc(base + G::U + part_b(q) * 8192), ID_64, v > 0 || q > 0, 32, 32);
+#pragma unroll 1
+                    for (int q = 0; q < 6; ++q)
+                        mma_ss_k4(tmem + G::D1, sw128_desc(base + G::A + part_a(q) * ATOM), sw128_desc(base + G::H + part_b(q) * ATOM), ID_KP, v > 0 || q > 0, 32, 32);
+                    mma_commit(bar_h);
+                }
+                __syncwarp();
+                if (next()) {
+#pragma unroll 1
+                    for (int q = 0; q < 6; ++q)      // (U's rows are the second 64: the first are whatever lies before it)
+                        mma_ss_k4(tmem + G::D3, sw128_desc(base + G::U + part_a(q) * 8192 - 8192), sw128_desc(base + G::DH + part_b(q) * ATOM), ID_KP,
+                                  v > 0 || q > 0, 32, 32);
+                    mma_commit(bar_e);
+                }
+                __syncwarp();
+            }
+            if (next()) {
+#pragma unroll 1
+                for (int pl = 2; pl >= 0; --pl)
+                    mma_ss_k4(tmem + G::D4, sw128_desc(base + G::M0 + pl * ATOM), mn_desc(base, ATOM), ID_KP | B_ACROSS, pl < 2, 32, 2048);
+#pragma unroll 1
+                for (int pl = 2; pl >= 0; --pl) {    // (blocks of rows 8 KB apart, the matrix the second)
+                    mma_ss_k4(tmem + G::D5, mn_desc(base + G::M1 + pl * 8192 - 8192, 8192), mn_desc(base + 8192, ATOM), ID_KP | A_ACROSS | B_ACROSS, pl < 2, 2048, 2048);
+                    mma_ss_k4(tmem + G::D5, mn_desc(base + G::M3 + pl * 8192 - 8192, 8192), mn_desc(base, ATOM), ID_KP | A_ACROSS | B_ACROSS, true, 2048, 2048);
+                }
+                mma_commit(bar_e);
+            }
+            __syncwarp();
+        }
+    } else {                                     // ---- the rows' warps
+        uint32_t turn_h = 0, turn_e = 0;
+        auto wait_h = [&]() {
+            wait_turn(bar_h, turn_h, abort_flag, err);
+            turn_h ^= 1;
+            tc_fence_after();
+        };
+        auto wait_e = [&]() {
+            wait_turn(bar_e, turn_e, abort_flag, err);
+            turn_e ^= 1;
+            tc_fence_after();
+        };
+        auto tell = [&]() {
+            fence_proxy_async();
+            tc_fence_before();
+            __syncwarp();
+            arrive_once(ready);
+        };
+        // the row of K (second 64 lanes) or Q that the lane holds: 16-byte pieces of the swizzled atoms
+        const int i = (wq & 1) * 32 + lane, isk = wq >> 1;
+        auto piece = [&](int row, int c) {       // columns 8 c .. of row (K: 0 .. 63, Q: 64 .. 127)
+            return *reinterpret_cast<const uint4*>(sm + (c >> 3) * ATOM + row * 128 + ((c & 7) ^ (row & 7)) * 16);
+        };
+        {
+            const int row = threadIdx.x >> 1;
+            float sum = 0.f;
+#pragma unroll 4
+            for (int c = threadIdx.x & 1; c < KP / 8; c += 2) {
+                const uint4 w = piece(row, c);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float a, b;
+                    bf2_unpack(e == 0 ? w.x : e == 1 ? w.y : e == 2 ? w.z : w.w, a, b);
+                    sum = fmaf(a, a, fmaf(b, b, sum));
+                }
+            }
+            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+            if ((threadIdx.x & 1) == 0) (row < 64 ? s.rk : s.rq)[row & 63] = p.norm ? 1.f / sqrtf(sum + QK_EPS) : 1.f;
+        }
+        float total[SHARED ? HC : 1];
+#pragma unroll
+        for (int c = 0; c < (SHARED ? HC : 1); ++c) total[c] = 0.f;
+        dep_wait();
+        // A thread's pieces of 8 columns: rows r8, r8 + 32, ...  What a block needs is on its way while the one before is worked
+        // on, in registers: with loads where they are used the kernel took 794 us instead of @@ (8192 tokens, 32 heads).
+        const int r8 = threadIdx.x >> 3, c8 = threadIdx.x & 7;
+        const uint32_t place = (uint32_t)(r8 * 128 + (c8 ^ (r8 & 7)) * 16);
+        float h0[KP / 32][8], u[2][8], dr[2][8];
+        uint4 dy[2], vv[2];
+        auto states = [&](const float* from, int h, int v, float (&x)[KP / 32][8]) {
+            const long long at = (long long)blockIdx.x * p.Hv + h;
+            const int col = v * 64 + c8 * 8;
+#pragma unroll
+            for (int j = 0; j < KP / 32; ++j) {
+                const int r = r8 + 32 * j;
+                floats8(from + (at * p.Dk + r) * p.Dvp + col, col < p.Dvp && r < p.Dk, col + 4 < p.Dvp && r < p.Dk, x[j]);
+            }
+        };
+        auto tokens = [&](int h, int v) {
+            const long long at = (long long)blockIdx.x * p.Hv + h;
+            const int col = v * 64 + c8 * 8;
+            const bool first = col < p.Dvp, second = col + 4 < p.Dvp;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int r = r8 + 32 * j;
+                floats8(p.saved + p.saved_u + (at * DC + r) * p.Dvp + col, first, second, u[j]);
+                floats8(p.dr + (at * DC + r) * p.Dvp + col, first, second, dr[j]);
+                dy[j] = row8(static_cast<const T*>(p.dy) + (cut.t0 + r) * p.dy_ld + h * p.Dv + col, col, p.Dv, r < cut.n, p.val_wide);
+                vv[j] = row8(static_cast<const T*>(p.v) + (cut.t0 + r) * p.v_ld + h * p.Dv + col, col, p.Dv, r < cut.n, p.val_wide);
+            }
+        };
+        states(p.saved, kh * rep, 0, h0);
+        tokens(kh * rep, 0);
+        for (int h = kh * rep; h < (kh + 1) * rep; ++h) {
+            float vdr[2] = {0.f, 0.f}, hh = 0.f;
+            bool from_zero = true;               // the state before the chunk is zero
+            for (int v = 0; v < blocks; ++v) {
+                const bool more = v + 1 < blocks || h + 1 < (kh + 1) * rep;
+                const int h_next = v + 1 < blocks ? h : h + 1, v_next = v + 1 < blocks ? v + 1 : 0;
+                if (v > 0) wait_h();                 // the block before has read its h0
+#pragma unroll
+                for (int j = 0; j < KP / 32; ++j) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) from_zero = from_zero && h0[j][e] == 0.f;
+                    split8(sm + G::H + place + j * 4096, ATOM, h0[j]);
+                }
+                float dh[KP / 32][8];
+                states(p.dstate, h, v, dh);
+                if (v > 0) wait_e();                 // and all else
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    split8(sm + G::U + place + j * 4096, 8192, u[j]);
+                    split8(sm + G::A + 8192 + place + j * 4096, ATOM, dr[j]);
+                    *reinterpret_cast<uint4*>(sm + G::A + place + j * 4096) = dy[j];
+                    const uint32_t w[4] = {vv[j].x, vv[j].y, vv[j].z, vv[j].w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float a, b;
+                        bf2_unpack(w[e], a, b);
+                        vdr[j] = fmaf(a, dr[j][2 * e], fmaf(b, dr[j][2 * e + 1], vdr[j]));
+                    }
+                }
+                tell();
+                if (more) tokens(h_next, v_next);
+#pragma unroll
+                for (int j = 0; j < KP / 32; ++j) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) hh = fmaf(h0[j][e], dh[j][e], hh);
+                    split8(sm + G::DH + place + j * 4096, ATOM, dh[j]);
+                }
+                tell();
+                if (more) states(p.saved, h_next, v_next, h0);
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+#pragma unroll
+                for (int d = 1; d < 8; d <<= 1) vdr[j] += __shfl_xor_sync(0xffffffffu, vdr[j], d);
+                if (c8 == 0) s.vdr[r8 + 32 * j] = vdr[j];
+            }
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) hh += __shfl_xor_sync(0xffffffffu, hh, d);
+            from_zero = __all_sync(0xffffffffu, from_zero);
+            if (lane == 0) {
+                s.hh[warp] = hh;
+                s.zero[warp] = from_zero;
+            }
+            if (warp == 0) {
+                float2 b[2];
+                chunk_decay(p.g + cut.t0 * p.g_ld + h, p.g_ld, cut.n, b);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int r = 2 * lane + e;
+                    s.b[r] = b[e];
+                    s.beta[r] = r < cut.n ? p.beta[(cut.t0 + r) * p.beta_ld + h] : 0.f;
+                }
+            }
+            meet();
+            const float2 bi = s.b[i], end = s.b[DC - 1];
+            const float rqi = s.rq[i], rki = s.rk[i], beta = s.beta[i];
+            wait_h();
+            wait_e();
+            // ---- the chunk's matrices from D2: 32 columns of the lane's row
+#pragma unroll
+            for (int c = 0; c < 32; c += 16) {
+                uint32_t d[16];
+                tmem_ld16(lanes + G::D2 + hf * 32 + c, d);
+                tmem_ld_wait();
+                const float f = isk ? -1.f : p.scale, own = isk ? beta * rki : rqi;
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    float by_key[8], by_row[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int j = hf * 32 + c + half * 8 + e;
+                        const float x = j < i || (j == i && !isk) ? f * __uint_as_float(d[half * 8 + e]) * decay_between(bi, s.b[j]) : 0.f;
+                        by_key[e] = x * s.rk[j];
+                        by_row[e] = x * own;
+                    }
+                    const int chunk = hf * 4 + c / 8 + half;
+                    split8(sm + G::M0 + (isk * 64 + i) * 128 + ((chunk ^ (i & 7)) * 16), ATOM, by_key);
+                    split8(sm + (isk ? G::M3 : G::M1) + i * 128 + ((chunk ^ (i & 7)) * 16), 8192, by_row);
+                }
+            }
+            tell();
+            const float eb = expf(bi.x) * (1.f + bi.y), fq = p.scale * eb, fz = decay_between(end, bi);
+            wait_e();
+            // ---- rows: dQ (first 64 lanes), X and Z (the others), in pieces of 16 columns
+            float dot[3][4] = {};                // (four sums each: their differences make dg)
+            float out[SHARED ? 1 : HC];
+#pragma unroll
+            for (int c = 0; c < HC; c += 16) {
+                const int col = hf * HC + c;
+                uint32_t d1[16], d4[16], d3[16], d5[16];
+                tmem_ld16(lanes + G::D1 + col, d1);
+                tmem_ld16(lanes + G::D4 + col, d4);
+                tmem_ld16(lanes + G::D3 + col, d3);
+                tmem_ld16(lanes + G::D5 + col, d5);
+                const int row = isk ? i : 64 + i;
+                const uint4 w0 = piece(row, col / 8), w1 = piece(row, col / 8 + 1);
+                const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    float lo, hi;
+                    bf2_unpack(w[e / 2], lo, hi);
+                    const float own = e & 1 ? hi : lo;
+                    float r;
+                    if (!isk) {
+                        r = fmaf(fq, __uint_as_float(d1[e]), __uint_as_float(d4[e]));
+                        dot[0][e & 3] = fmaf(own, r, dot[0][e & 3]);
+                    } else {
+                        const float x = fmaf(-eb, __uint_as_float(d1[e]), __uint_as_float(d4[e])), zu = fz * __uint_as_float(d3[e]);
+                        const float z = zu + __uint_as_float(d5[e]);
+                        dot[0][e & 3] = fmaf(own, x, dot[0][e & 3]);
+                        dot[1][e & 3] = fmaf(own, z, dot[1][e & 3]);
+                        dot[2][e & 3] = fmaf(own, zu, dot[2][e & 3]);
+                        r = fmaf(beta, x, z);
+                    }
+                    if (SHARED) total[SHARED ? c + e : 0] += r;
+                    else out[SHARED ? 0 : c + e] = r;
+                }
+            }
+            if (!isk) {
+                s.dots[0][hf][i] = (dot[0][0] + dot[0][1]) + (dot[0][2] + dot[0][3]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 3; ++k) s.dots[1 + k][hf][i] = (dot[k][0] + dot[k][1]) + (dot[k][2] + dot[k][3]);
+            }
+            meet();
+            if (warp == 0) {                     // dbeta and dg, two tokens a lane
+                float all = 0.f, sum3 = 0.f;
+                double db[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int r = 2 * lane + e;
+                    const float rq = s.rq[r], rk = s.rk[r], be = s.beta[r];
+                    const float qq = rq * (s.dots[0][0][r] + s.dots[0][1][r]), kx = rk * (s.dots[1][0][r] + s.dots[1][1][r]);
+                    const float kz = rk * (s.dots[2][0][r] + s.dots[2][1][r]);
+                    sum3 += rk * (s.dots[3][0][r] + s.dots[3][1][r]);
+                    db[e] = (double)(qq - kz) + (double)(be * kx);
+                    if (r < cut.n) p.dbeta[(cut.t0 + r) * p.dbeta_ld + h] = s.vdr[r] + kx;
+                    s.dotq[r] += qq;
+                    s.dotk[r] += fmaf(be, kx, kz);
+                }
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1) sum3 += __shfl_xor_sync(0xffffffffu, sum3, d);
+#pragma unroll
+                for (int w = 0; w < GT_WARPS; ++w) all += s.hh[w];
+                if (lane == 31) db[1] += (double)fmaf(expf(end.x) * (1.f + end.y), all, sum3);
+                double sum = db[0] + db[1];      // from the lane's first token on
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const double o = __shfl_down_sync(0xffffffffu, sum, d);
+                    if (lane + d < 32) sum += o;
+                }
+                const double after = __shfl_down_sync(0xffffffffu, sum, 1);
+                double dg[2] = {sum, db[1] + (lane < 31 ? after : 0.0)};
+                int zero = 1;
+#pragma unroll
+                for (int w = 0; w < GT_WARPS; ++w) zero = zero && s.zero[w];
+                // All of db together is <h0, gradient at h0>: nothing where h0 is.  The first half of the tokens then has dg from
+                // the sums before it, the very first none.
+                const double whole = __shfl_sync(0xffffffffu, sum, 0);
+                if (zero && lane < 16) {
+                    dg[0] -= whole;
+                    dg[1] -= whole;
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int r = 2 * lane + e;
+                    if (r < cut.n)               // (nothing passes a factor of zero)
+                        p.dg[(cut.t0 + r) * p.dg_ld + h] = expf(p.g[(cut.t0 + r) * p.g_ld + h]) == 0.f ? 0.f : (float)dg[e];
+                }
+            }
+            if (!SHARED || h == (kh + 1) * rep - 1) {
+                meet();
+                // through the lengths: d(k / |k|) = (d - k^ (k^.d)) / |k|
+                if (i < cut.n) {
+                    const float r = isk ? rki : rqi, f = p.norm ? (isk ? s.dotk[i] : s.dotq[i]) * r : 0.f;
+                    T* to = isk ? static_cast<T*>(p.dk) + (cut.t0 + i) * p.dk_ld + kh * p.Dk : static_cast<T*>(p.dq) + (cut.t0 + i) * p.dq_ld + kh * p.Dk;
+                    const int row = isk ? i : 64 + i;
+#pragma unroll
+                    for (int c = 0; c < HC; c += 8) {
+                        const int col = hf * HC + c;
+                        const uint4 q = piece(row, col / 8);
+                        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+                        float x[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            float lo, hi;
+                            bf2_unpack(w[e / 2], lo, hi);
+                            x[e] = r * ((SHARED ? total[SHARED ? c + e : 0] : out[SHARED ? 0 : c + e]) - (e & 1 ? hi : lo) * f);
+                        }
+                        if (p.key_wide) {
+                            if (col < p.Dk) seq_stv<8>(to + col, x);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                if (col + e < p.Dk) to[col + e] = __float2bfloat16_rn(x[e]);
+                        }
+                    }
+                }
+            }
+            meet();                              // (the next head's sums go where these were read)
+        }
+    }
+    if (s.abort && threadIdx.x == 0) {           // products that may still run: bounded, before TMEM goes
+        const long long since = clock64();
+        while (clock64() - since < WAIT_CYCLES / 8) {
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int KP, bool SHARED>
+cudaError_t launch_of(const SeqDeltaParams& p, unsigned* err, cudaStream_t stream) {
+    const auto kernel = delta_grad_tc_kernel<KP, SHARED>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)GradTc<KP>::BYTES);
+    if (e != cudaSuccess) return e;
+    return launch_kernel(kernel, dim3((unsigned)p.slots, (unsigned)p.Hk), dim3(GT_THREADS), GradTc<KP>::BYTES, stream, true, 1, p, err);
+}
+
+}  // namespace
+
+cudaError_t launch_seq_delta_grad_tc(const SeqDeltaParams& p, cudaStream_t stream) {
+    static_assert(sizeof(GradRest) <= 6144, "room behind the operands");
+    unsigned* err = device_error_word();
+    if (!err) return cudaErrorUnknown;
+    const bool shared = p.Hv > p.Hk;
+    if (p.Dk <= 64) return shared ? launch_of<64, true>(p, err, stream) : launch_of<64, false>(p, err, stream);
+    return shared ? launch_of<128, true>(p, err, stream) : launch_of<128, false>(p, err, stream);
+}
+
+}  // namespace convfwd

@@ -10,7 +10,7 @@
 //
 // What bounds a walk: the products and the threads' work between them follow one another, three times a chunk.
 #include "seq_delta.cuh"
-#include "tc_common.cuh"
+#include "seq_delta_tc.cuh"
 
 namespace convfwd {
 namespace {
@@ -19,17 +19,8 @@ constexpr int WT = 512;                       // threads that hold lanes: two wa
 constexpr int TPT = 64 * 128 / WT;            // tokens of a chunk a thread holds of its lane
 constexpr int LOADERS = 3;                    // warps behind the first, issuing, one that fetch
 constexpr int WALK_THREADS = WT + 32 * (1 + LOADERS);
-constexpr uint32_t ATOM = 128 * 128;          // 128 rows of 64 bf16
 constexpr uint32_t PLANES = 3 * ATOM;         // [T; A T] (backward: [T; A]) in three parts
 
-__device__ __forceinline__ uint64_t mn_desc(uint32_t saddr, uint32_t stride) {     // N side by side, blocks of 64 `stride` bytes apart
-    uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4);
-    d |= (uint64_t)((stride >> 4) & 0x3FFFu) << 16;
-    d |= (uint64_t)(1024 >> 4) << 32;
-    d |= (uint64_t)1 << 46;
-    d |= (uint64_t)2 << 61;
-    return d;
-}
 // D += A B for 64 of k, A in TMEM (a lane's 16 bf16 of a step in 8 columns), issued by the calling thread: four steps in one
 // block, B's address BSTEP bytes further each (4 steps one by one took about 100 cycles each to issue).
 template <int BSTEP>
@@ -97,33 +88,6 @@ struct WalkTc {
     static constexpr uint32_t H = 0, P = 3 * KP / 2, ACC = P + 96;       // TMEM columns
 };
 
-// A wait of a warp for a barrier's phase, for about a second at most.  The limit goes by the SM's clock: reading the global
-// timer between two looks costs more than a hand-off takes (8192 x 32 heads: walk 449 us with it, see the figures above).
-constexpr long long WAIT_CYCLES = 2000000000ll;
-// Every lane looks, and the arrivals below are predicated: a branch that only one lane takes costs a few hundred cycles
-// at each hand-off until its warp is together again (2048 x 16 heads: 233 us with them, 184 with the waits alone changed).
-__device__ __forceinline__ bool wait_turn(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned* err) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const long long since = clock64();
-    bool ok = true;
-    while (ok && !mbar_try_wait(bar, parity)) {
-        if (*abort_flag) {
-            ok = false;
-        } else if (clock64() - since > WAIT_CYCLES) {
-            *abort_flag = 1;
-            atomicOr(err, ERR_WAIT_TIMEOUT);
-            ok = false;
-        }
-    }
-    return __all_sync(0xffffffffu, ok) != 0;
-}
-__device__ __forceinline__ void arrive_once(uint32_t bar) {       // one arrival of a converged warp
-    asm volatile(
-        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-        "@e mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];\n\t}" ::"r"(bar)
-        : "memory");
-}
-
 // The barriers of a walk's CTA, every wait bounded.  The threads that hold lanes (16 warps) tell the issuing warp when its
 // operands are ready, and learn from `mma` when its products are done; `full`: a stage's operands have arrived, `empty`:
 // it may be written again.
@@ -160,19 +124,6 @@ struct Turns {
             }
     }
 };
-
-// K and Q rows of a chunk to [K; Q] atoms in the 128-byte swizzle; rows at and behind n and columns behind the width are zero.
-template <int KP>
-__device__ __forceinline__ void load_kq(uint32_t to, const __nv_bfloat16* k, const __nv_bfloat16* q, long long k_ld, long long q_ld, int n, int width, int thread) {
-    constexpr int CPR = KP / 8;                  // 16-byte pieces of a row
-    for (int i = thread; i < 128 * CPR; i += 32 * LOADERS) {
-        const int row = i / CPR, c = i % CPR, r = row & 63;
-        const bool there = r < n && c * 8 < width;
-        const __nv_bfloat16* from = row < 64 ? k : q;
-        const uint32_t step = (uint32_t)(row < 64 ? k_ld : q_ld);
-        cp_async_16(to + (uint32_t)(c / 8) * ATOM + row * 128 + ((c % 8) ^ (row & 7)) * 16, there ? from + r * step + c * 8 : from, there ? 16 : 0);
-    }
-}
 
 // The start of a walk's CTA: its place, barriers, TMEM.
 template <int KP>
@@ -244,7 +195,7 @@ struct Walk {
                 bulk_g2s(to + WalkTc<KP>::KQ, reinterpret_cast<const uint8_t*>(p.tri) + at(p, c) * PLANES, PLANES, bar);
                 bulk_g2s(to + WalkTc<KP>::KQ + PLANES, p.rows + at(p, c) * DELTA_ROWS, DELTA_ROWS * 4, bar);
             }
-            load_kq<KP>(to, static_cast<const __nv_bfloat16*>(p.k) + t * p.k_ld + kh * p.Dk, static_cast<const __nv_bfloat16*>(p.q) + t * p.q_ld + kh * p.Dk,
+            load_kq<KP, 32 * LOADERS>(to, static_cast<const __nv_bfloat16*>(p.k) + t * p.k_ld + kh * p.Dk, static_cast<const __nv_bfloat16*>(p.q) + t * p.q_ld + kh * p.Dk,
                         p.k_ld, p.q_ld, min(DC, t1 - t), p.Dk, thread);
             cp_async_commit();
             cp_async_wait<0>();

@@ -479,9 +479,13 @@ __global__ void __launch_bounds__(GT, BWD ? 3 : 4) gn_apply_kernel(const __grid_
     if (on) f.params(p, at.c);
     wait_before();
     if (SELF) {
-        if (cut.n <= 0) return;
-        const int g0 = blockIdx.y * txn * V / cpg;
-        join_groups<BWD>(p, cut, g0, min(txn * V, p.D - blockIdx.y * txn * V) / cpg, joined, buf);
+        const int g0 = blockIdx.y * txn * V / cpg, groups = min(txn * V, p.D - blockIdx.y * txn * V) / cpg;
+        if (cut.n <= 0) {           // (a first piece without tokens: an empty sequence; each has a slot of its own)
+            if (!BWD && p.stats && cut.index == 0)
+                for (int gi = threadIdx.x; gi < groups; gi += blockDim.x) reinterpret_cast<float2*>(p.stats)[(long long)cut.s * p.G + g0 + gi] = dup(0.f);
+            return;
+        }
+        join_groups<BWD>(p, cut, g0, groups, joined, buf);
     }
     if (!on) return;
     float2 c1[BWD ? P : 1], c2[BWD ? P : 1], rstd[BWD ? P : 1];
@@ -538,9 +542,8 @@ cudaError_t launch_act(const SeqGnormParams& p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     const long long groups = (long long)p.ax.S * p.G, slabs = p.ax.T / p.ax.S / p.slab + 1;
     const int own = s.tx * V / (p.D / p.G);           // groups of a block
-    // few entries: every block joins its groups' itself, one launch less.  (Unequal lengths with
-    // statistics wanted go the other way: empty sequences have statistics too.)
-    const bool self = s.grouped && own <= s.tx * s.ty && own * slabs <= 16 * GT && (BWD || !p.stats || p.ax.L > 0);
+    // few entries: every block joins its groups' itself, one launch less
+    const bool self = s.grouped && own <= s.tx * s.ty && own * slabs <= 16 * GT;
     if (!self) {
         // a warp for a few entries, a block for many
         const bool big = slabs * (s.grouped ? 1 : p.D / p.G) > 256;

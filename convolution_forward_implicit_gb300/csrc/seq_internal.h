@@ -231,12 +231,14 @@ struct SeqDeltaParams {
     long long saved_u;              // where the saved u begin, in floats: [slots][Hv][64][Dvp] behind [slots][Hv][Dk][Dvp]
     int wide;                       // q and k in whole aligned 16-byte groups
     int pairs, key_pairs;           // v, y, dy, dv; dq, dk in aligned pairs of elements
+    int val_wide, key_wide;         // v and dy; dq and dk in whole aligned 16-byte groups
     int quads;                      // step: states in whole aligned groups of 4
     int sms;
 };
 cudaError_t launch_seq_delta_fwd(const SeqDeltaParams& p, bool bf16, cudaStream_t stream);
 cudaError_t launch_seq_delta_bwd(const SeqDeltaParams& p, bool bf16, cudaStream_t stream);
 cudaError_t launch_seq_delta_walk_tc(const SeqDeltaParams& p, cudaStream_t stream);
+cudaError_t launch_seq_delta_grad_tc(const SeqDeltaParams& p, cudaStream_t stream);
 cudaError_t launch_seq_delta_back_tc(const SeqDeltaParams& p, cudaStream_t stream);
 cudaError_t launch_seq_delta_step(const SeqDeltaParams& p, bool bf16, cudaStream_t stream);
 
