@@ -12,29 +12,43 @@ namespace {
 constexpr int LSQ = 72;              // row of a 64 x 64 matrix in shared memory: conflict-free pairs along rows
 
 // (I + L)^-1 for the strictly lower triangular L in shared memory (rows of LSQ; the rest of it zero), to `inv` (all of it).
-// Diagonal blocks of 16 by forward substitution, a thread a column; then [[P, 0], [B, Q]]^-1 = [[P', 0], [-Q' B P', Q']]
-// for blocks of 16 and 32.  No powers of L: they cancel badly where keys are alike.
+// Diagonal blocks of 8 by forward substitution, a thread a column; then [[P, 0], [B, Q]]^-1 = [[P', 0], [-Q' B P', Q']]
+// for blocks of 8, 16 and 32.  No powers of L: they cancel badly where keys are alike.
 __device__ __forceinline__ void invert(const float* L, float* inv, float* tmp) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t2 = (lane & 3) * 2;
     for (int i = threadIdx.x; i < DC * DC / 4; i += DT) {
         const int r = i / (DC / 4), c = i % (DC / 4) * 4;
-        if (r / 16 != c / 16) *reinterpret_cast<float4*>(inv + r * LSQ + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r / 8 != c / 8) *reinterpret_cast<float4*>(inv + r * LSQ + c) = make_float4(0.f, 0.f, 0.f, 0.f);
     }
     if (threadIdx.x < DC) {
-        const int o = threadIdx.x / 16 * 16, c = threadIdx.x % 16;
-        float x[16];
+        const int o = threadIdx.x / 8 * 8, c = threadIdx.x % 8;
+        float x[8];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
+        for (int i = 0; i < 8; ++i) {
+            const float4 l0 = *reinterpret_cast<const float4*>(L + (o + i) * LSQ + o), l1 = *reinterpret_cast<const float4*>(L + (o + i) * LSQ + o + 4);
+            const float l[8] = {l0.x, l0.y, l0.z, l0.w, l1.x, l1.y, l1.z, l1.w};
             float s0 = i == c ? 1.f : 0.f, s1 = 0.f;
 #pragma unroll
             for (int j = 0; j < i; ++j) {
-                const float l = L[(o + i) * LSQ + o + j];
-                if (j & 1) s1 = fmaf(-l, x[j], s1);
-                else s0 = fmaf(-l, x[j], s0);
+                if (j & 1) s1 = fmaf(-l[j], x[j], s1);
+                else s0 = fmaf(-l[j], x[j], s0);
             }
             x[i] = s0 + s1;
             inv[(o + i) * LSQ + o + c] = x[i];
         }
+    }
+    __syncthreads();
+    {                                // blocks of 8: rows o + 8, columns o; a thread an element
+        const int o = threadIdx.x / 64 * 16, r = o + 8 + threadIdx.x % 64 / 8, c = o + threadIdx.x % 8;
+        float v = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v = fmaf(L[r * LSQ + o + k], inv[(o + k) * LSQ + c], v);
+        tmp[r * LSQ + c] = v;
+        __syncthreads();
+        v = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v = fmaf(inv[r * LSQ + o + 8 + k], tmp[(o + 8 + k) * LSQ + c], v);
+        inv[r * LSQ + c] = -v;
     }
     __syncthreads();
     if (warp < 4) {                  // blocks of 16: rows o + 16, columns o; a warp 8 columns
@@ -71,13 +85,16 @@ __device__ __forceinline__ void invert(const float* L, float* inv, float* tmp) {
     __syncthreads();
 }
 
+constexpr int CHUNK_HEADS = 4;       // value heads whose decay is prepared at once
+
 template <typename T, int KP>
 struct ChunkSmem {
     static constexpr int LD = KP + 8;
     T q[DC * LD], k[DC * LD];
     float L[DC * LSQ], inv[DC * LSQ], tmp[DC * LSQ], a[DC * LSQ];
-    float2 b[DC];
-    float rq[DC], rk[DC], beta[DC];
+    float2 b[CHUNK_HEADS][DC];
+    float rq[DC], rk[DC], beta[CHUNK_HEADS][DC];
+    float before[4][DC];             // exp(b_16r - b_j), j < 16 r: decay from a token to the first row of a tile
 };
 
 template <typename T, int KP>
@@ -108,38 +125,55 @@ __global__ void __launch_bounds__(DT) delta_chunk_kernel(const __grid_constant__
     for (int h = kh * rep; h < (kh + 1) * rep; ++h) {
         __syncthreads();             // (the lengths are there; the last head's matrices are read)
         float* tri = p.tri + ((long long)blockIdx.x * p.Hv + h) * (p.planes ? DELTA_PLANES / 4 : 2 * DC * DC);
-        if (warp == 0) {
-            float2 b[2];
-            chunk_decay(p.g + cut.t0 * p.g_ld + h, p.g_ld, cut.n, b);
-            float* rows = p.rows + ((long long)blockIdx.x * p.Hv + h) * DELTA_ROWS;
-            const float2 end = make_float2(__shfl_sync(0xffffffffu, b[1].x, 31), __shfl_sync(0xffffffffu, b[1].y, 31));
+        const int hs = (h - kh * rep) % CHUNK_HEADS;
+        if (hs == 0) {               // the next heads' decay, a warp each
+            const int hw = h + warp;
+            if (warp < CHUNK_HEADS && hw < (kh + 1) * rep) {
+                float2 b[2];
+                chunk_decay(p.g + cut.t0 * p.g_ld + hw, p.g_ld, cut.n, b);
+                float* rows = p.rows + ((long long)blockIdx.x * p.Hv + hw) * DELTA_ROWS;
+                const float2 end = make_float2(__shfl_sync(0xffffffffu, b[1].x, 31), __shfl_sync(0xffffffffu, b[1].y, 31));
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int r = 2 * lane + i;
-                const float beta = r < cut.n ? p.beta[(cut.t0 + r) * p.beta_ld + h] : 0.f;
-                const float e = expf(b[i].x) * (1.f + b[i].y);
-                s.b[r] = b[i];
-                s.beta[r] = beta;
-                rows[RF_IN + r] = beta * e * s.rk[r];
-                rows[RF_OUT + r] = p.scale * e * s.rq[r];
-                rows[RF_END + r] = decay_between(end, b[i]) * s.rk[r];
-                rows[RF_BETA + r] = beta;
+                for (int i = 0; i < 2; ++i) {
+                    const int r = 2 * lane + i;
+                    const float beta = r < cut.n ? p.beta[(cut.t0 + r) * p.beta_ld + hw] : 0.f;
+                    const float e = expf(b[i].x) * (1.f + b[i].y);
+                    s.b[warp][r] = b[i];
+                    s.beta[warp][r] = beta;
+                    rows[RF_IN + r] = beta * e * s.rk[r];
+                    rows[RF_OUT + r] = p.scale * e * s.rq[r];
+                    rows[RF_END + r] = decay_between(end, b[i]) * s.rk[r];
+                    rows[RF_BETA + r] = beta;
+                }
+                if (lane == 0) rows[RF_DECAY] = expf(end.x) * (1.f + end.y);
             }
-            if (lane == 0) rows[RF_DECAY] = expf(end.x) * (1.f + end.y);
+            __syncthreads();
+        }
+        {                            // (with the column's length: every use has both)
+            const int r = threadIdx.x >> 6, j = threadIdx.x & 63;
+            s.before[r][j] = j < 16 * r ? decay_between(s.b[hs][16 * r], s.b[hs][j]) * s.rk[j] : 0.f;
         }
         __syncthreads();
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             const int i = m0 + g + 8 * half;
-            const float2 bi = s.b[i];
-            const float f = warp < 4 ? s.beta[i] * s.rk[i] : p.scale * s.rq[i];
+            const float2 bi = s.b[hs][i];
+            const float f = warp < 4 ? s.beta[hs][i] * s.rk[i] : p.scale * s.rq[i];
+            const float lead = f * decay_between(bi, s.b[hs][m0]);       // from the tile's first row
+            const float* before = s.before[m0 >> 4];
 #pragma unroll
             for (int n = 0; n < 8; ++n) {
-                float v[2];
+                float v[2] = {0.f, 0.f};
+                if (8 * n < m0) {    // to the left of the diagonal tile: both factors are at most 1
+                    const float2 e = *reinterpret_cast<const float2*>(before + 8 * n + t2);
+                    v[0] = acc[n][2 * half] * lead * e.x;
+                    v[1] = acc[n][2 * half + 1] * lead * e.y;
+                } else if (8 * n < m0 + 16) {
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int j = 8 * n + t2 + e;
-                    v[e] = j < i || (j == i && warp >= 4) ? acc[n][2 * half + e] * f * s.rk[j] * decay_between(bi, s.b[j]) : 0.f;
+                    for (int e = 0; e < 2; ++e) {
+                        const int j = 8 * n + t2 + e;
+                        if (j < i || (j == i && warp >= 4)) v[e] = acc[n][2 * half + e] * f * s.rk[j] * decay_between(bi, s.b[hs][j]);
+                    }
                 }
                 float* to = warp < 4 ? s.L + i * LSQ : p.planes ? s.a + i * LSQ : tri + DC * DC + i * DC;
                 *reinterpret_cast<float2*>(to + 8 * n + t2) = make_float2(v[0], v[1]);

@@ -16,8 +16,7 @@
 namespace convfwd {
 namespace {
 
-constexpr int GT_WARPS = 8, GT_THREADS = 32 * (GT_WARPS + 1);        // the last warp issues
-constexpr int GW = 32 * GT_WARPS;
+constexpr int GT_WARPS = 16, GW = 32 * GT_WARPS;      // four warps a quarter of the lanes; the first also issues
 
 template <int KP>
 struct GradTc {
@@ -25,13 +24,13 @@ struct GradTc {
     static constexpr uint32_t A = KQ, U = A + 3 * ATOM, H = U + 3 * 8192, DH = H + 3 * ATOM;
     static constexpr uint32_t M0 = H, M1 = DH, M3 = DH + 3 * 8192;    // the chunk's matrices, where the states were
     static constexpr uint32_t REST = DH + 3 * ATOM;
-    static constexpr uint32_t BYTES = REST + 6144 + 1024;
+    static constexpr uint32_t BYTES = REST + 8192 + 1024;
     static constexpr uint32_t D1 = 0, D3 = 128, D4 = 256, D5 = 384, D2 = 384;      // TMEM columns
 };
 struct GradRest {
     float2 b[DC];
     float rq[DC], rk[DC], beta[DC], vdr[DC], dotq[DC], dotk[DC];
-    float dots[4][2][DC];
+    float dots[4][4][DC];
     float hh[GT_WARPS];
     int zero[GT_WARPS];
     alignas(8) uint64_t bars[4];
@@ -92,17 +91,17 @@ __device__ __forceinline__ int part_a(int q) { return 0x052 >> 2 * q & 3; }
 __device__ __forceinline__ int part_b(int q) { return 0x118 >> 2 * q & 3; }
 
 template <int KP, bool SHARED>
-__global__ void __launch_bounds__(GT_THREADS, 1) delta_grad_tc_kernel(const __grid_constant__ SeqDeltaParams p, unsigned* err) {
+__global__ void __launch_bounds__(GW, 1) delta_grad_tc_kernel(const __grid_constant__ SeqDeltaParams p, unsigned* err) {
     extern __shared__ uint8_t smem_raw[];
     using G = GradTc<KP>;
     using T = __nv_bfloat16;
-    constexpr int HC = KP / 2;                   // columns of a row that a thread holds of a result
+    constexpr int HC = KP / 4;                   // columns of a row that a thread holds of a result
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     uint8_t* sm = smem_raw + (base - smem_u32(smem_raw));
     GradRest& s = *reinterpret_cast<GradRest*>(sm + G::REST);
     const CutPiece cut = cut_piece(p.ax, blockIdx.x, DC);
     if (cut.n <= 0) return;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wq = warp & 3, hf = warp >> 2;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wq = warp & 3, cq = warp >> 2;
     const int kh = blockIdx.y, rep = SHARED ? p.Hv / p.Hk : 1, blocks = (p.Dv + 63) / 64;
     const uint32_t ready = smem_u32(&s.bars[0]), bar_h = smem_u32(&s.bars[1]), bar_e = smem_u32(&s.bars[2]);
     volatile int* abort_flag = &s.abort;
@@ -117,7 +116,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1) delta_grad_tc_kernel(const __gr
         tmem_alloc(smem_u32(&s.slot), 512);
         tmem_relinquish();
     }
-    if (warp < GT_WARPS) {
+    {
         load_kq<KP, GW>(base, static_cast<const T*>(p.k) + cut.t0 * p.k_ld + kh * p.Dk, static_cast<const T*>(p.q) + cut.t0 * p.q_ld + kh * p.Dk, p.k_ld,
                         p.q_ld, cut.n, p.Dk, threadIdx.x);
         cp_async_commit();
@@ -133,49 +132,44 @@ __global__ void __launch_bounds__(GT_THREADS, 1) delta_grad_tc_kernel(const __gr
     const uint32_t tmem = s.slot, lanes = tmem + ((uint32_t)(wq * 32) << 16);
     constexpr uint32_t B_ACROSS = 1u << 16, A_ACROSS = 1u << 15, ID_KP = idesc_f32acc(128, KP, 1u), ID_64 = idesc_f32acc(128, 64, 1u);
     // After a wait has run out every later one ends at once (see wait_turn); the warps go on together to the end.
-    if (warp == GT_WARPS) {                      // ---- the issuing warp
+    {
+        // what the first warp issues once all have told: D2 and D1 of a block, its D3, or D4 and D5
+        enum Part { ROWS, STATES, MATRICES };
         uint32_t turn = 0;
-        auto next = [&]() {
+        auto issue = [&](Part part, bool first) {
+            if (warp != 0) return;
             const bool ok = wait_turn(ready, turn, abort_flag, err);
             turn ^= 1;
             tc_fence_after();
-            return ok && lane == 0;
-        };
-        for (int h = 0; h < rep; ++h) {
-            for (int v = 0; v < blocks; ++v) {
-                if (next()) {
+            if (ok && lane == 0) {
+                if (part == ROWS) {
 #pragma unroll 1
                     for (int q = 0; q < 6; ++q)
-                        mma_ss_k4(tmem + G::D2, sw128_desc(base + G::A + part_a(q) * ATOM), sw128_desc(base + G::U + part_b(q) * 8192), ID_64, v > 0 || q > 0, 32, 32);
+                        mma_ss_k4(tmem + G::D2, sw128_desc(base + G::A + part_a(q) * ATOM), sw128_desc(base + G::U + part_b(q) * 8192), ID_64, !first || q > 0, 32, 32);
 #pragma unroll 1
                     for (int q = 0; q < 6; ++q)
-                        mma_ss_k4(tmem + G::D1, sw128_desc(base + G::A + part_a(q) * ATOM), sw128_desc(base + G::H + part_b(q) * ATOM), ID_KP, v > 0 || q > 0, 32, 32);
+                        mma_ss_k4(tmem + G::D1, sw128_desc(base + G::A + part_a(q) * ATOM), sw128_desc(base + G::H + part_b(q) * ATOM), ID_KP, !first || q > 0, 32, 32);
                     mma_commit(bar_h);
-                }
-                __syncwarp();
-                if (next()) {
+                } else if (part == STATES) {
 #pragma unroll 1
                     for (int q = 0; q < 6; ++q)      // (U's rows are the second 64: the first are whatever lies before it)
                         mma_ss_k4(tmem + G::D3, sw128_desc(base + G::U + part_a(q) * 8192 - 8192), sw128_desc(base + G::DH + part_b(q) * ATOM), ID_KP,
-                                  v > 0 || q > 0, 32, 32);
+                                  !first || q > 0, 32, 32);
+                    mma_commit(bar_e);
+                } else {
+#pragma unroll 1
+                    for (int pl = 2; pl >= 0; --pl)
+                        mma_ss_k4(tmem + G::D4, sw128_desc(base + G::M0 + pl * ATOM), mn_desc(base, ATOM), ID_KP | B_ACROSS, pl < 2, 32, 2048);
+#pragma unroll 1
+                    for (int pl = 2; pl >= 0; --pl) {    // (blocks of rows 8 KB apart, the matrix the second)
+                        mma_ss_k4(tmem + G::D5, mn_desc(base + G::M1 + pl * 8192 - 8192, 8192), mn_desc(base + 8192, ATOM), ID_KP | A_ACROSS | B_ACROSS, pl < 2, 2048, 2048);
+                        mma_ss_k4(tmem + G::D5, mn_desc(base + G::M3 + pl * 8192 - 8192, 8192), mn_desc(base, ATOM), ID_KP | A_ACROSS | B_ACROSS, true, 2048, 2048);
+                    }
                     mma_commit(bar_e);
                 }
-                __syncwarp();
-            }
-            if (next()) {
-#pragma unroll 1
-                for (int pl = 2; pl >= 0; --pl)
-                    mma_ss_k4(tmem + G::D4, sw128_desc(base + G::M0 + pl * ATOM), mn_desc(base, ATOM), ID_KP | B_ACROSS, pl < 2, 32, 2048);
-#pragma unroll 1
-                for (int pl = 2; pl >= 0; --pl) {    // (blocks of rows 8 KB apart, the matrix the second)
-                    mma_ss_k4(tmem + G::D5, mn_desc(base + G::M1 + pl * 8192 - 8192, 8192), mn_desc(base + 8192, ATOM), ID_KP | A_ACROSS | B_ACROSS, pl < 2, 2048, 2048);
-                    mma_ss_k4(tmem + G::D5, mn_desc(base + G::M3 + pl * 8192 - 8192, 8192), mn_desc(base, ATOM), ID_KP | A_ACROSS | B_ACROSS, true, 2048, 2048);
-                }
-                mma_commit(bar_e);
             }
             __syncwarp();
-        }
-    } else {                                     // ---- the rows' warps
+        };
         uint32_t turn_h = 0, turn_e = 0;
         auto wait_h = [&]() {
             wait_turn(bar_h, turn_h, abort_flag, err);
@@ -199,10 +193,10 @@ __global__ void __launch_bounds__(GT_THREADS, 1) delta_grad_tc_kernel(const __gr
             return *reinterpret_cast<const uint4*>(sm + (c >> 3) * ATOM + row * 128 + ((c & 7) ^ (row & 7)) * 16);
         };
         {
-            const int row = threadIdx.x >> 1;
+            const int row = threadIdx.x >> 2;
             float sum = 0.f;
-#pragma unroll 4
-            for (int c = threadIdx.x & 1; c < KP / 8; c += 2) {
+#pragma unroll
+            for (int c = threadIdx.x & 3; c < KP / 8; c += 4) {
                 const uint4 w = piece(row, c);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -212,24 +206,25 @@ __global__ void __launch_bounds__(GT_THREADS, 1) delta_grad_tc_kernel(const __gr
                 }
             }
             sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-            if ((threadIdx.x & 1) == 0) (row < 64 ? s.rk : s.rq)[row & 63] = p.norm ? 1.f / sqrtf(sum + QK_EPS) : 1.f;
+            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+            if ((threadIdx.x & 3) == 0) (row < 64 ? s.rk : s.rq)[row & 63] = p.norm ? 1.f / sqrtf(sum + QK_EPS) : 1.f;
         }
         float total[SHARED ? HC : 1];
 #pragma unroll
         for (int c = 0; c < (SHARED ? HC : 1); ++c) total[c] = 0.f;
         dep_wait();
-        // A thread's pieces of 8 columns: rows r8, r8 + 32, ...  What a block needs is on its way while the one before is worked
+        // A thread's pieces of 8 columns: row r8 of the tokens, rows r8 and r8 + 64 of the states.  What a block needs is on its way while the one before is worked
         // on, in registers: with loads where they are used the kernel took 794 us instead of @@ (8192 tokens, 32 heads).
         const int r8 = threadIdx.x >> 3, c8 = threadIdx.x & 7;
         const uint32_t place = (uint32_t)(r8 * 128 + (c8 ^ (r8 & 7)) * 16);
-        float h0[KP / 32][8], u[2][8], dr[2][8];
-        uint4 dy[2], vv[2];
-        auto states = [&](const float* from, int h, int v, float (&x)[KP / 32][8]) {
+        float h0[KP / 64][8], u[8], dr[8];
+        uint4 dy, vv;
+        auto states = [&](const float* from, int h, int v, float (&x)[KP / 64][8]) {
             const long long at = (long long)blockIdx.x * p.Hv + h;
             const int col = v * 64 + c8 * 8;
 #pragma unroll
-            for (int j = 0; j < KP / 32; ++j) {
-                const int r = r8 + 32 * j;
+            for (int j = 0; j < KP / 64; ++j) {
+                const int r = r8 + 64 * j;
                 floats8(from + (at * p.Dk + r) * p.Dvp + col, col < p.Dvp && r < p.Dk, col + 4 < p.Dvp && r < p.Dk, x[j]);
             }
         };
@@ -237,63 +232,55 @@ __global__ void __launch_bounds__(GT_THREADS, 1) delta_grad_tc_kernel(const __gr
             const long long at = (long long)blockIdx.x * p.Hv + h;
             const int col = v * 64 + c8 * 8;
             const bool first = col < p.Dvp, second = col + 4 < p.Dvp;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int r = r8 + 32 * j;
-                floats8(p.saved + p.saved_u + (at * DC + r) * p.Dvp + col, first, second, u[j]);
-                floats8(p.dr + (at * DC + r) * p.Dvp + col, first, second, dr[j]);
-                dy[j] = row8(static_cast<const T*>(p.dy) + (cut.t0 + r) * p.dy_ld + h * p.Dv + col, col, p.Dv, r < cut.n, p.val_wide);
-                vv[j] = row8(static_cast<const T*>(p.v) + (cut.t0 + r) * p.v_ld + h * p.Dv + col, col, p.Dv, r < cut.n, p.val_wide);
-            }
+            floats8(p.saved + p.saved_u + (at * DC + r8) * p.Dvp + col, first, second, u);
+            floats8(p.dr + (at * DC + r8) * p.Dvp + col, first, second, dr);
+            dy = row8(static_cast<const T*>(p.dy) + (cut.t0 + r8) * p.dy_ld + h * p.Dv + col, col, p.Dv, r8 < cut.n, p.val_wide);
+            vv = row8(static_cast<const T*>(p.v) + (cut.t0 + r8) * p.v_ld + h * p.Dv + col, col, p.Dv, r8 < cut.n, p.val_wide);
         };
         states(p.saved, kh * rep, 0, h0);
         tokens(kh * rep, 0);
         for (int h = kh * rep; h < (kh + 1) * rep; ++h) {
-            float vdr[2] = {0.f, 0.f}, hh = 0.f;
+            float vdr = 0.f, hh = 0.f;
             bool from_zero = true;               // the state before the chunk is zero
             for (int v = 0; v < blocks; ++v) {
                 const bool more = v + 1 < blocks || h + 1 < (kh + 1) * rep;
                 const int h_next = v + 1 < blocks ? h : h + 1, v_next = v + 1 < blocks ? v + 1 : 0;
                 if (v > 0) wait_h();                 // the block before has read its h0
 #pragma unroll
-                for (int j = 0; j < KP / 32; ++j) {
+                for (int j = 0; j < KP / 64; ++j) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) from_zero = from_zero && h0[j][e] == 0.f;
-                    split8(sm + G::H + place + j * 4096, ATOM, h0[j]);
+                    split8(sm + G::H + place + j * 8192, ATOM, h0[j]);
                 }
-                float dh[KP / 32][8];
+                float dh[KP / 64][8];
                 states(p.dstate, h, v, dh);
                 if (v > 0) wait_e();                 // and all else
+                split8(sm + G::U + place, 8192, u);
+                split8(sm + G::A + 8192 + place, ATOM, dr);
+                *reinterpret_cast<uint4*>(sm + G::A + place) = dy;
+                const uint32_t w[4] = {vv.x, vv.y, vv.z, vv.w};
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    split8(sm + G::U + place + j * 4096, 8192, u[j]);
-                    split8(sm + G::A + 8192 + place + j * 4096, ATOM, dr[j]);
-                    *reinterpret_cast<uint4*>(sm + G::A + place + j * 4096) = dy[j];
-                    const uint32_t w[4] = {vv[j].x, vv[j].y, vv[j].z, vv[j].w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float a, b;
-                        bf2_unpack(w[e], a, b);
-                        vdr[j] = fmaf(a, dr[j][2 * e], fmaf(b, dr[j][2 * e + 1], vdr[j]));
-                    }
+                for (int e = 0; e < 4; ++e) {
+                    float a, b;
+                    bf2_unpack(w[e], a, b);
+                    vdr = fmaf(a, dr[2 * e], fmaf(b, dr[2 * e + 1], vdr));
                 }
                 tell();
                 if (more) tokens(h_next, v_next);
+                issue(ROWS, v == 0);
 #pragma unroll
-                for (int j = 0; j < KP / 32; ++j) {
+                for (int j = 0; j < KP / 64; ++j) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) hh = fmaf(h0[j][e], dh[j][e], hh);
-                    split8(sm + G::DH + place + j * 4096, ATOM, dh[j]);
+                    split8(sm + G::DH + place + j * 8192, ATOM, dh[j]);
                 }
                 tell();
                 if (more) states(p.saved, h_next, v_next, h0);
+                issue(STATES, v == 0);
             }
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-#pragma unroll
-                for (int d = 1; d < 8; d <<= 1) vdr[j] += __shfl_xor_sync(0xffffffffu, vdr[j], d);
-                if (c8 == 0) s.vdr[r8 + 32 * j] = vdr[j];
-            }
+            for (int d = 1; d < 8; d <<= 1) vdr += __shfl_xor_sync(0xffffffffu, vdr, d);
+            if (c8 == 0) s.vdr[r8] = vdr;
 #pragma unroll
             for (int d = 16; d > 0; d >>= 1) hh += __shfl_xor_sync(0xffffffffu, hh, d);
             from_zero = __all_sync(0xffffffffu, from_zero);
@@ -301,7 +288,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1) delta_grad_tc_kernel(const __gr
                 s.hh[warp] = hh;
                 s.zero[warp] = from_zero;
             }
-            if (warp == 0) {
+            if (warp == GT_WARPS - 1) {          // (the first may still be issuing)
                 float2 b[2];
                 chunk_decay(p.g + cut.t0 * p.g_ld + h, p.g_ld, cut.n, b);
 #pragma unroll
@@ -316,11 +303,10 @@ __global__ void __launch_bounds__(GT_THREADS, 1) delta_grad_tc_kernel(const __gr
             const float rqi = s.rq[i], rki = s.rk[i], beta = s.beta[i];
             wait_h();
             wait_e();
-            // ---- the chunk's matrices from D2: 32 columns of the lane's row
-#pragma unroll
-            for (int c = 0; c < 32; c += 16) {
+            // ---- the chunk's matrices from D2: 16 columns of the lane's row
+            {
                 uint32_t d[16];
-                tmem_ld16(lanes + G::D2 + hf * 32 + c, d);
+                tmem_ld16(lanes + G::D2 + cq * 16, d);
                 tmem_ld_wait();
                 const float f = isk ? -1.f : p.scale, own = isk ? beta * rki : rqi;
 #pragma unroll
@@ -328,17 +314,18 @@ __global__ void __launch_bounds__(GT_THREADS, 1) delta_grad_tc_kernel(const __gr
                     float by_key[8], by_row[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        const int j = hf * 32 + c + half * 8 + e;
+                        const int j = cq * 16 + half * 8 + e;
                         const float x = j < i || (j == i && !isk) ? f * __uint_as_float(d[half * 8 + e]) * decay_between(bi, s.b[j]) : 0.f;
                         by_key[e] = x * s.rk[j];
                         by_row[e] = x * own;
                     }
-                    const int chunk = hf * 4 + c / 8 + half;
+                    const int chunk = cq * 2 + half;
                     split8(sm + G::M0 + (isk * 64 + i) * 128 + ((chunk ^ (i & 7)) * 16), ATOM, by_key);
                     split8(sm + (isk ? G::M3 : G::M1) + i * 128 + ((chunk ^ (i & 7)) * 16), 8192, by_row);
                 }
             }
             tell();
+            issue(MATRICES, true);
             const float eb = expf(bi.x) * (1.f + bi.y), fq = p.scale * eb, fz = decay_between(end, bi);
             wait_e();
             // ---- rows: dQ (first 64 lanes), X and Z (the others), in pieces of 16 columns
@@ -346,7 +333,7 @@ __global__ void __launch_bounds__(GT_THREADS, 1) delta_grad_tc_kernel(const __gr
             float out[SHARED ? 1 : HC];
 #pragma unroll
             for (int c = 0; c < HC; c += 16) {
-                const int col = hf * HC + c;
+                const int col = cq * HC + c;
                 uint32_t d1[16], d4[16], d3[16], d5[16];
                 tmem_ld16(lanes + G::D1 + col, d1);
                 tmem_ld16(lanes + G::D4 + col, d4);
@@ -378,22 +365,23 @@ __global__ void __launch_bounds__(GT_THREADS, 1) delta_grad_tc_kernel(const __gr
                 }
             }
             if (!isk) {
-                s.dots[0][hf][i] = (dot[0][0] + dot[0][1]) + (dot[0][2] + dot[0][3]);
+                s.dots[0][cq][i] = (dot[0][0] + dot[0][1]) + (dot[0][2] + dot[0][3]);
             } else {
 #pragma unroll
-                for (int k = 0; k < 3; ++k) s.dots[1 + k][hf][i] = (dot[k][0] + dot[k][1]) + (dot[k][2] + dot[k][3]);
+                for (int k = 0; k < 3; ++k) s.dots[1 + k][cq][i] = (dot[k][0] + dot[k][1]) + (dot[k][2] + dot[k][3]);
             }
             meet();
             if (warp == 0) {                     // dbeta and dg, two tokens a lane
+                auto of = [&](int k, int r) { return (s.dots[k][0][r] + s.dots[k][1][r]) + (s.dots[k][2][r] + s.dots[k][3][r]); };
                 float all = 0.f, sum3 = 0.f;
                 double db[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int r = 2 * lane + e;
                     const float rq = s.rq[r], rk = s.rk[r], be = s.beta[r];
-                    const float qq = rq * (s.dots[0][0][r] + s.dots[0][1][r]), kx = rk * (s.dots[1][0][r] + s.dots[1][1][r]);
-                    const float kz = rk * (s.dots[2][0][r] + s.dots[2][1][r]);
-                    sum3 += rk * (s.dots[3][0][r] + s.dots[3][1][r]);
+                    const float qq = rq * (of(0, r)), kx = rk * (of(1, r));
+                    const float kz = rk * (of(2, r));
+                    sum3 += rk * (of(3, r));
                     db[e] = (double)(qq - kz) + (double)(be * kx);
                     if (r < cut.n) p.dbeta[(cut.t0 + r) * p.dbeta_ld + h] = s.vdr[r] + kx;
                     s.dotq[r] += qq;
@@ -431,30 +419,42 @@ __global__ void __launch_bounds__(GT_THREADS, 1) delta_grad_tc_kernel(const __gr
             }
             if (!SHARED || h == (kh + 1) * rep - 1) {
                 meet();
-                // through the lengths: d(k / |k|) = (d - k^ (k^.d)) / |k|
-                if (i < cut.n) {
+                // through the lengths: d(k / |k|) = (d - k^ (k^.d)) / |k|; through shared memory, for whole rows: written by
+                // the lanes that hold them, 4 KB apart, they took 180 us of the call's 1390 (8192 tokens, 32 heads)
+                {
                     const float r = isk ? rki : rqi, f = p.norm ? (isk ? s.dotk[i] : s.dotq[i]) * r : 0.f;
-                    T* to = isk ? static_cast<T*>(p.dk) + (cut.t0 + i) * p.dk_ld + kh * p.Dk : static_cast<T*>(p.dq) + (cut.t0 + i) * p.dq_ld + kh * p.Dk;
                     const int row = isk ? i : 64 + i;
 #pragma unroll
                     for (int c = 0; c < HC; c += 8) {
-                        const int col = hf * HC + c;
+                        const int col = cq * HC + c;
                         const uint4 q = piece(row, col / 8);
                         const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-                        float x[8];
+                        uint32_t o[4];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
+                        for (int e = 0; e < 4; ++e) {
                             float lo, hi;
-                            bf2_unpack(w[e / 2], lo, hi);
-                            x[e] = r * ((SHARED ? total[SHARED ? c + e : 0] : out[SHARED ? 0 : c + e]) - (e & 1 ? hi : lo) * f);
+                            bf2_unpack(w[e], lo, hi);
+                            const float v0 = SHARED ? total[SHARED ? c + 2 * e : 0] : out[SHARED ? 0 : c + 2 * e];
+                            const float v1 = SHARED ? total[SHARED ? c + 2 * e + 1 : 0] : out[SHARED ? 0 : c + 2 * e + 1];
+                            o[e] = bf2_pack(r * (v0 - lo * f), r * (v1 - hi * f));
                         }
-                        if (p.key_wide) {
-                            if (col < p.Dk) seq_stv<8>(to + col, x);
-                        } else {
+                        // (16-byte pieces of a row turned by its number, so that neither side's accesses meet in a bank)
+                        *reinterpret_cast<uint4*>(sm + G::H + (row * (KP / 8) + ((col / 8) ^ (row & 7))) * 16) = make_uint4(o[0], o[1], o[2], o[3]);
+                    }
+                }
+                meet();
+                for (int j = threadIdx.x; j < 128 * (KP / 8); j += GW) {
+                    const int row = j / (KP / 8), c = j % (KP / 8) * 8, t = row & 63;
+                    if (t >= cut.n || c >= p.Dk) continue;
+                    const uint4 q = *reinterpret_cast<const uint4*>(sm + G::H + (row * (KP / 8) + ((c / 8) ^ (row & 7))) * 16);
+                    T* to = (row < 64 ? static_cast<T*>(p.dk) + (cut.t0 + t) * p.dk_ld : static_cast<T*>(p.dq) + (cut.t0 + t) * p.dq_ld) + kh * p.Dk + c;
+                    if (p.key_wide) {
+                        *reinterpret_cast<uint4*>(to) = q;
+                    } else {
+                        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                if (col + e < p.Dk) to[col + e] = __float2bfloat16_rn(x[e]);
-                        }
+                        for (int e = 0; e < 8; ++e)
+                            if (c + e < p.Dk) reinterpret_cast<uint16_t*>(to)[e] = (uint16_t)(w[e / 2] >> (e % 2 * 16));
                     }
                 }
             }
@@ -479,13 +479,13 @@ cudaError_t launch_of(const SeqDeltaParams& p, unsigned* err, cudaStream_t strea
     const auto kernel = delta_grad_tc_kernel<KP, SHARED>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)GradTc<KP>::BYTES);
     if (e != cudaSuccess) return e;
-    return launch_kernel(kernel, dim3((unsigned)p.slots, (unsigned)p.Hk), dim3(GT_THREADS), GradTc<KP>::BYTES, stream, true, 1, p, err);
+    return launch_kernel(kernel, dim3((unsigned)p.slots, (unsigned)p.Hk), dim3(GW), GradTc<KP>::BYTES, stream, true, 1, p, err);
 }
 
 }  // namespace
 
 cudaError_t launch_seq_delta_grad_tc(const SeqDeltaParams& p, cudaStream_t stream) {
-    static_assert(sizeof(GradRest) <= 6144, "room behind the operands");
+    static_assert(sizeof(GradRest) <= 8192, "room behind the operands");
     unsigned* err = device_error_word();
     if (!err) return cudaErrorUnknown;
     const bool shared = p.Hv > p.Hk;
