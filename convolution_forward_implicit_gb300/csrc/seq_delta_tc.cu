@@ -206,14 +206,24 @@ struct Walk {
         // after a wait ran out: what was copied to shared memory is waited for (bounded as well)
         if (thread == 0 && *turn.abort_flag) turn.drain(chunks);
     }
-    // The thread's values of a chunk's rows of v or dY, as pairs of tokens.
+    // The thread's values of a chunk's rows of v or dY, as pairs of tokens.  Where rows lie in aligned pairs (`pairs`), an even lane
+    // reads its own and its neighbour's column of the first token of each two, an odd one those of the second, and they exchange.
     __device__ __forceinline__ void values(const void* from, long long ld, const SeqDeltaParams& p, int c, uint32_t (&v)[TPT / 2]) const {
         const int t = t0 + c * DC + tok, n = on ? min(DC, t1 - t0 - c * DC) - tok : 0;
         const uint16_t* at = static_cast<const uint16_t*>(from) + t * ld + h * p.Dv + dv;
         const uint32_t step = (uint32_t)ld;       // (64 rows lie within 2^31 bytes: see the caller)
-        if (n >= TPT) {
+        if (__all_sync(0xffffffffu, p.pairs && n >= TPT)) {
+            const uint32_t odd = lane & 1;
+            const uint16_t* row = at + odd * step - odd;
+            uint32_t w[TPT / 2];
 #pragma unroll
-            for (int i = 0; i < TPT / 2; ++i) v[i] = (uint32_t)at[2 * i * step] | (uint32_t)at[(2 * i + 1) * step] << 16;
+            for (int i = 0; i < TPT / 2; ++i) w[i] = *reinterpret_cast<const uint32_t*>(row + 2 * i * step);
+#pragma unroll
+            for (int i = 0; i < TPT / 2; ++i) {
+                const uint32_t o = __shfl_xor_sync(0xffffffffu, w[i], 1);
+                // even: the low halves (own column) of token 2i (own) and 2i + 1 (the neighbour's); odd: the high ones
+                v[i] = odd ? __byte_perm(o, w[i], 0x7632) : __byte_perm(w[i], o, 0x5410);
+            }
         } else {
 #pragma unroll
             for (int i = 0; i < TPT / 2; ++i) {
@@ -222,14 +232,19 @@ struct Walk {
             }
         }
     }
-    // 16 of the thread's values to rows first .. of a tensor whose chunk has n tokens.
+    // 16 of the thread's values to rows first .. of a tensor whose chunk has n tokens; the same exchange.
     __device__ __forceinline__ void store(void* to, long long ld, const SeqDeltaParams& p, int t, int n, int first, const float (&x)[16]) const {
         __nv_bfloat16* at = static_cast<__nv_bfloat16*>(to) + (long long)(t + first) * ld + h * p.Dv + dv;
         const uint32_t step = (uint32_t)ld;
-        if (n - first >= 16) {
+        if (__all_sync(0xffffffffu, p.pairs && on && n - first >= 16)) {
+            const uint32_t odd = lane & 1;
+            __nv_bfloat16* row = at + odd * step - odd;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) at[i * step] = __float2bfloat16_rn(x[i]);
-        } else {
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t own = pack_bf16x2(x[2 * i], x[2 * i + 1]), o = __shfl_xor_sync(0xffffffffu, own, 1);
+                *reinterpret_cast<uint32_t*>(row + 2 * i * step) = odd ? __byte_perm(o, own, 0x7632) : __byte_perm(own, o, 0x5410);
+            }
+        } else if (on) {
 #pragma unroll
             for (int i = 0; i < 16; ++i)
                 if (first + i < n) at[i * step] = __float2bfloat16_rn(x[i]);
@@ -403,14 +418,12 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) delta_walk_tc_kernel(const __
             }
             const float decay = rows[RF_DECAY];
             w.turn.tell();
-            if (w.on) {
 #pragma unroll
-                for (int j = 0; j < TPT; j += 16) {
-                    float x[16];
+            for (int j = 0; j < TPT; j += 16) {
+                float x[16];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) x[i] = y[j + i];
-                    w.store(p.y, p.y_ld, p, t, n, tok + j, x);
-                }
+                for (int i = 0; i < 16; ++i) x[i] = y[j + i];
+                w.store(p.y, p.y_ld, p, t, n, tok + j, x);
             }
             if (!w.turn.next(w.turn.mma)) break;
             w.turn.release(c);
@@ -579,7 +592,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) delta_back_tc_kernel(const __
                 read16(rows + RF_BETA + tok + j, beta);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) beta[i] *= dr[j + i];
-                if (w.on) w.store(p.dv, p.dv_ld, p, t, n, tok + j, beta);
+                w.store(p.dv, p.dv_ld, p, t, n, tok + j, beta);
             }
             if (!w.turn.next(w.turn.mma)) break;
             w.turn.release(s);

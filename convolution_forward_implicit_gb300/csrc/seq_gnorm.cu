@@ -186,13 +186,47 @@ struct Affine {
     }
 };
 
-// Rows a thread has on their way at once.
-constexpr int AHEAD = 4, AHEAD_BWD = 2;
+// Rows a thread works on at once; as many more are on their way meanwhile.
+constexpr int AHEAD = 2, AHEAD_BWD = 2;
+// Blocks of 256 threads an SM: what the registers of the rows on their way leave room for (backward in bf16, 8 channels a
+// thread, three blocks spill: 32 x 56 x 56 x 512 253 us against 191).
+constexpr int gn_blocks(bool bwd, int esize) { return bwd ? (esize == 2 ? 2 : 3) : 4; }
+
+// Calls f(row, x, dy) for the rows first, first + step, ... below n.
+template <typename T, int V, int N, bool TWO, typename F>
+__device__ __forceinline__ void each_row(const T* x, long long x_ld, const T* dy, long long dy_ld, int first, int step, int n, F f) {
+    Raw<T, V> xr[2][N], dr[2][TWO ? N : 1];
+    auto fetch = [&](int b, int t) {
+#pragma unroll
+        for (int u = 0; u < N; ++u)
+            if (t + u * step < n) {
+                xr[b][u].load(x + (t + u * step) * x_ld);
+                if (TWO) dr[b][TWO ? u : 0].load(dy + (t + u * step) * dy_ld);
+            }
+    };
+    fetch(0, first);
+    for (int t = first; t < n; t += 2 * N * step) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            const int at = t + b * N * step;
+            if (at >= n) break;
+            fetch(b ^ 1, at + N * step);
+#pragma unroll
+            for (int u = 0; u < N; ++u)
+                if (at + u * step < n) {
+                    float2 v[Raw<T, V>::P], d[Raw<T, V>::P];
+                    xr[b][u].get(v);
+                    if (TWO) dr[b][TWO ? u : 0].get(d);
+                    f(at + u * step, v, d);
+                }
+        }
+    }
+}
 
 // The sums of a slab: forward a group's (or channel's) mean and sum of squared differences, backward every
 // channel's sums of dz and dz xhat and the groups' of those times w.  Empty slabs write zeros for the channels.
 template <typename T, int V, bool BWD, int ACT>
-__global__ void __launch_bounds__(GT, BWD ? 3 : 4) gn_sums_kernel(const __grid_constant__ SeqGnormParams p, int txn, int tyn, int grouped) {
+__global__ void __launch_bounds__(GT, gn_blocks(BWD, sizeof(T))) gn_sums_kernel(const __grid_constant__ SeqGnormParams p, int txn, int tyn, int grouped) {
     constexpr int P = Raw<T, V>::P, N = BWD ? AHEAD_BWD : AHEAD;
     extern __shared__ float2 part[];                  // [tyn][txn V]
     const CutPiece cut = cut_piece(p.ax, blockIdx.x, p.slab);
@@ -216,35 +250,21 @@ __global__ void __launch_bounds__(GT, BWD ? 3 : 4) gn_sums_kernel(const __grid_c
             r.get(shift);
         }
         int n = 0;
-        for (int t = at.ty; t < cut.n; t += N * tyn) {
-            Raw<T, V> xr[N], dr[BWD ? N : 1];
+        each_row<T, V, N, BWD>(x, p.x_ld, dy, p.dy_ld, at.ty, tyn, cut.n, [&](int, float2 (&v)[P], float2 (&d)[P]) {
+            ++n;
 #pragma unroll
-            for (int u = 0; u < N; ++u)
-                if (t + u * tyn < cut.n) {
-                    xr[u].load(x + (t + u * tyn) * p.x_ld);
-                    if (BWD) dr[BWD ? u : 0].load(dy + (t + u * tyn) * p.dy_ld);
+            for (int i = 0; i < P; ++i) {
+                if (BWD) {
+                    const float2 e = add2(v[i], neg2(f.mean[i])), dz = mul2(d[i], slope_of<ACT>(fma2(e, f.a[i], f.b[i])));
+                    a[i] = add2(a[i], dz);
+                    b[i] = fma2(dz, e, b[i]);
+                } else {
+                    const float2 e = add2(v[i], neg2(shift[i]));
+                    a[i] = add2(a[i], e);
+                    b[i] = fma2(e, e, b[i]);
                 }
-#pragma unroll
-            for (int u = 0; u < N; ++u)
-                if (t + u * tyn < cut.n) {
-                    ++n;
-                    float2 v[P], d[P];
-                    xr[u].get(v);
-                    if (BWD) dr[BWD ? u : 0].get(d);
-#pragma unroll
-                    for (int i = 0; i < P; ++i) {
-                        if (BWD) {
-                            const float2 e = add2(v[i], neg2(f.mean[i])), dz = mul2(d[i], slope_of<ACT>(fma2(e, f.a[i], f.b[i])));
-                            a[i] = add2(a[i], dz);
-                            b[i] = fma2(dz, e, b[i]);
-                        } else {
-                            const float2 e = add2(v[i], neg2(shift[i]));
-                            a[i] = add2(a[i], e);
-                            b[i] = fma2(e, e, b[i]);
-                        }
-                    }
-                }
-        }
+            }
+        });
         if (BWD) {
 #pragma unroll
             for (int i = 0; i < P; ++i) b[i] = mul2(b[i], rstd[BWD ? i : 0]);
@@ -338,94 +358,106 @@ __global__ void __launch_bounds__(GT, BWD ? 3 : 4) gn_sums_kernel(const __grid_c
     }
 }
 
-// Sum over the threads of a group: the lanes of a warp, or all of a block of GT.
-template <bool BLOCK>
-__device__ __forceinline__ float2 group_sum(float2 v, float2* buf) {
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) v = add2(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, d), __shfl_xor_sync(0xffffffffu, v.y, d)));
-    if (!BLOCK) return v;
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
-    __syncthreads();
-    float2 s = buf[0];
-#pragma unroll
-    for (int i = 1; i < GT / 32; ++i) s = add2(s, buf[i]);
-    return s;
+// A sequence's groups from its slabs' entries: forward mean and rstd, backward the means of dz w and dz w xhat.
+template <bool BWD>
+__device__ __forceinline__ void join_store(const SeqGnormParams& p, long long at, float2 st) {
+    reinterpret_cast<float2*>(p.coef)[at] = st;
+    if (!BWD && p.stats) reinterpret_cast<float2*>(p.stats)[at] = st;
 }
-
-// A sequence's group from its slabs' entries, a warp (BLOCK: a block) each: forward mean and rstd, backward the means of
-// dz w and dz w xhat.  An entry of `part` is a group's (sub = 1), or a channel's (sub = channels of a group).
-template <typename T, bool BWD, bool BLOCK>
-__global__ void __launch_bounds__(GT) gn_join_kernel(const __grid_constant__ SeqGnormParams p, int grouped) {
-    __shared__ float2 buf[GT / 32];
-    launch_next();
-    const long long at = BLOCK ? blockIdx.x : (long long)blockIdx.x * (GT / 32) + (threadIdx.x >> 5);
-    if (at >= (long long)p.ax.S * p.G) return;          // (whole warps)
-    const int s = (int)(at / p.G), gi = (int)(at - (long long)s * p.G), cpg = p.D / p.G, sub = grouped ? 1 : cpg;
+// Entries of groups: a block 32 neighbouring groups of a sequence, a warp every eighth slab.  Sums of the differences d from
+// the first slab's mean and of their squares: M2 = sum (M2k + nk d^2) - (sum nk d)^2 / n; the first slab is one of the data, so
+// that this loses about as little as a thread's own sums do.
+template <bool BWD>
+__device__ __forceinline__ float2 join_finish(const SeqGnormParams& p, float2 st, float about, float count) {
+    if (BWD) return make_float2(st.x / count, st.y / count);
+    const float shift = st.x / count, var = fmaf(-shift, shift, st.y / count);
+    return make_float2(about + shift, 1.f / sqrtf((var < 0.f ? 0.f : var) + p.eps));
+}
+template <bool BWD>
+__global__ void __launch_bounds__(GT) gn_join_groups_kernel(const __grid_constant__ SeqGnormParams p, int blocks) {
+    __shared__ float2 buf[GT];
+    const int s = blockIdx.x / blocks, gi = (blockIdx.x - s * blocks) * 32 + (threadIdx.x & 31), cpg = p.D / p.G;
     const int t0 = p.ax.L > 0 ? s * p.ax.L : seq_start(p.ax, s, 0), t1 = p.ax.L > 0 ? t0 + p.ax.L : seq_start(p.ax, s + 1, t0);
     const int len = t1 - t0, slabs = (len + p.slab - 1) / p.slab;
-    const long long row = grouped ? p.G : p.D;
-    const float2* from = reinterpret_cast<const float2*>(grouped ? p.gpart : p.part) + (long long)cut_base(p.ax, s, p.slab) * row + gi * sub;
-    // a thread takes every kstep-th slab's entries c0, c0 + cstep, ...
-    const int step = BLOCK ? GT : 32, first = BLOCK ? threadIdx.x : threadIdx.x & 31;
-    const int per = sub < step ? sub : step, k0 = first / per, c0 = first - k0 * per, kstep = step / per;
-    const bool on = k0 < kstep;
-    const float each = (float)(cpg / sub), tokens = (float)p.slab * each, rest = (float)(len - (slabs - 1) * p.slab) * each;
-    const float count = (float)len * (float)cpg;
+    const float2* from = reinterpret_cast<const float2*>(p.gpart) + (long long)cut_base(p.ax, s, p.slab) * p.G + gi;
+    const float tokens = (float)p.slab * (float)cpg, rest = (float)(len - (slabs - 1) * p.slab) * (float)cpg, count = (float)len * (float)cpg;
+    launch_next();
     wait_before();
     float2 st = dup(0.f);
-    if (BWD) {
-        const T* w = grouped ? nullptr : static_cast<const T*>(p.w);
-        for (int k = k0; on && k < slabs; k += kstep)
-            for (int c = c0; c < sub; c += per) {
-                const float2 v = from[k * row + c];
-                const float wc = w ? seq_ld(w + gi * cpg + c) : 1.f;
-                st = fma2(dup(wc), v, st);
+    const float about = !BWD && gi < p.G && len > 0 ? from[0].x : 0.f;
+    if (gi < p.G)
+#pragma unroll 4
+        for (int k = threadIdx.x >> 5; k < slabs; k += GT / 32) {
+            const float2 v = from[(long long)k * p.G];
+            if (BWD) {
+                st = add2(st, v);
+            } else {
+                const float d = v.x - about, n = k == slabs - 1 ? rest : tokens;
+                st.x = fmaf(n, d, st.x);
+                st.y += fmaf(n * d, d, v.y);
             }
-        st = group_sum<BLOCK>(st, buf);
-        if (len > 0) st = make_float2(st.x / count, st.y / count);
-        if (first == 0) reinterpret_cast<float2*>(p.coef)[at] = st;
-        return;
-    }
-    // about the first entry's mean, so that small differences of large means survive
-    const float about = len > 0 ? from[0].x : 0.f;
-    float sum = 0.f;
-    for (int k = k0; on && k < slabs; k += kstep)
-        for (int c = c0; c < sub; c += per) sum = fmaf(from[k * row + c].x - about, k == slabs - 1 ? rest : tokens, sum);
-    sum = group_sum<BLOCK>(make_float2(sum, 0.f), buf).x;
-    const float shift = len > 0 ? sum / count : 0.f;
-    float m2 = 0.f;
-    for (int k = k0; on && k < slabs; k += kstep)
-        for (int c = c0; c < sub; c += per) {
-            const float2 v = from[k * row + c];
-            const float d = (v.x - about) - shift;
-            m2 += fmaf(d * d, k == slabs - 1 ? rest : tokens, v.y);
         }
-    m2 = group_sum<BLOCK>(make_float2(m2, 0.f), buf).x;
-    if (first == 0) {
-        if (len > 0) st = make_float2(about + shift, 1.f / sqrtf(m2 / count + p.eps));
-        reinterpret_cast<float2*>(p.coef)[at] = st;
-        if (p.stats) reinterpret_cast<float2*>(p.stats)[at] = st;
+    buf[threadIdx.x] = st;
+    __syncthreads();
+    if (threadIdx.x < 32 && gi < p.G) {
+#pragma unroll
+        for (int w = 1; w < GT / 32; ++w) st = add2(st, buf[w * 32 + threadIdx.x]);
+        join_store<BWD>(p, (long long)s * p.G + gi, len > 0 ? join_finish<BWD>(p, st, about, count) : dup(0.f));
+    }
+}
+// Entries of channels (groups so wide that they lie in several blocks of the sums): a block a sequence and group.
+template <typename T, bool BWD>
+__global__ void __launch_bounds__(GT) gn_join_channels_kernel(const __grid_constant__ SeqGnormParams p) {
+    __shared__ float2 buf[GT / 32];
+    const long long at = blockIdx.x;
+    const int s = (int)(at / p.G), gi = (int)(at - (long long)s * p.G), cpg = p.D / p.G;
+    const int t0 = p.ax.L > 0 ? s * p.ax.L : seq_start(p.ax, s, 0), t1 = p.ax.L > 0 ? t0 + p.ax.L : seq_start(p.ax, s + 1, t0);
+    const int len = t1 - t0, slabs = (len + p.slab - 1) / p.slab;
+    const float2* from = reinterpret_cast<const float2*>(p.part) + (long long)cut_base(p.ax, s, p.slab) * p.D + gi * cpg;
+    const T* w = BWD ? static_cast<const T*>(p.w) : nullptr;
+    const float tokens = (float)p.slab, rest = (float)(len - (slabs - 1) * p.slab), count = (float)len * (float)cpg;
+    launch_next();
+    wait_before();
+    const float about = !BWD && len > 0 ? from[0].x : 0.f;
+    float2 st = dup(0.f);
+    for (int c = threadIdx.x; c < cpg; c += GT) {
+        const float wc = w ? seq_ld(w + gi * cpg + c) : 1.f;
+#pragma unroll 4
+        for (int k = 0; k < slabs; ++k) {
+            const float2 v = from[(long long)k * p.D + c];
+            if (BWD) {
+                st = fma2(dup(wc), v, st);
+            } else {
+                const float d = v.x - about, n = k == slabs - 1 ? rest : tokens;
+                st.x = fmaf(n, d, st.x);
+                st.y += fmaf(n * d, d, v.y);
+            }
+        }
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) st = add2(st, make_float2(__shfl_xor_sync(0xffffffffu, st.x, d), __shfl_xor_sync(0xffffffffu, st.y, d)));
+    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = st;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int i = 1; i < GT / 32; ++i) st = add2(st, buf[i]);
+        join_store<BWD>(p, at, len > 0 ? join_finish<BWD>(p, st, about, count) : dup(0.f));
     }
 }
 
-// dw and db: the slabs' sums of all sequences in order.
+// dw and db: the slabs' sums of all sequences in order.  It runs beside the kernel before it in the stream, which lets it go
+// once those sums are complete.
 __global__ void __launch_bounds__(COLUMN_THREADS, 2) gn_param_kernel(const __grid_constant__ SeqGnormParams p) {
     const long long col = (long long)blockIdx.x * 32 + (threadIdx.x & 31);      // db and dw of a channel side by side
     const bool on = col < 2LL * p.D;
-    launch_next();
-    wait_before();
     const float v = column_sum(p.part + col, 2LL * p.D, p.slots, on);
     if (threadIdx.x < 32 && on) {
         float* to = col & 1 ? p.dw : p.db;
         if (to) to[col >> 1] = v;
     }
+    wait_before();                  // (so that what follows in the stream follows the kernel before, too)
 }
 
-// The groups' joined entries of a sequence (see gn_join_kernel), by every block for its own channels: `groups` of them from
-// g0 on, to `to` (shared memory; `buf`: 2 float2 a thread).  Sums of the differences d from the first slab's mean and of
-// their squares: M2 = sum (M2k + nk d^2) - (sum nk d)^2 / n; the first slab is one of the data, so that this loses about
-// as little as a thread's own sums do.
+// The same by every block for its own channels: `groups` of a sequence from g0 on, to `to` (shared memory; `buf`: a float2 a thread).
 template <bool BWD>
 __device__ __forceinline__ void join_groups(const SeqGnormParams& p, const CutPiece& cut, int g0, int groups, float2* to, float2* buf) {
     const int parts = blockDim.x / groups, gi = threadIdx.x % groups, k0 = threadIdx.x / groups, cpg = p.D / p.G;
@@ -454,13 +486,8 @@ __device__ __forceinline__ void join_groups(const SeqGnormParams& p, const CutPi
     if (threadIdx.x < groups) {
         st = buf[threadIdx.x];
         for (int k = 1; k < parts; ++k) st = add2(st, buf[k * groups + threadIdx.x]);
-        if (BWD) {
-            st = make_float2(st.x / count, st.y / count);
-        } else {
-            const float shift = st.x / count, var = fmaf(-shift, shift, st.y / count);
-            st = make_float2(about + shift, 1.f / sqrtf((var < 0.f ? 0.f : var) + p.eps));
-            if (p.stats && cut.index == 0) reinterpret_cast<float2*>(p.stats)[(long long)cut.s * p.G + g0 + threadIdx.x] = st;
-        }
+        st = join_finish<BWD>(p, st, about, count);
+        if (!BWD && p.stats && cut.index == 0) reinterpret_cast<float2*>(p.stats)[(long long)cut.s * p.G + g0 + threadIdx.x] = st;
         to[threadIdx.x] = st;
     }
     __syncthreads();
@@ -468,7 +495,7 @@ __device__ __forceinline__ void join_groups(const SeqGnormParams& p, const CutPi
 
 // y, or dx, of a slab.  SELF: the block joins its groups' entries itself.
 template <typename T, int V, bool BWD, int ACT, bool SELF>
-__global__ void __launch_bounds__(GT, BWD ? 3 : 4) gn_apply_kernel(const __grid_constant__ SeqGnormParams p, int txn, int tyn) {
+__global__ void __launch_bounds__(GT, gn_blocks(BWD, sizeof(T))) gn_apply_kernel(const __grid_constant__ SeqGnormParams p, int txn, int tyn) {
     constexpr int P = Raw<T, V>::P, N = BWD ? AHEAD_BWD : AHEAD;
     __shared__ float2 joined[SELF ? GT : 1], buf[SELF ? GT : 1];
     const CutPiece cut = cut_piece(p.ax, gridDim.x - 1 - blockIdx.x, p.slab);
@@ -478,6 +505,7 @@ __global__ void __launch_bounds__(GT, BWD ? 3 : 4) gn_apply_kernel(const __grid_
     Affine<T, V> f;
     if (on) f.params(p, at.c);
     wait_before();
+    if (BWD) launch_next();         // the parameters' sums: see gn_param_kernel
     if (SELF) {
         const int g0 = blockIdx.y * txn * V / cpg, groups = min(txn * V, p.D - blockIdx.y * txn * V) / cpg;
         if (cut.n <= 0) {           // (a first piece without tokens: an empty sequence; each has a slot of its own)
@@ -505,33 +533,19 @@ __global__ void __launch_bounds__(GT, BWD ? 3 : 4) gn_apply_kernel(const __grid_
     const T* dy = BWD ? static_cast<const T*>(p.dy) + (long long)cut.t0 * p.dy_ld + at.c : nullptr;
     T* to = static_cast<T*>(BWD ? p.dx : p.y) + (long long)cut.t0 * (BWD ? p.dx_ld : p.y_ld) + at.c;
     const long long to_ld = BWD ? p.dx_ld : p.y_ld;
-    for (int t = at.ty; t < cut.n; t += N * tyn) {
-        Raw<T, V> xr[N], dr[BWD ? N : 1];
+    each_row<T, V, N, BWD>(x, p.x_ld, dy, p.dy_ld, at.ty, tyn, cut.n, [&](int t, float2 (&v)[P], float2 (&d)[P]) {
 #pragma unroll
-        for (int u = 0; u < N; ++u)
-            if (t + u * tyn < cut.n) {
-                xr[u].load(x + (t + u * tyn) * p.x_ld);
-                if (BWD) dr[BWD ? u : 0].load(dy + (t + u * tyn) * p.dy_ld);
+        for (int i = 0; i < P; ++i) {
+            const float2 e = add2(v[i], neg2(f.mean[i])), z = fma2(e, f.a[i], f.b[i]);
+            if (BWD) {
+                const float2 r = fma2(e, c2[BWD ? i : 0], c1[BWD ? i : 0]);
+                v[i] = fma2(f.a[i], mul2(d[i], slope_of<ACT>(z)), r);
+            } else {
+                v[i] = act_of<ACT>(z);
             }
-#pragma unroll
-        for (int u = 0; u < N; ++u)
-            if (t + u * tyn < cut.n) {
-                float2 v[P], d[P];
-                xr[u].get(v);
-                if (BWD) dr[BWD ? u : 0].get(d);
-#pragma unroll
-                for (int i = 0; i < P; ++i) {
-                    const float2 e = add2(v[i], neg2(f.mean[i])), z = fma2(e, f.a[i], f.b[i]);
-                    if (BWD) {
-                        const float2 r = fma2(e, c2[BWD ? i : 0], c1[BWD ? i : 0]);
-                        v[i] = fma2(f.a[i], mul2(d[i], slope_of<ACT>(z)), r);
-                    } else {
-                        v[i] = act_of<ACT>(z);
-                    }
-                }
-                put<T, V>(to + (t + u * tyn) * to_ld, v);
-            }
-    }
+        }
+        put<T, V>(to + t * to_ld, v);
+    });
 }
 
 template <typename T, int V, bool BWD, int ACT>
@@ -545,15 +559,14 @@ cudaError_t launch_act(const SeqGnormParams& p, cudaStream_t stream) {
     // few entries: every block joins its groups' itself, one launch less
     const bool self = s.grouped && own <= s.tx * s.ty && own * slabs <= 16 * GT;
     if (!self) {
-        // a warp for a few entries, a block for many
-        const bool big = slabs * (s.grouped ? 1 : p.D / p.G) > 256;
-        const dim3 jgrid((unsigned)(big ? groups : (groups + GT / 32 - 1) / (GT / 32)));
-        e = launch_kernel(big ? gn_join_kernel<T, BWD, true> : gn_join_kernel<T, BWD, false>, jgrid, dim3(GT), 0, stream, true, 1, p, s.grouped);
+        const int each = (p.G + 31) / 32;
+        if (s.grouped) e = launch_kernel(gn_join_groups_kernel<BWD>, dim3((unsigned)(p.ax.S * (long long)each)), dim3(GT), 0, stream, true, 1, p, each);
+        else e = launch_kernel(gn_join_channels_kernel<T, BWD>, dim3((unsigned)groups), dim3(GT), 0, stream, true, 1, p);
     }
-    if (BWD && e == cudaSuccess && (p.dw || p.db))
-        e = launch_kernel(gn_param_kernel, dim3((unsigned)((2LL * p.D + 31) / 32)), dim3(COLUMN_THREADS), 0, stream, true, 1, p);
     if (e == cudaSuccess)
         e = launch_kernel(self ? gn_apply_kernel<T, V, BWD, ACT, true> : gn_apply_kernel<T, V, BWD, ACT, false>, grid, block, 0, stream, true, 1, p, s.tx, s.ty);
+    if (BWD && e == cudaSuccess && (p.dw || p.db))
+        e = launch_kernel(gn_param_kernel, dim3((unsigned)((2LL * p.D + 31) / 32)), dim3(COLUMN_THREADS), 0, stream, true, 1, p);
     return e;
 }
 template <typename T, int V, bool BWD>
@@ -571,15 +584,18 @@ cudaError_t launch(const SeqGnormParams& p, cudaStream_t stream) {
 
 }  // namespace
 
-// Tokens of a slab: one round of four blocks an SM, 4 tokens a thread at least and 64 at most.
-int seq_gnorm_slab(long long S, long long T, int D, int G, int esize, int sms) {
+// Tokens of a slab: those of one round of blocks, but 16 rows a thread while every SM has a block (a block's first loads and
+// its part of the joining cost about as much as ten), 4 rows at least and 128 at most.
+int seq_gnorm_slab(long long S, long long T, int D, int G, int esize, bool bwd, int sms) {
     const GnShape s = gn_shape(D, D / G, 16 / esize);
-    const long long L = S > 0 && T > S ? T / S : 1, want = 4LL * sms * (s.tx * s.ty <= 128 ? 2 : 1);
-    long long slabs = want / ((S < 1 ? 1 : S) * s.cblocks);          // of a sequence
-    if (slabs < 1) slabs = 1;
-    long long len = (L + slabs - 1) / slabs;
+    const long long L = S > 0 && T > S ? T / S : 1, rows = (S < 1 ? 1 : S) * s.cblocks;
+    const long long round = (long long)(esize == 4 ? 4 : gn_blocks(bwd, esize)) * GT * sms / (s.tx * s.ty);
+    auto tokens = [&](long long blocks) { return (L + (blocks < rows ? 1 : blocks / rows) - 1) / (blocks < rows ? 1 : blocks / rows); };
+    long long len = tokens(round);
+    const long long enough = 16 * s.ty < tokens(sms) ? 16 * s.ty : tokens(sms);
+    if (len < enough) len = enough;
     if (len < 4 * s.ty) len = 4 * s.ty;
-    if (len > 64 * s.ty) len = 64 * s.ty;
+    if (len > 128 * s.ty) len = 128 * s.ty;
     return (int)len;
 }
 

@@ -28,7 +28,7 @@ conv_status seq_gnorm_plan_create(seq_plan_t* out, int64_t S, int64_t T, int64_t
     p->G = (int)G;
     p->act = (int)act;
     p->eps = eps;
-    p->run = seq_gnorm_slab(S, T, p->D, p->G, (int)p->esize(), p->sms);
+    p->run = seq_gnorm_slab(S, T, p->D, p->G, (int)p->esize(), direction == SEQ_BWD, p->sms);
     const int64_t slots = cut_slots(S, T, p->L, p->run);
     if (slots > INT32_MAX) {
         delete p;

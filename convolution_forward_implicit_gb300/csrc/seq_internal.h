@@ -202,7 +202,7 @@ struct SeqGnormParams {
 };
 cudaError_t launch_seq_gnorm_fwd(const SeqGnormParams& p, bool bf16, cudaStream_t stream);
 cudaError_t launch_seq_gnorm_bwd(const SeqGnormParams& p, bool bf16, cudaStream_t stream);
-int seq_gnorm_slab(long long S, long long T, int D, int G, int esize, int sms);
+int seq_gnorm_slab(long long S, long long T, int D, int G, int esize, bool bwd, int sms);
 
 // ---- gated delta rule ----
 constexpr int DELTA_CHUNK = 64;     // tokens worked on at once; saved states lie at every chunk's first token
