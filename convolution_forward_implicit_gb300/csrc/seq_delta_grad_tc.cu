@@ -79,7 +79,7 @@ __device__ __forceinline__ uint4 row8(const __nv_bfloat16* from, int c, int widt
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
-__device__ __forceinline__ void meet() { asm volatile("bar.sync 1, %0;" ::"n"(GW) : "memory"); }      // the eight warps
+__device__ __forceinline__ void meet() { asm volatile("bar.sync 1, %0;" ::"n"(GW) : "memory"); }      // all warps
 
 // A from shared memory too
 __device__ __forceinline__ void mma_ss_k4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate, uint32_t astep, uint32_t bstep) {
@@ -103,10 +103,13 @@ __global__ void __launch_bounds__(GW, 1) delta_grad_tc_kernel(const __grid_const
     if (cut.n <= 0) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wq = warp & 3, cq = warp >> 2;
     const int kh = blockIdx.y, rep = SHARED ? p.Hv / p.Hk : 1, blocks = (p.Dv + 63) / 64;
-    const uint32_t ready = smem_u32(&s.bars[0]), bar_h = smem_u32(&s.bars[1]), bar_e = smem_u32(&s.bars[2]);
+    // Two barriers say what is ready, the states' D3 by its own: a warp goes on from one telling to the other without a wait between,
+    // and would else be counted in place of one that has not told the first yet.
+    const uint32_t ready = smem_u32(&s.bars[0]), ready_dh = smem_u32(&s.bars[3]), bar_h = smem_u32(&s.bars[1]), bar_e = smem_u32(&s.bars[2]);
     volatile int* abort_flag = &s.abort;
     if (threadIdx.x == 0) {
         mbar_init(ready, GT_WARPS);
+        mbar_init(ready_dh, GT_WARPS);
         mbar_init(bar_h, 1);
         mbar_init(bar_e, 1);
         s.abort = 0;
@@ -135,11 +138,11 @@ __global__ void __launch_bounds__(GW, 1) delta_grad_tc_kernel(const __grid_const
     {
         // what the first warp issues once all have told: D2 and D1 of a block, its D3, or D4 and D5
         enum Part { ROWS, STATES, MATRICES };
-        uint32_t turn = 0;
+        uint32_t turn = 0, turn_dh = 0;
         auto issue = [&](Part part, bool first) {
             if (warp != 0) return;
-            const bool ok = wait_turn(ready, turn, abort_flag, err);
-            turn ^= 1;
+            const bool ok = part == STATES ? wait_turn(ready_dh, turn_dh, abort_flag, err) : wait_turn(ready, turn, abort_flag, err);
+            (part == STATES ? turn_dh : turn) ^= 1;
             tc_fence_after();
             if (ok && lane == 0) {
                 if (part == ROWS) {
@@ -181,11 +184,11 @@ __global__ void __launch_bounds__(GW, 1) delta_grad_tc_kernel(const __grid_const
             turn_e ^= 1;
             tc_fence_after();
         };
-        auto tell = [&]() {
+        auto tell = [&](uint32_t bar) {
             fence_proxy_async();
             tc_fence_before();
             __syncwarp();
-            arrive_once(ready);
+            arrive_once(bar);
         };
         // the row of K (second 64 lanes) or Q that the lane holds: 16-byte pieces of the swizzled atoms
         const int i = (wq & 1) * 32 + lane, isk = wq >> 1;
@@ -214,7 +217,7 @@ __global__ void __launch_bounds__(GW, 1) delta_grad_tc_kernel(const __grid_const
         for (int c = 0; c < (SHARED ? HC : 1); ++c) total[c] = 0.f;
         dep_wait();
         // A thread's pieces of 8 columns: row r8 of the tokens, rows r8 and r8 + 64 of the states.  What a block needs is on its way while the one before is worked
-        // on, in registers: with loads where they are used the kernel took 794 us instead of @@ (8192 tokens, 32 heads).
+        // on, in registers: with loads where they are used the call took 1470 us instead of 1391 (8192 tokens, 32 heads).
         const int r8 = threadIdx.x >> 3, c8 = threadIdx.x & 7;
         const uint32_t place = (uint32_t)(r8 * 128 + (c8 ^ (r8 & 7)) * 16);
         float h0[KP / 64][8], u[8], dr[8];
@@ -265,7 +268,7 @@ __global__ void __launch_bounds__(GW, 1) delta_grad_tc_kernel(const __grid_const
                     bf2_unpack(w[e], a, b);
                     vdr = fmaf(a, dr[2 * e], fmaf(b, dr[2 * e + 1], vdr));
                 }
-                tell();
+                tell(ready);
                 if (more) tokens(h_next, v_next);
                 issue(ROWS, v == 0);
 #pragma unroll
@@ -274,7 +277,7 @@ __global__ void __launch_bounds__(GW, 1) delta_grad_tc_kernel(const __grid_const
                     for (int e = 0; e < 8; ++e) hh = fmaf(h0[j][e], dh[j][e], hh);
                     split8(sm + G::DH + place + j * 8192, ATOM, dh[j]);
                 }
-                tell();
+                tell(ready_dh);
                 if (more) states(p.saved, h_next, v_next, h0);
                 issue(STATES, v == 0);
             }
@@ -324,7 +327,7 @@ __global__ void __launch_bounds__(GW, 1) delta_grad_tc_kernel(const __grid_const
                     split8(sm + (isk ? G::M3 : G::M1) + i * 128 + ((chunk ^ (i & 7)) * 16), 8192, by_row);
                 }
             }
-            tell();
+            tell(ready);
             issue(MATRICES, true);
             const float eb = expf(bi.x) * (1.f + bi.y), fq = p.scale * eb, fz = decay_between(end, bi);
             wait_e();

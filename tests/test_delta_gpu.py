@@ -266,6 +266,40 @@ def test_rows_beyond_32_bit_offsets(bf16):
     torch.cuda.empty_cache()
 
 
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("S,L,Hk,Hv,Dk,Dv", [(4, 2000, 16, 16, 128, 128), (4, 1000, 8, 32, 128, 128), (6, 700, 12, 12, 64, 192)])
+def test_a_large_batch_gives_what_its_sequences_give(bf16, S, L, Hk, Hv, Dk, Dv):
+    """Many times more chunks and heads than run at once: the bits of every sequence alone, each time."""
+    import torch
+    T = S * L
+    gen = torch.Generator("cuda").manual_seed(S + L)
+    dtype = torch.bfloat16 if bf16 else torch.float32
+
+    def normal(cols, dtype=dtype):
+        return torch.randn(T, cols, generator=gen, device="cuda").to(dtype)
+
+    ins = [normal(Hk * Dk), normal(Hk * Dk), normal(Hv * Dv), -0.1 * normal(Hv, torch.float32).abs(), torch.sigmoid(normal(Hv, torch.float32))]
+    dy = normal(Hv * Dv)
+
+    def run(n, rows):
+        f, b = (D.SeqDeltaPlan(n, n * L, Hk, Hv, Dk, Dv, CODE[bf16], d, qk_norm=True) for d in ("fwd", "bwd"))
+        x = [t[rows] for t in ins]
+        saved, y = b.allocate_saved(), torch.empty_like(x[2])
+        saved.fill_(float("nan"))
+        f.forward(*x, y, saved=saved)
+        out = [torch.empty_like(t) for t in x]
+        b.backward(*x, dy[rows], saved, *out)
+        f.check()
+        return [y, *out]
+
+    alone = [run(1, slice(s * L, (s + 1) * L)) for s in range(S)]
+    want = [torch.cat(t) for t in zip(*alone)]
+    assert all(bool(t.isfinite().all()) for t in want)
+    for _ in range(4):
+        for name, a, b in zip(("y", "dq", "dk", "dv", "dg", "dbeta"), run(S, slice(None)), want):
+            assert torch.equal(a, b), name
+
+
 def test_many_sequences():
     """More sequences than a launch's second dimension holds."""
     import torch
