@@ -144,6 +144,9 @@ __global__ void __launch_bounds__(DT) delta_chunk_kernel(const __grid_constant__
                     rows[RF_OUT + r] = p.scale * e * s.rq[r];
                     rows[RF_END + r] = decay_between(end, b[i]) * s.rk[r];
                     rows[RF_BETA + r] = beta;
+                    rows[RF_RQ + r] = s.rq[r];
+                    rows[RF_RK + r] = s.rk[r];
+                    *reinterpret_cast<float2*>(rows + RF_B + 2 * r) = b[i];
                 }
                 if (lane == 0) rows[RF_DECAY] = expf(end.x) * (1.f + end.y);
             }
@@ -235,7 +238,7 @@ struct WalkSmem {
     T k[DC * LD], q[DC * LD];
     float inv[DC * LSQ], a[DC * LSQ];
     float h[KP * LV], r[DC * LV], u[DC * LV];
-    float rows[DELTA_ROWS];
+    float rows[DELTA_FACTORS];
 };
 
 template <typename T, int KP, int DVB>
@@ -280,7 +283,7 @@ __global__ void __launch_bounds__(DT) delta_walk_kernel(const __grid_constant__ 
         load_rows<KP, LD>(s.q, static_cast<const T*>(p.q) + t * p.q_ld + kh * p.Dk, p.q_ld, n, p.Dk, p.wide);
         load_square<LSQ>(s.inv, p.tri + at * (2 * DC * DC));
         load_square<LSQ>(s.a, p.tri + at * (2 * DC * DC) + DC * DC);
-        if (threadIdx.x < DELTA_ROWS / 4) copy16_async(s.rows + threadIdx.x * 4, p.rows + at * DELTA_ROWS + threadIdx.x * 4, true);
+        if (threadIdx.x < DELTA_FACTORS / 4) copy16_async(s.rows + threadIdx.x * 4, p.rows + at * DELTA_ROWS + threadIdx.x * 4, true);
         copies_commit();
         const int i0 = (warp & 3) * 16 + g;
         float2 v[2][NT];             // the rows of v that R needs, as the product's sums lie

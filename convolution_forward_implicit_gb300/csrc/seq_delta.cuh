@@ -103,11 +103,12 @@ __device__ __forceinline__ void warp_mma(float (&acc)[NT][4], const A& a, const 
             mma8(acc[n], ah, bh);
         }
     }
-    if (A::EXACT && B::EXACT) return;
+    if constexpr (!A::EXACT || !B::EXACT) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[n][e] += low[n][e];
+            for (int e = 0; e < 4; ++e) acc[n][e] += low[n][e];
+    }
 }
 template <int N>
 __device__ __forceinline__ void zero(float (&acc)[N][4]) {
@@ -145,8 +146,9 @@ __device__ __forceinline__ void load_square(float* to, const float* from) {
 
 // ---- factors of a chunk's rows ----
 // In the workspace, by chunk and value head: RF_IN: beta exp(b) |k|^-1, RF_OUT: scale exp(b) |q|^-1, RF_END:
-// exp(b_C - b) |k|^-1, RF_BETA: beta, 64 each, and exp(b_C) at RF_DECAY.
-constexpr int RF_IN = 0, RF_OUT = DC, RF_END = 2 * DC, RF_BETA = 3 * DC, RF_DECAY = 4 * DC;
+// exp(b_C - b) |k|^-1, RF_BETA: beta, 64 each, and exp(b_C) at RF_DECAY; for the gradients |q|^-1, |k|^-1 and b (float2).
+constexpr int RF_IN = 0, RF_OUT = DC, RF_END = 2 * DC, RF_BETA = 3 * DC, RF_DECAY = 4 * DC, RF_RQ = DELTA_FACTORS, RF_RK = RF_RQ + DC,
+              RF_B = RF_RK + DC;
 
 // b of a chunk as two floats each (their sum is exact to 2^-48 or so): differences of neighbouring tokens keep
 // their accuracy however much has decayed before them.  g below -200 counts as -200, whose exponential is zero too;

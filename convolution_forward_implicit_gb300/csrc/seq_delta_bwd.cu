@@ -50,7 +50,7 @@ struct BackSmem {
     float inv[DC * LT], a[DC * LT];
     float dh[KP * LV], du[DC * LV], ndr[DC * LV];
     T dy[DC * LY];
-    float rows[DELTA_ROWS];
+    float rows[DELTA_FACTORS];
 };
 
 template <typename T, int KP, int DVB>
@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(DT) delta_back_kernel(const __grid_constant__ 
         load_rows<KP, LD>(s.q, static_cast<const T*>(p.q) + t * p.q_ld + kh * p.Dk, p.q_ld, n, p.Dk, p.wide);
         load_square<LT>(s.inv, p.tri + at * (2 * DC * DC));
         load_square<LT>(s.a, p.tri + at * (2 * DC * DC) + DC * DC);
-        if (threadIdx.x < DELTA_ROWS / 4) copy16_async(s.rows + threadIdx.x * 4, p.rows + at * DELTA_ROWS + threadIdx.x * 4, true);
+        if (threadIdx.x < DELTA_FACTORS / 4) copy16_async(s.rows + threadIdx.x * 4, p.rows + at * DELTA_ROWS + threadIdx.x * 4, true);
         copies_commit();
         load_block<DVB, LY>(s.dy, static_cast<const T*>(p.dy) + t * p.dy_ld + h * p.Dv + c0, p.dy_ld, n, c0, p.Dv, p.pairs);
         float* keep = p.dstate + at * p.Dk * p.Dvp;

@@ -29,7 +29,7 @@ struct GradTc {
 };
 struct GradRest {
     float2 b[DC];
-    float rq[DC], rk[DC], beta[DC], vdr[DC], dotq[DC], dotk[DC];
+    float rq[DC], rk[DC], beta[DC], g[DC], vdr[DC];
     float dots[4][4][DC];
     float hh[GT_WARPS];
     int zero[GT_WARPS];
@@ -86,6 +86,15 @@ __device__ __forceinline__ void mma_ss_k4(uint32_t d, uint64_t a, uint64_t b, ui
 #pragma unroll
     for (int k = 0; k < 4; ++k) mma_bf16(d, a + k * (astep >> 4), b + k * (bstep >> 4), idesc, accumulate || k > 0 ? 1u : 0u);
 }
+template <int N>
+__device__ __forceinline__ void lanes_of(uint32_t at, uint32_t (&v)[N]) {       // N columns of the warp's lanes
+    if constexpr (N == 16)
+        tmem_ld16(at, v);
+    else
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                     : "r"(at));
+}
 // the products of parts that carry 24 bits: (2, 0), (0, 2), (1, 1), (1, 0), (0, 1), (0, 0)
 __device__ __forceinline__ int part_a(int q) { return 0x052 >> 2 * q & 3; }
 __device__ __forceinline__ int part_b(int q) { return 0x118 >> 2 * q & 3; }
@@ -122,13 +131,37 @@ __global__ void __launch_bounds__(GW, 1) delta_grad_tc_kernel(const __grid_const
     {
         load_kq<KP, GW>(base, static_cast<const T*>(p.k) + cut.t0 * p.k_ld + kh * p.Dk, static_cast<const T*>(p.q) + cut.t0 * p.q_ld + kh * p.Dk, p.k_ld,
                         p.q_ld, cut.n, p.Dk, threadIdx.x);
-        cp_async_commit();
+        cp_async_commit();                       // (waited for where the first head's matrices are)
         for (int i = threadIdx.x; i < 2 * 8192 / 16; i += GW)      // dY is one part: its others are zero
             *reinterpret_cast<uint4*>(sm + G::A + (1 + i / 512) * ATOM + i % 512 * 16) = make_uint4(0, 0, 0, 0);
-        if (threadIdx.x < DC) s.dotq[threadIdx.x] = s.dotk[threadIdx.x] = 0.f;
-        cp_async_wait<0>();
-        fence_proxy_async();
     }
+    dep_wait();
+            // A thread's pieces of 8 columns: row r8 of the tokens, rows r8 and r8 + 64 of the states.  What a block needs is on its way while the one before is worked
+            // on, in registers: with loads where they are used the call took 1470 us instead of 1391 (8192 tokens, 32 heads).
+            const int r8 = threadIdx.x >> 3, c8 = threadIdx.x & 7;
+            const uint32_t place = (uint32_t)(r8 * 128 + (c8 ^ (r8 & 7)) * 16);
+            float h0[KP / 64][8], u[8], dr[8];
+            uint4 dy, vv;
+            auto states = [&](const float* from, int h, int v, float (&x)[KP / 64][8]) {
+                const long long at = (long long)blockIdx.x * p.Hv + h;
+                const int col = v * 64 + c8 * 8;
+    #pragma unroll
+                for (int j = 0; j < KP / 64; ++j) {
+                    const int r = r8 + 64 * j;
+                    floats8(from + (at * p.Dk + r) * p.Dvp + col, col < p.Dvp && r < p.Dk, col + 4 < p.Dvp && r < p.Dk, x[j]);
+                }
+            };
+            auto tokens = [&](int h, int v) {
+                const long long at = (long long)blockIdx.x * p.Hv + h;
+                const int col = v * 64 + c8 * 8;
+                const bool first = col < p.Dvp, second = col + 4 < p.Dvp;
+                floats8(p.saved + p.saved_u + (at * DC + r8) * p.Dvp + col, first, second, u);
+                floats8(p.dr + (at * DC + r8) * p.Dvp + col, first, second, dr);
+                dy = row8(static_cast<const T*>(p.dy) + (cut.t0 + r8) * p.dy_ld + h * p.Dv + col, col, p.Dv, r8 < cut.n, p.val_wide);
+                vv = row8(static_cast<const T*>(p.v) + (cut.t0 + r8) * p.v_ld + h * p.Dv + col, col, p.Dv, r8 < cut.n, p.val_wide);
+            };
+            states(p.saved, kh * rep, 0, h0);
+            tokens(kh * rep, 0);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -195,54 +228,20 @@ __global__ void __launch_bounds__(GW, 1) delta_grad_tc_kernel(const __grid_const
         auto piece = [&](int row, int c) {       // columns 8 c .. of row (K: 0 .. 63, Q: 64 .. 127)
             return *reinterpret_cast<const uint4*>(sm + (c >> 3) * ATOM + row * 128 + ((c & 7) ^ (row & 7)) * 16);
         };
-        {
-            const int row = threadIdx.x >> 2;
-            float sum = 0.f;
-#pragma unroll
-            for (int c = threadIdx.x & 3; c < KP / 8; c += 4) {
-                const uint4 w = piece(row, c);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float a, b;
-                    bf2_unpack(e == 0 ? w.x : e == 1 ? w.y : e == 2 ? w.z : w.w, a, b);
-                    sum = fmaf(a, a, fmaf(b, b, sum));
-                }
-            }
-            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-            if ((threadIdx.x & 3) == 0) (row < 64 ? s.rk : s.rq)[row & 63] = p.norm ? 1.f / sqrtf(sum + QK_EPS) : 1.f;
-        }
+        float along = 0.f;                       // <row of q or k, its gradient>
         float total[SHARED ? HC : 1];
 #pragma unroll
         for (int c = 0; c < (SHARED ? HC : 1); ++c) total[c] = 0.f;
-        dep_wait();
-        // A thread's pieces of 8 columns: row r8 of the tokens, rows r8 and r8 + 64 of the states.  What a block needs is on its way while the one before is worked
-        // on, in registers: with loads where they are used the call took 1470 us instead of 1391 (8192 tokens, 32 heads).
-        const int r8 = threadIdx.x >> 3, c8 = threadIdx.x & 7;
-        const uint32_t place = (uint32_t)(r8 * 128 + (c8 ^ (r8 & 7)) * 16);
-        float h0[KP / 64][8], u[8], dr[8];
-        uint4 dy, vv;
-        auto states = [&](const float* from, int h, int v, float (&x)[KP / 64][8]) {
-            const long long at = (long long)blockIdx.x * p.Hv + h;
-            const int col = v * 64 + c8 * 8;
-#pragma unroll
-            for (int j = 0; j < KP / 64; ++j) {
-                const int r = r8 + 64 * j;
-                floats8(from + (at * p.Dk + r) * p.Dvp + col, col < p.Dvp && r < p.Dk, col + 4 < p.Dvp && r < p.Dk, x[j]);
-            }
-        };
-        auto tokens = [&](int h, int v) {
-            const long long at = (long long)blockIdx.x * p.Hv + h;
-            const int col = v * 64 + c8 * 8;
-            const bool first = col < p.Dvp, second = col + 4 < p.Dvp;
-            floats8(p.saved + p.saved_u + (at * DC + r8) * p.Dvp + col, first, second, u);
-            floats8(p.dr + (at * DC + r8) * p.Dvp + col, first, second, dr);
-            dy = row8(static_cast<const T*>(p.dy) + (cut.t0 + r8) * p.dy_ld + h * p.Dv + col, col, p.Dv, r8 < cut.n, p.val_wide);
-            vv = row8(static_cast<const T*>(p.v) + (cut.t0 + r8) * p.v_ld + h * p.Dv + col, col, p.Dv, r8 < cut.n, p.val_wide);
-        };
-        states(p.saved, kh * rep, 0, h0);
-        tokens(kh * rep, 0);
         for (int h = kh * rep; h < (kh + 1) * rep; ++h) {
+            if (threadIdx.x >= GW - DC) {        // (read behind the meeting below)
+                const int r = threadIdx.x - (GW - DC);
+                const float* rows = p.rows + ((long long)blockIdx.x * p.Hv + h) * DELTA_ROWS;
+                s.b[r] = *reinterpret_cast<const float2*>(rows + RF_B + 2 * r);
+                s.rq[r] = rows[RF_RQ + r];
+                s.rk[r] = rows[RF_RK + r];
+                s.beta[r] = rows[RF_BETA + r];
+                s.g[r] = r < cut.n ? p.g[(cut.t0 + r) * p.g_ld + h] : 0.f;
+            }
             float vdr = 0.f, hh = 0.f;
             bool from_zero = true;               // the state before the chunk is zero
             for (int v = 0; v < blocks; ++v) {
@@ -291,16 +290,7 @@ __global__ void __launch_bounds__(GW, 1) delta_grad_tc_kernel(const __grid_const
                 s.hh[warp] = hh;
                 s.zero[warp] = from_zero;
             }
-            if (warp == GT_WARPS - 1) {          // (the first may still be issuing)
-                float2 b[2];
-                chunk_decay(p.g + cut.t0 * p.g_ld + h, p.g_ld, cut.n, b);
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int r = 2 * lane + e;
-                    s.b[r] = b[e];
-                    s.beta[r] = r < cut.n ? p.beta[(cut.t0 + r) * p.beta_ld + h] : 0.f;
-                }
-            }
+            cp_async_wait<0>();                  // K and Q: told with the matrices
             meet();
             const float2 bi = s.b[i], end = s.b[DC - 1];
             const float rqi = s.rq[i], rki = s.rk[i], beta = s.beta[i];
@@ -331,23 +321,28 @@ __global__ void __launch_bounds__(GW, 1) delta_grad_tc_kernel(const __grid_const
             issue(MATRICES, true);
             const float eb = expf(bi.x) * (1.f + bi.y), fq = p.scale * eb, fz = decay_between(end, bi);
             wait_e();
-            // ---- rows: dQ (first 64 lanes), X and Z (the others), in pieces of 16 columns
+            // ---- rows: dQ (first 64 lanes), X and Z (the others), in pieces of columns (with 16 and the sums of heads registers spill)
+            constexpr int PIECE = SHARED ? 8 : 16;
             float dot[3][4] = {};                // (four sums each: their differences make dg)
             float out[SHARED ? 1 : HC];
 #pragma unroll
-            for (int c = 0; c < HC; c += 16) {
+            for (int c = 0; c < HC; c += PIECE) {
                 const int col = cq * HC + c;
-                uint32_t d1[16], d4[16], d3[16], d5[16];
-                tmem_ld16(lanes + G::D1 + col, d1);
-                tmem_ld16(lanes + G::D4 + col, d4);
-                tmem_ld16(lanes + G::D3 + col, d3);
-                tmem_ld16(lanes + G::D5 + col, d5);
+                uint32_t d1[PIECE], d4[PIECE], d3[PIECE], d5[PIECE];
+                lanes_of(lanes + G::D1 + col, d1);
+                lanes_of(lanes + G::D4 + col, d4);
+                lanes_of(lanes + G::D3 + col, d3);
+                lanes_of(lanes + G::D5 + col, d5);
                 const int row = isk ? i : 64 + i;
-                const uint4 w0 = piece(row, col / 8), w1 = piece(row, col / 8 + 1);
-                const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+                uint32_t w[PIECE / 2];
+#pragma unroll
+                for (int e = 0; e < PIECE; e += 8) {
+                    const uint4 k = piece(row, (col + e) / 8);
+                    w[e / 2] = k.x; w[e / 2 + 1] = k.y; w[e / 2 + 2] = k.z; w[e / 2 + 3] = k.w;
+                }
                 tmem_ld_wait();
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
+                for (int e = 0; e < PIECE; ++e) {
                     float lo, hi;
                     bf2_unpack(w[e / 2], lo, hi);
                     const float own = e & 1 ? hi : lo;
@@ -374,58 +369,13 @@ __global__ void __launch_bounds__(GW, 1) delta_grad_tc_kernel(const __grid_const
                 for (int k = 0; k < 3; ++k) s.dots[1 + k][cq][i] = (dot[k][0] + dot[k][1]) + (dot[k][2] + dot[k][3]);
             }
             meet();
-            if (warp == 0) {                     // dbeta and dg, two tokens a lane
-                auto of = [&](int k, int r) { return (s.dots[k][0][r] + s.dots[k][1][r]) + (s.dots[k][2][r] + s.dots[k][3][r]); };
-                float all = 0.f, sum3 = 0.f;
-                double db[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int r = 2 * lane + e;
-                    const float rq = s.rq[r], rk = s.rk[r], be = s.beta[r];
-                    const float qq = rq * (of(0, r)), kx = rk * (of(1, r));
-                    const float kz = rk * (of(2, r));
-                    sum3 += rk * (of(3, r));
-                    db[e] = (double)(qq - kz) + (double)(be * kx);
-                    if (r < cut.n) p.dbeta[(cut.t0 + r) * p.dbeta_ld + h] = s.vdr[r] + kx;
-                    s.dotq[r] += qq;
-                    s.dotk[r] += fmaf(be, kx, kz);
-                }
-#pragma unroll
-                for (int d = 16; d > 0; d >>= 1) sum3 += __shfl_xor_sync(0xffffffffu, sum3, d);
-#pragma unroll
-                for (int w = 0; w < GT_WARPS; ++w) all += s.hh[w];
-                if (lane == 31) db[1] += (double)fmaf(expf(end.x) * (1.f + end.y), all, sum3);
-                double sum = db[0] + db[1];      // from the lane's first token on
-#pragma unroll
-                for (int d = 1; d < 32; d <<= 1) {
-                    const double o = __shfl_down_sync(0xffffffffu, sum, d);
-                    if (lane + d < 32) sum += o;
-                }
-                const double after = __shfl_down_sync(0xffffffffu, sum, 1);
-                double dg[2] = {sum, db[1] + (lane < 31 ? after : 0.0)};
-                int zero = 1;
-#pragma unroll
-                for (int w = 0; w < GT_WARPS; ++w) zero = zero && s.zero[w];
-                // All of db together is <h0, gradient at h0>: nothing where h0 is.  The first half of the tokens then has dg from
-                // the sums before it, the very first none.
-                const double whole = __shfl_sync(0xffffffffu, sum, 0);
-                if (zero && lane < 16) {
-                    dg[0] -= whole;
-                    dg[1] -= whole;
-                }
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int r = 2 * lane + e;
-                    if (r < cut.n)               // (nothing passes a factor of zero)
-                        p.dg[(cut.t0 + r) * p.dg_ld + h] = expf(p.g[(cut.t0 + r) * p.g_ld + h]) == 0.f ? 0.f : (float)dg[e];
-                }
-            }
+            auto of = [&](int k, int r) { return (s.dots[k][0][r] + s.dots[k][1][r]) + (s.dots[k][2][r] + s.dots[k][3][r]); };
+            along += isk ? fmaf(beta, rki * of(1, i), rki * of(2, i)) : rqi * of(0, i);
             if (!SHARED || h == (kh + 1) * rep - 1) {
-                meet();
                 // through the lengths: d(k / |k|) = (d - k^ (k^.d)) / |k|; through shared memory, for whole rows: written by
                 // the lanes that hold them, 4 KB apart, they took 180 us of the call's 1390 (8192 tokens, 32 heads)
                 {
-                    const float r = isk ? rki : rqi, f = p.norm ? (isk ? s.dotk[i] : s.dotq[i]) * r : 0.f;
+                    const float r = isk ? rki : rqi, f = p.norm ? along * r : 0.f;
                     const int row = isk ? i : 64 + i;
 #pragma unroll
                     for (int c = 0; c < HC; c += 8) {
@@ -459,6 +409,49 @@ __global__ void __launch_bounds__(GW, 1) delta_grad_tc_kernel(const __grid_const
                         for (int e = 0; e < 8; ++e)
                             if (c + e < p.Dk) reinterpret_cast<uint16_t*>(to)[e] = (uint16_t)(w[e / 2] >> (e % 2 * 16));
                     }
+                }
+            }
+            if (warp == GT_WARPS - 1) {                  // dbeta and dg, two tokens a lane
+                float all = 0.f, sum3 = 0.f;
+                double db[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int r = 2 * lane + e;
+                    const float rq = s.rq[r], rk = s.rk[r], be = s.beta[r];
+                    const float qq = rq * (of(0, r)), kx = rk * (of(1, r));
+                    const float kz = rk * (of(2, r));
+                    sum3 += rk * (of(3, r));
+                    db[e] = (double)(qq - kz) + (double)(be * kx);
+                    if (r < cut.n) p.dbeta[(cut.t0 + r) * p.dbeta_ld + h] = s.vdr[r] + kx;
+                }
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1) sum3 += __shfl_xor_sync(0xffffffffu, sum3, d);
+#pragma unroll
+                for (int w = 0; w < GT_WARPS; ++w) all += s.hh[w];
+                if (lane == 31) db[1] += (double)fmaf(expf(end.x) * (1.f + end.y), all, sum3);
+                double sum = db[0] + db[1];      // from the lane's first token on
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const double o = __shfl_down_sync(0xffffffffu, sum, d);
+                    if (lane + d < 32) sum += o;
+                }
+                const double after = __shfl_down_sync(0xffffffffu, sum, 1);
+                double dg[2] = {sum, db[1] + (lane < 31 ? after : 0.0)};
+                int zero = 1;
+#pragma unroll
+                for (int w = 0; w < GT_WARPS; ++w) zero = zero && s.zero[w];
+                // All of db together is <h0, gradient at h0>: nothing where h0 is.  The first half of the tokens then has dg from
+                // the sums before it, the very first none.
+                const double whole = __shfl_sync(0xffffffffu, sum, 0);
+                if (zero && lane < 16) {
+                    dg[0] -= whole;
+                    dg[1] -= whole;
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int r = 2 * lane + e;
+                    if (r < cut.n)               // (nothing passes a factor of zero)
+                        p.dg[(cut.t0 + r) * p.dg_ld + h] = expf(s.g[r]) == 0.f ? 0.f : (float)dg[e];
                 }
             }
             meet();                              // (the next head's sums go where these were read)

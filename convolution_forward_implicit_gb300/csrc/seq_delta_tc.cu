@@ -191,9 +191,9 @@ struct Walk {
             const uint32_t to = stage(i), bar = turn.full + 8 * (i & 1);
             if (!turn.free(i)) break;
             if (thread == 0) {
-                mbar_arrive_expect_tx(bar, PLANES + DELTA_ROWS * 4);
+                mbar_arrive_expect_tx(bar, PLANES + DELTA_FACTORS * 4);
                 bulk_g2s(to + WalkTc<KP>::KQ, reinterpret_cast<const uint8_t*>(p.tri) + at(p, c) * PLANES, PLANES, bar);
-                bulk_g2s(to + WalkTc<KP>::KQ + PLANES, p.rows + at(p, c) * DELTA_ROWS, DELTA_ROWS * 4, bar);
+                bulk_g2s(to + WalkTc<KP>::KQ + PLANES, p.rows + at(p, c) * DELTA_ROWS, DELTA_FACTORS * 4, bar);
             }
             load_kq<KP, 32 * LOADERS>(to, static_cast<const __nv_bfloat16*>(p.k) + t * p.k_ld + kh * p.Dk, static_cast<const __nv_bfloat16*>(p.q) + t * p.q_ld + kh * p.Dk,
                         p.k_ld, p.q_ld, min(DC, t1 - t), p.Dk, thread);

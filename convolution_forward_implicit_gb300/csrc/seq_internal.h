@@ -207,7 +207,7 @@ int seq_gnorm_slab(long long S, long long T, int D, int G, int esize, bool bwd, 
 // ---- gated delta rule ----
 constexpr int DELTA_CHUNK = 64;     // tokens worked on at once; saved states lie at every chunk's first token
 constexpr int DELTA_PLANES = 3 * 128 * 128;      // bytes of a chunk's matrices in parts
-constexpr int DELTA_ROWS = 264;     // floats of a chunk's row factors (see seq_delta.cuh)
+constexpr int DELTA_FACTORS = 264, DELTA_ROWS = 520;      // floats of a chunk's row factors, and with what they come from (see seq_delta.cuh)
 struct SeqDeltaParams {
     SeqAxis ax;
     SeqSlots sl;
