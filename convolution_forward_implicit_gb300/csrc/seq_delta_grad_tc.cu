@@ -8,8 +8,11 @@
 // are not exact in bf16 are three bf16 parts each (24 bits), written by the threads; products of two such take the six
 // large ones of the parts' nine.
 //
-// What bounds it: the products (about 10000 cycles of 64 for a chunk and value head at 128 x 128) and splitting the states into
-// parts, which runs beside them but for dY, dR and U.
+// What bounds it: one CTA is on an SM (210 KB of shared memory and all of TMEM), and its stages follow one another.  8192 tokens, 32 value
+// heads on 16 key heads of 128 x 128 take about 530 us: 13.5 CTAs an SM of two value heads each, at 75000 cycles, of which the
+// products take 21000, and the bytes (580 KB) would take 25000; the rest are splits, factors and row sums by 16 warps that wait for
+// one another.  A 17th warp that issues leaves 96 registers a thread instead of 128: the whole call took 1246 us with what spilled,
+// 1194 without it; products issued by three different warps made it 1187.
 #include "seq_delta.cuh"
 #include "seq_delta_tc.cuh"
 
@@ -136,32 +139,32 @@ __global__ void __launch_bounds__(GW, 1) delta_grad_tc_kernel(const __grid_const
             *reinterpret_cast<uint4*>(sm + G::A + (1 + i / 512) * ATOM + i % 512 * 16) = make_uint4(0, 0, 0, 0);
     }
     dep_wait();
-            // A thread's pieces of 8 columns: row r8 of the tokens, rows r8 and r8 + 64 of the states.  What a block needs is on its way while the one before is worked
-            // on, in registers: with loads where they are used the call took 1470 us instead of 1391 (8192 tokens, 32 heads).
-            const int r8 = threadIdx.x >> 3, c8 = threadIdx.x & 7;
-            const uint32_t place = (uint32_t)(r8 * 128 + (c8 ^ (r8 & 7)) * 16);
-            float h0[KP / 64][8], u[8], dr[8];
-            uint4 dy, vv;
-            auto states = [&](const float* from, int h, int v, float (&x)[KP / 64][8]) {
-                const long long at = (long long)blockIdx.x * p.Hv + h;
-                const int col = v * 64 + c8 * 8;
-    #pragma unroll
-                for (int j = 0; j < KP / 64; ++j) {
-                    const int r = r8 + 64 * j;
-                    floats8(from + (at * p.Dk + r) * p.Dvp + col, col < p.Dvp && r < p.Dk, col + 4 < p.Dvp && r < p.Dk, x[j]);
-                }
-            };
-            auto tokens = [&](int h, int v) {
-                const long long at = (long long)blockIdx.x * p.Hv + h;
-                const int col = v * 64 + c8 * 8;
-                const bool first = col < p.Dvp, second = col + 4 < p.Dvp;
-                floats8(p.saved + p.saved_u + (at * DC + r8) * p.Dvp + col, first, second, u);
-                floats8(p.dr + (at * DC + r8) * p.Dvp + col, first, second, dr);
-                dy = row8(static_cast<const T*>(p.dy) + (cut.t0 + r8) * p.dy_ld + h * p.Dv + col, col, p.Dv, r8 < cut.n, p.val_wide);
-                vv = row8(static_cast<const T*>(p.v) + (cut.t0 + r8) * p.v_ld + h * p.Dv + col, col, p.Dv, r8 < cut.n, p.val_wide);
-            };
-            states(p.saved, kh * rep, 0, h0);
-            tokens(kh * rep, 0);
+    // A thread's pieces of 8 columns: row r8 of the tokens, rows r8 and r8 + 64 of the states.  What a block needs
+    // is on its way while the one before is worked on, in registers: with loads where they are used the call took 1470 us instead of 1391 (8192 tokens, 32 heads).
+    const int r8 = threadIdx.x >> 3, c8 = threadIdx.x & 7;
+    const uint32_t place = (uint32_t)(r8 * 128 + (c8 ^ (r8 & 7)) * 16);
+    float h0[KP / 64][8], u[8], dr[8];
+    uint4 dy, vv;
+    auto states = [&](const float* from, int h, int v, float (&x)[KP / 64][8]) {
+        const long long at = (long long)blockIdx.x * p.Hv + h;
+        const int col = v * 64 + c8 * 8;
+#pragma unroll
+        for (int j = 0; j < KP / 64; ++j) {
+            const int r = r8 + 64 * j;
+            floats8(from + (at * p.Dk + r) * p.Dvp + col, col < p.Dvp && r < p.Dk, col + 4 < p.Dvp && r < p.Dk, x[j]);
+        }
+    };
+    auto tokens = [&](int h, int v) {
+        const long long at = (long long)blockIdx.x * p.Hv + h;
+        const int col = v * 64 + c8 * 8;
+        const bool first = col < p.Dvp, second = col + 4 < p.Dvp;
+        floats8(p.saved + p.saved_u + (at * DC + r8) * p.Dvp + col, first, second, u);
+        floats8(p.dr + (at * DC + r8) * p.Dvp + col, first, second, dr);
+        dy = row8(static_cast<const T*>(p.dy) + (cut.t0 + r8) * p.dy_ld + h * p.Dv + col, col, p.Dv, r8 < cut.n, p.val_wide);
+        vv = row8(static_cast<const T*>(p.v) + (cut.t0 + r8) * p.v_ld + h * p.Dv + col, col, p.Dv, r8 < cut.n, p.val_wide);
+    };
+    states(p.saved, kh * rep, 0, h0);
+    tokens(kh * rep, 0);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
