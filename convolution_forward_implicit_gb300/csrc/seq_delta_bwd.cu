@@ -10,7 +10,8 @@
 //   dg is the sum of db from its token on.
 //
 // Three kernels: the forward pass's first again (T, A, factors of the rows); a walk over the chunks from the last to the
-// first for a block of columns (dV, the gradients of the states); and every chunk by itself for the rest.
+// first for a block of columns (dV, the gradients of the states); and every chunk by itself for the rest.  In fp32 2 sequences of 1500
+// tokens, 6 heads of 64 x 64 take 17, 135 and 50 us: the walk's 24 chunks in order are what bounds them (see seq_delta.cu).
 #include "seq_delta.cuh"
 
 namespace convfwd {
