@@ -277,7 +277,9 @@ __global__ void splitk_reduce_kernel(const float* __restrict__ ws, int splits, l
 
 unsigned* convfwd::device_error_word() { return error_word_ptr(); }
 
-conv_status convfwd::check_error_word(cudaStream_t stream) {
+namespace convfwd {
+// Waits for the stream; CONV_ERR_TIMEOUT (and the word cleared) if an error was raised.
+conv_status check_error_word(cudaStream_t stream) {
     if (cudaStreamSynchronize(stream) != cudaSuccess) return CONV_ERR_CUDA;
     unsigned v = 0;
     if (cudaMemcpyFromSymbol(&v, g_error_word, sizeof(v)) != cudaSuccess) return CONV_ERR_CUDA;
@@ -288,6 +290,7 @@ conv_status convfwd::check_error_word(cudaStream_t stream) {
     }
     return CONV_OK;
 }
+}  // namespace convfwd
 
 // ----------------------------------------------------------------------------- plan
 enum Variant { VAR_TC = 0, VAR_SIMT = 1, VAR_DG_SIMT = 2, VAR_WG_SIMT = 3, VAR_WG_TC = 4, VAR_DG_PHASED = 5 };

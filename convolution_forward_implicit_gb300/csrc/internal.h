@@ -6,8 +6,6 @@
 
 #include <utility>
 
-#include "conv.h"
-
 namespace convfwd {
 
 // A problem in the 3-spatial form (conv1d: D = H = 1, conv2d: D = 1), channels last.
@@ -91,8 +89,6 @@ inline cudaError_t launch_kernel(void (*kernel)(KArgs...), dim3 grid, dim3 block
 enum : unsigned { ERR_WAIT_TIMEOUT = 1u };
 // The word of the current GPU that kernels raise them in (nullptr: there is none); read by conv_plan_check and seq_delta_check.
 unsigned* device_error_word();
-// Waits for the stream; CONV_ERR_TIMEOUT (and the word cleared) if one was raised.
-conv_status check_error_word(cudaStream_t stream);
 
 // Output placement.  Normally output pixel (n, od, oh, ow) is row ((n*Do + od)*Ho + oh)*Wo + ow
 // of y.  With on = 1 the outputs are a lattice of a larger tensor of D x H x W pixels: pixel

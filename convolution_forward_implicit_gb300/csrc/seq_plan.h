@@ -5,6 +5,7 @@
 
 #include <new>
 
+#include "conv.h"
 #include "seq_internal.h"
 
 namespace convfwd {
@@ -24,6 +25,8 @@ inline int sm_count() {
 }
 
 inline size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+conv_status check_error_word(cudaStream_t stream);       // capi.cu
 
 }  // namespace convfwd
 
