@@ -246,18 +246,22 @@ struct WalkSmem {
     float rows[DELTA_FACTORS];
 };
 
-template <typename T, int KP, int DVB>
-__global__ void __launch_bounds__(DT) delta_walk_kernel(const __grid_constant__ SeqDeltaParams p, int dvbs) {
+template <typename T, int KP, int DVB, int MODE>
+__global__ void __launch_bounds__(DT) delta_walk_kernel(const __grid_constant__ SeqDeltaParams p, int dvbs, int dkbs) {
     extern __shared__ __align__(16) unsigned char raw[];
     using Smem = WalkSmem<T, KP, DVB>;
     Smem& s = *reinterpret_cast<Smem*>(raw);
     constexpr int LD = Smem::LD, LV = Smem::LV, NT = DVB / 8, MT = KP / 64;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t2 = (lane & 3) * 2;
-    const int dvb = blockIdx.x % dvbs, sh = blockIdx.x / dvbs, h = sh % p.Hv, seq = sh / p.Hv;
-    const int c0 = dvb * DVB, kh = h / (p.Hv / p.Hk);
-    const int t0 = p.ax.L > 0 ? seq * p.ax.L : seq_start(p.ax, seq, 0), t1 = p.ax.L > 0 ? t0 + p.ax.L : seq_start(p.ax, seq + 1, t0);
-    const int chunks = (t1 - t0 + DC - 1) / DC, slot0 = cut_base(p.ax, seq, DC);
-    const long long row = seq_slot(p.sl, seq), state = (row * p.Hv + h) * (long long)p.Dk * p.Dv;
+    const WalkPlace w = walk_place<MODE>(p, dvbs, dkbs);
+    if (MODE != DELTA_WHOLE) dep_wait();
+    if (w.none) return;
+    const int h = w.h, c0 = w.dvb * DVB, kh = h / (p.Hv / p.Hk), t0 = w.t0, t1 = w.t1, chunks = w.chunks, slot0 = w.slot0;
+    const long long row = seq_slot(p.sl, w.seq), state = (row * p.Hv + h) * (long long)p.Dk * p.Dv;
+    const long long kept = ((long long)w.piece * p.Hv + h) * p.Dk;            // rows of what is kept by piece
+    const bool joined = MODE == DELTA_JOINED && !(w.first && w.last);
+    float* saved = MODE == DELTA_PIECES ? nullptr : p.saved;
+    const int Dv = w.unit ? 0 : p.Dv;
     // the state in the layout of a product's sums: rows 16 (warp MT + m) + g and + 8, columns c0 + 8 n + t2 and + 1
     float st[MT][NT][4];
 #pragma unroll
@@ -267,7 +271,12 @@ __global__ void __launch_bounds__(DT) delta_walk_kernel(const __grid_constant__ 
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int r = (warp * MT + m) * 16 + g + (e >> 1) * 8, c = c0 + 8 * n + t2 + (e & 1);
-                st[m][n][e] = warp < 4 && p.h_in && row >= 0 && r < p.Dk && c < p.Dv ? p.h_in[state + (long long)r * p.Dv + c] : 0.f;
+                st[m][n][e] = 0.f;
+                if (warp < 4 && r < p.Dk) {
+                    if (w.unit) st[m][n][e] = r == c ? 1.f : 0.f;
+                    else if (joined) st[m][n][e] = c < p.Dvp ? p.start[(kept + r) * p.Dvp + c] : 0.f;
+                    else if ((MODE != DELTA_PIECES || w.first) && p.h_in && row >= 0 && c < p.Dv) st[m][n][e] = p.h_in[state + (long long)r * p.Dv + c];
+                }
             }
     auto put_state = [&]() {
 #pragma unroll
@@ -280,7 +289,7 @@ __global__ void __launch_bounds__(DT) delta_walk_kernel(const __grid_constant__ 
             }
     };
     if (warp < 4) put_state();
-    dep_wait();
+    if (MODE == DELTA_WHOLE) dep_wait();
     for (int c = 0; c < chunks; ++c) {
         const int t = t0 + c * DC, n = min(DC, t1 - t);
         const long long at = (long long)(slot0 + c) * p.Hv + h;
@@ -298,10 +307,10 @@ __global__ void __launch_bounds__(DT) delta_walk_kernel(const __grid_constant__ 
 #pragma unroll
                 for (int j = 0; j < NT; ++j) {
                     const int i = i0 + 8 * half, col = c0 + 8 * j + t2;
-                    v[half][j] = i < n ? load_pair(static_cast<const T*>(p.v) + (t + i) * p.v_ld + h * p.Dv + col, col, p.Dv, p.pairs) : make_float2(0.f, 0.f);
+                    v[half][j] = i < n ? load_pair(static_cast<const T*>(p.v) + (t + i) * p.v_ld + h * p.Dv + col, col, Dv, p.pairs) : make_float2(0.f, 0.f);
                 }
-            if (p.saved) {           // the state before the chunk
-                float* to = p.saved + at * p.Dk * p.Dvp;
+            if (saved) {             // the state before the chunk
+                float* to = saved + at * p.Dk * p.Dvp;
 #pragma unroll
                 for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -318,7 +327,8 @@ __global__ void __launch_bounds__(DT) delta_walk_kernel(const __grid_constant__ 
         __syncthreads();
         float acc[NT][4];            // K h0 (warps 0..3), Q h0 (4..7)
         zero(acc);
-        warp_mma<NT>(acc, Along<T>{warp < 4 ? s.k : s.q, LD}, Across<float>{s.h, LV}, (warp & 3) * 16, 0, 0, KP);
+        if (MODE != DELTA_PIECES || warp < 4)
+            warp_mma<NT>(acc, Along<T>{warp < 4 ? s.k : s.q, LD}, Across<float>{s.h, LV}, (warp & 3) * 16, 0, 0, KP);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             const int i = i0 + 8 * half;
@@ -349,8 +359,8 @@ __global__ void __launch_bounds__(DT) delta_walk_kernel(const __grid_constant__ 
                 *reinterpret_cast<float2*>(to) = make_float2(u[j][0], u[j][1]);
                 *reinterpret_cast<float2*>(to + 8 * LV) = make_float2(u[j][2], u[j][3]);
             }
-            if (p.saved) {
-                float* keep = p.saved + p.saved_u + at * DC * p.Dvp;
+            if (saved) {
+                float* keep = saved + p.saved_u + at * DC * p.Dvp;
 #pragma unroll
                 for (int j = 0; j < NT / 2; ++j) {
                     const int col = c0 + n0 + 8 * j + t2;
@@ -375,7 +385,7 @@ __global__ void __launch_bounds__(DT) delta_walk_kernel(const __grid_constant__ 
                     for (int e = 0; e < 4; ++e) st[m][j][e] = fmaf(decay, st[m][j][e], d[j][e]);
             }
             put_state();
-        } else {                     // Y = scale exp(b) Q h0 + A U
+        } else if (MODE != DELTA_PIECES) {       // Y = scale exp(b) Q h0 + A U
             const int m0 = (warp & 3) * 16;
             float d[NT][4];
             zero(d);
@@ -395,7 +405,22 @@ __global__ void __launch_bounds__(DT) delta_walk_kernel(const __grid_constant__ 
         }
         __syncthreads();
     }
-    if (warp < 4 && p.h_out && row >= 0) {
+    if (MODE == DELTA_PIECES) {
+        float* to = w.unit ? p.through : p.added;
+        const int width = w.unit ? p.Dkp : p.Dvp;
+        if (warp < 4)
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int r = (warp * MT + m) * 16 + g + (e >> 1) * 8, c = c0 + 8 * n + t2 + (e & 1);
+                        if (r < p.Dk && c < width) to[(kept + r) * width + c] = st[m][n][e];
+                    }
+        return;
+    }
+    if (warp < 4 && p.h_out && row >= 0 && w.last) {
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -416,19 +441,97 @@ cudaError_t launch_chunks(const SeqDeltaParams& p, cudaStream_t stream) {
     return launch_kernel(delta_chunk_kernel<T, KP>, dim3((unsigned)p.slots, (unsigned)p.Hk), dim3(DT), smem, stream, false, 1, p);
 }
 
+// The states that the pieces of a sequence start from, 32 columns of a value head a block: h <- through h + added from piece to piece.
+template <int KP>
+struct JoinSmem {
+    static constexpr int LP = KP + 8, LV = 36;
+    float m[2][KP * LP], h[2][KP * LV];
+};
+template <int KP>
+__global__ void __launch_bounds__(DT) delta_join_kernel(const __grid_constant__ SeqDeltaParams p, int cols) {
+    extern __shared__ __align__(16) unsigned char raw[];
+    using Smem = JoinSmem<KP>;
+    Smem& s = *reinterpret_cast<Smem*>(raw);
+    constexpr int LP = Smem::LP, LV = Smem::LV, NT = KP / 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t2 = (lane & 3) * 2;
+    const int c0 = blockIdx.x % cols * 32, sh = blockIdx.x / cols, h = sh % p.Hv, seq = sh / p.Hv, per = p.run * DC;
+    const int t0 = p.ax.L > 0 ? seq * p.ax.L : seq_start(p.ax, seq, 0), t1 = p.ax.L > 0 ? t0 + p.ax.L : seq_start(p.ax, seq + 1, t0);
+    const int n = (t1 - t0 + per - 1) / per;
+    dep_wait();
+    if (n < 2) return;
+    const int base = cut_base(p.ax, seq, per);
+    const long long row = seq_slot(p.sl, seq), state = (row * p.Hv + h) * (long long)p.Dk * p.Dv;
+    auto rows_of = [&](int i) { return ((long long)(base + i) * p.Hv + h) * p.Dk; };
+    auto load = [&](int i) {             // the matrix of piece i
+        for (int e = threadIdx.x; e < KP * (KP / 4); e += DT) {
+            const int r = e / (KP / 4), c = e % (KP / 4) * 4;
+            const bool on = i < n - 1 && r < p.Dk && c < p.Dkp;
+            copy16_async(s.m[i & 1] + r * LP + c, on ? p.through + (rows_of(i) + r) * p.Dkp + c : p.through, on);
+        }
+        copies_commit();
+    };
+    load(1);
+    for (int e = threadIdx.x; e < KP * 32; e += DT) {
+        const int r = e / 32, c = c0 + e % 32;
+        const bool on = r < p.Dk && c < p.Dvp;
+        const float v = on ? p.added[(rows_of(0) + r) * p.Dvp + c] : 0.f;
+        s.h[0][r * LV + e % 32] = v;
+        if (on) {
+            p.start[(rows_of(0) + r) * p.Dvp + c] = p.h_in && row >= 0 && c < p.Dv ? p.h_in[state + (long long)r * p.Dv + c] : 0.f;
+            p.start[(rows_of(1) + r) * p.Dvp + c] = v;
+        }
+    }
+    const int m0 = warp % (KP / 16) * 16, n0 = warp / (KP / 16) * 16;
+    for (int i = 1; i < n - 1; ++i) {
+        copies_wait<0>();
+        __syncthreads();                 // (the last one's matrix and state have been read)
+        load(i + 1);
+        float acc[NT][4];
+        zero(acc);
+        warp_mma<NT>(acc, Along<float>{s.m[i & 1], LP}, Across<float>{s.h[(i - 1) & 1], LV}, m0, n0, 0, KP);
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int r = m0 + g + (e >> 1) * 8, cl = n0 + 8 * j + t2 + (e & 1), c = c0 + cl;
+                const bool on = r < p.Dk && c < p.Dvp;
+                const float v = on ? acc[j][e] + p.added[(rows_of(i) + r) * p.Dvp + c] : 0.f;
+                s.h[i & 1][r * LV + cl] = v;
+                if (on) p.start[(rows_of(i + 1) + r) * p.Dvp + c] = v;
+            }
+    }
+    copies_wait<0>();
+}
+template <int KP>
+cudaError_t launch_join(const SeqDeltaParams& p, cudaStream_t stream) {
+    constexpr int smem = (int)sizeof(JoinSmem<KP>);
+    cudaError_t e = cudaFuncSetAttribute(delta_join_kernel<KP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const int cols = (p.Dv + 31) / 32;
+    return launch_kernel(delta_join_kernel<KP>, dim3((unsigned)(p.ax.S * (long long)p.Hv * cols)), dim3(DT), smem, stream, true, 1, p, cols);
+}
+
+template <typename T, int KP, int DVB, int MODE>
+cudaError_t launch_mode(const SeqDeltaParams& p, cudaStream_t stream) {
+    constexpr int smem = (int)sizeof(WalkSmem<T, KP, DVB>);
+    cudaError_t e = cudaFuncSetAttribute(delta_walk_kernel<T, KP, DVB, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const int dvbs = (p.Dv + DVB - 1) / DVB, dkbs = (p.Dk + DVB - 1) / DVB;
+    const long long blocks = (MODE == DELTA_WHOLE ? p.ax.S : p.pieces) * (long long)p.Hv * (MODE == DELTA_PIECES ? dvbs + dkbs : dvbs);
+    return launch_kernel(delta_walk_kernel<T, KP, DVB, MODE>, dim3((unsigned)blocks), dim3(DT), smem, stream, p.slots > 0, 1, p, dvbs, dkbs);
+}
 template <typename T, int KP, int DVB>
 cudaError_t launch_walk(const SeqDeltaParams& p, cudaStream_t stream) {
-    constexpr int smem = (int)sizeof(WalkSmem<T, KP, DVB>);
-    cudaError_t e = cudaFuncSetAttribute(delta_walk_kernel<T, KP, DVB>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    const int dvbs = (p.Dv + DVB - 1) / DVB;
-    return launch_kernel(delta_walk_kernel<T, KP, DVB>, dim3((unsigned)(p.ax.S * (long long)p.Hv * dvbs)), dim3(DT), smem, stream, p.slots > 0, 1, p, dvbs);
+    if (!p.run) return launch_mode<T, KP, DVB, DELTA_WHOLE>(p, stream);
+    cudaError_t e = launch_mode<T, KP, DVB, DELTA_PIECES>(p, stream);
+    if (e == cudaSuccess) e = launch_join<KP>(p, stream);
+    return e == cudaSuccess ? launch_mode<T, KP, DVB, DELTA_JOINED>(p, stream) : e;
 }
 
 template <typename T>
 cudaError_t launch(const SeqDeltaParams& p, cudaStream_t stream) {
     // 32 columns a block, or 16 where that leaves SMs without one
-    const bool narrow = p.Dv <= 16 || p.ax.S * (long long)p.Hv * ((p.Dv + 31) / 32) < p.sms;
+    const bool narrow = p.Dv <= 16 || (p.run ? p.pieces : p.ax.S) * (long long)p.Hv * ((p.Dv + 31) / 32) < p.sms;
     if (p.Dk <= 64) return narrow ? launch_walk<T, 64, 16>(p, stream) : launch_walk<T, 64, 32>(p, stream);
     return narrow ? launch_walk<T, 128, 16>(p, stream) : launch_walk<T, 128, 32>(p, stream);
 }
@@ -446,7 +549,12 @@ cudaError_t launch_seq_delta_fwd(const SeqDeltaParams& args, bool bf16, cudaStre
     p.planes = bf16 && p.wide && p.compact && p.Dv > 16 ? 1 : 0;
     const cudaError_t e = launch_seq_delta_chunks(p, bf16, stream);
     if (e != cudaSuccess) return e;
-    if (p.planes) return launch_seq_delta_walk_tc(p, stream);
+    if (p.planes) {
+        if (!p.run) return launch_seq_delta_walk_tc(p, DELTA_WHOLE, stream);
+        cudaError_t f = launch_seq_delta_walk_tc(p, DELTA_PIECES, stream);
+        if (f == cudaSuccess) f = p.Dk <= 64 ? launch_join<64>(p, stream) : launch_join<128>(p, stream);
+        return f == cudaSuccess ? launch_seq_delta_walk_tc(p, DELTA_JOINED, stream) : f;
+    }
     return bf16 ? launch<__nv_bfloat16>(p, stream) : launch<float>(p, stream);
 }
 

@@ -208,6 +208,47 @@ __device__ __forceinline__ void store_pair(T* at, int c, int width, bool pair, f
     }
 }
 
+// ---- a walk's place ----
+// With few heads the chunks of a long sequence in order leave most SMs without work.  Its axis is then cut into pieces of p.run chunks, whose walks
+// are: what a piece adds to a state (from zero; the first piece: from the sequence's state), and, as its columns, what becomes of the unit
+// matrix with v = 0 (DELTA_PIECES, the last piece of a sequence needs neither); h = through h + added from piece to piece gives the states
+// they start from (delta_join_kernel); and the walks themselves from these (DELTA_JOINED).
+struct WalkPlace {
+    int h, seq, dvb, t0, t1, chunks, slot0, piece;
+    bool first, last, unit;          // piece of its sequence; columns of the unit matrix
+    bool none;                       // nothing to do
+};
+template <int MODE>
+__device__ __forceinline__ WalkPlace walk_place(const SeqDeltaParams& p, int dvbs, int dkbs) {
+    WalkPlace w;
+    const int per = MODE == DELTA_PIECES ? dvbs + dkbs : dvbs, sh = blockIdx.x / per;
+    w.dvb = blockIdx.x % per;
+    w.unit = MODE == DELTA_PIECES && w.dvb >= dvbs;
+    if (w.unit) w.dvb -= dvbs;
+    w.h = sh % p.Hv;
+    w.piece = sh / p.Hv;
+    if (MODE == DELTA_WHOLE) {
+        w.seq = w.piece;
+        w.t0 = p.ax.L > 0 ? w.seq * p.ax.L : seq_start(p.ax, w.seq, 0);
+        w.t1 = p.ax.L > 0 ? w.t0 + p.ax.L : seq_start(p.ax, w.seq + 1, w.t0);
+        w.slot0 = cut_base(p.ax, w.seq, DC);
+        w.first = w.last = true;
+        w.none = false;
+    } else {
+        const CutPiece c = cut_piece(p.ax, w.piece, p.run * DC);
+        w.seq = c.s;
+        w.t0 = c.t0;
+        w.t1 = c.t0 + max(c.n, 0);
+        w.slot0 = cut_base(p.ax, w.seq, DC) + c.index * p.run;
+        w.first = c.index == 0;
+        const int end = p.ax.L > 0 ? (w.seq + 1) * p.ax.L : seq_start(p.ax, w.seq + 1, seq_start(p.ax, w.seq, 0));
+        w.last = w.t1 >= end;
+        w.none = (c.n <= 0 && !w.first) || (MODE == DELTA_PIECES && (w.last || (w.unit && w.first)));
+    }
+    w.chunks = (w.t1 - w.t0 + DC - 1) / DC;
+    return w;
+}
+
 // T, A and the row factors of every chunk (the first kernel of a forward and of a backward call).
 cudaError_t launch_seq_delta_chunks(const SeqDeltaParams& p, bool bf16, cudaStream_t stream);
 

@@ -18,6 +18,32 @@ size_t row_bytes(const seq_plan* p) { return align256((size_t)p->slots * p->Hv *
 size_t state_bytes(const seq_plan* p) { return align256((size_t)p->slots * p->Hv * p->N * padded(p) * sizeof(float)); }
 size_t token_bytes(const seq_plan* p) { return align256((size_t)p->slots * p->Hv * DELTA_CHUNK * padded(p) * sizeof(float)); }
 
+int padded_keys(const seq_plan* p) { return (p->N + 3) / 4 * 4; }
+size_t piece_bytes(const seq_plan* p) { return align256((size_t)p->pieces * p->Hv * p->N * padded(p) * sizeof(float)); }
+size_t through_bytes(const seq_plan* p) { return align256((size_t)p->pieces * p->Hv * p->N * padded_keys(p) * sizeof(float)); }
+
+// Chunks of a piece of the axis (0: it is not cut), by the time of the longest walk in chunks: pieces walk at once, but twice, the
+// first time with the columns of a unit matrix (without outputs: 0.8), and their states are joined in order (0.5 a piece; launches: 2).
+// Without lengths the longest sequence is taken to hold all tokens, and cutting has to promise more.
+int choose_run(const seq_plan* p) {
+    const bool wide = p->dtype == CONV_BF16 && p->W > 16;
+    const int64_t width = wide ? 128 : 16, cap = wide ? p->sms : 2 * (int64_t)p->sms;
+    const int64_t dv = (p->W + width - 1) / width, dk = (p->N + width - 1) / width, S = p->L > 0 ? p->S : 1;
+    const int64_t n = ((p->L > 0 ? p->L : p->T) + DELTA_CHUNK - 1) / DELTA_CHUNK;
+    auto rounds = [&](int64_t blocks) { return (double)((blocks + cap - 1) / cap); };
+    double best = (p->L > 0 ? 0.8 : 0.7) * (double)n * rounds(S * p->Hv * dv);
+    int run = 0;
+    for (int64_t r = 2; r <= n / 2; r += 1 + r / 16) {
+        const int64_t m = (n + r - 1) / r;
+        const double t = r * (rounds(S * m * p->Hv * dv) + 0.8 * rounds(S * (m - 1) * p->Hv * (dv + dk))) + 0.5 * (m - 2) * rounds(S * p->Hv * ((p->W + 31) / 32)) + 2;
+        if (t < best && cut_slots(p->S, p->T, p->L, (int)(r * DELTA_CHUNK)) * p->Hv * (dv + dk) < (1 << 24)) {
+            best = t;
+            run = (int)r;
+        }
+    }
+    return run;
+}
+
 }  // namespace
 
 extern "C" {
@@ -43,10 +69,15 @@ conv_status seq_delta_plan_create(seq_plan_t* out, int64_t S, int64_t T, int64_t
     }
     p->slots = (int)slots;
     if (direction != SEQ_STEP) p->ws_bytes = tri_bytes(p) + row_bytes(p);
+    if (direction == SEQ_FWD) {
+        p->run = choose_run(p);
+        p->pieces = p->run ? (int)cut_slots(S, T, p->L, p->run * DELTA_CHUNK) : 0;
+        p->ws_bytes += 2 * piece_bytes(p) + through_bytes(p);
+    }
     if (direction == SEQ_BWD) p->ws_bytes += state_bytes(p) + token_bytes(p);
     snprintf(p->desc, sizeof p->desc,
-             "op=delta direction=%s dtype=%s sequences=%d tokens=%d ragged=%d key_heads=%d value_heads=%d key_width=%d value_width=%d qk_norm=%d chunks=%d",
-             dir_name(direction), type_name(dtype), p->S, p->T, p->ragged(), p->Hk, p->Hv, p->N, p->W, !!(flags & SEQ_DELTA_QK_NORM), p->slots);
+             "op=delta direction=%s dtype=%s sequences=%d tokens=%d ragged=%d key_heads=%d value_heads=%d key_width=%d value_width=%d qk_norm=%d chunks=%d piece_chunks=%d",
+             dir_name(direction), type_name(dtype), p->S, p->T, p->ragged(), p->Hk, p->Hv, p->N, p->W, !!(flags & SEQ_DELTA_QK_NORM), p->slots, p->run);
     *out = p;
     return CONV_OK;
 }
@@ -99,6 +130,12 @@ static conv_status delta_call(seq_plan_t p, const seq_delta_args* a, seq_directi
     if (dir != SEQ_STEP) {
         q.tri = reinterpret_cast<float*>(w);
         q.rows = reinterpret_cast<float*>(w + tri_bytes(p));
+        if (dir == SEQ_FWD) {
+            q.run = p->run; q.pieces = p->pieces; q.Dkp = padded_keys(p);
+            q.added = reinterpret_cast<float*>(w + tri_bytes(p) + row_bytes(p));
+            q.start = q.added + piece_bytes(p) / sizeof(float);
+            q.through = q.start + piece_bytes(p) / sizeof(float);
+        }
         q.dstate = reinterpret_cast<float*>(w + tri_bytes(p) + row_bytes(p));
         q.dr = reinterpret_cast<float*>(w + tri_bytes(p) + row_bytes(p) + state_bytes(p));
     }

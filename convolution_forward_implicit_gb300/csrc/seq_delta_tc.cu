@@ -137,7 +137,7 @@ struct Walk {
     bool on;
     long long row, state;
     Turns turn;
-    __device__ __forceinline__ Walk(const SeqDeltaParams& p, int dvbs, unsigned* err, uint8_t* raw) {
+    __device__ __forceinline__ Walk(const SeqDeltaParams& p, const WalkPlace& place, unsigned* err, uint8_t* raw) {
         using W = WalkTc<KP>;
         base = (smem_u32(raw) + 1023u) & ~1023u;
         smem = raw + (base - smem_u32(raw));
@@ -148,16 +148,15 @@ struct Walk {
         lane = threadIdx.x & 31;
         cq = (warp >> 2) - 1;                     // (the first four warps hold no lanes)
         tok = cq * TPT;                           // the thread's tokens of a chunk: tok .. tok + TPT - 1
-        const int dvb = blockIdx.x % dvbs, sh = blockIdx.x / dvbs;
-        h = sh % p.Hv;
-        seq = sh / p.Hv;
+        h = place.h;
+        seq = place.seq;
         kh = h / (p.Hv / p.Hk);
-        dv = dvb * 128 + (warp & 3) * 32 + lane;
-        on = dv < p.Dv && warp > LOADERS;
-        t0 = p.ax.L > 0 ? seq * p.ax.L : seq_start(p.ax, seq, 0);
-        t1 = p.ax.L > 0 ? t0 + p.ax.L : seq_start(p.ax, seq + 1, t0);
-        chunks = (t1 - t0 + DC - 1) / DC;
-        slot0 = cut_base(p.ax, seq, DC);
+        dv = place.dvb * 128 + (warp & 3) * 32 + lane;
+        on = dv < p.Dv && warp > LOADERS && !place.unit;
+        t0 = place.t0;
+        t1 = place.t1;
+        chunks = place.chunks;
+        slot0 = place.slot0;
         row = seq_slot(p.sl, seq);
         state = (row * p.Hv + h) * (long long)p.Dk * p.Dv + dv;
         if (threadIdx.x == 0) {
@@ -253,17 +252,17 @@ struct Walk {
                 if (first + i < n) at[i * step] = __float2bfloat16_rn(x[i]);
         }
     }
-    // The thread's part of a state to rows of Dvp floats.
-    __device__ __forceinline__ void keep(float* to, const SeqDeltaParams& p, const float (&st)[KP * 128 / WT]) const {
-        if (dv >= p.Dvp) return;
-        float* at = to + cq * (KP * 128 / WT) * p.Dvp + dv;
+    // The thread's part of a state to rows of `width` floats.
+    __device__ __forceinline__ void keep(float* to, const SeqDeltaParams& p, int width, const float (&st)[KP * 128 / WT]) const {
+        if (dv >= width) return;
+        float* at = to + cq * (KP * 128 / WT) * width + dv;
         if (p.Dk == KP) {
 #pragma unroll
-            for (int i = 0; i < KP * 128 / WT; ++i) at[i * p.Dvp] = st[i];
+            for (int i = 0; i < KP * 128 / WT; ++i) at[i * width] = st[i];
         } else {
 #pragma unroll
             for (int i = 0; i < KP * 128 / WT; ++i)
-                if (cq * (KP * 128 / WT) + i < p.Dk) at[i * p.Dvp] = st[i];
+                if (cq * (KP * 128 / WT) + i < p.Dk) at[i * width] = st[i];
         }
     }
     __device__ __forceinline__ void close() {
@@ -300,14 +299,20 @@ __device__ __forceinline__ void next_state(uint32_t from, float decay, float (&s
     }
 }
 
-template <int KP>
-__global__ void __launch_bounds__(WALK_THREADS, 1) delta_walk_tc_kernel(const __grid_constant__ SeqDeltaParams p, int dvbs, unsigned* err) {
+template <int KP, int MODE>
+__global__ void __launch_bounds__(WALK_THREADS, 1) delta_walk_tc_kernel(const __grid_constant__ SeqDeltaParams p, int dvbs, int dkbs, unsigned* err) {
     extern __shared__ uint8_t smem_raw[];
     using W = WalkTc<KP>;
     using T = __nv_bfloat16;
     constexpr int HK = KP * 128 / WT;                  // the thread's rows of the state: cq HK ..
     constexpr uint32_t ID_64 = idesc_f32acc(128, 64, 1u), ID_128 = idesc_f32acc(128, 128, 1u), ID_KP = idesc_f32acc(128, KP, 1u) | (1u << 16);
-    Walk<KP> w(p, dvbs, err, smem_raw);
+    constexpr bool Y = MODE != DELTA_PIECES;           // outputs too
+    const WalkPlace place = walk_place<MODE>(p, dvbs, dkbs);
+    if (MODE != DELTA_WHOLE) dep_wait();
+    if (place.none) return;
+    Walk<KP> w(p, place, err, smem_raw);
+    const long long kept = ((long long)place.piece * p.Hv + place.h) * p.Dk;       // rows of what is kept by piece
+    const bool joined = MODE == DELTA_JOINED && !(place.first && place.last);
     if (w.warp > 0 && w.warp <= LOADERS) {
         dep_wait();
         w.load(p, false);
@@ -322,7 +327,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) delta_walk_tc_kernel(const __
 #pragma unroll 1
                 for (int q = 0; q < 3; ++q) {
                     const int pl = q == 0 ? 1 : q == 1 ? 0 : 2;
-                    steps<KP / 16, false>(acc, w.tmem + W::H + pl * (KP / 2), sw128_desc(kq), pl == 2 ? ID_64 : ID_128, q > 0);
+                    steps<KP / 16, false>(acc, w.tmem + W::H + pl * (KP / 2), sw128_desc(kq), !Y || pl == 2 ? ID_64 : ID_128, q > 0);
                 }
                 mma_commit(w.turn.mma);
             }
@@ -332,7 +337,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) delta_walk_tc_kernel(const __
                 // U needs six products of parts, y the three large ones: (1, 0), (0, 1), (0, 0), then (2, 0), (0, 2), (1, 1)
 #pragma unroll 1
                 for (int q = 0; q < 6; ++q)
-                    steps<4, false>(acc, w.tmem + W::P + (0x481 >> 2 * q & 3) * 32, sw128_desc(tp + (0x604 >> 2 * q & 3) * ATOM), q < 3 ? ID_128 : ID_64, q > 0);
+                    steps<4, false>(acc, w.tmem + W::P + (0x481 >> 2 * q & 3) * 32, sw128_desc(tp + (0x604 >> 2 * q & 3) * ATOM), Y && q < 3 ? ID_128 : ID_64, q > 0);
                 mma_commit(w.turn.mma);
             }
             __syncwarp();
@@ -349,7 +354,10 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) delta_walk_tc_kernel(const __
 #pragma unroll
         for (int i = 0; i < HK; ++i) {
             const int r = w.cq * HK + i;
-            st[i] = p.h_in && w.row >= 0 && w.on && r < p.Dk ? p.h_in[w.state + (long long)r * p.Dv] : 0.f;
+            st[i] = 0.f;
+            if (place.unit) st[i] = r == w.dv && r < p.Dk ? 1.f : 0.f;
+            else if (joined) st[i] = w.dv < p.Dvp && r < p.Dk ? p.start[(kept + r) * p.Dvp + w.dv] : 0.f;
+            else if ((Y || place.first) && p.h_in && w.row >= 0 && w.on && r < p.Dk) st[i] = p.h_in[w.state + (long long)r * p.Dv];
         }
         uint32_t v[TPT / 2];
         dep_wait();
@@ -362,7 +370,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) delta_walk_tc_kernel(const __
             const int t = w.t0 + c * DC, n = min(DC, w.t1 - t);
             w.turn.tell();                        // h0's parts are in TMEM
             const float* rows = w.rows(c);
-            if (p.saved) w.keep(p.saved + w.at(p, c) * p.Dk * p.Dvp, p, st);
+            if (Y && p.saved) w.keep(p.saved + w.at(p, c) * p.Dk * p.Dvp, p, p.Dvp, st);
             if (!w.turn.next(w.turn.mma) || !w.turn.arrived(c)) break;
             float y[TPT];
 #pragma unroll
@@ -382,15 +390,17 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) delta_walk_tc_kernel(const __
                 }
                 put_parts(w.lanes + W::P + (tok + j) / 2, 32, r);
             }
+            if constexpr (Y) {
 #pragma unroll
-            for (int j = 0; j < TPT; j += 16) {       // (before the products with R overwrite it)
-                uint32_t a[16];
-                tmem_ld16(w.lanes + W::ACC + 64 + tok + j, a);
-                float f[16];
-                read16(rows + RF_OUT + tok + j, f);
-                tmem_ld_wait();
+                for (int j = 0; j < TPT; j += 16) {       // (before the products with R overwrite it)
+                    uint32_t a[16];
+                    tmem_ld16(w.lanes + W::ACC + 64 + tok + j, a);
+                    float f[16];
+                    read16(rows + RF_OUT + tok + j, f);
+                    tmem_ld_wait();
 #pragma unroll
-                for (int i = 0; i < 16; ++i) y[j + i] = f[i] * __uint_as_float(a[i]);
+                    for (int i = 0; i < 16; ++i) y[j + i] = f[i] * __uint_as_float(a[i]);
+                }
             }
             w.turn.tell();
             if (c + 1 < w.chunks) w.values(p.v, p.v_ld, p, c + 1, v);
@@ -402,7 +412,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) delta_walk_tc_kernel(const __
                 float f[16];
                 read16(rows + RF_END + tok + j, f);
                 tmem_ld_wait();
-                if (p.saved && w.dv < p.Dvp) {
+                if (Y && p.saved && w.dv < p.Dvp) {
                     float* to = p.saved + p.saved_u + (w.at(p, c) * DC + tok + j) * p.Dvp + w.dv;
 #pragma unroll
                     for (int i = 0; i < 16; ++i) to[i * p.Dvp] = __uint_as_float(a[i]);
@@ -411,29 +421,36 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) delta_walk_tc_kernel(const __
                 for (int i = 0; i < 16; ++i) f[i] *= __uint_as_float(a[i]);
                 put_parts(w.lanes + W::P + (tok + j) / 2, 32, f);
             }
+            if constexpr (Y) {
 #pragma unroll
-            for (int j = 0; j < TPT; j += 16) {
-                uint32_t a[16];
-                tmem_ld16(w.lanes + W::ACC + 64 + tok + j, a);
-                tmem_ld_wait();
+                for (int j = 0; j < TPT; j += 16) {
+                    uint32_t a[16];
+                    tmem_ld16(w.lanes + W::ACC + 64 + tok + j, a);
+                    tmem_ld_wait();
 #pragma unroll
-                for (int i = 0; i < 16; ++i) y[j + i] += __uint_as_float(a[i]);
+                    for (int i = 0; i < 16; ++i) y[j + i] += __uint_as_float(a[i]);
+                }
             }
             const float decay = rows[RF_DECAY];
             w.turn.tell();
+            if constexpr (Y) {
 #pragma unroll
-            for (int j = 0; j < TPT; j += 16) {
-                float x[16];
+                for (int j = 0; j < TPT; j += 16) {
+                    float x[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) x[i] = y[j + i];
-                w.store(p.y, p.y_ld, p, t, n, tok + j, x);
+                    for (int i = 0; i < 16; ++i) x[i] = y[j + i];
+                    w.store(p.y, p.y_ld, p, t, n, tok + j, x);
+                }
             }
             if (!w.turn.next(w.turn.mma)) break;
             w.turn.release(c);
             next_state<KP>(w.lanes + W::ACC + w.cq * HK, decay, st);
             if (c + 1 < w.chunks) put_state<KP>(w.lanes + W::H + w.cq * (HK / 2), st);
         }
-        if (p.h_out && w.row >= 0 && w.on) {
+        if (MODE == DELTA_PIECES) {
+            if (place.unit) w.keep(p.through + kept * p.Dkp, p, p.Dkp, st);
+            else w.keep(p.added + kept * p.Dvp, p, p.Dvp, st);
+        } else if (p.h_out && w.row >= 0 && w.on && place.last) {
 #pragma unroll
             for (int i = 0; i < HK; ++i)
                 if (w.cq * HK + i < p.Dk) p.h_out[w.state + (long long)(w.cq * HK + i) * p.Dv] = st[i];
@@ -442,13 +459,20 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) delta_walk_tc_kernel(const __
     w.close();
 }
 
-template <int KP>
+template <int KP, int MODE>
 cudaError_t launch_walk_tc(const SeqDeltaParams& p, unsigned* err, cudaStream_t stream) {
-    cudaError_t e = cudaFuncSetAttribute(delta_walk_tc_kernel<KP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)WalkTc<KP>::BYTES);
+    const auto kernel = delta_walk_tc_kernel<KP, MODE>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)WalkTc<KP>::BYTES);
     if (e != cudaSuccess) return e;
-    const int dvbs = (p.Dv + 127) / 128;
-    return launch_kernel(delta_walk_tc_kernel<KP>, dim3((unsigned)(p.ax.S * (long long)p.Hv * dvbs)), dim3(WALK_THREADS), WalkTc<KP>::BYTES, stream, p.slots > 0, 1, p,
-                         dvbs, err);
+    const int dvbs = (p.Dv + 127) / 128, dkbs = 1;
+    const long long blocks = (MODE == DELTA_WHOLE ? p.ax.S : p.pieces) * (long long)p.Hv * (MODE == DELTA_PIECES ? dvbs + dkbs : dvbs);
+    return launch_kernel(kernel, dim3((unsigned)blocks), dim3(WALK_THREADS), WalkTc<KP>::BYTES, stream, p.slots > 0, 1, p, dvbs, dkbs, err);
+}
+template <int KP>
+cudaError_t launch_walk_tc(const SeqDeltaParams& p, DeltaWalk mode, unsigned* err, cudaStream_t stream) {
+    return mode == DELTA_WHOLE    ? launch_walk_tc<KP, DELTA_WHOLE>(p, err, stream)
+           : mode == DELTA_PIECES ? launch_walk_tc<KP, DELTA_PIECES>(p, err, stream)
+                                  : launch_walk_tc<KP, DELTA_JOINED>(p, err, stream);
 }
 
 // ---- backward ----
@@ -469,7 +493,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) delta_back_tc_kernel(const __
     using T = __nv_bfloat16;
     constexpr int HK = KP * 128 / WT;
     constexpr uint32_t ACROSS = 1u << 16, ID_64 = idesc_f32acc(128, 64, 1u), ID_KP = idesc_f32acc(128, KP, 1u) | ACROSS;
-    Walk<KP> w(p, dvbs, err, smem_raw);
+    Walk<KP> w(p, walk_place<DELTA_WHOLE>(p, dvbs, 0), err, smem_raw);
     dep_launch();
     if (w.warp > 0 && w.warp <= LOADERS) {
         dep_wait();
@@ -537,7 +561,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) delta_back_tc_kernel(const __
             const int c = w.chunks - 1 - s, t = w.t0 + c * DC, n = min(DC, w.t1 - t);
             w.turn.tell();
             const float* rows = w.rows(s);
-            w.keep(p.dstate + w.at(p, c) * p.Dk * p.Dvp, p, st);
+            w.keep(p.dstate + w.at(p, c) * p.Dk * p.Dvp, p, p.Dvp, st);
             if (!w.turn.next(w.turn.mma) || !w.turn.arrived(s)) break;
 #pragma unroll
             for (int j = 0; j < TPT; j += 16) {
@@ -625,10 +649,10 @@ cudaError_t launch_back_tc(const SeqDeltaParams& p, unsigned* err, cudaStream_t 
 
 }  // namespace
 
-cudaError_t launch_seq_delta_walk_tc(const SeqDeltaParams& p, cudaStream_t stream) {
+cudaError_t launch_seq_delta_walk_tc(const SeqDeltaParams& p, DeltaWalk mode, cudaStream_t stream) {
     unsigned* err = device_error_word();
     if (!err) return cudaErrorUnknown;
-    return p.Dk <= 64 ? launch_walk_tc<64>(p, err, stream) : launch_walk_tc<128>(p, err, stream);
+    return p.Dk <= 64 ? launch_walk_tc<64>(p, mode, err, stream) : launch_walk_tc<128>(p, mode, err, stream);
 }
 
 cudaError_t launch_seq_delta_back_tc(const SeqDeltaParams& p, cudaStream_t stream) {

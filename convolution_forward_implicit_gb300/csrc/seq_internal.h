@@ -233,11 +233,16 @@ struct SeqDeltaParams {
     int pairs, key_pairs;           // v, y, dy, dv; dq, dk in aligned pairs of elements
     int val_wide, key_wide;         // v and dy; dq and dk in whole aligned 16-byte groups
     int quads;                      // step: states in whole aligned groups of 4
+    // forward, where the axis is cut for the walk (run > 0): chunks of a piece, pieces at most, and by piece and value head what
+    // a piece adds to a state [Dk][Dvp], the matrix it passes one through [Dk][Dkp], and the state it starts from [Dk][Dvp]
+    int run, pieces, Dkp;
+    float *added, *through, *start;
     int sms;
 };
 cudaError_t launch_seq_delta_fwd(const SeqDeltaParams& p, bool bf16, cudaStream_t stream);
 cudaError_t launch_seq_delta_bwd(const SeqDeltaParams& p, bool bf16, cudaStream_t stream);
-cudaError_t launch_seq_delta_walk_tc(const SeqDeltaParams& p, cudaStream_t stream);
+enum DeltaWalk { DELTA_WHOLE = 0, DELTA_PIECES = 1, DELTA_JOINED = 2 };     // see seq_delta.cuh
+cudaError_t launch_seq_delta_walk_tc(const SeqDeltaParams& p, DeltaWalk mode, cudaStream_t stream);
 cudaError_t launch_seq_delta_grad_tc(const SeqDeltaParams& p, cudaStream_t stream);
 cudaError_t launch_seq_delta_back_tc(const SeqDeltaParams& p, cudaStream_t stream);
 cudaError_t launch_seq_delta_step(const SeqDeltaParams& p, bool bf16, cudaStream_t stream);

@@ -37,7 +37,7 @@ struct seq_plan {
     unsigned flags;
     int S, T, D, L;        // L: tokens per sequence, 0 when ragged (or T = 0)
     int W, N, G;
-    int run;               // conv: tokens a thread walks
+    int run;               // conv: tokens a thread walks; group norm: of a slab; delta rule: chunks of a piece (0: none)
     int sms;
     convfwd::ScanPieces pc;
     int blocks;            // conv backward: token blocks; scan backward: channel blocks; norm backward: partial rows
@@ -48,6 +48,7 @@ struct seq_plan {
     float scale;           // delta rule
     int act;               // group norm
     int slots;             // delta rule, group norm: chunks or slabs of the token axis
+    int pieces;            // delta rule: of `run` chunks each (0: the axis is not cut for the walk)
     char desc[256];
 
     bool ragged() const { return flags & SEQ_RAGGED; }

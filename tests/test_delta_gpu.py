@@ -281,23 +281,79 @@ def test_a_large_batch_gives_what_its_sequences_give(bf16, S, L, Hk, Hv, Dk, Dv)
     ins = [normal(Hk * Dk), normal(Hk * Dk), normal(Hv * Dv), -0.1 * normal(Hv, torch.float32).abs(), torch.sigmoid(normal(Hv, torch.float32))]
     dy = normal(Hv * Dv)
 
-    def run(n, rows):
-        f, b = (D.SeqDeltaPlan(n, n * L, Hk, Hv, Dk, Dv, CODE[bf16], d, qk_norm=True) for d in ("fwd", "bwd"))
-        x = [t[rows] for t in ins]
-        saved, y = b.allocate_saved(), torch.empty_like(x[2])
-        saved.fill_(float("nan"))
-        f.forward(*x, y, saved=saved)
-        out = [torch.empty_like(t) for t in x]
-        b.backward(*x, dy[rows], saved, *out)
-        f.check()
-        return [y, *out]
+    def plans(n):
+        return (D.SeqDeltaPlan(n, n * L, Hk, Hv, Dk, Dv, CODE[bf16], d, qk_norm=True) for d in ("fwd", "bwd"))
 
-    alone = [run(1, slice(s * L, (s + 1) * L)) for s in range(S)]
+    f, b = plans(S)
+    saved, y, chunks = b.allocate_saved(), torch.empty_like(dy), S * (-(-L // 64)) * Hv
+    assert saved.numel() == chunks * (Dk + 64) * Dv
+
+    def backward(plan, saved, rows):
+        x = [t[rows] for t in ins]
+        out = [torch.empty_like(t) for t in x]
+        plan.backward(*x, dy[rows], saved, *out)
+        return out
+
+    saved.fill_(float("nan"))
+    f.forward(*ins, y, saved=saved)
+    states, tokens = saved[:chunks * Dk * Dv].view(S, -1), saved[chunks * Dk * Dv:].view(S, -1)
+    alone, one = [], torch.empty_like(y[:L])
+    fa, ba = plans(1)
+    for s in range(S):
+        rows = slice(s * L, (s + 1) * L)
+        alone.append(backward(ba, torch.cat((states[s], tokens[s])), rows))
+        # the walk of one sequence may be cut where the batch's is not: sums of fp32 in another order, and a rounding
+        fa.forward(*(t[rows] for t in ins), one)
+        close = (2.0 ** -7 if bf16 else 1e-5) * one.float().abs().max()
+        assert float((one.float() - y[rows].float()).abs().max()) <= float(close)
     want = [torch.cat(t) for t in zip(*alone)]
-    assert all(bool(t.isfinite().all()) for t in want)
+    assert all(bool(t.isfinite().all()) for t in (y, *want))
+    again = torch.empty_like(y)
     for _ in range(4):
-        for name, a, b in zip(("y", "dq", "dk", "dv", "dg", "dbeta"), run(S, slice(None)), want):
-            assert torch.equal(a, b), name
+        f.forward(*ins, again, saved=saved)
+        assert torch.equal(y, again)
+        for name, a, b_ in zip(("dq", "dk", "dv", "dg", "dbeta"), backward(b, saved, slice(None)), want):
+            assert torch.equal(a, b_), name
+    f.check()
+
+
+CUT = [([2000], False, 1, 2, 128, 128), ([1500] * 2, False, 1, 2, 64, 64), ([700, 0, 1300, 64, 1, 65], True, 1, 1, 104, 200),
+       ([900, 1, 1100], True, 1, 2, 37, 19), ([1290], False, 2, 2, 16, 16), ([640, 641], True, 1, 1, 128, 128)]
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("lens,ragged,Hk,Hv,Dk,Dv", CUT)
+def test_pieces_of_long_sequences(bf16, lens, ragged, Hk, Hv, Dk, Dv):
+    """Few heads and long sequences: the axis is cut for the walk, and what the pieces start from is joined."""
+    c = Case(Dk + Dv + len(lens), bf16, lens, Hk, Hv, Dk, Dv, ragged, norm=True, decay=0.02)
+    fwd, bwd = c.plan("fwd"), c.plan("bwd")
+    assert int(Q.seq_plan_describe(fwd.handle).split("piece_chunks=")[1]) > 0
+    h_in, h0, at, sl = c.states([1] if c.S > 2 else [])
+    ref = R.delta(**c.exact, lens=lens, h0=h0, norm=True, dy=c.dye.reshape(c.T, Hv, Dv))
+    fwd.allocate()
+    fwd.workspace.fill_(0xFF)
+    y, h_out, saved = c.b.out(c.T, Hv * Dv), c.b.out(c.S + 2, Hv, Dk, Dv, dtype=c.f32), bwd.allocate_saved()
+    saved.fill_(float("nan"))
+    fwd.forward(*c.ins(), y, starts=c.starts, h_in=h_in, h_out=h_out, slots=sl, saved=saved)
+    c.check(dict(y=y), ref)
+    c.check_states("h", h_out, ref["h"], at, R.FORWARD)
+    d = c.grads()
+    bwd.backward(*c.ins(), c.dy, saved, **d, starts=c.starts, slots=sl)
+    c.check(d, ref)
+    fwd.check()
+    c.b.check_guards()
+    both, y2 = h_in.clone(), c.b.out(c.T, Hv * Dv)
+    fwd.forward(*c.ins(), y2, starts=c.starts, h_in=both, h_out=both, slots=sl)
+    assert bool((y2 == y).all())
+    left, want = host(both), host(h_out)
+    for s in range(c.S):
+        if at[s] >= 0:
+            assert np.array_equal(left[at[s]], want[at[s]])
+    # rows that are not whole 16-byte groups, and no state: kernels of their own in bf16
+    o = Case(Dk + Dv + len(lens), bf16, lens, Hk, Hv, Dk, Dv, ragged, norm=True, decay=0.02, shift=1)
+    ref = R.delta(**o.exact, lens=lens, h0=0 * h0, norm=True)
+    fwd.forward(*o.ins(), y2, starts=o.starts)
+    o.check(dict(y=y2), ref)
 
 
 def test_many_sequences():
