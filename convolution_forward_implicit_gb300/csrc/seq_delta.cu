@@ -7,7 +7,7 @@
 //
 // What bounds them: the first, latency between its stages (inversion, products of 64 rows, factors by one warp a head): 8192 tokens, 32 value heads on
 // 16 key heads of 128 x 128 in bf16 take 117 us, 220 MB of traffic (28% of copy rate).  The walk, the order of its chunks: 3802 tokens of a head of
-// 48 x 80 in fp32 (60 chunks) take 244 us, 4 us a chunk, about as many in any number of CTAs an SM holds at once.  Operands on their way
+// 48 x 80 in fp32 (60 chunks) take 244 us, 4 us a chunk, about as many in any number of CTAs an SM holds at once; in pieces of the axis 55 + 10 + 76.  Operands on their way
 // a chunk ahead made no difference (257 us against 255): the products of 16 or 32 columns and their splits are one chain.
 #include "seq_delta.cuh"
 
@@ -441,10 +441,11 @@ cudaError_t launch_chunks(const SeqDeltaParams& p, cudaStream_t stream) {
     return launch_kernel(delta_chunk_kernel<T, KP>, dim3((unsigned)p.slots, (unsigned)p.Hk), dim3(DT), smem, stream, false, 1, p);
 }
 
-// The states that the pieces of a sequence start from, 32 columns of a value head a block: h <- through h + added from piece to piece.
+// The states that the pieces of a sequence start from, 16 columns of a value head a block: h <- through h + added from piece to piece, the
+// next piece's matrix and this one's sums on their way during the products.
 template <int KP>
 struct JoinSmem {
-    static constexpr int LP = KP + 8, LV = 36;
+    static constexpr int LP = KP + 8, LV = 20;
     float m[2][KP * LP], h[2][KP * LV];
 };
 template <int KP>
@@ -452,9 +453,9 @@ __global__ void __launch_bounds__(DT) delta_join_kernel(const __grid_constant__ 
     extern __shared__ __align__(16) unsigned char raw[];
     using Smem = JoinSmem<KP>;
     Smem& s = *reinterpret_cast<Smem*>(raw);
-    constexpr int LP = Smem::LP, LV = Smem::LV, NT = KP / 32;
+    constexpr int LP = Smem::LP, LV = Smem::LV, NT = KP / 64;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t2 = (lane & 3) * 2;
-    const int c0 = blockIdx.x % cols * 32, sh = blockIdx.x / cols, h = sh % p.Hv, seq = sh / p.Hv, per = p.run * DC;
+    const int c0 = blockIdx.x % cols * 16, sh = blockIdx.x / cols, h = sh % p.Hv, seq = sh / p.Hv, per = p.run * DC;
     const int t0 = p.ax.L > 0 ? seq * p.ax.L : seq_start(p.ax, seq, 0), t1 = p.ax.L > 0 ? t0 + p.ax.L : seq_start(p.ax, seq + 1, t0);
     const int n = (t1 - t0 + per - 1) / per;
     dep_wait();
@@ -471,23 +472,30 @@ __global__ void __launch_bounds__(DT) delta_join_kernel(const __grid_constant__ 
         copies_commit();
     };
     load(1);
-    for (int e = threadIdx.x; e < KP * 32; e += DT) {
-        const int r = e / 32, c = c0 + e % 32;
+    for (int e = threadIdx.x; e < KP * 16; e += DT) {
+        const int r = e / 16, c = c0 + e % 16;
         const bool on = r < p.Dk && c < p.Dvp;
         const float v = on ? p.added[(rows_of(0) + r) * p.Dvp + c] : 0.f;
-        s.h[0][r * LV + e % 32] = v;
+        s.h[0][r * LV + e % 16] = v;
         if (on) {
             p.start[(rows_of(0) + r) * p.Dvp + c] = p.h_in && row >= 0 && c < p.Dv ? p.h_in[state + (long long)r * p.Dv + c] : 0.f;
             p.start[(rows_of(1) + r) * p.Dvp + c] = v;
         }
     }
-    const int m0 = warp % (KP / 16) * 16, n0 = warp / (KP / 16) * 16;
+    const int m0 = warp % (KP / 16) * 16, n0 = warp / (KP / 16) * 8;
     for (int i = 1; i < n - 1; ++i) {
         copies_wait<0>();
         __syncthreads();                 // (the last one's matrix and state have been read)
         load(i + 1);
-        float acc[NT][4];
+        float acc[NT][4], more[NT][4];
         zero(acc);
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int r = m0 + g + (e >> 1) * 8, c = c0 + n0 + 8 * j + t2 + (e & 1);
+                more[j][e] = r < p.Dk && c < p.Dvp ? p.added[(rows_of(i) + r) * p.Dvp + c] : 0.f;
+            }
         warp_mma<NT>(acc, Along<float>{s.m[i & 1], LP}, Across<float>{s.h[(i - 1) & 1], LV}, m0, n0, 0, KP);
 #pragma unroll
         for (int j = 0; j < NT; ++j)
@@ -495,7 +503,7 @@ __global__ void __launch_bounds__(DT) delta_join_kernel(const __grid_constant__ 
             for (int e = 0; e < 4; ++e) {
                 const int r = m0 + g + (e >> 1) * 8, cl = n0 + 8 * j + t2 + (e & 1), c = c0 + cl;
                 const bool on = r < p.Dk && c < p.Dvp;
-                const float v = on ? acc[j][e] + p.added[(rows_of(i) + r) * p.Dvp + c] : 0.f;
+                const float v = on ? acc[j][e] + more[j][e] : 0.f;
                 s.h[i & 1][r * LV + cl] = v;
                 if (on) p.start[(rows_of(i + 1) + r) * p.Dvp + c] = v;
             }
@@ -507,7 +515,7 @@ cudaError_t launch_join(const SeqDeltaParams& p, cudaStream_t stream) {
     constexpr int smem = (int)sizeof(JoinSmem<KP>);
     cudaError_t e = cudaFuncSetAttribute(delta_join_kernel<KP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    const int cols = (p.Dv + 31) / 32;
+    const int cols = (p.Dv + 15) / 16;
     return launch_kernel(delta_join_kernel<KP>, dim3((unsigned)(p.ax.S * (long long)p.Hv * cols)), dim3(DT), smem, stream, true, 1, p, cols);
 }
 
@@ -530,8 +538,9 @@ cudaError_t launch_walk(const SeqDeltaParams& p, cudaStream_t stream) {
 
 template <typename T>
 cudaError_t launch(const SeqDeltaParams& p, cudaStream_t stream) {
-    // 32 columns a block, or 16 where that leaves SMs without one
-    const bool narrow = p.Dv <= 16 || (p.run ? p.pieces : p.ax.S) * (long long)p.Hv * ((p.Dv + 31) / 32) < p.sms;
+    // 32 columns a block, or 16 where that leaves SMs without one, or where the axis is cut (5003 tokens of 6 heads of
+    // 48 x 80 in pieces: the last walk takes 76 us with 16, 103 with 32)
+    const bool narrow = p.Dv <= 16 || p.run || p.ax.S * (long long)p.Hv * ((p.Dv + 31) / 32) < p.sms;
     if (p.Dk <= 64) return narrow ? launch_walk<T, 64, 16>(p, stream) : launch_walk<T, 64, 32>(p, stream);
     return narrow ? launch_walk<T, 128, 16>(p, stream) : launch_walk<T, 128, 32>(p, stream);
 }

@@ -317,17 +317,18 @@ def test_a_large_batch_gives_what_its_sequences_give(bf16, S, L, Hk, Hv, Dk, Dv)
     f.check()
 
 
-CUT = [([2000], False, 1, 2, 128, 128), ([1500] * 2, False, 1, 2, 64, 64), ([700, 0, 1300, 64, 1, 65], True, 1, 1, 104, 200),
-       ([900, 1, 1100], True, 1, 2, 37, 19), ([1290], False, 2, 2, 16, 16), ([640, 641], True, 1, 1, 128, 128)]
+# the last: whether the axis is cut
+CUT = [([2000], False, 1, 2, 128, 128, True), ([1500] * 2, False, 1, 2, 64, 64, True), ([700, 0, 1300, 64, 1, 65], True, 1, 1, 104, 200, True),
+       ([900, 1, 1100], True, 1, 2, 37, 19, True), ([1290], False, 2, 2, 16, 16, True), ([640, 641], True, 1, 1, 128, 128, False)]
 
 
 @pytest.mark.parametrize("bf16", [False, True])
-@pytest.mark.parametrize("lens,ragged,Hk,Hv,Dk,Dv", CUT)
-def test_pieces_of_long_sequences(bf16, lens, ragged, Hk, Hv, Dk, Dv):
+@pytest.mark.parametrize("lens,ragged,Hk,Hv,Dk,Dv,cut", CUT)
+def test_pieces_of_long_sequences(bf16, lens, ragged, Hk, Hv, Dk, Dv, cut):
     """Few heads and long sequences: the axis is cut for the walk, and what the pieces start from is joined."""
     c = Case(Dk + Dv + len(lens), bf16, lens, Hk, Hv, Dk, Dv, ragged, norm=True, decay=0.02)
     fwd, bwd = c.plan("fwd"), c.plan("bwd")
-    assert int(Q.seq_plan_describe(fwd.handle).split("piece_chunks=")[1]) > 0
+    assert (int(Q.seq_plan_describe(fwd.handle).split("piece_chunks=")[1]) > 0) == cut
     h_in, h0, at, sl = c.states([1] if c.S > 2 else [])
     ref = R.delta(**c.exact, lens=lens, h0=h0, norm=True, dy=c.dye.reshape(c.T, Hv, Dv))
     fwd.allocate()
