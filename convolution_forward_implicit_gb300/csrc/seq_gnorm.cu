@@ -530,6 +530,12 @@ __global__ void __launch_bounds__(GT, gn_blocks(BWD, sizeof(T))) gn_apply_kernel
             c1[BWD ? i : 0] = mul2(make_float2(-m0.x, -m1.x), r);
             c2[BWD ? i : 0] = mul2(make_float2(-m0.y, -m1.y), mul2(r, r));
         }
+        // a group of one value is its mean, whatever it is: no gradient, and not what is left of terms that cancel
+        const int from = p.ax.L > 0 ? 0 : seq_start(p.ax, cut.s, 0);
+        if (cpg == 1 && (p.ax.L > 0 ? p.ax.L : seq_start(p.ax, cut.s + 1, from) - from) == 1) {
+#pragma unroll
+            for (int i = 0; i < P; ++i) f.a[i] = c1[BWD ? i : 0] = c2[BWD ? i : 0] = dup(0.f);
+        }
     }
     const T* x = static_cast<const T*>(p.x) + (long long)cut.t0 * p.x_ld + at.c;
     const T* dy = BWD ? static_cast<const T*>(p.dy) + (long long)cut.t0 * p.dy_ld + at.c : nullptr;

@@ -393,6 +393,19 @@ def test_bounds_outside_their_contract():
             c.b.check_guards()
 
 
+def test_bounds_outside_their_contract_in_pieces():
+    import torch
+    for bf16 in (False, True):
+        c = Case(22, bf16, [900, 1000, 300], 1, 2, 64, 64, True)
+        fwd, bwd = c.plan("fwd"), c.plan("bwd")
+        assert int(Q.seq_plan_describe(fwd.handle).split("piece_chunks=")[1]) > 0
+        for bad in ([0, 5000, -7, 2200], [0, 2000, 20, 2200], [1900, 10, 5, 2], [0, 0, 0, 0]):
+            st = torch.tensor(bad, dtype=torch.int32, device="cuda")
+            y, h = c.b.out(c.T, 128), c.b.out(3, 2, 64, 64, dtype=c.f32)
+            fwd.forward(*c.ins(), y, starts=st, h_out=h, saved=bwd.allocate_saved())
+            c.b.check_guards()
+
+
 # ------------------------------------------------------------------------------- streams and graphs
 def test_streams_and_graphs():
     """A prompt and its backward call on another stream, two streams with one plan, and captured; an eager autograd graph
@@ -439,6 +452,39 @@ def test_streams_and_graphs():
         same()
     loss.backward()
     assert torch.equal(leaf.grad, (2 * leaf.detach().float()).to(leaf.dtype))
+    fwd.check()
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+def test_pieces_on_streams_and_in_a_graph(bf16):
+    """A plan that cuts the axis, in place of its states: on two streams one after the other, and captured and replayed."""
+    import torch
+    c = Case(23, bf16, [1400], 1, 2, 128, 128, False, decay=0.02)
+    fwd, y = c.plan("fwd"), c.b.out(1400, 256)
+    assert int(Q.seq_plan_describe(fwd.handle).split("piece_chunks=")[1]) > 0
+    h0, _ = c.b.normal(1, 2, 128, 128, std=0.3, dtype=c.f32)
+    h = h0.clone()
+    fwd.forward(*c.ins(), y, h_in=h, h_out=h)
+    want = y.clone(), h.clone()
+    side = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(3):
+        for s in side:
+            s.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(s):
+                h.copy_(h0)
+                y.fill_(1.0)
+                fwd.forward(*c.ins(), y, h_in=h, h_out=h)
+            torch.cuda.current_stream().wait_stream(s)
+            assert torch.equal(y, want[0]) and torch.equal(h, want[1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        h.copy_(h0)
+        fwd.forward(*c.ins(), y, h_in=h, h_out=h)
+    for _ in range(3):
+        y.fill_(1.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want[0]) and torch.equal(h, want[1])
     fwd.check()
 
 

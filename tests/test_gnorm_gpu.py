@@ -236,3 +236,30 @@ def test_streams_and_graphs():
     for _ in range(3):
         graph.replay()
         same()
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("lens,ragged", [([1] * 7, False), ([1, 3, 0, 1, 200, 1], True)])
+@pytest.mark.parametrize("act", ["none", "silu", "gelu"])
+def test_groups_of_one_value_pass_no_gradient(bf16, lens, ragged, act):
+    """A token by itself and as many groups as channels: the value is its mean, so dx is zero, exactly; the others as ever."""
+    import torch
+    D, T = 384, sum(lens)
+    b = Box(D + T, bf16)
+    x, xe = b.normal(T, D)
+    w, we = b.put(b.rng.uniform(0.5, 1.5, D))
+    bias, be = b.normal(D, std=0.3)
+    dy, dye = b.normal(T, D)
+    out = run(None, b, bf16, x, w, bias, dy, lens, D, D, act, ragged)
+    at = np.cumsum([0] + list(lens))
+    for s, n in enumerate(lens):
+        if n == 1:
+            assert bool((out["dx"][at[s]] == 0).all())
+    ref, mag = R.gnorm(xe, we, be, D, lens, act, 1e-5, dy=dye)
+    compare(out, ref, mag, bf16, terms=T)
+    # a value that is not finite still shows in its own place, and there only
+    dy[0, 5] = float("nan")
+    bad = b.out(T, D)
+    N.SeqGroupNormPlan(len(lens), T, D, D, CODE[bf16], "bwd", ragged=ragged, act=act).backward(
+        x, out["stats"], dy, bad, w=w, b=bias, starts=starts_of(lens) if ragged else None)
+    assert bool(torch.isnan(bad[0, 5])) and int(torch.isnan(bad.float()).sum()) == 1
