@@ -19,7 +19,7 @@
 namespace convfwd {
 namespace {
 
-constexpr int WT = 512;                       // threads that hold lanes: two warps a quarter of the lanes, half of the columns each
+constexpr int WT = 512;                       // threads that hold lanes: four warps a quarter of the lanes, a quarter of the columns each
 constexpr int TPT = 64 * 128 / WT;            // tokens of a chunk a thread holds of its lane
 constexpr int LOADERS = 3;                    // warps behind the first, issuing, one that fetch
 constexpr int WALK_THREADS = WT + 32 * (1 + LOADERS);

@@ -16,7 +16,7 @@ __device__ __forceinline__ uint64_t mn_desc(uint32_t saddr, uint32_t stride) {  
     return d;
 }
 // A wait of a warp for a barrier's phase, for about a second at most.  The limit goes by the SM's clock: reading the global
-// timer between two looks costs more than a hand-off takes (8192 tokens, 32 heads of 128 x 128: the walk took 449 us with it, 335 without).
+// timer between two looks costs more than a hand-off takes (8192 tokens, 32 heads of 128 x 128: the forward walk then took 449 us with it, 249 without).
 constexpr long long WAIT_CYCLES = 2000000000ll;
 // Every lane looks, and the arrivals below are predicated: a branch that only one lane takes costs a few hundred cycles
 // at each hand-off until its warp is together again (2048 x 16 heads: 233 us with them, 184 with the waits alone changed).

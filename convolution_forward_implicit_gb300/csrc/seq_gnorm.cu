@@ -2,8 +2,8 @@
 // cross the whole sequence, so a call reads its rows twice: a pass for the sums of every slab of tokens, a
 // small one that joins them to the groups' statistics (a warp or a block a sequence and group), and one that
 // applies them, last slabs first, so that it finds in L2 what the first pass read last.  32 x 56 x 56 x 512 in bf16 (103 MB) takes 31 and 40 us
-// forward, 47 and 55 backward, 620 MB from and to memory besides what L2 gives, 3.6 TB/s: a block's chain of loads, sums and stores at 8 to 32
-// warps an SM.  16 of them (51 MB, both passes within L2) take 37 us with 21 and 22 of kernels, of which the bytes alone would take 15.
+// forward, 47 and 55 backward, 750 MB from and to memory, 4.3 TB/s: a block's chain of loads, sums and stores at 8 to 32
+// warps an SM.  16 of them (51 MB, both passes within L2) take 37 us (21 and 22 cold), of which the bytes alone would take 15.
 //
 // A slab's statistics are means and sums of squared differences, joined pairwise: M2 = M2a + M2b + d^2 na nb / n.  A thread
 // sums over differences from the first value it meets in a channel; that value is one of the data, so the

@@ -17,6 +17,7 @@
  * Whole sequences are worked on in chunks of 64 tokens: an infinity or NaN in a token may reach
  * every token of its chunk and all later ones of its sequence, in its value head (q, k: in the
  * heads that share them), and nothing else.  g may be minus infinity (the state is dropped).
+ * Where g is above 0 and its sum between two tokens of a chunk passes 80, the results may overflow.
  * Where few heads have long sequences the plan of a forward call cuts the axis (the description
  * has the chunks of a piece): sums are then taken in another order than by a plan of other sizes.
  */
