@@ -15,25 +15,23 @@ __device__ __forceinline__ uint64_t mn_desc(uint32_t saddr, uint32_t stride) {  
     d |= (uint64_t)2 << 61;
     return d;
 }
-// A wait of a warp for a barrier's phase, for about a second at most.  The limit goes by the SM's clock: reading the global
+// A wait of a converged warp for a barrier's phase, for about a second at most.  The limit goes by the SM's clock: reading the global
 // timer between two looks costs more than a hand-off takes (8192 tokens, 32 heads of 128 x 128: the forward walk then took 449 us with it, 249 without).
 constexpr long long WAIT_CYCLES = 2000000000ll;
-// Every lane looks, and the arrivals below are predicated: a branch that only one lane takes costs a few hundred cycles
-// at each hand-off until its warp is together again (2048 x 16 heads: 233 us with them, 184 with the waits alone changed).
+// Every lane looks, and what follows is the warp's decision: lanes that look at once need not see the same, and one that went on
+// alone would leave the others in a vote that it never joins.  The arrivals below are predicated: a branch that only one lane takes costs a few
+// hundred cycles at each hand-off until its warp is together again (2048 x 16 heads: 233 us with them, 184 with the waits alone changed).
 __device__ __forceinline__ bool wait_turn(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned* err) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
     const long long since = clock64();
-    bool ok = true;
-    while (ok && !mbar_try_wait(bar, parity)) {
-        if (*abort_flag) {
-            ok = false;
-        } else if (clock64() - since > WAIT_CYCLES) {
+    while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) {
+        if (__any_sync(0xffffffffu, *abort_flag != 0 || clock64() - since > WAIT_CYCLES)) {
             *abort_flag = 1;
             atomicOr(err, ERR_WAIT_TIMEOUT);
-            ok = false;
+            return false;
         }
     }
-    return __all_sync(0xffffffffu, ok) != 0;
+    return true;
 }
 __device__ __forceinline__ void arrive_once(uint32_t bar) {       // one arrival of a converged warp
     asm volatile(
