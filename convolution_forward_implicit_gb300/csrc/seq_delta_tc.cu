@@ -119,13 +119,12 @@ struct Turns {
     }
     __device__ __forceinline__ bool free(int n) { return n < 2 || wait_turn(empty + 8 * (n & 1), ((n >> 1) & 1) ^ 1, abort_flag, err); }
     __device__ __forceinline__ bool arrived(int n) { return wait_turn(full + 8 * (n & 1), (n >> 1) & 1, abort_flag, err); }
-    // After a wait ran out: copies to shared memory and products that were issued, before it and TMEM go (bounded as well).
-    __device__ __forceinline__ void drain(int stages) {
-        const long long since = clock64();
-        for (int n = 0; n < 2 && n < stages; ++n)         // either phase: the last one that began has ended
-            while (!(mbar_try_wait(full + 8 * n, 0) && !mbar_try_wait(full + 8 * n, 1)) && !(mbar_try_wait(full + 8 * n, 1) && !mbar_try_wait(full + 8 * n, 0)) &&
-                   clock64() - since < WAIT_CYCLES) {
-            }
+    // The issuing threads' last: the copies of the `sent` stages begun (the last two of them), the products committed so far.
+    __device__ __forceinline__ void settle_copies(int sent) const {
+        for (int n = sent > 2 ? sent - 2 : 0; n < sent; ++n) settle(full + 8 * (n & 1), (n >> 1) & 1);
+    }
+    __device__ __forceinline__ void settle_products(int committed) const {
+        if (committed > 0) settle(mma, (committed - 1) & 1);
     }
 };
 
@@ -189,6 +188,7 @@ struct Walk {
     // in copies of 16 bytes.
     __device__ __forceinline__ void load(const SeqDeltaParams& p, bool backward) {
         const int thread = threadIdx.x - 32;
+        int sent = 0;
         for (int i = 0; i < chunks; ++i) {
             const int c = backward ? chunks - 1 - i : i, t = t0 + c * DC;
             const uint32_t to = stage(i), bar = turn.full + 8 * (i & 1);
@@ -197,6 +197,7 @@ struct Walk {
                 mbar_arrive_expect_tx(bar, PLANES + DELTA_FACTORS * 4);
                 bulk_g2s(to + WalkTc<KP>::KQ, reinterpret_cast<const uint8_t*>(p.tri) + at(p, c) * PLANES, PLANES, bar);
                 bulk_g2s(to + WalkTc<KP>::KQ + PLANES, p.rows + at(p, c) * DELTA_ROWS, DELTA_FACTORS * 4, bar);
+                sent = i + 1;
             }
             load_kq<KP, 32 * LOADERS>(to, static_cast<const __nv_bfloat16*>(p.k) + t * p.k_ld + kh * p.Dk, static_cast<const __nv_bfloat16*>(p.q) + t * p.q_ld + kh * p.Dk,
                         p.k_ld, p.q_ld, min(DC, t1 - t), p.Dk, thread);
@@ -206,8 +207,7 @@ struct Walk {
             __syncwarp();
             arrive_once(bar);
         }
-        // after a wait ran out: what was copied to shared memory is waited for (bounded as well)
-        if (thread == 0 && *turn.abort_flag) turn.drain(chunks);
+        if (thread == 0) turn.settle_copies(sent);
     }
     // The thread's values of a chunk's rows of v or dY, as pairs of tokens.  Where rows lie in aligned pairs (`pairs`), an even lane
     // reads its own and its neighbour's column of the first token of each two, an odd one those of the second, and they exchange.
@@ -319,6 +319,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) delta_walk_tc_kernel(const __
         w.load(p, false);
     } else if (w.warp == 0) {                   // the issuing warp (the first: the oldest is served first)
         bool ok = true;
+        int committed = 0;
         for (int c = 0; c < w.chunks && ok; ++c) {
             const uint32_t kq = w.stage(c), tp = kq + W::KQ, acc = w.tmem + W::ACC;
             ok = w.turn.arrived(c) && w.turn.next(w.turn.ready);
@@ -332,6 +333,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) delta_walk_tc_kernel(const __
                 }
                 mma_commit(w.turn.mma);
             }
+            ++committed;
             __syncwarp();
             if (!(ok = w.turn.next(w.turn.ready))) break;
             if (w.lane == 0) {
@@ -341,6 +343,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) delta_walk_tc_kernel(const __
                     steps<4, false>(acc, w.tmem + W::P + (0x481 >> 2 * q & 3) * 32, sw128_desc(tp + (0x604 >> 2 * q & 3) * ATOM), Y && q < 3 ? ID_128 : ID_64, q > 0);
                 mma_commit(w.turn.mma);
             }
+            ++committed;
             __syncwarp();
             if (!(ok = w.turn.next(w.turn.ready))) break;
             if (w.lane == 0) {
@@ -348,8 +351,11 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) delta_walk_tc_kernel(const __
                 for (int pl = 2; pl >= 0; --pl) steps<4, true>(acc, w.tmem + W::P + pl * 32, mn_desc(kq, ATOM), ID_KP, pl < 2);
                 mma_commit(w.turn.mma);
             }
+            ++committed;
             __syncwarp();
         }
+        if (w.lane == 0) w.turn.settle_products(committed);
+        __syncwarp();
     } else {
         float st[HK];                           // of column dv
 #pragma unroll
@@ -501,6 +507,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) delta_back_tc_kernel(const __
         w.load(p, true);
     } else if (w.warp == 0) {                   // the issuing warp (the first: the oldest is served first)
         bool ok = true;
+        int committed = 0;
         for (int s = 0; s < w.chunks && ok; ++s) {
             const uint32_t kq = w.stage(s), tp = kq + W::KQ, acc = w.tmem + B::ACC;
             ok = w.turn.arrived(s) && w.turn.next(w.turn.ready);
@@ -513,6 +520,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) delta_back_tc_kernel(const __
                     steps<4, true>(acc + 64, w.tmem + B::P, mn_desc(tp + pl * ATOM + 8192, ATOM), ID_64 | ACROSS, pl < 2);
                 mma_commit(w.turn.mma);
             }
+            ++committed;
             __syncwarp();
             if (!(ok = w.turn.next(w.turn.ready))) break;
             if (w.lane == 0) {
@@ -522,6 +530,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) delta_back_tc_kernel(const __
                     steps<4, true>(acc, w.tmem + B::P + (0x052 >> 2 * q & 3) * 32, mn_desc(tp + (0x118 >> 2 * q & 3) * ATOM, ATOM), ID_64 | ACROSS, q > 0);
                 mma_commit(w.turn.mma);
             }
+            ++committed;
             __syncwarp();
             if (!(ok = w.turn.next(w.turn.ready))) break;
             if (w.lane == 0) {
@@ -532,8 +541,11 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) delta_back_tc_kernel(const __
                 }
                 mma_commit(w.turn.mma);
             }
+            ++committed;
             __syncwarp();
         }
+        if (w.lane == 0) w.turn.settle_products(committed);
+        __syncwarp();
     } else {
         float st[HK];                           // of column dv: the gradient at the state the chunk leaves
 #pragma unroll

@@ -33,6 +33,13 @@ __device__ __forceinline__ bool wait_turn(uint32_t bar, uint32_t parity, volatil
     }
     return true;
 }
+// By the one thread that issued copies or products, before it ends: the phase that the last of them complete, for about a second
+// at most.  Shared memory and TMEM are then given back with nothing of its own on the way, also after a wait has run out.
+__device__ __forceinline__ void settle(uint32_t bar, uint32_t parity) {
+    const long long since = clock64();
+    while (!mbar_try_wait(bar, parity) && clock64() - since < WAIT_CYCLES) {
+    }
+}
 __device__ __forceinline__ void arrive_once(uint32_t bar) {       // one arrival of a converged warp
     asm volatile(
         "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"

@@ -32,3 +32,10 @@ def test_lanes_leave_a_wait_together(tmp_path):
     out = build(tmp_path, "delta_wait_check", "delta_wait.inc",
                 [cut("seq_delta_tc.cuh", "constexpr long long WAIT_CYCLES", ";\n"), cut("seq_delta_tc.cuh", D + "bool wait_turn(")])
     assert out.returncode == 0 and " 0 wrong" in out.stdout, out.stdout + out.stderr
+
+
+def test_a_walk_ends_with_nothing_on_its_way(tmp_path):
+    out = build(tmp_path, "delta_settle_check", "delta_settle.inc",
+                [cut("seq_delta_tc.cuh", "constexpr long long WAIT_CYCLES", ";\n"), cut("seq_delta_tc.cuh", D + "void settle("),
+                 cut("seq_delta_tc.cu", "struct Turns {", "\n};\n")])
+    assert out.returncode == 0 and " 0 wrong" in out.stdout, out.stdout + out.stderr
