@@ -24,7 +24,7 @@ static int completed(int b) {
     return n;
 }
 static bool mbar_try_wait(uint32_t bar, uint32_t parity) { return (completed(bar / 8) & 1) != (int)parity; }
-static long long clock64() { return now += 1000; }
+static long long clock64() { return now += 20000; }
 static bool wait_turn(uint32_t, uint32_t, volatile int*, unsigned*) { return true; }
 
 #include "delta_settle.inc"
@@ -52,7 +52,7 @@ int main() {
         ++cases;
         const bool all = completed(0) == begun[0] && completed(1) == begun[1] && completed(2) == begun[2];
         const int open = (begun[0] > 0) + (begun[1] > 0) + (begun[2] > 0);
-        if (round % 10 == 9 ? took > open * (WAIT_CYCLES + 10000) : !all || took > 3 * 60000000) ++wrong;
+        if (round % 10 == 9 ? took > open * (WAIT_CYCLES + 40000) : !all || took > 3 * 60000000) ++wrong;
     }
     printf("%d cases, %d wrong\n", cases, wrong);
     return wrong != 0;
