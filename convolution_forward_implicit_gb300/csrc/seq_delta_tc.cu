@@ -9,7 +9,7 @@
 // on, the next one's are on their way.
 //
 // What bounds a walk: the products and the threads' work between them follow one another, three times a chunk.  2048 tokens of 16 heads
-// of 128 x 128 (16 CTAs, 32 chunks in order) take 143 us: 4.5 us a chunk, of which the products are 2 (72 of 44 to 64 cycles);
+// of 128 x 128 (16 CTAs, 32 chunks in order) take 143 us: 4.5 us a chunk, of which the products are 2 (60 of 64 cycles);
 // in five pieces of the axis 35, 20 to join them and 42.
 // 8192 tokens, 32 heads, 4 sequences (128 CTAs) take 184 us, backward 188, where the kernel moves 760 MB, most of it what is saved
 // (61% of copy rate); with mma.sync they took 814 and 776.
@@ -306,8 +306,8 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) delta_walk_tc_kernel(const __
     using W = WalkTc<KP>;
     using T = __nv_bfloat16;
     constexpr int HK = KP * 128 / WT;                  // the thread's rows of the state: cq HK ..
-    constexpr uint32_t ID_64 = idesc_f32acc(128, 64, 1u), ID_128 = idesc_f32acc(128, 128, 1u), ID_KP = idesc_f32acc(128, KP, 1u) | (1u << 16);
     constexpr bool Y = MODE != DELTA_PIECES;           // outputs too
+    constexpr uint32_t ID_ROWS = idesc_f32acc(128, Y ? 128 : 64, 1u), ID_KP = idesc_f32acc(128, KP, 1u) | (1u << 16);
     const WalkPlace place = walk_place<MODE>(p, dvbs, dkbs);
     if (MODE != DELTA_WHOLE) dep_wait();
     if (place.none) return;
@@ -325,22 +325,18 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) delta_walk_tc_kernel(const __
             ok = w.turn.arrived(c) && w.turn.next(w.turn.ready);
             if (!ok) break;
             if (w.lane == 0) {
-                // y needs two parts of h only: the last one goes with K alone
 #pragma unroll 1
-                for (int q = 0; q < 3; ++q) {
-                    const int pl = q == 0 ? 1 : q == 1 ? 0 : 2;
-                    steps<KP / 16, false>(acc, w.tmem + W::H + pl * (KP / 2), sw128_desc(kq), !Y || pl == 2 ? ID_64 : ID_128, q > 0);
-                }
+                for (int pl = 2; pl >= 0; --pl) steps<KP / 16, false>(acc, w.tmem + W::H + pl * (KP / 2), sw128_desc(kq), ID_ROWS, pl < 2);
                 mma_commit(w.turn.mma);
             }
             ++committed;
             __syncwarp();
             if (!(ok = w.turn.next(w.turn.ready))) break;
             if (w.lane == 0) {
-                // U needs six products of parts, y the three large ones: (1, 0), (0, 1), (0, 0), then (2, 0), (0, 2), (1, 1)
+                // the six products of parts, small ones first: (2, 0), (0, 2), (1, 1), (1, 0), (0, 1), (0, 0)
 #pragma unroll 1
                 for (int q = 0; q < 6; ++q)
-                    steps<4, false>(acc, w.tmem + W::P + (0x481 >> 2 * q & 3) * 32, sw128_desc(tp + (0x604 >> 2 * q & 3) * ATOM), Y && q < 3 ? ID_128 : ID_64, q > 0);
+                    steps<4, false>(acc, w.tmem + W::P + (0x052 >> 2 * q & 3) * 32, sw128_desc(tp + (0x118 >> 2 * q & 3) * ATOM), ID_ROWS, q > 0);
                 mma_commit(w.turn.mma);
             }
             ++committed;
