@@ -8,6 +8,10 @@
 //   dK = beta X + Z,   dbeta_i = V_i.dR_i + k_i.X_i
 //   db_i = q_i.dQ_i + beta_i k_i.X_i - k_i.Z_i, and at the chunk's last token exp(b_C) <h0, dh> + sum_j k_j.(exp(b_C - b) U dh^T)_j;
 //   dg is the sum of db from its token on.
+// Two terms of db stand in it twice, with either sign, and are as large as the outputs' gradients, while dg is as small as its factor exp(g):
+// q_i k_i scale dY_i.U_i, in q_i.dQ_i and k_i.Z_i, and the last token's k.(U dh^T), in k.Z and in the sum over j.  They are left out on both sides: with
+// them dg was off by 4e-3 of its terms at g = -12 for all tokens, now by 1e-6 at any.  (What tokens behind a strong decay do among themselves still cancels in
+// that token's dg: it is off by 1e-7 or so of theirs.)
 //
 // Three kernels: the forward pass's first again (T, A, factors of the rows); a walk over the chunks from the last to the
 // first for a block of columns (dV, the gradients of the states); and every chunk by itself for the rest.  In fp32 2 sequences of 1500
@@ -182,6 +186,7 @@ struct GradSmem {
     };
     float2 b[DC];
     float rq[DC], rk[DC], beta[DC], vdr[DC];
+    float qk[DC], own[DC];           // q.k and scale dY.U of a token
     float dots[4][2][DC];            // q.dQ, k.X, k.Z, k.(exp(b_C - b) U dh^T): by the two warps of a row
     float dotq[DC], dotk[DC];        // sums over the value heads
     float hh[DT / 32];
@@ -218,6 +223,18 @@ __global__ void __launch_bounds__(DT, 1) delta_grad_kernel(const __grid_constant
     {
         const float r = p.norm ? row_length<KP, LD>(threadIdx.x < 128 ? s.q : s.k) : 1.f;
         if ((threadIdx.x & 1) == 0) (threadIdx.x < 128 ? s.rq : s.rk)[(threadIdx.x & 127) >> 1] = r;
+    }
+    {
+        const int r = threadIdx.x >> 2;
+        float d = 0.f;
+#pragma unroll 4
+        for (int c = (threadIdx.x & 3) * 2; c < KP; c += 8) {
+            const float2 a = seq_ld2(s.q + r * LD + c), b = seq_ld2(s.k + r * LD + c);
+            d = fmaf(a.x, b.x, fmaf(a.y, b.y, d));
+        }
+        d += __shfl_xor_sync(0xffffffffu, d, 1);
+        d += __shfl_xor_sync(0xffffffffu, d, 2);
+        if ((threadIdx.x & 3) == 0) s.qk[r] = d;
     }
     if (threadIdx.x < DC) s.dotq[threadIdx.x] = s.dotk[threadIdx.x] = 0.f;
     float tq[SHARED ? NT : 1][4], tk[SHARED ? NT : 1][4];
@@ -303,8 +320,9 @@ __global__ void __launch_bounds__(DT, 1) delta_grad_kernel(const __grid_constant
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int j = j0 + 8 * n + t2 + e, o = i * LP + j;
-                    const float E = j <= i ? decay_between(bi, s.b[j]) : 0.f, rkj = s.rk[j];
-                    const float a = j <= i ? p.scale * da[n][2 * half + e] * E : 0.f, l = j < i ? -dl[n][2 * half + e] * E : 0.f;
+                    const float E = j < i ? decay_between(bi, s.b[j]) : 0.f, rkj = s.rk[j];
+                    const float a = j < i ? p.scale * da[n][2 * half + e] * E : 0.f, l = j < i ? -dl[n][2 * half + e] * E : 0.f;
+                    if (j == i) s.own[i] = p.scale * da[n][2 * half + e];
                     s.m[0][o] = a * rkj;
                     s.m[1][o] = a * rqi;
                     s.m[2][o] = l * rkj;
@@ -343,6 +361,20 @@ __global__ void __launch_bounds__(DT, 1) delta_grad_kernel(const __grid_constant
         row_dot(dq, s.q, dot[0]);
         row_dot(x, s.k, dot[1]);
         row_dot(z, s.k, dot[2]);
+        // a token's own term (see above), behind the products for db
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int i = m0 + g + 8 * half;
+            const float own = s.own[i], oq = own * s.rk[i], ok = own * s.rq[i];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const float2 kv = seq_ld2(s.k + i * LD + n0 + 8 * n + t2), qv = seq_ld2(s.q + i * LD + n0 + 8 * n + t2);
+                dq[n][2 * half] = fmaf(oq, kv.x, dq[n][2 * half]);
+                dq[n][2 * half + 1] = fmaf(oq, kv.y, dq[n][2 * half + 1]);
+                z[n][2 * half] = fmaf(ok, qv.x, z[n][2 * half]);
+                z[n][2 * half + 1] = fmaf(ok, qv.y, z[n][2 * half + 1]);
+            }
+        }
 #pragma unroll
         for (int k = 0; k < 4; ++k)
 #pragma unroll
@@ -362,11 +394,13 @@ __global__ void __launch_bounds__(DT, 1) delta_grad_kernel(const __grid_constant
                 const float rq = s.rq[r], rk = s.rk[r], beta = s.beta[r];
                 const float qq = rq * (s.dots[0][0][r] + s.dots[0][1][r]), kx = rk * (s.dots[1][0][r] + s.dots[1][1][r]);
                 const float kz = rk * (s.dots[2][0][r] + s.dots[2][1][r]);
-                total += rk * (s.dots[3][0][r] + s.dots[3][1][r]);
-                db[i] = (double)(qq - kz) + (double)(beta * kx);
+                const float own = s.own[r] * s.qk[r] * rq * rk;
+                const bool end = r == cut.n - 1;             // (no token behind it has a part in its k.Z)
+                total += end ? 0.f : rk * (s.dots[3][0][r] + s.dots[3][1][r]);
+                db[i] = (double)(end ? qq : qq - kz) + (double)(beta * kx);
                 if (r < cut.n) p.dbeta[(cut.t0 + r) * p.dbeta_ld + h] = s.vdr[r] + kx;
-                s.dotq[r] += qq;
-                s.dotk[r] += fmaf(beta, kx, kz);
+                s.dotq[r] += qq + own;
+                s.dotk[r] += fmaf(beta, kx, kz + own);
             }
 #pragma unroll
             for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);

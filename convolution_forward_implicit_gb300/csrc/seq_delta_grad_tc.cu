@@ -2,9 +2,10 @@
 // formulas.  A CTA takes a chunk and a key head, its value heads in turn, and 64 columns of their states at a time.  Rows of
 // the chunk are TMEM lanes, those of dY (and dQ) the first 64, those of dR, U (and X, Z) the others:
 //   D1 = [dY; dR] h0^T     D2 = [dY; dR] U^T     D3 = [.; U] dh^T            over all columns, then with
-//   P = E . dY U^T, S = -E . dR U^T (from D2):
+//   P = E . dY U^T, S = -E . dR U^T (from D2), both below the diagonal:
 //   D4 = [P |k|^-1; S |k|^-1] K                  D5 = [.; (P |q|^-1)^T Q + (S beta |k|^-1)^T K]
-// and dQ = scale exp(b) D1 + scale D4, X = D4 - exp(b) D1, Z = exp(b_C - b) D3 + D5 in the rows of a lane.  Operands that
+// and dQ = scale exp(b) D1 + scale D4, X = D4 - exp(b) D1, Z = exp(b_C - b) D3 + D5 in the rows of a lane, to which P's diagonal adds
+// its multiples of k and q once the products for the decay's gradient are taken.  Operands that
 // are not exact in bf16 are three bf16 parts each (24 bits), written by the threads; products of two such take the six
 // large ones of the parts' nine.
 //
@@ -32,8 +33,8 @@ struct GradTc {
 };
 struct GradRest {
     float2 b[DC];
-    float rq[DC], rk[DC], beta[DC], g[DC], vdr[DC];
-    float dots[4][4][DC];
+    float rq[DC], rk[DC], beta[DC], g[DC], vdr[DC], own[DC];
+    float dots[5][4][DC];            // q.dQ, k.X, k.Z, k.(exp(b_C - b) U dh^T), q.k: by the four warps of a row
     float hh[GT_WARPS];
     int zero[GT_WARPS];
     alignas(8) uint64_t bars[4];
@@ -311,7 +312,8 @@ __global__ void __launch_bounds__(GW, 1) delta_grad_tc_kernel(const __grid_const
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const int j = cq * 16 + half * 8 + e;
-                        const float x = j < i || (j == i && !isk) ? f * __uint_as_float(d[half * 8 + e]) * decay_between(bi, s.b[j]) : 0.f;
+                        const float x = j < i ? f * __uint_as_float(d[half * 8 + e]) * decay_between(bi, s.b[j]) : 0.f;
+                        if (j == i && !isk) s.own[i] = f * __uint_as_float(d[half * 8 + e]);
                         by_key[e] = x * s.rk[j];
                         by_row[e] = x * own;
                     }
@@ -322,8 +324,10 @@ __global__ void __launch_bounds__(GW, 1) delta_grad_tc_kernel(const __grid_const
             }
             tell(ready);
             issue(MATRICES, true);
+            meet();                              // (P's diagonal is there)
             const float eb = expf(bi.x) * (1.f + bi.y), fq = p.scale * eb, fz = decay_between(end, bi);
             wait_e();
+            const float own_f = s.own[i] * (isk ? rqi : rki);
             // ---- rows: dQ (first 64 lanes), X and Z (the others), in pieces of columns (with 16 and the sums of heads registers spill)
             constexpr int PIECE = SHARED ? 8 : 16;
             float dot[3][4] = {};                // (four sums each: their differences make dg)
@@ -337,11 +341,12 @@ __global__ void __launch_bounds__(GW, 1) delta_grad_tc_kernel(const __grid_const
                 lanes_of(lanes + G::D3 + col, d3);
                 lanes_of(lanes + G::D5 + col, d5);
                 const int row = isk ? i : 64 + i;
-                uint32_t w[PIECE / 2];
+                uint32_t w[PIECE / 2], o[PIECE / 2];        // the token's k (or q), and its q (or k)
 #pragma unroll
                 for (int e = 0; e < PIECE; e += 8) {
-                    const uint4 k = piece(row, (col + e) / 8);
+                    const uint4 k = piece(row, (col + e) / 8), q = piece(row ^ 64, (col + e) / 8);
                     w[e / 2] = k.x; w[e / 2 + 1] = k.y; w[e / 2 + 2] = k.z; w[e / 2 + 3] = k.w;
+                    o[e / 2] = q.x; o[e / 2 + 1] = q.y; o[e / 2 + 2] = q.z; o[e / 2 + 3] = q.w;
                 }
                 tmem_ld_wait();
 #pragma unroll
@@ -349,10 +354,13 @@ __global__ void __launch_bounds__(GW, 1) delta_grad_tc_kernel(const __grid_const
                     float lo, hi;
                     bf2_unpack(w[e / 2], lo, hi);
                     const float own = e & 1 ? hi : lo;
+                    bf2_unpack(o[e / 2], lo, hi);
+                    const float other = e & 1 ? hi : lo;
                     float r;
                     if (!isk) {
                         r = fmaf(fq, __uint_as_float(d1[e]), __uint_as_float(d4[e]));
                         dot[0][e & 3] = fmaf(own, r, dot[0][e & 3]);
+                        dot[1][e & 3] = fmaf(own, other, dot[1][e & 3]);
                     } else {
                         const float x = fmaf(-eb, __uint_as_float(d1[e]), __uint_as_float(d4[e])), zu = fz * __uint_as_float(d3[e]);
                         const float z = zu + __uint_as_float(d5[e]);
@@ -361,19 +369,21 @@ __global__ void __launch_bounds__(GW, 1) delta_grad_tc_kernel(const __grid_const
                         dot[2][e & 3] = fmaf(own, zu, dot[2][e & 3]);
                         r = fmaf(beta, x, z);
                     }
+                    r = fmaf(own_f, other, r);
                     if (SHARED) total[SHARED ? c + e : 0] += r;
                     else out[SHARED ? 0 : c + e] = r;
                 }
             }
             if (!isk) {
                 s.dots[0][cq][i] = (dot[0][0] + dot[0][1]) + (dot[0][2] + dot[0][3]);
+                s.dots[4][cq][i] = (dot[1][0] + dot[1][1]) + (dot[1][2] + dot[1][3]);
             } else {
 #pragma unroll
                 for (int k = 0; k < 3; ++k) s.dots[1 + k][cq][i] = (dot[k][0] + dot[k][1]) + (dot[k][2] + dot[k][3]);
             }
             meet();
             auto of = [&](int k, int r) { return (s.dots[k][0][r] + s.dots[k][1][r]) + (s.dots[k][2][r] + s.dots[k][3][r]); };
-            along += isk ? fmaf(beta, rki * of(1, i), rki * of(2, i)) : rqi * of(0, i);
+            along += s.own[i] * rqi * rki * of(4, i) + (isk ? fmaf(beta, rki * of(1, i), rki * of(2, i)) : rqi * of(0, i));
             if (!SHARED || h == (kh + 1) * rep - 1) {
                 // through the lengths: d(k / |k|) = (d - k^ (k^.d)) / |k|; through shared memory, for whole rows: written by
                 // the lanes that hold them, 4 KB apart, they took 180 us of the call's 1390 (8192 tokens, 32 heads)
@@ -422,8 +432,9 @@ __global__ void __launch_bounds__(GW, 1) delta_grad_tc_kernel(const __grid_const
                     const int r = 2 * lane + e;
                     const float rq = s.rq[r], rk = s.rk[r], be = s.beta[r];
                     const float qq = rq * (of(0, r)), kx = rk * (of(1, r));
-                    const float kz = rk * (of(2, r));
-                    sum3 += rk * (of(3, r));
+                    const bool last = r == cut.n - 1;        // (see seq_delta_bwd.cu: without what stands in both sums)
+                    const float kz = last ? 0.f : rk * (of(2, r));
+                    sum3 += last ? 0.f : rk * (of(3, r));
                     db[e] = (double)(qq - kz) + (double)(be * kx);
                     if (r < cut.n) p.dbeta[(cut.t0 + r) * p.dbeta_ld + h] = s.vdr[r] + kx;
                 }
