@@ -366,18 +366,43 @@ __device__ __forceinline__ void join_store(const SeqGnormParams& p, long long at
     reinterpret_cast<float2*>(p.coef)[at] = st;
     if (!BWD && p.stats) reinterpret_cast<float2*>(p.stats)[at] = st;
 }
-// Entries of groups: a block 32 neighbouring groups of a sequence, a warp every eighth slab.  Sums of the differences d from
-// the first slab's mean and of their squares: M2 = sum (M2k + nk d^2) - (sum nk d)^2 / n; the first slab is one of the data, so
-// that this loses about as little as a thread's own sums do.
+// Parts joined.  Forward: number, mean (less the first entry's, `about`) and sum of squared differences of the values in them; of several parts first
+// the mean of all, then M2 = sum (M2k + nk (mean k - mean)^2), whose terms are positive: it keeps its relative accuracy wherever the parts' means
+// lie (sums of d and d^2 about one entry, subtracted at the end, were off by 4e-3 with one channel of 4096 far from the others).  Backward: two sums.
 template <bool BWD>
-__device__ __forceinline__ float2 join_finish(const SeqGnormParams& p, float2 st, float about, float count) {
-    if (BWD) return make_float2(st.x / count, st.y / count);
-    const float shift = st.x / count, var = fmaf(-shift, shift, st.y / count);
-    return make_float2(about + shift, 1.f / sqrtf((var < 0.f ? 0.f : var) + p.eps));
+struct Joined {
+    float n, a, b;
+    __device__ __forceinline__ float2 finish(const SeqGnormParams& p, float about, float count) const {
+        if (BWD) return make_float2(a / count, b / count);
+        return make_float2(about + a, 1.f / sqrtf(b / count + p.eps));
+    }
+};
+// `each` calls its argument with (n, a, b) of every part; forward twice.
+template <bool BWD, typename Each>
+__device__ __forceinline__ Joined<BWD> joined_of(Each each) {
+    Joined<BWD> s = {};
+    if (BWD) {
+        each([&](float, float a, float b) {
+            s.a += a;
+            s.b += b;
+        });
+        return s;
+    }
+    each([&](float n, float a, float) {
+        s.n += n;
+        s.a = fmaf(n, a, s.a);
+    });
+    s.a = s.n > 0.f ? s.a / s.n : 0.f;
+    each([&](float n, float a, float b) {
+        const float d = a - s.a;
+        s.b += fmaf(n * d, d, b);
+    });
+    return s;
 }
+// Entries of groups: a block 32 neighbouring groups of a sequence, a warp every eighth slab.
 template <bool BWD>
 __global__ void __launch_bounds__(GT) gn_join_groups_kernel(const __grid_constant__ SeqGnormParams p, int blocks) {
-    __shared__ float2 buf[GT];
+    __shared__ Joined<BWD> buf[GT];
     const int s = blockIdx.x / blocks, gi = (blockIdx.x - s * blocks) * 32 + (threadIdx.x & 31), cpg = p.D / p.G;
     const int t0 = p.ax.L > 0 ? s * p.ax.L : seq_start(p.ax, s, 0), t1 = p.ax.L > 0 ? t0 + p.ax.L : seq_start(p.ax, s + 1, t0);
     const int len = t1 - t0, slabs = (len + p.slab - 1) / p.slab;
@@ -385,32 +410,28 @@ __global__ void __launch_bounds__(GT) gn_join_groups_kernel(const __grid_constan
     const float tokens = (float)p.slab * (float)cpg, rest = (float)(len - (slabs - 1) * p.slab) * (float)cpg, count = (float)len * (float)cpg;
     launch_next();
     wait_before();
-    float2 st = dup(0.f);
     const float about = !BWD && gi < p.G && len > 0 ? from[0].x : 0.f;
-    if (gi < p.G)
+    buf[threadIdx.x] = joined_of<BWD>([&](auto part) {
+        if (gi < p.G)
 #pragma unroll 4
-        for (int k = threadIdx.x >> 5; k < slabs; k += GT / 32) {
-            const float2 v = from[(long long)k * p.G];
-            if (BWD) {
-                st = add2(st, v);
-            } else {
-                const float d = v.x - about, n = k == slabs - 1 ? rest : tokens;
-                st.x = fmaf(n, d, st.x);
-                st.y += fmaf(n * d, d, v.y);
+            for (int k = threadIdx.x >> 5; k < slabs; k += GT / 32) {
+                const float2 v = from[(long long)k * p.G];
+                part(k == slabs - 1 ? rest : tokens, v.x - about, v.y);
             }
-        }
-    buf[threadIdx.x] = st;
+    });
     __syncthreads();
     if (threadIdx.x < 32 && gi < p.G) {
+        const Joined<BWD> st = joined_of<BWD>([&](auto part) {
 #pragma unroll
-        for (int w = 1; w < GT / 32; ++w) st = add2(st, buf[w * 32 + threadIdx.x]);
-        join_store<BWD>(p, (long long)s * p.G + gi, len > 0 ? join_finish<BWD>(p, st, about, count) : dup(0.f));
+            for (int w = 0; w < GT / 32; ++w) part(buf[w * 32 + threadIdx.x].n, buf[w * 32 + threadIdx.x].a, buf[w * 32 + threadIdx.x].b);
+        });
+        join_store<BWD>(p, (long long)s * p.G + gi, len > 0 ? st.finish(p, about, count) : dup(0.f));
     }
 }
 // Entries of channels (groups so wide that they lie in several blocks of the sums): a block a sequence and group.
 template <typename T, bool BWD>
 __global__ void __launch_bounds__(GT) gn_join_channels_kernel(const __grid_constant__ SeqGnormParams p) {
-    __shared__ float2 buf[GT / 32];
+    __shared__ Joined<BWD> buf[GT];
     const long long at = blockIdx.x;
     const int s = (int)(at / p.G), gi = (int)(at - (long long)s * p.G), cpg = p.D / p.G;
     const int t0 = p.ax.L > 0 ? s * p.ax.L : seq_start(p.ax, s, 0), t1 = p.ax.L > 0 ? t0 + p.ax.L : seq_start(p.ax, s + 1, t0);
@@ -421,29 +442,29 @@ __global__ void __launch_bounds__(GT) gn_join_channels_kernel(const __grid_const
     launch_next();
     wait_before();
     const float about = !BWD && len > 0 ? from[0].x : 0.f;
-    float2 st = dup(0.f);
-    for (int c = threadIdx.x; c < cpg; c += GT) {
-        const float wc = w ? seq_ld(w + gi * cpg + c) : 1.f;
+    buf[threadIdx.x] = joined_of<BWD>([&](auto part) {
+        for (int c = threadIdx.x; c < cpg; c += GT) {
+            const float wc = w ? seq_ld(w + gi * cpg + c) : 1.f;
 #pragma unroll 4
-        for (int k = 0; k < slabs; ++k) {
-            const float2 v = from[(long long)k * p.D + c];
-            if (BWD) {
-                st = fma2(dup(wc), v, st);
-            } else {
-                const float d = v.x - about, n = k == slabs - 1 ? rest : tokens;
-                st.x = fmaf(n, d, st.x);
-                st.y += fmaf(n * d, d, v.y);
+            for (int k = 0; k < slabs; ++k) {
+                const float2 v = from[(long long)k * p.D + c];
+                part(k == slabs - 1 ? rest : tokens, BWD ? wc * v.x : v.x - about, BWD ? wc * v.y : v.y);
             }
         }
-    }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) st = add2(st, make_float2(__shfl_xor_sync(0xffffffffu, st.x, d), __shfl_xor_sync(0xffffffffu, st.y, d)));
-    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = st;
+    });
     __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int i = 1; i < GT / 32; ++i) st = add2(st, buf[i]);
-        join_store<BWD>(p, at, len > 0 ? join_finish<BWD>(p, st, about, count) : dup(0.f));
-    }
+    // 256 parts to 32, to one
+    auto fold = [&](int parts, int step) {
+        return joined_of<BWD>([&](auto part) {
+            for (int i = threadIdx.x; i < parts; i += step) part(buf[i].n, buf[i].a, buf[i].b);
+        });
+    };
+    if (threadIdx.x >= 32) return;
+    const Joined<BWD> st = fold(GT, 32);
+    __syncwarp();
+    buf[threadIdx.x] = st;
+    __syncwarp();
+    if (threadIdx.x == 0) join_store<BWD>(p, at, len > 0 ? fold(32, 1).finish(p, about, count) : dup(0.f));
 }
 
 // dw and db: the slabs' sums of all sequences in order.  It runs beside the kernel before it in the stream, which lets it go
@@ -459,38 +480,49 @@ __global__ void __launch_bounds__(COLUMN_THREADS, 2) gn_param_kernel(const __gri
     wait_before();                  // (so that what follows in the stream follows the kernel before, too)
 }
 
-// The same by every block for its own channels: `groups` of a sequence from g0 on, to `to` (shared memory; `buf`: a float2 a thread).
+// The same by every block for its own channels: `groups` of a sequence from g0 on, to `to` (shared memory; `buf`: an entry a thread).
 template <bool BWD>
-__device__ __forceinline__ void join_groups(const SeqGnormParams& p, const CutPiece& cut, int g0, int groups, float2* to, float2* buf) {
+__device__ __forceinline__ void join_groups(const SeqGnormParams& p, const CutPiece& cut, int g0, int groups, float2* to, Joined<BWD>* buf) {
     const int parts = blockDim.x / groups, gi = threadIdx.x % groups, k0 = threadIdx.x / groups, cpg = p.D / p.G;
     const int t0 = cut.t0 - cut.index * p.slab, t1 = p.ax.L > 0 ? t0 + p.ax.L : seq_start(p.ax, cut.s + 1, t0);
     const int len = t1 - t0, slabs = (len + p.slab - 1) / p.slab;
     const float2* from = reinterpret_cast<const float2*>(p.gpart) + (long long)cut_base(p.ax, cut.s, p.slab) * p.G + g0 + gi;
     const float tokens = (float)p.slab * (float)cpg, rest = (float)(len - (slabs - 1) * p.slab) * (float)cpg, count = (float)len * (float)cpg;
-    float2 st = dup(0.f);
+    // A thread's 16 or so in one pass, as differences from its first: what subtracting their mean loses goes with their number.
     float about = 0.f;
     if (k0 < parts) {
         if (!BWD) about = from[0].x;
+        const float first = !BWD && k0 < slabs ? from[(long long)k0 * p.G].x : 0.f;
+        Joined<BWD> st = {};
 #pragma unroll 4
         for (int k = k0; k < slabs; k += parts) {
             const float2 v = from[(long long)k * p.G];
             if (BWD) {
-                st = add2(st, v);
+                st.a += v.x;
+                st.b += v.y;
             } else {
-                const float d = v.x - about, n = k == slabs - 1 ? rest : tokens;
-                st.x = fmaf(n, d, st.x);
-                st.y += fmaf(n * d, d, v.y);
+                const float d = v.x - first, n = k == slabs - 1 ? rest : tokens;
+                st.n += n;
+                st.a = fmaf(n, d, st.a);
+                st.b += fmaf(n * d, d, v.y);
             }
+        }
+        if (!BWD && st.n > 0.f) {
+            const float mean = st.a / st.n, m2 = fmaf(-st.a, mean, st.b);
+            st.b = m2 < 0.f ? 0.f : m2;
+            st.a = (first - about) + mean;
         }
         buf[threadIdx.x] = st;
     }
     __syncthreads();
     if (threadIdx.x < groups) {
-        st = buf[threadIdx.x];
-        for (int k = 1; k < parts; ++k) st = add2(st, buf[k * groups + threadIdx.x]);
-        st = join_finish<BWD>(p, st, about, count);
-        if (!BWD && p.stats && cut.index == 0) reinterpret_cast<float2*>(p.stats)[(long long)cut.s * p.G + g0 + threadIdx.x] = st;
-        to[threadIdx.x] = st;
+        const Joined<BWD> st = joined_of<BWD>([&](auto part) {
+#pragma unroll 4
+            for (int k = 0; k < parts; ++k) part(buf[k * groups + threadIdx.x].n, buf[k * groups + threadIdx.x].a, buf[k * groups + threadIdx.x].b);
+        });
+        const float2 all = st.finish(p, about, count);
+        if (!BWD && p.stats && cut.index == 0) reinterpret_cast<float2*>(p.stats)[(long long)cut.s * p.G + g0 + threadIdx.x] = all;
+        to[threadIdx.x] = all;
     }
     __syncthreads();
 }
@@ -499,7 +531,8 @@ __device__ __forceinline__ void join_groups(const SeqGnormParams& p, const CutPi
 template <typename T, int V, bool BWD, int ACT, bool SELF>
 __global__ void __launch_bounds__(GT, gn_blocks(BWD, sizeof(T))) gn_apply_kernel(const __grid_constant__ SeqGnormParams p, int txn, int tyn) {
     constexpr int P = Raw<T, V>::P, N = BWD ? AHEAD_BWD : AHEAD;
-    __shared__ float2 joined[SELF ? GT : 1], buf[SELF ? GT : 1];
+    __shared__ float2 joined[SELF ? GT : 1];
+    __shared__ Joined<BWD> buf[SELF ? GT : 1];
     const CutPiece cut = cut_piece(p.ax, gridDim.x - 1 - blockIdx.x, p.slab);
     const GnPlace at(V, p.D, txn);
     const bool on = at.on && at.ty < tyn && at.ty < cut.n;
