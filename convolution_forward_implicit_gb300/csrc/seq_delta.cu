@@ -442,7 +442,9 @@ cudaError_t launch_chunks(const SeqDeltaParams& p, cudaStream_t stream) {
 }
 
 // The states that the pieces of a sequence start from, 16 columns of a value head a block: h <- through h + added from piece to piece, the
-// next piece's matrix and this one's sums on their way during the products.
+// next piece's matrix and this one's sums on their way during the products.  A matrix of a piece over which states grow (keys longer than 1, g above
+// 0) may hold what is beyond fp32's range; where the state is zero nothing of it passes on, as in a walk: results that are not finite are taken
+// again, without the products of zeros.
 template <int KP>
 struct JoinSmem {
     static constexpr int LP = KP + 8, LV = 20;
@@ -497,6 +499,22 @@ __global__ void __launch_bounds__(DT) delta_join_kernel(const __grid_constant__ 
                 more[j][e] = r < p.Dk && c < p.Dvp ? p.added[(rows_of(i) + r) * p.Dvp + c] : 0.f;
             }
         warp_mma<NT>(acc, Along<float>{s.m[i & 1], LP}, Across<float>{s.h[(i - 1) & 1], LV}, m0, n0, 0, KP);
+        bool finite = true;
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) finite = finite && isfinite(acc[j][e]);
+        if (!finite) {
+            for (int j = 0; j < NT; ++j)
+                for (int e = 0; e < 4; ++e) {
+                    const float* m = s.m[i & 1] + (m0 + g + (e >> 1) * 8) * LP;
+                    const float* h = s.h[(i - 1) & 1] + n0 + 8 * j + t2 + (e & 1);
+                    float v = 0.f;
+                    for (int k = 0; k < KP; ++k)
+                        if (h[k * LV] != 0.f) v = fmaf(m[k], h[k * LV], v);
+                    acc[j][e] = v;
+                }
+        }
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
