@@ -258,8 +258,8 @@ __global__ void __launch_bounds__(DT) delta_walk_kernel(const __grid_constant__ 
     if (w.none) return;
     const int h = w.h, c0 = w.dvb * DVB, kh = h / (p.Hv / p.Hk), t0 = w.t0, t1 = w.t1, chunks = w.chunks, slot0 = w.slot0;
     const long long row = seq_slot(p.sl, w.seq), state = (row * p.Hv + h) * (long long)p.Dk * p.Dv;
-    const long long kept = ((long long)w.piece * p.Hv + h) * p.Dk;            // rows of what is kept by piece
-    const bool joined = MODE == DELTA_JOINED && !(w.first && w.last);
+    const long long kept = ((long long)w.mark * p.Hv + h) * p.Dk;             // rows of what is kept by piece
+    const float* from = MODE == DELTA_JOINED && !(w.first && w.last) ? (w.first ? p.added : p.left) + kept * p.Dvp : nullptr;
     float* saved = MODE == DELTA_PIECES ? nullptr : p.saved;
     const int Dv = w.unit ? 0 : p.Dv;
     // the state in the layout of a product's sums: rows 16 (warp MT + m) + g and + 8, columns c0 + 8 n + t2 and + 1
@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(DT) delta_walk_kernel(const __grid_constant__ 
                 st[m][n][e] = 0.f;
                 if (warp < 4 && r < p.Dk) {
                     if (w.unit) st[m][n][e] = r == c ? 1.f : 0.f;
-                    else if (joined) st[m][n][e] = c < p.Dvp ? p.start[(kept + r) * p.Dvp + c] : 0.f;
+                    else if (from) st[m][n][e] = c < p.Dvp ? from[(long long)r * p.Dvp + c] : 0.f;
                     else if ((MODE != DELTA_PIECES || w.first) && p.h_in && row >= 0 && c < p.Dv) st[m][n][e] = p.h_in[state + (long long)r * p.Dv + c];
                 }
             }
@@ -441,7 +441,7 @@ cudaError_t launch_chunks(const SeqDeltaParams& p, cudaStream_t stream) {
     return launch_kernel(delta_chunk_kernel<T, KP>, dim3((unsigned)p.slots, (unsigned)p.Hk), dim3(DT), smem, stream, false, 1, p);
 }
 
-// The states that the pieces of a sequence start from, 16 columns of a value head a block: h <- through h + added from piece to piece, the
+// The states that the pieces of a sequence leave, but for the last, 16 columns of a value head a block: h <- through h + added from piece to piece, the
 // next piece's matrix and this one's sums on their way during the products.  A matrix of a piece over which states grow (keys longer than 1, g above
 // 0) may hold what is beyond fp32's range; where the state is zero nothing of it passes on, as in a walk: results that are not finite are taken
 // again, without the products of zeros.
@@ -457,12 +457,19 @@ __global__ void __launch_bounds__(DT) delta_join_kernel(const __grid_constant__ 
     Smem& s = *reinterpret_cast<Smem*>(raw);
     constexpr int LP = Smem::LP, LV = Smem::LV, NT = KP / 64;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t2 = (lane & 3) * 2;
-    const int c0 = blockIdx.x % cols * 16, sh = blockIdx.x / cols, h = sh % p.Hv, seq = sh / p.Hv, per = p.run * DC;
+    const int c0 = blockIdx.x % cols * 16, sh = blockIdx.x / cols, h = sh % p.Hv, at = sh / p.Hv, len = p.run * DC;
+    int seq = at;
+    bool first = true;
+    if (p.ax.S > p.marks) {              // by the marks of first pieces, where those are fewer
+        const MarkPiece c = mark_piece(p.ax, at, len);
+        first = c.index == 0;
+        seq = c.s;
+    }
     const int t0 = p.ax.L > 0 ? seq * p.ax.L : seq_start(p.ax, seq, 0), t1 = p.ax.L > 0 ? t0 + p.ax.L : seq_start(p.ax, seq + 1, t0);
-    const int n = (t1 - t0 + per - 1) / per;
+    const int n = (t1 - t0 + len - 1) / len;
     dep_wait();
-    if (n < 2) return;
-    const int base = cut_base(p.ax, seq, per);
+    if (n < 2 || !first) return;
+    const int base = first_mark(t0, len);
     const long long row = seq_slot(p.sl, seq), state = (row * p.Hv + h) * (long long)p.Dk * p.Dv;
     auto rows_of = [&](int i) { return ((long long)(base + i) * p.Hv + h) * p.Dk; };
     auto load = [&](int i) {             // the matrix of piece i
@@ -480,8 +487,8 @@ __global__ void __launch_bounds__(DT) delta_join_kernel(const __grid_constant__ 
         const float v = on ? p.added[(rows_of(0) + r) * p.Dvp + c] : 0.f;
         s.h[0][r * LV + e % 16] = v;
         if (on) {
-            p.start[(rows_of(0) + r) * p.Dvp + c] = p.h_in && row >= 0 && c < p.Dv ? p.h_in[state + (long long)r * p.Dv + c] : 0.f;
-            p.start[(rows_of(1) + r) * p.Dvp + c] = v;
+            p.left[(rows_of(0) + r) * p.Dvp + c] = v;
+            p.added[(rows_of(0) + r) * p.Dvp + c] = p.h_in && row >= 0 && c < p.Dv ? p.h_in[state + (long long)r * p.Dv + c] : 0.f;
         }
     }
     const int m0 = warp % (KP / 16) * 16, n0 = warp / (KP / 16) * 8;
@@ -523,7 +530,7 @@ __global__ void __launch_bounds__(DT) delta_join_kernel(const __grid_constant__ 
                 const bool on = r < p.Dk && c < p.Dvp;
                 const float v = on ? acc[j][e] + more[j][e] : 0.f;
                 s.h[i & 1][r * LV + cl] = v;
-                if (on) p.start[(rows_of(i + 1) + r) * p.Dvp + c] = v;
+                if (on) p.left[(rows_of(i) + r) * p.Dvp + c] = v;
             }
     }
     copies_wait<0>();
@@ -534,7 +541,7 @@ cudaError_t launch_join(const SeqDeltaParams& p, cudaStream_t stream) {
     cudaError_t e = cudaFuncSetAttribute(delta_join_kernel<KP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int cols = (p.Dv + 15) / 16;
-    return launch_kernel(delta_join_kernel<KP>, dim3((unsigned)(p.ax.S * (long long)p.Hv * cols)), dim3(DT), smem, stream, true, 1, p, cols);
+    return launch_kernel(delta_join_kernel<KP>, dim3((unsigned)(delta_joined(p.ax.S, p.marks) * p.Hv * cols)), dim3(DT), smem, stream, true, 1, p, cols);
 }
 
 template <typename T, int KP, int DVB, int MODE>
@@ -543,7 +550,7 @@ cudaError_t launch_mode(const SeqDeltaParams& p, cudaStream_t stream) {
     cudaError_t e = cudaFuncSetAttribute(delta_walk_kernel<T, KP, DVB, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int dvbs = (p.Dv + DVB - 1) / DVB, dkbs = (p.Dk + DVB - 1) / DVB;
-    const long long blocks = (MODE == DELTA_WHOLE ? p.ax.S : p.pieces) * (long long)p.Hv * (MODE == DELTA_PIECES ? dvbs + dkbs : dvbs);
+    const long long blocks = (MODE == DELTA_WHOLE ? p.ax.S : MODE == DELTA_PIECES ? p.marks : p.pieces) * (long long)p.Hv * (MODE == DELTA_PIECES ? dvbs + dkbs : dvbs);
     return launch_kernel(delta_walk_kernel<T, KP, DVB, MODE>, dim3((unsigned)blocks), dim3(DT), smem, stream, p.slots > 0, 1, p, dvbs, dkbs);
 }
 template <typename T, int KP, int DVB>

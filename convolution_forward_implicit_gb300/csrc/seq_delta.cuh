@@ -212,38 +212,78 @@ __device__ __forceinline__ void store_pair(T* at, int c, int width, bool pair, f
 // With few heads the chunks of a long sequence in order leave most SMs without work.  Its axis is then cut into pieces of p.run chunks, whose walks
 // are: what a piece adds to a state (from zero; the first piece: from the sequence's state), and, as its columns, what becomes of the unit
 // matrix with v = 0 (DELTA_PIECES, the last piece of a sequence needs neither); h = through h + added from piece to piece gives the states
-// they start from (delta_join_kernel); and the walks themselves from these (DELTA_JOINED).
+// that they leave (delta_join_kernel); and the walks themselves from these (DELTA_JOINED).  The first of several starts from a copy of the
+// sequence's state, which the joining puts where what the piece adds has been: the last one may be writing the state in its place.
+// The piece whose mark is token m * len (see delta_marks): its sequence, index in it, and first token; `t1`: the sequence's end.
+struct MarkPiece {
+    int s, index, t0, t1;
+};
+__device__ __forceinline__ MarkPiece mark_piece(const SeqAxis& a, int m, int len) {
+    const int t = m * len;           // (a token: below T)
+    MarkPiece c;
+    if (a.L > 0) {
+        c.s = t / a.L;
+    } else {
+        int lo = 0, hi = a.S - 1;    // the last sequence that begins at or before the mark
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (seq_start(a, mid, 0) <= t) lo = mid; else hi = mid - 1;
+        }
+        c.s = lo;
+    }
+    const int begin = seq_start(a, c.s, 0);
+    c.t1 = seq_start(a, c.s + 1, begin);
+    c.index = t > begin ? (t - begin) / len : 0;
+    c.t0 = begin + c.index * len;
+    return c;
+}
+// The mark of the first piece of a sequence that begins at t0.
+__device__ __forceinline__ int first_mark(int t0, int len) { return (int)(((long long)t0 + len - 1) / len); }
 struct WalkPlace {
-    int h, seq, dvb, t0, t1, chunks, slot0, piece;
+    int h, seq, dvb, t0, t1, chunks, slot0;
+    int mark;                        // of the piece, or (DELTA_JOINED, but for the first) of the one before it
     bool first, last, unit;          // piece of its sequence; columns of the unit matrix
     bool none;                       // nothing to do
 };
 template <int MODE>
 __device__ __forceinline__ WalkPlace walk_place(const SeqDeltaParams& p, int dvbs, int dkbs) {
     WalkPlace w;
-    const int per = MODE == DELTA_PIECES ? dvbs + dkbs : dvbs, sh = blockIdx.x / per;
+    const int per = MODE == DELTA_PIECES ? dvbs + dkbs : dvbs, sh = blockIdx.x / per, piece = sh / p.Hv;
     w.dvb = blockIdx.x % per;
     w.unit = MODE == DELTA_PIECES && w.dvb >= dvbs;
     if (w.unit) w.dvb -= dvbs;
     w.h = sh % p.Hv;
-    w.piece = sh / p.Hv;
+    w.mark = 0;
     if (MODE == DELTA_WHOLE) {
-        w.seq = w.piece;
+        w.seq = piece;
         w.t0 = p.ax.L > 0 ? w.seq * p.ax.L : seq_start(p.ax, w.seq, 0);
         w.t1 = p.ax.L > 0 ? w.t0 + p.ax.L : seq_start(p.ax, w.seq + 1, w.t0);
         w.slot0 = cut_base(p.ax, w.seq, DC);
         w.first = w.last = true;
         w.none = false;
+    } else if (MODE == DELTA_PIECES) {
+        const int len = p.run * DC;
+        const MarkPiece c = mark_piece(p.ax, piece, len);
+        w.seq = c.s;
+        w.mark = piece;
+        w.t0 = c.t0;
+        w.t1 = c.t0 + len;
+        w.slot0 = cut_base(p.ax, w.seq, DC) + c.index * p.run;
+        w.first = c.index == 0;
+        w.last = w.t1 >= c.t1;
+        w.none = w.last || (w.unit && w.first);
     } else {
-        const CutPiece c = cut_piece(p.ax, w.piece, p.run * DC);
+        const int len = p.run * DC;
+        const CutPiece c = cut_piece(p.ax, piece, len);
         w.seq = c.s;
         w.t0 = c.t0;
         w.t1 = c.t0 + max(c.n, 0);
         w.slot0 = cut_base(p.ax, w.seq, DC) + c.index * p.run;
         w.first = c.index == 0;
-        const int end = p.ax.L > 0 ? (w.seq + 1) * p.ax.L : seq_start(p.ax, w.seq + 1, seq_start(p.ax, w.seq, 0));
-        w.last = w.t1 >= end;
-        w.none = (c.n <= 0 && !w.first) || (MODE == DELTA_PIECES && (w.last || (w.unit && w.first)));
+        const int begin = seq_start(p.ax, w.seq, 0);
+        w.last = w.t1 >= seq_start(p.ax, w.seq + 1, begin);
+        w.none = c.n <= 0 && !w.first;
+        w.mark = first_mark(begin, len) + max(c.index - 1, 0);
     }
     w.chunks = (w.t1 - w.t0 + DC - 1) / DC;
     return w;

@@ -19,25 +19,35 @@ size_t state_bytes(const seq_plan* p) { return align256((size_t)p->slots * p->Hv
 size_t token_bytes(const seq_plan* p) { return align256((size_t)p->slots * p->Hv * DELTA_CHUNK * padded(p) * sizeof(float)); }
 
 int padded_keys(const seq_plan* p) { return (p->N + 3) / 4 * 4; }
-size_t piece_bytes(const seq_plan* p) { return align256((size_t)p->pieces * p->Hv * p->N * padded(p) * sizeof(float)); }
-size_t through_bytes(const seq_plan* p) { return align256((size_t)p->pieces * p->Hv * p->N * padded_keys(p) * sizeof(float)); }
+size_t marks(const seq_plan* p) { return p->run ? (size_t)delta_marks(p->T, p->run) : 0; }
+size_t piece_bytes(const seq_plan* p) { return align256(marks(p) * p->Hv * p->N * padded(p) * sizeof(float)); }
+size_t through_bytes(const seq_plan* p) { return align256(marks(p) * p->Hv * p->N * padded_keys(p) * sizeof(float)); }
 
 // Chunks of a piece of the axis (0: it is not cut), by times in chunks (4 to 5 us): a walk takes 2 more to begin; pieces walk at once, but
 // twice, the first time also with the columns of a unit matrix (without outputs: 0.8 of it); their states are joined in order (0.7
-// a piece); launches 3.  It has to promise a fifth; without lengths, where the longest sequence is taken to hold all tokens, two.
-// 2048 tokens, 16 heads of 128 x 128 bf16: 117 us cut, 174 not; 13 sequences, 6011 tokens, 32 heads: 498 cut (in pieces of 16), 364 not.
+// a piece); launches 3.  It has to promise a fifth.  Of lengths that the plan does not know the longest is taken to be four times the mean, three
+// quarters of all tokens at most; beside it the others' blocks (2 chunks to begin, half a chunk at the end) fill the SMs.
+// 2048 tokens, 16 heads of 128 x 128 bf16: 117 us cut, 174 not; 13 sequences, 6011 tokens, 32 heads: 498 cut (in pieces of 16), 364 not;
+// 64 and 256 sequences of 64 tokens by their bounds, 8 heads: 125 and 471 when only their tokens counted and the plan cut, 77 and 295 now.
 int choose_run(const seq_plan* p) {
-    const bool wide = p->dtype == CONV_BF16 && p->W > 16;
-    const int64_t width = wide ? 128 : 16, cap = wide ? p->sms : 2 * (int64_t)p->sms;
-    const int64_t dv = (p->W + width - 1) / width, dk = (p->N + width - 1) / width, S = p->L > 0 ? p->S : 1;
-    const int64_t n = ((p->L > 0 ? p->L : p->T) + DELTA_CHUNK - 1) / DELTA_CHUNK;
+    const bool wide = p->dtype == CONV_BF16 && p->W > 16, known = p->L > 0 || p->S == 1;
+    const int64_t width = wide ? 128 : 16, cap = wide ? p->sms : 2 * (int64_t)p->sms, S = p->S, T = p->T;
+    const int64_t dv = (p->W + width - 1) / width, dk = (p->N + width - 1) / width, cols = (p->W + 15) / 16;
+    const int64_t longest = known ? T / S : 4 * T / S < 3 * T / 4 ? 4 * T / S : 3 * T / 4, alike = known ? S : 1;
+    const int64_t n = (longest + DELTA_CHUNK - 1) / DELTA_CHUNK;
     auto rounds = [&](int64_t blocks) { return (double)((blocks + cap - 1) / cap); };
-    double best = (p->L > 0 ? 0.8 : 0.6) * (n + 2) * rounds(S * p->Hv * dv);
+    // the longest sequences' blocks, and those of all (unknown lengths) with `more` that begin, in chunks
+    auto walk = [&](double time, int64_t blocks, int64_t more) {
+        const double own = time * rounds(blocks * p->Hv * dv), all = known ? 0 : ((double)T / DELTA_CHUNK + 2.5 * (S + more)) * p->Hv * dv / cap;
+        return own > all ? own : all;
+    };
+    double best = 0.8 * walk(n + 2, alike, 0);
     int run = 0;
     for (int64_t r = 2; r <= n / 2; r += 1 + r / 16) {
-        const int64_t m = (n + r - 1) / r;
-        const double t = (r + 2) * (rounds(S * m * p->Hv * dv) + 0.8 * rounds(S * (m - 1) * p->Hv * (dv + dk))) + 0.7 * (m - 2) * rounds(S * p->Hv * ((p->W + 15) / 16)) + 3;
-        if (t < best && cut_slots(p->S, p->T, p->L, (int)(r * DELTA_CHUNK)) * p->Hv * (dv + dk) < (1 << 24)) {
+        const int64_t m = (n + r - 1) / r, marks = delta_marks(T, (int)r);
+        const double t = 0.8 * (r + 2) * rounds((known ? S * (m - 1) : marks - 1) * p->Hv * (dv + dk)) + walk(r + 2, alike * m, marks) +
+                         0.7 * (m - 2) * rounds(alike * p->Hv * cols) + (known ? 0 : 0.2 * rounds(delta_joined(S, marks) * p->Hv * cols)) + 3;
+        if (t < best && cut_slots(S, T, p->L, (int)(r * DELTA_CHUNK)) * p->Hv * (dv + dk) < (1 << 24)) {
             best = t;
             run = (int)r;
         }
@@ -132,10 +142,10 @@ static conv_status delta_call(seq_plan_t p, const seq_delta_args* a, seq_directi
         q.tri = reinterpret_cast<float*>(w);
         q.rows = reinterpret_cast<float*>(w + tri_bytes(p));
         if (dir == SEQ_FWD) {
-            q.run = p->run; q.pieces = p->pieces; q.Dkp = padded_keys(p);
+            q.run = p->run; q.pieces = p->pieces; q.marks = (int)marks(p); q.Dkp = padded_keys(p);
             q.added = reinterpret_cast<float*>(w + tri_bytes(p) + row_bytes(p));
-            q.start = q.added + piece_bytes(p) / sizeof(float);
-            q.through = q.start + piece_bytes(p) / sizeof(float);
+            q.left = q.added + piece_bytes(p) / sizeof(float);
+            q.through = q.left + piece_bytes(p) / sizeof(float);
         }
         q.dstate = reinterpret_cast<float*>(w + tri_bytes(p) + row_bytes(p));
         q.dr = reinterpret_cast<float*>(w + tri_bytes(p) + row_bytes(p) + state_bytes(p));

@@ -312,8 +312,8 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) delta_walk_tc_kernel(const __
     if (MODE != DELTA_WHOLE) dep_wait();
     if (place.none) return;
     Walk<KP> w(p, place, err, smem_raw);
-    const long long kept = ((long long)place.piece * p.Hv + place.h) * p.Dk;       // rows of what is kept by piece
-    const bool joined = MODE == DELTA_JOINED && !(place.first && place.last);
+    const long long kept = ((long long)place.mark * p.Hv + place.h) * p.Dk;        // rows of what is kept by piece
+    const float* from = MODE == DELTA_JOINED && !(place.first && place.last) ? (place.first ? p.added : p.left) + kept * p.Dvp : nullptr;
     if (w.warp > 0 && w.warp <= LOADERS) {
         dep_wait();
         w.load(p, false);
@@ -359,7 +359,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) delta_walk_tc_kernel(const __
             const int r = w.cq * HK + i;
             st[i] = 0.f;
             if (place.unit) st[i] = r == w.dv && r < p.Dk ? 1.f : 0.f;
-            else if (joined) st[i] = w.dv < p.Dvp && r < p.Dk ? p.start[(kept + r) * p.Dvp + w.dv] : 0.f;
+            else if (from) st[i] = w.dv < p.Dvp && r < p.Dk ? from[(long long)r * p.Dvp + w.dv] : 0.f;
             else if ((Y || place.first) && p.h_in && w.row >= 0 && w.on && r < p.Dk) st[i] = p.h_in[w.state + (long long)r * p.Dv];
         }
         uint32_t v[TPT / 2];
@@ -468,7 +468,7 @@ cudaError_t launch_walk_tc(const SeqDeltaParams& p, unsigned* err, cudaStream_t 
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)WalkTc<KP>::BYTES);
     if (e != cudaSuccess) return e;
     const int dvbs = (p.Dv + 127) / 128, dkbs = 1;
-    const long long blocks = (MODE == DELTA_WHOLE ? p.ax.S : p.pieces) * (long long)p.Hv * (MODE == DELTA_PIECES ? dvbs + dkbs : dvbs);
+    const long long blocks = (MODE == DELTA_WHOLE ? p.ax.S : MODE == DELTA_PIECES ? p.marks : p.pieces) * (long long)p.Hv * (MODE == DELTA_PIECES ? dvbs + dkbs : dvbs);
     return launch_kernel(kernel, dim3((unsigned)blocks), dim3(WALK_THREADS), WalkTc<KP>::BYTES, stream, p.slots > 0, 1, p, dvbs, dkbs, err);
 }
 template <int KP>

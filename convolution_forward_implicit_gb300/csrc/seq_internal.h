@@ -208,6 +208,14 @@ int seq_gnorm_slab(long long S, long long T, int D, int G, int esize, bool bwd, 
 constexpr int DELTA_CHUNK = 64;     // tokens worked on at once; saved states lie at every chunk's first token
 constexpr int DELTA_PLANES = 3 * 128 * 128;      // bytes of a chunk's matrices in parts
 constexpr int DELTA_FACTORS = 264, DELTA_ROWS = 520;      // floats of a chunk's row factors, and with what they come from (see seq_delta.cuh)
+// Pieces of `run` chunks that another piece of their sequence follows are whole: each holds exactly one token whose index is a multiple of
+// their length, its mark, whatever the lengths of the sequences, and the pieces of a sequence follow one another by marks.  So there are
+// T / length marks and no more, and blocks and memory go by them, not by the number of sequences.
+__host__ __device__ inline long long delta_marks(long long T, int run) {
+    const long long len = (long long)run * DELTA_CHUNK;
+    return (T + len - 1) / len;
+}
+__host__ __device__ inline long long delta_joined(long long S, long long marks) { return S < marks ? S : marks; }
 struct SeqDeltaParams {
     SeqAxis ax;
     SeqSlots sl;
@@ -233,10 +241,11 @@ struct SeqDeltaParams {
     int pairs, key_pairs;           // v, y, dy, dv; dq, dk in aligned pairs of elements
     int val_wide, key_wide;         // v and dy; dq and dk in whole aligned 16-byte groups
     int quads;                      // step: states in whole aligned groups of 4
-    // forward, where the axis is cut for the walk (run > 0): chunks of a piece, pieces at most, and by piece and value head what
-    // a piece adds to a state [Dk][Dvp], the matrix it passes one through [Dk][Dkp], and the state it starts from [Dk][Dvp]
-    int run, pieces, Dkp;
-    float *added, *through, *start;
+    // forward, where the axis is cut for the walk (run > 0): chunks of a piece, pieces at most, the marks of those that another follows
+    // (see delta_marks), and by mark and value head what a piece adds to a state [Dk][Dvp] (of a sequence's first, once joined: the state it
+    // starts from), the matrix it passes one through [Dk][Dkp], and the state it leaves [Dk][Dvp]
+    int run, pieces, marks, Dkp;
+    float *added, *through, *left;
     int sms;
 };
 cudaError_t launch_seq_delta_fwd(const SeqDeltaParams& p, bool bf16, cudaStream_t stream);

@@ -49,3 +49,26 @@ def test_nothing_grows_from_nothing(bf16, shift, Dk, Dv):
     assert not bool(torch.isfinite(h[..., 2::3]).all())
     plan.check()
     b.check_guards()
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("lens", [[64] * 40, [1] * 100 + [1500] + [70] * 20 + [0] * 30 + [900], [0] * 50 + [2300] + [0] * 50, [1400] + [1] * 300,
+                                  [1] * 20 + [3000, 0, 3300, 99], [0, 1800, 2] * 3 + [700]])
+def test_few_long_sequences_among_many(bf16, lens):
+    """The plan does not know where the tokens are.  In place of the states, too."""
+    c = Case(len(lens), bf16, lens, 1, 1, 64, 64, True, decay=0.02)
+    at, sl = slots_of(c.S, c.b.rng, c.S + 2, [0, c.S // 2])
+    h_in, full = c.b.normal(c.S + 2, 1, 64, 64, std=0.3, dtype=c.f32)
+    h0 = np.where((at >= 0)[:, None, None, None], full[at], 0)
+    ref = R.delta(**c.exact, lens=lens, h0=h0, norm=True)
+    fwd, y, h = c.plan("fwd").allocate(), c.b.out(c.T, 64), c.b.out(c.S + 2, 1, 64, 64, dtype=c.f32)
+    fwd.workspace.fill_(0xFF)
+    fwd.forward(*c.ins(), y, starts=c.starts, h_in=h_in, h_out=h, slots=sl)
+    c.check(dict(y=y), ref)
+    c.check_states("h", h, ref["h"], at, R.FORWARD)
+    fwd.check()
+    c.b.check_guards()
+    both, y2 = h_in.clone(), c.b.out(c.T, 64)
+    fwd.forward(*c.ins(), y2, starts=c.starts, h_in=both, h_out=both, slots=sl)
+    assert bool((y2 == y).all()) and np.array_equal(host(both)[at[at >= 0]], host(h)[at[at >= 0]])
+    assert (pieces(fwd) > 0) == (max(lens) in (3300, 1800))
