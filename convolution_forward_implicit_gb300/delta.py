@@ -70,8 +70,8 @@ class SeqDeltaPlan(_SeqPlan):
     def __init__(self, S, T, Hk, Hv, Dk, Dv, dtype, direction="fwd", ragged=False, qk_norm=True, scale=None):
         code = self._direction(direction, self._names)
         self.S, self.T, self.Hk, self.Hv, self.Dk, self.Dv = int(S), int(T), int(Hk), int(Hv), int(Dk), int(Dv)
-        if scale is not None and not scale:
-            raise ValueError("scale is zero")
+        if scale is not None and not ctypes.c_float(scale).value:       # (zero stands for 1 / sqrt(Dk) there)
+            raise ValueError("scale is zero in fp32")
         self._tokens, self._sequences = self.T, self.S
         self._keys, self._values_width, self._row = self.Hk * self.Dk, self.Hv * self.Dv, (self.Hv, self.Dk, self.Dv)
         self._open(seq_delta_plan_create(S, T, Hk, Hv, Dk, Dv, dtype, code,

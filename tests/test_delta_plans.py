@@ -52,3 +52,11 @@ def test_places_of_pieces(tmp_path):
              cut("seq_delta.cuh", DEVICE + "WalkPlace walk_place(")]
     out = build(tmp_path, "delta_place_check", "delta_place.inc", parts)
     assert out.returncode == 0 and " 0 wrong" in out.stdout, out.stdout + out.stderr
+
+
+@pytest.mark.parametrize("scale", [1e-50, -1e-60, 0.0, 2.0 ** -151])
+def test_a_scale_too_small_for_fp32_is_refused(lib, scale):
+    """Rounded to fp32 it is zero, which the C call takes for 1 / sqrt(Dk)."""
+    with pytest.raises(ValueError):
+        D.SeqDeltaPlan(1, 8, 1, 1, 16, 16, CONV_F32, scale=scale)
+    D.SeqDeltaPlan(1, 8, 1, 1, 16, 16, CONV_F32, scale=2.0 ** -149).close()
