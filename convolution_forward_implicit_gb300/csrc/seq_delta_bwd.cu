@@ -211,7 +211,10 @@ __global__ void __launch_bounds__(DT, 1) delta_grad_kernel(const __grid_constant
     Smem& s = *reinterpret_cast<Smem*>(raw);
     constexpr int LD = Smem::LD, NT = KP / 16;
     const CutPiece cut = cut_piece(p.ax, blockIdx.x, DC);
-    if (cut.n <= 0) return;
+    if (cut.n <= 0) {
+        dep_wait();                  // (what follows in the stream then follows the walk before it, too)
+        return;
+    }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t2 = (lane & 3) * 2;
     const int kh = blockIdx.y, rep = SHARED ? p.Hv / p.Hk : 1;
     const int m0 = (warp & 3) * 16, n0 = (warp >> 2) * (KP / 2), j0 = (warp >> 2) * 32;

@@ -113,7 +113,10 @@ __global__ void __launch_bounds__(GW, 1) delta_grad_tc_kernel(const __grid_const
     uint8_t* sm = smem_raw + (base - smem_u32(smem_raw));
     GradRest& s = *reinterpret_cast<GradRest*>(sm + G::REST);
     const CutPiece cut = cut_piece(p.ax, blockIdx.x, DC);
-    if (cut.n <= 0) return;
+    if (cut.n <= 0) {
+        dep_wait();                              // (what follows in the stream then follows the walk before it, too)
+        return;
+    }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wq = warp & 3, cq = warp >> 2;
     const int kh = blockIdx.y, rep = SHARED ? p.Hv / p.Hk : 1, blocks = (p.Dv + 63) / 64;
     // Two barriers say what is ready, the states' D3 by its own: a warp goes on from one telling to the other without a wait between,
