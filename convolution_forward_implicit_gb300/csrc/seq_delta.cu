@@ -7,7 +7,7 @@
 //
 // What bounds them: the first, latency between its stages (inversion, products of 64 rows, factors by one warp a head): 8192 tokens, 32 value heads on
 // 16 key heads of 128 x 128 in bf16 take 117 us, 220 MB of traffic (28% of copy rate).  The walk, the order of its chunks: 3802 tokens of a head of
-// 48 x 80 in fp32 (60 chunks) take 244 us, 4 us a chunk, about as many in any number of CTAs an SM holds at once; in pieces of the axis 55 + 10 + 76.  Operands on their way
+// 48 x 80 in fp32 (60 chunks) take 244 us, 4 us a chunk, about as many in any number of CTAs an SM holds at once; in pieces of the axis 54 + 11 + 77.  Operands on their way
 // a chunk ahead made no difference (257 us against 255): the products of 16 or 32 columns and their splits are one chain.
 #include "seq_delta.cuh"
 

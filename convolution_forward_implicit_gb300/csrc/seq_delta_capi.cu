@@ -27,7 +27,7 @@ size_t through_bytes(const seq_plan* p) { return align256(marks(p) * p->Hv * p->
 // twice, the first time also with the columns of a unit matrix (without outputs: 0.8 of it); their states are joined in order (0.7
 // a piece); launches 3.  It has to promise a fifth.  Of lengths that the plan does not know the longest is taken to be four times the mean, three
 // quarters of all tokens at most; beside it the others' blocks (2 chunks to begin, half a chunk at the end) fill the SMs.
-// 2048 tokens, 16 heads of 128 x 128 bf16: 117 us cut, 174 not; 13 sequences, 6011 tokens, 32 heads: 498 cut (in pieces of 16), 364 not;
+// 2048 tokens, 16 heads of 128 x 128 bf16: 119 us cut, 187 not; 13 sequences, 6011 tokens, 32 heads: 385 us not cut, a third more in pieces of 16;
 // 64 and 256 sequences of 64 tokens by their bounds, 8 heads: 125 and 471 when only their tokens counted and the plan cut, 77 and 295 now.
 int choose_run(const seq_plan* p) {
     const bool wide = p->dtype == CONV_BF16 && p->W > 16, known = p->L > 0 || p->S == 1;
@@ -72,7 +72,7 @@ conv_status seq_delta_plan_create(seq_plan_t* out, int64_t S, int64_t T, int64_t
     if (!p) return CONV_ERR_INVALID_ARG;
     p->Hk = (int)Hk; p->Hv = (int)Hv; p->N = (int)Dk; p->W = (int)Dv;
     p->scale = scale != 0.f ? scale : 1.f / sqrtf((float)Dk);
-    // blocks a kernel launches at most: 16 columns of a state each; 8 when there is one token
+    // blocks a kernel launches at most: 16 columns of a state each (a step: 32 or 128)
     const int64_t slots = direction == SEQ_STEP ? 0 : cut_slots(S, T, p->L, DELTA_CHUNK);
     if (slots > INT32_MAX || S * Hv * ((Dv + 15) / 16) > INT32_MAX) {
         delete p;

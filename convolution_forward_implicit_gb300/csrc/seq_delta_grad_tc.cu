@@ -10,7 +10,7 @@
 // large ones of the parts' nine.
 //
 // What bounds it: one CTA is on an SM (210 KB of shared memory and all of TMEM), and its stages follow one another.  8192 tokens, 32 value
-// heads on 16 key heads of 128 x 128 take about 530 us: 13.5 CTAs an SM of two value heads each, at 75000 cycles, of which the
+// heads on 16 key heads of 128 x 128 take about 550 us (578 by itself): 13.5 CTAs an SM of two value heads each, at 78000 cycles, of which the
 // products take 21000, and the bytes (580 KB) would take 25000; the rest are splits, factors and row sums by 16 warps that wait for
 // one another.  A 17th warp that issues leaves 96 registers a thread instead of 128: the whole call took 1246 us with what spilled,
 // 1194 without it; products issued by three different warps made it 1187.

@@ -10,9 +10,9 @@
 //
 // What bounds a walk: the products and the threads' work between them follow one another, three times a chunk.  2048 tokens of 16 heads
 // of 128 x 128 (16 CTAs, 32 chunks in order) take 143 us: 4.5 us a chunk, of which the products are 2 (60 of 64 cycles);
-// in five pieces of the axis 35, 20 to join them and 42.
-// 8192 tokens, 32 heads, 4 sequences (128 CTAs) take 184 us, backward 188, where the kernel moves 760 MB, most of it what is saved
-// (61% of copy rate); with mma.sync they took 814 and 776.
+// in five pieces of the axis 37, 22 to join them and 42.
+// 8192 tokens, 32 heads, 4 sequences (128 CTAs) take 194 us, backward 201, where the kernel moves 760 MB, most of it what is saved
+// (57% of copy rate); with mma.sync they took 814 and 776.
 #include "seq_delta.cuh"
 #include "seq_delta_tc.cuh"
 

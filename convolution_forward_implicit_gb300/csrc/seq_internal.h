@@ -184,7 +184,7 @@ cudaError_t launch_seq_norm_bwd(const SeqNormParams& p, bool bf16, bool res_bf16
 int seq_norm_bwd_blocks(int rows, int D, unsigned flags, int esize, int rsize, int sms);
 
 // ---- group norm with an activation ----
-// The token axis is cut into slabs of `slab` tokens that do not cross sequences (AxisCut).
+// The token axis is cut into slabs of `slab` tokens that do not cross sequences (CutPiece).
 struct SeqGnormParams {
     SeqAxis ax;
     int D, G, act;

@@ -16,9 +16,10 @@
  *
  * Whole sequences are worked on in chunks of 64 tokens: an infinity or NaN in a token may reach
  * every token of its chunk and all later ones of its sequence, in its value head (q, k: in the
- * heads that share them), and nothing else.  g may be minus infinity (a finite state is dropped).
+ * heads that share them), and nothing else; of gradients any token of its sequence.  g may be minus infinity (a finite state is dropped).
  * Where g is above 0 and its sum between two tokens of a chunk passes 80, or a state grows beyond fp32's range over the
- * tokens of a piece (below) from however small values, the results may overflow; a state of zero stays zero.
+ * tokens of a piece (below) from however small values, the results may overflow; across pieces a state of zero stays zero.
+ * dg of a token whose factor is much smaller than those behind it in its chunk is off by 1e-7 or so of what these have.
  * Where few heads have long sequences the plan of a forward call cuts the axis (the description
  * has the chunks of a piece): sums are then taken in another order than by a plan of other sizes.
  */
