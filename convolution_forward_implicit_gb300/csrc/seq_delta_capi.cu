@@ -1,6 +1,7 @@
 // C-ABI of the gated delta rule: plan, argument checks, workspace layout.  Declarations and the contract of
 // every entry point are in include/delta.h.
 #include <math.h>
+#include <stdlib.h>
 
 #include "delta.h"
 #include "seq_plan.h"
@@ -79,6 +80,8 @@ conv_status seq_delta_plan_create(seq_plan_t* out, int64_t S, int64_t T, int64_t
         return CONV_ERR_UNSUPPORTED;
     }
     p->slots = (int)slots;
+    const char* stall = getenv("CONV_TEST_STALL");
+    p->test_stall = stall && atoi(stall) ? 1 : 0;
     if (direction != SEQ_STEP) p->ws_bytes = tri_bytes(p) + row_bytes(p);
     if (direction == SEQ_FWD) {
         p->run = choose_run(p);
@@ -163,6 +166,7 @@ static conv_status delta_call(seq_plan_t p, const seq_delta_args* a, seq_directi
     auto aligned = [](const void* v) { return reinterpret_cast<uintptr_t>(v) % 16 == 0; };
     q.quads = p->W % 4 == 0 && aligned(a->h_in) && aligned(a->h_out);
     q.sms = p->sms;
+    q.test_stall = p->test_stall;
     const bool bf16 = p->dtype == CONV_BF16;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return finish(dir == SEQ_FWD ? launch_seq_delta_fwd(q, bf16, s) : bwd ? launch_seq_delta_bwd(q, bf16, s)

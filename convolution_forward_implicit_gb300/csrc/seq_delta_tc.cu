@@ -321,6 +321,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) delta_walk_tc_kernel(const __
         bool ok = true;
         int committed = 0;
         for (int c = 0; c < w.chunks && ok; ++c) {
+            if (p.test_stall && c == 1) break;       // (test hook: the other warps' wait runs out)
             const uint32_t kq = w.stage(c), tp = kq + W::KQ, acc = w.tmem + W::ACC;
             ok = w.turn.arrived(c) && w.turn.next(w.turn.ready);
             if (!ok) break;
@@ -505,6 +506,7 @@ __global__ void __launch_bounds__(WALK_THREADS, 1) delta_back_tc_kernel(const __
         bool ok = true;
         int committed = 0;
         for (int s = 0; s < w.chunks && ok; ++s) {
+            if (p.test_stall && s == 1) break;       // (test hook: the other warps' wait runs out)
             const uint32_t kq = w.stage(s), tp = kq + W::KQ, acc = w.tmem + B::ACC;
             ok = w.turn.arrived(s) && w.turn.next(w.turn.ready);
             if (!ok) break;

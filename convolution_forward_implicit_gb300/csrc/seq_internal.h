@@ -247,6 +247,7 @@ struct SeqDeltaParams {
     int run, pieces, marks, Dkp;
     float *added, *through, *left;
     int sms;
+    int test_stall;                 // test hook: products that others wait for are never issued (bf16 kernels)
 };
 cudaError_t launch_seq_delta_fwd(const SeqDeltaParams& p, bool bf16, cudaStream_t stream);
 cudaError_t launch_seq_delta_bwd(const SeqDeltaParams& p, bool bf16, cudaStream_t stream);

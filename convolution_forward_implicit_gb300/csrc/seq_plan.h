@@ -49,6 +49,7 @@ struct seq_plan {
     int act;               // group norm
     int slots;             // delta rule, group norm: chunks or slabs of the token axis
     int pieces;            // delta rule: of `run` chunks each (0: the axis is not cut for the walk)
+    int test_stall;        // delta rule, CONV_TEST_STALL: see SeqDeltaParams
     char desc[256];
 
     bool ragged() const { return flags & SEQ_RAGGED; }
