@@ -3,8 +3,8 @@
 // Bound by the bytes of the states, each read and written once.  With a = h^T k and c = h^T q of the old state,
 //   u = beta (v - exp(g) a),  h <- exp(g) h + k u^T,  y = scale (exp(g) c + (q.k) u),
 // so that one pass over the state in registers does both sums, and one meeting of the block's warps joins them.  The states pass
-// L2 as what is used once, and three blocks are on an SM, so that some load while others store: 256 sequences of 32 heads of 128 x 128 take 178 us,
-// 6.0 TB/s, with plain accesses and two blocks 210 us (with blocks of 512 threads 338).
+// L2 as what is used once, and three blocks are on an SM, so that some load while others store: 256 sequences of 32 heads of 128 x 128 take 178 to 187 us,
+// 5.8 to 6.0 TB/s, with plain accesses and two blocks 210 us (with blocks of 512 threads 338).
 #include "seq_delta.cuh"
 
 namespace convfwd {
